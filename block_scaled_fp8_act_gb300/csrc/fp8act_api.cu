@@ -198,6 +198,28 @@ int w8a16_common(const void* x, const void* w, const float* sw, int M, int N, in
                                                    static_cast<cudaStream_t>(stream)));
 }
 
+constexpr int kNormMaxK = 32768;  // one CTA holds a row: 1024 threads x 4 chunks of 8
+constexpr int kMaxQLen = 1 << 20;
+
+// The cache's own rules; fills the launchers' form of it.
+int check_cache(const fp8act_kv_cache* c, fp8act::KvCache* out) {
+    if (!c) return FP8ACT_ERR_NULL;
+    const int ps = c->page_size;
+    if (c->num_pages < 0 || c->kv_heads <= 0 || ps < 16 || ps > 256 || (ps & (ps - 1)) ||
+        (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256))
+        return FP8ACT_ERR_SHAPE;
+    if (c->num_pages > 0) {
+        if (!c->k_e4m3 || !c->v_e4m3 || !c->k_scale || !c->v_scale) return FP8ACT_ERR_NULL;
+        if (!aligned(c->k_e4m3, 16) || !aligned(c->v_e4m3, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
+            return FP8ACT_ERR_ALIGN;
+    }
+    int log2 = 4;
+    while ((1 << log2) < ps) ++log2;
+    *out = {static_cast<uint8_t*>(c->k_e4m3), static_cast<uint8_t*>(c->v_e4m3), c->k_scale, c->v_scale,
+            c->num_pages, log2, c->kv_heads, c->head_dim};
+    return FP8ACT_OK;
+}
+
 }  // namespace
 
 namespace fp8act {
@@ -294,18 +316,123 @@ int fp8_block_gemm_grouped_f32(const fp8act_gemm_problem* problems, int count, v
     return gemm_grouped_common(problems, count, true, stream);
 }
 
+int fp8_rmsnorm_quant(const void* x_bf16, const void* residual_bf16, const void* weight_bf16, float eps,
+                      float weight_offset, int M, int K, void* q_e4m3, float* sa, void* residual_out_bf16,
+                      void* stream) {
+    if (M < 0 || K > kNormMaxK) return FP8ACT_ERR_SHAPE;
+    if (int st = check_k(K)) return st;
+    if (M == 0) return FP8ACT_OK;
+    if (!x_bf16 || !weight_bf16 || !q_e4m3 || !sa || !residual_bf16 != !residual_out_bf16) return FP8ACT_ERR_NULL;
+    if (!aligned(x_bf16, 16) || !aligned(residual_bf16, 16) || !aligned(weight_bf16, 16) || !aligned(q_e4m3, 16) ||
+        !aligned(residual_out_bf16, 16) || !aligned(sa, 4))
+        return FP8ACT_ERR_ALIGN;
+    int st = FP8ACT_OK;
+    const int sms = current_device_sms(&st);
+    if (st) return st;
+    return launch_status(fp8act::launch_rmsnorm_quant(x_bf16, residual_bf16, weight_bf16, eps, weight_offset, M, K,
+                                                      q_e4m3, sa, residual_out_bf16, sms,
+                                                      static_cast<cudaStream_t>(stream)));
+}
+
+int fp8_silu_mul_quant(const void* gate_up_bf16, int M, int I, void* q_e4m3, float* sa, void* stream) {
+    if (M < 0) return FP8ACT_ERR_SHAPE;
+    if (int st = check_k(I)) return st;
+    if (M == 0) return FP8ACT_OK;
+    if (!gate_up_bf16 || !q_e4m3 || !sa) return FP8ACT_ERR_NULL;
+    if (!aligned(gate_up_bf16, 16) || !aligned(q_e4m3, 16) || !aligned(sa, 4)) return FP8ACT_ERR_ALIGN;
+    int st = FP8ACT_OK;
+    const int sms = current_device_sms(&st);
+    if (st) return st;
+    return launch_status(
+        fp8act::launch_silu_mul_quant(gate_up_bf16, M, I, q_e4m3, sa, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8_kv_append(const void* k_bf16, const void* v_bf16, const int64_t* slots, int T, int64_t k_stride,
+                  int64_t v_stride, const fp8act_kv_cache* cache, void* stream) {
+    fp8act::KvCache c;
+    if (int st = check_cache(cache, &c)) return st;
+    const int64_t width = static_cast<int64_t>(c.heads) * c.head_dim;
+    if (T < 0 || k_stride < width || v_stride < width) return FP8ACT_ERR_SHAPE;
+    if (T > (int64_t{1} << 38) / width) return FP8ACT_ERR_SHAPE;  // keeps the grid within 2^31 CTAs
+    if (T == 0) return FP8ACT_OK;
+    if (!k_bf16 || !v_bf16 || !slots) return FP8ACT_ERR_NULL;
+    if (!aligned(k_bf16, 16) || !aligned(v_bf16, 16) || !aligned(slots, 8) || k_stride % 8 || v_stride % 8)
+        return FP8ACT_ERR_ALIGN;
+    int st = FP8ACT_OK;
+    current_device_sms(&st);
+    if (st) return st;
+    return launch_status(fp8act::launch_kv_append(k_bf16, v_bf16, slots, T, k_stride, v_stride, c,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp8_kv_attention_workspace(int max_q_len, int q_heads, const fp8act_kv_cache* cache) {
+    fp8act::KvCache c;
+    if (check_cache(cache, &c) || max_q_len < 0 || max_q_len > kMaxQLen || q_heads <= 0 || q_heads % c.heads) return 0;
+    return fp8act::kv_attention_workspace(max_q_len, q_heads / c.heads, c.head_dim);
+}
+
+int fp8_kv_attention(const void* q_bf16, int64_t q_stride, const int* cu_q, const int* kv_lens, const int* page_table,
+                     int max_pages, int batch, int tokens, int max_q_len, int q_heads, float softmax_scale,
+                     const fp8act_kv_cache* cache, void* out_bf16, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    fp8act::KvCache c;
+    if (int st = check_cache(cache, &c)) return st;
+    if (batch < 0 || tokens < 0 || max_pages < 0 || max_q_len < 0 || max_q_len > kMaxQLen || q_heads <= 0 ||
+        q_heads % c.heads || q_heads / c.heads > 256 || q_stride < static_cast<int64_t>(q_heads) * c.head_dim ||
+        static_cast<int64_t>(max_pages) << c.page_log2 > 0x7FFFFF00 ||
+        static_cast<int64_t>(tokens) * (q_heads / c.heads) > 0x7FFFFF00)
+        return FP8ACT_ERR_SHAPE;
+    if (batch == 0 || tokens == 0) return FP8ACT_OK;
+    if (!q_bf16 || !cu_q || !kv_lens || !out_bf16 || !workspace || (max_pages > 0 && !page_table))
+        return FP8ACT_ERR_NULL;
+    if (!aligned(q_bf16, 16) || q_stride % 8 || !aligned(out_bf16, 16) || !aligned(workspace, 16) || !aligned(cu_q, 4) ||
+        !aligned(kv_lens, 4) || !aligned(page_table, 4) || !aligned(lse, 4))
+        return FP8ACT_ERR_ALIGN;
+    if (workspace_bytes < fp8act::kv_attention_workspace(max_q_len, q_heads / c.heads, c.head_dim))
+        return FP8ACT_ERR_SHAPE;
+    int st = FP8ACT_OK;
+    const int sms = current_device_sms(&st);
+    if (st) return st;
+    const fp8act::AttentionProblem p = {q_bf16,    q_stride,  cu_q,          kv_lens, page_table, max_pages,
+                                        batch,     tokens,    max_q_len,     q_heads / c.heads,   softmax_scale,
+                                        c,         out_bf16,  lse,           workspace};
+    return launch_status(fp8act::launch_kv_attention(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8act_verify_drafts(const void* target, const void* draft, int logits_f32, const int* draft_tokens,
+                         const float* uniform, const float* noise, const float* temperature, const int* n_draft, int B,
+                         int k, int V, int* accepted, int* tokens, float* accept_prob, void* stream) {
+    if (B < 0 || k < 0 || k > fp8act::kMaxDrafts || V <= 0 || V > 0x7FFFFF00 / 16) return FP8ACT_ERR_SHAPE;
+    if (B > 0x7FFFFFFF / 16) return FP8ACT_ERR_SHAPE;
+    if (B == 0) return FP8ACT_OK;
+    if (!target || !noise || !temperature || !accepted || !tokens || (k > 0 && (!draft_tokens || !uniform)))
+        return FP8ACT_ERR_NULL;
+    if (!aligned(target, 16) || !aligned(draft, 16) || !aligned(draft_tokens, 4) || !aligned(uniform, 4) ||
+        !aligned(noise, 4) || !aligned(temperature, 4) || !aligned(n_draft, 4) || !aligned(accepted, 4) ||
+        !aligned(tokens, 4) || !aligned(accept_prob, 4))
+        return FP8ACT_ERR_ALIGN;
+    int st = FP8ACT_OK;
+    current_device_sms(&st);
+    if (st) return st;
+    const fp8act::VerifyProblem p = {target,  k > 0 ? draft : nullptr, draft_tokens, uniform, noise, temperature,
+                                     n_draft, B, k, V, logits_f32 != 0, accepted, tokens, accept_prob};
+    return launch_status(fp8act::launch_verify_drafts(p, static_cast<cudaStream_t>(stream)));
+}
+
 const char* fp8act_strerror(int status) {
     switch (status) {
         case FP8ACT_OK: return "ok";
         case FP8ACT_ERR_NULL: return "a required pointer is NULL";
         case FP8ACT_ERR_SHAPE:
             return "bad shape: M, N must be >= 0 and K a positive multiple of 128 (grouped calls: at most 16 "
-                   "problems; fp8_linear: min(8, M) rows of K codes and scales must fit in 200 KiB)";
+                   "problems; fp8_linear: min(8, M) rows of K codes and scales must fit in 200 KiB; the operators "
+                   "between the linear layers: see the limits at each)";
         case FP8ACT_ERR_ALIGN: return "misaligned pointer: tensors need 16-byte, scales 4-byte alignment";
         case FP8ACT_ERR_LAUNCH: return "kernel launch failed";
         case FP8ACT_ERR_TIMEOUT: return "a kernel gave up a bounded wait (device-side timeout)";
         case FP8ACT_ERR_DEVICE: return "no current CUDA device of compute capability 10.3 (GB300)";
         case FP8ACT_ERR_CUDA: return "CUDA runtime error";
+        case FP8ACT_ERR_INDEX: return "a slot, page, length or token index on the device was out of range";
         default: return "unknown fp8act status";
     }
 }
@@ -318,7 +445,10 @@ int fp8act_check_status(void* stream) {
     const unsigned int tc = fp8act::read_and_clear_tc_error();
     const unsigned int mid = fp8act::read_and_clear_midm_error();
     const unsigned int rd = fp8act::read_and_clear_read_error();
-    return (tc | mid | rd) ? FP8ACT_ERR_TIMEOUT : FP8ACT_OK;
+    const unsigned int index = fp8act::read_and_clear_kv_index_error() | fp8act::read_and_clear_attn_index_error() |
+                               fp8act::read_and_clear_verify_index_error();
+    if (tc | mid | rd) return FP8ACT_ERR_TIMEOUT;
+    return index ? FP8ACT_ERR_INDEX : FP8ACT_OK;
 }
 
 int fp8act_set_wait_limit(long long limit_ns, int withhold_first_load) {
@@ -338,6 +468,6 @@ int fp8act_stream_read(const void* src, size_t bytes, unsigned int* sink, void* 
                                                     static_cast<cudaStream_t>(stream)));
 }
 
-int fp8act_version(void) { return 200; }
+int fp8act_version(void) { return 300; }
 
 }  // extern "C"

@@ -2,6 +2,7 @@
 // Arguments are validated by the C-ABI layer before any of these is called.
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -97,6 +98,71 @@ cudaError_t launch_gemm_midm(const uint8_t* q, const float* sa, const uint8_t* w
 // per SM, a ring of TMA bulk copies, launched like the GEMMs; folds the data
 // into *sink.
 cudaError_t launch_stream_read(const void* src, int64_t bytes, unsigned int* sink, int num_sms, cudaStream_t stream);
+
+// RMS norm of x (+ residual) with E4M3 codes and 1x128 scales out; K / 8
+// chunks of at most 4096. residual and residual_out are both null or neither.
+cudaError_t launch_rmsnorm_quant(const void* x, const void* residual, const void* weight, float eps,
+                                 float weight_offset, int M, int K, void* q, float* sa, void* residual_out,
+                                 int num_sms, cudaStream_t stream);
+
+// silu(gate) * up of gate_up bf16 [M, 2I] with E4M3 codes and 1x128 scales out.
+cudaError_t launch_silu_mul_quant(const void* gate_up, int M, int I, void* q, float* sa, int num_sms,
+                                  cudaStream_t stream);
+
+// The paged key / value cache: codes [num_pages, heads, page, head_dim],
+// scales [num_pages, heads, page], page = 1 << page_log2.
+struct KvCache {
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int num_pages, page_log2, heads, head_dim;
+};
+
+// Quantise T tokens' keys and values into their slots (strides in elements).
+cudaError_t launch_kv_append(const void* k, const void* v, const int64_t* slots, int T, int64_t k_stride,
+                             int64_t v_stride, const KvCache& cache, cudaStream_t stream);
+
+// Attention of `tokens` new tokens of `batch` sequences over the cache.
+struct AttentionProblem {
+    const void* q;
+    int64_t q_stride;
+    const int* cu_q;
+    const int* kv_lens;
+    const int* page_table;
+    int64_t table_stride;
+    int batch, tokens, max_q_len, group;
+    float softmax_scale;
+    KvCache cache;
+    void* out;
+    float* lse;
+    void* workspace;
+};
+size_t kv_attention_workspace(int max_q_len, int group, int head_dim);
+cudaError_t launch_kv_attention(const AttentionProblem& p, int num_sms, cudaStream_t stream);
+
+// Verification of k drafted tokens per sequence.
+struct VerifyProblem {
+    const void* target;  // [B, k + 1, V]
+    const void* draft;   // [B, k, V] or null
+    const int* draft_tokens;
+    const float* uniform;
+    const float* noise;
+    const float* temperature;
+    const int* n_draft;
+    int B, k, V;
+    bool f32;
+    int* accepted;
+    int* tokens;
+    float* accept_prob;
+};
+constexpr int kMaxDrafts = 32;
+cudaError_t launch_verify_drafts(const VerifyProblem& p, cudaStream_t stream);
+
+// Device-side words set by a page, slot, length or token index out of range.
+unsigned int read_and_clear_kv_index_error();
+unsigned int read_and_clear_attn_index_error();
+unsigned int read_and_clear_verify_index_error();
 
 // Device-side error words of the tcgen05 kernels (non-zero after a bounded
 // wait gave up); reading one synchronises with the device and clears it.

@@ -1,0 +1,130 @@
+// The two elementwise operators that feed a block-FP8 product: RMS norm with
+// the residual's addition, and silu(gate) * up, each ending in the product's
+// own activation format (E4M3 codes, one fp32 scale per 128 columns).
+#include "decoder_util.cuh"
+#include "kernels.h"
+
+namespace fp8act {
+namespace {
+
+// One CTA per row; thread t holds the 8-column chunks t, t + blockDim, ... so
+// a half-warp always holds one 128-wide quantisation group and the row is
+// read once. blockDim is a multiple of 32.
+template <int kChunks, bool kResidual>
+__global__ void rmsnorm_quant_kernel(const uint4* x, const uint4* residual, const uint4* weight, float eps,
+                                     float weight_offset, int chunks, uint2* q, float* sa, uint4* residual_out) {
+    __shared__ float part[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = blockIdx.x;
+    x += row * chunks;
+    q += row * chunks;
+    sa += row * (chunks / 16);
+    if (kResidual) {
+        residual += row * chunks;
+        residual_out += row * chunks;
+    }
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    float h[kChunks][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        const bool in = c < chunks;
+        unpack_bf16x8(in ? ld_dep_stream_v4(x + c) : make_uint4(0, 0, 0, 0), h[i]);
+        if (kResidual) {
+            float r[8];
+            unpack_bf16x8(in ? ld_dep_stream_v4(residual + c) : make_uint4(0, 0, 0, 0), r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+            if (in) residual_out[c] = pack_bf16x8(h[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (lane == 0) part[warp] = ss;
+    __syncthreads();
+    ss = lane < (blockDim.x >> 5) ? part[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float rstd = rsqrtf(ss / static_cast<float>(chunks * 8) + eps);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        const bool in = c < chunks;
+        float w[8];
+        unpack_bf16x8(in ? __ldg(weight + c) : make_uint4(0, 0, 0, 0), w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = h[i][j] * rstd * (w[j] + weight_offset);
+        uint2 codes;
+        const float s = quant_f32_group_halfwarp(w, codes);
+        if (in) {
+            q[c] = codes;
+            if ((lane & 15) == 0) sa[c / 16] = s;
+        }
+    }
+}
+
+// silu(gate) * up of one row [gate (I) | up (I)]: a half-warp per 128-wide
+// group, warps striding over (row, pair of groups).
+__global__ void silu_mul_quant_kernel(const uint4* gate_up, int64_t M, int groups, uint2* q, float* sa) {
+    const int lane = threadIdx.x & 31, hl = lane & 15;
+    const int pairs = (groups + 1) / 2;
+    const int64_t items = M * pairs;
+    const int64_t step = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    for (int64_t item = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; item < items; item += step) {
+        const int64_t row = item / pairs;
+        const int g = static_cast<int>(item - row * pairs) * 2 + (lane >> 4);
+        const bool in = g < groups;
+        const uint4* p = gate_up + row * groups * 32 + g * 16 + hl;
+        float a[8], b[8];
+        unpack_bf16x8(in ? ld_dep_stream_v4(p) : make_uint4(0, 0, 0, 0), a);
+        unpack_bf16x8(in ? ld_dep_stream_v4(p + groups * 16) : make_uint4(0, 0, 0, 0), b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = __fdividef(a[j], 1.0f + __expf(-a[j])) * b[j];
+        uint2 codes;
+        const float s = quant_f32_group_halfwarp(a, codes);
+        if (in) {
+            q[(row * groups + g) * 16 + hl] = codes;
+            if (hl == 0) sa[row * groups + g] = s;
+        }
+    }
+}
+
+template <int kChunks>
+cudaError_t launch_norm(const void* x, const void* residual, const void* weight, float eps, float weight_offset,
+                        int64_t M, int chunks, void* q, float* sa, void* residual_out, cudaStream_t stream) {
+    const int threads = ((chunks + kChunks - 1) / kChunks + 31) / 32 * 32;
+    return launch_dependent(residual ? rmsnorm_quant_kernel<kChunks, true> : rmsnorm_quant_kernel<kChunks, false>,
+                            dim3(static_cast<unsigned>(M)), threads, 0, stream, 1, static_cast<const uint4*>(x),
+                            static_cast<const uint4*>(residual), static_cast<const uint4*>(weight), eps, weight_offset,
+                            chunks, static_cast<uint2*>(q), sa, static_cast<uint4*>(residual_out));
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm_quant(const void* x, const void* residual, const void* weight, float eps,
+                                 float weight_offset, int M, int K, void* q, float* sa, void* residual_out,
+                                 int num_sms, cudaStream_t stream) {
+    const int chunks = K / 8;
+    if (chunks <= 1024 && M <= 2 * num_sms)
+        return launch_norm<1>(x, residual, weight, eps, weight_offset, M, chunks, q, sa, residual_out, stream);
+    return launch_norm<4>(x, residual, weight, eps, weight_offset, M, chunks, q, sa, residual_out, stream);
+}
+
+cudaError_t launch_silu_mul_quant(const void* gate_up, int M, int I, void* q, float* sa, int num_sms,
+                                  cudaStream_t stream) {
+    const int groups = I / kGroup;
+    const int64_t warps = static_cast<int64_t>(M) * ((groups + 1) / 2);
+    int64_t blocks = (warps + 7) / 8;
+    if (blocks > 8 * static_cast<int64_t>(num_sms)) blocks = 8 * static_cast<int64_t>(num_sms);
+    return launch_dependent(silu_mul_quant_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 1,
+                            static_cast<const uint4*>(gate_up), static_cast<int64_t>(M), groups,
+                            static_cast<uint2*>(q), sa);
+}
+
+}  // namespace fp8act

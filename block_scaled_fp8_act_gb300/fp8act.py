@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from typing import NamedTuple
 
 import torch
 
@@ -20,7 +21,8 @@ G = 128
 _lib = None
 
 STATUS = {0: "FP8ACT_OK", 1: "FP8ACT_ERR_NULL", 2: "FP8ACT_ERR_SHAPE", 3: "FP8ACT_ERR_ALIGN",
-          4: "FP8ACT_ERR_LAUNCH", 5: "FP8ACT_ERR_TIMEOUT", 6: "FP8ACT_ERR_DEVICE", 7: "FP8ACT_ERR_CUDA"}
+          4: "FP8ACT_ERR_LAUNCH", 5: "FP8ACT_ERR_TIMEOUT", 6: "FP8ACT_ERR_DEVICE", 7: "FP8ACT_ERR_CUDA",
+          8: "FP8ACT_ERR_INDEX"}
 
 
 class Fp8ActError(RuntimeError):
@@ -65,7 +67,16 @@ def load(build: bool = False) -> ctypes.CDLL:
     L.fp8act_check_status.argtypes = [p]
     L.fp8act_set_wait_limit.argtypes = [ctypes.c_longlong, i]
     L.fp8act_stream_read.argtypes = [p, ctypes.c_size_t, p, p]
-    for fn in (L.fp8_act_quant, L.fp8_weight_quant, L.fp8_block_gemm, L.fp8_block_gemm_f32,
+    f, i64 = ctypes.c_float, ctypes.c_int64
+    L.fp8_rmsnorm_quant.argtypes = [p, p, p, f, f, i, i, p, p, p, p]
+    L.fp8_silu_mul_quant.argtypes = [p, i, i, p, p, p]
+    L.fp8_kv_append.argtypes = [p, p, p, i, i64, i64, p, p]
+    L.fp8_kv_attention.argtypes = [p, i64, p, p, p, i, i, i, i, i, f, p, p, p, p, ctypes.c_size_t, p]
+    L.fp8_kv_attention_workspace.argtypes = [i, i, p]
+    L.fp8_kv_attention_workspace.restype = ctypes.c_size_t
+    L.fp8act_verify_drafts.argtypes = [p, p, i, p, p, p, p, p, i, i, i, p, p, p, p]
+    for fn in (L.fp8_rmsnorm_quant, L.fp8_silu_mul_quant, L.fp8_kv_append, L.fp8_kv_attention,
+               L.fp8act_verify_drafts, L.fp8_act_quant, L.fp8_weight_quant, L.fp8_block_gemm, L.fp8_block_gemm_f32,
                L.fp8_block_gemm_w8a16, L.fp8_block_gemm_w8a16_f32,
                L.fp8_act_quant_grouped, L.fp8_block_gemm_grouped, L.fp8_block_gemm_grouped_f32,
                L.fp8_linear, L.fp8_linear_f32,
@@ -269,6 +280,191 @@ def fp8_block_gemm_grouped(problems, outs=None, stream=None) -> list:
 def fp8_block_gemm_grouped_f32(problems, outs=None, stream=None) -> list:
     """fp32 outputs of the grouped kernels (no bf16 cast)."""
     return _gemm_grouped("fp8_block_gemm_grouped_f32", torch.float32, problems, outs, stream)
+
+
+def _cuda(t, dtypes, shape, name: str) -> int:
+    """Checks a contiguous CUDA tensor of a known shape; its address."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a CUDA tensor with dtype in {dtypes}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+_BF16, _F32, _I32, _I64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
+
+
+def _codes_out(M: int, K: int, q, sa, device):
+    q = torch.empty((M, K), dtype=torch.uint8, device=device) if q is None else q
+    sa = torch.empty((M, K // G), dtype=torch.float32, device=device) if sa is None else sa
+    return q, sa, _cuda(q, _CODES, (M, K), "q"), _cuda(sa, _F32, (M, K // G), "sa")
+
+
+def fp8_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0, q=None, sa=None,
+                      residual_out=None, stream=None):
+    """RMS norm of x (+ residual) with E4M3 codes out, bf16 x, residual [M, K], weight [K].
+
+    Returns (q, sa), or (q, sa, residual_out) with a residual; residual_out = bf16(x + residual)
+    may be x or residual. The weight applied is weight + weight_offset."""
+    _cuda2d(x, _BF16, "x")
+    M, K = x.shape
+    wp = _cuda(weight, _BF16, (K,), "weight")
+    q, sa, qp, sp = _codes_out(M, K, q, sa, x.device)
+    rp = op = None
+    if residual is not None:
+        rp = _cuda(residual, _BF16, (M, K), "residual")
+        residual_out = torch.empty_like(x) if residual_out is None else residual_out
+        op = _cuda(residual_out, _BF16, (M, K), "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    _check("fp8_rmsnorm_quant", load().fp8_rmsnorm_quant(x.data_ptr(), rp, wp, eps, weight_offset, M, K, qp, sp, op,
+                                                         _stream(stream)))
+    return (q, sa) if residual is None else (q, sa, residual_out)
+
+
+def fp8_silu_mul_quant(gate_up, q=None, sa=None, stream=None):
+    """silu(gate) * up of bf16 rows [gate | up] ([M, 2 I]) -> (q E4M3 codes [M, I], sa fp32 [M, I/128])."""
+    _cuda2d(gate_up, _BF16, "gate_up")
+    M, width = gate_up.shape
+    if width % 2:
+        raise ValueError("gate_up must have an even number of columns")
+    q, sa, qp, sp = _codes_out(M, width // 2, q, sa, gate_up.device)
+    _check("fp8_silu_mul_quant", load().fp8_silu_mul_quant(gate_up.data_ptr(), M, width // 2, qp, sp, _stream(stream)))
+    return q, sa
+
+
+class KvCache(NamedTuple):
+    """The paged E4M3 cache: codes [pages, kv_heads, page_size, head_dim], scales [pages, kv_heads, page_size]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+class KvCacheStruct(ctypes.Structure):
+    """fp8act_kv_cache of include/fp8act.h."""
+    _fields_ = [("k_e4m3", ctypes.c_void_p), ("v_e4m3", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+def kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> KvCache:
+    """A cache of zeroed pages."""
+    shape = (num_pages, kv_heads, page_size)
+    return KvCache(torch.zeros((*shape, head_dim), dtype=torch.uint8, device=device),
+                   torch.zeros((*shape, head_dim), dtype=torch.uint8, device=device),
+                   torch.ones(shape, device=device), torch.ones(shape, device=device))
+
+
+def _cache_struct(cache) -> KvCacheStruct:
+    k, v, ks, vs = cache
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("the cache's codes must be 4-D [pages, kv_heads, page_size, head_dim]")
+    shape = k.shape
+    return KvCacheStruct(_cuda(k, _CODES, shape, "cache.k"), _cuda(v, _CODES, shape, "cache.v"),
+                         _cuda(ks, _F32, shape[:3], "cache.k_scale"), _cuda(vs, _F32, shape[:3], "cache.v_scale"),
+                         shape[0], shape[2], shape[1], shape[3])
+
+
+def _heads(t, heads, dim: int, name: str) -> int:
+    """Checks a bf16 [tokens, heads, dim] tensor whose tokens may be apart (columns of wider rows); its token stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bf16 CUDA tensor")
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, heads, {dim}], got {tuple(t.shape)}")
+    token, head, one = t.stride()
+    if one != 1 or (head != dim and t.shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return token if t.shape[0] > 1 else max(token, t.shape[1] * dim)
+
+
+def fp8_kv_append(k, v, slots, cache, stream=None) -> None:
+    """Quantise bf16 k, v [T, kv_heads, head_dim] into the cache's slots (int64 [T], negative = skip)."""
+    c = _cache_struct(cache)
+    ks, vs = _heads(k, c.kv_heads, c.head_dim, "k"), _heads(v, c.kv_heads, c.head_dim, "v")
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v have different numbers of tokens")
+    _check("fp8_kv_append", load().fp8_kv_append(k.data_ptr(), v.data_ptr(), _cuda(slots, _I64, (T,), "slots"), T, ks,
+                                                 vs, ctypes.byref(c), _stream(stream)))
+
+
+_workspaces: dict = {}
+
+
+def _workspace(nbytes: int, device, stream: ctypes.c_void_p) -> torch.Tensor:
+    """A zeroed workspace kept per device and stream (calls of one stream share it)."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)  # belongs to the graph
+    key = (device, stream.value)
+    w = _workspaces.get(key)
+    if w is None or w.numel() < nbytes:
+        w = _workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    return w
+
+
+def kv_attention_workspace(max_q_len: int, q_heads: int, cache) -> int:
+    """Bytes of workspace fp8_kv_attention needs."""
+    return int(load().fp8_kv_attention_workspace(max_q_len, q_heads, ctypes.byref(_cache_struct(cache))))
+
+
+def fp8_kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len: int | None = None,
+                     softmax_scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
+    """bf16 [tokens, q_heads, head_dim] = causal attention of the new tokens q over the cache.
+
+    page_table int32 [B, max_pages], kv_lens int32 [B] (cached tokens, the new ones included),
+    cu_q int32 [B + 1] (rows of q per sequence). max_q_len (the most new tokens of a sequence)
+    picks the row tile; softmax_scale defaults to head_dim ** -0.5. `lse` (fp32 [tokens, q_heads])
+    is filled if given. `workspace`: a zeroed uint8 tensor of kv_attention_workspace() bytes, kept
+    by the caller per stream; without one the binding keeps its own per device and stream."""
+    c = _cache_struct(cache)
+    qs = _heads(q, None, c.head_dim, "q")
+    T, Hq, D = q.shape
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be 2-D [B, max_pages]")
+    B, max_pages = page_table.shape
+    if max_q_len is None:
+        max_q_len = 1 if T == B else T
+    out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+    st, L = _stream(stream), load()
+    need = L.fp8_kv_attention_workspace(max_q_len, Hq, ctypes.byref(c))
+    if workspace is None:
+        workspace = _workspace(max(need, 16), q.device, st)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor")
+    _check("fp8_kv_attention", L.fp8_kv_attention(
+        q.data_ptr(), qs, _cuda(cu_q, _I32, (B + 1,), "cu_q"), _cuda(kv_lens, _I32, (B,), "kv_lens"),
+        _cuda(page_table, _I32, (B, max_pages), "page_table"), max_pages, B, T, max_q_len, Hq,
+        D ** -0.5 if softmax_scale is None else softmax_scale, ctypes.byref(c), _cuda(out, _BF16, (T, Hq, D), "out"),
+        None if lse is None else _cuda(lse, _F32, (T, Hq), "lse"), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), st))
+    return out
+
+
+def verify_drafts(target_logits, draft_tokens, uniform, noise, temperature, draft_logits=None, n_draft=None,
+                  accepted=None, tokens=None, accept_prob=None, stream=None):
+    """Speculative sampling of drafted tokens -> (accepted int32 [B], tokens int32 [B, k+1], accept_prob fp32 [B, k]).
+
+    target_logits [B, k+1, V] and draft_logits [B, k, V] (None: greedy drafts) bf16 or fp32,
+    draft_tokens int32 [B, k], uniform fp32 [B, k], noise fp32 [B, V] (exponential, rate 1),
+    temperature fp32 [B] (0 = greedy), n_draft int32 [B] (None: k each)."""
+    if target_logits.dim() != 3:
+        raise ValueError("target_logits must be [B, k + 1, V]")
+    B, rows, V = target_logits.shape
+    k, kind, dev = rows - 1, (target_logits.dtype,), target_logits.device
+    accepted = torch.empty(B, dtype=torch.int32, device=dev) if accepted is None else accepted
+    tokens = torch.empty((B, rows), dtype=torch.int32, device=dev) if tokens is None else tokens
+    accept_prob = torch.empty((B, k), dtype=torch.float32, device=dev) if accept_prob is None else accept_prob
+    _check("fp8act_verify_drafts", load().fp8act_verify_drafts(
+        _cuda(target_logits, _BF16 + _F32, (B, rows, V), "target_logits"),
+        None if draft_logits is None else _cuda(draft_logits, kind, (B, k, V), "draft_logits"),
+        int(kind[0] == torch.float32), _cuda(draft_tokens, _I32, (B, k), "draft_tokens"),
+        _cuda(uniform, _F32, (B, k), "uniform"), _cuda(noise, _F32, (B, V), "noise"),
+        _cuda(temperature, _F32, (B,), "temperature"),
+        None if n_draft is None else _cuda(n_draft, _I32, (B,), "n_draft"), B, k, V,
+        _cuda(accepted, _I32, (B,), "accepted"), _cuda(tokens, _I32, (B, rows), "tokens"),
+        _cuda(accept_prob, _F32, (B, k), "accept_prob"), _stream(stream)))
+    return accepted, tokens, accept_prob
 
 
 def check_status(stream=None) -> int:

@@ -1,5 +1,6 @@
 /*
- * fp8act.h - C ABI of libfp8act.so, the W8A8 block-FP8 linear layer for GB300 (sm_103a).
+ * fp8act.h - C ABI of libfp8act.so, the W8A8 block-FP8 linear layer for GB300 (sm_103a),
+ * and the operators of a served decoder that stand between such layers.
  *
  * The layer: y = x W^T with x [M, K] quantised per token in 1x128 K groups and
  * W [N, K] quantised per 128x128 block, both to FP8 E4M3 with one fp32 scale
@@ -47,6 +48,7 @@
 #endif
 
 #include <stddef.h>
+#include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
@@ -61,7 +63,9 @@ typedef enum {
     FP8ACT_ERR_LAUNCH = 4,   /* the kernel launch failed (cudaGetLastError)       */
     FP8ACT_ERR_TIMEOUT = 5,  /* a kernel's bounded wait gave up (see check_status) */
     FP8ACT_ERR_DEVICE = 6,   /* no current device, or not compute capability 10.3 */
-    FP8ACT_ERR_CUDA = 7      /* another CUDA runtime error                         */
+    FP8ACT_ERR_CUDA = 7,     /* another CUDA runtime error                         */
+    FP8ACT_ERR_INDEX = 8     /* a device-side slot, page, length or token index was out
+                                of range (see check_status)                         */
 } fp8act_status;
 
 /*
@@ -231,16 +235,147 @@ FP8ACT_API int fp8_act_quant_grouped(const fp8act_quant_problem* problems, int c
 FP8ACT_API int fp8_block_gemm_grouped(const fp8act_gemm_problem* problems, int count, void* stream);
 FP8ACT_API int fp8_block_gemm_grouped_f32(const fp8act_gemm_problem* problems, int count, void* stream);
 
+/*
+ * Operators between the linear layers
+ * -----------------------------------
+ * One decode or draft-verify step of a decoder layer runs
+ *   fp8_rmsnorm_quant -> fp8_block_gemm (q, k, v) -> fp8_kv_append ->
+ *   fp8_kv_attention -> fp8_act_quant -> fp8_block_gemm -> fp8_rmsnorm_quant ->
+ *   fp8_block_gemm (gate, up) -> fp8_silu_mul_quant -> fp8_block_gemm,
+ * and after the vocabulary head fp8act_verify_drafts. They follow the
+ * conventions above (device pointers, no allocation, capturable, launched with
+ * programmatic dependent launch; every input but fp8_rmsnorm_quant's weight
+ * is read after the previous kernel on the stream has completed).
+ * Index arrays live on the device, so the library checks them there: an index
+ * out of range is never followed, and is reported by fp8act_check_status() as
+ * FP8ACT_ERR_INDEX.
+ */
+
+/*
+ * Residual addition, RMS norm and activation quantisation in one pass:
+ *   h = x + residual (fp32; h = x without a residual), residual_out = bf16(h),
+ *   y = h * rsqrt(mean(h^2) + eps) * (weight + weight_offset)   (fp32),
+ *   sa = max|y| / 448 over each 128 columns (1 if that is 0), q = E4M3(y / sa).
+ * y is quantised as it is, with no rounding to bf16 between.
+ *   x, residual, residual_out [M, K] bf16 (residual and residual_out: both or
+ *   neither NULL; residual_out may be x or residual); weight [K] bf16;
+ *   q [M, K]; sa [M, K/128]; K a multiple of 128, at most 32768.
+ */
+FP8ACT_API int fp8_rmsnorm_quant(const void* x_bf16, const void* residual_bf16, const void* weight_bf16, float eps,
+                                 float weight_offset, int M, int K, void* q_e4m3, float* sa, void* residual_out_bf16,
+                                 void* stream);
+
+/*
+ * Gated activation and quantisation: y = g / (1 + exp(-g)) * u (fp32) with
+ * [g | u] the rows of gate_up [M, 2 I] bf16, quantised as above into q [M, I]
+ * and sa [M, I/128]. I is a multiple of 128.
+ */
+FP8ACT_API int fp8_silu_mul_quant(const void* gate_up_bf16, int M, int I, void* q_e4m3, float* sa, void* stream);
+
+/*
+ * The paged E4M3 key / value cache. The caller owns the four buffers:
+ *   k_e4m3, v_e4m3   [num_pages, kv_heads, page_size, head_dim] codes
+ *   k_scale, v_scale [num_pages, kv_heads, page_size] fp32, one scale per
+ *                    token and head; a value is code * scale
+ * page_size is 16, 32, 64, 128 or 256, head_dim 64, 128 or 256, all four
+ * buffers 16-byte aligned. Slot s is place s % page_size of page s / page_size.
+ */
+typedef struct {
+    void* k_e4m3;
+    void* v_e4m3;
+    float* k_scale;
+    float* v_scale;
+    int num_pages, page_size, kv_heads, head_dim;
+} fp8act_kv_cache;
+
+/*
+ * Quantise new keys and values into the cache: token t's goes to slot
+ * slots[t]; a negative slot (padding) is skipped, and its input is not read.
+ * The scale and codes of a head vector follow the activation rule over
+ * head_dim values (bit-exact with the IEEE division). A vector with a NaN or
+ * an infinity is stored as zero codes with a NaN scale. Two tokens with one
+ * slot leave either's values.
+ *   k, v   [T, kv_heads, head_dim] bf16, tokens k_stride / v_stride elements
+ *          apart (multiples of 8, at least kv_heads * head_dim)
+ *   slots  [T] int64
+ */
+FP8ACT_API int fp8_kv_append(const void* k_bf16, const void* v_bf16, const int64_t* slots, int T, int64_t k_stride,
+                             int64_t v_stride, const fp8act_kv_cache* cache, void* stream);
+
+/*
+ * Attention of new tokens over the cache, for any number of new tokens per
+ * sequence: decode (1), draft verify (k + 1), prompt chunks. Sequence b's new
+ * tokens are rows cu_q[b] .. cu_q[b + 1] of q; they are the last of its
+ * kv_lens[b] cached tokens (append them first), and new token i of n sees the
+ * positions <= kv_lens[b] - n + i. Query head h reads KV head
+ * h / (q_heads / kv_heads).
+ *   out[t, h] = softmax_j(softmax_scale * q[t, h] . k[j]) v[j]     (bf16)
+ *   lse[t, h] = log sum_j exp(softmax_scale * q[t, h] . k[j])      (fp32, may be NULL)
+ * A row that sees nothing (kv_lens[b] = 0, or fewer cached than new tokens)
+ * gets zeros and lse = -infinity. Slots at or past kv_lens[b] are never read.
+ * A NaN in a cached token reaches the rows that see it and no other.
+ *   q          [tokens, q_heads, head_dim] bf16, tokens q_stride elements apart
+ *   cu_q       [batch + 1] int32, cu_q[0] = 0, non-decreasing
+ *   kv_lens    [batch] int32, at most max_pages * page_size
+ *   page_table [batch, max_pages] int32
+ *   max_q_len  the most new tokens of a sequence, a hint: it sizes the row
+ *              tiles and the workspace, any value gives the same results to
+ *              rounding
+ *   workspace  fp8_kv_attention_workspace(...) bytes, 16-byte aligned, zeroed
+ *              once by the caller; the calls leave its counters zero, so calls
+ *              of one stream share it, two streams do not
+ * q_heads is a multiple of kv_heads (at most 256 times it). Results do not
+ * depend on timing. Errors beside the usual: FP8ACT_ERR_SHAPE for a workspace
+ * that is too small.
+ */
+FP8ACT_API int fp8_kv_attention(const void* q_bf16, int64_t q_stride, const int* cu_q, const int* kv_lens,
+                                const int* page_table, int max_pages, int batch, int tokens, int max_q_len,
+                                int q_heads, float softmax_scale, const fp8act_kv_cache* cache, void* out_bf16,
+                                float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for fp8_kv_attention; 0 for arguments it would refuse. */
+FP8ACT_API size_t fp8_kv_attention_workspace(int max_q_len, int q_heads, const fp8act_kv_cache* cache);
+
+/*
+ * Verification of drafted tokens (speculative sampling) from given random
+ * numbers. p_j = softmax(target[b, j] / T), q_j = softmax(draft[b, j] / T)
+ * with T = temperature[b]; with draft == NULL the drafts were chosen greedily
+ * and q_j is 1 at the drafted token. Draft x_j (j < n_draft[b]) is accepted
+ * while uniform[b, j] < accept_prob[b, j] = min(1, p_j(x_j) / q_j(x_j)). After
+ * the a accepted drafts comes one token more: argmax_v w_v / noise[b, v] over
+ * w_v > 0, with w = max(p_a - q_a, 0) if draft a was rejected (p_a where that
+ * is zero everywhere), w = p_a if all were accepted; equal quotients go to the
+ * lowest v. With exponential noise of rate 1 that draws v in proportion to w.
+ * T <= 0 decodes greedily: p_j is 1 at target row j's first largest logit, a
+ * draft is accepted if it is that token, and noise is not read.
+ * A logit of -infinity or NaN is masked; a row with nothing left accepts no
+ * draft and draws token -1.
+ *   target       [B, k + 1, V] bf16 (fp32 with logits_f32), contiguous
+ *   draft        [B, k, V] of the same type, or NULL
+ *   draft_tokens [B, k] int32; uniform [B, k] fp32 in [0, 1)
+ *   noise        [B, V] fp32, positive; temperature [B] fp32
+ *   n_draft      [B] int32 drafts of each sequence, 0 .. k, or NULL for k
+ *   accepted     [B] int32 out: a
+ *   tokens       [B, k + 1] int32 out: the a accepted drafts, the drawn token, -1s
+ *   accept_prob  [B, k] fp32 out (0 past n_draft), or NULL
+ * k is at most 32, V at most 134217712.
+ */
+FP8ACT_API int fp8act_verify_drafts(const void* target, const void* draft, int logits_f32, const int* draft_tokens,
+                                    const float* uniform, const float* noise, const float* temperature,
+                                    const int* n_draft, int B, int k, int V, int* accepted, int* tokens,
+                                    float* accept_prob, void* stream);
+
 /* A static English description of a status code (never NULL). */
 FP8ACT_API const char* fp8act_strerror(int status);
 
 /*
  * Synchronises `stream` and reports whether any kernel of this library on the
- * current device gave up a bounded wait since the last call (FP8ACT_ERR_TIMEOUT),
- * then clears the flag. The flag is one word per device, shared by every
- * stream: a timeout in a kernel on another stream is reported here too (and
- * cleared), and work still running on other streams may set it after the
- * call returns. Returns FP8ACT_ERR_CUDA if the stream itself failed.
+ * current device gave up a bounded wait since the last call (FP8ACT_ERR_TIMEOUT)
+ * or met a device-side index out of range (FP8ACT_ERR_INDEX; a timeout is
+ * reported first), then clears the flags. A flag is one word per device,
+ * shared by every stream: a timeout in a kernel on another stream is reported
+ * here too (and cleared), and work still running on other streams may set it
+ * after the call returns. Returns FP8ACT_ERR_CUDA if the stream itself failed.
  * Not capturable (it synchronises); meant for tests and health checks.
  */
 FP8ACT_API int fp8act_check_status(void* stream);
