@@ -382,7 +382,9 @@ int fp8_kv_attention(const void* q_bf16, int64_t q_stride, const int* cu_q, cons
         static_cast<int64_t>(max_pages) << c.page_log2 > 0x7FFFFF00 ||
         static_cast<int64_t>(tokens) * (q_heads / c.heads) > 0x7FFFFF00)
         return FP8ACT_ERR_SHAPE;
+    if (!(softmax_scale > 0.0f) || softmax_scale > 3e38f) return FP8ACT_ERR_SHAPE;
     if (batch == 0 || tokens == 0) return FP8ACT_OK;
+    if (c.num_pages == 0) return FP8ACT_ERR_SHAPE;
     if (!q_bf16 || !cu_q || !kv_lens || !out_bf16 || !workspace || (max_pages > 0 && !page_table))
         return FP8ACT_ERR_NULL;
     if (!aligned(q_bf16, 16) || q_stride % 8 || !aligned(out_bf16, 16) || !aligned(workspace, 16) || !aligned(cu_q, 4) ||

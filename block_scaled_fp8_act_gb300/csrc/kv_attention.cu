@@ -7,25 +7,35 @@
 //   O[r]    = sum_j P[r, j] s_v[j] v_j.
 //
 // Arithmetic. Codes widen exactly to f16 (cvt.rn.f16x2.e4m3x2), so both
-// products run as f16 MMAs with fp32 accumulation. A query row is scaled by a
-// power of two so that its largest value is in [1, 2): bf16 then fits f16
-// exactly down to 2^-17 of the largest value, and below that to within 2^-25
-// of it. The value product's weights p * s_v are rounded to f16 (11 bits; bf16
-// would give 8) after scaling by 2^14 / R, R the power of two below the
-// largest s_v so far: they keep full precision down to 2^-28 of the largest
-// weight. Maxima, sums, and both accumulations are fp32.
+// products run as f16 MMAs with fp32 accumulation. (The warp-level E4M3 MMA is
+// built from f16 ones with conversions and fp32 additions by the compiler:
+// queries as pairs of E4M3 rows took 106 us where f16 takes XX, at 8 tokens
+// over 131072.) Both are transposed, S^T = K Q^T and O^T = V^T W^T, so that the
+// cached tokens and the output columns are the MMA's 16 rows and the query rows
+// its 8 columns: a decode step of 6 or 8 heads fills them. A query row is
+// scaled by a power of two so that its largest value is in [1, 2): bf16 then
+// fits f16 exactly down to 2^-17 of the largest value, and below that to
+// within 2^-25 of it. The weights W = p * s_v are rounded to f16 (11 bits; bf16
+// would give 8) after scaling by 2^6 / R, R the power of two below the largest
+// s_v so far: they keep full precision down to 2^-20 of the largest weight. The
+// running maximum moves only when a score passes it by 8 (in log2), so that
+// the accumulators are seldom rescaled; a weight then stays below 2^15. Maxima, sums, and both accumulations are fp32.
 //
-// Work split. A row tile is kMT * 16 rows of (new token, query head of one KV
-// head); a unit is one row tile x 64 cached tokens. The units of all
-// sequences, KV heads and row tiles form one list, which the CTAs of a fixed
-// grid share evenly: no host knowledge of the lengths is needed and a ragged
-// batch balances itself. A CTA whose range ends inside a (sequence, head, row
-// tile) item leaves an fp32 partial in the workspace; the last CTA to arrive
-// at the item adds the parts in a fixed order, so results do not depend on
-// timing.
+// Work split. A row tile is up to 192 rows of (new token, query head of one KV
+// head); a unit is one row tile x 32 cached tokens. The units of all
+// sequences, KV heads and row tiles form one list, which one CTA per SM shares
+// evenly: no host knowledge of the lengths is needed and a ragged batch
+// balances itself. An item (sequence, head, row tile) counts kItemCost units
+// more than it has, about what its start and end cost, so that short ones
+// spread out. In a CTA, groups of warps take an item's units in turn, each with
+// its own ring of cached tokens and its own running softmax; a group's warps
+// share a ring and split the rows. The groups join in shared memory. An item
+// that crosses CTAs leaves fp32 parts in the workspace, which a second kernel,
+// launched dependently, adds in unit order: results do not depend on timing.
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "decoder_util.cuh"
 #include "kernels.h"
@@ -35,9 +45,12 @@ namespace {
 
 __device__ unsigned int g_attn_index_error;
 
-constexpr int kTile = 64;     // cached tokens per unit
-constexpr int kThreads = 128;
+constexpr int kTile = 32;  // cached tokens per unit
+constexpr int kLeastUnits = 8;  // least share of a CTA
+constexpr int kItemCost = 12;   // units that an item counts beside its own
 constexpr float kNegInf = -__builtin_huge_valf();
+
+struct SplitItem;
 
 struct AttnArgs {
     const uint16_t* q;
@@ -53,8 +66,12 @@ struct AttnArgs {
     float* lse;      // [tokens, heads * group] or null
     float* part_o;   // [2 * grid][rows][D]
     float* part_ml;  // [2 * grid][rows][2]
-    int* counters;   // [grid]
-    int min_units;
+    SplitItem* split;  // [grid]: the item that starts in a CTA and goes on in the next
+};
+
+struct __align__(16) SplitItem {
+    int parts, second;  // CTAs it spans (0: no such item); whether its part of the first CTA is that CTA's second
+    int q0, h, row0, nrows, pad[2];
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
@@ -69,8 +86,8 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
 }
 
-// Two E4M3 codes (low 16 bits of `codes`) to f16x2, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+// Two E4M3 codes (the low or the high 16 bits of `codes`) to f16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_lo_to_f16x2(uint32_t codes) {
     uint32_t r;
     asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(r) : "r"(codes));
     return r;
@@ -81,50 +98,66 @@ __device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t codes) {
     return r;
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit values held as an MMA fragment.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 
-__device__ __forceinline__ uint4 ldmatrix_x4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-// Byte offset of 16-byte chunk c of cached token `row` in a stage. The chunk
-// index is permuted by the token so that both the key fragments (8 tokens x 4
-// chunks) and the value fragments (tokens 2q + const, the same chunk) read
-// distinct banks.
+// A stage holds the cached codes as 128-byte lines, as the cache does (a token
+// is half a line, a line or two); chunk c of a line sits at c ^ (line % 8).
+// Byte offset of 16-byte chunk c of
+// token `row`:
 template <int kD>
 __device__ __forceinline__ uint32_t stage_offset(int row, int c) {
-    const int swz = kD == 64 ? (row >> 1) & 3 : ((row & 1) << 2) ^ (((row >> 1) & 3) << 1);
-    return row * kD + ((c ^ swz) << 4);
+    const int line = kD == 64 ? row >> 1 : kD == 128 ? row : row * 2 + (c >> 3);
+    const int chunk = kD == 64 ? ((row & 1) << 2) | c : c & 7;
+    return line * 128 + ((chunk ^ (line & 7)) << 4);
 }
 
-template <int kD, int kMT>
-struct AttnSmem {
-    static constexpr int kRows = kMT * 16;
-    static constexpr int kStages = kD == 256 ? 2 : 3;
+// The MMA's rows are the cached tokens of a block of 8 in an order of our own:
+// row i is token order<kD>(i). The 8 lanes of a shared-memory phase read 4
+// chunks of 2 neighbouring rows; the order gives those two tokens swizzles
+// that differ in bit 2, so that they read distinct banks.
+template <int kD>
+__device__ __forceinline__ int order(int i) {
+    if (kD == 64) return i;
+    if (kD == 128) return (i >> 1) | ((i & 1) << 2);
+    return ((i >> 1) & 1) | ((i & 1) << 1) | (i & 4);
+}
+
+// kWR warps of a group split the row tile, kRW groups of 8 rows each; kG groups.
+template <int kD, int kWR, int kRW, int kG>
+struct Attn {
+    static constexpr int kWarpRows = kRW * 8;
+    static constexpr int kRows = kWR * kWarpRows;
+    static constexpr int kWarps = kWR * kG;
+    static constexpr int kThreads = kWarps * 32;
     static constexpr int kStageBytes = 2 * kTile * kD + 2 * kTile * 4;  // keys, values, key scales, value scales
-    static constexpr int kPStride = kTile + 8;                          // halves; 144 bytes: ldmatrix without conflicts
-    static constexpr int kQ = kStages * kStageBytes;
-    static constexpr int kP = kQ + kRows * kD * 2;
-    static constexpr int kRed = kP + kRows * kPStride * 2;
-    static constexpr int kQScale = kRed + 4 * kRows * 4;
-    static constexpr int kBytes = kQScale + kRows * 4;
+    static constexpr int kQ = 0;
+    static constexpr int kML = kQ + kRows * kD * 2;
+    static constexpr int kQScale = kML + kG * kRows * 8;
+    static constexpr int kRing = (kQScale + kRows * 4 + 127) / 128 * 128;
+    static constexpr int kFit = (226 * 1024 - kRing) / kG / kStageBytes;
+    static constexpr int kStages = kFit < 8 ? kFit : kFit < 16 && kG > 1 ? 8 : kFit < 16 ? kFit : 16;
+    static constexpr int kRingBytes = kStages * kStageBytes;
+    static constexpr int kOStride = kD + 4;  // floats of a row of a group's result, which replaces its ring at the end
+    static_assert(kStages >= 2 && kRows * kOStride * 4 <= kRingBytes, "a stage in flight, and room for the result");
+    static constexpr int kBytes = kRing + kG * kRingBytes;
 };
 
 // One (sequence, KV head, row tile) and where it lies in the unit list.
 struct Item {
     int b, h, rt;      // sequence, KV head, row tile
     int nq, q0, len;   // new tokens, first one's row in q, cached tokens
-    int rts, tiles;    // row tiles and units per row tile of this sequence
+    int rts, tiles;    // row tiles of this sequence and units of each, kItemCost included
     int64_t first;     // index of the item's first unit
 };
 
@@ -141,75 +174,101 @@ __device__ __forceinline__ void load_sequence(const AttnArgs& a, int rows, int b
     }
     it.len = len;
     it.rts = (it.nq * a.group + rows - 1) / rows;
-    it.tiles = (len + kTile - 1) / kTile;
-    if (it.tiles == 0) it.tiles = 1;  // an empty sequence still writes its rows
+    it.tiles = (len + kTile - 1) / kTile + kItemCost;  // (an empty sequence still writes its rows)
 }
 
-template <int kD, int kMT>
-__global__ void __launch_bounds__(kThreads) kv_attention_kernel(const __grid_constant__ AttnArgs a) {
-    using S = AttnSmem<kD, kMT>;
-    constexpr int kRows = S::kRows;
-    constexpr int kKS = kD / 16;   // k-steps of the score product
-    constexpr int kNT = kD / 32;   // 8-column tiles of the output per warp
+__device__ __forceinline__ uint32_t scale_exponent(float s) {
+    const uint32_t e = __float_as_uint(s) & 0x7F800000u;
+    return e == 0x7F800000u ? 0u : e;
+}
+
+// Units per CTA: an even share, but not less than is worth a part of an item.
+__device__ __forceinline__ int64_t units_per_cta(int64_t total, int least) {
+    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    return per < least ? least : per;
+}
+
+// One finished row: lane's kD / 32 columns of sum p s_v v, the row's maximum (log2) and sum of p.
+template <int kD>
+__device__ __forceinline__ void write_row(const AttnArgs& a, int q0, int h, int row, int lane, float m, float sum,
+                                          const float (&o)[kD / 32]) {
+    const int qi = row / a.group, hg = row - qi * a.group;
+    const int64_t at = static_cast<int64_t>(q0 + qi) * (a.c.heads * a.group) + h * a.group + hg;
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int x = 0; x < kD / 32; x += 2) a.out[(at * kD + lane * (kD / 32) + x) >> 1] = pack_bf16x2(o[x] * f, o[x + 1] * f);
+    if (a.lse && lane == 0) a.lse[at] = sum == 0.0f ? kNegInf : (m + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <int kD, int kWR, int kRW, int kG>
+__global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG>::kThreads, 1) kv_attention_kernel(const __grid_constant__ AttnArgs a) {
+    using S = Attn<kD, kWR, kRW, kG>;
+    constexpr int kRows = S::kRows, kStages = S::kStages;
+    constexpr int kKS = kD / 32;  // pairs of k-steps of the score product
+    constexpr int kDT = kD / 16;  // 16-row tiles of the transposed output
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_total;
     __shared__ int s_b;
     __shared__ int64_t s_first;
-    __shared__ int s_last;
-    const uint32_t sbase = ptx::smem_u32(smem);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, qd = lane & 3;
-    float* red = reinterpret_cast<float*>(smem + S::kRed);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
+    const int og = order<kD>(g);                  // the token of a block of 8 that is the lane's MMA row
+    const int vg = kD == 64 ? g : order<128>(g);  // the chunk of output columns that is the lane's (the same reason)
+    const int group = warp / kWR, wr = warp % kWR;
+    uint8_t* const ring = smem + S::kRing + group * S::kRingBytes;
     float* qscale = reinterpret_cast<float*>(smem + S::kQScale);
+    float2* ml = reinterpret_cast<float2*>(smem + S::kML);
+    auto group_sync = [&]() {
+        if constexpr (kWR == 1)
+            __syncwarp();
+        else
+            ptx::named_bar_sync(1 + group, kWR * 32);
+    };
 
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
 
     // Total units, and the sequence that holds this CTA's first one.
-    if (warp == 0) {
+    if (threadIdx.x < 32) {
+        auto units_of = [&](int b) -> int64_t {
+            if (b >= a.batch) return 0;
+            Item it;
+            load_sequence(a, kRows, b, it);
+            return static_cast<int64_t>(a.c.heads) * it.rts * it.tiles;
+        };
+        const int64_t u_lane = units_of(lane);
         int64_t total = 0;
         for (int b0 = 0; b0 < a.batch; b0 += 32) {
-            int64_t u = 0;
-            if (b0 + lane < a.batch) {
-                Item it;
-                load_sequence(a, kRows, b0 + lane, it);
-                u = static_cast<int64_t>(a.c.heads) * it.rts * it.tiles;
-            }
+            int64_t n = b0 == 0 ? u_lane : units_of(b0 + lane);
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-            total += u;
+            for (int o = 16; o >= 1; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            total += n;
         }
-        int64_t per = (total + gridDim.x - 1) / gridDim.x;
-        if (per < a.min_units) per = a.min_units;
-        const int64_t u0 = per * blockIdx.x;
+        const int64_t u0 = units_per_cta(total, kLeastUnits) * blockIdx.x;
         int64_t base = 0;
-        if (lane == 0) s_b = a.batch;
         for (int b0 = 0; b0 < a.batch && u0 < total; b0 += 32) {
-            int64_t u = 0;
-            if (b0 + lane < a.batch) {
-                Item it;
-                load_sequence(a, kRows, b0 + lane, it);
-                u = static_cast<int64_t>(a.c.heads) * it.rts * it.tiles;
-            }
-            int64_t incl = u;
+            const int64_t n = b0 == 0 ? u_lane : units_of(b0 + lane);
+            int64_t incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += v;
             }
-            const int64_t lo = base + incl - u;
-            if (u0 >= lo && u0 < lo + u) {
+            const int64_t lo = base + incl - n;
+            if (u0 >= lo && u0 < lo + n) {
                 s_b = b0 + lane;
                 s_first = lo;
             }
-            base = __shfl_sync(0xffffffffu, base + incl, 31);
+            base += __shfl_sync(0xffffffffu, incl, 31);
             if (base > u0) break;
         }
-        if (lane == 0) s_total = total;
+        if (lane == 0) {
+            s_total = total;
+            a.split[blockIdx.x].parts = 0;
+        }
     }
     __syncthreads();
     const int64_t total = s_total;
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < a.min_units) per = a.min_units;
+    const int64_t per = units_per_cta(total, kLeastUnits);
     int64_t u = per * blockIdx.x;
     const int64_t u_end = u + per < total ? u + per : total;
     if (u >= u_end) return;
@@ -232,18 +291,66 @@ __global__ void __launch_bounds__(kThreads) kv_attention_kernel(const __grid_con
         const int rows_total = it.nq * a.group;
         const int row0 = it.rt * kRows;
         const int nrows = rows_total - row0 < kRows ? rows_total - row0 : kRows;
-        // Tokens that some row of the tile sees; the units past them are empty.
-        const int last_q = (row0 + nrows - 1) / a.group;
-        int seen = it.len - it.nq + last_q + 1;
-        if (seen < 0) seen = 0;
-        const int t_stop = (seen + kTile - 1) / kTile < t1 ? (seen + kTile - 1) / kTile : t1;
+        // This CTA's tiles [f0, f1): units past the item's cost, as far as some row of the tile sees.
+        const int seen = max(it.len - it.nq + (row0 + nrows - 1) / a.group + 1, 0);
+        const int f0 = max(t0 - kItemCost, 0), f1 = min((seen + kTile - 1) / kTile, t1 - kItemCost);
+
+        // The group's tiles are f0 + group, + kG, ... Pages of its next 16, one per 16 tokens and lane.
+        const int* table = a.table + it.b * a.table_stride;
+        auto look_up = [&](int t) -> int {
+            t += (lane >> 1) * kG;
+            const int pos = t * kTile + (lane & 1) * 16;
+            if (t >= f1 || pos >= it.len) return -1;
+            const int p = ld_dep_s32(table + (pos >> a.c.page_log2));
+            if (p >= 0 && p < a.c.num_pages) return p;
+            atomicOr(&g_attn_index_error, 1u);
+            return -1;
+        };
+        int pages = look_up(f0 + group), asked = 0;
+        // Request the group's next tile, t, into `stage`: the group's warps share the 16-byte chunks.
+        auto request = [&](int t, int stage) {
+            if (t < f1) {
+                const int p0 = __shfl_sync(0xffffffffu, pages, 2 * asked), p1 = __shfl_sync(0xffffffffu, pages, 2 * asked + 1);
+                const uint32_t dst = ptx::smem_u32(ring) + stage * S::kStageBytes;
+                constexpr int kC = kD / 16, kStep = 32 / kC;  // chunks per token, tokens per instruction
+                const int c = lane % kC, r0 = lane / kC;
+                const int pos0 = t * kTile, in_page = (1 << a.c.page_log2) - 1;
+                const int64_t row_a = ((static_cast<int64_t>(p0) * a.c.heads + it.h) << a.c.page_log2) + (pos0 & in_page);
+                const int64_t row_b =
+                    ((static_cast<int64_t>(p1) * a.c.heads + it.h) << a.c.page_log2) + ((pos0 + 16) & in_page) - 16;
+                const int end_a = p0 >= 0 ? it.len - pos0 : 0, end_b = p1 >= 0 ? it.len - pos0 : 0;  // tokens there are
+#pragma unroll
+                for (int j = 0; j < 32 / kStep; ++j) {
+                    if (kWR > 1 && j % kWR != wr) continue;
+                    const int row = j * kStep + r0;
+                    const bool first = j * kStep < 16;
+                    const bool in = row < (first ? end_a : end_b);
+                    const int64_t at = in ? ((first ? row_a : row_b) + row) * kD + c * 16 : 0;
+                    const uint32_t off = dst + stage_offset<kD>(row, c);
+                    cp_async16(off, a.c.k + at, in);
+                    cp_async16(off + kTile * kD, a.c.v + at, in);
+                }
+                if (wr == 0) {
+                    const bool in = lane < (lane < 16 ? end_a : end_b);
+                    const int64_t at = in ? (lane < 16 ? row_a : row_b) + lane : 0;
+                    cp_async4(dst + 2 * kTile * kD + lane * 4, a.c.k_scale + at, in);
+                    cp_async4(dst + 2 * kTile * kD + kTile * 4 + lane * 4, a.c.v_scale + at, in);
+                }
+                if (++asked == 16) {
+                    asked = 0;
+                    pages = look_up(t + kG);
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < kStages - 1; ++i) request(f0 + group + i * kG, i);
 
         // Queries: power-of-two scaled f16 in fragment order.
-        __syncthreads();
         {
             constexpr int kLanes = kD / 8;
-            const int c = tid % kLanes;
-            for (int r = tid / kLanes; r < kRows; r += kThreads / kLanes) {
+            const int c = threadIdx.x % kLanes;
+            for (int r = threadIdx.x / kLanes; r < kRows; r += S::kWarps * 32 / kLanes) {
                 uint4 x = make_uint4(0, 0, 0, 0);
                 if (r < nrows) {
                     const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
@@ -253,347 +360,280 @@ __global__ void __launch_bounds__(kThreads) kv_attention_kernel(const __grid_con
                                         __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
                 top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
-                for (int o = (kLanes < 32 ? kLanes : 32) / 2; o >= 1; o >>= 1)
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                uint32_t e = top >> 7;
-                if (e > 253) e = 253;
+                for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(__activemask(), top, o));
+                // (a zero row's exponent is as good as any)
+                const uint32_t e = top == 0 ? 127 : min(max(top >> 7, 1u), 253u);
                 const float up = __uint_as_float((254 - e) << 23);  // 2^(127 - e)
-                if (c == 0) qscale[r] = __uint_as_float(e << 23) * a.scale_log2;
+                if (c == 0) qscale[r] = fmaxf(__uint_as_float(e << 23) * a.scale_log2, 0x1p-126f);
                 float f[8];
                 unpack_bf16x8(x, f);
-                const int i = c / 8, qq = (c % 8) / 2, w0 = (c & 1) * 2;
-                const int l = (r & 7) * 4 + qq, reg = (r & 15) >= 8 ? 1 : 0;
+                uint32_t h[4];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const __half2 hh = __floats2half2_rn(f[2 * p] * up, f[2 * p + 1] * up);
-                    const int ks = i * 4 + w0 + (p >> 1);
-                    const int at = (((r >> 4) * kKS + ks) * 32 + l) * 4 + reg + (p & 1) * 2;
-                    reinterpret_cast<uint32_t*>(smem + S::kQ)[at] = *reinterpret_cast<const uint32_t*>(&hh);
+                for (int j = 0; j < 4; ++j) {
+                    const __half2 v = __floats2half2_rn(f[2 * j] * up, f[2 * j + 1] * up);
+                    h[j] = *reinterpret_cast<const uint32_t*>(&v);
                 }
+                // d = 8c .. 8c + 7: two k-steps of lane (r & 7, (c % 8) / 2)
+                const int ks = (c / 8) * 2 + (c & 1);
+                reinterpret_cast<uint4*>(smem + S::kQ)[((r >> 3) * kKS + ks) * 32 + (r & 7) * 4 + (c % 8) / 2] =
+                    make_uint4(h[0], h[1], h[2], h[3]);
             }
         }
-        const int64_t page_bytes = static_cast<int64_t>(kD) << a.c.page_log2;
-        const int* table = a.table + it.b * a.table_stride;
-        // Pages of the next tile to request: one per 16 cached tokens.
-        int page[4];
-        auto look_up = [&](int t) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int pos = t * kTile + j * 16;
-                page[j] = -1;
-                if (t < t_stop && pos < it.len) {
-                    const int p = ld_dep_s32(table + (pos >> a.c.page_log2));
-                    if (p >= 0 && p < a.c.num_pages)
-                        page[j] = p;
-                    else if (tid == 0)
-                        atomicOr(&g_attn_index_error, 1u);
-                }
-            }
-        };
-        auto request = [&](int t, int stage) {
-            if (t < t_stop) {
-                const uint32_t dst = sbase + stage * S::kStageBytes;
-                constexpr int kC = kD / 16;
-                const int c = tid % kC;
-#pragma unroll
-                for (int i = 0; i < kTile * kC / kThreads; ++i) {
-                    const int row = tid / kC + i * (kThreads / kC);
-                    const int pos = t * kTile + row;
-                    const int p = kThreads / kC > 16 ? (tid / kC < 16 ? page[2 * i] : page[2 * i + 1]) : page[i * (kThreads / kC) / 16];
-                    const bool in = p >= 0 && pos < it.len;
-                    const int64_t at = in ? (static_cast<int64_t>(p) * a.c.heads + it.h) * page_bytes +
-                                                (pos & ((1 << a.c.page_log2) - 1)) * kD + c * 16
-                                          : 0;
-                    const uint32_t off = stage_offset<kD>(row, c);
-                    cp_async16(dst + off, a.c.k + at, in);
-                    cp_async16(dst + kTile * kD + off, a.c.v + at, in);
-                }
-                const int row = tid & 63, pos = t * kTile + row;
-                const int p = row < 32 ? (row < 16 ? page[0] : page[1]) : (row < 48 ? page[2] : page[3]);
-                const bool in = p >= 0 && pos < it.len;
-                const int64_t at = in ? ((static_cast<int64_t>(p) * a.c.heads + it.h) << a.c.page_log2) +
-                                            (pos & ((1 << a.c.page_log2) - 1))
-                                      : 0;
-                cp_async4(dst + 2 * kTile * kD + tid * 4, (tid < 64 ? a.c.k_scale : a.c.v_scale) + at, in);
-            }
-            cp_async_commit();
-        };
+        __syncthreads();
 
-        float acc[kMT][kNT][4];
-        float m[kMT][2], l[kMT][2], r_ref = 0x1p-100f;
+        float acc[kDT][kRW][4];
+        // m: largest (q . k) s_k of rows 2q, 2q + 1 of each 8, not yet times qs
+        float m[kRW][2], l[kRW][2], qs[kRW][2], r_ref = 0x1p-100f;
+        int limit[kRW][2];  // first position that the row does not see
 #pragma unroll
-        for (int i = 0; i < kMT; ++i) {
+        for (int i = 0; i < kRW; ++i) {
 #pragma unroll
-            for (int j = 0; j < kNT; ++j)
+            for (int j = 0; j < kDT; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
-            m[i][0] = m[i][1] = kNegInf;
-            l[i][0] = l[i][1] = 0.0f;
-        }
-        int limit[kMT][2];  // first position that the row does not see
-#pragma unroll
-        for (int i = 0; i < kMT; ++i)
+                for (int e = 0; e < 4; ++e) acc[j][i][e] = 0.0f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = row0 + i * 16 + g + e * 8;
-                limit[i][e] = it.len - it.nq + r / a.group + 1;
+                const int r = wr * S::kWarpRows + i * 8 + qd * 2 + e;
+                m[i][e] = kNegInf;
+                l[i][e] = 0.0f;
+                qs[i][e] = qscale[r];
+                limit[i][e] = it.len - it.nq + (row0 + r) / a.group + 1;
             }
-
-#pragma unroll
-        for (int s = 0; s < S::kStages - 1; ++s) {
-            look_up(t0 + s);
-            request(t0 + s, s);
         }
-        look_up(t0 + S::kStages - 1);
+        const int all_see = it.len - it.nq + row0 / a.group + 1;  // positions below it need no mask
+        const uint4* qf = reinterpret_cast<const uint4*>(smem + S::kQ) + wr * kRW * kKS * 32 + lane;
+
         int stage = 0;
-        for (int t = t0; t < t_stop; ++t) {
-            cp_async_wait<S::kStages - 2>();
-            __syncthreads();
-            {
-                const int next = stage + S::kStages - 1;
-                request(t + S::kStages - 1, next >= S::kStages ? next - S::kStages : next);
-                look_up(t + S::kStages);
-            }
-            const uint8_t* kt = smem + stage * S::kStageBytes;
+        for (int t = f0 + group; t < f1; t += kG) {
+            cp_async_wait<kStages - 2>();
+            group_sync();  // the tile is there, and the stage before it is free
+            request(t + (kStages - 1) * kG, stage == 0 ? kStages - 1 : stage - 1);
+            const uint8_t* kt = ring + stage * S::kStageBytes;
             const uint8_t* vt = kt + kTile * kD;
             const float* sk = reinterpret_cast<const float*>(kt + 2 * kTile * kD);
             const float* sv = sk + kTile;
 
-            // Scores of this warp's 16 tokens.
-            float s[kMT][2][4];
+            // S^T of 2 x 16 tokens: s[x][i] rows are tokens 16x + g, + 8, columns query rows 2q, 2q + 1.
+            float s[2][kRW][4];
 #pragma unroll
-            for (int i = 0; i < kMT; ++i)
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int i = 0; i < kRW; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i][j][e] = 0.0f;
+                    for (int e = 0; e < 4; ++e) s[x][i][e] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kD / 64; ++i) {
-                uint4 kw[2];
+            for (int w = 0; w < kD / 64; ++w) {
+                uint4 ka[2][2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    kw[j] = *reinterpret_cast<const uint4*>(kt + stage_offset<kD>(warp * 16 + j * 8 + g, i * 4 + qd));
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint32_t b[2][2];
+                    for (int y = 0; y < 2; ++y)
+                        ka[x][y] = *reinterpret_cast<const uint4*>(kt + stage_offset<kD>(x * 16 + y * 8 + og, w * 4 + qd));
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t v = w == 0 ? kw[j].x : w == 1 ? kw[j].y : w == 2 ? kw[j].z : kw[j].w;
-                        b[j][0] = e4m3x2_to_f16x2(v);
-                        b[j][1] = e4m3x2_hi_to_f16x2(v);
-                    }
+                for (int z = 0; z < 4; ++z) {  // 4 codes of a chunk: one k-step
+                    uint32_t af[2][4];
 #pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt) {
-                        const uint4 qa = reinterpret_cast<const uint4*>(smem + S::kQ)[(mt * kKS + i * 4 + w) * 32 + lane];
-                        mma_f16(s[mt][0], qa, b[0][0], b[0][1]);
-                        mma_f16(s[mt][1], qa, b[1][0], b[1][1]);
-                    }
-                }
-            }
-            // Scale, mask, and the tile's maximum per row.
+                    for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int col = warp * 16 + j * 8 + qd * 2;
-                const float2 ks = *reinterpret_cast<const float2*>(sk + col);
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t v = z == 0 ? ka[x][y].x : z == 1 ? ka[x][y].y : z == 2 ? ka[x][y].z : ka[x][y].w;
+                            af[x][y] = e4m3x2_lo_to_f16x2(v);
+                            af[x][y + 2] = e4m3x2_hi_to_f16x2(v);
+                        }
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float qs = qscale[mt * 16 + g + (e >> 1) * 8];
-                        const float v = s[mt][j][e] * ((e & 1) ? ks.y : ks.x) * qs;
-                        s[mt][j][e] = t * kTile + col + (e & 1) < limit[mt][e >> 1] ? v : kNegInf;
+                    for (int i = 0; i < kRW; ++i) {
+                        const uint2 b = reinterpret_cast<const uint2*>(qf + (i * kKS + w * 2 + (z >> 1)) * 32)[z & 1];
+                        mma_f16(s[0][i], af[0], b.x, b.y);
+                        mma_f16(s[1][i], af[1], b.x, b.y);
                     }
                 }
             }
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x = fmaxf(fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]), fmaxf(s[mt][1][2 * e], s[mt][1][2 * e + 1]));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                    if (qd == 0) red[warp * kRows + mt * 16 + g + e * 8] = x;
-                }
-            // The largest value scale of the tile, as a power of two.
-            float r_new = fmaxf(sv[lane], sv[lane + 32]);
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) r_new = fmaxf(r_new, __shfl_xor_sync(0xffffffffu, r_new, o));
-            r_new = fmaxf(__uint_as_float(__float_as_uint(r_new) & 0x7F800000u), r_ref);
-            const float r_inv = 0x1p14f / r_new;
-            const float r_step = r_ref / r_new;
+            // The tile's largest value scale as a power of two (a NaN scale marks a poisoned token).
+            const uint32_t rb = __reduce_max_sync(0xffffffffu, scale_exponent(sv[lane]));
+            const float r_new = fmaxf(__uint_as_float(rb), r_ref);
+            const float r_step = __fdividef(r_ref, r_new), r_inv = __fdividef(0x1p6f, r_new);
             r_ref = r_new;
-            __syncthreads();
+            float ks[4], vs[4];
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
+            for (int x = 0; x < 4; ++x) {
+                ks[x] = sk[x * 8 + og];
+                vs[x] = sv[x * 8 + og] * r_inv;
+            }
+            uint32_t wb[2][kRW][2];  // weights as the B operand
+            float beta[kRW][2];
+            // Key scales, mask, running maximum, weights p * s_v and sums. A tile that every row sees whole
+            // needs no mask.
+            auto softmax = [&](auto edge) {
+                constexpr bool kEdge = decltype(edge)::value;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = mt * 16 + g + e * 8;
-                    const float x = fmaxf(fmaxf(red[r], red[kRows + r]), fmaxf(red[2 * kRows + r], red[3 * kRows + r]));
-                    const float m_new = fmaxf(m[mt][e], x);
-                    const float m_use = m_new == kNegInf ? 0.0f : m_new;
-                    const float alpha = ex2(m[mt][e] - m_use);
-                    m[mt][e] = m_new;
-                    const float beta = alpha * r_step;
+                for (int i = 0; i < kRW; ++i) {
+                    float mq[2];
 #pragma unroll
-                    for (int j = 0; j < kNT; ++j) {
-                        acc[mt][j][2 * e] *= beta;
-                        acc[mt][j][2 * e + 1] *= beta;
+                    for (int e = 0; e < 2; ++e) {
+                        float top = kNegInf;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            float& v = s[x >> 1][i][(x & 1) * 2 + e];
+                            v *= ks[x];
+                            if (kEdge && t * kTile + x * 8 + og >= limit[i][e]) v = kNegInf;
+                            top = fmaxf(top, v);
+                        }
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        // the reference moves only when the maximum passes it by 2^8
+                        const float m_new = (top - m[i][e]) * qs[i][e] > 8.0f ? top : m[i][e];
+                        mq[e] = (kEdge && m_new == kNegInf ? 0.0f : m_new) * qs[i][e];
+                        const float alpha = m_new == m[i][e] ? 1.0f : ex2(fmaf(m[i][e], qs[i][e], -mq[e]));
+                        m[i][e] = m_new;
+                        beta[i][e] = alpha * r_step;
+                        l[i][e] *= alpha;
                     }
-                    float sum = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int col = warp * 16 + j * 8 + qd * 2;
-                        const float2 vs = *reinterpret_cast<const float2*>(sv + col);
-                        const float s0 = s[mt][j][2 * e], s1 = s[mt][j][2 * e + 1];
-                        const float p0 = ex2(s0 - m_use), p1 = ex2(s1 - m_use);
-                        sum += p0 + p1;
-                        // a masked weight is zero whatever its scale holds
-                        const __half2 w = __floats2half2_rn(s0 == kNegInf ? 0.0f : p0 * (vs.x * r_inv),
-                                                            s1 == kNegInf ? 0.0f : p1 * (vs.y * r_inv));
-                        *reinterpret_cast<__half2*>(smem + S::kP + (r * S::kPStride + col) * 2) = w;
-                    }
-                    l[mt][e] = l[mt][e] * alpha + sum;
-                }
-            __syncthreads();
-            // Output columns [warp * D/4, ...) += weights x values.
-#pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks) {
-                uint32_t vw[4][kNT / 4 ? kNT / 4 : 1];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int row = ks * 16 + qd * 2 + (x & 1) + (x >> 1) * 8;
-                    const int d = warp * (kD / 4) + g * kNT;
-                    const uint8_t* p = vt + stage_offset<kD>(row, d >> 4) + (d & 15);
-                    if constexpr (kNT == 2) {
-                        vw[x][0] = *reinterpret_cast<const uint16_t*>(p);
-                    } else if constexpr (kNT == 4) {
-                        vw[x][0] = *reinterpret_cast<const uint32_t*>(p);
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2*>(p);
-                        vw[x][0] = v.x;
-                        vw[x][1] = v.y;
+                    for (int x = 0; x < 4; ++x) {
+                        const float s0 = s[x >> 1][i][(x & 1) * 2], s1 = s[x >> 1][i][(x & 1) * 2 + 1];
+                        const float p0 = ex2(fmaf(s0, qs[i][0], -mq[0])), p1 = ex2(fmaf(s1, qs[i][1], -mq[1]));
+                        l[i][0] += p0;
+                        l[i][1] += p1;
+                        float w0 = p0 * vs[x], w1 = p1 * vs[x];
+                        if (kEdge) {  // a masked weight is zero whatever its scale holds
+                            if (s0 == kNegInf) w0 = 0.0f;
+                            if (s1 == kNegInf) w1 = 0.0f;
+                        }
+                        const __half2 h = __floats2half2_rn(w0, w1);
+                        wb[x >> 1][i][x & 1] = movmatrix(*reinterpret_cast<const uint32_t*>(&h));
                     }
                 }
-                uint32_t b[kNT][2];
+            };
+            if (t * kTile + kTile > all_see)
+                softmax(std::true_type{});
+            else
+                softmax(std::false_type{});
+            bool moved = false;
 #pragma unroll
-                for (int n = 0; n < kNT; n += 2) {
-                    const int wi = n / 4;
-                    const uint32_t sel = (n & 2) ? 0x7362u : 0x5140u;
-                    const uint32_t lo = __byte_perm(vw[0][wi], vw[1][wi], sel);
-                    const uint32_t hi = __byte_perm(vw[2][wi], vw[3][wi], sel);
-                    b[n][0] = e4m3x2_to_f16x2(lo);
-                    b[n][1] = e4m3x2_to_f16x2(hi);
-                    b[n + 1][0] = e4m3x2_hi_to_f16x2(lo);
-                    b[n + 1][1] = e4m3x2_hi_to_f16x2(hi);
-                }
+            for (int i = 0; i < kRW; ++i) moved = moved || beta[i][0] != 1.0f || beta[i][1] != 1.0f;
+            if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) {
-                    const uint4 pa = ldmatrix_x4(sbase + S::kP +
-                                                 ((mt * 16 + (lane & 15)) * S::kPStride + ks * 16 + (lane >> 4) * 8) * 2);
+                for (int j = 0; j < kDT; ++j)
 #pragma unroll
-                    for (int n = 0; n < kNT; ++n) mma_f16(acc[mt][n], pa, b[n][0], b[n][1]);
+                    for (int i = 0; i < kRW; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j][i][e] *= beta[i][e & 1];
+            }
+            // O^T += V^T W^T. Lane (g, q) reads the tokens of MMA columns 2q, 2q + 1, 2q + 8, 2q + 9 of each 16;
+            // its bytes 2j and 2j + 1 are rows g and g + 8 of output tile j.
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                constexpr int kParts = kD == 256 ? 2 : 1, kWords = kD == 64 ? 2 : 4;
+#pragma unroll
+                for (int h = 0; h < kParts; ++h) {
+                    uint32_t vw[4][kWords];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int row = x * 16 + (y >> 1) * 8 + order<kD>(qd * 2 + (y & 1));
+                        if constexpr (kD == 64) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(vt + stage_offset<kD>(row, g >> 1) + (g & 1) * 8);
+                            vw[y][0] = v.x;
+                            vw[y][1] = v.y;
+                        } else {
+                            const uint4 v = *reinterpret_cast<const uint4*>(vt + stage_offset<kD>(row, h * 8 + vg));
+                            vw[y][0] = v.x;
+                            vw[y][1] = v.y;
+                            vw[y][2] = v.z;
+                            vw[y][3] = v.w;
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2 * kWords; ++j) {
+                        const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+                        const uint32_t lo = __byte_perm(vw[0][j >> 1], vw[1][j >> 1], sel);
+                        const uint32_t hi = __byte_perm(vw[2][j >> 1], vw[3][j >> 1], sel);
+                        const uint32_t va[4] = {e4m3x2_lo_to_f16x2(lo), e4m3x2_hi_to_f16x2(lo), e4m3x2_lo_to_f16x2(hi),
+                                                e4m3x2_hi_to_f16x2(hi)};
+#pragma unroll
+                        for (int i = 0; i < kRW; ++i) mma_f16(acc[h * 8 + j][i], va, wb[x][i][0], wb[x][i][1]);
+                    }
                 }
             }
-            stage = stage + 1 == S::kStages ? 0 : stage + 1;
+            stage = stage + 1 == kStages ? 0 : stage + 1;
         }
         cp_async_wait<0>();
-        // Row sums over the four warps' tokens.
-        __syncthreads();
+        group_sync();
+
+        // The group's result, in place of its ring: o = sum p s_v v and, per row, its maximum (log2) and sum of p.
+        float mx[kRW][2];
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
+        for (int i = 0; i < kRW; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float x = l[mt][e];
-                x += __shfl_xor_sync(0xffffffffu, x, 1);
-                x += __shfl_xor_sync(0xffffffffu, x, 2);
-                if (qd == 0) red[warp * kRows + mt * 16 + g + e * 8] = x;
+                l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 4);
+                l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 8);
+                l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 16);
+                mx[i][e] = m[i][e] == kNegInf ? kNegInf : m[i][e] * qs[i][e];
+            }
+        const float r_out = r_ref * 0x1p-6f;
+        // Column of output tile j's row g (row g + 8 is the next one).
+        constexpr int kRun = kD == 64 ? 8 : 16;  // consecutive columns of a lane
+        auto column = [&](int j) { return (j / (kRun / 2)) * 128 + vg * kRun + (j % (kRun / 2)) * 2; };
+#pragma unroll
+        for (int i = 0; i < kRW; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = wr * S::kWarpRows + i * 8 + qd * 2 + e;
+                float* o = reinterpret_cast<float*>(ring) + r * S::kOStride;
+#pragma unroll
+                for (int j = 0; j < kDT; j += 2)
+                    *reinterpret_cast<float4*>(o + column(j)) =
+                        make_float4(acc[j][i][e] * r_out, acc[j][i][e + 2] * r_out, acc[j + 1][i][e] * r_out,
+                                    acc[j + 1][i][e + 2] * r_out);
+                if (g == 0) ml[group * kRows + r] = make_float2(mx[i][e], l[i][e]);
             }
         __syncthreads();
+
         const bool whole = t0 == 0 && t1 == it.tiles;
-        const float r_out = r_ref * 0x1p-14f;
         const int slot = 2 * blockIdx.x + (it.first > u_begin ? 1 : 0);
-        const int hq = a.c.heads * a.group;
+        constexpr int kV = kD / 32;  // columns per lane
+        for (int r = warp; r < nrows; r += S::kWarps) {
+            float mm = kNegInf, sum = 0.0f, o[kV];
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
+            for (int j = 0; j < kG; ++j) mm = fmaxf(mm, ml[j * kRows + r].x);
+            const float m_use = mm == kNegInf ? 0.0f : mm;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = mt * 16 + g + e * 8;
-                if (r >= nrows) continue;
-                const float sum = (red[r] + red[kRows + r]) + (red[2 * kRows + r] + red[3 * kRows + r]);
-                if (whole) {
-                    const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
-                    const int64_t orow = static_cast<int64_t>(it.q0 + qi) * hq + it.h * a.group + hg;
-                    const float f = sum == 0.0f ? 0.0f : r_out / sum;
+            for (int x = 0; x < kV; ++x) o[x] = 0.0f;
 #pragma unroll
-                    for (int n = 0; n < kNT; n += 2) {
+            for (int j = 0; j < kG; ++j) {
+                const float2 t = ml[j * kRows + r];
+                const float f = ex2(t.x - m_use);
+                sum = fmaf(t.y, f, sum);
+                const float* src =
+                    reinterpret_cast<const float*>(smem + S::kRing + j * S::kRingBytes) + r * S::kOStride + lane * kV;
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int d = warp * (kD / 4) + (2 * qd + x) * kNT + n;
-                            a.out[(orow * kD + d) >> 1] =
-                                pack_bf16x2(acc[mt][n][2 * e + x] * f, acc[mt][n + 1][2 * e + x] * f);
-                        }
-                    }
-                    if (a.lse && warp == 0 && qd == 0)
-                        a.lse[orow] = sum == 0.0f ? kNegInf : (m[mt][e] + log2f(sum)) * 0.6931471805599453f;
-                } else {
-                    float* po = a.part_o + (static_cast<int64_t>(slot) * kRows + r) * kD;
-#pragma unroll
-                    for (int n = 0; n < kNT; n += 2)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            *reinterpret_cast<float2*>(po + warp * (kD / 4) + (2 * qd + x) * kNT + n) =
-                                make_float2(acc[mt][n][2 * e + x] * r_out, acc[mt][n + 1][2 * e + x] * r_out);
-                    if (warp == 0 && qd == 0)
-                        *reinterpret_cast<float2*>(a.part_ml + (static_cast<int64_t>(slot) * kRows + r) * 2) =
-                            make_float2(m[mt][e], sum);
-                }
+                for (int x = 0; x < kV; ++x) o[x] = fmaf(src[x], f, o[x]);
             }
-        if (!whole) {
-            // The last CTA to arrive at the item joins its parts, in unit order.
-            const int c0 = static_cast<int>(it.first / per), c1 = static_cast<int>((item_end - 1) / per);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int n = atomicAdd(a.counters + c0, 1);
-                s_last = n == c1 - c0;
-                if (s_last) a.counters[c0] = 0;
+            if (whole) {
+                write_row<kD>(a, it.q0, it.h, row0 + r, lane, mm, sum, o);
+            } else {
+                float* po = a.part_o + (static_cast<int64_t>(slot) * kRows + r) * kD + lane * kV;
+#pragma unroll
+                for (int x = 0; x < kV; x += 2) *reinterpret_cast<float2*>(po + x) = make_float2(o[x], o[x + 1]);
+                if (lane == 0)
+                    *reinterpret_cast<float2*>(a.part_ml + (static_cast<int64_t>(slot) * kRows + r) * 2) =
+                        make_float2(mm, sum);
             }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                constexpr int kV = kD / 32;  // columns per lane
-                for (int r = warp; r < nrows; r += kThreads / 32) {
-                    float mm = kNegInf, sum = 0.0f, o[kV];
-#pragma unroll
-                    for (int x = 0; x < kV; ++x) o[x] = 0.0f;
-                    for (int c = c0; c <= c1; ++c) {
-                        const int64_t sl = 2 * c + (c == c0 && it.first > per * c ? 1 : 0);
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + sl * kRows + r);
-                        const float m_new = fmaxf(mm, ml.x);
-                        const float m_use = m_new == kNegInf ? 0.0f : m_new;
-                        const float f0 = ex2(mm - m_use), f1 = ex2(ml.x - m_use);
-                        mm = m_new;
-                        sum = sum * f0 + ml.y * f1;
-                        const float* po = a.part_o + (sl * kRows + r) * kD + lane * kV;
-#pragma unroll
-                        for (int x = 0; x < kV; x += 2) {
-                            const float2 v = __ldcg(reinterpret_cast<const float2*>(po + x));
-                            o[x] = o[x] * f0 + v.x * f1;
-                            o[x + 1] = o[x + 1] * f0 + v.y * f1;
-                        }
-                    }
-                    const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
-                    const int64_t orow = static_cast<int64_t>(it.q0 + qi) * hq + it.h * a.group + hg;
-                    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-                    for (int x = 0; x < kV; x += 2)
-                        a.out[(orow * kD + lane * kV + x) >> 1] = pack_bf16x2(o[x] * f, o[x + 1] * f);
-                    if (a.lse && lane == 0) a.lse[orow] = sum == 0.0f ? kNegInf : (mm + log2f(sum)) * 0.6931471805599453f;
-                }
-            }
+        }
+        if (!whole && t0 == 0 && threadIdx.x == 0) {  // it starts here and goes on in the next CTA
+            SplitItem sp = {};
+            sp.parts = static_cast<int>((item_end - 1) / per) - static_cast<int>(blockIdx.x) + 1;
+            sp.second = slot & 1;
+            sp.q0 = it.q0;
+            sp.h = it.h;
+            sp.row0 = row0;
+            sp.nrows = nrows;
+            a.split[blockIdx.x] = sp;
         }
         if (item_end >= u_end) break;
         // Next item.
+        __syncthreads();
         u = item_end;
         it.first = item_end;
         if (++it.rt == it.rts) {
@@ -607,54 +647,126 @@ __global__ void __launch_bounds__(kThreads) kv_attention_kernel(const __grid_con
     }
 }
 
-constexpr int kMaxGrid = 152 * 4;
+// Adds the parts of the items that cross CTAs, a warp per row: CTA (c, y) takes
+// rows 8 y .. 8 y + 7 of the item that starts in CTA c of the first kernel.
+constexpr int kJoinRows = 8;
 
-template <int kD, int kMT>
+template <int kD, int kRows>
+__global__ void __launch_bounds__(kJoinRows * 32) kv_attention_join_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int kV = kD / 32, kAhead = 8;
+    const int lane = threadIdx.x & 31;
+    const int c = blockIdx.x, r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const SplitItem* sp = a.split + c;
+    const int parts = ld_dep_s32(&sp->parts);
+    if (parts == 0 || r >= ld_dep_s32(&sp->nrows)) return;
+    const int second = ld_dep_s32(&sp->second);
+    auto slot_of = [&](int i) { return static_cast<int64_t>(2 * (c + i) + (i == 0 ? second : 0)) * kRows + r; };
+    const float2* pml = reinterpret_cast<const float2*>(a.part_ml);
+    float mm = kNegInf;
+    for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, __ldcg(pml + slot_of(i)).x);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    const float m_use = mm == kNegInf ? 0.0f : mm;
+    float sum = 0.0f, o[kV];
+#pragma unroll
+    for (int x = 0; x < kV; ++x) o[x] = 0.0f;
+    for (int i0 = 0; i0 < parts; i0 += kAhead) {
+        float v[kAhead][kV], f[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j < parts ? i0 + j : parts - 1;
+            const float2 t = __ldcg(pml + slot_of(i));
+            f[j] = i0 + j < parts ? ex2(t.x - m_use) : 0.0f;
+            sum = i0 + j < parts ? fmaf(t.y, f[j], sum) : sum;
+            const float* src = a.part_o + slot_of(i) * kD + lane * kV;
+#pragma unroll
+            for (int x = 0; x < kV; x += 2) {
+                const float2 p = __ldcg(reinterpret_cast<const float2*>(src + x));
+                v[j][x] = p.x;
+                v[j][x + 1] = p.y;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (i0 + j < parts)
+#pragma unroll
+                for (int x = 0; x < kV; ++x) o[x] = fmaf(v[j][x], f[j], o[x]);
+    }
+    write_row<kD>(a, ld_dep_s32(&sp->q0), ld_dep_s32(&sp->h), ld_dep_s32(&sp->row0) + r, lane, mm, sum, o);
+}
+
+constexpr int kMaxGrid = 256;  // CTAs of the first kernel: one per SM
+
+template <int kD, int kWR, int kRW, int kG>
 cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t stream) {
-    using S = AttnSmem<kD, kMT>;
-    static std::atomic<int> per_sm[64];
+    using S = Attn<kD, kWR, kRW, kG>;
+    static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
-    int v = per_sm[dev & 63].load(std::memory_order_relaxed);
-    if (v == 0) {
-        cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<kD, kMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             S::kBytes);
+    auto kernel = kv_attention_kernel<kD, kWR, kRW, kG>;
+    if (!configured[dev & 63].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
         if (e != cudaSuccess) return e;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kv_attention_kernel<kD, kMT>, kThreads, S::kBytes);
-        if (e != cudaSuccess) return e;
-        if (v < 1) v = 1;
-        per_sm[dev & 63].store(v, std::memory_order_relaxed);
+        configured[dev & 63].store(true, std::memory_order_relaxed);
     }
-    int grid = num_sms * v;
-    if (grid > kMaxGrid) grid = kMaxGrid;
-    return launch_dependent(kv_attention_kernel<kD, kMT>, dim3(grid), kThreads, S::kBytes, stream, 1, a);
+    const int grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
+    const cudaError_t e = launch_dependent(kernel, dim3(grid), S::kThreads, S::kBytes, stream, 1, a);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kv_attention_join_kernel<kD, S::kRows>, dim3(grid, S::kRows / kJoinRows), kJoinRows * 32, 0,
+                            stream, 1, a);
+}
+
+// Row tiles: the smallest that holds a sequence's rows, else the largest. The
+// registers of a thread go by the CTA's warps (255 up to 8 warps, 168 up to
+// 12), and a warp needs 32 accumulators for every 8 rows x 128 columns.
+int rows_of(int max_q_len, int group, int head_dim) {
+    const int64_t rows = static_cast<int64_t>(max_q_len) * group;
+    const int wide[] = {8, 16, 24, 32, 48, 96, 192}, narrow[] = {8, 16, 32, 64};
+    if (head_dim == 256) {
+        for (int r : narrow)
+            if (rows <= r) return r;
+        return 64;
+    }
+    for (int r : wide)
+        if (rows <= r) return r;
+    return 192;
 }
 
 template <int kD>
-cudaError_t launch_attention_d(const AttnArgs& a, int mt, int num_sms, cudaStream_t stream) {
-    switch (mt) {
-        case 1: return launch_attention<kD, 1>(a, num_sms, stream);
-        case 2: return launch_attention<kD, 2>(a, num_sms, stream);
-        case 3: return launch_attention<kD, 3>(a, num_sms, stream);
-        default: return launch_attention<kD, 4>(a, num_sms, stream);
+cudaError_t launch_rows(const AttnArgs& a, int rows, int num_sms, cudaStream_t stream) {
+    switch (rows) {
+        case 8: return launch_attention<kD, 1, 1, 12>(a, num_sms, stream);
+        case 16: return launch_attention<kD, 1, 2, 12>(a, num_sms, stream);
+        case 24: return launch_attention<kD, 1, 3, 8>(a, num_sms, stream);
+        case 32: return launch_attention<kD, 2, 2, 6>(a, num_sms, stream);
+        case 48: return launch_attention<kD, 2, 3, 4>(a, num_sms, stream);
+        case 96: return launch_attention<kD, 4, 3, 2>(a, num_sms, stream);
+        default: return launch_attention<kD, 8, 3, 1>(a, num_sms, stream);
     }
 }
 
-int row_tiles_of(int max_q_len, int group) {
-    const int64_t rows = static_cast<int64_t>(max_q_len) * group;
-    return rows > 48 ? 4 : rows > 32 ? 3 : rows > 16 ? 2 : 1;
+template <>
+cudaError_t launch_rows<256>(const AttnArgs& a, int rows, int num_sms, cudaStream_t stream) {
+    switch (rows) {
+        case 8: return launch_attention<256, 1, 1, 6>(a, num_sms, stream);
+        case 16: return launch_attention<256, 1, 2, 6>(a, num_sms, stream);
+        case 32: return launch_attention<256, 2, 2, 4>(a, num_sms, stream);
+        default: return launch_attention<256, 4, 2, 2>(a, num_sms, stream);
+    }
 }
 
 }  // namespace
 
 size_t kv_attention_workspace(int max_q_len, int group, int head_dim) {
-    const size_t rows = 16 * static_cast<size_t>(row_tiles_of(max_q_len, group));
-    return kMaxGrid * 16 + 2 * static_cast<size_t>(kMaxGrid) * rows * (head_dim + 2) * sizeof(float);
+    const size_t rows = rows_of(max_q_len, group, head_dim);
+    return kMaxGrid * sizeof(SplitItem) + 2 * static_cast<size_t>(kMaxGrid) * rows * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv_attention(const AttentionProblem& p, int num_sms, cudaStream_t stream) {
-    const int mt = row_tiles_of(p.max_q_len, p.group);
-    const size_t slots = 2 * static_cast<size_t>(kMaxGrid) * 16 * mt;
+    const int rows = rows_of(p.max_q_len, p.group, p.cache.head_dim);
+    const size_t slots = 2 * static_cast<size_t>(kMaxGrid) * rows;
     AttnArgs a;
     a.q = static_cast<const uint16_t*>(p.q);
     a.q_stride = p.q_stride;
@@ -669,14 +781,13 @@ cudaError_t launch_kv_attention(const AttentionProblem& p, int num_sms, cudaStre
     a.c = p.cache;
     a.out = static_cast<uint32_t*>(p.out);
     a.lse = p.lse;
-    a.counters = static_cast<int*>(p.workspace);
-    a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kMaxGrid * 16);
+    a.split = static_cast<SplitItem*>(p.workspace);
+    a.part_ml = reinterpret_cast<float*>(a.split + kMaxGrid);
     a.part_o = a.part_ml + slots * 2;
-    a.min_units = 4;
     switch (p.cache.head_dim) {
-        case 64: return launch_attention_d<64>(a, mt, num_sms, stream);
-        case 128: return launch_attention_d<128>(a, mt, num_sms, stream);
-        default: return launch_attention_d<256>(a, mt, num_sms, stream);
+        case 64: return launch_rows<64>(a, rows, num_sms, stream);
+        case 128: return launch_rows<128>(a, rows, num_sms, stream);
+        default: return launch_rows<256>(a, rows, num_sms, stream);
     }
 }
 

@@ -393,13 +393,13 @@ _workspaces: dict = {}
 
 
 def _workspace(nbytes: int, device, stream: ctypes.c_void_p) -> torch.Tensor:
-    """A zeroed workspace kept per device and stream (calls of one stream share it)."""
+    """A workspace kept per device and stream (calls of one stream share it)."""
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)  # belongs to the graph
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)  # belongs to the graph
     key = (device, stream.value)
     w = _workspaces.get(key)
     if w is None or w.numel() < nbytes:
-        w = _workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        w = _workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return w
 
 
@@ -415,8 +415,8 @@ def fp8_kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len: int | None 
     page_table int32 [B, max_pages], kv_lens int32 [B] (cached tokens, the new ones included),
     cu_q int32 [B + 1] (rows of q per sequence). max_q_len (the most new tokens of a sequence)
     picks the row tile; softmax_scale defaults to head_dim ** -0.5. `lse` (fp32 [tokens, q_heads])
-    is filled if given. `workspace`: a zeroed uint8 tensor of kv_attention_workspace() bytes, kept
-    by the caller per stream; without one the binding keeps its own per device and stream."""
+    is filled if given. `workspace`: a uint8 tensor of kv_attention_workspace() bytes, kept by the
+    caller per stream; without one the binding keeps its own per device and stream."""
     c = _cache_struct(cache)
     qs = _heads(q, None, c.head_dim, "q")
     T, Hq, D = q.shape

@@ -321,12 +321,12 @@ FP8ACT_API int fp8_kv_append(const void* k_bf16, const void* v_bf16, const int64
  *   max_q_len  the most new tokens of a sequence, a hint: it sizes the row
  *              tiles and the workspace, any value gives the same results to
  *              rounding
- *   workspace  fp8_kv_attention_workspace(...) bytes, 16-byte aligned, zeroed
- *              once by the caller; the calls leave its counters zero, so calls
- *              of one stream share it, two streams do not
- * q_heads is a multiple of kv_heads (at most 256 times it). Results do not
- * depend on timing. Errors beside the usual: FP8ACT_ERR_SHAPE for a workspace
- * that is too small.
+ *   workspace  fp8_kv_attention_workspace(...) bytes, 16-byte aligned, of any
+ *              content; calls of one stream share it, two streams do not
+ * q_heads is a multiple of kv_heads (at most 256 times it), softmax_scale is
+ * positive and finite, the cache has a page at least. Results do not depend on
+ * timing. Errors beside the usual: FP8ACT_ERR_SHAPE for a workspace that is
+ * too small.
  */
 FP8ACT_API int fp8_kv_attention(const void* q_bf16, int64_t q_stride, const int* cu_q, const int* kv_lens,
                                 const int* page_table, int max_pages, int batch, int tokens, int max_q_len,
