@@ -200,6 +200,7 @@ int w8a16_common(const void* x, const void* w, const float* sw, int M, int N, in
 
 constexpr int kNormMaxK = 32768;  // one CTA holds a row: 1024 threads x 4 chunks of 8
 constexpr int kMaxQLen = 1 << 20;
+constexpr int kMaxVerifyB = 65535;
 
 // The cache's own rules; fills the launchers' form of it.
 int check_cache(const fp8act_kv_cache* c, fp8act::KvCache* out) {
@@ -403,22 +404,29 @@ int fp8_kv_attention(const void* q_bf16, int64_t q_stride, const int* cu_q, cons
 
 int fp8act_verify_drafts(const void* target, const void* draft, int logits_f32, const int* draft_tokens,
                          const float* uniform, const float* noise, const float* temperature, const int* n_draft, int B,
-                         int k, int V, int* accepted, int* tokens, float* accept_prob, void* stream) {
+                         int k, int V, int* accepted, int* tokens, float* accept_prob, void* workspace,
+                         size_t workspace_bytes, void* stream) {
     if (B < 0 || k < 0 || k > fp8act::kMaxDrafts || V <= 0 || V > 0x7FFFFF00 / 16) return FP8ACT_ERR_SHAPE;
-    if (B > 0x7FFFFFFF / 16) return FP8ACT_ERR_SHAPE;
+    if (B > kMaxVerifyB) return FP8ACT_ERR_SHAPE;
     if (B == 0) return FP8ACT_OK;
-    if (!target || !noise || !temperature || !accepted || !tokens || (k > 0 && (!draft_tokens || !uniform)))
+    if (!target || !noise || !temperature || !accepted || !tokens || !workspace || (k > 0 && (!draft_tokens || !uniform)))
         return FP8ACT_ERR_NULL;
     if (!aligned(target, 16) || !aligned(draft, 16) || !aligned(draft_tokens, 4) || !aligned(uniform, 4) ||
         !aligned(noise, 4) || !aligned(temperature, 4) || !aligned(n_draft, 4) || !aligned(accepted, 4) ||
-        !aligned(tokens, 4) || !aligned(accept_prob, 4))
+        !aligned(tokens, 4) || !aligned(accept_prob, 4) || !aligned(workspace, 16))
         return FP8ACT_ERR_ALIGN;
+    if (workspace_bytes < fp8act::verify_drafts_workspace(B, k)) return FP8ACT_ERR_SHAPE;
     int st = FP8ACT_OK;
-    current_device_sms(&st);
+    const int sms = current_device_sms(&st);
     if (st) return st;
     const fp8act::VerifyProblem p = {target,  k > 0 ? draft : nullptr, draft_tokens, uniform, noise, temperature,
-                                     n_draft, B, k, V, logits_f32 != 0, accepted, tokens, accept_prob};
-    return launch_status(fp8act::launch_verify_drafts(p, static_cast<cudaStream_t>(stream)));
+                                     n_draft, B, k, V, logits_f32 != 0, accepted, tokens, accept_prob, workspace};
+    return launch_status(fp8act::launch_verify_drafts(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp8act_verify_drafts_workspace(int B, int k) {
+    if (B < 0 || B > kMaxVerifyB || k < 0 || k > fp8act::kMaxDrafts) return 0;
+    return fp8act::verify_drafts_workspace(B, k);
 }
 
 const char* fp8act_strerror(int status) {

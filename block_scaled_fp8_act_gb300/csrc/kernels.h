@@ -155,9 +155,11 @@ struct VerifyProblem {
     int* accepted;
     int* tokens;
     float* accept_prob;
+    void* workspace;
 };
 constexpr int kMaxDrafts = 32;
-cudaError_t launch_verify_drafts(const VerifyProblem& p, cudaStream_t stream);
+size_t verify_drafts_workspace(int B, int k);
+cudaError_t launch_verify_drafts(const VerifyProblem& p, int num_sms, cudaStream_t stream);
 
 // Device-side words set by a page, slot, length or token index out of range.
 unsigned int read_and_clear_kv_index_error();

@@ -11,7 +11,7 @@ namespace {
 // a half-warp always holds one 128-wide quantisation group and the row is
 // read once. blockDim is a multiple of 32.
 template <int kChunks, bool kResidual>
-__global__ void rmsnorm_quant_kernel(const uint4* x, const uint4* residual, const uint4* weight, float eps,
+__global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint4* x, const uint4* residual, const uint4* weight, float eps,
                                      float weight_offset, int chunks, uint2* q, float* sa, uint4* residual_out) {
     __shared__ float part[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -24,6 +24,12 @@ __global__ void rmsnorm_quant_kernel(const uint4* x, const uint4* residual, cons
         residual_out += row * chunks;
     }
     ptx::griddep_launch_dependents();
+    uint4 wv[kChunks];  // the weight is constant: read while the previous kernel ends
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        wv[i] = c < chunks ? __ldg(weight + c) : make_uint4(0, 0, 0, 0);
+    }
     ptx::griddep_wait();
     float h[kChunks][8];
     float ss = 0.0f;
@@ -55,7 +61,7 @@ __global__ void rmsnorm_quant_kernel(const uint4* x, const uint4* residual, cons
         const int c = threadIdx.x + i * blockDim.x;
         const bool in = c < chunks;
         float w[8];
-        unpack_bf16x8(in ? __ldg(weight + c) : make_uint4(0, 0, 0, 0), w);
+        unpack_bf16x8(wv[i], w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] = h[i][j] * rstd * (w[j] + weight_offset);
         uint2 codes;
@@ -76,21 +82,41 @@ __global__ void silu_mul_quant_kernel(const uint4* gate_up, int64_t M, int group
     const int64_t step = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    for (int64_t item = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; item < items; item += step) {
-        const int64_t row = item / pairs;
-        const int g = static_cast<int>(item - row * pairs) * 2 + (lane >> 4);
-        const bool in = g < groups;
+    int64_t item = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    int64_t row = item / pairs;
+    int pair = static_cast<int>(item - row * pairs);
+    const int64_t step_rows = step / pairs;
+    const int step_pairs = static_cast<int>(step - step_rows * pairs);
+    uint4 va, vb;
+    auto load = [&]() {
+        const int g = pair * 2 + (lane >> 4);
+        const bool in = item < items && g < groups;
         const uint4* p = gate_up + row * groups * 32 + g * 16 + hl;
+        va = in ? ld_dep_stream_v4(p) : make_uint4(0, 0, 0, 0);
+        vb = in ? ld_dep_stream_v4(p + groups * 16) : make_uint4(0, 0, 0, 0);
+    };
+    load();
+    while (item < items) {
         float a[8], b[8];
-        unpack_bf16x8(in ? ld_dep_stream_v4(p) : make_uint4(0, 0, 0, 0), a);
-        unpack_bf16x8(in ? ld_dep_stream_v4(p + groups * 16) : make_uint4(0, 0, 0, 0), b);
+        unpack_bf16x8(va, a);
+        unpack_bf16x8(vb, b);
+        const int64_t at = row * groups + pair * 2 + (lane >> 4);
+        const bool in = pair * 2 + (lane >> 4) < groups;
+        item += step;  // the next item's loads run under this one's arithmetic
+        row += step_rows;
+        pair += step_pairs;
+        if (pair >= pairs) {
+            pair -= pairs;
+            ++row;
+        }
+        load();
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = __fdividef(a[j], 1.0f + __expf(-a[j])) * b[j];
         uint2 codes;
         const float s = quant_f32_group_halfwarp(a, codes);
         if (in) {
-            q[(row * groups + g) * 16 + hl] = codes;
-            if (hl == 0) sa[row * groups + g] = s;
+            q[at * 16 + hl] = codes;
+            if (hl == 0) sa[at] = s;
         }
     }
 }

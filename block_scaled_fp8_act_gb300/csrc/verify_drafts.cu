@@ -9,13 +9,15 @@
 // e, which draws v with probability w_v / sum w. No cumulative sum is taken,
 // so no draw depends on the order of one.
 //
-// One thread-block cluster per sequence; its CTAs share the vocabulary.
-// Pass 1 reads every row once for its maximum and sum (fp32, running rescale;
-// a warp per part of a row), the parts meet through distributed shared
-// memory, every CTA decides the acceptance alike, and pass 2 reads the one row
-// (or pair) drawn from, by then in L2, with the noise.
-#include <cfloat>
-
+// Two launches. The first reads every row once for its maximum and sum (fp32,
+// running rescale), rows cut into as many parts as fill the SMs a few times.
+// The second, dependent, has a thread-block cluster per sequence: its CTAs
+// join the parts and decide the acceptance alike, then share the vocabulary of
+// the one row (or pair) drawn from, by then in L2, and meet through
+// distributed shared memory for the draw. While it waits for the first it
+// prefetches the noise. (One launch with a cluster of 16 per sequence for
+// both took 20.5 us for 7 drafts at one sequence, where 16 SMs read 4.6 MB,
+// and 53 us for 34 x 2 drafts.)
 #include "decoder_util.cuh"
 #include "kernels.h"
 
@@ -24,10 +26,12 @@ namespace {
 
 __device__ unsigned int g_verify_index_error;
 
-constexpr int kThreads = 512;
+constexpr int kStatThreads = 256;
+constexpr int kStatWarps = kStatThreads / 32;
+constexpr int kThreads = 512;  // of the second kernel
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRows = 2 * kMaxDrafts + 1;
-constexpr int kMaxParts = 8;
+constexpr int kMaxParts = 32;
 constexpr int kMaxCluster = 16;
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -37,7 +41,7 @@ struct Stat {
     int at;
 };
 
-__device__ __forceinline__ float clean(float v) { return fminf(fmaxf(v, kNegInf), FLT_MAX); }  // NaN counts as masked
+__device__ __forceinline__ float clean(float v) { return fmaxf(v, kNegInf); }  // NaN counts as masked
 
 template <bool kF32>
 struct Row {
@@ -56,8 +60,8 @@ struct Row {
         const int h = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15) / kBytes;
         return h < V ? h : V;
     }
-    __device__ __forceinline__ void vec(int i, float (&f)[kPer]) const {
-        const uint4 v = ld_dep_v4(base + static_cast<int64_t>(i) * kBytes);
+    __device__ __forceinline__ uint4 raw(int i) const { return ld_dep_v4(base + static_cast<int64_t>(i) * kBytes); }
+    static __device__ __forceinline__ void widen(const uint4& v, float (&f)[kPer]) {
         if constexpr (kF32) {
             f[0] = clean(__uint_as_float(v.x));
             f[1] = clean(__uint_as_float(v.y));
@@ -93,25 +97,109 @@ __device__ __forceinline__ void better(Best& a, float key, int at) {
     }
 }
 
+// What both kernels know of a sequence.
+template <bool kF32>
+struct Sequence {
+    const uint8_t* target;
+    const uint8_t* draft;
+    int64_t row_bytes;
+    int V, targets, rows;
+    float c;  // log2(e) / temperature
+    bool greedy;
+    __device__ __forceinline__ Sequence(const VerifyProblem& p, int b) : V(p.V), targets(p.k + 1) {
+        rows = p.draft ? 2 * p.k + 1 : p.k + 1;
+        row_bytes = static_cast<int64_t>(V) * Row<kF32>::kBytes;
+        target = static_cast<const uint8_t*>(p.target) + static_cast<int64_t>(b) * targets * row_bytes;
+        draft = p.draft ? static_cast<const uint8_t*>(p.draft) + static_cast<int64_t>(b) * p.k * row_bytes : nullptr;
+    }
+    __device__ __forceinline__ void read_temperature(const VerifyProblem& p, int b) {
+        const float temp = ld_dep_f32(p.temperature + b);
+        greedy = !(temp > 0.0f);
+        c = greedy ? 1.0f : 1.4426950408889634f / temp;
+    }
+    __device__ __forceinline__ Row<kF32> row(int r) const {
+        return {r < targets ? target + r * row_bytes : draft + (r - targets) * row_bytes, V};
+    }
+};
+
+// Maximum and sum of part x of row y of sequence z.
+template <bool kF32>
+__global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const VerifyProblem p, Stat* parts) {
+    using R = Row<kF32>;
+    __shared__ Stat part[kStatWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sequence<kF32> q(p, blockIdx.z);
+    const R row = q.row(blockIdx.y);
+    const int share = blockIdx.x, shares = gridDim.x;
+    const int head = row.head(), vecs = (p.V - head) / R::kPer, tail = head + vecs * R::kPer;
+    const int v0 = static_cast<int>(static_cast<int64_t>(vecs) * share / shares);
+    const int v1 = static_cast<int>(static_cast<int64_t>(vecs) * (share + 1) / shares);
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    q.read_temperature(p, blockIdx.z);
+    Stat st = {kNegInf, 0.0f, 0x7FFFFFFF};
+    auto one = [&](int i) {
+        const Stat o = {row.at(i), 1.0f, i};
+        if (o.m > kNegInf) join(st, o, q.c);
+    };
+    if (share == 0 && static_cast<int>(threadIdx.x) < head) one(threadIdx.x);
+    // kAhead vectors are requested before the first is used.
+    constexpr int kAhead = 4;
+    for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kStatThreads * kAhead) {
+        uint4 raw[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (v + kStatThreads * u < v1) raw[u] = row.raw(head + (v + kStatThreads * u) * R::kPer);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (v + kStatThreads * u >= v1) break;
+            float f[R::kPer];
+            R::widen(raw[u], f);
+            float top = f[0];
+#pragma unroll
+            for (int j = 1; j < R::kPer; ++j) top = fmaxf(top, f[j]);
+            if (top > st.m) {
+                st.s *= st.m > kNegInf ? ex2((st.m - top) * q.c) : 0.0f;
+                st.m = top;
+                if (q.greedy) {
+                    const int i = head + (v + kStatThreads * u) * R::kPer;
+#pragma unroll
+                    for (int j = R::kPer - 1; j >= 0; --j)
+                        if (f[j] == top) st.at = i + j;
+                }
+            }
+            // (the row's values are -inf or finite, and so is st.m, unless all so far were -inf)
+            const float m = st.m > kNegInf ? st.m : 0.0f;
+#pragma unroll
+            for (int j = 0; j < R::kPer; ++j) st.s += ex2((f[j] - m) * q.c);
+        }
+    }
+    if (share == shares - 1 && tail + static_cast<int>(threadIdx.x) < p.V) one(tail + threadIdx.x);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        Stat other;
+        other.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+        other.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+        other.at = __shfl_xor_sync(0xffffffffu, st.at, o);
+        join(st, other, q.c);
+    }
+    if (lane == 0) part[warp] = st;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kStatWarps; ++i) join(st, part[i], q.c);
+        parts[(static_cast<int64_t>(blockIdx.z) * q.rows + blockIdx.y) * shares + share] = st;
+    }
+}
+
 struct VerifyShared {
-    Stat part[kMaxRows * kMaxParts];
-    Stat mine[kMaxRows];   // this CTA's share of every row (read by the cluster)
-    Stat row[kMaxRows];    // whole rows
+    Stat row[kMaxRows];
     float prob[kMaxDrafts];
-    int taken, n;
+    int taken;
     Best warp_best[kWarps];
-    Best best[2];          // this CTA's best draw (read by the cluster); one slot per pass
+    Best best[2];  // this CTA's best draw (read by the cluster); one slot per pass
     Best all;
 };
 
-__device__ __forceinline__ Stat ld_cluster_stat(const Stat* p, uint32_t rank) {
-    const uint32_t at = ptx::mapa_shared(ptx::smem_u32(p), rank);
-    Stat r;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r.m) : "r"(at) : "memory");
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r.s) : "r"(at + 4) : "memory");
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(r.at) : "r"(at + 8) : "memory");
-    return r;
-}
 __device__ __forceinline__ Best ld_cluster_best(const Best* p, uint32_t rank) {
     const uint32_t at = ptx::mapa_shared(ptx::smem_u32(p), rank);
     Best r;
@@ -121,84 +209,41 @@ __device__ __forceinline__ Best ld_cluster_best(const Best* p, uint32_t rank) {
 }
 
 template <bool kF32>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyProblem p, int cluster, int parts) {
+__global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyProblem p, const Stat* parts, int cluster,
+                                                               int shares) {
     using R = Row<kF32>;
     __shared__ VerifyShared sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.x / cluster;
     const int rank = static_cast<int>(blockIdx.x) % cluster;
     const int V = p.V, k = p.k;
-    const int targets = k + 1, rows = p.draft ? 2 * k + 1 : k + 1;
-    const int64_t row_bytes = static_cast<int64_t>(V) * R::kBytes;
-    const uint8_t* target = static_cast<const uint8_t*>(p.target) + static_cast<int64_t>(b) * targets * row_bytes;
-    const uint8_t* draft =
-        p.draft ? static_cast<const uint8_t*>(p.draft) + static_cast<int64_t>(b) * k * row_bytes : nullptr;
-    auto row_of = [&](int r) { return R{r < targets ? target + r * row_bytes : draft + (r - targets) * row_bytes, V}; };
+    Sequence<kF32> q(p, b);
+    const int targets = q.targets;
     const float* noise = p.noise + static_cast<int64_t>(b) * V;
+    const int i0 = static_cast<int>(static_cast<int64_t>(V) * rank / cluster);
+    const int i1 = static_cast<int>(static_cast<int64_t>(V) * (rank + 1) / cluster);
     ptx::griddep_launch_dependents();
+    for (int i = i0 + static_cast<int>(threadIdx.x) * 32; i < i1; i += kThreads * 32) prefetch_l2(noise + i);
     ptx::griddep_wait();
-    const float temp = ld_dep_f32(p.temperature + b);
-    const bool greedy = !(temp > 0.0f);
-    const float c = greedy ? 1.0f : 1.4426950408889634f / temp;
+    q.read_temperature(p, b);
+    const float c = q.c;
+    const bool greedy = q.greedy, draft = p.draft != nullptr;
+    auto row_of = [&](int r) { return q.row(r); };
     int n = p.n_draft ? ld_dep_s32(p.n_draft + b) : k;
     if (n < 0 || n > k) {
         if (threadIdx.x == 0) atomicOr(&g_verify_index_error, 1u);
         n = n < 0 ? 0 : k;
     }
-
-    // Pass 1: maximum and sum of this CTA's share of every row.
-    const int tasks = rows * parts;
-    for (int task = warp; task < tasks; task += kWarps) {
-        const int r = task / parts, share = rank * parts + task % parts, shares = cluster * parts;
-        const R row = row_of(r);
-        const int head = row.head(), vecs = (V - head) / R::kPer, tail = head + vecs * R::kPer;
-        const int v0 = static_cast<int>(static_cast<int64_t>(vecs) * share / shares);
-        const int v1 = static_cast<int>(static_cast<int64_t>(vecs) * (share + 1) / shares);
+    for (int r = threadIdx.x; r < q.rows; r += kThreads) {
+        const Stat* from = parts + (static_cast<int64_t>(b) * q.rows + r) * shares;
         Stat st = {kNegInf, 0.0f, 0x7FFFFFFF};
-        auto one = [&](int i) {
-            const Stat o = {row.at(i), 1.0f, i};
-            if (o.m > kNegInf) join(st, o, c);
-        };
-        if (share == 0 && lane < head) one(lane);
-        for (int v = v0 + lane; v < v1; v += 32) {
-            float f[R::kPer];
-            const int i = head + v * R::kPer;
-            row.vec(i, f);
-            float top = f[0];
-#pragma unroll
-            for (int j = 1; j < R::kPer; ++j) top = fmaxf(top, f[j]);
-            if (top > st.m) {
-                st.s *= st.m > kNegInf ? ex2((st.m - top) * c) : 0.0f;
-                st.m = top;
-                st.at = i;
-#pragma unroll
-                for (int j = R::kPer - 1; j >= 0; --j)
-                    if (f[j] == top) st.at = i + j;
-            }
-#pragma unroll
-            for (int j = 0; j < R::kPer; ++j) st.s += exp_below(f[j], st.m, c);
+        for (int i = 0; i < shares; ++i) {
+            Stat o;
+            o.m = __ldcg(&from[i].m);
+            o.s = __ldcg(&from[i].s);
+            o.at = __ldcg(&from[i].at);
+            join(st, o, c);
         }
-        if (share == shares - 1 && tail + lane < V) one(tail + lane);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            Stat other;
-            other.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-            other.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-            other.at = __shfl_xor_sync(0xffffffffu, st.at, o);
-            join(st, other, c);
-        }
-        if (lane == 0) sh.part[task] = st;
-    }
-    __syncthreads();
-    for (int r = threadIdx.x; r < rows; r += kThreads) {
-        Stat st = sh.part[r * parts];
-        for (int i = 1; i < parts; ++i) join(st, sh.part[r * parts + i], c);
-        sh.mine[r] = st;
-    }
-    ptx::cluster_sync();
-    for (int r = threadIdx.x; r < rows; r += kThreads) {
-        Stat st = ld_cluster_stat(&sh.mine[r], 0);
-        for (int i = 1; i < cluster; ++i) join(st, ld_cluster_stat(&sh.mine[r], i), c);
         sh.row[r] = st;
     }
     __syncthreads();
@@ -254,8 +299,6 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyProblem p,
         const R row = row_of(taken);
         const int skip = rest && !draft ? ld_dep_s32(p.draft_tokens + static_cast<int64_t>(b) * k + taken) : -1;
         const float inv_p = __fdiv_rn(1.0f, st.s);
-        const int i0 = static_cast<int>(static_cast<int64_t>(V) * rank / cluster);
-        const int i1 = static_cast<int>(static_cast<int64_t>(V) * (rank + 1) / cluster);
         for (int pass = 0; pass < 2; ++pass) {
             Best best = {0.0f, 0x7FFFFFFF};
             Stat sd = {0.0f, 1.0f, 0};
@@ -264,15 +307,56 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyProblem p,
                 sd = sh.row[targets + taken];
                 inv_q = sd.s > 0.0f ? __fdiv_rn(1.0f, sd.s) : 0.0f;
             }
-            for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += kThreads) {
-                float w = exp_below(row.at(i), st.m, c) * inv_p;
+            const R other = rest && draft ? row_of(targets + taken) : row;
+            auto consider = [&](float t, float d, float e, int i) {
+                float w = exp_below(t, st.m, c) * inv_p;
                 if (rest) {
                     if (draft)
-                        w -= exp_below(row_of(targets + taken).at(i), sd.m, c) * inv_q;
+                        w -= exp_below(d, sd.m, c) * inv_q;
                     else if (i == skip)
                         w = 0.0f;
                 }
-                if (w > 0.0f) better(best, __fdiv_rn(w, ld_dep_f32(noise + i)), i);
+                if (w > 0.0f) better(best, __fdiv_rn(w, e), i);
+            };
+            if (V % 8 == 0) {  // every row starts on a 16-byte boundary
+                const int n8 = V / 8;
+                const int v0 = static_cast<int>(static_cast<int64_t>(n8) * rank / cluster);
+                const int v1 = static_cast<int>(static_cast<int64_t>(n8) * (rank + 1) / cluster);
+                for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kThreads) {
+                    const int i = v * 8;
+                    uint4 n0 = ld_dep_v4(noise + i), n1 = ld_dep_v4(noise + i + 4), t[8 / R::kPer], d[8 / R::kPer];
+#pragma unroll
+                    for (int u = 0; u < 8 / R::kPer; ++u) {
+                        t[u] = row.raw(i + u * R::kPer);
+                        d[u] = other.raw(i + u * R::kPer);
+                    }
+                    const float e[8] = {__uint_as_float(n0.x), __uint_as_float(n0.y), __uint_as_float(n0.z),
+                                        __uint_as_float(n0.w), __uint_as_float(n1.x), __uint_as_float(n1.y),
+                                        __uint_as_float(n1.z), __uint_as_float(n1.w)};
+#pragma unroll
+                    for (int u = 0; u < 8 / R::kPer; ++u) {
+                        float ft[R::kPer], fd[R::kPer];
+                        R::widen(t[u], ft);
+                        R::widen(d[u], fd);
+#pragma unroll
+                        for (int j = 0; j < R::kPer; ++j) consider(ft[j], fd[j], e[u * R::kPer + j], i + u * R::kPer + j);
+                    }
+                }
+            } else {
+                constexpr int kAhead = 4;
+                for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += kAhead * kThreads) {
+                    float t[kAhead], d[kAhead], e[kAhead];
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) {
+                        const int x = i + u * kThreads < i1 ? i + u * kThreads : i;
+                        t[u] = row.at(x);
+                        d[u] = other.at(x);
+                        e[u] = ld_dep_f32(noise + x);
+                    }
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u)
+                        if (i + u * kThreads < i1) consider(t[u], d[u], e[u], i + u * kThreads);
+                }
             }
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) {
@@ -314,19 +398,29 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyProblem p,
 
 }  // namespace
 
-cudaError_t launch_verify_drafts(const VerifyProblem& p, cudaStream_t stream) {
+size_t verify_drafts_workspace(int B, int k) {
+    return static_cast<size_t>(B < 1 ? 1 : B) * (2 * k + 1) * kMaxParts * sizeof(Stat);
+}
+
+cudaError_t launch_verify_drafts(const VerifyProblem& p, int num_sms, cudaStream_t stream) {
     const int rows = p.draft ? 2 * p.k + 1 : p.k + 1;
+    // Parts of a row: about 4 CTAs of the first kernel per SM, of 2048 logits at least.
+    int shares = static_cast<int>((4 * static_cast<int64_t>(num_sms) + static_cast<int64_t>(p.B) * rows - 1) /
+                                  (static_cast<int64_t>(p.B) * rows));
+    if (shares > kMaxParts) shares = kMaxParts;
+    while (shares > 1 && p.V < 2048 * shares) --shares;
+    // CTAs of a sequence in the second: as many as stay within two per SM, of 2048 logits at least.
     int cluster = kMaxCluster;
-    while (cluster > 1 && p.V < 2048 * cluster) cluster /= 2;
-    // Parts per row: the count that keeps the CTA's warps busiest.
-    int parts = 1;
-    for (int i = 2; i <= kMaxParts; ++i)
-        if (((rows * i + kWarps - 1) / kWarps) * parts < ((rows * parts + kWarps - 1) / kWarps) * i) parts = i;
-    auto kernel = p.f32 ? verify_kernel<true> : verify_kernel<false>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    while (cluster > 1 && (p.V < 2048 * cluster || static_cast<int64_t>(p.B) * cluster > 2 * num_sms)) cluster /= 2;
+    Stat* parts = static_cast<Stat*>(p.workspace);
+    auto draw = p.f32 ? verify_draw_kernel<true> : verify_draw_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(draw, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, dim3(static_cast<unsigned>(p.B) * cluster), kThreads, 0, stream, cluster, p, cluster,
-                            parts);
+    e = launch_dependent(p.f32 ? verify_stats_kernel<true> : verify_stats_kernel<false>, dim3(shares, rows, p.B),
+                         kStatThreads, 0, stream, 1, p, parts);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(draw, dim3(static_cast<unsigned>(p.B) * cluster), kThreads, 0, stream, cluster, p, parts,
+                            cluster, shares);
 }
 
 unsigned int read_and_clear_verify_index_error() {

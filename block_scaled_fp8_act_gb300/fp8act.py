@@ -74,7 +74,9 @@ def load(build: bool = False) -> ctypes.CDLL:
     L.fp8_kv_attention.argtypes = [p, i64, p, p, p, i, i, i, i, i, f, p, p, p, p, ctypes.c_size_t, p]
     L.fp8_kv_attention_workspace.argtypes = [i, i, p]
     L.fp8_kv_attention_workspace.restype = ctypes.c_size_t
-    L.fp8act_verify_drafts.argtypes = [p, p, i, p, p, p, p, p, i, i, i, p, p, p, p]
+    L.fp8act_verify_drafts.argtypes = [p, p, i, p, p, p, p, p, i, i, i, p, p, p, p, ctypes.c_size_t, p]
+    L.fp8act_verify_drafts_workspace.argtypes = [i, i]
+    L.fp8act_verify_drafts_workspace.restype = ctypes.c_size_t
     for fn in (L.fp8_rmsnorm_quant, L.fp8_silu_mul_quant, L.fp8_kv_append, L.fp8_kv_attention,
                L.fp8act_verify_drafts, L.fp8_act_quant, L.fp8_weight_quant, L.fp8_block_gemm, L.fp8_block_gemm_f32,
                L.fp8_block_gemm_w8a16, L.fp8_block_gemm_w8a16_f32,
@@ -90,10 +92,11 @@ def strerror(status: int) -> str:
     return load().fp8act_strerror(int(status)).decode()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
+    """The cudaStream_t to launch on, as an integer (None: the current device's current stream)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream))
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _check(fn: str, status: int) -> None:
@@ -284,11 +287,11 @@ def fp8_block_gemm_grouped_f32(problems, outs=None, stream=None) -> list:
 
 def _cuda(t, dtypes, shape, name: str) -> int:
     """Checks a contiguous CUDA tensor of a known shape; its address."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
-        raise TypeError(f"{name} must be a CUDA tensor with dtype in {dtypes}")
-    if t.shape != shape or not t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_cuda:
+        if t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
         raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    raise TypeError(f"{name} must be a CUDA tensor with dtype in {dtypes}")
 
 
 _BF16, _F32, _I32, _I64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
@@ -360,22 +363,24 @@ def _cache_struct(cache) -> KvCacheStruct:
     k, v, ks, vs = cache
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("the cache's codes must be 4-D [pages, kv_heads, page_size, head_dim]")
-    shape = k.shape
+    pages, heads, page, dim = shape = k.shape
+    rows = (pages, heads, page)
     return KvCacheStruct(_cuda(k, _CODES, shape, "cache.k"), _cuda(v, _CODES, shape, "cache.v"),
-                         _cuda(ks, _F32, shape[:3], "cache.k_scale"), _cuda(vs, _F32, shape[:3], "cache.v_scale"),
-                         shape[0], shape[2], shape[1], shape[3])
+                         _cuda(ks, _F32, rows, "cache.k_scale"), _cuda(vs, _F32, rows, "cache.v_scale"),
+                         pages, page, heads, dim)
 
 
 def _heads(t, heads, dim: int, name: str) -> int:
     """Checks a bf16 [tokens, heads, dim] tensor whose tokens may be apart (columns of wider rows); its token stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a bf16 CUDA tensor")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [tokens, heads, {dim}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, heads, {dim}], got {tuple(shape)}")
     token, head, one = t.stride()
-    if one != 1 or (head != dim and t.shape[1] > 1):
+    if one != 1 or (head != dim and shape[1] > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return token if t.shape[0] > 1 else max(token, t.shape[1] * dim)
+    return token if shape[0] > 1 else max(token, shape[1] * dim)
 
 
 def fp8_kv_append(k, v, slots, cache, stream=None) -> None:
@@ -392,14 +397,13 @@ def fp8_kv_append(k, v, slots, cache, stream=None) -> None:
 _workspaces: dict = {}
 
 
-def _workspace(nbytes: int, device, stream: ctypes.c_void_p) -> torch.Tensor:
+def _workspace(nbytes: int, device, stream: int) -> torch.Tensor:
     """A workspace kept per device and stream (calls of one stream share it)."""
-    if torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)  # belongs to the graph
-    key = (device, stream.value)
-    w = _workspaces.get(key)
+    w = _workspaces.get((device, stream))
     if w is None or w.numel() < nbytes:
-        w = _workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        w = _workspaces[(device, stream)] = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return w
 
 
@@ -441,13 +445,20 @@ def fp8_kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len: int | None 
     return out
 
 
+def verify_drafts_workspace(B: int, k: int) -> int:
+    """Bytes of workspace verify_drafts needs."""
+    return int(load().fp8act_verify_drafts_workspace(B, k))
+
+
 def verify_drafts(target_logits, draft_tokens, uniform, noise, temperature, draft_logits=None, n_draft=None,
-                  accepted=None, tokens=None, accept_prob=None, stream=None):
+                  accepted=None, tokens=None, accept_prob=None, workspace=None, stream=None):
     """Speculative sampling of drafted tokens -> (accepted int32 [B], tokens int32 [B, k+1], accept_prob fp32 [B, k]).
 
     target_logits [B, k+1, V] and draft_logits [B, k, V] (None: greedy drafts) bf16 or fp32,
     draft_tokens int32 [B, k], uniform fp32 [B, k], noise fp32 [B, V] (exponential, rate 1),
-    temperature fp32 [B] (0 = greedy), n_draft int32 [B] (None: k each)."""
+    temperature fp32 [B] (0 = greedy), n_draft int32 [B] (None: k each). `workspace`: a uint8 tensor
+    of verify_drafts_workspace() bytes, kept by the caller per stream; without one the binding
+    keeps its own per device and stream."""
     if target_logits.dim() != 3:
         raise ValueError("target_logits must be [B, k + 1, V]")
     B, rows, V = target_logits.shape
@@ -455,7 +466,12 @@ def verify_drafts(target_logits, draft_tokens, uniform, noise, temperature, draf
     accepted = torch.empty(B, dtype=torch.int32, device=dev) if accepted is None else accepted
     tokens = torch.empty((B, rows), dtype=torch.int32, device=dev) if tokens is None else tokens
     accept_prob = torch.empty((B, k), dtype=torch.float32, device=dev) if accept_prob is None else accept_prob
-    _check("fp8act_verify_drafts", load().fp8act_verify_drafts(
+    L, st = load(), _stream(stream)
+    if workspace is None:
+        workspace = _workspace(L.fp8act_verify_drafts_workspace(B, k), dev, st)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor")
+    _check("fp8act_verify_drafts", L.fp8act_verify_drafts(
         _cuda(target_logits, _BF16 + _F32, (B, rows, V), "target_logits"),
         None if draft_logits is None else _cuda(draft_logits, kind, (B, k, V), "draft_logits"),
         int(kind[0] == torch.float32), _cuda(draft_tokens, _I32, (B, k), "draft_tokens"),
@@ -463,7 +479,8 @@ def verify_drafts(target_logits, draft_tokens, uniform, noise, temperature, draf
         _cuda(temperature, _F32, (B,), "temperature"),
         None if n_draft is None else _cuda(n_draft, _I32, (B,), "n_draft"), B, k, V,
         _cuda(accepted, _I32, (B,), "accepted"), _cuda(tokens, _I32, (B, rows), "tokens"),
-        _cuda(accept_prob, _F32, (B, k), "accept_prob"), _stream(stream)))
+        _cuda(accept_prob, _F32, (B, k), "accept_prob"), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), st))
     return accepted, tokens, accept_prob
 
 

@@ -348,7 +348,7 @@ FP8ACT_API size_t fp8_kv_attention_workspace(int max_q_len, int q_heads, const f
  * lowest v. With exponential noise of rate 1 that draws v in proportion to w.
  * T <= 0 decodes greedily: p_j is 1 at target row j's first largest logit, a
  * draft is accepted if it is that token, and noise is not read.
- * A logit of -infinity or NaN is masked; a row with nothing left accepts no
+ * A logit of -infinity or NaN is masked (+infinity is none); a row with nothing left accepts no
  * draft and draws token -1.
  *   target       [B, k + 1, V] bf16 (fp32 with logits_f32), contiguous
  *   draft        [B, k, V] of the same type, or NULL
@@ -358,12 +358,18 @@ FP8ACT_API size_t fp8_kv_attention_workspace(int max_q_len, int q_heads, const f
  *   accepted     [B] int32 out: a
  *   tokens       [B, k + 1] int32 out: the a accepted drafts, the drawn token, -1s
  *   accept_prob  [B, k] fp32 out (0 past n_draft), or NULL
- * k is at most 32, V at most 134217712.
+ *   workspace    fp8act_verify_drafts_workspace(B, k) bytes, 16-byte aligned,
+ *                of any content; calls of one stream share it, two streams do
+ *                not (FP8ACT_ERR_SHAPE if it is too small)
+ * k is at most 32, B at most 65535, V at most 134217712.
  */
 FP8ACT_API int fp8act_verify_drafts(const void* target, const void* draft, int logits_f32, const int* draft_tokens,
                                     const float* uniform, const float* noise, const float* temperature,
                                     const int* n_draft, int B, int k, int V, int* accepted, int* tokens,
-                                    float* accept_prob, void* stream);
+                                    float* accept_prob, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for fp8act_verify_drafts; 0 for arguments it would refuse. */
+FP8ACT_API size_t fp8act_verify_drafts_workspace(int B, int k);
 
 /* A static English description of a status code (never NULL). */
 FP8ACT_API const char* fp8act_strerror(int status);

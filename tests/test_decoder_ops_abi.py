@@ -106,11 +106,16 @@ def test_attention_argument_checks(lib):
 def test_verify_argument_checks(lib):
     f = lib.fp8act_verify_drafts
 
-    def call(t=A16, d=A16, f32=0, x=A16, u=A16, e=A16, temp=A16, n=None, B=1, k=2, V=100, a=A16, out=A16, pr=None):
-        return f(t, d, f32, x, u, e, temp, n, B, k, V, a, out, pr, None)
+    def call(t=A16, d=A16, f32=0, x=A16, u=A16, e=A16, temp=A16, n=None, B=1, k=2, V=100, a=A16, out=A16, pr=None,
+             ws=A16, size=1 << 40):
+        return f(t, d, f32, x, u, e, temp, n, B, k, V, a, out, pr, ws, size, None)
+    need = lib.fp8act_verify_drafts_workspace(1, 2)
+    assert 0 < need < lib.fp8act_verify_drafts_workspace(34, 2)
+    assert lib.fp8act_verify_drafts_workspace(1, 33) == 0 and lib.fp8act_verify_drafts_workspace(-1, 2) == 0
+    assert call(size=need - 1) == SHAPE and call(B=65536) == SHAPE and call(ws=A16 + 4) == ALIGN
     assert call(k=33) == SHAPE and call(k=-1) == SHAPE and call(V=0) == SHAPE and call(B=-1) == SHAPE
     assert call(t=None, B=0) == OK
-    for name in ("t", "x", "u", "e", "temp", "a", "out"):
+    for name in ("t", "x", "u", "e", "temp", "a", "out", "ws"):
         assert call(**{name: None}) == NULL, name
     assert call(t=A16 + 2) == ALIGN and call(d=A16 + 8) == ALIGN and call(e=A16 + 2) == ALIGN
     assert call(pr=A16 + 1) == ALIGN
@@ -138,4 +143,5 @@ def test_a_call_without_a_gb300_is_refused(lib):
     assert lib.fp8_kv_append(A16, A16, A16, 1, 256, 256, ctypes.byref(c), None) == DEVICE
     assert lib.fp8_kv_attention(A16, 1024, A16, A16, A16, 4, 1, 1, 1, 8, 0.1, ctypes.byref(c), A16, None, A16, 1 << 40,
                                 None) == DEVICE
-    assert lib.fp8act_verify_drafts(A16, None, 0, A16, A16, A16, A16, None, 1, 2, 100, A16, A16, None, None) == DEVICE
+    assert lib.fp8act_verify_drafts(A16, None, 0, A16, A16, A16, A16, None, 1, 2, 100, A16, A16, None, A16, 1 << 40,
+                                    None) == DEVICE
