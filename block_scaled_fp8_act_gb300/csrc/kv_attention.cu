@@ -649,52 +649,67 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG>::kThreads, 1) kv_attent
 
 // Adds the parts of the items that cross CTAs, a warp per row: CTA (c, y) takes
 // rows 8 y .. 8 y + 7 of the item that starts in CTA c of the first kernel.
+// Latency is all it is: the item's record is one load, then every lane fetches
+// the maximum and sum of its own parts while the rows of 16 parts are on their
+// way.
 constexpr int kJoinRows = 8;
 
 template <int kD, int kRows>
 __global__ void __launch_bounds__(kJoinRows * 32) kv_attention_join_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int kV = kD / 32, kAhead = 8;
+    constexpr int kV = kD / 32, kAhead = 128 / kV / 2;
     const int lane = threadIdx.x & 31;
     const int c = blockIdx.x, r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const SplitItem* sp = a.split + c;
-    const int parts = ld_dep_s32(&sp->parts);
-    if (parts == 0 || r >= ld_dep_s32(&sp->nrows)) return;
-    const int second = ld_dep_s32(&sp->second);
+    const uint4 s0 = ld_dep_v4(a.split + c), s1 = ld_dep_v4(reinterpret_cast<const uint4*>(a.split + c) + 1);
+    const int parts = static_cast<int>(s0.x), second = static_cast<int>(s0.y);
+    if (parts == 0 || r >= static_cast<int>(s1.y)) return;
     auto slot_of = [&](int i) { return static_cast<int64_t>(2 * (c + i) + (i == 0 ? second : 0)) * kRows + r; };
     const float2* pml = reinterpret_cast<const float2*>(a.part_ml);
-    float mm = kNegInf;
-    for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, __ldcg(pml + slot_of(i)).x);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    const float m_use = mm == kNegInf ? 0.0f : mm;
-    float sum = 0.0f, o[kV];
+    float mm = kNegInf, sum = 0.0f, o[kV];
 #pragma unroll
     for (int x = 0; x < kV; ++x) o[x] = 0.0f;
-    for (int i0 = 0; i0 < parts; i0 += kAhead) {
-        float v[kAhead][kV], f[kAhead];
+    for (int base = 0; base < parts; base += 32) {  // 32 parts: the lanes hold their maxima and sums
+        const int here = min(parts - base, 32);
+        const float2 mine = lane < here ? __ldcg(pml + slot_of(base + lane)) : make_float2(kNegInf, 0.0f);
+        float f = 0.0f;
+        for (int i0 = 0; i0 < here; i0 += kAhead) {
+            float2 v[kAhead][kV / 2];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int i = i0 + j < parts ? i0 + j : parts - 1;
-            const float2 t = __ldcg(pml + slot_of(i));
-            f[j] = i0 + j < parts ? ex2(t.x - m_use) : 0.0f;
-            sum = i0 + j < parts ? fmaf(t.y, f[j], sum) : sum;
-            const float* src = a.part_o + slot_of(i) * kD + lane * kV;
+            for (int j = 0; j < kAhead; ++j) {
+                const float2* src = reinterpret_cast<const float2*>(a.part_o + slot_of(base + min(i0 + j, here - 1)) * kD) +
+                                    lane * (kV / 2);
 #pragma unroll
-            for (int x = 0; x < kV; x += 2) {
-                const float2 p = __ldcg(reinterpret_cast<const float2*>(src + x));
-                v[j][x] = p.x;
-                v[j][x + 1] = p.y;
+                for (int x = 0; x < kV / 2; ++x) v[j][x] = __ldcg(src + x);
+            }
+            if (i0 == 0) {
+                float top = mine.x;
+#pragma unroll
+                for (int w = 16; w >= 1; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                const float m_new = fmaxf(mm, top), m_use = m_new == kNegInf ? 0.0f : m_new;
+                const float back = ex2(mm - m_use);
+                f = ex2(mine.x - m_use);
+                float add = mine.y * f;
+#pragma unroll
+                for (int w = 16; w >= 1; w >>= 1) add += __shfl_xor_sync(0xffffffffu, add, w);
+                sum = fmaf(sum, back, add);
+#pragma unroll
+                for (int x = 0; x < kV; ++x) o[x] *= back;
+                mm = m_new;
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const float w = __shfl_sync(0xffffffffu, f, (i0 + j) & 31);
+                if (i0 + j < here)
+#pragma unroll
+                    for (int x = 0; x < kV / 2; ++x) {
+                        o[2 * x] = fmaf(v[j][x].x, w, o[2 * x]);
+                        o[2 * x + 1] = fmaf(v[j][x].y, w, o[2 * x + 1]);
+                    }
             }
         }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (i0 + j < parts)
-#pragma unroll
-                for (int x = 0; x < kV; ++x) o[x] = fmaf(v[j][x], f[j], o[x]);
     }
-    write_row<kD>(a, ld_dep_s32(&sp->q0), ld_dep_s32(&sp->h), ld_dep_s32(&sp->row0) + r, lane, mm, sum, o);
+    write_row<kD>(a, static_cast<int>(s0.z), static_cast<int>(s0.w), static_cast<int>(s1.x) + r, lane, mm, sum, o);
 }
 
 constexpr int kMaxGrid = 256;  // CTAs of the first kernel: one per SM

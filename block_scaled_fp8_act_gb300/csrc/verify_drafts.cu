@@ -18,6 +18,8 @@
 // prefetches the noise. (One launch with a cluster of 16 per sequence for
 // both took 20.5 us for 7 drafts at one sequence, where 16 SMs read 4.6 MB,
 // and 53 us for 34 x 2 drafts.)
+#include <atomic>
+
 #include "decoder_util.cuh"
 #include "kernels.h"
 
@@ -31,6 +33,7 @@ constexpr int kStatWarps = kStatThreads / 32;
 constexpr int kThreads = 512;  // of the second kernel
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRows = 2 * kMaxDrafts + 1;
+static_assert(kMaxDrafts <= 32, "a lane per draft");
 constexpr int kMaxParts = 32;
 constexpr int kMaxCluster = 16;
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -234,57 +237,61 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyProbl
         if (threadIdx.x == 0) atomicOr(&g_verify_index_error, 1u);
         n = n < 0 ? 0 : k;
     }
-    for (int r = threadIdx.x; r < q.rows; r += kThreads) {
-        const Stat* from = parts + (static_cast<int64_t>(b) * q.rows + r) * shares;
-        Stat st = {kNegInf, 0.0f, 0x7FFFFFFF};
-        for (int i = 0; i < shares; ++i) {
-            Stat o;
-            o.m = __ldcg(&from[i].m);
-            o.s = __ldcg(&from[i].s);
-            o.at = __ldcg(&from[i].at);
-            join(st, o, c);
+    // Warp 0's lane j holds draft j and what its acceptance needs, requested together with the row statistics.
+    int x = 0;
+    float u = 1.0f, lt = kNegInf, ld = kNegInf;
+    bool there = false;
+    if (warp == 0 && lane < k) {
+        x = ld_dep_s32(p.draft_tokens + static_cast<int64_t>(b) * k + lane);
+        u = ld_dep_f32(p.uniform + static_cast<int64_t>(b) * k + lane);
+        there = x >= 0 && x < V;
+        if (there) {
+            lt = row_of(lane).at(x);
+            if (draft) ld = row_of(targets + lane).at(x);
+        } else if (lane < n && rank == 0) {
+            atomicOr(&g_verify_index_error, 1u);
         }
-        sh.row[r] = st;
+    }
+    for (int r = warp; r < q.rows; r += kWarps) {  // a warp per row, a lane per part
+        const Stat* from = parts + (static_cast<int64_t>(b) * q.rows + r) * shares + lane;
+        Stat st = {kNegInf, 0.0f, 0x7FFFFFFF};
+        if (lane < shares) {
+            st.m = __ldcg(&from->m);
+            st.s = __ldcg(&from->s);
+            st.at = __ldcg(&from->at);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            Stat other;
+            other.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+            other.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+            other.at = __shfl_xor_sync(0xffffffffu, st.at, o);
+            join(st, other, c);
+        }
+        if (lane == 0) sh.row[r] = st;
     }
     __syncthreads();
 
     // Acceptance, decided alike in every CTA.
     if (warp == 0) {
-        int taken = 0;
-        bool open = true;
-        for (int j0 = 0; j0 < k; j0 += 32) {
-            const int j = j0 + lane;
-            bool ok = false;
-            if (j < k) {
-                const int x = ld_dep_s32(p.draft_tokens + static_cast<int64_t>(b) * k + j);
-                const bool there = x >= 0 && x < V;
-                if (!there && j < n && rank == 0) atomicOr(&g_verify_index_error, 1u);
-                float prob = 0.0f;
-                if (there && j < n) {
-                    const Stat st = sh.row[j];
-                    if (greedy) {
-                        prob = st.m > kNegInf && st.at == x ? 1.0f : 0.0f;
-                    } else {
-                        const float px = st.s > 0.0f ? __fdiv_rn(exp_below(row_of(j).at(x), st.m, c), st.s) : 0.0f;
-                        float qx = 1.0f;
-                        if (draft) {
-                            const Stat sd = sh.row[targets + j];
-                            qx = sd.s > 0.0f ? __fdiv_rn(exp_below(row_of(targets + j).at(x), sd.m, c), sd.s) : 0.0f;
-                        }
-                        prob = qx > 0.0f ? fminf(__fdiv_rn(px, qx), 1.0f) : px > 0.0f ? 1.0f : 0.0f;
-                    }
+        float prob = 0.0f;
+        if (there && lane < n) {
+            const Stat st = sh.row[lane];
+            if (greedy) {
+                prob = st.m > kNegInf && st.at == x ? 1.0f : 0.0f;
+            } else {
+                const float px = st.s > 0.0f ? __fdiv_rn(exp_below(lt, st.m, c), st.s) : 0.0f;
+                float qx = 1.0f;
+                if (draft) {
+                    const Stat sd = sh.row[targets + lane];
+                    qx = sd.s > 0.0f ? __fdiv_rn(exp_below(ld, sd.m, c), sd.s) : 0.0f;
                 }
-                sh.prob[j] = prob;
-                ok = j < n && ld_dep_f32(p.uniform + static_cast<int64_t>(b) * k + j) < prob;
-            }
-            const uint32_t no = ~__ballot_sync(0xffffffffu, ok);
-            if (open) {
-                const int run = no ? __ffs(no) - 1 : 32;
-                taken += run;
-                open = run == 32;
+                prob = qx > 0.0f ? fminf(__fdiv_rn(px, qx), 1.0f) : px > 0.0f ? 1.0f : 0.0f;
             }
         }
-        if (lane == 0) sh.taken = taken;
+        if (lane < k) sh.prob[lane] = prob;
+        const uint32_t no = ~__ballot_sync(0xffffffffu, lane < n && u < prob);
+        if (lane == 0) sh.taken = no ? __ffs(no) - 1 : 32;
     }
     __syncthreads();
     const int taken = sh.taken;
@@ -324,7 +331,8 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyProbl
                 const int v1 = static_cast<int>(static_cast<int64_t>(n8) * (rank + 1) / cluster);
                 for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kThreads) {
                     const int i = v * 8;
-                    uint4 n0 = ld_dep_v4(noise + i), n1 = ld_dep_v4(noise + i + 4), t[8 / R::kPer], d[8 / R::kPer];
+                    const uint4 n0 = ld_dep_v4(noise + i), n1 = ld_dep_v4(noise + i + 4);
+                    uint4 t[8 / R::kPer], d[8 / R::kPer];
 #pragma unroll
                     for (int u = 0; u < 8 / R::kPer; ++u) {
                         t[u] = row.raw(i + u * R::kPer);
@@ -366,18 +374,23 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyProbl
             }
             if (lane == 0) sh.warp_best[warp] = best;
             __syncthreads();
-            if (threadIdx.x == 0) {
-                for (int w = 1; w < kWarps; ++w) better(best, sh.warp_best[w].key, sh.warp_best[w].at);
-                sh.best[pass] = best;
+            auto reduce = [&](int width) {
+                for (int o = width / 2; o >= 1; o >>= 1) {
+                    const float key = __shfl_xor_sync(0xffffffffu, best.key, o);
+                    const int at = __shfl_xor_sync(0xffffffffu, best.at, o);
+                    better(best, key, at);
+                }
+            };
+            if (warp == 0) {
+                best = sh.warp_best[lane % kWarps];
+                reduce(kWarps);
+                if (lane == 0) sh.best[pass] = best;
             }
             ptx::cluster_sync();
-            if (threadIdx.x == 0) {
-                Best all = ld_cluster_best(&sh.best[pass], 0);
-                for (int i = 1; i < cluster; ++i) {
-                    const Best o = ld_cluster_best(&sh.best[pass], i);
-                    better(all, o.key, o.at);
-                }
-                sh.all = all;
+            if (warp == 0) {
+                best = ld_cluster_best(&sh.best[pass], lane % cluster);
+                reduce(cluster);
+                if (lane == 0) sh.all = best;
             }
             __syncthreads();
             if (sh.all.at < V) token = sh.all.at;
@@ -414,9 +427,15 @@ cudaError_t launch_verify_drafts(const VerifyProblem& p, int num_sms, cudaStream
     while (cluster > 1 && (p.V < 2048 * cluster || static_cast<int64_t>(p.B) * cluster > 2 * num_sms)) cluster /= 2;
     Stat* parts = static_cast<Stat*>(p.workspace);
     auto draw = p.f32 ? verify_draw_kernel<true> : verify_draw_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(draw, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    e = launch_dependent(p.f32 ? verify_stats_kernel<true> : verify_stats_kernel<false>, dim3(shares, rows, p.B),
+    static std::atomic<bool> configured[2][64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!configured[p.f32][dev & 63].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(draw, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        configured[p.f32][dev & 63].store(true, std::memory_order_relaxed);
+    }
+    const cudaError_t e = launch_dependent(p.f32 ? verify_stats_kernel<true> : verify_stats_kernel<false>, dim3(shares, rows, p.B),
                          kStatThreads, 0, stream, 1, p, parts);
     if (e != cudaSuccess) return e;
     return launch_dependent(draw, dim3(static_cast<unsigned>(p.B) * cluster), kThreads, 0, stream, cluster, p, parts,
