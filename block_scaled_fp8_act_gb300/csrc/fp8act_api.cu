@@ -457,7 +457,8 @@ int fp8act_check_status(void* stream) {
     const unsigned int rd = fp8act::read_and_clear_read_error();
     const unsigned int index = fp8act::read_and_clear_kv_index_error() | fp8act::read_and_clear_attn_index_error() |
                                fp8act::read_and_clear_verify_index_error();
-    if (tc | mid | rd) return FP8ACT_ERR_TIMEOUT;
+    const unsigned int at = fp8act::read_and_clear_attn_timeout();
+    if (tc | mid | rd | at) return FP8ACT_ERR_TIMEOUT;
     return index ? FP8ACT_ERR_INDEX : FP8ACT_OK;
 }
 

@@ -164,6 +164,7 @@ cudaError_t launch_verify_drafts(const VerifyProblem& p, int num_sms, cudaStream
 // Device-side words set by a page, slot, length or token index out of range.
 unsigned int read_and_clear_kv_index_error();
 unsigned int read_and_clear_attn_index_error();
+unsigned int read_and_clear_attn_timeout();
 unsigned int read_and_clear_verify_index_error();
 
 // Device-side error words of the tcgen05 kernels (non-zero after a bounded

@@ -32,13 +32,10 @@
 // share a ring and split the rows. The groups join in shared memory. An item
 // that crosses CTAs leaves fp32 parts in the workspace, which a second kernel,
 // launched dependently, adds in unit order: results do not depend on timing.
-#include <cuda_fp16.h>
-
 #include <atomic>
 #include <type_traits>
 
-#include "decoder_util.cuh"
-#include "kernels.h"
+#include "kv_attention.cuh"
 
 namespace fp8act {
 namespace {
@@ -48,31 +45,7 @@ __device__ unsigned int g_attn_index_error;
 constexpr int kTile = 32;  // cached tokens per unit
 constexpr int kLeastUnits = 8;  // least share of a CTA
 constexpr int kItemCost = 12;   // units that an item counts beside its own
-constexpr float kNegInf = -__builtin_huge_valf();
-
-struct SplitItem;
-
-struct AttnArgs {
-    const uint16_t* q;
-    int64_t q_stride;
-    const int* cu_q;
-    const int* kv_lens;
-    const int* table;
-    int64_t table_stride;
-    int batch, tokens, group;
-    float scale_log2;
-    KvCache c;
-    uint32_t* out;   // bf16 [tokens, heads * group, D]
-    float* lse;      // [tokens, heads * group] or null
-    float* part_o;   // [2 * grid][rows][D]
-    float* part_ml;  // [2 * grid][rows][2]
-    SplitItem* split;  // [grid]: the item that starts in a CTA and goes on in the next
-};
-
-struct __align__(16) SplitItem {
-    int parts, second;  // CTAs it spans (0: no such item); whether its part of the first CTA is that CTA's second
-    int q0, h, row0, nrows, pad[2];
-};
+using Work = Units<kTile, kItemCost>;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
@@ -84,18 +57,6 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int kN>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
-}
-
-// Two E4M3 codes (the low or the high 16 bits of `codes`) to f16x2, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_lo_to_f16x2(uint32_t codes) {
-    uint32_t r;
-    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(r) : "r"(codes));
-    return r;
-}
-__device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t codes) {
-    uint32_t r;
-    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, hi;\n}" : "=r"(r) : "r"(codes));
-    return r;
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -153,41 +114,6 @@ struct Attn {
     static constexpr int kBytes = kRing + kG * kRingBytes;
 };
 
-// One (sequence, KV head, row tile) and where it lies in the unit list.
-struct Item {
-    int b, h, rt;      // sequence, KV head, row tile
-    int nq, q0, len;   // new tokens, first one's row in q, cached tokens
-    int rts, tiles;    // row tiles of this sequence and units of each, kItemCost included
-    int64_t first;     // index of the item's first unit
-};
-
-__device__ __forceinline__ void load_sequence(const AttnArgs& a, int rows, int b, Item& it) {
-    const int q0 = ld_dep_s32(a.cu_q + b), q1 = ld_dep_s32(a.cu_q + b + 1);
-    int len = ld_dep_s32(a.kv_lens + b);
-    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.tokens;
-    it.q0 = q0;
-    it.nq = ok ? q1 - q0 : 0;
-    const int64_t most = a.table_stride << a.c.page_log2;
-    if (!ok || len < 0 || len > most) {
-        atomicOr(&g_attn_index_error, 1u);
-        len = len < 0 ? 0 : static_cast<int>(len > most ? most : len);
-    }
-    it.len = len;
-    it.rts = (it.nq * a.group + rows - 1) / rows;
-    it.tiles = (len + kTile - 1) / kTile + kItemCost;  // (an empty sequence still writes its rows)
-}
-
-__device__ __forceinline__ uint32_t scale_exponent(float s) {
-    const uint32_t e = __float_as_uint(s) & 0x7F800000u;
-    return e == 0x7F800000u ? 0u : e;
-}
-
-// Units per CTA: an even share, but not less than is worth a part of an item.
-__device__ __forceinline__ int64_t units_per_cta(int64_t total, int least) {
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    return per < least ? least : per;
-}
-
 // One finished row: lane's kD / 32 columns of sum p s_v v, the row's maximum (log2) and sum of p.
 template <int kD>
 __device__ __forceinline__ void write_row(const AttnArgs& a, int q0, int h, int row, int lane, float m, float sum,
@@ -207,9 +133,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG>::kThreads, 1) kv_attent
     constexpr int kKS = kD / 32;  // pairs of k-steps of the score product
     constexpr int kDT = kD / 16;  // 16-row tiles of the transposed output
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_total;
-    __shared__ int s_b;
-    __shared__ int64_t s_first;
+    __shared__ Work::Scratch scratch;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
     const int og = order<kD>(g);                  // the token of a block of 8 that is the lane's MMA row
     const int vg = kD == 64 ? g : order<128>(g);  // the chunk of output columns that is the lane's (the same reason)
@@ -227,62 +151,10 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG>::kThreads, 1) kv_attent
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
 
-    // Total units, and the sequence that holds this CTA's first one.
-    if (threadIdx.x < 32) {
-        auto units_of = [&](int b) -> int64_t {
-            if (b >= a.batch) return 0;
-            Item it;
-            load_sequence(a, kRows, b, it);
-            return static_cast<int64_t>(a.c.heads) * it.rts * it.tiles;
-        };
-        const int64_t u_lane = units_of(lane);
-        int64_t total = 0;
-        for (int b0 = 0; b0 < a.batch; b0 += 32) {
-            int64_t n = b0 == 0 ? u_lane : units_of(b0 + lane);
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-            total += n;
-        }
-        const int64_t u0 = units_per_cta(total, kLeastUnits) * blockIdx.x;
-        int64_t base = 0;
-        for (int b0 = 0; b0 < a.batch && u0 < total; b0 += 32) {
-            const int64_t n = b0 == 0 ? u_lane : units_of(b0 + lane);
-            int64_t incl = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            const int64_t lo = base + incl - n;
-            if (u0 >= lo && u0 < lo + n) {
-                s_b = b0 + lane;
-                s_first = lo;
-            }
-            base += __shfl_sync(0xffffffffu, incl, 31);
-            if (base > u0) break;
-        }
-        if (lane == 0) {
-            s_total = total;
-            a.split[blockIdx.x].parts = 0;
-        }
-    }
-    __syncthreads();
-    const int64_t total = s_total;
-    const int64_t per = units_per_cta(total, kLeastUnits);
-    int64_t u = per * blockIdx.x;
-    const int64_t u_end = u + per < total ? u + per : total;
-    if (u >= u_end) return;
-    const int64_t u_begin = u;
-
     Item it;
-    it.b = s_b;
-    load_sequence(a, kRows, it.b, it);
-    {
-        const int64_t rel = (u - s_first) / it.tiles;
-        it.h = static_cast<int>(rel / it.rts);
-        it.rt = static_cast<int>(rel % it.rts);
-        it.first = s_first + rel * it.tiles;
-    }
+    int64_t per, u, u_end;
+    if (!Work::first_item(a, kLeastUnits, scratch, it, per, u, u_end)) return;
+    const int64_t u_begin = u;
 
     while (true) {
         const int t0 = static_cast<int>(u - it.first);
@@ -303,7 +175,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG>::kThreads, 1) kv_attent
             if (t >= f1 || pos >= it.len) return -1;
             const int p = ld_dep_s32(table + (pos >> a.c.page_log2));
             if (p >= 0 && p < a.c.num_pages) return p;
-            atomicOr(&g_attn_index_error, 1u);
+            atomicOr(a.index_error, 1u);
             return -1;
         };
         int pages = look_up(f0 + group), asked = 0;
@@ -356,9 +228,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG>::kThreads, 1) kv_attent
                     const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
                     x = ld_dep_v4(a.q + (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD + c * 8);
                 }
-                uint32_t top = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
-                                        __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
-                top = max(top & 0xFFFFu, top >> 16);
+                uint32_t top = top_bits(x);
 #pragma unroll
                 for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(__activemask(), top, o));
                 // (a zero row's exponent is as good as any)
@@ -622,28 +492,13 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG>::kThreads, 1) kv_attent
             }
         }
         if (!whole && t0 == 0 && threadIdx.x == 0) {  // it starts here and goes on in the next CTA
-            SplitItem sp = {};
-            sp.parts = static_cast<int>((item_end - 1) / per) - static_cast<int>(blockIdx.x) + 1;
-            sp.second = slot & 1;
-            sp.q0 = it.q0;
-            sp.h = it.h;
-            sp.row0 = row0;
-            sp.nrows = nrows;
-            a.split[blockIdx.x] = sp;
+            write_split(a, it, per, slot, row0, nrows);
         }
         if (item_end >= u_end) break;
         // Next item.
         __syncthreads();
         u = item_end;
-        it.first = item_end;
-        if (++it.rt == it.rts) {
-            it.rt = 0;
-            if (++it.h == a.c.heads) {
-                it.h = 0;
-                do load_sequence(a, kRows, ++it.b, it);
-                while (it.rts == 0);
-            }
-        }
+        Work::next_item(a, it);
     }
 }
 
@@ -654,7 +509,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG>::kThreads, 1) kv_attent
 // way.
 constexpr int kJoinRows = 8;
 
-template <int kD, int kRows>
+template <int kD>
 __global__ void __launch_bounds__(kJoinRows * 32) kv_attention_join_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int kV = kD / 32, kAhead = 128 / kV / 2;
     const int lane = threadIdx.x & 31;
@@ -664,7 +519,7 @@ __global__ void __launch_bounds__(kJoinRows * 32) kv_attention_join_kernel(const
     const uint4 s0 = ld_dep_v4(a.split + c), s1 = ld_dep_v4(reinterpret_cast<const uint4*>(a.split + c) + 1);
     const int parts = static_cast<int>(s0.x), second = static_cast<int>(s0.y);
     if (parts == 0 || r >= static_cast<int>(s1.y)) return;
-    auto slot_of = [&](int i) { return static_cast<int64_t>(2 * (c + i) + (i == 0 ? second : 0)) * kRows + r; };
+    auto slot_of = [&](int i) { return static_cast<int64_t>(2 * (c + i) + (i == 0 ? second : 0)) * a.rows + r; };
     const float2* pml = reinterpret_cast<const float2*>(a.part_ml);
     float mm = kNegInf, sum = 0.0f, o[kV];
 #pragma unroll
@@ -712,8 +567,6 @@ __global__ void __launch_bounds__(kJoinRows * 32) kv_attention_join_kernel(const
     write_row<kD>(a, static_cast<int>(s0.z), static_cast<int>(s0.w), static_cast<int>(s1.x) + r, lane, mm, sum, o);
 }
 
-constexpr int kMaxGrid = 256;  // CTAs of the first kernel: one per SM
-
 template <int kD, int kWR, int kRW, int kG>
 cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t stream) {
     using S = Attn<kD, kWR, kRW, kG>;
@@ -726,19 +579,19 @@ cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t stream
         if (e != cudaSuccess) return e;
         configured[dev & 63].store(true, std::memory_order_relaxed);
     }
-    const int grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
-    const cudaError_t e = launch_dependent(kernel, dim3(grid), S::kThreads, S::kBytes, stream, 1, a);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kv_attention_join_kernel<kD, S::kRows>, dim3(grid, S::kRows / kJoinRows), kJoinRows * 32, 0,
-                            stream, 1, a);
+    return launch_dependent(kernel, dim3(num_sms), S::kThreads, S::kBytes, stream, 1, a);
 }
 
 // Row tiles: the smallest that holds a sequence's rows, else the largest. The
 // registers of a thread go by the CTA's warps (255 up to 8 warps, 168 up to
-// 12), and a warp needs 32 accumulators for every 8 rows x 128 columns.
+// 12), and a warp needs 32 accumulators for every 8 rows x 128 columns. From
+// kWideRows rows on, head size 128 takes the tcgen05 kernel's row tiles of any
+// multiple of 8 up to 128, or 256.
+constexpr int kWideRows = 25;
 int rows_of(int max_q_len, int group, int head_dim) {
     const int64_t rows = static_cast<int64_t>(max_q_len) * group;
-    const int wide[] = {8, 16, 24, 32, 48, 96, 192}, narrow[] = {8, 16, 32, 64};
+    if (head_dim == 128 && rows >= kWideRows) return rows > 128 ? 256 : static_cast<int>((rows + 7) / 8 * 8);
+    const int wide[] = {8, 16, 24, 48, 96, 192}, narrow[] = {8, 16, 32, 64};
     if (head_dim == 256) {
         for (int r : narrow)
             if (rows <= r) return r;
@@ -750,21 +603,33 @@ int rows_of(int max_q_len, int group, int head_dim) {
 }
 
 template <int kD>
-cudaError_t launch_rows(const AttnArgs& a, int rows, int num_sms, cudaStream_t stream) {
-    switch (rows) {
-        case 8: return launch_attention<kD, 1, 1, 12>(a, num_sms, stream);
-        case 16: return launch_attention<kD, 1, 2, 12>(a, num_sms, stream);
-        case 24: return launch_attention<kD, 1, 3, 8>(a, num_sms, stream);
-        case 32: return launch_attention<kD, 2, 2, 6>(a, num_sms, stream);
-        case 48: return launch_attention<kD, 2, 3, 4>(a, num_sms, stream);
-        case 96: return launch_attention<kD, 4, 3, 2>(a, num_sms, stream);
-        default: return launch_attention<kD, 8, 3, 1>(a, num_sms, stream);
+cudaError_t launch_rows(const AttnArgs& a, int num_sms, cudaStream_t stream);
+
+template <>
+cudaError_t launch_rows<64>(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+    switch (a.rows) {
+        case 8: return launch_attention<64, 1, 1, 12>(a, num_sms, stream);
+        case 16: return launch_attention<64, 1, 2, 12>(a, num_sms, stream);
+        case 24: return launch_attention<64, 1, 3, 8>(a, num_sms, stream);
+        case 48: return launch_attention<64, 2, 3, 4>(a, num_sms, stream);
+        case 96: return launch_attention<64, 4, 3, 2>(a, num_sms, stream);
+        default: return launch_attention<64, 8, 3, 1>(a, num_sms, stream);
     }
 }
 
 template <>
-cudaError_t launch_rows<256>(const AttnArgs& a, int rows, int num_sms, cudaStream_t stream) {
-    switch (rows) {
+cudaError_t launch_rows<128>(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+    switch (a.rows) {
+        case 8: return launch_attention<128, 1, 1, 12>(a, num_sms, stream);
+        case 16: return launch_attention<128, 1, 2, 12>(a, num_sms, stream);
+        case 24: return launch_attention<128, 1, 3, 8>(a, num_sms, stream);
+        default: return launch_attention_tc(a, num_sms, stream);
+    }
+}
+
+template <>
+cudaError_t launch_rows<256>(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+    switch (a.rows) {
         case 8: return launch_attention<256, 1, 1, 6>(a, num_sms, stream);
         case 16: return launch_attention<256, 1, 2, 6>(a, num_sms, stream);
         case 32: return launch_attention<256, 2, 2, 4>(a, num_sms, stream);
@@ -772,16 +637,25 @@ cudaError_t launch_rows<256>(const AttnArgs& a, int rows, int num_sms, cudaStrea
     }
 }
 
+template <int kD>
+cudaError_t launch_both(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+    if (num_sms > kMaxAttnGrid) num_sms = kMaxAttnGrid;
+    const cudaError_t e = launch_rows<kD>(a, num_sms, stream);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kv_attention_join_kernel<kD>, dim3(num_sms, (a.rows + kJoinRows - 1) / kJoinRows),
+                            kJoinRows * 32, 0, stream, 1, a);
+}
+
 }  // namespace
 
 size_t kv_attention_workspace(int max_q_len, int group, int head_dim) {
     const size_t rows = rows_of(max_q_len, group, head_dim);
-    return kMaxGrid * sizeof(SplitItem) + 2 * static_cast<size_t>(kMaxGrid) * rows * (head_dim + 2) * sizeof(float);
+    return kMaxAttnGrid * sizeof(SplitItem) + 2 * static_cast<size_t>(kMaxAttnGrid) * rows * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv_attention(const AttentionProblem& p, int num_sms, cudaStream_t stream) {
     const int rows = rows_of(p.max_q_len, p.group, p.cache.head_dim);
-    const size_t slots = 2 * static_cast<size_t>(kMaxGrid) * rows;
+    const size_t slots = 2 * static_cast<size_t>(kMaxAttnGrid) * rows;
     AttnArgs a;
     a.q = static_cast<const uint16_t*>(p.q);
     a.q_stride = p.q_stride;
@@ -792,17 +666,22 @@ cudaError_t launch_kv_attention(const AttentionProblem& p, int num_sms, cudaStre
     a.batch = p.batch;
     a.tokens = p.tokens;
     a.group = p.group;
+    a.rows = rows;
+    void* error = nullptr;
+    const cudaError_t found = cudaGetSymbolAddress(&error, g_attn_index_error);
+    if (found != cudaSuccess) return found;
+    a.index_error = static_cast<unsigned int*>(error);
     a.scale_log2 = p.softmax_scale * 1.4426950408889634f;
     a.c = p.cache;
     a.out = static_cast<uint32_t*>(p.out);
     a.lse = p.lse;
     a.split = static_cast<SplitItem*>(p.workspace);
-    a.part_ml = reinterpret_cast<float*>(a.split + kMaxGrid);
+    a.part_ml = reinterpret_cast<float*>(a.split + kMaxAttnGrid);
     a.part_o = a.part_ml + slots * 2;
     switch (p.cache.head_dim) {
-        case 64: return launch_rows<64>(a, rows, num_sms, stream);
-        case 128: return launch_rows<128>(a, rows, num_sms, stream);
-        default: return launch_rows<256>(a, rows, num_sms, stream);
+        case 64: return launch_both<64>(a, num_sms, stream);
+        case 128: return launch_both<128>(a, num_sms, stream);
+        default: return launch_both<256>(a, num_sms, stream);
     }
 }
 

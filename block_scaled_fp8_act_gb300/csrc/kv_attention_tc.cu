@@ -1,0 +1,700 @@
+// Attention over the E4M3 cache for wide row tiles (verify steps, chunks of a
+// prompt; head size 128) on the 5th-generation tensor cores. The mathematics,
+// the masks and the work list are those of kv_attention.cu; a unit is a row
+// tile x 128 cached tokens.
+//
+// S = Q K^T takes the cached codes as they are (kind::f8f6f4, fed by tensor
+// copies, no conversion): a query row, scaled by a power of two so that its
+// largest value is in [128, 256), is the sum of two E4M3 rows, hi = E4M3(q) and
+// lo = E4M3(q - hi), whose products add up in one accumulator. A bf16 value
+// has 8 significant bits and each part 4, so hi + lo is exact down to 2^-9 of
+// the row's largest value, and within 2^-17 of it below. O += W V runs in f16
+// (kind::f16): four warps widen the value codes exactly, the weights
+// W = p * s_v are rounded to f16 (11 bits; one or two E4M3 parts would give 4
+// or 8) after scaling by 2^6 / R, R the power of two below the largest s_v so
+// far, and go from registers to tensor memory over the scores they came from.
+//
+// Two score tiles are in flight, each with a warpgroup whose threads own a row:
+// with more than 128 rows they are the two halves of a 256-row tile on the same
+// cached tokens, which are loaded and widened once for both; else they are the
+// even and the odd token tiles of one row tile of up to 128 rows, whose two
+// results join in tensor memory at the end (warps without rows skip the
+// softmax). While one warpgroup works the tensor cores serve the other. A
+// row's reference maximum moves only when a score passes it by 2^8, so the
+// output accumulator is seldom rescaled.
+//
+// Every wait is bounded by wall time. The first that gives up sets the error
+// word and the CTA's abort flag; every role then leaves its loop, copies and
+// MMAs in flight are waited for, tensor memory is freed.
+#include <atomic>
+
+#include "host_util.h"
+#include "kv_attention.cuh"
+#include "tc_ptx.cuh"
+
+namespace fp8act {
+
+__device__ unsigned int g_attn_timeout;
+
+namespace {
+
+constexpr int kTok = 128;
+constexpr int kD = 128;
+constexpr int kItemCost = 4;    // units that an item counts beside its own
+constexpr int kLeastUnits = 2;  // least share of a CTA
+using Work = Units<kTok, kItemCost>;
+
+constexpr int kThreads = 512;  // warps 0 keys, 1 values, 2 MMA; 4..7 widening; 8..11 and 12..15 softmax
+constexpr int kTileBytes = kTok * kD;
+
+template <bool kPair>  // two row tiles of 128 on the same tokens
+struct Tc {
+    static constexpr int kQTiles = kPair ? 2 : 1;
+    static constexpr int kKStages = kPair ? 3 : 4;
+    static constexpr int kVStages = kPair ? 2 : 3;
+    static constexpr int kQ = 0;                                   // per tile: hi, lo
+    static constexpr int kK = kQ + kQTiles * 2 * kTileBytes;
+    static constexpr int kV8 = kK + kKStages * kTileBytes;
+    static constexpr int kV16 = kV8 + kVStages * kTileBytes;       // 2 buffers of two 64-column halves
+    static constexpr int kScale8 = kV16 + 2 * 2 * kTileBytes;      // per value stage: key scales, value scales
+    static constexpr int kScale16 = kScale8 + kVStages * 2 * kTok * 4;  // per buffer: the same, value scales times 2^6 / R
+    static constexpr int kR = kScale16 + 2 * 2 * kTok * 4;         // per buffer: R
+    static constexpr int kQScale = kR + 16;
+    static constexpr int kML = kQScale + kQTiles * 128 * 4;        // second result's (maximum, sum, R) per row
+    static constexpr int kBytes = kML + 128 * 16 + 1024;           // (the base is rounded up to 1024)
+};
+
+struct TcExtra {
+    unsigned long long wait_ns;  // bound of every wait
+    int withhold;                // test hook: the CTA's first key tile is never requested
+};
+
+__device__ __forceinline__ void st_16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] x B[smem desc], f16 with fp32 accumulation.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of the widened values as the N x K operand with N contiguous
+// (128-byte swizzle): blocks of 64 columns x 8 tokens, column blocks 16 KB
+// apart (leading byte offset), token blocks 1 KB apart (stride byte offset).
+__device__ __forceinline__ uint64_t desc_values(uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(kTileBytes >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+constexpr uint32_t kIdescScores = tc::idesc_e4m3_f32(128, kTok);
+constexpr uint32_t kIdescValues = (1u << 4)                                   // D fp32; A, B f16
+                                  | (1u << 16)                                // B with N contiguous
+                                  | (static_cast<uint32_t>(kD >> 3) << 17) | (128u >> 4 << 24);
+
+__device__ __forceinline__ void load_tokens(uint32_t dst, const CUtensorMap* map, uint32_t bar, int line) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(0), "r"(line)
+        : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+// Arrive on `bar` (one of its expected arrivals) once this thread's cp.asyncs so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <bool kPair>
+__global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __grid_constant__ AttnArgs a,
+                                                                      const __grid_constant__ CUtensorMap k_map,
+                                                                      const __grid_constant__ CUtensorMap v_map,
+                                                                      const TcExtra x) {
+    using C = Tc<kPair>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* const smem = smem_raw + (base - ptx::smem_u32(smem_raw));
+    __shared__ Work::Scratch scratch;
+    __shared__ __align__(8) uint64_t bars[2 * C::kKStages + 2 * C::kVStages + 2 * 2 + 3 * 2 + 4];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    const uint32_t k_full = ptx::smem_u32(bars), k_empty = k_full + 8 * C::kKStages;
+    const uint32_t v8_full = k_empty + 8 * C::kKStages, v8_empty = v8_full + 8 * C::kVStages;
+    const uint32_t v16_full = v8_empty + 8 * C::kVStages, v16_empty = v16_full + 16;
+    const uint32_t s_full = v16_empty + 16, p_full = s_full + 16, pv_done = p_full + 16;  // [slot]
+    const uint32_t q_full = pv_done + 16, item_done = q_full + 8, ml_full = item_done + 8, drain = ml_full + 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kKStages; ++i) {
+            ptx::mbar_init(k_full + 8 * i, 1);
+            ptx::mbar_init(k_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < C::kVStages; ++i) {
+            ptx::mbar_init(v8_full + 8 * i, 1 + 32);  // the copies' bytes and the scales' 32 lanes
+            ptx::mbar_init(v8_empty + 8 * i, 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(v16_full + 8 * i, 4);
+            ptx::mbar_init(v16_empty + 8 * i, 1);
+            ptx::mbar_init(s_full + 8 * i, 1);
+            ptx::mbar_init(p_full + 8 * i, 4);
+            ptx::mbar_init(pv_done + 8 * i, 1);
+        }
+        ptx::mbar_init(q_full, 8);
+        ptx::mbar_init(item_done, 1);
+        ptx::mbar_init(ml_full, 4);
+        ptx::mbar_init(drain, 1);
+        s_abort = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 2) {
+        tc::tmem_alloc(ptx::smem_u32(&s_tmem), 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;  // columns: scores of slot 0 and 1, outputs of slot 0 and 1
+
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+
+    Item it;
+    int64_t per, u, u_end;
+    const bool any = Work::first_item(a, kLeastUnits, scratch, it, per, u, u_end);
+    const int64_t u_begin = u;
+    // Tiles used by the items before, K and V alike.
+    uint32_t seq = 0;
+
+    // A bounded wait by the whole warp; false once any wait of the CTA has run out.
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        bool ok = ptx::mbar_try_wait(bar, parity);
+        if (!ok) {
+            const uint64_t start = ptx::globaltimer_ns();
+            while (!ok) {
+#pragma unroll 1
+                for (int i = 0; i < 16 && !ok; ++i) ok = ptx::mbar_try_wait(bar, parity);
+                if (!ok && (s_abort || ptx::globaltimer_ns() - start > x.wait_ns)) break;
+            }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok && lane == 0) {
+            s_abort = 1;
+            atomicOr(&g_attn_timeout, 1u);
+        }
+        return ok;
+    };
+
+    // What every role knows of an item.
+    struct Span {
+        int row0, nrows, slots;  // rows of the row tile; row halves in use (kPair) or 2
+        int f0, n;               // first token tile and how many
+        bool whole;              // no other CTA works on the item
+    };
+    auto span_of = [&]() {
+        Span s;
+        const int t0 = static_cast<int>(u - it.first);
+        const int64_t item_end = it.first + it.tiles;
+        const int t1 = static_cast<int>((item_end < u_end ? item_end : u_end) - it.first);
+        s.row0 = it.rt * a.rows;
+        s.nrows = min(it.nq * a.group - s.row0, a.rows);
+        s.slots = kPair && s.nrows <= 128 ? 1 : 2;
+        const int seen = max(it.len - it.nq + (s.row0 + s.nrows - 1) / a.group + 1, 0);
+        s.f0 = max(t0 - kItemCost, 0);
+        s.n = max(min((seen + kTok - 1) / kTok, t1 - kItemCost) - s.f0, 0);
+        s.whole = t0 == 0 && t1 == it.tiles;
+        return s;
+    };
+    auto next = [&](const Span& s) -> bool {  // to the next item of this CTA
+        seq += s.n;
+        u = it.first + it.tiles;
+        if (u >= u_end) return false;
+        Work::next_item(a, it);
+        return true;
+    };
+
+    if (!any) {
+        // nothing to do: only tensor memory to free
+    } else if (warp < 2) {
+        // ------------------------------------------------------------ copies
+        const bool values = warp == 1;
+        const int stages = values ? C::kVStages : C::kKStages;
+        const uint32_t full = values ? v8_full : k_full, empty = values ? v8_empty : k_empty;
+        const uint32_t ring = base + (values ? C::kV8 : C::kK);
+        const CUtensorMap* map = values ? &v_map : &k_map;
+        const int page = 1 << a.c.page_log2, box = min(page, kTok);
+        bool ok = true;
+        uint32_t n = 0;  // tiles requested
+        while (ok) {
+            const Span s = span_of();
+            const int* table = a.table + it.b * a.table_stride;
+            // Pages of 4 tiles at a time, one per 16 tokens and lane, looked up one such span ahead.
+            auto look_up = [&](int t) -> int {
+                const int pos = t * kTok + lane * 16;
+                if (t >= s.f0 + s.n || pos >= it.len) return -1;
+                const int p = ld_dep_s32(table + (pos >> a.c.page_log2));
+                if (p >= 0 && p < a.c.num_pages) return p;
+                atomicOr(a.index_error, 1u);
+                return -1;
+            };
+            int ahead = look_up(s.f0), now = -1;
+            for (int i = 0; i < s.n && ok; ++i, ++n) {
+                if ((i & 3) == 0) {
+                    now = ahead;
+                    ahead = look_up(s.f0 + i + 4);
+                }
+                const uint32_t stage = n % stages, round = n / stages, bar = full + 8 * stage;
+                if (round > 0 && !(ok = wait(empty + 8 * stage, (round - 1) & 1))) break;
+                const int pos = (s.f0 + i) * kTok;
+                // Lane j < 128 / box: copy j of the tile, if it holds a token.
+                const int mine = __shfl_sync(0xffffffffu, now, (i & 3) * 8 + min(lane * box / 16, 7));
+                const bool copy = lane < kTok / box && pos + lane * box < it.len && mine >= 0;
+                const uint32_t copies = __ballot_sync(0xffffffffu, copy);
+                const bool withheld = x.withhold && !values && n == 0;
+                if (lane == 0 && !withheld) ptx::mbar_arrive_expect_tx(bar, __popc(copies) * box * kD);
+                __syncwarp();
+                if (copy && !withheld) {
+                    const int64_t token = ((static_cast<int64_t>(mine) * a.c.heads + it.h) << a.c.page_log2) +
+                                          ((pos + lane * box) & (page - 1));
+                    load_tokens(ring + stage * kTileBytes + lane * box * kD, map, bar, static_cast<int>(token));
+                }
+                if (values) {  // both scales travel with the values
+                    const uint32_t dst = base + C::kScale8 + stage * 2 * kTok * 4;
+#pragma unroll
+                    for (int j = 0; j < kTok / 32; ++j) {
+                        const int t = j * 32 + lane;
+                        const int p = __shfl_sync(0xffffffffu, now, (i & 3) * 8 + t / 16);
+                        const bool in = p >= 0 && pos + t < it.len;
+                        const int64_t at =
+                            in ? ((static_cast<int64_t>(p) * a.c.heads + it.h) << a.c.page_log2) + ((pos + t) & (page - 1)) : 0;
+                        cp_async4(dst + t * 4, a.c.k_scale + at, in);
+                        cp_async4(dst + kTok * 4 + t * 4, a.c.v_scale + at, in);
+                    }
+                    cp_async_arrive(bar);
+                }
+            }
+            if (!ok || !next(s)) break;
+        }
+        // Every copy must have landed before the CTA leaves (its consumer has usually seen it).
+        for (uint32_t i = n > stages ? n - stages : 0; i < n; ++i)
+            if (!(x.withhold && !values && i == 0) &&
+                !ptx::mbar_wait(full + 8 * (i % stages), (i / stages) & 1) && lane == 0)
+                atomicOr(&g_attn_timeout, 2u);
+    } else if (warp == 2) {
+        // --------------------------------------------------------------- MMA
+        bool ok = true;
+        uint32_t item = 0;
+        uint32_t done[2] = {0, 0};  // score tiles issued per slot
+        uint32_t waited[2] = {0, 0};
+        while (ok) {
+            const Span s = span_of();
+            const int depth = s.slots;                            // score tiles in flight
+            const int jobs = kPair ? s.n * s.slots : s.n;
+            auto slot_of = [&](int j) { return depth == 2 ? j & 1 : 0; };
+            auto tile_of = [&](int j) { return kPair ? j / s.slots : j; };
+            auto first_use = [&](int j) { return !kPair || slot_of(j) == 0; };
+            auto last_use = [&](int j) { return !kPair || slot_of(j) == s.slots - 1; };
+            auto scores = [&](int j) {
+                const int slot = slot_of(j);
+                const uint32_t n = seq + tile_of(j), stage = n % C::kKStages;
+                if (first_use(j) && !(ok = wait(k_full + 8 * stage, (n / C::kKStages) & 1))) return;
+                tc::fence_after_sync();
+                if (lane == 0) {
+                    const uint32_t q = base + C::kQ + (kPair ? slot : 0) * 2 * kTileBytes, k = base + C::kK + stage * kTileBytes;
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int i = 0; i < kD / 32; ++i)
+                            tc::mma_f8f6f4(tmem + slot * 128, tc::desc_kmajor_sw128(q + part * kTileBytes + 32 * i),
+                                           tc::desc_kmajor_sw128(k + 32 * i), kIdescScores, part + i > 0 ? 1u : 0u);
+                    tc::commit(s_full + 8 * slot);
+                    if (last_use(j)) tc::commit(k_empty + 8 * stage);
+                }
+                __syncwarp();
+                ++done[slot];
+            };
+            if (!(ok = wait(q_full, item & 1))) break;
+            for (int j = 0; j < depth && j < jobs && ok; ++j) scores(j);
+            for (int j = 0; j < jobs && ok; ++j) {
+                const int slot = slot_of(j);
+                const uint32_t n = seq + tile_of(j), buf = n & 1;
+                if (!(ok = wait(p_full + 8 * slot, waited[slot]++ & 1))) break;
+                if (first_use(j) && !(ok = wait(v16_full + 8 * buf, (n >> 1) & 1))) break;
+                tc::fence_after_sync();
+                if (lane == 0) {
+                    const uint32_t v = base + C::kV16 + buf * 2 * kTileBytes;
+                    const bool fresh = kPair ? tile_of(j) == 0 : j < 2;
+#pragma unroll
+                    for (int i = 0; i < kTok / 16; ++i)
+                        mma_f16_ts(tmem + 256 + slot * 128, tmem + slot * 128 + 8 * i, desc_values(v + 2048 * i), kIdescValues,
+                                   fresh && i == 0 ? 0u : 1u);
+                    tc::commit(pv_done + 8 * slot);
+                    if (last_use(j)) tc::commit(v16_empty + 8 * buf);
+                }
+                __syncwarp();
+                if (j + depth < jobs) scores(j + depth);
+            }
+            if (!ok) break;
+            if (lane == 0) tc::commit(item_done);
+            __syncwarp();
+            ++item;
+            if (!next(s)) break;
+        }
+        // No MMA may still run when tensor memory is freed or the CTA leaves.
+        if (lane == 0) {
+            tc::commit(drain);
+            if (!ptx::mbar_wait(drain, 0)) atomicOr(&g_attn_timeout, 4u);
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 8) {
+        // ---------------------------------------------------------- widening
+        const int t = threadIdx.x - 128;  // this thread's token of a tile
+        bool ok = true;
+        while (ok) {
+            const Span s = span_of();
+            float r_ref = 0x1p-100f;
+            for (int i = 0; i < s.n && ok; ++i) {
+                const uint32_t n = seq + i, stage = n % C::kVStages, buf = n & 1;
+                if (!(ok = wait(v8_full + 8 * stage, (n / C::kVStages) & 1))) break;
+                if (n >= 2 && !(ok = wait(v16_empty + 8 * buf, ((n >> 1) - 1) & 1))) break;
+                const uint8_t* v8 = smem + C::kV8 + stage * kTileBytes + t * kD;
+                uint8_t* v16 = smem + C::kV16 + buf * 2 * kTileBytes + t * 128;
+                const bool in = (s.f0 + i) * kTok + t < it.len;  // else anything may be there
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint4 v = *reinterpret_cast<const uint4*>(v8 + ((c ^ (t & 7)) << 4));
+                    if (!in) v = make_uint4(0, 0, 0, 0);
+                    const uint4 lo = make_uint4(e4m3x2_lo_to_f16x2(v.x), e4m3x2_hi_to_f16x2(v.x), e4m3x2_lo_to_f16x2(v.y),
+                                                e4m3x2_hi_to_f16x2(v.y));
+                    const uint4 hi = make_uint4(e4m3x2_lo_to_f16x2(v.z), e4m3x2_hi_to_f16x2(v.z), e4m3x2_lo_to_f16x2(v.w),
+                                                e4m3x2_hi_to_f16x2(v.w));
+                    uint8_t* half = v16 + (c >> 2) * kTileBytes;  // columns 64 (c / 4) ..
+                    *reinterpret_cast<uint4*>(half + ((((c & 3) * 2) ^ (t & 7)) << 4)) = lo;
+                    *reinterpret_cast<uint4*>(half + ((((c & 3) * 2 + 1) ^ (t & 7)) << 4)) = hi;
+                }
+                // R: the power of two below the largest value scale so far, the same in every warp.
+                const float* sc = reinterpret_cast<const float*>(smem + C::kScale8 + stage * 2 * kTok * 4);
+                uint32_t rb = 0;
+#pragma unroll
+                for (int j = 0; j < kTok / 32; ++j) rb = max(rb, scale_exponent(sc[kTok + j * 32 + lane]));
+                rb = __reduce_max_sync(0xffffffffu, rb);
+                r_ref = fmaxf(__uint_as_float(rb), r_ref);
+                float* out = reinterpret_cast<float*>(smem + C::kScale16 + buf * 2 * kTok * 4);
+                out[t] = sc[t];
+                out[kTok + t] = sc[kTok + t] * __fdividef(0x1p6f, r_ref);
+                if (t == 0) reinterpret_cast<float*>(smem + C::kR)[buf] = r_ref;
+                fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive(v16_full + 8 * buf);
+                    ptx::mbar_arrive(v8_empty + 8 * stage);
+                }
+            }
+            if (!ok || !next(s)) break;
+        }
+    } else if (warp >= 8) {
+        // ----------------------------------------------------------- softmax
+        const int slot = (warp - 8) >> 2, quad = warp & 3;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const uint32_t t_s = lane_base + slot * 128, t_o = lane_base + 256 + slot * 128;
+        const int row_in = (kPair ? slot * 128 : 0) + quad * 32 + lane;  // this thread's row of the row tile
+        float* qscale = reinterpret_cast<float*>(smem + C::kQScale);
+        float4* ml = reinterpret_cast<float4*>(smem + C::kML);
+        uint32_t jobs_done = 0, item = 0;
+        bool ok = true;
+        while (ok) {
+            const Span s = span_of();
+            // Queries. The MMAs of the item before have read theirs (item_done was waited for).
+            {
+                constexpr int kWarpRows = kPair ? 32 : 16;  // the 8 warps share the rows
+                const int r0 = (warp - 8) * kWarpRows, c = lane & 15;
+#pragma unroll 4
+                for (int r = r0 + (lane >> 4); r < r0 + kWarpRows; r += 2) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (r < s.nrows) {
+                        const int qi = (s.row0 + r) / a.group, hg = (s.row0 + r) - qi * a.group;
+                        v = ld_dep_v4(a.q + (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD + c * 8);
+                    }
+                    uint32_t top = top_bits(v);
+#pragma unroll
+                    for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // (a zero row's exponent is as good as any)
+                    const uint32_t e = top == 0 ? 127 : min(max(top >> 7, 8u), 253u);
+                    const float up = __uint_as_float((261 - e) << 23);  // 2^(134 - e)
+                    if (c == 0) qscale[r] = fmaxf(__uint_as_float((e - 7) << 23) * a.scale_log2, 0x1p-126f);
+                    const bool bad = top >= 0x7F80u;  // NaN or infinite: the whole row is NaN
+                    float f[8];
+                    unpack_bf16x8(v, f);
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        float d[4];
+                        hi[w] = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; j += 2) {
+                            const float x0 = f[w * 4 + j] * up, x1 = f[w * 4 + j + 1] * up;
+                            const uint32_t pair = cvt_e4m3x2(x0, x1), back = e4m3x2_lo_to_f16x2(pair);
+                            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
+                            d[j] = x0 - b.x;
+                            d[j + 1] = x1 - b.y;
+                            hi[w] |= pair << (8 * j);
+                        }
+                        lo[w] = cvt_e4m3x2(d[0], d[1]) | (cvt_e4m3x2(d[2], d[3]) << 16);
+                        if (bad) hi[w] = 0x7F7F7F7Fu;
+                    }
+                    uint8_t* q = smem + C::kQ + (r >> 7) * 2 * kTileBytes + (r & 127) * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+                    *reinterpret_cast<uint2*>(q) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2*>(q + kTileBytes) = make_uint2(lo[0], lo[1]);
+                }
+                fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(q_full);
+                if (!(ok = wait(q_full, item & 1))) break;
+            }
+            const float qs = qscale[row_in];
+            const int r = s.row0 + row_in;
+            const bool rows_here = row_in - lane < s.nrows;  // of this warp
+            const int limit = it.len - it.nq + r / a.group + 1;                     // first position the row does not see
+            const int all_see = it.len - it.nq + (r - lane) / a.group + 1;          // positions below it need no mask
+            float m = kNegInf, l = 0.0f, r_ref = 0x1p-100f;  // m: largest (q . k) s_k, not yet times qs
+            const int first = kPair ? 0 : slot, step = kPair ? 1 : 2;
+            const int last = slot < s.slots ? s.n : 0;
+            int mine = 0;
+            for (int i = first; i < last && ok; i += step, ++mine) {
+                const uint32_t n = seq + i, buf = n & 1;
+                if (!(ok = wait(s_full + 8 * slot, jobs_done & 1))) break;
+                if (!(ok = wait(v16_full + 8 * buf, (n >> 1) & 1))) break;
+                tc::fence_after_sync();
+                if (rows_here) {
+                    const float* ks = reinterpret_cast<const float*>(smem + C::kScale16 + buf * 2 * kTok * 4);
+                    const float* vs = ks + kTok;
+                    const int pos = (s.f0 + i) * kTok;
+                    const bool edge = pos + kTok > all_see;
+                    float top = kNegInf;
+#pragma unroll
+                    for (int c = 0; c < kTok; c += 64) {
+                        uint32_t v[64];
+                        tc::ld_32x32b_x32(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(v));
+                        tc::ld_32x32b_x32(t_s + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+                        tc::wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 64; j += 4) {
+                            const float4 k4 = *reinterpret_cast<const float4*>(ks + c + j);
+                            float2 x0 = __fmul2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), make_float2(k4.x, k4.y));
+                            float2 x1 = __fmul2_rn(make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), make_float2(k4.z, k4.w));
+                            if (edge) {
+                                if (pos + c + j >= limit) x0.x = kNegInf;
+                                if (pos + c + j + 1 >= limit) x0.y = kNegInf;
+                                if (pos + c + j + 2 >= limit) x1.x = kNegInf;
+                                if (pos + c + j + 3 >= limit) x1.y = kNegInf;
+                            }
+                            top = fmaxf(fmaxf(top, fmaxf(x0.x, x0.y)), fmaxf(x1.x, x1.y));
+                        }
+                    }
+                    const float r_new = reinterpret_cast<const float*>(smem + C::kR)[buf];
+                    // The reference moves only when the maximum passes it by 2^8.
+                    const float m_new = (top - m) * qs > 8.0f ? top : m;
+                    const float mq = (m_new == kNegInf ? 0.0f : m_new) * qs;
+                    const float alpha = m_new == m ? 1.0f : ex2(fmaf(m, qs, -mq));
+                    const float beta = alpha * __fdividef(r_ref, r_new);
+                    m = m_new;
+                    r_ref = r_new;
+                    l *= alpha;
+                    if (mine > 0 && __any_sync(0xffffffffu, beta != 1.0f)) {
+                        if (!(ok = wait(pv_done + 8 * slot, (jobs_done - 1) & 1))) break;
+                        tc::fence_after_sync();
+#pragma unroll 1
+                        for (int c = 0; c < kD; c += 16) {
+                            uint32_t o[16];
+                            tc::ld_32x32b_x16(t_o + c, o);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * beta);
+                            st_16(t_o + c, o);
+                        }
+                    }
+                    const float2 qs2 = make_float2(qs, qs), mq2 = make_float2(-mq, -mq);
+                    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int c = 0; c < kTok; c += 32) {
+                        uint32_t v[32], w[16];
+                        tc::ld_32x32b_x32(t_s + c, v);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 k4 = *reinterpret_cast<const float4*>(ks + c + j), v4 = *reinterpret_cast<const float4*>(vs + c + j);
+                            const float2 k2[2] = {make_float2(k4.x, k4.y), make_float2(k4.z, k4.w)};
+                            const float2 v2[2] = {make_float2(v4.x, v4.y), make_float2(v4.z, v4.w)};
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int at = j + 2 * h;
+                                float2 y = __fmul2_rn(make_float2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), k2[h]);
+                                y = __ffma2_rn(y, qs2, mq2);
+                                float2 p = make_float2(ex2(y.x), ex2(y.y));
+                                float2 u2 = __fmul2_rn(p, v2[h]);
+                                if (edge) {  // a masked weight is zero whatever its scores and scales hold
+                                    if (pos + c + at >= limit) p.x = u2.x = 0.0f;
+                                    if (pos + c + at + 1 >= limit) p.y = u2.y = 0.0f;
+                                }
+                                sum = __fadd2_rn(sum, p);
+                                const __half2 h2 = __floats2half2_rn(u2.x, u2.y);
+                                w[at >> 1] = *reinterpret_cast<const uint32_t*>(&h2);
+                            }
+                        }
+                        st_16(t_s + (c >> 1), w);  // over scores already read
+                    }
+                    l += sum.x + sum.y;
+                    wait_st();
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(p_full + 8 * slot);
+                ++jobs_done;
+            }
+            if (!ok) break;
+            // The item's result: o = sum p s_v v / (2^6 / R) and, per row, its reference (log2) and sum of p.
+            float mx = m == kNegInf ? kNegInf : m * qs;
+            if (!kPair && slot == 1) {
+                ml[row_in] = make_float4(mx, l, r_ref, 0.0f);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ml_full);
+            }
+            if (!(ok = wait(item_done, item & 1))) break;
+            tc::fence_after_sync();
+            if (kPair || slot == 0) {
+                float f0 = r_ref * 0x1p-6f, f1 = 0.0f;
+                bool has1 = false;
+                if (!kPair) {
+                    if (!(ok = wait(ml_full, item & 1))) break;
+                    const float4 other = ml[row_in];
+                    const float most = fmaxf(mx, other.x), use = most == kNegInf ? 0.0f : most;
+                    const float e0 = ex2(mx - use), e1 = ex2(other.x - use);
+                    f0 *= e0;
+                    f1 = other.z * 0x1p-6f * e1;
+                    l = l * e0 + other.y * e1;
+                    mx = most;
+                    has1 = s.n > 1;
+                }
+                const bool has0 = s.n > 0 && slot < s.slots;
+                const int part = 2 * blockIdx.x + (it.first > u_begin ? 1 : 0);
+                const int qi = r / a.group, hg = r - qi * a.group;
+                const int64_t orow = static_cast<int64_t>(it.q0 + qi) * (a.c.heads * a.group) + it.h * a.group + hg;
+                const int64_t prow = static_cast<int64_t>(part) * a.rows + row_in;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                if (rows_here) {
+#pragma unroll 1
+                    for (int c = 0; c < kD; c += 16) {
+                        uint32_t o0[16], o1[16];
+                        if (has0) tc::ld_32x32b_x16(t_o + c, o0);
+                        if (has1) tc::ld_32x32b_x16(t_o + 128 + c, o1);
+                        tc::wait_ld();
+                        float o[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            o[j] = has0 && f0 != 0.0f ? __uint_as_float(o0[j]) * f0 : 0.0f;
+                            if (has1 && f1 != 0.0f) o[j] = fmaf(__uint_as_float(o1[j]), f1, o[j]);
+                        }
+                        if (row_in < s.nrows) {
+                            if (s.whole) {
+                                uint4* dst = reinterpret_cast<uint4*>(a.out + ((orow * kD + c) >> 1));
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    dst[j] = make_uint4(pack_bf16x2(o[8 * j] * inv, o[8 * j + 1] * inv),
+                                                        pack_bf16x2(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
+                                                        pack_bf16x2(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
+                                                        pack_bf16x2(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
+                            } else {
+                                float4* dst = reinterpret_cast<float4*>(a.part_o + prow * kD + c);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (row_in < s.nrows) {
+                        if (!s.whole)
+                            *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(mx, l);
+                        else if (a.lse)
+                            a.lse[orow] = l == 0.0f ? kNegInf : (mx + log2f(l)) * 0.6931471805599453f;
+                    }
+                }
+                if (!s.whole && u == it.first && warp == 8 && lane == 0) write_split(a, it, per, part, s.row0, s.nrows);
+            }
+            tc::fence_before_sync();
+            ++item;
+            if (!next(s)) break;
+        }
+    }
+
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 2) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <bool kPair>
+cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+    using C = Tc<kPair>;
+    static std::atomic<bool> configured[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    auto kernel = kv_attention_tc_kernel<kPair>;
+    if (!configured[dev & 63].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+        if (e != cudaSuccess) return e;
+        configured[dev & 63].store(true, std::memory_order_relaxed);
+    }
+    // The cache as rows of one token and head; a copy is a page's tokens, 128 at most.
+    const uint64_t tokens = static_cast<uint64_t>(a.c.num_pages) * a.c.heads << a.c.page_log2;
+    const uint32_t box = 1u << a.c.page_log2 < kTok ? 1u << a.c.page_log2 : kTok;
+    CUtensorMap k_map, v_map;
+    if (!encode_tmap_2d_u8(&k_map, a.c.k, kD, tokens, kD, kD, box, true) ||
+        !encode_tmap_2d_u8(&v_map, a.c.v, kD, tokens, kD, kD, box, true))
+        return cudaErrorInvalidValue;
+    const TcExtra x = {tile_wait_limit_ns(), tile_withhold_first_load() ? 1 : 0};
+    return launch_dependent(kernel, dim3(num_sms), kThreads, C::kBytes, stream, 1, a, k_map, v_map, x);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tc(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+    return a.rows > 128 ? launch<true>(a, num_sms, stream) : launch<false>(a, num_sms, stream);
+}
+
+unsigned int read_and_clear_attn_timeout() {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_attn_timeout, sizeof(v)) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (v) {
+        const unsigned int zero = 0;
+        cudaMemcpyToSymbol(g_attn_timeout, &zero, sizeof(zero));
+    }
+    return v;
+}
+
+}  // namespace fp8act
