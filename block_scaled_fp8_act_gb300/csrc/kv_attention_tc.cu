@@ -45,6 +45,10 @@ constexpr int kLeastUnits = 2;  // least share of a CTA
 using Work = Units<kTok, kItemCost>;
 
 constexpr int kThreads = 512;  // warps 0 keys, 1 values, 2 MMA; 4..7 widening; 8..11 and 12..15 softmax
+// A softmax thread keeps a row of 128 scores: the other two warpgroups hand it
+// registers, 256 x 56 + 256 x 200 = 512 x 128, exactly the launch's.
+constexpr int kRegsOther = 56, kRegsSoftmax = 200;
+static_assert(256 * kRegsOther + 256 * kRegsSoftmax <= kThreads * 128, "register split exceeds the launch's registers");
 constexpr int kTileBytes = kTok * kD;
 
 template <bool kPair>  // two row tiles of 128 on the same tokens
@@ -123,6 +127,10 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ float2 pair_of(const uint32_t (&v)[kTok], int j) {
+    return make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+}
 
 template <bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __grid_constant__ AttnArgs a,
@@ -233,6 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
         return true;
     };
 
+    if (warp < 8) {
+    tc::regs_decrease<kRegsOther>();
     if (!any) {
         // nothing to do: only tensor memory to free
     } else if (warp < 2) {
@@ -366,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
             if (!ptx::mbar_wait(drain, 0)) atomicOr(&g_attn_timeout, 4u);
         }
         __syncwarp();
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= 4) {
         // ---------------------------------------------------------- widening
         const int t = threadIdx.x - 128;  // this thread's token of a tile
         bool ok = true;
@@ -412,8 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
             }
             if (!ok || !next(s)) break;
         }
-    } else if (warp >= 8) {
+    }
+    } else {
         // ----------------------------------------------------------- softmax
+        tc::regs_increase<kRegsSoftmax>();
         const int slot = (warp - 8) >> 2, quad = warp & 3;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const uint32_t t_s = lane_base + slot * 128, t_o = lane_base + 256 + slot * 128;
@@ -421,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
         float* qscale = reinterpret_cast<float*>(smem + C::kQScale);
         float4* ml = reinterpret_cast<float4*>(smem + C::kML);
         uint32_t jobs_done = 0, item = 0;
-        bool ok = true;
+        bool ok = any;
         while (ok) {
             const Span s = span_of();
             // Queries. The MMAs of the item before have read theirs (item_done was waited for).
@@ -490,27 +502,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                     const float* vs = ks + kTok;
                     const int pos = (s.f0 + i) * kTok;
                     const bool edge = pos + kTok > all_see;
+                    uint32_t v[kTok];
+#pragma unroll
+                    for (int c = 0; c < kTok; c += 32)
+                        tc::ld_32x32b_x32(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(v + c));
+                    tc::wait_ld();
                     float top = kNegInf;
 #pragma unroll
-                    for (int c = 0; c < kTok; c += 64) {
-                        uint32_t v[64];
-                        tc::ld_32x32b_x32(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(v));
-                        tc::ld_32x32b_x32(t_s + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-                        tc::wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 64; j += 4) {
-                            const float4 k4 = *reinterpret_cast<const float4*>(ks + c + j);
-                            float2 x0 = __fmul2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), make_float2(k4.x, k4.y));
-                            float2 x1 = __fmul2_rn(make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), make_float2(k4.z, k4.w));
-                            if (edge) {
-                                if (pos + c + j >= limit) x0.x = kNegInf;
-                                if (pos + c + j + 1 >= limit) x0.y = kNegInf;
-                                if (pos + c + j + 2 >= limit) x1.x = kNegInf;
-                                if (pos + c + j + 3 >= limit) x1.y = kNegInf;
-                            }
-                            top = fmaxf(fmaxf(top, fmaxf(x0.x, x0.y)), fmaxf(x1.x, x1.y));
-                        }
+                    for (int j = 0; j < kTok; j += 4) {
+                        const float4 k4 = *reinterpret_cast<const float4*>(ks + j);
+                        const float2 x0 = __fmul2_rn(pair_of(v, j), make_float2(k4.x, k4.y));
+                        const float2 x1 = __fmul2_rn(pair_of(v, j + 2), make_float2(k4.z, k4.w));
+                        v[j] = __float_as_uint(x0.x);
+                        v[j + 1] = __float_as_uint(x0.y);
+                        v[j + 2] = __float_as_uint(x1.x);
+                        v[j + 3] = __float_as_uint(x1.y);
                     }
+                    if (edge) {  // a masked score's weight is zero (p = 0, and see below)
+#pragma unroll
+                        for (int j = 0; j < kTok; ++j)
+                            if (pos + j >= limit) v[j] = 0xFF800000u;
+                    }
+#pragma unroll
+                    for (int j = 0; j < kTok; j += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
                     const float r_new = reinterpret_cast<const float*>(smem + C::kR)[buf];
                     // The reference moves only when the maximum passes it by 2^8.
                     const float m_new = (top - m) * qs > 8.0f ? top : m;
@@ -537,31 +551,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                     float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
                     for (int c = 0; c < kTok; c += 32) {
-                        uint32_t v[32], w[16];
-                        tc::ld_32x32b_x32(t_s + c, v);
-                        tc::wait_ld();
+                        uint32_t w[16];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 k4 = *reinterpret_cast<const float4*>(ks + c + j), v4 = *reinterpret_cast<const float4*>(vs + c + j);
-                            const float2 k2[2] = {make_float2(k4.x, k4.y), make_float2(k4.z, k4.w)};
-                            const float2 v2[2] = {make_float2(v4.x, v4.y), make_float2(v4.z, v4.w)};
+                        for (int j = c; j < c + 32; j += 4) {
+                            const float4 v4 = *reinterpret_cast<const float4*>(vs + j);
+                            const float2 y0 = __ffma2_rn(pair_of(v, j), qs2, mq2), y1 = __ffma2_rn(pair_of(v, j + 2), qs2, mq2);
+                            const float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
+                            const float2 w0 = __fmul2_rn(p0, make_float2(v4.x, v4.y)), w1 = __fmul2_rn(p1, make_float2(v4.z, v4.w));
+                            sum = __fadd2_rn(sum, __fadd2_rn(p0, p1));
+                            const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
+                            w[(j - c) >> 1] = *reinterpret_cast<const uint32_t*>(&h0);
+                            w[((j - c) >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                        }
+                        if (edge) {  // whatever the masked token's scale holds
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int at = j + 2 * h;
-                                float2 y = __fmul2_rn(make_float2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), k2[h]);
-                                y = __ffma2_rn(y, qs2, mq2);
-                                float2 p = make_float2(ex2(y.x), ex2(y.y));
-                                float2 u2 = __fmul2_rn(p, v2[h]);
-                                if (edge) {  // a masked weight is zero whatever its scores and scales hold
-                                    if (pos + c + at >= limit) p.x = u2.x = 0.0f;
-                                    if (pos + c + at + 1 >= limit) p.y = u2.y = 0.0f;
-                                }
-                                sum = __fadd2_rn(sum, p);
-                                const __half2 h2 = __floats2half2_rn(u2.x, u2.y);
-                                w[at >> 1] = *reinterpret_cast<const uint32_t*>(&h2);
+                            for (int j = 0; j < 32; j += 2) {
+                                if (pos + c + j >= limit) w[j >> 1] = 0u;
+                                else if (pos + c + j + 1 >= limit) w[j >> 1] &= 0xFFFFu;
                             }
                         }
-                        st_16(t_s + (c >> 1), w);  // over scores already read
+                        st_16(t_s + (c >> 1), w);  // over the scores
                     }
                     l += sum.x + sum.y;
                     wait_st();
