@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG>::kThreads, 1) kv_attent
             // The tile's largest value scale as a power of two (a NaN scale marks a poisoned token).
             const uint32_t rb = __reduce_max_sync(0xffffffffu, scale_exponent(sv[lane]));
             const float r_new = fmaxf(__uint_as_float(rb), r_ref);
-            const float r_step = __fdividef(r_ref, r_new), r_inv = __fdividef(0x1p6f, r_new);
+            const float r_step = r_new == r_ref ? 1.0f : __fdividef(r_ref, r_new), r_inv = __fdividef(0x1p6f, r_new);
             r_ref = r_new;
             float ks[4], vs[4];
 #pragma unroll
@@ -532,8 +532,8 @@ __global__ void __launch_bounds__(kJoinRows * 32) kv_attention_join_kernel(const
             float2 v[kAhead][kV / 2];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const float2* src = reinterpret_cast<const float2*>(a.part_o + slot_of(base + min(i0 + j, here - 1)) * kD) +
-                                    lane * (kV / 2);
+                if (i0 + j >= here) break;
+                const float2* src = reinterpret_cast<const float2*>(a.part_o + slot_of(base + i0 + j) * kD) + lane * (kV / 2);
 #pragma unroll
                 for (int x = 0; x < kV / 2; ++x) v[j][x] = __ldcg(src + x);
             }

@@ -8,11 +8,14 @@
 // largest value is in [128, 256), is the sum of two E4M3 rows, hi = E4M3(q) and
 // lo = E4M3(q - hi), whose products add up in one accumulator. A bf16 value
 // has 8 significant bits and each part 4, so hi + lo is exact down to 2^-9 of
-// the row's largest value, and within 2^-17 of it below. O += W V runs in f16
-// (kind::f16): four warps widen the value codes exactly, the weights
-// W = p * s_v are rounded to f16 (11 bits; one or two E4M3 parts would give 4
-// or 8) after scaling by 2^6 / R, R the power of two below the largest s_v so
-// far, and go from registers to tensor memory over the scores they came from.
+// the row's largest value, and within 2^-17 of it below. O += P V runs in f16
+// (kind::f16; an E4M3 P would have 4 bits): four warps widen the value codes
+// times s_v 2^6 / R, R the power of two below the largest s_v so far, so that
+// values keep their 11 bits down to 2^-20 of the largest; the weights, scaled by
+// 2^6 too, keep theirs down to 2^-20 of the row's reference, and go from
+// registers to tensor memory over the scores they came from. A token whose value
+// scale is NaN (poisoned) gets zero values and a NaN key scale, which reaches
+// the rows that see it and no other.
 //
 // Two score tiles are in flight, each with a warpgroup whose threads own a row:
 // with more than 128 rows they are the two halves of a 256-row tile on the same
@@ -20,8 +23,8 @@
 // even and the odd token tiles of one row tile of up to 128 rows, whose two
 // results join in tensor memory at the end (warps without rows skip the
 // softmax). While one warpgroup works the tensor cores serve the other. A
-// row's reference maximum moves only when a score passes it by 2^8, so the
-// output accumulator is seldom rescaled.
+// row's reference moves only when a score passes it by 2^8, so the output
+// accumulator is seldom rescaled.
 //
 // Every wait is bounded by wall time. The first that gives up sets the error
 // word and the CTA's abort flag; every role then leaves its loop, copies and
@@ -61,8 +64,8 @@ struct Tc {
     static constexpr int kV8 = kK + kKStages * kTileBytes;
     static constexpr int kV16 = kV8 + kVStages * kTileBytes;       // 2 buffers of two 64-column halves
     static constexpr int kScale8 = kV16 + 2 * 2 * kTileBytes;      // per value stage: key scales, value scales
-    static constexpr int kScale16 = kScale8 + kVStages * 2 * kTok * 4;  // per buffer: the same, value scales times 2^6 / R
-    static constexpr int kR = kScale16 + 2 * 2 * kTok * 4;         // per buffer: R
+    static constexpr int kScale16 = kScale8 + kVStages * 2 * kTok * 4;  // per buffer: key scales
+    static constexpr int kR = kScale16 + 2 * kTok * 4;             // per buffer: R
     static constexpr int kQScale = kR + 16;
     static constexpr int kML = kQScale + kQTiles * 128 * 4;        // second result's (maximum, sum, R) per row
     static constexpr int kBytes = kML + 128 * 16 + 1024;           // (the base is rounded up to 1024)
@@ -83,16 +86,40 @@ __device__ __forceinline__ void st_16(uint32_t taddr, const uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The whole warp executes these, and one elected lane issues the MMA.
 // D[tmem] (+)= A[tmem] x B[smem desc], f16 with fp32 accumulation.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                            uint32_t accumulate) {
     asm volatile(
         "{\n"
-        ".reg .pred p;\n"
+        ".reg .pred p, e;\n"
+        "elect.sync _|e, 0xffffffff;\n"
         "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
         "}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D[tmem] (+)= A[smem desc] x B[smem desc], E4M3 with fp32 accumulation.
+__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p, e;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t mbar) {
+    asm volatile(
+        "{\n"
+        ".reg .pred e;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+        "}\n" ::"r"(mbar)
         : "memory");
 }
 
@@ -125,6 +152,11 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in
 // Arrive on `bar` (one of its expected arrivals) once this thread's cp.asyncs so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ float4 lds_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -196,13 +228,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
 
     // A bounded wait by the whole warp; false once any wait of the CTA has run out.
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        // The timer is read only after a while: it is far from the SM, and a wait here is a link of the chain scores -
+        // softmax - weights (read at the first miss it took 166 us for a 512-token chunk over 16384 instead of XX).
         bool ok = ptx::mbar_try_wait(bar, parity);
-        if (!ok) {
-            const uint64_t start = ptx::globaltimer_ns();
-            while (!ok) {
-#pragma unroll 1
-                for (int i = 0; i < 16 && !ok; ++i) ok = ptx::mbar_try_wait(bar, parity);
-                if (!ok && (s_abort || ptx::globaltimer_ns() - start > x.wait_ns)) break;
+        uint64_t start = 0;
+        for (uint32_t n = 1; !ok; ++n) {
+            ok = ptx::mbar_try_wait(bar, parity);
+            if (!ok && n % 64 == 0) {
+                const uint64_t now = ptx::globaltimer_ns();
+                if (start == 0) start = now;
+                if (s_abort || now - start > x.wait_ns) break;
             }
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -314,8 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
         // --------------------------------------------------------------- MMA
         bool ok = true;
         uint32_t item = 0;
-        uint32_t done[2] = {0, 0};  // score tiles issued per slot
-        uint32_t waited[2] = {0, 0};
+        uint32_t waited[2] = {0, 0};  // weight tiles waited for per slot
         while (ok) {
             const Span s = span_of();
             const int depth = s.slots;                            // score tiles in flight
@@ -324,57 +358,52 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
             auto tile_of = [&](int j) { return kPair ? j / s.slots : j; };
             auto first_use = [&](int j) { return !kPair || slot_of(j) == 0; };
             auto last_use = [&](int j) { return !kPair || slot_of(j) == s.slots - 1; };
+            auto keys = [&](int j) {  // wait for the keys of score tile j
+                const uint32_t n = seq + tile_of(j);
+                if (j < jobs && first_use(j)) ok = wait(k_full + 8 * (n % C::kKStages), (n / C::kKStages) & 1);
+                return ok;
+            };
             auto scores = [&](int j) {
                 const int slot = slot_of(j);
-                const uint32_t n = seq + tile_of(j), stage = n % C::kKStages;
-                if (first_use(j) && !(ok = wait(k_full + 8 * stage, (n / C::kKStages) & 1))) return;
-                tc::fence_after_sync();
-                if (lane == 0) {
-                    const uint32_t q = base + C::kQ + (kPair ? slot : 0) * 2 * kTileBytes, k = base + C::kK + stage * kTileBytes;
+                const uint32_t stage = (seq + tile_of(j)) % C::kKStages;
+                const uint32_t q = base + C::kQ + (kPair ? slot : 0) * 2 * kTileBytes, k = base + C::kK + stage * kTileBytes;
+                const uint64_t q_desc = tc::desc_kmajor_sw128(q), k_desc = tc::desc_kmajor_sw128(k);
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                for (int part = 0; part < 2; ++part)
 #pragma unroll
-                        for (int i = 0; i < kD / 32; ++i)
-                            tc::mma_f8f6f4(tmem + slot * 128, tc::desc_kmajor_sw128(q + part * kTileBytes + 32 * i),
-                                           tc::desc_kmajor_sw128(k + 32 * i), kIdescScores, part + i > 0 ? 1u : 0u);
-                    tc::commit(s_full + 8 * slot);
-                    if (last_use(j)) tc::commit(k_empty + 8 * stage);
-                }
-                __syncwarp();
-                ++done[slot];
+                    for (int i = 0; i < kD / 32; ++i)  // (a descriptor counts 16 bytes)
+                        mma_e4m3_ss(tmem + slot * 128, q_desc + (part * kTileBytes + 32 * i) / 16, k_desc + 2 * i, kIdescScores,
+                                    part + i > 0 ? 1u : 0u);
+                commit_elected(s_full + 8 * slot);
+                if (last_use(j)) commit_elected(k_empty + 8 * stage);
             };
             if (!(ok = wait(q_full, item & 1))) break;
-            for (int j = 0; j < depth && j < jobs && ok; ++j) scores(j);
+            tc::fence_after_sync();
+            for (int j = 0; j < depth && j < jobs && keys(j); ++j) scores(j);
             for (int j = 0; j < jobs && ok; ++j) {
                 const int slot = slot_of(j);
-                const uint32_t n = seq + tile_of(j), buf = n & 1;
-                if (!(ok = wait(p_full + 8 * slot, waited[slot]++ & 1))) break;
-                if (first_use(j) && !(ok = wait(v16_full + 8 * buf, (n >> 1) & 1))) break;
+                const uint32_t buf = (seq + tile_of(j)) & 1;
+                // (the softmax warps have waited for the widened values before they arrive)
+                if (!keys(j + depth) || !(ok = wait(p_full + 8 * slot, waited[slot]++ & 1))) break;
                 tc::fence_after_sync();
-                if (lane == 0) {
-                    const uint32_t v = base + C::kV16 + buf * 2 * kTileBytes;
-                    const bool fresh = kPair ? tile_of(j) == 0 : j < 2;
+                const uint64_t v_desc = desc_values(base + C::kV16 + buf * 2 * kTileBytes);
+                const bool fresh = kPair ? tile_of(j) == 0 : j < 2;
 #pragma unroll
-                    for (int i = 0; i < kTok / 16; ++i)
-                        mma_f16_ts(tmem + 256 + slot * 128, tmem + slot * 128 + 8 * i, desc_values(v + 2048 * i), kIdescValues,
-                                   fresh && i == 0 ? 0u : 1u);
-                    tc::commit(pv_done + 8 * slot);
-                    if (last_use(j)) tc::commit(v16_empty + 8 * buf);
-                }
-                __syncwarp();
+                for (int i = 0; i < kTok / 16; ++i)
+                    mma_f16_ts(tmem + 256 + slot * 128, tmem + slot * 128 + 8 * i, v_desc + 2048 * i / 16, kIdescValues,
+                               fresh && i == 0 ? 0u : 1u);
+                commit_elected(pv_done + 8 * slot);
+                if (last_use(j)) commit_elected(v16_empty + 8 * buf);
                 if (j + depth < jobs) scores(j + depth);
             }
             if (!ok) break;
-            if (lane == 0) tc::commit(item_done);
-            __syncwarp();
+            commit_elected(item_done);
             ++item;
             if (!next(s)) break;
         }
         // No MMA may still run when tensor memory is freed or the CTA leaves.
-        if (lane == 0) {
-            tc::commit(drain);
-            if (!ptx::mbar_wait(drain, 0)) atomicOr(&g_attn_timeout, 4u);
-        }
+        commit_elected(drain);
+        if (!ptx::mbar_wait(drain, 0)) atomicOr(&g_attn_timeout, 4u);
         __syncwarp();
     } else if (warp >= 4) {
         // ---------------------------------------------------------- widening
@@ -387,21 +416,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                 const uint32_t n = seq + i, stage = n % C::kVStages, buf = n & 1;
                 if (!(ok = wait(v8_full + 8 * stage, (n / C::kVStages) & 1))) break;
                 if (n >= 2 && !(ok = wait(v16_empty + 8 * buf, ((n >> 1) - 1) & 1))) break;
-                const uint8_t* v8 = smem + C::kV8 + stage * kTileBytes + t * kD;
-                uint8_t* v16 = smem + C::kV16 + buf * 2 * kTileBytes + t * 128;
-                const bool in = (s.f0 + i) * kTok + t < it.len;  // else anything may be there
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint4 v = *reinterpret_cast<const uint4*>(v8 + ((c ^ (t & 7)) << 4));
-                    if (!in) v = make_uint4(0, 0, 0, 0);
-                    const uint4 lo = make_uint4(e4m3x2_lo_to_f16x2(v.x), e4m3x2_hi_to_f16x2(v.x), e4m3x2_lo_to_f16x2(v.y),
-                                                e4m3x2_hi_to_f16x2(v.y));
-                    const uint4 hi = make_uint4(e4m3x2_lo_to_f16x2(v.z), e4m3x2_hi_to_f16x2(v.z), e4m3x2_lo_to_f16x2(v.w),
-                                                e4m3x2_hi_to_f16x2(v.w));
-                    uint8_t* half = v16 + (c >> 2) * kTileBytes;  // columns 64 (c / 4) ..
-                    *reinterpret_cast<uint4*>(half + ((((c & 3) * 2) ^ (t & 7)) << 4)) = lo;
-                    *reinterpret_cast<uint4*>(half + ((((c & 3) * 2 + 1) ^ (t & 7)) << 4)) = hi;
-                }
                 // R: the power of two below the largest value scale so far, the same in every warp.
                 const float* sc = reinterpret_cast<const float*>(smem + C::kScale8 + stage * 2 * kTok * 4);
                 uint32_t rb = 0;
@@ -409,9 +423,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                 for (int j = 0; j < kTok / 32; ++j) rb = max(rb, scale_exponent(sc[kTok + j * 32 + lane]));
                 rb = __reduce_max_sync(0xffffffffu, rb);
                 r_ref = fmaxf(__uint_as_float(rb), r_ref);
-                float* out = reinterpret_cast<float*>(smem + C::kScale16 + buf * 2 * kTok * 4);
-                out[t] = sc[t];
-                out[kTok + t] = sc[kTok + t] * __fdividef(0x1p6f, r_ref);
+                const bool in = (s.f0 + i) * kTok + t < it.len;  // else anything may be there
+                const float sv = sc[kTok + t], sk = sc[t];
+                const bool poisoned = !(fabsf(sv) < 3e38f);
+                const float f = in && !poisoned ? sv * __fdividef(0x1p6f, r_ref) : 0.0f;
+                const uint8_t* v8 = smem + C::kV8 + stage * kTileBytes + t * kD;
+                uint8_t* v16 = smem + C::kV16 + buf * 2 * kTileBytes + t * 128;
+                const __half2 f2 = __float2half2_rn(f);
+                // code * s_v 2^6 / R in one f16 rounding of the product of the code and the f16 scale's two parts
+                const __half2 g2 = __float2half2_rn(f - __low2float(f2));
+                auto widen = [&](uint32_t h) {
+                    const __half2 c = *reinterpret_cast<const __half2*>(&h);
+                    const __half2 w = __hfma2(c, f2, __hmul2(c, g2));
+                    return *reinterpret_cast<const uint32_t*>(&w);
+                };
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint4 v = *reinterpret_cast<const uint4*>(v8 + ((c ^ (t & 7)) << 4));
+                    if (!in || poisoned) v = make_uint4(0, 0, 0, 0);
+                    const uint4 lo = make_uint4(widen(e4m3x2_lo_to_f16x2(v.x)), widen(e4m3x2_hi_to_f16x2(v.x)),
+                                                widen(e4m3x2_lo_to_f16x2(v.y)), widen(e4m3x2_hi_to_f16x2(v.y)));
+                    const uint4 hi = make_uint4(widen(e4m3x2_lo_to_f16x2(v.z)), widen(e4m3x2_hi_to_f16x2(v.z)),
+                                                widen(e4m3x2_lo_to_f16x2(v.w)), widen(e4m3x2_hi_to_f16x2(v.w)));
+                    uint8_t* half = v16 + (c >> 2) * kTileBytes;  // columns 64 (c / 4) ..
+                    *reinterpret_cast<uint4*>(half + ((((c & 3) * 2) ^ (t & 7)) << 4)) = lo;
+                    *reinterpret_cast<uint4*>(half + ((((c & 3) * 2 + 1) ^ (t & 7)) << 4)) = hi;
+                }
+                reinterpret_cast<float*>(smem + C::kScale16)[buf * kTok + t] = poisoned ? sv : sk;
                 if (t == 0) reinterpret_cast<float*>(smem + C::kR)[buf] = r_ref;
                 fence_async_proxy();
                 __syncwarp();
@@ -440,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
             {
                 constexpr int kWarpRows = kPair ? 32 : 16;  // the 8 warps share the rows
                 const int r0 = (warp - 8) * kWarpRows, c = lane & 15;
-#pragma unroll 4
+#pragma unroll 2
                 for (int r = r0 + (lane >> 4); r < r0 + kWarpRows; r += 2) {
                     uint4 v = make_uint4(0, 0, 0, 0);
                     if (r < s.nrows) {
@@ -488,52 +526,91 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
             const bool rows_here = row_in - lane < s.nrows;  // of this warp
             const int limit = it.len - it.nq + r / a.group + 1;                     // first position the row does not see
             const int all_see = it.len - it.nq + (r - lane) / a.group + 1;          // positions below it need no mask
-            float m = kNegInf, l = 0.0f, r_ref = 0x1p-100f;  // m: largest (q . k) s_k, not yet times qs
+            // The row's reference: the largest (q . k) s_k that moved it, not yet times qs, and what is subtracted
+            // from a score in the exponent. The weights carry 2^kLift.
+            constexpr float kLift = 6.0f;
+            float m = kNegInf, mq = 0.0f, l = 0.0f, r_ref = 0x1p-100f;
             const int first = kPair ? 0 : slot, step = kPair ? 1 : 2;
             const int last = slot < s.slots ? s.n : 0;
             int mine = 0;
             for (int i = first; i < last && ok; i += step, ++mine) {
                 const uint32_t n = seq + i, buf = n & 1;
-                if (!(ok = wait(s_full + 8 * slot, jobs_done & 1))) break;
                 if (!(ok = wait(v16_full + 8 * buf, (n >> 1) & 1))) break;
+                if (!(ok = wait(s_full + 8 * slot, jobs_done & 1))) break;
                 tc::fence_after_sync();
                 if (rows_here) {
-                    const float* ks = reinterpret_cast<const float*>(smem + C::kScale16 + buf * 2 * kTok * 4);
-                    const float* vs = ks + kTok;
+                    const uint32_t ks = base + C::kScale16 + buf * kTok * 4;
+                    const float r_new = reinterpret_cast<const float*>(smem + C::kR)[buf];
                     const int pos = (s.f0 + i) * kTok;
                     const bool edge = pos + kTok > all_see;
                     uint32_t v[kTok];
 #pragma unroll
                     for (int c = 0; c < kTok; c += 32)
                         tc::ld_32x32b_x32(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(v + c));
+                    // Key scales are requested 16 at a time, one step before their use: left to the compiler each load
+                    // waited for its own latency (173 us instead of XX for a 512-token chunk over 16384).
+                    float4 k4[2][4];
+                    auto request = [&](int step) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) k4[step & 1][j] = lds_v4(ks + step * 64 + j * 16);
+                    };
+                    request(0);
                     tc::wait_ld();
-                    float top = kNegInf;
+                    float top4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-                    for (int j = 0; j < kTok; j += 4) {
-                        const float4 k4 = *reinterpret_cast<const float4*>(ks + j);
-                        const float2 x0 = __fmul2_rn(pair_of(v, j), make_float2(k4.x, k4.y));
-                        const float2 x1 = __fmul2_rn(pair_of(v, j + 2), make_float2(k4.z, k4.w));
-                        v[j] = __float_as_uint(x0.x);
-                        v[j + 1] = __float_as_uint(x0.y);
-                        v[j + 2] = __float_as_uint(x1.x);
-                        v[j + 3] = __float_as_uint(x1.y);
+                    for (int step = 0; step < kTok / 16; ++step) {
+                        if (step + 1 < kTok / 16) request(step + 1);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int at = step * 16 + j * 4;
+                            const float4 k = k4[step & 1][j];
+                            const float2 x0 = __fmul2_rn(pair_of(v, at), make_float2(k.x, k.y));
+                            const float2 x1 = __fmul2_rn(pair_of(v, at + 2), make_float2(k.z, k.w));
+                            v[at] = __float_as_uint(x0.x);
+                            v[at + 1] = __float_as_uint(x0.y);
+                            v[at + 2] = __float_as_uint(x1.x);
+                            v[at + 3] = __float_as_uint(x1.y);
+                            if (!edge) top4[j] = fmaxf(fmaxf(top4[j], fmaxf(x0.x, x0.y)), fmaxf(x1.x, x1.y));
+                        }
                     }
-                    if (edge) {  // a masked score's weight is zero (p = 0, and see below)
+                    if (edge) {
+                        const int end = limit - pos;
 #pragma unroll
-                        for (int j = 0; j < kTok; ++j)
-                            if (pos + j >= limit) v[j] = 0xFF800000u;
+                        for (int j = 0; j < kTok; ++j) {
+                            if (j >= end) v[j] = 0xFF800000u;
+                            top4[j & 3] = fmaxf(top4[j & 3], __uint_as_float(v[j]));
+                        }
                     }
-#pragma unroll
-                    for (int j = 0; j < kTok; j += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
-                    const float r_new = reinterpret_cast<const float*>(smem + C::kR)[buf];
+                    const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
                     // The reference moves only when the maximum passes it by 2^8.
-                    const float m_new = (top - m) * qs > 8.0f ? top : m;
-                    const float mq = (m_new == kNegInf ? 0.0f : m_new) * qs;
-                    const float alpha = m_new == m ? 1.0f : ex2(fmaf(m, qs, -mq));
-                    const float beta = alpha * __fdividef(r_ref, r_new);
-                    m = m_new;
+                    float alpha = 1.0f;
+                    if ((top - m) * qs > 8.0f) {
+                        const float mq_new = fmaf(top, qs, -kLift);
+                        alpha = ex2(fmaf(m, qs, -kLift) - mq_new);
+                        m = top;
+                        mq = mq_new;
+                    }
+                    const float2 qs2 = make_float2(qs, qs), mq2 = make_float2(-mq, -mq);
+                    float2 sum = make_float2(0.0f, 0.0f), sum2 = sum;
+#pragma unroll
+                    for (int c = 0; c < kTok; c += 32) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float2 y0 = __ffma2_rn(pair_of(v, c + j), qs2, mq2), y1 = __ffma2_rn(pair_of(v, c + j + 2), qs2, mq2);
+                            const float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
+                            sum = __fadd2_rn(sum, p0);
+                            sum2 = __fadd2_rn(sum2, p1);
+                            const __half2 h0 = __floats2half2_rn(p0.x, p0.y), h1 = __floats2half2_rn(p1.x, p1.y);
+                            w[j >> 1] = *reinterpret_cast<const uint32_t*>(&h0);
+                            w[(j >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                        }
+                        st_16(t_s + c / 2, w);  // over the scores
+                    }
+                    sum = __fadd2_rn(sum, sum2);
+                    const float beta = r_new == r_ref ? alpha : alpha * __fdividef(r_ref, r_new);
                     r_ref = r_new;
-                    l *= alpha;
+                    l = fmaf(l, alpha, sum.x + sum.y);
                     if (mine > 0 && __any_sync(0xffffffffu, beta != 1.0f)) {
                         if (!(ok = wait(pv_done + 8 * slot, (jobs_done - 1) & 1))) break;
                         tc::fence_after_sync();
@@ -547,32 +624,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                             st_16(t_o + c, o);
                         }
                     }
-                    const float2 qs2 = make_float2(qs, qs), mq2 = make_float2(-mq, -mq);
-                    float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-                    for (int c = 0; c < kTok; c += 32) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = c; j < c + 32; j += 4) {
-                            const float4 v4 = *reinterpret_cast<const float4*>(vs + j);
-                            const float2 y0 = __ffma2_rn(pair_of(v, j), qs2, mq2), y1 = __ffma2_rn(pair_of(v, j + 2), qs2, mq2);
-                            const float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
-                            const float2 w0 = __fmul2_rn(p0, make_float2(v4.x, v4.y)), w1 = __fmul2_rn(p1, make_float2(v4.z, v4.w));
-                            sum = __fadd2_rn(sum, __fadd2_rn(p0, p1));
-                            const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
-                            w[(j - c) >> 1] = *reinterpret_cast<const uint32_t*>(&h0);
-                            w[((j - c) >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-                        }
-                        if (edge) {  // whatever the masked token's scale holds
-#pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                if (pos + c + j >= limit) w[j >> 1] = 0u;
-                                else if (pos + c + j + 1 >= limit) w[j >> 1] &= 0xFFFFu;
-                            }
-                        }
-                        st_16(t_s + (c >> 1), w);  // over the scores
-                    }
-                    l += sum.x + sum.y;
                     wait_st();
                 }
                 tc::fence_before_sync();
@@ -581,8 +632,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                 ++jobs_done;
             }
             if (!ok) break;
-            // The item's result: o = sum p s_v v / (2^6 / R) and, per row, its reference (log2) and sum of p.
-            float mx = m == kNegInf ? kNegInf : m * qs;
+            // The item's result: o = sum p s_v v / (2^6 / R) and, per row, its reference (log2) and sum of p, both with the
+            // weights' 2^kLift.
+            float mx = m == kNegInf ? kNegInf : mq;
             if (!kPair && slot == 1) {
                 ml[row_in] = make_float4(mx, l, r_ref, 0.0f);
                 __syncwarp();
