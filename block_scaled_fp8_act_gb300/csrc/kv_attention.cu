@@ -23,7 +23,7 @@
 //
 // Work split. A row tile is up to 192 rows of (new token, query head of one KV
 // head); a unit is one row tile x 32 cached tokens. The units of all
-// sequences, KV heads and row tiles form one list, which one CTA per SM shares
+// sequences, KV heads and row tiles form one list, which the SMs' CTAs share
 // evenly: no host knowledge of the lengths is needed and a ragged batch
 // balances itself. An item (sequence, head, row tile) counts kItemCost units
 // more than it has, about what its start and end cost, so that short ones
@@ -44,7 +44,7 @@ __device__ unsigned int g_attn_index_error;
 
 constexpr int kTile = 32;  // cached tokens per unit
 constexpr int kLeastUnits = 8;  // least share of a CTA
-constexpr int kItemCost = 12;   // units that an item counts beside its own
+constexpr int kItemCost = 20;   // units that an item counts beside its own
 using Work = Units<kTile, kItemCost>;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
@@ -94,9 +94,12 @@ __device__ __forceinline__ int order(int i) {
     return ((i >> 1) & 1) | ((i & 1) << 1) | (i & 4);
 }
 
-// kWR warps of a group split the row tile, kRW groups of 8 rows each; kG groups.
-template <int kD, int kWR, int kRW, int kG>
+// kWR warps of a group split the row tile, kRW groups of 8 rows each; kG groups in a CTA; kCtas CTAs per SM (two
+// where a group is one warp: one streams while the other starts or ends an item, 38 us instead of 46 for 34 ragged
+// sequences x 3 tokens).
+template <int kD, int kWR, int kRW, int kG, int kCtas_>
 struct Attn {
+    static constexpr int kCtas = kCtas_;
     static constexpr int kWarpRows = kRW * 8;
     static constexpr int kRows = kWR * kWarpRows;
     static constexpr int kWarps = kWR * kG;
@@ -106,7 +109,7 @@ struct Attn {
     static constexpr int kML = kQ + kRows * kD * 2;
     static constexpr int kQScale = kML + kG * kRows * 8;
     static constexpr int kRing = (kQScale + kRows * 4 + 127) / 128 * 128;
-    static constexpr int kFit = (226 * 1024 - kRing) / kG / kStageBytes;
+    static constexpr int kFit = (226 * 1024 / kCtas - 1024 * (kCtas - 1) - kRing) / kG / kStageBytes;
     static constexpr int kStages = kFit < 8 ? kFit : kFit < 16 && kG > 1 ? 8 : kFit < 16 ? kFit : 16;
     static constexpr int kRingBytes = kStages * kStageBytes;
     static constexpr int kOStride = kD + 4;  // floats of a row of a group's result, which replaces its ring at the end
@@ -126,9 +129,10 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int q0, int h, int 
     if (a.lse && lane == 0) a.lse[at] = sum == 0.0f ? kNegInf : (m + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <int kD, int kWR, int kRW, int kG>
-__global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG>::kThreads, 1) kv_attention_kernel(const __grid_constant__ AttnArgs a) {
-    using S = Attn<kD, kWR, kRW, kG>;
+template <int kD, int kWR, int kRW, int kG, int kCtas>
+__global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas)
+    kv_attention_kernel(const __grid_constant__ AttnArgs a) {
+    using S = Attn<kD, kWR, kRW, kG, kCtas>;
     constexpr int kRows = S::kRows, kStages = S::kStages;
     constexpr int kKS = kD / 32;  // pairs of k-steps of the score product
     constexpr int kDT = kD / 16;  // 16-row tiles of the transposed output
@@ -191,22 +195,42 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG>::kThreads, 1) kv_attent
                 const int64_t row_b =
                     ((static_cast<int64_t>(p1) * a.c.heads + it.h) << a.c.page_log2) + ((pos0 + 16) & in_page) - 16;
                 const int end_a = p0 >= 0 ? it.len - pos0 : 0, end_b = p1 >= 0 ? it.len - pos0 : 0;  // tokens there are
+                constexpr int kSteps = 32 / kStep;
+                const uint32_t scales = dst + 2 * kTile * kD + lane * 4;
+                if (min(end_a, end_b) >= kTile) {
+                    // A whole tile, almost always: addresses are a base per page and constant offsets.
+                    const int64_t at_a = (row_a + r0) * kD + c * 16, at_b = (row_b + r0) * kD + c * 16;
+                    const uint8_t *ka = a.c.k + at_a, *kb = a.c.k + at_b, *va = a.c.v + at_a, *vb = a.c.v + at_b;
 #pragma unroll
-                for (int j = 0; j < 32 / kStep; ++j) {
-                    if (kWR > 1 && j % kWR != wr) continue;
-                    const int row = j * kStep + r0;
-                    const bool first = j * kStep < 16;
-                    const bool in = row < (first ? end_a : end_b);
-                    const int64_t at = in ? ((first ? row_a : row_b) + row) * kD + c * 16 : 0;
-                    const uint32_t off = dst + stage_offset<kD>(row, c);
-                    cp_async16(off, a.c.k + at, in);
-                    cp_async16(off + kTile * kD, a.c.v + at, in);
-                }
-                if (wr == 0) {
-                    const bool in = lane < (lane < 16 ? end_a : end_b);
-                    const int64_t at = in ? (lane < 16 ? row_a : row_b) + lane : 0;
-                    cp_async4(dst + 2 * kTile * kD + lane * 4, a.c.k_scale + at, in);
-                    cp_async4(dst + 2 * kTile * kD + kTile * 4 + lane * 4, a.c.v_scale + at, in);
+                    for (int j = 0; j < kSteps; ++j) {
+                        if (kWR > 1 && j % kWR != wr) continue;
+                        const uint32_t off = dst + stage_offset<kD>(j * kStep + r0, c);
+                        cp_async16(off, (j * kStep < 16 ? ka : kb) + j * kStep * kD, true);
+                        cp_async16(off + kTile * kD, (j * kStep < 16 ? va : vb) + j * kStep * kD, true);
+                    }
+                    if (wr == 0) {
+                        const int64_t at = (lane < 16 ? row_a : row_b) + lane;
+                        cp_async4(scales, a.c.k_scale + at, true);
+                        cp_async4(scales + kTile * 4, a.c.v_scale + at, true);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int j = 0; j < kSteps; ++j) {
+                        if (kWR > 1 && j % kWR != wr) continue;
+                        const int row = j * kStep + r0;
+                        const bool first = j * kStep < 16;
+                        const bool in = row < (first ? end_a : end_b);
+                        const int64_t at = in ? ((first ? row_a : row_b) + row) * kD + c * 16 : 0;
+                        const uint32_t off = dst + stage_offset<kD>(row, c);
+                        cp_async16(off, a.c.k + at, in);
+                        cp_async16(off + kTile * kD, a.c.v + at, in);
+                    }
+                    if (wr == 0) {
+                        const bool in = lane < (lane < 16 ? end_a : end_b);
+                        const int64_t at = in ? (lane < 16 ? row_a : row_b) + lane : 0;
+                        cp_async4(scales, a.c.k_scale + at, in);
+                        cp_async4(scales + kTile * 4, a.c.v_scale + at, in);
+                    }
                 }
                 if (++asked == 16) {
                     asked = 0;
@@ -567,19 +591,20 @@ __global__ void __launch_bounds__(kJoinRows * 32) kv_attention_join_kernel(const
     write_row<kD>(a, static_cast<int>(s0.z), static_cast<int>(s0.w), static_cast<int>(s1.x) + r, lane, mm, sum, o);
 }
 
-template <int kD, int kWR, int kRW, int kG>
-cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t stream) {
-    using S = Attn<kD, kWR, kRW, kG>;
+template <int kD, int kWR, int kRW, int kG, int kCtas>
+cudaError_t launch_attention(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream) {
+    using S = Attn<kD, kWR, kRW, kG, kCtas>;
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
-    auto kernel = kv_attention_kernel<kD, kWR, kRW, kG>;
+    auto kernel = kv_attention_kernel<kD, kWR, kRW, kG, kCtas>;
     if (!configured[dev & 63].load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
         if (e != cudaSuccess) return e;
         configured[dev & 63].store(true, std::memory_order_relaxed);
     }
-    return launch_dependent(kernel, dim3(num_sms), S::kThreads, S::kBytes, stream, 1, a);
+    grid = kCtas * num_sms;
+    return launch_dependent(kernel, dim3(grid), S::kThreads, S::kBytes, stream, 1, a);
 }
 
 // Row tiles: the smallest that holds a sequence's rows, else the largest. The
@@ -602,48 +627,50 @@ int rows_of(int max_q_len, int group, int head_dim) {
     return 192;
 }
 
+// Launches the kernel for the row tile; `grid` is its CTAs.
 template <int kD>
-cudaError_t launch_rows(const AttnArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_rows(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream);
 
 template <>
-cudaError_t launch_rows<64>(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rows<64>(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream) {
     switch (a.rows) {
-        case 8: return launch_attention<64, 1, 1, 12>(a, num_sms, stream);
-        case 16: return launch_attention<64, 1, 2, 12>(a, num_sms, stream);
-        case 24: return launch_attention<64, 1, 3, 8>(a, num_sms, stream);
-        case 48: return launch_attention<64, 2, 3, 4>(a, num_sms, stream);
-        case 96: return launch_attention<64, 4, 3, 2>(a, num_sms, stream);
-        default: return launch_attention<64, 8, 3, 1>(a, num_sms, stream);
+        case 8: return launch_attention<64, 1, 1, 6, 2>(a, num_sms, grid, stream);
+        case 16: return launch_attention<64, 1, 2, 6, 2>(a, num_sms, grid, stream);
+        case 24: return launch_attention<64, 1, 3, 4, 2>(a, num_sms, grid, stream);
+        case 48: return launch_attention<64, 2, 3, 4, 1>(a, num_sms, grid, stream);
+        case 96: return launch_attention<64, 4, 3, 2, 1>(a, num_sms, grid, stream);
+        default: return launch_attention<64, 8, 3, 1, 1>(a, num_sms, grid, stream);
     }
 }
 
 template <>
-cudaError_t launch_rows<128>(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rows<128>(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream) {
     switch (a.rows) {
-        case 8: return launch_attention<128, 1, 1, 12>(a, num_sms, stream);
-        case 16: return launch_attention<128, 1, 2, 12>(a, num_sms, stream);
-        case 24: return launch_attention<128, 1, 3, 8>(a, num_sms, stream);
-        default: return launch_attention_tc(a, num_sms, stream);
+        case 8: return launch_attention<128, 1, 1, 6, 2>(a, num_sms, grid, stream);
+        case 16: return launch_attention<128, 1, 2, 6, 2>(a, num_sms, grid, stream);
+        case 24: return launch_attention<128, 1, 3, 4, 2>(a, num_sms, grid, stream);
+        default: grid = num_sms; return launch_attention_tc(a, num_sms, stream);
     }
 }
 
 template <>
-cudaError_t launch_rows<256>(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rows<256>(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream) {
     switch (a.rows) {
-        case 8: return launch_attention<256, 1, 1, 6>(a, num_sms, stream);
-        case 16: return launch_attention<256, 1, 2, 6>(a, num_sms, stream);
-        case 32: return launch_attention<256, 2, 2, 4>(a, num_sms, stream);
-        default: return launch_attention<256, 4, 2, 2>(a, num_sms, stream);
+        case 8: return launch_attention<256, 1, 1, 3, 2>(a, num_sms, grid, stream);
+        case 16: return launch_attention<256, 1, 2, 3, 2>(a, num_sms, grid, stream);
+        case 32: return launch_attention<256, 2, 2, 4, 1>(a, num_sms, grid, stream);
+        default: return launch_attention<256, 4, 2, 2, 1>(a, num_sms, grid, stream);
     }
 }
 
 template <int kD>
 cudaError_t launch_both(const AttnArgs& a, int num_sms, cudaStream_t stream) {
-    if (num_sms > kMaxAttnGrid) num_sms = kMaxAttnGrid;
-    const cudaError_t e = launch_rows<kD>(a, num_sms, stream);
+    if (num_sms > kMaxAttnGrid / 2) num_sms = kMaxAttnGrid / 2;
+    int grid = 0;
+    const cudaError_t e = launch_rows<kD>(a, num_sms, grid, stream);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kv_attention_join_kernel<kD>, dim3(num_sms, (a.rows + kJoinRows - 1) / kJoinRows),
-                            kJoinRows * 32, 0, stream, 1, a);
+    return launch_dependent(kv_attention_join_kernel<kD>, dim3(grid, (a.rows + kJoinRows - 1) / kJoinRows), kJoinRows * 32,
+                            0, stream, 1, a);
 }
 
 }  // namespace

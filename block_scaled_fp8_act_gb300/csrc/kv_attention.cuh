@@ -36,8 +36,8 @@ struct AttnArgs {
     unsigned int* index_error;
 };
 
-// CTAs of the main kernel (one per SM) that the workspace is made for.
-constexpr int kMaxAttnGrid = 160;
+// CTAs of the main kernel (two per SM at most) that the workspace is made for.
+constexpr int kMaxAttnGrid = 2 * 160;
 
 // Two E4M3 codes (the low or the high 16 bits of `codes`) to f16x2, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_lo_to_f16x2(uint32_t codes) {
