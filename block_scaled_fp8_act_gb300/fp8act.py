@@ -11,6 +11,8 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
+from functools import lru_cache
 from typing import NamedTuple
 
 import torch
@@ -295,6 +297,7 @@ def _cuda(t, dtypes, shape, name: str) -> int:
 
 
 _BF16, _F32, _I32, _I64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
+_LOGITS = _BF16 + _F32
 
 
 def _codes_out(M: int, K: int, q, sa, device):
@@ -359,15 +362,19 @@ def kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, devic
                    torch.ones(shape, device=device), torch.ones(shape, device=device))
 
 
-def _cache_struct(cache) -> KvCacheStruct:
+_pack_cache = struct.Struct("@PPPPiiii").pack  # fp8act_kv_cache, a third of the time of filling a KvCacheStruct
+
+
+def _cache_struct(cache) -> tuple[bytes, int, int]:
+    """Checks a cache; its fp8act_kv_cache as bytes, its heads and its head dimension."""
     k, v, ks, vs = cache
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("the cache's codes must be 4-D [pages, kv_heads, page_size, head_dim]")
     pages, heads, page, dim = shape = k.shape
     rows = (pages, heads, page)
-    return KvCacheStruct(_cuda(k, _CODES, shape, "cache.k"), _cuda(v, _CODES, shape, "cache.v"),
-                         _cuda(ks, _F32, rows, "cache.k_scale"), _cuda(vs, _F32, rows, "cache.v_scale"),
-                         pages, page, heads, dim)
+    return _pack_cache(_cuda(k, _CODES, shape, "cache.k"), _cuda(v, _CODES, shape, "cache.v"),
+                       _cuda(ks, _F32, rows, "cache.k_scale"), _cuda(vs, _F32, rows, "cache.v_scale"),
+                       pages, page, heads, dim), heads, dim
 
 
 def _heads(t, heads, dim: int, name: str) -> int:
@@ -385,13 +392,13 @@ def _heads(t, heads, dim: int, name: str) -> int:
 
 def fp8_kv_append(k, v, slots, cache, stream=None) -> None:
     """Quantise bf16 k, v [T, kv_heads, head_dim] into the cache's slots (int64 [T], negative = skip)."""
-    c = _cache_struct(cache)
-    ks, vs = _heads(k, c.kv_heads, c.head_dim, "k"), _heads(v, c.kv_heads, c.head_dim, "v")
+    c, heads, dim = _cache_struct(cache)
+    ks, vs = _heads(k, heads, dim, "k"), _heads(v, heads, dim, "v")
     T = k.shape[0]
     if v.shape[0] != T:
         raise ValueError("k and v have different numbers of tokens")
     _check("fp8_kv_append", load().fp8_kv_append(k.data_ptr(), v.data_ptr(), _cuda(slots, _I64, (T,), "slots"), T, ks,
-                                                 vs, ctypes.byref(c), _stream(stream)))
+                                                 vs, c, _stream(stream)))
 
 
 _workspaces: dict = {}
@@ -399,17 +406,24 @@ _workspaces: dict = {}
 
 def _workspace(nbytes: int, device, stream: int) -> torch.Tensor:
     """A workspace kept per device and stream (calls of one stream share it)."""
-    if torch._C._cuda_isCurrentStreamCapturing():
+    if stream and torch.cuda.is_current_stream_capturing():  # (the default stream cannot be captured)
         return torch.empty(nbytes, dtype=torch.uint8, device=device)  # belongs to the graph
     w = _workspaces.get((device, stream))
     if w is None or w.numel() < nbytes:
-        w = _workspaces[(device, stream)] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        w = _workspaces[(device, stream)] = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
     return w
+
+
+@lru_cache(maxsize=None)
+def _attention_bytes(max_q_len: int, q_heads: int, kv_heads: int, dim: int) -> int:
+    c = KvCacheStruct(None, None, None, None, 0, 16, kv_heads, dim)
+    return int(load().fp8_kv_attention_workspace(max_q_len, q_heads, ctypes.byref(c)))
 
 
 def kv_attention_workspace(max_q_len: int, q_heads: int, cache) -> int:
     """Bytes of workspace fp8_kv_attention needs."""
-    return int(load().fp8_kv_attention_workspace(max_q_len, q_heads, ctypes.byref(_cache_struct(cache))))
+    _, heads, dim = _cache_struct(cache)
+    return _attention_bytes(max_q_len, q_heads, heads, dim)
 
 
 def fp8_kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len: int | None = None,
@@ -421,30 +435,29 @@ def fp8_kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len: int | None 
     picks the row tile; softmax_scale defaults to head_dim ** -0.5. `lse` (fp32 [tokens, q_heads])
     is filled if given. `workspace`: a uint8 tensor of kv_attention_workspace() bytes, kept by the
     caller per stream; without one the binding keeps its own per device and stream."""
-    c = _cache_struct(cache)
-    qs = _heads(q, None, c.head_dim, "q")
-    T, Hq, D = q.shape
+    c, heads, D = _cache_struct(cache)
+    qs = _heads(q, None, D, "q")
+    T, Hq, _ = shape = q.shape
     if page_table.dim() != 2:
         raise ValueError("page_table must be 2-D [B, max_pages]")
-    B, max_pages = page_table.shape
+    B, max_pages = tshape = page_table.shape
     if max_q_len is None:
         max_q_len = 1 if T == B else T
     out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
-    st, L = _stream(stream), load()
-    need = L.fp8_kv_attention_workspace(max_q_len, Hq, ctypes.byref(c))
+    st = _stream(stream)
     if workspace is None:
-        workspace = _workspace(max(need, 16), q.device, st)
+        workspace = _workspace(_attention_bytes(max_q_len, Hq, heads, D), q.device, st)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
-    _check("fp8_kv_attention", L.fp8_kv_attention(
+    _check("fp8_kv_attention", load().fp8_kv_attention(
         q.data_ptr(), qs, _cuda(cu_q, _I32, (B + 1,), "cu_q"), _cuda(kv_lens, _I32, (B,), "kv_lens"),
-        _cuda(page_table, _I32, (B, max_pages), "page_table"), max_pages, B, T, max_q_len, Hq,
-        D ** -0.5 if softmax_scale is None else softmax_scale, ctypes.byref(c), _cuda(out, _BF16, (T, Hq, D), "out"),
-        None if lse is None else _cuda(lse, _F32, (T, Hq), "lse"), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), st))
+        _cuda(page_table, _I32, tshape, "page_table"), max_pages, B, T, max_q_len, Hq,
+        D ** -0.5 if softmax_scale is None else softmax_scale, c, _cuda(out, _BF16, shape, "out"),
+        None if lse is None else _cuda(lse, _F32, (T, Hq), "lse"), workspace.data_ptr(), workspace.nbytes, st))
     return out
 
 
+@lru_cache(maxsize=None)
 def verify_drafts_workspace(B: int, k: int) -> int:
     """Bytes of workspace verify_drafts needs."""
     return int(load().fp8act_verify_drafts_workspace(B, k))
@@ -461,26 +474,25 @@ def verify_drafts(target_logits, draft_tokens, uniform, noise, temperature, draf
     keeps its own per device and stream."""
     if target_logits.dim() != 3:
         raise ValueError("target_logits must be [B, k + 1, V]")
-    B, rows, V = target_logits.shape
+    B, rows, V = shape = target_logits.shape
     k, kind, dev = rows - 1, (target_logits.dtype,), target_logits.device
     accepted = torch.empty(B, dtype=torch.int32, device=dev) if accepted is None else accepted
     tokens = torch.empty((B, rows), dtype=torch.int32, device=dev) if tokens is None else tokens
     accept_prob = torch.empty((B, k), dtype=torch.float32, device=dev) if accept_prob is None else accept_prob
-    L, st = load(), _stream(stream)
+    st = _stream(stream)
     if workspace is None:
-        workspace = _workspace(L.fp8act_verify_drafts_workspace(B, k), dev, st)
+        workspace = _workspace(verify_drafts_workspace(B, k), dev, st)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
-    _check("fp8act_verify_drafts", L.fp8act_verify_drafts(
-        _cuda(target_logits, _BF16 + _F32, (B, rows, V), "target_logits"),
+    bk = (B, k)
+    _check("fp8act_verify_drafts", load().fp8act_verify_drafts(
+        _cuda(target_logits, _LOGITS, shape, "target_logits"),
         None if draft_logits is None else _cuda(draft_logits, kind, (B, k, V), "draft_logits"),
-        int(kind[0] == torch.float32), _cuda(draft_tokens, _I32, (B, k), "draft_tokens"),
-        _cuda(uniform, _F32, (B, k), "uniform"), _cuda(noise, _F32, (B, V), "noise"),
-        _cuda(temperature, _F32, (B,), "temperature"),
+        kind == _F32, _cuda(draft_tokens, _I32, bk, "draft_tokens"), _cuda(uniform, _F32, bk, "uniform"),
+        _cuda(noise, _F32, (B, V), "noise"), _cuda(temperature, _F32, (B,), "temperature"),
         None if n_draft is None else _cuda(n_draft, _I32, (B,), "n_draft"), B, k, V,
         _cuda(accepted, _I32, (B,), "accepted"), _cuda(tokens, _I32, (B, rows), "tokens"),
-        _cuda(accept_prob, _F32, (B, k), "accept_prob"), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), st))
+        _cuda(accept_prob, _F32, bk, "accept_prob"), workspace.data_ptr(), workspace.nbytes, st))
     return accepted, tokens, accept_prob
 
 
