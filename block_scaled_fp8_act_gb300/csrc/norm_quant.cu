@@ -137,7 +137,9 @@ cudaError_t launch_rmsnorm_quant(const void* x, const void* residual, const void
                                  float weight_offset, int M, int K, void* q, float* sa, void* residual_out,
                                  int num_sms, cudaStream_t stream) {
     const int chunks = K / 8;
-    if (chunks <= 1024 && M <= 2 * num_sms)
+    // One chunk per thread wherever a CTA holds the row: 4096 x 5120 with residual takes 27.4 us, with 2 or 4 chunks
+    // per thread 28.9 or 32.5.
+    if (chunks <= 1024)
         return launch_norm<1>(x, residual, weight, eps, weight_offset, M, chunks, q, sa, residual_out, stream);
     return launch_norm<4>(x, residual, weight, eps, weight_offset, M, chunks, q, sa, residual_out, stream);
 }

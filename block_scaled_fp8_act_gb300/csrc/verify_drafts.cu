@@ -14,8 +14,7 @@
 // The second, dependent, has a thread-block cluster per sequence: its CTAs
 // join the parts and decide the acceptance alike, then share the vocabulary of
 // the one row (or pair) drawn from, by then in L2, and meet through
-// distributed shared memory for the draw. While it waits for the first it
-// prefetches the noise. (One launch with a cluster of 16 per sequence for
+// distributed shared memory for the draw. (One launch with a cluster of 16 per sequence for
 // both took 20.5 us for 7 drafts at one sequence, where 16 SMs read 4.6 MB,
 // and 53 us for 34 x 2 drafts.)
 #include <atomic>
@@ -146,13 +145,19 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const Verify
         if (o.m > kNegInf) join(st, o, q.c);
     };
     if (share == 0 && static_cast<int>(threadIdx.x) < head) one(threadIdx.x);
-    // kAhead vectors are requested before the first is used.
+    // kAhead vectors are in flight while kAhead are used.
     constexpr int kAhead = 4;
-    for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kStatThreads * kAhead) {
-        uint4 raw[kAhead];
+    uint4 raw[kAhead];
+    auto request = [&](int v, uint4 (&to)[kAhead]) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            if (v + kStatThreads * u < v1) raw[u] = row.raw(head + (v + kStatThreads * u) * R::kPer);
+            if (v + kStatThreads * u < v1) to[u] = row.raw(head + (v + kStatThreads * u) * R::kPer);
+    };
+    const int first = v0 + static_cast<int>(threadIdx.x);
+    request(first, raw);
+    for (int v = first; v < v1; v += kStatThreads * kAhead) {
+        uint4 next[kAhead];
+        request(v + kStatThreads * kAhead, next);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (v + kStatThreads * u >= v1) break;
@@ -176,6 +181,8 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const Verify
 #pragma unroll
             for (int j = 0; j < R::kPer; ++j) st.s += ex2((f[j] - m) * q.c);
         }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) raw[u] = next[u];
     }
     if (share == shares - 1 && tail + static_cast<int>(threadIdx.x) < p.V) one(tail + threadIdx.x);
 #pragma unroll
@@ -212,7 +219,7 @@ __device__ __forceinline__ Best ld_cluster_best(const Best* p, uint32_t rank) {
 }
 
 template <bool kF32>
-__global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyProblem p, const Stat* parts, int cluster,
+__global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyProblem p, const Stat* parts, int cluster,
                                                                int shares) {
     using R = Row<kF32>;
     __shared__ VerifyShared sh;
@@ -226,7 +233,6 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyProbl
     const int i0 = static_cast<int>(static_cast<int64_t>(V) * rank / cluster);
     const int i1 = static_cast<int>(static_cast<int64_t>(V) * (rank + 1) / cluster);
     ptx::griddep_launch_dependents();
-    for (int i = i0 + static_cast<int>(threadIdx.x) * 32; i < i1; i += kThreads * 32) prefetch_l2(noise + i);
     ptx::griddep_wait();
     q.read_temperature(p, b);
     const float c = q.c;
@@ -323,32 +329,41 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyProbl
                     else if (i == skip)
                         w = 0.0f;
                 }
-                if (w > 0.0f) better(best, __fdiv_rn(w, e), i);
+                if (w > 0.0f) better(best, __fdividef(w, e), i);
             };
             if (V % 8 == 0) {  // every row starts on a 16-byte boundary
                 const int n8 = V / 8;
                 const int v0 = static_cast<int>(static_cast<int64_t>(n8) * rank / cluster);
                 const int v1 = static_cast<int>(static_cast<int64_t>(n8) * (rank + 1) / cluster);
-                for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kThreads) {
-                    const int i = v * 8;
-                    const uint4 n0 = ld_dep_v4(noise + i), n1 = ld_dep_v4(noise + i + 4);
-                    uint4 t[8 / R::kPer], d[8 / R::kPer];
+                struct Loaded {
+                    uint4 n[2], t[8 / R::kPer], d[8 / R::kPer];
+                };
+                auto request = [&](int v, Loaded& to) {
+                    if (v >= v1) return;
+                    to.n[0] = ld_dep_v4(noise + v * 8);
+                    to.n[1] = ld_dep_v4(noise + v * 8 + 4);
 #pragma unroll
                     for (int u = 0; u < 8 / R::kPer; ++u) {
-                        t[u] = row.raw(i + u * R::kPer);
-                        d[u] = other.raw(i + u * R::kPer);
+                        to.t[u] = row.raw(v * 8 + u * R::kPer);
+                        to.d[u] = other.raw(v * 8 + u * R::kPer);
                     }
-                    const float e[8] = {__uint_as_float(n0.x), __uint_as_float(n0.y), __uint_as_float(n0.z),
-                                        __uint_as_float(n0.w), __uint_as_float(n1.x), __uint_as_float(n1.y),
-                                        __uint_as_float(n1.z), __uint_as_float(n1.w)};
+                };
+                Loaded now, next;
+                request(v0 + static_cast<int>(threadIdx.x), now);
+                for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kThreads) {
+                    request(v + kThreads, next);
+                    const float e[8] = {__uint_as_float(now.n[0].x), __uint_as_float(now.n[0].y), __uint_as_float(now.n[0].z),
+                                        __uint_as_float(now.n[0].w), __uint_as_float(now.n[1].x), __uint_as_float(now.n[1].y),
+                                        __uint_as_float(now.n[1].z), __uint_as_float(now.n[1].w)};
 #pragma unroll
                     for (int u = 0; u < 8 / R::kPer; ++u) {
                         float ft[R::kPer], fd[R::kPer];
-                        R::widen(t[u], ft);
-                        R::widen(d[u], fd);
+                        R::widen(now.t[u], ft);
+                        R::widen(now.d[u], fd);
 #pragma unroll
-                        for (int j = 0; j < R::kPer; ++j) consider(ft[j], fd[j], e[u * R::kPer + j], i + u * R::kPer + j);
+                        for (int j = 0; j < R::kPer; ++j) consider(ft[j], fd[j], e[u * R::kPer + j], v * 8 + u * R::kPer + j);
                     }
+                    now = next;
                 }
             } else {
                 constexpr int kAhead = 4;

@@ -476,15 +476,15 @@ def verify_drafts(target_logits, draft_tokens, uniform, noise, temperature, draf
         raise ValueError("target_logits must be [B, k + 1, V]")
     B, rows, V = shape = target_logits.shape
     k, kind, dev = rows - 1, (target_logits.dtype,), target_logits.device
+    bk = (B, k)
     accepted = torch.empty(B, dtype=torch.int32, device=dev) if accepted is None else accepted
     tokens = torch.empty((B, rows), dtype=torch.int32, device=dev) if tokens is None else tokens
-    accept_prob = torch.empty((B, k), dtype=torch.float32, device=dev) if accept_prob is None else accept_prob
+    accept_prob = torch.empty(bk, dtype=torch.float32, device=dev) if accept_prob is None else accept_prob
     st = _stream(stream)
     if workspace is None:
         workspace = _workspace(verify_drafts_workspace(B, k), dev, st)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
-    bk = (B, k)
     _check("fp8act_verify_drafts", load().fp8act_verify_drafts(
         _cuda(target_logits, _LOGITS, shape, "target_logits"),
         None if draft_logits is None else _cuda(draft_logits, kind, (B, k, V), "draft_logits"),
