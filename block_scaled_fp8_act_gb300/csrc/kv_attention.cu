@@ -612,7 +612,7 @@ cudaError_t launch_attention(const AttnArgs& a, int num_sms, int& grid, cudaStre
 // 12), and a warp needs 32 accumulators for every 8 rows x 128 columns. From
 // kWideRows rows on, head size 128 takes the tcgen05 kernel's row tiles of any
 // multiple of 8 up to 128, or 256.
-constexpr int kWideRows = 25;
+constexpr int kWideRows = 49;
 int rows_of(int max_q_len, int group, int head_dim) {
     const int64_t rows = static_cast<int64_t>(max_q_len) * group;
     if (head_dim == 128 && rows >= kWideRows) return rows > 128 ? 256 : static_cast<int>((rows + 7) / 8 * 8);
@@ -649,6 +649,7 @@ cudaError_t launch_rows<128>(const AttnArgs& a, int num_sms, int& grid, cudaStre
         case 8: return launch_attention<128, 1, 1, 6, 2>(a, num_sms, grid, stream);
         case 16: return launch_attention<128, 1, 2, 6, 2>(a, num_sms, grid, stream);
         case 24: return launch_attention<128, 1, 3, 4, 2>(a, num_sms, grid, stream);
+        case 48: return launch_attention<128, 2, 3, 4, 1>(a, num_sms, grid, stream);
         default: grid = num_sms; return launch_attention_tc(a, num_sms, stream);
     }
 }

@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                     now = ahead;
                     ahead = look_up(s.f0 + i + 4);
                 }
-                const uint32_t stage = n % stages, round = n / stages, bar = full + 8 * stage;
+                const uint32_t round = values ? n / C::kVStages : n / C::kKStages;  // (constant divisors)
+                const uint32_t stage = n - round * stages, bar = full + 8 * stage;
                 if (round > 0 && !(ok = wait(empty + 8 * stage, (round - 1) & 1))) break;
                 const int pos = (s.f0 + i) * kTok;
                 // Lane j < 128 / box: copy j of the tile, if it holds a token.
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
             const int depth = s.slots;                            // score tiles in flight
             const int jobs = kPair ? s.n * s.slots : s.n;
             auto slot_of = [&](int j) { return depth == 2 ? j & 1 : 0; };
-            auto tile_of = [&](int j) { return kPair ? j / s.slots : j; };
+            auto tile_of = [&](int j) { return kPair ? j >> (depth - 1) : j; };  // (depth is 1 or 2)
             auto first_use = [&](int j) { return !kPair || slot_of(j) == 0; };
             auto last_use = [&](int j) { return !kPair || slot_of(j) == s.slots - 1; };
             auto keys = [&](int j) {  // wait for the keys of score tile j
