@@ -2,8 +2,10 @@
 
 Each .cu file under csrc/ compiles to an object in parallel, then nvcc links
 the shared library against the shared CUDA runtime (the same libcudart.so.13
-PyTorch loads). No CMake; a rebuild happens only when a source is newer than
-the library.
+PyTorch loads). csrc/binding.cpp, the Python binding of the operators between
+the linear layers, compiles with the host compiler against PyTorch's headers
+into an extension module beside it, linked to the library. No CMake; a rebuild
+happens only when a source is newer than the libraries.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libfp8act.so")
 INCLUDE = os.path.join(ROOT, "include")
+BINDING = os.path.join(CSRC, "binding.cpp")
+EXT_PATH = os.path.join(BUILD_DIR, "_fp8act.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -37,19 +42,19 @@ def sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return sources() + [BINDING] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(EXT_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(EXT_PATH))
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every CUDA source and link libfp8act.so; returns its path."""
+    """Compile every CUDA source and link libfp8act.so, and the binding; returns the library's path."""
     if not force and not _stale():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -66,8 +71,27 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(r.stderr, end="")
         return obj
 
+    import torch
+
+    torch_dir = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(cc))
+    binding_obj = os.path.join(BUILD_DIR, "binding.cpp.o")
+
+    def run(cmd: list[str], what: str) -> None:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{what} failed:\n{r.stderr}")
+
+    def compile_binding() -> None:
+        run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             "-I", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"],
+             "-I", os.path.join(cuda, "include"), "-c", BINDING, "-o", binding_obj], f"g++ on {BINDING}")
+
     with ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, sources()))
+        binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-cudart", "shared", *objs, "-o", tmp,
            "-Xlinker", "-rpath", "-Xlinker", "/usr/local/cuda/lib64"]
@@ -75,6 +99,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    tmp = EXT_PATH + f".tmp{os.getpid()}"
+    torch_lib, cuda_lib = os.path.join(torch_dir, "lib"), os.path.join(cuda, "lib64")
+    run(["g++", "-shared", binding_obj, "-o", tmp, "-L", BUILD_DIR, "-l:libfp8act.so", "-L", torch_lib, "-ltorch_python",
+         "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", cuda_lib, "-lcudart",
+         f"-Wl,-rpath,$ORIGIN,-rpath,{torch_lib},-rpath,{cuda_lib}"], "linking the binding")
+    os.replace(tmp, EXT_PATH)
     return LIB_PATH
 
 

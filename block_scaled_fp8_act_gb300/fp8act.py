@@ -1,4 +1,9 @@
-"""ctypes binding of libfp8act.so (argument marshalling only).
+"""Binding of libfp8act.so (argument marshalling only).
+
+The linear layer's functions go through ctypes, the operators between the
+layers (fp8_rmsnorm_quant .. verify_drafts) through an extension module that
+does the same in C++ (csrc/binding.cpp), since a decode step's calls of them
+are shorter on the device than their argument checks are in Python.
 
 Each function takes CUDA torch tensors, checks dtype / device / contiguity,
 passes raw device pointers, sizes and the current CUDA stream to the C entry
@@ -9,10 +14,10 @@ no fallback: if the library is not built, loading it raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
-import struct
-from functools import lru_cache
 from typing import NamedTuple
 
 import torch
@@ -21,6 +26,7 @@ from . import build as _build
 
 G = 128
 _lib = None
+_ext = None
 
 STATUS = {0: "FP8ACT_OK", 1: "FP8ACT_ERR_NULL", 2: "FP8ACT_ERR_SHAPE", 3: "FP8ACT_ERR_ALIGN",
           4: "FP8ACT_ERR_LAUNCH", 5: "FP8ACT_ERR_TIMEOUT", 6: "FP8ACT_ERR_DEVICE", 7: "FP8ACT_ERR_CUDA",
@@ -88,6 +94,25 @@ def load(build: bool = False) -> ctypes.CDLL:
         fn.restype = ctypes.c_int
     _lib = L
     return L
+
+
+def _raise(fn: str, status: int) -> None:
+    raise Fp8ActError(fn, status, strerror(status))
+
+
+def _native():
+    """The extension module of the operators between the linear layers."""
+    global _ext
+    if _ext is None:
+        load()
+        if not os.path.exists(_build.EXT_PATH):
+            raise RuntimeError(f"the binding is not built ({_build.EXT_PATH}); run block_scaled_fp8_act_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_fp8act", _build.EXT_PATH)
+        ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fp8act", loader))
+        loader.exec_module(ext)
+        ext.set_error(_raise)
+        _ext = ext
+    return _ext
 
 
 def strerror(status: int) -> str:
@@ -287,56 +312,18 @@ def fp8_block_gemm_grouped_f32(problems, outs=None, stream=None) -> list:
     return _gemm_grouped("fp8_block_gemm_grouped_f32", torch.float32, problems, outs, stream)
 
 
-def _cuda(t, dtypes, shape, name: str) -> int:
-    """Checks a contiguous CUDA tensor of a known shape; its address."""
-    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_cuda:
-        if t.shape == shape and t.is_contiguous():
-            return t.data_ptr()
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise TypeError(f"{name} must be a CUDA tensor with dtype in {dtypes}")
-
-
-_BF16, _F32, _I32, _I64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
-_LOGITS = _BF16 + _F32
-
-
-def _codes_out(M: int, K: int, q, sa, device):
-    q = torch.empty((M, K), dtype=torch.uint8, device=device) if q is None else q
-    sa = torch.empty((M, K // G), dtype=torch.float32, device=device) if sa is None else sa
-    return q, sa, _cuda(q, _CODES, (M, K), "q"), _cuda(sa, _F32, (M, K // G), "sa")
-
-
 def fp8_rmsnorm_quant(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0, q=None, sa=None,
                       residual_out=None, stream=None):
     """RMS norm of x (+ residual) with E4M3 codes out, bf16 x, residual [M, K], weight [K].
 
     Returns (q, sa), or (q, sa, residual_out) with a residual; residual_out = bf16(x + residual)
     may be x or residual. The weight applied is weight + weight_offset."""
-    _cuda2d(x, _BF16, "x")
-    M, K = x.shape
-    wp = _cuda(weight, _BF16, (K,), "weight")
-    q, sa, qp, sp = _codes_out(M, K, q, sa, x.device)
-    rp = op = None
-    if residual is not None:
-        rp = _cuda(residual, _BF16, (M, K), "residual")
-        residual_out = torch.empty_like(x) if residual_out is None else residual_out
-        op = _cuda(residual_out, _BF16, (M, K), "residual_out")
-    elif residual_out is not None:
-        raise ValueError("residual_out without a residual")
-    _check("fp8_rmsnorm_quant", load().fp8_rmsnorm_quant(x.data_ptr(), rp, wp, eps, weight_offset, M, K, qp, sp, op,
-                                                         _stream(stream)))
-    return (q, sa) if residual is None else (q, sa, residual_out)
+    return _native().rmsnorm_quant(x, weight, residual, eps, weight_offset, q, sa, residual_out, stream)
 
 
 def fp8_silu_mul_quant(gate_up, q=None, sa=None, stream=None):
     """silu(gate) * up of bf16 rows [gate | up] ([M, 2 I]) -> (q E4M3 codes [M, I], sa fp32 [M, I/128])."""
-    _cuda2d(gate_up, _BF16, "gate_up")
-    M, width = gate_up.shape
-    if width % 2:
-        raise ValueError("gate_up must have an even number of columns")
-    q, sa, qp, sp = _codes_out(M, width // 2, q, sa, gate_up.device)
-    _check("fp8_silu_mul_quant", load().fp8_silu_mul_quant(gate_up.data_ptr(), M, width // 2, qp, sp, _stream(stream)))
-    return q, sa
+    return _native().silu_mul_quant(gate_up, q, sa, stream)
 
 
 class KvCache(NamedTuple):
@@ -362,68 +349,16 @@ def kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, devic
                    torch.ones(shape, device=device), torch.ones(shape, device=device))
 
 
-_pack_cache = struct.Struct("@PPPPiiii").pack  # fp8act_kv_cache, a third of the time of filling a KvCacheStruct
-
-
-def _cache_struct(cache) -> tuple[bytes, int, int]:
-    """Checks a cache; its fp8act_kv_cache as bytes, its heads and its head dimension."""
-    k, v, ks, vs = cache
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise ValueError("the cache's codes must be 4-D [pages, kv_heads, page_size, head_dim]")
-    pages, heads, page, dim = shape = k.shape
-    rows = (pages, heads, page)
-    return _pack_cache(_cuda(k, _CODES, shape, "cache.k"), _cuda(v, _CODES, shape, "cache.v"),
-                       _cuda(ks, _F32, rows, "cache.k_scale"), _cuda(vs, _F32, rows, "cache.v_scale"),
-                       pages, page, heads, dim), heads, dim
-
-
-def _heads(t, heads, dim: int, name: str) -> int:
-    """Checks a bf16 [tokens, heads, dim] tensor whose tokens may be apart (columns of wider rows); its token stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
-        raise TypeError(f"{name} must be a bf16 CUDA tensor")
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name} must be [tokens, heads, {dim}], got {tuple(shape)}")
-    token, head, one = t.stride()
-    if one != 1 or (head != dim and shape[1] > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return token if shape[0] > 1 else max(token, shape[1] * dim)
-
-
 def fp8_kv_append(k, v, slots, cache, stream=None) -> None:
     """Quantise bf16 k, v [T, kv_heads, head_dim] into the cache's slots (int64 [T], negative = skip)."""
-    c, heads, dim = _cache_struct(cache)
-    ks, vs = _heads(k, heads, dim, "k"), _heads(v, heads, dim, "v")
-    T = k.shape[0]
-    if v.shape[0] != T:
-        raise ValueError("k and v have different numbers of tokens")
-    _check("fp8_kv_append", load().fp8_kv_append(k.data_ptr(), v.data_ptr(), _cuda(slots, _I64, (T,), "slots"), T, ks,
-                                                 vs, c, _stream(stream)))
-
-
-_workspaces: dict = {}
-
-
-def _workspace(nbytes: int, device, stream: int) -> torch.Tensor:
-    """A workspace kept per device and stream (calls of one stream share it)."""
-    if stream and torch.cuda.is_current_stream_capturing():  # (the default stream cannot be captured)
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)  # belongs to the graph
-    w = _workspaces.get((device, stream))
-    if w is None or w.numel() < nbytes:
-        w = _workspaces[(device, stream)] = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    return w
-
-
-@lru_cache(maxsize=None)
-def _attention_bytes(max_q_len: int, q_heads: int, kv_heads: int, dim: int) -> int:
-    c = KvCacheStruct(None, None, None, None, 0, 16, kv_heads, dim)
-    return int(load().fp8_kv_attention_workspace(max_q_len, q_heads, ctypes.byref(c)))
+    _native().kv_append(k, v, slots, cache, stream)
 
 
 def kv_attention_workspace(max_q_len: int, q_heads: int, cache) -> int:
     """Bytes of workspace fp8_kv_attention needs."""
-    _, heads, dim = _cache_struct(cache)
-    return _attention_bytes(max_q_len, q_heads, heads, dim)
+    pages, heads, page, dim = cache[0].shape
+    c = KvCacheStruct(None, None, None, None, 0, page, heads, dim)
+    return int(load().fp8_kv_attention_workspace(max_q_len, q_heads, ctypes.byref(c)))
 
 
 def fp8_kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len: int | None = None,
@@ -435,29 +370,10 @@ def fp8_kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len: int | None 
     picks the row tile; softmax_scale defaults to head_dim ** -0.5. `lse` (fp32 [tokens, q_heads])
     is filled if given. `workspace`: a uint8 tensor of kv_attention_workspace() bytes, kept by the
     caller per stream; without one the binding keeps its own per device and stream."""
-    c, heads, D = _cache_struct(cache)
-    qs = _heads(q, None, D, "q")
-    T, Hq, _ = shape = q.shape
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be 2-D [B, max_pages]")
-    B, max_pages = tshape = page_table.shape
-    if max_q_len is None:
-        max_q_len = 1 if T == B else T
-    out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
-    st = _stream(stream)
-    if workspace is None:
-        workspace = _workspace(_attention_bytes(max_q_len, Hq, heads, D), q.device, st)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous CUDA tensor")
-    _check("fp8_kv_attention", load().fp8_kv_attention(
-        q.data_ptr(), qs, _cuda(cu_q, _I32, (B + 1,), "cu_q"), _cuda(kv_lens, _I32, (B,), "kv_lens"),
-        _cuda(page_table, _I32, tshape, "page_table"), max_pages, B, T, max_q_len, Hq,
-        D ** -0.5 if softmax_scale is None else softmax_scale, c, _cuda(out, _BF16, shape, "out"),
-        None if lse is None else _cuda(lse, _F32, (T, Hq), "lse"), workspace.data_ptr(), workspace.nbytes, st))
-    return out
+    return _native().kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, out, lse, workspace,
+                                  stream)
 
 
-@lru_cache(maxsize=None)
 def verify_drafts_workspace(B: int, k: int) -> int:
     """Bytes of workspace verify_drafts needs."""
     return int(load().fp8act_verify_drafts_workspace(B, k))
@@ -472,28 +388,8 @@ def verify_drafts(target_logits, draft_tokens, uniform, noise, temperature, draf
     temperature fp32 [B] (0 = greedy), n_draft int32 [B] (None: k each). `workspace`: a uint8 tensor
     of verify_drafts_workspace() bytes, kept by the caller per stream; without one the binding
     keeps its own per device and stream."""
-    if target_logits.dim() != 3:
-        raise ValueError("target_logits must be [B, k + 1, V]")
-    B, rows, V = shape = target_logits.shape
-    k, kind, dev = rows - 1, (target_logits.dtype,), target_logits.device
-    bk = (B, k)
-    accepted = torch.empty(B, dtype=torch.int32, device=dev) if accepted is None else accepted
-    tokens = torch.empty((B, rows), dtype=torch.int32, device=dev) if tokens is None else tokens
-    accept_prob = torch.empty(bk, dtype=torch.float32, device=dev) if accept_prob is None else accept_prob
-    st = _stream(stream)
-    if workspace is None:
-        workspace = _workspace(verify_drafts_workspace(B, k), dev, st)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous CUDA tensor")
-    _check("fp8act_verify_drafts", load().fp8act_verify_drafts(
-        _cuda(target_logits, _LOGITS, shape, "target_logits"),
-        None if draft_logits is None else _cuda(draft_logits, kind, (B, k, V), "draft_logits"),
-        kind == _F32, _cuda(draft_tokens, _I32, bk, "draft_tokens"), _cuda(uniform, _F32, bk, "uniform"),
-        _cuda(noise, _F32, (B, V), "noise"), _cuda(temperature, _F32, (B,), "temperature"),
-        None if n_draft is None else _cuda(n_draft, _I32, (B,), "n_draft"), B, k, V,
-        _cuda(accepted, _I32, (B,), "accepted"), _cuda(tokens, _I32, (B, rows), "tokens"),
-        _cuda(accept_prob, _F32, bk, "accept_prob"), workspace.data_ptr(), workspace.nbytes, st))
-    return accepted, tokens, accept_prob
+    return _native().verify_drafts(target_logits, draft_tokens, uniform, noise, temperature, draft_logits, n_draft,
+                                   accepted, tokens, accept_prob, workspace, stream)
 
 
 def check_status(stream=None) -> int:
