@@ -276,8 +276,9 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
         __syncthreads();
 
         float acc[kDT][kRW][4];
-        // m: largest (q . k) s_k of rows 2q, 2q + 1 of each 8, not yet times qs
-        float m[kRW][2], l[kRW][2], qs[kRW][2], r_ref = 0x1p-100f;
+        // mq: the reference of rows 2q, 2q + 1 of each 8 in log2, -inf before the first score; l: sum of p
+        constexpr float kSlack = 8.0f;
+        float mq[kRW][2], l[kRW][2], qs[kRW][2], r_ref = 0x1p-100f;
         int limit[kRW][2];  // first position that the row does not see
 #pragma unroll
         for (int i = 0; i < kRW; ++i) {
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = wr * S::kWarpRows + i * 8 + qd * 2 + e;
-                m[i][e] = kNegInf;
+                mq[i][e] = kNegInf;
                 l[i][e] = 0.0f;
                 qs[i][e] = qscale[r];
                 limit[i][e] = it.len - it.nq + (row0 + r) / a.group + 1;
@@ -324,96 +325,117 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
                     for (int y = 0; y < 2; ++y)
                         ka[x][y] = *reinterpret_cast<const uint4*>(kt + stage_offset<kD>(x * 16 + y * 8 + og, w * 4 + qd));
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {  // 4 codes of a chunk: one k-step
-                    uint32_t af[2][4];
+                for (int z = 0; z < 4; z += 2) {  // 4 codes of a chunk are a k-step
+                    uint32_t af[2][2][4];
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            const uint32_t v = z == 0 ? ka[x][y].x : z == 1 ? ka[x][y].y : z == 2 ? ka[x][y].z : ka[x][y].w;
-                            af[x][y] = e4m3x2_lo_to_f16x2(v);
-                            af[x][y + 2] = e4m3x2_hi_to_f16x2(v);
+                            const uint32_t v0 = z == 0 ? ka[x][y].x : ka[x][y].z, v1 = z == 0 ? ka[x][y].y : ka[x][y].w;
+                            af[0][x][y] = e4m3x2_lo_to_f16x2(v0);
+                            af[0][x][y + 2] = e4m3x2_hi_to_f16x2(v0);
+                            af[1][x][y] = e4m3x2_lo_to_f16x2(v1);
+                            af[1][x][y + 2] = e4m3x2_hi_to_f16x2(v1);
                         }
 #pragma unroll
                     for (int i = 0; i < kRW; ++i) {
-                        const uint2 b = reinterpret_cast<const uint2*>(qf + (i * kKS + w * 2 + (z >> 1)) * 32)[z & 1];
-                        mma_f16(s[0][i], af[0], b.x, b.y);
-                        mma_f16(s[1][i], af[1], b.x, b.y);
+                        const uint4 b = qf[(i * kKS + w * 2 + (z >> 1)) * 32];
+                        mma_f16(s[0][i], af[0][0], b.x, b.y);
+                        mma_f16(s[1][i], af[0][1], b.x, b.y);
+                        mma_f16(s[0][i], af[1][0], b.z, b.w);
+                        mma_f16(s[1][i], af[1][1], b.z, b.w);
                     }
                 }
             }
             // The tile's largest value scale as a power of two (a NaN scale marks a poisoned token).
             const uint32_t rb = __reduce_max_sync(0xffffffffu, scale_exponent(sv[lane]));
-            const float r_new = fmaxf(__uint_as_float(rb), r_ref);
-            const float r_step = r_new == r_ref ? 1.0f : __fdividef(r_ref, r_new), r_inv = __fdividef(0x1p6f, r_new);
-            r_ref = r_new;
             float ks[4], vs[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 ks[x] = sk[x * 8 + og];
-                vs[x] = sv[x * 8 + og] * r_inv;
+                vs[x] = sv[x * 8 + og];
             }
-            uint32_t wb[2][kRW][2];  // weights as the B operand
-            float beta[kRW][2];
-            // Key scales, mask, running maximum, weights p * s_v and sums. A tile that every row sees whole
-            // needs no mask.
-            auto softmax = [&](auto edge) {
-                constexpr bool kEdge = decltype(edge)::value;
+            // Key scales and mask; exponents relative to the rows' references. A tile that every row sees whole needs
+            // no mask.
+            const bool edge = t * kTile + kTile > all_see;
+            bool passed = __uint_as_float(rb) > r_ref;
+            auto masked = [&](int i, int x, int e) { return edge && t * kTile + x * 8 + og >= limit[i][e]; };
+#pragma unroll
+            for (int i = 0; i < kRW; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) s[x >> 1][i][(x & 1) * 2 + e] *= ks[x];
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < kRW; ++i)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (masked(i, x, e)) s[x >> 1][i][(x & 1) * 2 + e] = kNegInf;
+            }
+#pragma unroll
+            for (int i = 0; i < kRW; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float top = fmaxf(fmaxf(s[0][i][e], s[0][i][e + 2]), fmaxf(s[1][i][e], s[1][i][e + 2]));
+                    passed = passed || fmaf(top, qs[i][e], -mq[i][e]) > kSlack;
+                }
+            // A reference moves only when a score passes it by 2^8, so this is rare past the first tiles; without it
+            // no maximum is shared between lanes and nothing is rescaled.
+            if (__any_sync(0xffffffffu, passed)) {
+                const float r_new = fmaxf(__uint_as_float(rb), r_ref);
+                const float r_step = r_new == r_ref ? 1.0f : __fdividef(r_ref, r_new);
+                r_ref = r_new;
 #pragma unroll
                 for (int i = 0; i < kRW; ++i) {
-                    float mq[2];
+                    float beta[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = kNegInf;
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            float& v = s[x >> 1][i][(x & 1) * 2 + e];
-                            v *= ks[x];
-                            if (kEdge && t * kTile + x * 8 + og >= limit[i][e]) v = kNegInf;
-                            top = fmaxf(top, v);
-                        }
+                        float top = fmaxf(fmaxf(s[0][i][e], s[0][i][e + 2]), fmaxf(s[1][i][e], s[1][i][e + 2]));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        // the reference moves only when the maximum passes it by 2^8
-                        const float m_new = (top - m[i][e]) * qs[i][e] > 8.0f ? top : m[i][e];
-                        mq[e] = (kEdge && m_new == kNegInf ? 0.0f : m_new) * qs[i][e];
-                        const float alpha = m_new == m[i][e] ? 1.0f : ex2(fmaf(m[i][e], qs[i][e], -mq[e]));
-                        m[i][e] = m_new;
-                        beta[i][e] = alpha * r_step;
+                        const float next = fmaf(top, qs[i][e], -mq[i][e]) > kSlack ? top * qs[i][e] : mq[i][e];
+                        const float alpha = next == mq[i][e] ? 1.0f : ex2(mq[i][e] - next);
+                        mq[i][e] = next;
+                        beta[e] = alpha * r_step;
                         l[i][e] *= alpha;
                     }
 #pragma unroll
+                    for (int j = 0; j < kDT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j][i][e] *= beta[e & 1];
+                }
+            }
+            // Weights p * s_v as the B operand, and sums.
+            const float r_inv = __fdividef(0x1p6f, r_ref);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) vs[x] *= r_inv;
+            uint32_t wb[2][kRW][2];
+            auto weigh = [&](auto masks) {
+#pragma unroll
+                for (int i = 0; i < kRW; ++i)
+#pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const float s0 = s[x >> 1][i][(x & 1) * 2], s1 = s[x >> 1][i][(x & 1) * 2 + 1];
-                        const float p0 = ex2(fmaf(s0, qs[i][0], -mq[0])), p1 = ex2(fmaf(s1, qs[i][1], -mq[1]));
-                        l[i][0] += p0;
-                        l[i][1] += p1;
-                        float w0 = p0 * vs[x], w1 = p1 * vs[x];
-                        if (kEdge) {  // a masked weight is zero whatever its scale holds
-                            if (s0 == kNegInf) w0 = 0.0f;
-                            if (s1 == kNegInf) w1 = 0.0f;
+                        float p[2], w[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            p[e] = ex2(fmaf(s[x >> 1][i][(x & 1) * 2 + e], qs[i][e], -mq[i][e]));
+                            w[e] = p[e] * vs[x];
+                            // a masked weight is zero whatever its row's reference and its scale hold
+                            if (decltype(masks)::value && masked(i, x, e)) p[e] = w[e] = 0.0f;
+                            l[i][e] += p[e];
                         }
-                        const __half2 h = __floats2half2_rn(w0, w1);
+                        const __half2 h = __floats2half2_rn(w[0], w[1]);
                         wb[x >> 1][i][x & 1] = movmatrix(*reinterpret_cast<const uint32_t*>(&h));
                     }
-                }
             };
-            if (t * kTile + kTile > all_see)
-                softmax(std::true_type{});
+            if (edge)
+                weigh(std::true_type{});
             else
-                softmax(std::false_type{});
-            bool moved = false;
-#pragma unroll
-            for (int i = 0; i < kRW; ++i) moved = moved || beta[i][0] != 1.0f || beta[i][1] != 1.0f;
-            if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                for (int j = 0; j < kDT; ++j)
-#pragma unroll
-                    for (int i = 0; i < kRW; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[j][i][e] *= beta[i][e & 1];
-            }
+                weigh(std::false_type{});
             // O^T += V^T W^T. Lane (g, q) reads the tokens of MMA columns 2q, 2q + 1, 2q + 8, 2q + 9 of each 16;
             // its bytes 2j and 2j + 1 are rows g and g + 8 of output tile j.
 #pragma unroll
@@ -455,7 +477,6 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
         group_sync();
 
         // The group's result, in place of its ring: o = sum p s_v v and, per row, its maximum (log2) and sum of p.
-        float mx[kRW][2];
 #pragma unroll
         for (int i = 0; i < kRW; ++i)
 #pragma unroll
@@ -463,7 +484,6 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
                 l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 4);
                 l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 8);
                 l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 16);
-                mx[i][e] = m[i][e] == kNegInf ? kNegInf : m[i][e] * qs[i][e];
             }
         const float r_out = r_ref * 0x1p-6f;
         // Column of output tile j's row g (row g + 8 is the next one).
@@ -480,7 +500,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
                     *reinterpret_cast<float4*>(o + column(j)) =
                         make_float4(acc[j][i][e] * r_out, acc[j][i][e + 2] * r_out, acc[j + 1][i][e] * r_out,
                                     acc[j + 1][i][e + 2] * r_out);
-                if (g == 0) ml[group * kRows + r] = make_float2(mx[i][e], l[i][e]);
+                if (g == 0) ml[group * kRows + r] = make_float2(mq[i][e], l[i][e]);
             }
         __syncthreads();
 
