@@ -228,8 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
 
     // A bounded wait by the whole warp; false once any wait of the CTA has run out.
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-        // The timer is read only after a while: it is far from the SM, and a wait here is a link of the chain scores -
-        // softmax - weights (read at the first miss it took 166 us for a 512-token chunk over 16384 instead of XX).
+        // (the timer is far from the SM and is read only after a while)
         bool ok = ptx::mbar_try_wait(bar, parity);
         uint64_t start = 0;
         for (uint32_t n = 1; !ok; ++n) {
@@ -549,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                     for (int c = 0; c < kTok; c += 32)
                         tc::ld_32x32b_x32(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(v + c));
                     // Key scales are requested 16 at a time, one step before their use: left to the compiler each load
-                    // waited for its own latency (173 us instead of XX for a 512-token chunk over 16384).
+                    // waited for its own latency (173 us instead of 136 for a 512-token chunk over 16384).
                     float4 k4[2][4];
                     auto request = [&](int step) {
 #pragma unroll

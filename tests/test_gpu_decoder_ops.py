@@ -348,7 +348,82 @@ def test_attention_peaked_scores_and_uneven_scales(fp8act):
     attend_and_check(fp8act, torch.zeros_like(randn(5, 8, 128, seed=7)), cache, table, lens, ns)
 
 
-@pytest.mark.parametrize("n", [3, 40])
+# Row tiles from 49 rows on, head size 128: the tcgen05 kernel, with one row tile (up to 128 rows), two halves of one
+# (up to 256), and several. Its values are widened with their scales, to within 2^-31 of the largest scale's power of
+# two, R: an absolute error of at most 2^-30 of the sequence's largest |v| beside the others.
+WIDE = [(9, 6), (64, 2), (22, 6), (32, 8), (43, 6), (100, 7)]
+
+
+@pytest.mark.parametrize("n,group", WIDE)
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_attention_wide_row_tiles(fp8act, n, group, page):
+    lens = [n, 127, 128, 129, 1, 700, 0, 2500]
+    ns = [min(n, L) if i % 2 == 0 else n for i, L in enumerate(lens)]  # some with more new tokens than cached
+    cache, table = make_cache(fp8act, lens, 2, 128, page, seed=n + page)
+    q = randn(sum(ns), 2 * group, 128, seed=3)
+    first = attend_and_check(fp8act, q, cache, table, lens, ns)
+    assert torch.equal(attend(fp8act, q, cache, table, lens, ns), first)
+
+
+@pytest.mark.parametrize("n,group", [(20, 6), (60, 6)])
+def test_attention_wide_rows_peaked_scores_and_uneven_scales(fp8act, n, group):
+    def v_scale(total):
+        return torch.exp2(torch.randint(-12, 13, (total,), device="cuda", generator=gen(5)).float())
+    lens, ns = [777, 300], [n, n // 2]
+    cache, table = make_cache(fp8act, lens, 2, 128, 32, seed=6, v_scale=v_scale)
+    for scale, softmax_scale in ((1.0, 1.0), (1e-30, None), (0.0, None)):
+        q = randn(sum(ns), 2 * group, 128, seed=7, scale=scale)
+        out = attend(fp8act, q, cache, table, lens, ns, softmax_scale=softmax_scale)
+        ref, mag, _ = attention_ref(q, cache, table, lens, ns, softmax_scale or 128 ** -0.5)
+        vmax = 448.0 * float(cache.v_scale.nan_to_num(0.0).max())
+        assert ((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * mag + 2.0 ** -30 * vmax).all()
+
+
+def test_attention_wide_rows_long_context_and_batch(fp8act):
+    lens, ns = [9000], [16]
+    cache, table = make_cache(fp8act, lens, 2, 128, 64, seed=61)
+    attend_and_check(fp8act, randn(16, 12, 128, seed=62), cache, table, lens, ns)
+    rng = np.random.default_rng(4)
+    lens = [int(x) for x in rng.integers(1, 1500, 40)]
+    ns = [min(int(x), L) for x, L in zip(rng.integers(0, 40, 40), lens)]
+    cache, table = make_cache(fp8act, lens, 2, 128, 16, seed=63)
+    q = randn(sum(ns), 8, 128, seed=64)
+    for hint in (20, 100):  # one row tile of 80 rows, or 256
+        attend_and_check(fp8act, q, cache, table, lens, ns, max_q_len=hint)
+
+
+def test_attention_wide_rows_nan_query(fp8act):
+    lens, ns = [500], [20]
+    cache, table = make_cache(fp8act, lens, 2, 128, 16, seed=65)
+    q = randn(20, 12, 128, seed=66)
+    clean = attend(fp8act, q, cache, table, lens, ns)
+    q[7, 3, 5], q[9, 11, 0] = math.nan, math.inf
+    out = attend(fp8act, q, cache, table, lens, ns)
+    bad = torch.isnan(out).all(-1)
+    assert bad.sum() == 2 and bad[7, 3] and bad[9, 11]
+    assert torch.equal(out[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("n", [16, 60])
+def test_attention_wait_that_runs_out(fp8act, n):
+    """The tcgen05 kernel leaves cleanly when a copy never comes, and the next call is right."""
+    lens, ns = [3000, 100], [n, n]
+    cache, table = make_cache(fp8act, lens, 2, 128, 64, seed=71)
+    q = randn(2 * n, 12, 128, seed=72)
+    want = attend_and_check(fp8act, q, cache, table, lens, ns)
+    try:
+        fp8act.set_wait_limit(1_000_000, True)
+        attend(fp8act, q, cache, table, lens, ns)
+        assert fp8act.check_status() == 5  # FP8ACT_ERR_TIMEOUT
+        fp8act.set_wait_limit(0, False)
+        attend(fp8act, q, cache, table, lens, ns)
+        assert fp8act.check_status() in (0, 5)
+    finally:
+        fp8act.set_wait_limit(-1, False)
+    assert torch.equal(attend(fp8act, q, cache, table, lens, ns), want)
+
+
+@pytest.mark.parametrize("n", [3, 40, 100])
 def test_attention_nan_reaches_only_rows_that_see_it(fp8act, n):
     L, H = 100, 2
     cache, table = make_cache(fp8act, [L], H, 128, 16, seed=21)
