@@ -17,7 +17,7 @@
 // scale is NaN (poisoned) gets zero values and a NaN key scale, which reaches
 // the rows that see it and no other.
 //
-// Two score tiles are in flight, each with a warpgroup whose threads own a row:
+// Two score tiles are in flight, each with a warpgroup whose warps own 32 rows:
 // with more than 128 rows they are the two halves of a 256-row tile on the same
 // cached tokens, which are loaded and widened once for both; else they are the
 // even and the odd token tiles of one row tile of up to 128 rows, whose two
@@ -25,6 +25,24 @@
 // softmax). While one warpgroup works the tensor cores serve the other. A
 // row's reference moves only when a score passes it by 2^8, so the output
 // accumulator is seldom rescaled.
+//
+// A softmax thread has 2 of every 8 columns of its rows (the accumulator layout
+// of the warp-level MMAs), 16 rows of the warp at a time: with a row per thread
+// every thread read all 128 key scales from shared memory, a third of what moves
+// there in all (16 tokens x 6 heads over 131072: 81.7 us, now 62.0; 512 over
+// 16384: 135.7, now 122.8, with the queries' way through shared memory below).
+// The two passes of 16 rows are a loop: the hot code of the roles that share an
+// instruction cache stays small.
+//
+// What bounds it: the chain of a score tile, 128 rows x 128 tokens, of about 4900
+// clocks: S 520 clocks, softmax 2500, weights through tensor memory, P V 520, and
+// the waits between. Two such chains keep the tensor cores half busy (512 tokens
+// x 24 heads over 16384: 826 TFLOP/s, S counted once); there is no
+// room for a third, whose scores would take the columns of an output, and score
+// tiles of 64 tokens do not help, since an MMA 64 columns wide takes longer than
+// one of 128 (104 clocks against 64). Measured and slower: the softmax on 16
+// warps with 96 registers, the weights taken first and the maximum checked after,
+// a third widened buffer.
 //
 // Every wait is bounded by wall time. The first that gives up sets the error
 // word and the CTA's abort flag; every role then leaves its loop, copies and
@@ -43,19 +61,22 @@ namespace {
 
 constexpr int kTok = 128;
 constexpr int kD = 128;
-constexpr int kItemCost = 4;    // units that an item counts beside its own
 constexpr int kLeastUnits = 2;  // least share of a CTA
-using Work = Units<kTok, kItemCost>;
 
 constexpr int kThreads = 512;  // warps 0 keys, 1 values, 2 MMA; 4..7 widening; 8..11 and 12..15 softmax
-// A softmax thread keeps a row of 128 scores: the other two warpgroups hand it
-// registers, 256 x 56 + 256 x 200 = 512 x 128, exactly the launch's.
-constexpr int kRegsOther = 56, kRegsSoftmax = 200;
+// The softmax warps take what the other two warpgroups hand back of their
+// registers, 256 x 64 + 256 x 192 = 512 x 128, exactly the launch's.
+constexpr int kRegsOther = 64, kRegsSoftmax = 192;
 static_assert(256 * kRegsOther + 256 * kRegsSoftmax <= kThreads * 128, "register split exceeds the launch's registers");
 constexpr int kTileBytes = kTok * kD;
+constexpr int kKSets = 4;  // tiles whose key scales are at hand (the values widened are at most 2 behind)
 
 template <bool kPair>  // two row tiles of 128 on the same tokens
 struct Tc {
+    // Units that an item counts beside its own, for its queries and its result. (Rows up to 128, 16 tokens x 6 heads over
+    // 131072: 5 units 63.6 us, 8 62.0; two row tiles, 512 tokens over 16384: 4 units 122.8 us, 6 126.5.)
+    static constexpr int kItemCost = kPair ? 4 : 8;
+    using Work = Units<kTok, kItemCost>;
     static constexpr int kQTiles = kPair ? 2 : 1;
     static constexpr int kKStages = kPair ? 3 : 4;
     static constexpr int kVStages = kPair ? 2 : 3;
@@ -64,9 +85,9 @@ struct Tc {
     static constexpr int kV8 = kK + kKStages * kTileBytes;
     static constexpr int kV16 = kV8 + kVStages * kTileBytes;       // 2 buffers of two 64-column halves
     static constexpr int kScale8 = kV16 + 2 * 2 * kTileBytes;      // per value stage: key scales, value scales
-    static constexpr int kScale16 = kScale8 + kVStages * 2 * kTok * 4;  // per buffer: key scales
-    static constexpr int kR = kScale16 + 2 * kTok * 4;             // per buffer: R
-    static constexpr int kQScale = kR + 16;
+    static constexpr int kScaleK = kScale8 + kVStages * 2 * kTok * 4;  // ring of kKSets: key scales
+    static constexpr int kR = kScaleK + kKSets * kTok * 4;         // the same ring: R
+    static constexpr int kQScale = kR + kKSets * 4;
     static constexpr int kML = kQScale + kQTiles * 128 * 4;        // second result's (maximum, sum, R) per row
     static constexpr int kBytes = kML + 128 * 16 + 1024;           // (the base is rounded up to 1024)
 };
@@ -82,6 +103,38 @@ __device__ __forceinline__ void st_16(uint32_t taddr, const uint32_t (&r)[16]) {
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
         "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
+// Score tiles move in the layout of the warp-level MMAs' accumulators: lane l holds rows l / 4 (+ 8) of 16 and of every 8
+// columns two, 2 (l % 4) and the next. 128 columns of the 16 lanes at `taddr`: v[4 n + 2 i + j] is row l / 4 + 8 i,
+// column 8 n + 2 (l % 4) + j.
+__device__ __forceinline__ void ld_16x256b_x16(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr));
+}
+// The same layout with a column holding two f16: r[2 n + i] is row l / 4 + 8 i, column 4 n + l % 4.
+__device__ __forceinline__ void st_16x128b_x16(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x16.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+        "r"(taddr)
         : "memory");
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -149,6 +202,10 @@ __device__ __forceinline__ void load_tokens(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Arrive on `bar` (one of its expected arrivals) once this thread's cp.asyncs so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -160,8 +217,14 @@ __device__ __forceinline__ float4 lds_v4(uint32_t addr) {
 }
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ float2 pair_of(const uint32_t (&v)[kTok], int j) {
-    return make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+// Where the key scale of a tile's token lies, so that a lane reads those of its columns 4 at a time.
+__device__ __forceinline__ int scale_at(int t) { return (t & ~15) | ((t >> 1 & 3) << 2) | ((t >> 3 & 1) << 1) | (t & 1); }
+
+template <typename T>
+__device__ __forceinline__ void swap(T& a, T& b) {
+    const T c = a;
+    a = b;
+    b = c;
 }
 
 template <bool kPair>
@@ -170,11 +233,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                                                                       const __grid_constant__ CUtensorMap v_map,
                                                                       const TcExtra x) {
     using C = Tc<kPair>;
+    using Work = typename C::Work;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* const smem = smem_raw + (base - ptx::smem_u32(smem_raw));
-    __shared__ Work::Scratch scratch;
-    __shared__ __align__(8) uint64_t bars[2 * C::kKStages + 2 * C::kVStages + 2 * 2 + 3 * 2 + 4];
+    __shared__ typename Work::Scratch scratch;
+    __shared__ __align__(8) uint64_t bars[2 * C::kKStages + 2 * C::kVStages + 2 * 2 + 3 * 2 + 4 + kKSets];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const uint32_t k_full = ptx::smem_u32(bars), k_empty = k_full + 8 * C::kKStages;
@@ -182,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
     const uint32_t v16_full = v8_empty + 8 * C::kVStages, v16_empty = v16_full + 16;
     const uint32_t s_full = v16_empty + 16, p_full = s_full + 16, pv_done = p_full + 16;  // [slot]
     const uint32_t q_full = pv_done + 16, item_done = q_full + 8, ml_full = item_done + 8, drain = ml_full + 8;
+    const uint32_t ks_full = drain + 8;  // [set]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     if (threadIdx.x == 0) {
@@ -200,10 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
             ptx::mbar_init(p_full + 8 * i, 4);
             ptx::mbar_init(pv_done + 8 * i, 1);
         }
-        ptx::mbar_init(q_full, 8);
+        ptx::mbar_init(q_full, kPair ? 8 : 4);
         ptx::mbar_init(item_done, 1);
         ptx::mbar_init(ml_full, 4);
         ptx::mbar_init(drain, 1);
+        for (int i = 0; i < kKSets; ++i) ptx::mbar_init(ks_full + 8 * i, 4);
         s_abort = 0;
         ptx::fence_mbar_init();
     }
@@ -262,8 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
         s.nrows = min(it.nq * a.group - s.row0, a.rows);
         s.slots = kPair && s.nrows <= 128 ? 1 : 2;
         const int seen = max(it.len - it.nq + (s.row0 + s.nrows - 1) / a.group + 1, 0);
-        s.f0 = max(t0 - kItemCost, 0);
-        s.n = max(min((seen + kTok - 1) / kTok, t1 - kItemCost) - s.f0, 0);
+        s.f0 = max(t0 - C::kItemCost, 0);
+        s.n = max(min((seen + kTok - 1) / kTok, t1 - C::kItemCost) - s.f0, 0);
         s.whole = t0 == 0 && t1 == it.tiles;
         return s;
     };
@@ -383,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
             for (int j = 0; j < jobs && ok; ++j) {
                 const int slot = slot_of(j);
                 const uint32_t buf = (seq + tile_of(j)) & 1;
-                // (the softmax warps have waited for the widened values before they arrive)
+                if (first_use(j) && !(ok = wait(v16_full + 8 * buf, (seq + tile_of(j)) >> 1 & 1))) break;
                 if (!keys(j + depth) || !(ok = wait(p_full + 8 * slot, waited[slot]++ & 1))) break;
                 tc::fence_after_sync();
                 const uint64_t v_desc = desc_values(base + C::kV16 + buf * 2 * kTileBytes);
@@ -415,7 +481,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
             for (int i = 0; i < s.n && ok; ++i) {
                 const uint32_t n = seq + i, stage = n % C::kVStages, buf = n & 1;
                 if (!(ok = wait(v8_full + 8 * stage, (n / C::kVStages) & 1))) break;
-                if (n >= 2 && !(ok = wait(v16_empty + 8 * buf, ((n >> 1) - 1) & 1))) break;
                 // R: the power of two below the largest value scale so far, the same in every warp.
                 const float* sc = reinterpret_cast<const float*>(smem + C::kScale8 + stage * 2 * kTok * 4);
                 uint32_t rb = 0;
@@ -426,6 +491,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                 const bool in = (s.f0 + i) * kTok + t < it.len;  // else anything may be there
                 const float sv = sc[kTok + t], sk = sc[t];
                 const bool poisoned = !(fabsf(sv) < 3e38f);
+                // The softmax may go ahead with the key scales.
+                reinterpret_cast<float*>(smem + C::kScaleK)[(n % kKSets) * kTok + scale_at(t)] = poisoned ? sv : sk;
+                if (t == 0) reinterpret_cast<float*>(smem + C::kR)[n % kKSets] = r_ref;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ks_full + 8 * (n % kKSets));
+                if (n >= 2 && !(ok = wait(v16_empty + 8 * buf, ((n >> 1) - 1) & 1))) break;
                 const float f = in && !poisoned ? sv * __fdividef(0x1p6f, r_ref) : 0.0f;
                 const uint8_t* v8 = smem + C::kV8 + stage * kTileBytes + t * kD;
                 uint8_t* v16 = smem + C::kV16 + buf * 2 * kTileBytes + t * 128;
@@ -437,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                     const __half2 w = __hfma2(c, f2, __hmul2(c, g2));
                     return *reinterpret_cast<const uint32_t*>(&w);
                 };
-#pragma unroll
+#pragma unroll 4
                 for (int c = 0; c < 8; ++c) {
                     uint4 v = *reinterpret_cast<const uint4*>(v8 + ((c ^ (t & 7)) << 4));
                     if (!in || poisoned) v = make_uint4(0, 0, 0, 0);
@@ -449,8 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                     *reinterpret_cast<uint4*>(half + ((((c & 3) * 2) ^ (t & 7)) << 4)) = lo;
                     *reinterpret_cast<uint4*>(half + ((((c & 3) * 2 + 1) ^ (t & 7)) << 4)) = hi;
                 }
-                reinterpret_cast<float*>(smem + C::kScale16)[buf * kTok + t] = poisoned ? sv : sk;
-                if (t == 0) reinterpret_cast<float*>(smem + C::kR)[buf] = r_ref;
                 fence_async_proxy();
                 __syncwarp();
                 if (lane == 0) {
@@ -475,145 +544,212 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
         while (ok) {
             const Span s = span_of();
             // Queries. The MMAs of the item before have read theirs (item_done was waited for).
-            {
-                constexpr int kWarpRows = kPair ? 32 : 16;  // the 8 warps share the rows
-                const int r0 = (warp - 8) * kWarpRows, c = lane & 15;
-#pragma unroll 2
-                for (int r = r0 + (lane >> 4); r < r0 + kWarpRows; r += 2) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (r < s.nrows) {
-                        const int qi = (s.row0 + r) / a.group, hg = (s.row0 + r) - qi * a.group;
-                        v = ld_dep_v4(a.q + (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD + c * 8);
+            const int r = s.row0 + row_in;
+            if (kPair || slot == 0) {
+                // A warp's rows are those that its threads own. Their bf16 values land where the two parts of the row will be
+                // (256 bytes either way), all requested together.
+                uint8_t* const q = smem + C::kQ + slot * 2 * kTileBytes + quad * 32 * 128;
+                {
+                    const int qi = r / a.group, hg = r - qi * a.group;
+                    const int64_t at = (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD;
+                    const int c = lane & 15;
+#pragma unroll 4
+                    for (int j = 0; j < 32; j += 2) {
+                        const int row = j + (lane >> 4);
+                        const int64_t from = __shfl_sync(0xffffffffu, at, row) + c * 8;
+                        const bool in = row_in - lane + row < s.nrows;
+                        cp_async16(ptx::smem_u32(q) + (c >> 3) * kTileBytes + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                                   a.q + (in ? from : 0), in);
                     }
-                    uint32_t top = top_bits(v);
+                    cp_async_wait_all();
+                    __syncwarp();
+                }
+                // 4 lanes a row, 32 columns each.
+                const int quarter = lane & 3;
+#pragma unroll 1
+                for (int row = lane >> 2; row < 32; row += 8) {
+                    uint8_t* const at = q + row * 128;
+                    uint4 v[4];
 #pragma unroll
-                    for (int o = 8; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = *reinterpret_cast<const uint4*>(at + (quarter >> 1) * kTileBytes +
+                                                               ((((quarter & 1) * 4 + i) ^ (row & 7)) << 4));
+                    __syncwarp();  // before the row's other lanes write over them
+                    uint32_t top = max(max(top_bits(v[0]), top_bits(v[1])), max(top_bits(v[2]), top_bits(v[3])));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     // (a zero row's exponent is as good as any)
                     const uint32_t e = top == 0 ? 127 : min(max(top >> 7, 8u), 253u);
                     const float up = __uint_as_float((261 - e) << 23);  // 2^(134 - e)
-                    if (c == 0) qscale[r] = fmaxf(__uint_as_float((e - 7) << 23) * a.scale_log2, 0x1p-126f);
+                    if (quarter == 0) qscale[row_in - lane + row] = fmaxf(__uint_as_float((e - 7) << 23) * a.scale_log2, 0x1p-126f);
                     const bool bad = top >= 0x7F80u;  // NaN or infinite: the whole row is NaN
-                    float f[8];
-                    unpack_bf16x8(v, f);
-                    uint32_t hi[2], lo[2];
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        float d[4];
-                        hi[w] = 0;
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int j = 0; j < 4; j += 2) {
-                            const float x0 = f[w * 4 + j] * up, x1 = f[w * 4 + j + 1] * up;
-                            const uint32_t pair = cvt_e4m3x2(x0, x1), back = e4m3x2_lo_to_f16x2(pair);
-                            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
-                            d[j] = x0 - b.x;
-                            d[j + 1] = x1 - b.y;
-                            hi[w] |= pair << (8 * j);
+                        for (int w = 0; w < 4; ++w) {
+                            float f[8];
+                            unpack_bf16x8(v[2 * i + (w >> 1)], f);
+                            float d[4];
+                            hi[w] = 0;
+#pragma unroll
+                            for (int j = 0; j < 4; j += 2) {
+                                const float x0 = f[(w & 1) * 4 + j] * up, x1 = f[(w & 1) * 4 + j + 1] * up;
+                                const uint32_t pair = cvt_e4m3x2(x0, x1), back = e4m3x2_lo_to_f16x2(pair);
+                                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
+                                d[j] = x0 - b.x;
+                                d[j + 1] = x1 - b.y;
+                                hi[w] |= pair << (8 * j);
+                            }
+                            lo[w] = cvt_e4m3x2(d[0], d[1]) | (cvt_e4m3x2(d[2], d[3]) << 16);
+                            if (bad) hi[w] = 0x7F7F7F7Fu;
                         }
-                        lo[w] = cvt_e4m3x2(d[0], d[1]) | (cvt_e4m3x2(d[2], d[3]) << 16);
-                        if (bad) hi[w] = 0x7F7F7F7Fu;
+                        uint8_t* const to = at + (((quarter * 2 + i) ^ (row & 7)) << 4);
+                        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(to + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                    uint8_t* q = smem + C::kQ + (r >> 7) * 2 * kTileBytes + (r & 127) * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-                    *reinterpret_cast<uint2*>(q) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2*>(q + kTileBytes) = make_uint2(lo[0], lo[1]);
                 }
                 fence_async_proxy();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(q_full);
-                if (!(ok = wait(q_full, item & 1))) break;
             }
-            const float qs = qscale[row_in];
-            const int r = s.row0 + row_in;
-            const bool rows_here = row_in - lane < s.nrows;  // of this warp
-            const int limit = it.len - it.nq + r / a.group + 1;                     // first position the row does not see
+            if (!(ok = wait(q_full, item & 1))) break;
+            const bool rows_here = row_in - lane < s.nrows;                         // of this warp
             const int all_see = it.len - it.nq + (r - lane) / a.group + 1;          // positions below it need no mask
-            // The row's reference: the largest (q . k) s_k that moved it, not yet times qs, and what is subtracted
-            // from a score in the exponent. The weights carry 2^kLift.
+            // A thread works on 4 rows of its warp's 32, lane / 4 + 8 i, and a quarter of their columns. A row's reference:
+            // the largest (q . k) s_k that moved it, not yet times qs, and what is subtracted from a score in the exponent.
+            // The weights carry 2^kLift.
             constexpr float kLift = 6.0f;
-            float m = kNegInf, mq = 0.0f, l = 0.0f, r_ref = 0x1p-100f;
+            float qs[4], m[4], mq[4], l[4], r_ref = 0x1p-100f;
+            int limit[4];  // first position that the row does not see
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = row_in - lane + (lane >> 2) + 8 * i;
+                qs[i] = qscale[at];
+                limit[i] = it.len - it.nq + (s.row0 + at) / a.group + 1;
+                m[i] = kNegInf;
+                mq[i] = 0.0f;
+                l[i] = 0.0f;
+            }
+            // The value that row `lane` of the warp's has, from the threads' four.
+            auto of_row = [&](const float (&x)[4]) {
+                const int from = (lane & 7) * 4;
+                float y = __shfl_sync(0xffffffffu, x[0], from);
+#pragma unroll
+                for (int i = 1; i < 4; ++i) {
+                    const float z = __shfl_sync(0xffffffffu, x[i], from);
+                    if (lane >> 3 == i) y = z;
+                }
+                return y;
+            };
             const int first = kPair ? 0 : slot, step = kPair ? 1 : 2;
             const int last = slot < s.slots ? s.n : 0;
             int mine = 0;
             for (int i = first; i < last && ok; i += step, ++mine) {
-                const uint32_t n = seq + i, buf = n & 1;
-                if (!(ok = wait(v16_full + 8 * buf, (n >> 1) & 1))) break;
+                const uint32_t n = seq + i, set = n % kKSets;
+                if (!(ok = wait(ks_full + 8 * set, (n / kKSets) & 1))) break;
                 if (!(ok = wait(s_full + 8 * slot, jobs_done & 1))) break;
                 tc::fence_after_sync();
                 if (rows_here) {
-                    const uint32_t ks = base + C::kScale16 + buf * kTok * 4;
-                    const float r_new = reinterpret_cast<const float*>(smem + C::kR)[buf];
+                    const uint32_t ks = base + C::kScaleK + set * kTok * 4 + (lane & 3) * 16;
+                    const float r_new = reinterpret_cast<const float*>(smem + C::kR)[set];
                     const int pos = (s.f0 + i) * kTok;
                     const bool edge = pos + kTok > all_see;
-                    uint32_t v[kTok];
+                    float alpha[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+                    bool rescale = false;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {  // rows lane / 4 + 16 h (+ 8)
+                        const uint32_t t_half = t_s + (static_cast<uint32_t>(16 * h) << 16);
+                        uint32_t v[64];
+                        ld_16x256b_x16(t_half, v);
+                        float4 k4[2];  // a step ahead
+                        k4[0] = lds_v4(ks);
+                        tc::wait_ld();
+                        float top[2] = {kNegInf, kNegInf};
+                        auto scaled = [&](bool masked) {
 #pragma unroll
-                    for (int c = 0; c < kTok; c += 32)
-                        tc::ld_32x32b_x32(t_s + c, *reinterpret_cast<uint32_t(*)[32]>(v + c));
-                    // Key scales are requested 16 at a time, one step before their use: left to the compiler each load
-                    // waited for its own latency (173 us instead of 136 for a 512-token chunk over 16384).
-                    float4 k4[2][4];
-                    auto request = [&](int step) {
+                            for (int j = 0; j < kTok / 16; ++j) {
+                                if (j + 1 < kTok / 16) k4[(j + 1) & 1] = lds_v4(ks + (j + 1) * 64);
+                                const float4 k = k4[j & 1];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) k4[step & 1][j] = lds_v4(ks + step * 64 + j * 16);
-                    };
-                    request(0);
-                    tc::wait_ld();
-                    float top4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+                                for (int e = 0; e < 2; ++e) {
+                                    const int n = 2 * j + e;
 #pragma unroll
-                    for (int step = 0; step < kTok / 16; ++step) {
-                        if (step + 1 < kTok / 16) request(step + 1);
+                                    for (int x = 0; x < 2; ++x) {
+                                        uint32_t &v0 = v[4 * n + 2 * x], &v1 = v[4 * n + 2 * x + 1];
+                                        float2 y = __fmul2_rn(make_float2(__uint_as_float(v0), __uint_as_float(v1)),
+                                                              e ? make_float2(k.z, k.w) : make_float2(k.x, k.y));
+                                        if (masked) {
+                                            const int end = limit[x] - pos - 2 * (lane & 3);
+                                            if (8 * n >= end) y.x = kNegInf;
+                                            if (8 * n + 1 >= end) y.y = kNegInf;
+                                        }
+                                        top[x] = fmaxf(top[x], fmaxf(y.x, y.y));
+                                        v0 = __float_as_uint(y.x);
+                                        v1 = __float_as_uint(y.y);
+                                    }
+                                }
+                            }
+                        };
+                        if (edge)
+                            scaled(true);
+                        else
+                            scaled(false);
+                        // A reference moves only when the row's maximum passes it by 2^8.
+                        bool moves = false;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int at = step * 16 + j * 4;
-                            const float4 k = k4[step & 1][j];
-                            const float2 x0 = __fmul2_rn(pair_of(v, at), make_float2(k.x, k.y));
-                            const float2 x1 = __fmul2_rn(pair_of(v, at + 2), make_float2(k.z, k.w));
-                            v[at] = __float_as_uint(x0.x);
-                            v[at + 1] = __float_as_uint(x0.y);
-                            v[at + 2] = __float_as_uint(x1.x);
-                            v[at + 3] = __float_as_uint(x1.y);
-                            if (!edge) top4[j] = fmaxf(fmaxf(top4[j], fmaxf(x0.x, x0.y)), fmaxf(x1.x, x1.y));
+                        for (int x = 0; x < 2; ++x) moves |= (top[x] - m[x]) * qs[x] > 8.0f;
+                        if (__any_sync(0xffffffffu, moves)) {
+                            rescale = true;
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int row = x;
+                                top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+                                top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+                                if ((top[x] - m[row]) * qs[row] > 8.0f) {
+                                    const float mq_new = fmaf(top[x], qs[row], -kLift);
+                                    alpha[row] = ex2(fmaf(m[row], qs[row], -kLift) - mq_new);
+                                    m[row] = top[x];
+                                    mq[row] = mq_new;
+                                }
+                            }
+                        }
+                        uint32_t w[32];
+                        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                        for (int n = 0; n < 16; ++n)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const float q = qs[x], ref = -mq[x];
+                                const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[4 * n + 2 * x]),
+                                                                        __uint_as_float(v[4 * n + 2 * x + 1])),
+                                                            make_float2(q, q), make_float2(ref, ref));
+                                const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                                sum[x] = __fadd2_rn(sum[x], e);
+                                const __half2 e16 = __floats2half2_rn(e.x, e.y);
+                                w[2 * n + x] = *reinterpret_cast<const uint32_t*>(&e16);
+                            }
+                        st_16x128b_x16(t_half, w);  // over the scores
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) l[x] = fmaf(l[x], alpha[x], sum[x].x + sum[x].y);
+                        // The other rows' values take the place of these.
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            swap(qs[x], qs[x + 2]);
+                            swap(m[x], m[x + 2]);
+                            swap(mq[x], mq[x + 2]);
+                            swap(l[x], l[x + 2]);
+                            swap(alpha[x], alpha[x + 2]);
+                            swap(limit[x], limit[x + 2]);
                         }
                     }
-                    if (edge) {
-                        const int end = limit - pos;
-#pragma unroll
-                        for (int j = 0; j < kTok; ++j) {
-                            if (j >= end) v[j] = 0xFF800000u;
-                            top4[j & 3] = fmaxf(top4[j & 3], __uint_as_float(v[j]));
-                        }
-                    }
-                    const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-                    // The reference moves only when the maximum passes it by 2^8.
-                    float alpha = 1.0f;
-                    if ((top - m) * qs > 8.0f) {
-                        const float mq_new = fmaf(top, qs, -kLift);
-                        alpha = ex2(fmaf(m, qs, -kLift) - mq_new);
-                        m = top;
-                        mq = mq_new;
-                    }
-                    const float2 qs2 = make_float2(qs, qs), mq2 = make_float2(-mq, -mq);
-                    float2 sum = make_float2(0.0f, 0.0f), sum2 = sum;
-#pragma unroll
-                    for (int c = 0; c < kTok; c += 32) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float2 y0 = __ffma2_rn(pair_of(v, c + j), qs2, mq2), y1 = __ffma2_rn(pair_of(v, c + j + 2), qs2, mq2);
-                            const float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
-                            sum = __fadd2_rn(sum, p0);
-                            sum2 = __fadd2_rn(sum2, p1);
-                            const __half2 h0 = __floats2half2_rn(p0.x, p0.y), h1 = __floats2half2_rn(p1.x, p1.y);
-                            w[j >> 1] = *reinterpret_cast<const uint32_t*>(&h0);
-                            w[(j >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-                        }
-                        st_16(t_s + c / 2, w);  // over the scores
-                    }
-                    sum = __fadd2_rn(sum, sum2);
-                    const float beta = r_new == r_ref ? alpha : alpha * __fdividef(r_ref, r_new);
+                    const float gain = r_new == r_ref ? 1.0f : __fdividef(r_ref, r_new);
                     r_ref = r_new;
-                    l = fmaf(l, alpha, sum.x + sum.y);
-                    if (mine > 0 && __any_sync(0xffffffffu, beta != 1.0f)) {
+                    rescale |= gain != 1.0f;  // (the same in every lane)
+                    if (mine > 0 && rescale) {
                         if (!(ok = wait(pv_done + 8 * slot, (jobs_done - 1) & 1))) break;
                         tc::fence_after_sync();
+                        const float beta = of_row(alpha) * gain;
 #pragma unroll 1
                         for (int c = 0; c < kD; c += 16) {
                             uint32_t o[16];
@@ -634,9 +770,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
             if (!ok) break;
             // The item's result: o = sum p s_v v / (2^6 / R) and, per row, its reference (log2) and sum of p, both with the
             // weights' 2^kLift.
-            float mx = m == kNegInf ? kNegInf : mq;
+            float mx, sum;
+            {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+                    mq[i] = m[i] == kNegInf ? kNegInf : mq[i];
+                }
+                mx = of_row(mq);
+                sum = of_row(l);
+            }
             if (!kPair && slot == 1) {
-                ml[row_in] = make_float4(mx, l, r_ref, 0.0f);
+                ml[row_in] = make_float4(mx, sum, r_ref, 0.0f);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ml_full);
             }
@@ -652,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                     const float e0 = ex2(mx - use), e1 = ex2(other.x - use);
                     f0 *= e0;
                     f1 = other.z * 0x1p-6f * e1;
-                    l = l * e0 + other.y * e1;
+                    sum = sum * e0 + other.y * e1;
                     mx = most;
                     has1 = s.n > 1;
                 }
@@ -661,42 +807,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                 const int qi = r / a.group, hg = r - qi * a.group;
                 const int64_t orow = static_cast<int64_t>(it.q0 + qi) * (a.c.heads * a.group) + it.h * a.group + hg;
                 const int64_t prow = static_cast<int64_t>(part) * a.rows + row_in;
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 if (rows_here) {
+                    // Through the shared memory of the warp's own queries, which no MMA reads any more, so that 8 lanes
+                    // store 32 columns of a row (with a lane per row each store touched 32 lines: 13000 clocks an item).
+                    uint8_t* const stage = smem + C::kQ + slot * 2 * kTileBytes + quad * 32 * 128;
+                    const float f = s.whole ? inv : 1.0f;
+                    const int64_t mine_at = (s.whole ? orow : prow) * kD;
 #pragma unroll 1
-                    for (int c = 0; c < kD; c += 16) {
-                        uint32_t o0[16], o1[16];
-                        if (has0) tc::ld_32x32b_x16(t_o + c, o0);
-                        if (has1) tc::ld_32x32b_x16(t_o + 128 + c, o1);
+                    for (int c = 0; c < kD; c += 32) {
+                        uint32_t o0[32], o1[32];
+                        if (has0) tc::ld_32x32b_x32(t_o + c, o0);
+                        if (has1) tc::ld_32x32b_x32(t_o + 128 + c, o1);
                         tc::wait_ld();
-                        float o[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            o[j] = has0 && f0 != 0.0f ? __uint_as_float(o0[j]) * f0 : 0.0f;
-                            if (has1 && f1 != 0.0f) o[j] = fmaf(__uint_as_float(o1[j]), f1, o[j]);
+                        for (int j = 0; j < 32; j += 4) {
+                            float o[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                o[i] = has0 && f0 != 0.0f ? __uint_as_float(o0[j + i]) * f0 : 0.0f;
+                                if (has1 && f1 != 0.0f) o[i] = fmaf(__uint_as_float(o1[j + i]), f1, o[i]);
+                            }
+                            *reinterpret_cast<float4*>(stage + lane * 128 + (((j >> 2) ^ (lane & 7)) << 4)) =
+                                make_float4(o[0] * f, o[1] * f, o[2] * f, o[3] * f);
                         }
-                        if (row_in < s.nrows) {
-                            if (s.whole) {
-                                uint4* dst = reinterpret_cast<uint4*>(a.out + ((orow * kD + c) >> 1));
+                        __syncwarp();
 #pragma unroll
-                                for (int j = 0; j < 2; ++j)
-                                    dst[j] = make_uint4(pack_bf16x2(o[8 * j] * inv, o[8 * j + 1] * inv),
-                                                        pack_bf16x2(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
-                                                        pack_bf16x2(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
-                                                        pack_bf16x2(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
-                            } else {
-                                float4* dst = reinterpret_cast<float4*>(a.part_o + prow * kD + c);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        for (int j = 0; j < 8; ++j) {
+                            const int row = j * 4 + (lane >> 3), at = c + (lane & 7) * 4;
+                            const float4 o = *reinterpret_cast<const float4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+                            const int64_t to = __shfl_sync(0xffffffffu, mine_at, row) + at;
+                            if (row_in - lane + row < s.nrows) {
+                                if (s.whole)
+                                    *reinterpret_cast<uint2*>(a.out + (to >> 1)) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+                                else
+                                    *reinterpret_cast<float4*>(a.part_o + to) = o;
                             }
                         }
                         __syncwarp();
                     }
                     if (row_in < s.nrows) {
                         if (!s.whole)
-                            *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(mx, l);
+                            *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(mx, sum);
                         else if (a.lse)
-                            a.lse[orow] = l == 0.0f ? kNegInf : (mx + log2f(l)) * 0.6931471805599453f;
+                            a.lse[orow] = sum == 0.0f ? kNegInf : (mx + log2f(sum)) * 0.6931471805599453f;
                     }
                 }
                 if (!s.whole && u == it.first && warp == 8 && lane == 0) write_split(a, it, per, part, s.row0, s.nrows);
