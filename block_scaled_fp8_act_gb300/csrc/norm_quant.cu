@@ -1,6 +1,12 @@
 // The two elementwise operators that feed a block-FP8 product: RMS norm with
 // the residual's addition, and silu(gate) * up, each ending in the product's
 // own activation format (E4M3 codes, one fp32 scale per 128 columns).
+//   norm: h = x + residual (stored as bf16), y = h / sqrt(mean h^2 + eps) * (weight + offset)
+//   silu: y = gate / (1 + exp(-gate)) * up
+// Both read and write each value once, so memory bounds them: 4096 x 5120 with
+// residual moves 147 MB in 27.4 us (5.4 TB/s, 0.79 of a copy's rate), 4096 x
+// 8704 gates 180 MB in 34.5 us (5.2 TB/s, 0.77). One row takes 1.8 us, a launch
+// with one trip to memory and the row's reductions. The sum of squares is fp32.
 #include "decoder_util.cuh"
 #include "kernels.h"
 
