@@ -43,29 +43,52 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float (&f)[8]) {
                       cvt_e4m3x2(f[4], f[5]) | (cvt_e4m3x2(f[6], f[7]) << 16));
 }
 
+// The same in pairs, for the two-wide fp32 instructions.
+__device__ __forceinline__ void unpack_bf16x8(const uint4& v, float2 (&f)[4]) {
+    f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+    f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+    f[2] = make_float2(bf16_lo(v.z), bf16_hi(v.z));
+    f[3] = make_float2(bf16_lo(v.w), bf16_hi(v.w));
+}
+__device__ __forceinline__ uint4 pack_bf16x8(const float2 (&f)[4]) {
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                      pack_bf16x2(f[3].x, f[3].y));
+}
+
 // Quantises one 128-wide group of fp32 values held by a half-warp (8 per
 // lane; the whole warp executes the call): s = amax / 448 (1 for an all-zero
-// group), code = E4M3(f / s). f is itself a rounded fp32 result here, so the
-// quotient is taken as f * RN(1 / s), within 1.5 fp32 ulp of the IEEE one: a
-// code differs from the IEEE quotient's only where that lies within 1.5 ulp
-// of a rounding midpoint, closer than f's own error. Outside [2^-100, 2^100],
-// where 1 / s nears the ends of the range, the division is done.
-__device__ __forceinline__ float quant_f32_group_halfwarp(float (&f)[8], uint2& codes) {
+// group), code = E4M3(f / s). s is the IEEE quotient: q0 = amax * RN(1/448) is
+// within 2 ulp, its remainder 448 q0 - amax is a small multiple of an ulp and
+// so exact, and amax / 448 = amax / (7 * 64) lies at least 1/14 ulp from any
+// rounding midpoint, far more than the corrected sum's error before its one
+// rounding. f is itself a rounded fp32 result here, so its quotient is taken as
+// f * y, y the approximate reciprocal after a Newton-Raphson step, within 2 fp32
+// ulp of the IEEE one: a code differs from the IEEE quotient's only where that
+// lies within 2 ulp of a rounding midpoint, closer than f's own error. Outside
+// [2^-100, 2^100], where the remainder or 1 / s nears the ends of the range,
+// the divisions are done.
+__device__ __forceinline__ float quant_f32_group_halfwarp(float2 (&f)[4], uint2& codes) {
     float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+    for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
 #pragma unroll
     for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float s = amax == 0.0f ? 1.0f : __fdiv_rn(amax, kE4M3Max);
+    float s;
     if (amax >= 0x1p-100f && amax <= 0x1p100f) {
-        const float y = __frcp_rn(s);
+        constexpr float kInv448 = 1.0f / kE4M3Max;
+        const float s0 = __fmul_rn(amax, kInv448);
+        s = __fmaf_rn(-__fmaf_rn(kE4M3Max, s0, -amax), kInv448, s0);
+        const float y0 = rcp_approx_ftz(s);
+        const float y = __fmaf_rn(__fmaf_rn(-s, y0, 1.0f), y0, y0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= y;
+        for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(f[i], make_float2(y, y));
     } else {
+        s = amax == 0.0f ? 1.0f : __fdiv_rn(amax, kE4M3Max);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], s);
+        for (int i = 0; i < 4; ++i) f[i] = make_float2(__fdiv_rn(f[i].x, s), __fdiv_rn(f[i].y, s));
     }
-    codes = pack_e4m3x8(f);
+    codes = make_uint2(cvt_e4m3x2(f[0].x, f[0].y) | (cvt_e4m3x2(f[1].x, f[1].y) << 16),
+                       cvt_e4m3x2(f[2].x, f[2].y) | (cvt_e4m3x2(f[3].x, f[3].y) << 16));
     return s;
 }
 

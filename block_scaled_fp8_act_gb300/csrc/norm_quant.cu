@@ -4,9 +4,11 @@
 //   norm: h = x + residual (stored as bf16), y = h / sqrt(mean h^2 + eps) * (weight + offset)
 //   silu: y = gate / (1 + exp(-gate)) * up
 // Both read and write each value once, so memory bounds them: 4096 x 5120 with
-// residual moves 147 MB in 27.4 us (5.4 TB/s, 0.79 of a copy's rate), 4096 x
-// 8704 gates 180 MB in 34.5 us (5.2 TB/s, 0.77). One row takes 1.8 us, a launch
+// residual moves 147 MB in 26.2 us (5.6 TB/s, 0.83 of a copy's rate), 4096 x
+// 8704 gates 179 MB in 30.0 us (6.0 TB/s, 0.88). One row takes 1.8 us, a launch
 // with one trip to memory and the row's reductions. The sum of squares is fp32.
+// Arithmetic goes in pairs and the scale and its reciprocal without divisions:
+// at 250 instructions per 8 columns issue slots were 72 % busy (27.4 us).
 #include "decoder_util.cuh"
 #include "kernels.h"
 
@@ -37,23 +39,23 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint4* x, con
         wv[i] = c < chunks ? __ldg(weight + c) : make_uint4(0, 0, 0, 0);
     }
     ptx::griddep_wait();
-    float h[kChunks][8];
-    float ss = 0.0f;
+    float2 h[kChunks][4], ss2 = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         const bool in = c < chunks;
         unpack_bf16x8(in ? ld_dep_stream_v4(x + c) : make_uint4(0, 0, 0, 0), h[i]);
         if (kResidual) {
-            float r[8];
+            float2 r[4];
             unpack_bf16x8(in ? ld_dep_stream_v4(residual + c) : make_uint4(0, 0, 0, 0), r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+            for (int j = 0; j < 4; ++j) h[i][j] = __fadd2_rn(h[i][j], r[j]);
             if (in) residual_out[c] = pack_bf16x8(h[i]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+        for (int j = 0; j < 4; ++j) ss2 = __ffma2_rn(h[i][j], h[i][j], ss2);
     }
+    float ss = ss2.x + ss2.y;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if (lane == 0) part[warp] = ss;
@@ -62,14 +64,15 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint4* x, con
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float rstd = rsqrtf(ss / static_cast<float>(chunks * 8) + eps);
+    const float2 rstd2 = make_float2(rstd, rstd), offset2 = make_float2(weight_offset, weight_offset);
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         const bool in = c < chunks;
-        float w[8];
+        float2 w[4];
         unpack_bf16x8(wv[i], w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = h[i][j] * rstd * (w[j] + weight_offset);
+        for (int j = 0; j < 4; ++j) w[j] = __fmul2_rn(__fmul2_rn(h[i][j], rstd2), __fadd2_rn(w[j], offset2));
         uint2 codes;
         const float s = quant_f32_group_halfwarp(w, codes);
         if (in) {
@@ -79,9 +82,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint4* x, con
     }
 }
 
+constexpr int kSiluCtas = 6;  // per SM, at 40 registers a thread
 // silu(gate) * up of one row [gate (I) | up (I)]: a half-warp per 128-wide
 // group, warps striding over (row, pair of groups).
-__global__ void silu_mul_quant_kernel(const uint4* gate_up, int64_t M, int groups, uint2* q, float* sa) {
+__global__ void __launch_bounds__(256) silu_mul_quant_kernel(const uint4* gate_up, int64_t M, int groups, uint2* q, float* sa) {
     const int lane = threadIdx.x & 31, hl = lane & 15;
     const int pairs = (groups + 1) / 2;
     const int64_t items = M * pairs;
@@ -103,7 +107,7 @@ __global__ void silu_mul_quant_kernel(const uint4* gate_up, int64_t M, int group
     };
     load();
     while (item < items) {
-        float a[8], b[8];
+        float2 a[4], b[4];
         unpack_bf16x8(va, a);
         unpack_bf16x8(vb, b);
         const int64_t at = row * groups + pair * 2 + (lane >> 4);
@@ -116,8 +120,14 @@ __global__ void silu_mul_quant_kernel(const uint4* gate_up, int64_t M, int group
             ++row;
         }
         load();
+        // (an infinite exponential gives 0, as a division by it would; the approximations are within 2 fp32 ulp each)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = __fdividef(a[j], 1.0f + __expf(-a[j])) * b[j];
+        for (int j = 0; j < 4; ++j) {
+            const float2 t = __fmul2_rn(a[j], make_float2(-1.4426950408889634f, -1.4426950408889634f));
+            const float2 d = __fadd2_rn(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.0f, 1.0f));
+            const float2 g = __fmul2_rn(a[j], make_float2(rcp_approx_ftz(d.x), rcp_approx_ftz(d.y)));
+            a[j] = __fmul2_rn(g, b[j]);
+        }
         uint2 codes;
         const float s = quant_f32_group_halfwarp(a, codes);
         if (in) {
@@ -143,8 +153,8 @@ cudaError_t launch_rmsnorm_quant(const void* x, const void* residual, const void
                                  float weight_offset, int M, int K, void* q, float* sa, void* residual_out,
                                  int num_sms, cudaStream_t stream) {
     const int chunks = K / 8;
-    // One chunk per thread wherever a CTA holds the row: 4096 x 5120 with residual takes 27.4 us, with 2 or 4 chunks
-    // per thread 28.9 or 32.5.
+    // One chunk per thread wherever a CTA holds the row: 4096 x 5120 with residual took 27.4 us so, with 2 or 4 chunks
+    // per thread 28.9 or 32.5. (CTAs that stay and request the next row early: 26.7 to 31, now 26.2 with a CTA a row.)
     if (chunks <= 1024)
         return launch_norm<1>(x, residual, weight, eps, weight_offset, M, chunks, q, sa, residual_out, stream);
     return launch_norm<4>(x, residual, weight, eps, weight_offset, M, chunks, q, sa, residual_out, stream);
@@ -155,7 +165,9 @@ cudaError_t launch_silu_mul_quant(const void* gate_up, int M, int I, void* q, fl
     const int groups = I / kGroup;
     const int64_t warps = static_cast<int64_t>(M) * ((groups + 1) / 2);
     int64_t blocks = (warps + 7) / 8;
-    if (blocks > 8 * static_cast<int64_t>(num_sms)) blocks = 8 * static_cast<int64_t>(num_sms);
+    // No more CTAs than run at once: 4096 x 8704 takes 30.0 us, with 8 per SM, a third of them in a second wave, 34.4,
+    // with 8 at 32 registers (spills) 33.6.
+    if (blocks > kSiluCtas * static_cast<int64_t>(num_sms)) blocks = kSiluCtas * static_cast<int64_t>(num_sms);
     return launch_dependent(silu_mul_quant_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 1,
                             static_cast<const uint4*>(gate_up), static_cast<int64_t>(M), groups,
                             static_cast<uint2*>(q), sa);
