@@ -68,7 +68,7 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -76,7 +76,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 // Transpose of an 8 x 8 matrix of 16-bit values held as an MMA fragment.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 
@@ -345,13 +345,18 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
                             af[1][x][y] = e4m3x2_lo_to_f16x2(v1);
                             af[1][x][y + 2] = e4m3x2_hi_to_f16x2(v1);
                         }
+                    uint4 b[kRW];
+#pragma unroll
+                    for (int i = 0; i < kRW; ++i) b[i] = qf[(i * kKS + w * 2 + (z >> 1)) * 32];
 #pragma unroll
                     for (int i = 0; i < kRW; ++i) {
-                        const uint4 b = qf[(i * kKS + w * 2 + (z >> 1)) * 32];
-                        mma_f16(s[0][i], af[0][0], b.x, b.y);
-                        mma_f16(s[1][i], af[0][1], b.x, b.y);
-                        mma_f16(s[0][i], af[1][0], b.z, b.w);
-                        mma_f16(s[1][i], af[1][1], b.z, b.w);
+                        mma_f16(s[0][i], af[0][0], b[i].x, b[i].y);
+                        mma_f16(s[1][i], af[0][1], b[i].x, b[i].y);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kRW; ++i) {
+                        mma_f16(s[0][i], af[1][0], b[i].z, b[i].w);
+                        mma_f16(s[1][i], af[1][1], b[i].z, b[i].w);
                     }
                 }
             }
