@@ -18,11 +18,13 @@
 // both took 20.5 us for 7 drafts at one sequence, where 16 SMs read 4.6 MB,
 // and 53 us for 34 x 2 drafts.)
 //
-// Measured over 151936 bf16 logits: 26.8 us for 34 sequences of 2 drafts (72 MB read once, 2.7 TB/s; 10.7 us at the
-// rate of a copy) and 11.2 us for one sequence of 7 (0.8). What bounds it: the first kernel, about half of the time, by
+// Measured over 151936 bf16 logits: 26.0 us for 34 sequences of 2 drafts (72 MB read once, 2.8 TB/s; 10.7 us at the
+// rate of a copy) and 10.3 us for one sequence of 7 (0.8). What bounds it: the first kernel, about half of the time, by
 // issue (an exponential, a widening and a maximum per logit: 2.6 of 4 instructions a clock); the second, and a single
 // sequence, by the chain of dependent latencies: statistics, acceptance, the row drawn from, the cluster's meeting.
 // Widening and adding in pairs (packed maximum, fp32 pairs) took 0.8 us off the first.
+// The first starts the second after its own wait, so that the second reads the drafts' tokens, numbers and logits while
+// the first still runs (0.6-1.1 us).
 #include <atomic>
 
 #include "decoder_util.cuh"
@@ -162,8 +164,8 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const Verify
     const int head = row.head(), vecs = (p.V - head) / R::kPer, tail = head + vecs * R::kPer;
     const int v0 = static_cast<int>(static_cast<int64_t>(vecs) * share / shares);
     const int v1 = static_cast<int>(static_cast<int64_t>(vecs) * (share + 1) / shares);
-    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();  // (after the wait: the second kernel reads inputs before its own)
     q.read_temperature(p, blockIdx.z);
     Stat st = {kNegInf, 0.0f, 0x7FFFFFFF};
     auto one = [&](int i) {
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyPr
     const int i0 = static_cast<int>(static_cast<int64_t>(V) * rank / cluster);
     const int i1 = static_cast<int>(static_cast<int64_t>(V) * (rank + 1) / cluster);
     ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
+    // The inputs are complete, since the first kernel starts this one after its own wait: only what it wrote is waited for.
     q.read_temperature(p, b);
     const float c = q.c;
     const bool greedy = q.greedy, draft = p.draft != nullptr;
@@ -288,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyPr
             atomicOr(&g_verify_index_error, 1u);
         }
     }
+    ptx::griddep_wait();
     for (int r = warp; r < q.rows; r += kWarps) {  // a warp per row, a lane per part
         const Stat* from = parts + (static_cast<int64_t>(b) * q.rows + r) * shares + lane;
         Stat st = {kNegInf, 0.0f, 0x7FFFFFFF};
