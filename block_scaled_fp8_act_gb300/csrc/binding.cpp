@@ -110,6 +110,13 @@ PyObject* tuple(const std::array<at::Tensor, kN>& v, size_t n = kN) {
     return t;
 }
 
+// Memory that is let go here may still be in use on `stream`; if it came from another stream's pool, that one must not
+// hand it out again before.
+void let_go(const at::Tensor& t, cudaStream_t stream) {
+    if (t.defined() && stream != c10::cuda::getCurrentCUDAStream(t.get_device()).stream())
+        t.record_stream(c10::cuda::getStreamFromExternal(stream, t.get_device()).unwrap());
+}
+
 // A workspace: the caller's, or one kept per device and stream (calls of one stream share it; a graph being captured
 // gets its own).
 struct Workspace {
@@ -129,11 +136,15 @@ Workspace workspace(PyObject* o, size_t need, const at::Tensor& like, cudaStream
     if (stream && cudaStreamIsCapturing(stream, &capturing) != cudaSuccess) cudaGetLastError();
     if (capturing != cudaStreamCaptureStatusNone) {
         at::Tensor t = fresh();
+        let_go(t, stream);  // (after the call)
         return {t, t.data_ptr(), need};
     }
     static auto* kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>;  // outlives the CUDA context
     at::Tensor& t = (*kept)[{like.get_device(), stream}];
-    if (!t.defined() || t.nbytes() < need) t = fresh();
+    if (!t.defined() || t.nbytes() < need) {
+        let_go(t, stream);
+        t = fresh();
+    }
     return {t, t.data_ptr(), static_cast<size_t>(t.nbytes())};
 }
 

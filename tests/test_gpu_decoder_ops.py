@@ -662,3 +662,46 @@ def test_verify_keeps_the_targets_distribution(fp8act, greedy_draft):
     seen = torch.bincount(tokens[:, 0].long(), minlength=V).double()
     chi2 = float(((seen - want) ** 2 / want).sum())
     assert chi2 < (V - 1) + 5 * math.sqrt(2 * (V - 1)) + 25
+
+
+def test_verify_right_behind_its_producers(fp8act):
+    """Logits come from two products just before, step after step without a pause; nothing old may be read."""
+    B, k, V, K = 2, 3, 4096, 256
+    w, sw = fp8act.fp8_weight_quant(randn(V, K, seed=1))
+    acts = [(fp8act.fp8_act_quant(randn(B * (k + 1), K, seed=10 + i)), fp8act.fp8_act_quant(randn(B * k, K, seed=20 + i)))
+            for i in range(3)]
+    _, _, x, u, e = drafts(B, k, V, seed=3)
+    temp = torch.tensor([1.0, 0.6], device="cuda")
+    t = torch.empty((B * (k + 1), V), dtype=torch.bfloat16, device="cuda")
+    d = torch.empty((B * k, V), dtype=torch.bfloat16, device="cuda")
+
+    def step(i, pause):
+        fp8act.fp8_block_gemm(*acts[i][1], w, sw, out=d)
+        fp8act.fp8_block_gemm(*acts[i][0], w, sw, out=t)
+        if pause:
+            torch.cuda.synchronize()
+        return fp8act.verify_drafts(t.view(B, k + 1, V), x, u, e, temp, draft_logits=d.view(B, k, V))
+
+    want = [step(i, True) for i in range(3)]
+    torch.cuda.synchronize()
+    got = [step(i % 3, False) for i in range(30)]
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 3]))
+
+
+def test_kept_workspace_grows_on_a_stream_that_is_passed(fp8act):
+    """A call that needs more memory than the one before lets the old go while the stream still works on it."""
+    side = torch.cuda.Stream()
+    small, large = drafts(1, 1, 5000, seed=1), drafts(40, 7, 5000, seed=2)
+    temp = [torch.ones(1, device="cuda"), torch.ones(40, device="cuda")]
+
+    def call(s, t, **kw):
+        return fp8act.verify_drafts(s[0], s[2], s[3], s[4], t, draft_logits=s[1], **kw)
+
+    want = call(small, temp[0]), call(large, temp[1])
+    torch.cuda.synchronize()
+    got = call(small, temp[0], stream=side), call(large, temp[1], stream=side)
+    # the current stream asks for memory of the old one's size and writes it
+    junk = [torch.full((512,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    side.synchronize()
+    assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w)) and len(junk) == 8
