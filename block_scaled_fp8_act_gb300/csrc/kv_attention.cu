@@ -34,11 +34,11 @@
 // launched dependently, adds in unit order: results do not depend on timing.
 //
 // What bounds it, by rows of a tile (D = 128): with up to 8 (one token) the
-// cache's bytes, 34 us for 131072 tokens x 4 heads (0.81 of a copy's rate while
+// cache's bytes, 31 us for 131072 tokens x 4 heads (0.81 of a copy's rate while
 // it streams); with 24 (34 sequences x 3 tokens, ragged up to 16384: 33 us, 0.38)
-// and 48 (8 tokens over 131072: 62 us, 0.33) the latency of a unit's chain, keys
+// and 48 (8 tokens over 131072: 59 us, 0.35) the latency of a unit's chain, keys
 // to scores to weights to output, with 8 and 12 warps an SM to hide it: their
-// accumulators fill the registers. A single token over 4096 tokens takes 10.2
+// accumulators fill the registers. A single token over 4096 tokens takes 9.0
 // us, the chain of the two kernels.
 #include <atomic>
 #include <type_traits>
@@ -104,7 +104,8 @@ __device__ __forceinline__ int order(int i) {
 
 // kWR warps of a group split the row tile, kRW groups of 8 rows each; kG groups in a CTA; kCtas CTAs per SM (two
 // where a group is one warp: one streams while the other starts or ends an item, 38 us instead of 46 for 34 ragged
-// sequences x 3 tokens).
+// sequences x 3 tokens; but one for D = 256, whose stages are twice as large: one token over 32768 with 8 heads on 4
+// 30.2 us instead of 42.2, two tokens of 8 ragged sequences 23.1 instead of 32.8).
 template <int kD, int kWR, int kRW, int kG, int kCtas_>
 struct Attn {
     static constexpr int kCtas = kCtas_;
@@ -559,30 +560,55 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
     }
 }
 
-// Adds the parts of the items that cross CTAs, a warp per row: CTA (c, y) takes
-// rows 8 y .. 8 y + 7 of the item that starts in CTA c of the first kernel.
-// Latency is all it is: the item's record is one load, then every lane fetches
-// the maximum and sum of its own parts while the rows of 16 parts are on their
-// way.
-constexpr int kJoinRows = 8;
+// Adds the parts of the items that cross CTAs: CTA (c, y) takes some rows of
+// the item that starts in CTA c of the first kernel, kSplit of its 8 warps per
+// row. Latency is all it is: the item's record is one load, then every lane
+// fetches the maximum and sum of one of the warp's parts while the rows of 8 or
+// 16 parts are on their way. A long context of few rows has tens of parts, which
+// 4 warps a row take in one or two such trips (one token over 131072: 34.0 us with
+// 1 warp a row, 30.9 with 4); many rows have enough warps as it is.
+constexpr int kJoinWarps = 8;
 
-template <int kD>
-__global__ void __launch_bounds__(kJoinRows * 32) kv_attention_join_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int kV = kD / 32, kAhead = 128 / kV / 2;
-    const int lane = threadIdx.x & 31;
-    const int c = blockIdx.x, r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+template <int kD, int kSplit>
+__global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_join_kernel(const __grid_constant__ AttnArgs a, int listed) {
+    constexpr int kV = kD / 32, kAhead = 128 / kV / 2, kRows = kJoinWarps / kSplit;
+    __shared__ float2 part_ml[kJoinWarps];
+    __shared__ float part_o[kSplit > 1 ? kJoinWarps : 1][kSplit > 1 ? kD : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slice = warp % kSplit;
+    const int r = blockIdx.y * kRows + warp / kSplit;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
+    int c = blockIdx.x;
+    if (kSplit > 1 && listed) {  // the x-th record that holds an item
+        uint32_t held[kMaxAttnGrid / 32];
+#pragma unroll
+        for (int i = 0; i < kMaxAttnGrid / 32; ++i)
+            held[i] = i * 32 + lane < listed ? ld_dep_s32(&a.split[i * 32 + lane].parts) : 0;
+        c = -1;
+        int before = blockIdx.x;
+#pragma unroll
+        for (int i = 0; i < kMaxAttnGrid / 32; ++i) {
+            const uint32_t bits = __ballot_sync(0xffffffffu, held[i] != 0);
+            const uint32_t hit = __ballot_sync(0xffffffffu, held[i] != 0 && __popc(bits & ((1u << lane) - 1)) == before);
+            if (hit) c = i * 32 + __ffs(hit) - 1;
+            before -= __popc(bits);
+        }
+        if (c < 0) return;  // (the whole CTA)
+    }
     const uint4 s0 = ld_dep_v4(a.split + c), s1 = ld_dep_v4(reinterpret_cast<const uint4*>(a.split + c) + 1);
-    const int parts = static_cast<int>(s0.x), second = static_cast<int>(s0.y);
-    if (parts == 0 || r >= static_cast<int>(s1.y)) return;
-    auto slot_of = [&](int i) { return static_cast<int64_t>(2 * (c + i) + (i == 0 ? second : 0)) * a.rows + r; };
+    const int parts = static_cast<int>(s0.x), second = static_cast<int>(s0.y), nrows = static_cast<int>(s1.y);
+    if (parts == 0 || static_cast<int>(blockIdx.y) * kRows >= nrows) return;  // (the whole CTA)
+    const int mine_n = r < nrows ? (parts - slice + kSplit - 1) / kSplit : 0;  // parts slice, slice + kSplit, ...
+    auto slot_of = [&](int j) {
+        const int i = slice + j * kSplit;
+        return static_cast<int64_t>(2 * (c + i) + (i == 0 ? second : 0)) * a.rows + r;
+    };
     const float2* pml = reinterpret_cast<const float2*>(a.part_ml);
     float mm = kNegInf, sum = 0.0f, o[kV];
 #pragma unroll
     for (int x = 0; x < kV; ++x) o[x] = 0.0f;
-    for (int base = 0; base < parts; base += 32) {  // 32 parts: the lanes hold their maxima and sums
-        const int here = min(parts - base, 32);
+    for (int base = 0; base < mine_n; base += 32) {  // 32 parts: the lanes hold their maxima and sums
+        const int here = min(mine_n - base, 32);
         const float2 mine = lane < here ? __ldcg(pml + slot_of(base + lane)) : make_float2(kNegInf, 0.0f);
         float f = 0.0f;
         for (int i0 = 0; i0 < here; i0 += kAhead) {
@@ -621,7 +647,28 @@ __global__ void __launch_bounds__(kJoinRows * 32) kv_attention_join_kernel(const
             }
         }
     }
-    write_row<kD>(a, static_cast<int>(s0.z), static_cast<int>(s0.w), static_cast<int>(s1.x) + r, lane, mm, sum, o);
+    if constexpr (kSplit > 1) {
+        if (lane == 0) part_ml[warp] = make_float2(mm, sum);
+#pragma unroll
+        for (int x = 0; x < kV; ++x) part_o[warp][lane * kV + x] = o[x];
+        __syncthreads();
+        if (slice != 0) return;
+#pragma unroll
+        for (int w = 1; w < kSplit; ++w) mm = fmaxf(mm, part_ml[warp + w].x);
+        const float use = mm == kNegInf ? 0.0f : mm;
+        sum = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kV; ++x) o[x] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kSplit; ++w) {
+            const float f = ex2(part_ml[warp + w].x - use);
+            sum = fmaf(part_ml[warp + w].y, f, sum);
+#pragma unroll
+            for (int x = 0; x < kV; ++x) o[x] = fmaf(part_o[warp + w][lane * kV + x], f, o[x]);
+        }
+    }
+    if (r < nrows)
+        write_row<kD>(a, static_cast<int>(s0.z), static_cast<int>(s0.w), static_cast<int>(s1.x) + r, lane, mm, sum, o);
 }
 
 template <int kD, int kWR, int kRW, int kG, int kCtas>
@@ -669,7 +716,7 @@ cudaError_t launch_rows<64>(const AttnArgs& a, int num_sms, int& grid, cudaStrea
     switch (a.rows) {
         case 8: return launch_attention<64, 1, 1, 6, 2>(a, num_sms, grid, stream);
         case 16: return launch_attention<64, 1, 2, 6, 2>(a, num_sms, grid, stream);
-        case 24: return launch_attention<64, 1, 3, 4, 2>(a, num_sms, grid, stream);
+        case 24: return launch_attention<64, 1, 3, 6, 2>(a, num_sms, grid, stream);
         case 48: return launch_attention<64, 2, 3, 4, 1>(a, num_sms, grid, stream);
         case 96: return launch_attention<64, 4, 3, 2, 1>(a, num_sms, grid, stream);
         default: return launch_attention<64, 8, 3, 1, 1>(a, num_sms, grid, stream);
@@ -690,21 +737,31 @@ cudaError_t launch_rows<128>(const AttnArgs& a, int num_sms, int& grid, cudaStre
 template <>
 cudaError_t launch_rows<256>(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream) {
     switch (a.rows) {
-        case 8: return launch_attention<256, 1, 1, 3, 2>(a, num_sms, grid, stream);
-        case 16: return launch_attention<256, 1, 2, 3, 2>(a, num_sms, grid, stream);
+        case 8: return launch_attention<256, 1, 1, 6, 1>(a, num_sms, grid, stream);
+        case 16: return launch_attention<256, 2, 1, 4, 1>(a, num_sms, grid, stream);
         case 32: return launch_attention<256, 2, 2, 4, 1>(a, num_sms, grid, stream);
         default: return launch_attention<256, 4, 2, 2, 1>(a, num_sms, grid, stream);
     }
 }
 
 template <int kD>
-cudaError_t launch_both(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_both(const AttnArgs& a, int max_q_len, int num_sms, cudaStream_t stream) {
     if (num_sms > kMaxAttnGrid / 2) num_sms = kMaxAttnGrid / 2;
     int grid = 0;
     const cudaError_t e = launch_rows<kD>(a, num_sms, grid, stream);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kv_attention_join_kernel<kD>, dim3(grid, (a.rows + kJoinRows - 1) / kJoinRows), kJoinRows * 32,
-                            0, stream, 1, a);
+    const int64_t items = static_cast<int64_t>(a.batch) * a.c.heads * ((static_cast<int64_t>(max_q_len) * a.group + a.rows - 1) / a.rows);
+    // 4 warps a row while the items are few, so that each has many parts: (us, 1 and 4 warps) one token over 4096 10.1 and
+    // 8.9, over 131072 34.0 and 30.6, 8 over 131072 61.9 and 58.9, one of 12 heads on 1 39.7 and 22.2; but 8 sequences
+    // x 8 tokens 28.1 and 31.4. Up to 16 rows a CTA looks at each record, most of which hold no item; with more rows
+    // the CTAs, one per item there can be, find theirs in the list, which costs 1 us and saves the empty CTAs 2 to 3.
+    const bool many = items * (a.rows <= 16 ? 4 : 8) <= grid, listed = many && a.rows > 16;
+    const int rows = many ? kJoinWarps / 4 : kJoinWarps;
+    // (a sequence may have more tokens than max_q_len says: room for every row tile that the tokens can make)
+    const int64_t most = a.c.heads * ((static_cast<int64_t>(a.tokens) * a.group + static_cast<int64_t>(a.batch) * (a.rows - 1)) / a.rows);
+    const dim3 join(listed && most < grid ? static_cast<int>(most) : grid, (a.rows + rows - 1) / rows);
+    return launch_dependent(many ? kv_attention_join_kernel<kD, 4> : kv_attention_join_kernel<kD, 1>, join, kJoinWarps * 32, 0,
+                            stream, 1, a, listed ? grid : 0);
 }
 
 }  // namespace
@@ -740,9 +797,9 @@ cudaError_t launch_kv_attention(const AttentionProblem& p, int num_sms, cudaStre
     a.part_ml = reinterpret_cast<float*>(a.split + kMaxAttnGrid);
     a.part_o = a.part_ml + slots * 2;
     switch (p.cache.head_dim) {
-        case 64: return launch_both<64>(a, num_sms, stream);
-        case 128: return launch_both<128>(a, num_sms, stream);
-        default: return launch_both<256>(a, num_sms, stream);
+        case 64: return launch_both<64>(a, p.max_q_len, num_sms, stream);
+        case 128: return launch_both<128>(a, p.max_q_len, num_sms, stream);
+        default: return launch_both<256>(a, p.max_q_len, num_sms, stream);
     }
 }
 

@@ -705,3 +705,19 @@ def test_kept_workspace_grows_on_a_stream_that_is_passed(fp8act):
     junk = [torch.full((512,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
     side.synchronize()
     assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w)) and len(junk) == 8
+
+
+@pytest.mark.parametrize("n", [1, 2, 4, 9, 30])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_one_long_context_and_short_ones(fp8act, D, n):
+    """Items of tens of parts, joined by several warps a row, next to items of one part and to empty sequences."""
+    lens, ns = [9000, 0, 33, 700], [n, 0, 1, 2]
+    cache, table = make_cache(fp8act, lens, 2, D, 64, seed=61)
+    q = randn(sum(ns), 2 * 6, D, seed=62)
+    attend_and_check(fp8act, q, cache, table, lens, ns)
+    # fewer tokens announced than a sequence has: other row tiles, the same attention
+    attend_and_check(fp8act, q, cache, table, lens, ns, max_q_len=max(1, n // 3))
+    one, table = make_cache(fp8act, [20000], 1, D, 64, seed=63)
+    q = randn(n, 6, D, seed=64)
+    attend_and_check(fp8act, q, one, table, [20000], [n])
+    attend_and_check(fp8act, q, one, table, [20000], [n], max_q_len=1)
