@@ -30,14 +30,15 @@
 // of the warp-level MMAs), 16 rows of the warp at a time: with a row per thread
 // every thread read all 128 key scales from shared memory, a third of what moves
 // there in all (16 tokens x 6 heads over 131072: 81.7 us, now 62.0; 512 over
-// 16384: 135.7, now 122.8, with the queries' way through shared memory below).
+// 16384: 135.7 and 122.8, with the queries' way through shared memory below; now
+// 60.0 and 117.6 with a faster join).
 // The two passes of 16 rows are a loop: the hot code of the roles that share an
 // instruction cache stays small.
 //
 // What bounds it: the chain of a score tile, 128 rows x 128 tokens, of about 4900
 // clocks: S 520 clocks, softmax 2500, weights through tensor memory, P V 520, and
 // the waits between. Two such chains keep the tensor cores half busy (512 tokens
-// x 24 heads over 16384: 826 TFLOP/s, S counted once); there is no
+// x 24 heads over 16384: 863 TFLOP/s, S counted once); there is no
 // room for a third, whose scores would take the columns of an output, and score
 // tiles of 64 tokens do not help, since an MMA 64 columns wide takes longer than
 // one of 128 (104 clocks against 64). Measured and slower: the softmax on 16
