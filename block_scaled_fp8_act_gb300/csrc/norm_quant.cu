@@ -4,8 +4,9 @@
 //   norm: h = x + residual (stored as bf16), y = h / sqrt(mean h^2 + eps) * (weight + offset)
 //   silu: y = gate / (1 + exp(-gate)) * up
 // Both read and write each value once, so memory bounds them: 4096 x 5120 with
-// residual moves 147 MB in 26.2 us (5.6 TB/s, 0.83 of a copy's rate), 4096 x
-// 8704 gates 179 MB in 30.0 us (6.0 TB/s, 0.88). One row takes 1.8 us, a launch
+// residual moves 147 MB in 25.9 us (5.7 TB/s, 0.84 of a copy's rate), 4096 x
+// 8704 gates 179 MB in 29.3 us (6.1 TB/s, 0.90; loads that pass L1 by: 26.2 and
+// 30.0). One row takes 1.8 us, a launch
 // with one trip to memory and the row's reductions. The sum of squares is fp32.
 // Arithmetic goes in pairs and the scale and its reciprocal without divisions:
 // at 250 instructions per 8 columns issue slots were 72 % busy (27.4 us).
@@ -44,10 +45,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint4* x, con
     for (int i = 0; i < kChunks; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         const bool in = c < chunks;
-        unpack_bf16x8(in ? ld_dep_stream_v4(x + c) : make_uint4(0, 0, 0, 0), h[i]);
+        unpack_bf16x8(in ? ld_dep_v4(x + c) : make_uint4(0, 0, 0, 0), h[i]);
         if (kResidual) {
             float2 r[4];
-            unpack_bf16x8(in ? ld_dep_stream_v4(residual + c) : make_uint4(0, 0, 0, 0), r);
+            unpack_bf16x8(in ? ld_dep_v4(residual + c) : make_uint4(0, 0, 0, 0), r);
 #pragma unroll
             for (int j = 0; j < 4; ++j) h[i][j] = __fadd2_rn(h[i][j], r[j]);
             if (in) residual_out[c] = pack_bf16x8(h[i]);
@@ -102,8 +103,8 @@ __global__ void __launch_bounds__(256) silu_mul_quant_kernel(const uint4* gate_u
         const int g = pair * 2 + (lane >> 4);
         const bool in = item < items && g < groups;
         const uint4* p = gate_up + row * groups * 32 + g * 16 + hl;
-        va = in ? ld_dep_stream_v4(p) : make_uint4(0, 0, 0, 0);
-        vb = in ? ld_dep_stream_v4(p + groups * 16) : make_uint4(0, 0, 0, 0);
+        va = in ? ld_dep_v4(p) : make_uint4(0, 0, 0, 0);
+        vb = in ? ld_dep_v4(p + groups * 16) : make_uint4(0, 0, 0, 0);
     };
     load();
     while (item < items) {
@@ -154,7 +155,7 @@ cudaError_t launch_rmsnorm_quant(const void* x, const void* residual, const void
                                  int num_sms, cudaStream_t stream) {
     const int chunks = K / 8;
     // One chunk per thread wherever a CTA holds the row: 4096 x 5120 with residual took 27.4 us so, with 2 or 4 chunks
-    // per thread 28.9 or 32.5. (CTAs that stay and request the next row early: 26.7 to 31, now 26.2 with a CTA a row.)
+    // per thread 28.9 or 32.5. (CTAs that stay and request the next row early: 26.7 to 31, then 26.2 with a CTA a row.)
     if (chunks <= 1024)
         return launch_norm<1>(x, residual, weight, eps, weight_offset, M, chunks, q, sa, residual_out, stream);
     return launch_norm<4>(x, residual, weight, eps, weight_offset, M, chunks, q, sa, residual_out, stream);
@@ -165,7 +166,7 @@ cudaError_t launch_silu_mul_quant(const void* gate_up, int M, int I, void* q, fl
     const int groups = I / kGroup;
     const int64_t warps = static_cast<int64_t>(M) * ((groups + 1) / 2);
     int64_t blocks = (warps + 7) / 8;
-    // No more CTAs than run at once: 4096 x 8704 takes 30.0 us, with 8 per SM, a third of them in a second wave, 34.4,
+    // No more CTAs than run at once: 4096 x 8704 took 30.0 us, with 8 per SM, a third of them in a second wave, 34.4,
     // with 8 at 32 registers (spills) 33.6.
     if (blocks > kSiluCtas * static_cast<int64_t>(num_sms)) blocks = kSiluCtas * static_cast<int64_t>(num_sms);
     return launch_dependent(silu_mul_quant_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 1,
