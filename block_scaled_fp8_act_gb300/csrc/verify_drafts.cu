@@ -364,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyPr
                 }
                 if (w > 0.0f) better(best, __fdividef(w, e), i);
             };
-            if (V % 8 == 0) {  // every row starts on a 16-byte boundary
+            // Logit rows start on 16-byte boundaries if V is a multiple of 8; the caller's noise may start on any 4-byte one.
+            if (V % 8 == 0 && (reinterpret_cast<uintptr_t>(noise) & 15) == 0) {
                 const int n8 = V / 8;
                 const int v0 = static_cast<int>(static_cast<int64_t>(n8) * rank / cluster);
                 const int v1 = static_cast<int>(static_cast<int64_t>(n8) * (rank + 1) / cluster);

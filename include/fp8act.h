@@ -350,10 +350,12 @@ FP8ACT_API size_t fp8_kv_attention_workspace(int max_q_len, int q_heads, const f
  * draft is accepted if it is that token, and noise is not read.
  * A logit of -infinity or NaN is masked (+infinity is none); a row with nothing left accepts no
  * draft and draws token -1.
- *   target       [B, k + 1, V] bf16 (fp32 with logits_f32), contiguous
+ *   target       [B, k + 1, V] bf16 (fp32 with logits_f32), contiguous, as draft
+ *                16-byte aligned
  *   draft        [B, k, V] of the same type, or NULL
  *   draft_tokens [B, k] int32; uniform [B, k] fp32 in [0, 1)
- *   noise        [B, V] fp32, positive; temperature [B] fp32
+ *   noise        [B, V] fp32, positive, 4-byte aligned (read faster from a
+ *                16-byte boundary); temperature [B] fp32
  *   n_draft      [B] int32 drafts of each sequence, 0 .. k, or NULL for k
  *   accepted     [B] int32 out: a
  *   tokens       [B, k + 1] int32 out: the a accepted drafts, the drawn token, -1s
