@@ -18,13 +18,15 @@
 // both took 20.5 us for 7 drafts at one sequence, where 16 SMs read 4.6 MB,
 // and 53 us for 34 x 2 drafts.)
 //
-// Measured over 151936 bf16 logits: 26.0 us for 34 sequences of 2 drafts (72 MB read once, 2.8 TB/s; 10.7 us at the
-// rate of a copy) and 10.3 us for one sequence of 7 (0.8). What bounds it: the first kernel, about half of the time, by
+// Measured over 151936 bf16 logits: 27.2 us for 34 sequences of 2 drafts (72 MB read once, 2.7 TB/s; 10.7 us at the
+// rate of a copy) and 11.3 us for one sequence of 7 (0.8). What bounds it: the first kernel, about half of the time, by
 // issue (an exponential, a widening and a maximum per logit: 2.6 of 4 instructions a clock); the second, and a single
 // sequence, by the chain of dependent latencies: statistics, acceptance, the row drawn from, the cluster's meeting.
 // Widening and adding in pairs (packed maximum, fp32 pairs) took 0.8 us off the first.
-// The first starts the second after its own wait, so that the second reads the drafts' tokens, numbers and logits while
-// the first still runs (0.6-1.1 us).
+// The second reads nothing before its own wait, which alone makes what earlier kernels wrote visible to it; so that its
+// acceptance is still one trip to memory, the first notes the drafted token's logit in the record of a row's first part.
+// (Inputs read while the first still ran took 0.7 to 1.1 us less, on the ground that their writers have ended; but
+// only the wait orders what they wrote before a read here.)
 #include <atomic>
 
 #include "decoder_util.cuh"
@@ -50,6 +52,12 @@ struct Stat {
     float m, s;
     int at;
 };
+// What the first kernel leaves of a part of a row; `drafted`: the row's logit at the token drafted there (in part 0).
+struct __align__(16) Part {
+    Stat st;
+    float drafted;
+};
+static_assert(sizeof(Part) == 16, "one load");
 
 __device__ __forceinline__ float clean(float v) { return fmaxf(v, kNegInf); }  // NaN counts as masked
 
@@ -154,7 +162,7 @@ struct Sequence {
 
 // Maximum and sum of part x of row y of sequence z.
 template <bool kF32>
-__global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const VerifyProblem p, Stat* parts) {
+__global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const VerifyProblem p, Part* parts) {
     using R = Row<kF32>;
     __shared__ Stat part[kStatWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -165,7 +173,7 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const Verify
     const int v0 = static_cast<int>(static_cast<int64_t>(vecs) * share / shares);
     const int v1 = static_cast<int>(static_cast<int64_t>(vecs) * (share + 1) / shares);
     ptx::griddep_wait();
-    ptx::griddep_launch_dependents();  // (after the wait: the second kernel reads inputs before its own)
+    ptx::griddep_launch_dependents();
     q.read_temperature(p, blockIdx.z);
     Stat st = {kNegInf, 0.0f, 0x7FFFFFFF};
     auto one = [&](int i) {
@@ -184,6 +192,12 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const Verify
     const int first = v0 + static_cast<int>(threadIdx.x);
     float2 sum = make_float2(st.s, 0.0f);
     request(first, raw);
+    float drafted = kNegInf;
+    const int draft_row = static_cast<int>(blockIdx.y) - (static_cast<int>(blockIdx.y) < q.targets ? 0 : q.targets);
+    if (share == 0 && threadIdx.x == 0 && draft_row < p.k) {
+        const int x = ld_dep_s32(p.draft_tokens + static_cast<int64_t>(blockIdx.z) * p.k + draft_row);
+        if (x >= 0 && x < p.V) drafted = row.at(x);
+    }
     for (int v = first; v < v1; v += kStatThreads * kAhead) {
         uint4 next[kAhead];
         request(v + kStatThreads * kAhead, next);
@@ -229,14 +243,15 @@ __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(const Verify
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int i = 1; i < kStatWarps; ++i) join(st, part[i], q.c);
-        parts[(static_cast<int64_t>(blockIdx.z) * q.rows + blockIdx.y) * shares + share] = st;
+        parts[(static_cast<int64_t>(blockIdx.z) * q.rows + blockIdx.y) * shares + share] = {st, drafted};
     }
 }
 
 struct VerifyShared {
     Stat row[kMaxRows];
+    float drafted[kMaxRows];
     float prob[kMaxDrafts];
-    int taken;
+    int taken, n;
     Best warp_best[kWarps];
     Best best[2];  // this CTA's best draw (read by the cluster); one slot per pass
     Best all;
@@ -251,7 +266,7 @@ __device__ __forceinline__ Best ld_cluster_best(const Best* p, uint32_t rank) {
 }
 
 template <bool kF32>
-__global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyProblem p, const Stat* parts, int cluster,
+__global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyProblem p, const Part* parts, int cluster,
                                                                int shares) {
     using R = Row<kF32>;
     __shared__ VerifyShared sh;
@@ -265,39 +280,28 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyPr
     const int i0 = static_cast<int>(static_cast<int64_t>(V) * rank / cluster);
     const int i1 = static_cast<int>(static_cast<int64_t>(V) * (rank + 1) / cluster);
     ptx::griddep_launch_dependents();
-    // The inputs are complete, since the first kernel starts this one after its own wait: only what it wrote is waited for.
+    ptx::griddep_wait();
     q.read_temperature(p, b);
     const float c = q.c;
-    const bool greedy = q.greedy, draft = p.draft != nullptr;
+    const bool greedy = q.greedy;
+    const bool draft = p.draft != nullptr;
     auto row_of = [&](int r) { return q.row(r); };
     int n = p.n_draft ? ld_dep_s32(p.n_draft + b) : k;
-    if (n < 0 || n > k) {
-        if (threadIdx.x == 0) atomicOr(&g_verify_index_error, 1u);
-        n = n < 0 ? 0 : k;
-    }
-    // Warp 0's lane j holds draft j and what its acceptance needs, requested together with the row statistics.
-    int x = 0;
-    float u = 1.0f, lt = kNegInf, ld = kNegInf;
-    bool there = false;
+    // Warp 0's lane j holds draft j and its number, requested together with the row statistics and looked at after them.
+    int x = -1;
+    float u = 1.0f;
     if (warp == 0 && lane < k) {
         x = ld_dep_s32(p.draft_tokens + static_cast<int64_t>(b) * k + lane);
         u = ld_dep_f32(p.uniform + static_cast<int64_t>(b) * k + lane);
-        there = x >= 0 && x < V;
-        if (there) {
-            lt = row_of(lane).at(x);
-            if (draft) ld = row_of(targets + lane).at(x);
-        } else if (lane < n && rank == 0) {
-            atomicOr(&g_verify_index_error, 1u);
-        }
     }
-    ptx::griddep_wait();
     for (int r = warp; r < q.rows; r += kWarps) {  // a warp per row, a lane per part
-        const Stat* from = parts + (static_cast<int64_t>(b) * q.rows + r) * shares + lane;
+        const Part* from = parts + (static_cast<int64_t>(b) * q.rows + r) * shares + lane;
         Stat st = {kNegInf, 0.0f, 0x7FFFFFFF};
+        float drafted = kNegInf;
         if (lane < shares) {
-            st.m = __ldcg(&from->m);
-            st.s = __ldcg(&from->s);
-            st.at = __ldcg(&from->at);
+            const uint4 v = ld_dep_v4(from);
+            st = {__uint_as_float(v.x), __uint_as_float(v.y), static_cast<int>(v.z)};
+            drafted = __uint_as_float(v.w);
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) {
@@ -307,23 +311,33 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyPr
             other.at = __shfl_xor_sync(0xffffffffu, st.at, o);
             join(st, other, c);
         }
-        if (lane == 0) sh.row[r] = st;
+        if (lane == 0) {
+            sh.row[r] = st;
+            sh.drafted[r] = drafted;
+        }
+    }
+    if (threadIdx.x == 0) {
+        if (n < 0 || n > k) atomicOr(&g_verify_index_error, 1u);
+        sh.n = min(max(n, 0), k);
     }
     __syncthreads();
 
     // Acceptance, decided alike in every CTA.
     if (warp == 0) {
+        const bool there = x >= 0 && x < V;
+        n = sh.n;
+        if (!there && lane < n && rank == 0) atomicOr(&g_verify_index_error, 1u);
         float prob = 0.0f;
         if (there && lane < n) {
             const Stat st = sh.row[lane];
             if (greedy) {
                 prob = st.m > kNegInf && st.at == x ? 1.0f : 0.0f;
             } else {
-                const float px = st.s > 0.0f ? __fdiv_rn(exp_below(lt, st.m, c), st.s) : 0.0f;
+                const float px = st.s > 0.0f ? __fdiv_rn(exp_below(sh.drafted[lane], st.m, c), st.s) : 0.0f;
                 float qx = 1.0f;
                 if (draft) {
                     const Stat sd = sh.row[targets + lane];
-                    qx = sd.s > 0.0f ? __fdiv_rn(exp_below(ld, sd.m, c), sd.s) : 0.0f;
+                    qx = sd.s > 0.0f ? __fdiv_rn(exp_below(sh.drafted[targets + lane], sd.m, c), sd.s) : 0.0f;
                 }
                 prob = qx > 0.0f ? fminf(__fdiv_rn(px, qx), 1.0f) : px > 0.0f ? 1.0f : 0.0f;
             }
@@ -338,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyPr
     // Pass 2: the draw. `rest` draws from max(p - q, 0), else from p.
     const Stat st = sh.row[taken];
     int token = -1;
-    bool rest = taken < n && !greedy;
+    bool rest = taken < sh.n && !greedy;
     if (greedy) {
         if (st.m > kNegInf) token = st.at;
     } else if (st.s > 0.0f) {
@@ -461,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_draw_kernel(const VerifyPr
 }  // namespace
 
 size_t verify_drafts_workspace(int B, int k) {
-    return static_cast<size_t>(B < 1 ? 1 : B) * (2 * k + 1) * kMaxParts * sizeof(Stat);
+    return static_cast<size_t>(B < 1 ? 1 : B) * (2 * k + 1) * kMaxParts * sizeof(Part);
 }
 
 cudaError_t launch_verify_drafts(const VerifyProblem& p, int num_sms, cudaStream_t stream) {
@@ -476,7 +490,7 @@ cudaError_t launch_verify_drafts(const VerifyProblem& p, int num_sms, cudaStream
     // CTAs of a sequence in the second: as many as stay within two per SM, of 2048 logits at least.
     int cluster = kMaxCluster;
     while (cluster > 1 && (p.V < 2048 * cluster || static_cast<int64_t>(p.B) * cluster > 2 * num_sms)) cluster /= 2;
-    Stat* parts = static_cast<Stat*>(p.workspace);
+    Part* parts = static_cast<Part*>(p.workspace);
     auto draw = p.f32 ? verify_draw_kernel<true> : verify_draw_kernel<false>;
     static std::atomic<bool> configured[2][64];
     int dev = 0;

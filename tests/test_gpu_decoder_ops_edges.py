@@ -29,3 +29,30 @@ def test_verify_noise_at_any_offset(fp8act, V, dtype):  # noqa: F811
             got = check_verify(fp8act, t, draft, x, u, view, temp)
             if draft is not None:
                 assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_verify_right_behind_the_writers_of_its_small_inputs(fp8act):  # noqa: F811
+    """Tokens, numbers, temperatures, counts and noise are written just before, step after step without a pause."""
+    B, k, V = 3, 4, 5000
+    steps = []
+    for i in range(3):
+        t, d, x, u, e = drafts(B, k, V, seed=100 + i, err=0.2)
+        temp = torch.tensor([1.0, 0.0, 0.5], device="cuda").roll(i)
+        n = torch.tensor([k, 2, 3], dtype=torch.int32, device="cuda").roll(i)
+        steps.append((t, d, x, u * 0.5, e, temp, n))
+    now = [torch.empty_like(a) for a in steps[0]]
+
+    def step(i, pause):
+        for dst, src in zip(now, steps[i]):
+            dst.copy_(src)
+        if pause:
+            torch.cuda.synchronize()
+        return fp8act.verify_drafts(now[0], now[2], now[3], now[4], now[5], draft_logits=now[1], n_draft=now[6])
+
+    want = [step(i, True) for i in range(3)]
+    for w, (t, d, x, u, e, temp, n) in zip(want, steps):
+        got = check_verify(fp8act, t, d, x, u, e, temp, n)
+        assert all(torch.equal(a, b) for a, b in zip(got, w))
+    got = [step(i % 3, False) for i in range(60)]
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 3]))
