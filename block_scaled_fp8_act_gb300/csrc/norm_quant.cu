@@ -33,13 +33,13 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(const uint4* x, con
         residual_out += row * chunks;
     }
     ptx::griddep_launch_dependents();
-    uint4 wv[kChunks];  // the weight is constant: read while the previous kernel ends
+    ptx::griddep_wait();
+    uint4 wv[kChunks];  // (after the wait too: a weight may be a cast or a sum made just before)
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
-        wv[i] = c < chunks ? __ldg(weight + c) : make_uint4(0, 0, 0, 0);
+        wv[i] = c < chunks ? ld_dep_v4(weight + c) : make_uint4(0, 0, 0, 0);
     }
-    ptx::griddep_wait();
     float2 h[kChunks][4], ss2 = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {

@@ -244,8 +244,8 @@ FP8ACT_API int fp8_block_gemm_grouped_f32(const fp8act_gemm_problem* problems, i
  *   fp8_block_gemm (gate, up) -> fp8_silu_mul_quant -> fp8_block_gemm,
  * and after the vocabulary head fp8act_verify_drafts. They follow the
  * conventions above (device pointers, no allocation, capturable, launched with
- * programmatic dependent launch; every input but fp8_rmsnorm_quant's weight
- * is read after the previous kernel on the stream has completed).
+ * programmatic dependent launch; every input is read after the previous kernel
+ * on the stream has completed, fp8_rmsnorm_quant's weight too).
  * Index arrays live on the device, so the library checks them there: an index
  * out of range is never followed, and is reported by fp8act_check_status() as
  * FP8ACT_ERR_INDEX.

@@ -5,7 +5,7 @@ from __future__ import annotations
 
 import pytest
 import torch
-from test_gpu_decoder_ops import check_verify, clean_status, drafts, fp8act, gen  # noqa: F401  (fixtures among them)
+from test_gpu_decoder_ops import check_verify, clean_status, drafts, fp8act, gen, randn  # noqa: F401  (fixtures too)
 
 pytestmark = pytest.mark.gpu
 
@@ -54,5 +54,24 @@ def test_verify_right_behind_the_writers_of_its_small_inputs(fp8act):  # noqa: F
         got = check_verify(fp8act, t, d, x, u, e, temp, n)
         assert all(torch.equal(a, b) for a, b in zip(got, w))
     got = [step(i % 3, False) for i in range(60)]
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 3]))
+
+
+# ------------------------------------------------------------------- norm
+@pytest.mark.parametrize("M,K", [(1, 5120), (300, 1152), (2, 16384)])
+def test_rmsnorm_right_behind_the_writer_of_its_weight(fp8act, M, K):  # noqa: F811
+    """The weight may be a cast just made, with one of the library's own kernels between or none."""
+    x = randn(M, K, seed=1)
+    weights = [randn(K, seed=10 + i).float() for i in range(3)]
+    want = [fp8act.fp8_rmsnorm_quant(x, w.bfloat16()) for w in weights]
+    torch.cuda.synchronize()
+    w = torch.empty(K, dtype=torch.bfloat16, device="cuda")
+    got = []
+    for i in range(60):
+        w.copy_(weights[i % 3])
+        if i & 1:
+            fp8act.fp8_act_quant(x)  # lets the kernel behind it start at once
+        got.append(fp8act.fp8_rmsnorm_quant(x, w))
     for i, g in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(g, want[i % 3]))
