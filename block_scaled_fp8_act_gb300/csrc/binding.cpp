@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <cuda_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -65,11 +66,6 @@ T* optional(PyObject* o, at::ScalarType a, at::IntArrayRef shape, const char* na
     return given(o) ? data<T>(o, a, shape, name) : nullptr;
 }
 
-// An output: the caller's tensor, or a new one.
-at::Tensor output(PyObject* o, at::ScalarType kind, at::IntArrayRef shape, const at::Tensor& like, const char* name) {
-    return given(o) ? tensor(o, name) : at::empty(shape, like.options().dtype(kind));
-}
-
 // A bf16 [M, K] tensor of any M and K.
 const at::Tensor& matrix(PyObject* o, const char* name) {
     const at::Tensor& t = tensor(o, name);
@@ -110,11 +106,40 @@ PyObject* tuple(const std::array<at::Tensor, kN>& v, size_t n = kN) {
     return t;
 }
 
-// Memory that is let go here may still be in use on `stream`; if it came from another stream's pool, that one must not
-// hand it out again before.
-void let_go(const at::Tensor& t, cudaStream_t stream) {
-    if (t.defined() && stream != c10::cuda::getCurrentCUDAStream(t.get_device()).stream())
-        t.record_stream(c10::cuda::getStreamFromExternal(stream, t.get_device()).unwrap());
+// The graph capture that `stream` takes part in, 0 for none.
+unsigned long long capture_of(cudaStream_t stream) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (stream && cudaStreamGetCaptureInfo(stream, &status, &id) != cudaSuccess) {  // (the legacy stream cannot be captured)
+        cudaGetLastError();
+        return 0;
+    }
+    return status == cudaStreamCaptureStatusNone ? 0 : id;
+}
+
+// Uninitialised memory for a kernel on `stream`, from that stream's own pool whatever torch's current one is: what used
+// it before has ended when the kernel starts, and once let go it is handed out again behind the kernel. In a graph the
+// pool is the graph's, which torch knows for its own captures; a capture that the current stream has no part in may not
+// be one, and its replays would outlive the memory.
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType kind, const at::Tensor& like, cudaStream_t stream) {
+    const auto options = like.options().dtype(kind);
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(like.get_device());
+    if (current.stream() == stream) return at::empty(shape, options);
+    const unsigned long long capture = capture_of(stream);
+    if (capture && capture != capture_of(current.stream()))
+        raise(PyExc_ValueError, "a call captured on a stream that is not torch's current one needs its outputs and workspace");
+    const c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(stream, like.get_device()));
+    return at::empty(shape, options);
+}
+
+// An output: the caller's tensor, or a new one, which the caller reads on the current stream.
+at::Tensor output(PyObject* o, at::ScalarType kind, at::IntArrayRef shape, const at::Tensor& like, cudaStream_t stream,
+                  const char* name) {
+    if (given(o)) return tensor(o, name);
+    at::Tensor t = fresh(shape, kind, like, stream);
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(like.get_device());
+    if (current.stream() != stream) t.record_stream(current.unwrap());
+    return t;
 }
 
 // A workspace: the caller's, or one kept per device and stream (calls of one stream share it; a graph being captured
@@ -131,20 +156,14 @@ Workspace workspace(PyObject* o, size_t need, const at::Tensor& like, cudaStream
         return {t, t.data_ptr(), static_cast<size_t>(t.nbytes())};
     }
     if (need < 16) need = 16;
-    const auto fresh = [&] { return at::empty({static_cast<int64_t>(need)}, like.options().dtype(kU8)); };
-    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-    if (stream && cudaStreamIsCapturing(stream, &capturing) != cudaSuccess) cudaGetLastError();
-    if (capturing != cudaStreamCaptureStatusNone) {
-        at::Tensor t = fresh();
-        let_go(t, stream);  // (after the call)
+    const auto make = [&] { return fresh({static_cast<int64_t>(need)}, kU8, like, stream); };
+    if (capture_of(stream)) {
+        at::Tensor t = make();
         return {t, t.data_ptr(), need};
     }
     static auto* kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>;  // outlives the CUDA context
     at::Tensor& t = (*kept)[{like.get_device(), stream}];
-    if (!t.defined() || t.nbytes() < need) {
-        let_go(t, stream);
-        t = fresh();
-    }
+    if (!t.defined() || t.nbytes() < need) t = make();
     return {t, t.data_ptr(), static_cast<size_t>(t.nbytes())};
 }
 
@@ -195,21 +214,22 @@ PyObject* rmsnorm_quant(PyObject* const* a) {
     const void* w = data(a[1], kBf16, {K}, "weight");
     const double eps = PyFloat_AsDouble(a[3]), offset = PyFloat_AsDouble(a[4]);
     if (PyErr_Occurred()) throw Raised{};
-    at::Tensor q = output(a[5], kU8, {M, K}, x, "q"), sa = output(a[6], kF32, {M, K / 128}, x, "sa"), out;
+    cudaStream_t stream = stream_of(a[8]);
+    at::Tensor q = output(a[5], kU8, {M, K}, x, stream, "q"), sa = output(a[6], kF32, {M, K / 128}, x, stream, "sa"), out;
     void* qp = data<void>(q, kU8, kE4m3, {M, K}, "q");
     float* sp = data<float>(sa, kF32, {M, K / 128}, "sa");
     const void* r = nullptr;
     void* op = nullptr;
     if (given(a[2])) {
         r = data(a[2], kBf16, {M, K}, "residual");
-        out = output(a[7], kBf16, {M, K}, x, "residual_out");
+        out = output(a[7], kBf16, {M, K}, x, stream, "residual_out");
         op = data(out, kBf16, {M, K}, "residual_out");
     } else if (given(a[7])) {
         raise(PyExc_ValueError, "residual_out without a residual");
     }
     check("fp8_rmsnorm_quant",
           fp8_rmsnorm_quant(x.data_ptr(), r, w, static_cast<float>(eps), static_cast<float>(offset), to_int(M, "M"),
-                            to_int(K, "K"), qp, sp, op, stream_of(a[8])));
+                            to_int(K, "K"), qp, sp, op, stream));
     return tuple<3>({q, sa, out}, given(a[2]) ? 3 : 2);
 }
 
@@ -218,11 +238,12 @@ PyObject* silu_mul_quant(PyObject* const* a) {
     const at::Tensor& x = matrix(a[0], "gate_up");
     if (x.size(1) % 2) raise(PyExc_ValueError, "gate_up must have an even number of columns");
     const int64_t M = x.size(0), I = x.size(1) / 2;
-    at::Tensor q = output(a[1], kU8, {M, I}, x, "q"), sa = output(a[2], kF32, {M, I / 128}, x, "sa");
+    cudaStream_t stream = stream_of(a[3]);
+    at::Tensor q = output(a[1], kU8, {M, I}, x, stream, "q"), sa = output(a[2], kF32, {M, I / 128}, x, stream, "sa");
     void* qp = data<void>(q, kU8, kE4m3, {M, I}, "q");
     float* sp = data<float>(sa, kF32, {M, I / 128}, "sa");
     check("fp8_silu_mul_quant",
-          fp8_silu_mul_quant(x.data_ptr(), to_int(M, "M"), to_int(I, "I"), qp, sp, stream_of(a[3])));
+          fp8_silu_mul_quant(x.data_ptr(), to_int(M, "M"), to_int(I, "I"), qp, sp, stream));
     return tuple<2>({q, sa});
 }
 
@@ -251,10 +272,10 @@ PyObject* kv_attention(PyObject* const* a) {
     const int64_t most = given(a[5]) ? PyLong_AsLongLong(a[5]) : T == B ? 1 : T;
     const double scale = given(a[6]) ? PyFloat_AsDouble(a[6]) : 1.0 / std::sqrt(static_cast<double>(c.head_dim));
     if (PyErr_Occurred()) throw Raised{};
-    at::Tensor out = output(a[7], kBf16, {T, Hq, c.head_dim}, q, "out");
+    cudaStream_t stream = stream_of(a[10]);
+    at::Tensor out = output(a[7], kBf16, {T, Hq, c.head_dim}, q, stream, "out");
     void* op = data(out, kBf16, {T, Hq, c.head_dim}, "out");
     float* lse = optional<float>(a[8], kF32, {T, Hq}, "lse");
-    cudaStream_t stream = stream_of(a[10]);
     const int max_q = to_int(most, "max_q_len"), hq = to_int(Hq, "q_heads");
     const Workspace w = workspace(a[9], fp8_kv_attention_workspace(max_q, hq, &c), q, stream);
     check("fp8_kv_attention", fp8_kv_attention(q.data_ptr(), qs, cu, lens, tp, to_int(pages, "max_pages"), to_int(B, "B"),
@@ -277,12 +298,13 @@ PyObject* verify_drafts(PyObject* const* a) {
     const float* e = data<float>(a[3], kF32, {B, V}, "noise");
     const float* temp = data<float>(a[4], kF32, {B}, "temperature");
     const int* n = optional<int>(a[6], kI32, {B}, "n_draft");
-    at::Tensor took = output(a[7], kI32, {B}, t, "accepted"), tokens = output(a[8], kI32, {B, rows}, t, "tokens"),
-               prob = output(a[9], kF32, {B, k}, t, "accept_prob");
+    cudaStream_t stream = stream_of(a[11]);
+    at::Tensor took = output(a[7], kI32, {B}, t, stream, "accepted"),
+               tokens = output(a[8], kI32, {B, rows}, t, stream, "tokens"),
+               prob = output(a[9], kF32, {B, k}, t, stream, "accept_prob");
     int* ap = data<int>(took, kI32, {B}, "accepted");
     int* op = data<int>(tokens, kI32, {B, rows}, "tokens");
     float* pp = data<float>(prob, kF32, {B, k}, "accept_prob");
-    cudaStream_t stream = stream_of(a[11]);
     const int b = to_int(B, "B"), kk = to_int(k, "k");
     const Workspace w = workspace(a[10], fp8act_verify_drafts_workspace(b, kk), t, stream);
     check("fp8act_verify_drafts", fp8act_verify_drafts(tp, dp, kind == kF32, x, u, e, temp, n, b, kk, to_int(V, "V"), ap, op,

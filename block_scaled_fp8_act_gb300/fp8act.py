@@ -10,6 +10,12 @@ passes raw device pointers, sizes and the current CUDA stream to the C entry
 point of the same name (include/fp8act.h) and raises Fp8ActError on a
 non-zero status. All arithmetic runs in the library's CUDA kernels; there is
 no fallback: if the library is not built, loading it raises.
+
+With a `stream` that is not torch's current one, what an operator between the
+layers makes itself (outputs, a workspace) comes from that stream's memory
+pool; the outputs may be read and dropped on the current stream once it has
+waited for the other. In a graph captured on a stream that is not the current
+one they have to be brought (ValueError).
 """
 from __future__ import annotations
 

@@ -75,3 +75,171 @@ def test_rmsnorm_right_behind_the_writer_of_its_weight(fp8act, M, K):  # noqa: F
         got.append(fp8act.fp8_rmsnorm_quant(x, w))
     for i, g in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(g, want[i % 3]))
+
+
+# ---------------------------------------------------------------- streams
+def segment_stream(t):
+    """The stream whose memory pool holds `t`."""
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("not in any segment")
+
+
+def allocated(stream):
+    return sum(s["allocated_size"] for s in torch.cuda.memory_snapshot() if s["stream"] == stream)
+
+
+def busy(x, n):
+    """Some milliseconds of work on the current stream."""
+    for _ in range(n):
+        x = torch.tanh(x)
+    return x
+
+
+def verify_problem(B, k, V, seed):
+    t, d, x, u, e = drafts(B, k, V, seed=seed)
+    return (t, x, u, e, torch.ones(B, device="cuda")), d
+
+
+def test_memory_made_for_a_passed_stream_is_from_its_pool(fp8act):  # noqa: F811
+    side = torch.cuda.Stream()
+    x, w = randn(3, 640, seed=1), randn(640, seed=2)
+    cache = fp8act.kv_cache(2, 1, 16, 64)
+    q = randn(1, 2, 64, seed=3)
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    lens = torch.ones(1, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    args, draft = verify_problem(2, 2, 1000, 4)
+    torch.cuda.synchronize()
+    calls = [lambda **kw: fp8act.fp8_rmsnorm_quant(x, w, x, **kw), lambda **kw: fp8act.fp8_silu_mul_quant(x[:, :512].contiguous(), **kw),
+             lambda **kw: (fp8act.fp8_kv_attention(q, cache, table, lens, cu, **kw),),
+             lambda **kw: fp8act.verify_drafts(*args, draft_logits=draft, **kw)]
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        for stream in (side, side.cuda_stream):
+            got = call(stream=stream)
+            assert all(segment_stream(t) == side.cuda_stream for t in got)
+            torch.cuda.current_stream().wait_stream(side)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(segment_stream(t) == torch.cuda.current_stream().cuda_stream for t in want)
+
+
+def test_kept_workspace_is_the_streams_own(fp8act):  # noqa: F811
+    """However the calls come, passed or current, a stream's workspace and its growth stay in that stream's pool."""
+    side = torch.cuda.Stream()
+    (small, ds), (large, dl) = verify_problem(1, 1, 3000, 1), verify_problem(60, 7, 3000, 2)
+    outs = [dict(accepted=torch.empty(B, dtype=torch.int32, device="cuda"),
+                 tokens=torch.empty((B, k + 1), dtype=torch.int32, device="cuda"),
+                 accept_prob=torch.empty((B, k), device="cuda")) for B, k in ((1, 1), (60, 7))]
+    main = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    before = allocated(main)
+    fp8act.verify_drafts(*small, draft_logits=ds, **outs[0], stream=side)
+    first = allocated(side.cuda_stream)
+    with torch.cuda.stream(side):
+        fp8act.verify_drafts(*large, draft_logits=dl, **outs[1])
+    second = allocated(side.cuda_stream)
+    side.synchronize()
+    assert allocated(main) == before
+    assert 0 < fp8act.verify_drafts_workspace(1, 1) <= first and fp8act.verify_drafts_workspace(60, 7) <= second
+
+
+def test_growth_under_the_stream_itself_while_it_works(fp8act):  # noqa: F811
+    """First call by a passed stream, second under it: the workspace that is let go must not reach another stream."""
+    side = torch.cuda.Stream()
+    (small, ds), (large, dl) = verify_problem(1, 1, 5000, 1), verify_problem(40, 7, 5000, 2)
+    want = fp8act.verify_drafts(*small, draft_logits=ds), fp8act.verify_drafts(*large, draft_logits=dl)
+    x = randn(4096, 4096, seed=3)
+    size = fp8act.verify_drafts_workspace(1, 1)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        held = busy(x, 200)
+    first = fp8act.verify_drafts(*small, draft_logits=ds, stream=side)
+    with torch.cuda.stream(side):
+        second = fp8act.verify_drafts(*large, draft_logits=dl)
+    junk = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g, w in zip((first, second), want) for a, b in zip(g, w))
+    assert len(junk) == 64 and held.shape == x.shape
+
+
+def test_memory_that_the_current_stream_still_uses(fp8act):  # noqa: F811
+    """Blocks freed on the current stream with writes to them still queued there are not what a passed stream gets."""
+    side = torch.cuda.Stream()
+    args, draft = verify_problem(9, 3, 5000, 5)
+    want = fp8act.verify_drafts(*args, draft_logits=draft)
+    x = randn(4096, 4096, seed=3)
+    sizes = [fp8act.verify_drafts_workspace(9, 3)] + [t.numel() * t.element_size() for t in want]
+    torch.cuda.synchronize()
+    held = busy(x, 200)
+    for _ in range(16):
+        for n in sizes:
+            torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # freed at once, written late
+    got = [fp8act.verify_drafts(*args, draft_logits=draft, stream=side) for _ in range(4)]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want)) and held.shape == x.shape
+
+
+def test_outputs_dropped_while_their_stream_works(fp8act):  # noqa: F811
+    side = torch.cuda.Stream()
+    args, draft = verify_problem(9, 3, 5000, 6)
+    want = fp8act.verify_drafts(*args, draft_logits=draft)
+    x = randn(4096, 4096, seed=3)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        held = busy(x, 200)
+    took, tokens, _ = fp8act.verify_drafts(*args, draft_logits=draft, stream=side)
+    junk = [torch.full((9, 3), 7.0, device="cuda") for _ in range(64)]
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(took, want[0]) and torch.equal(tokens, want[1])
+    assert all((j == 7).all() for j in junk) and held.shape == x.shape
+
+
+def test_capture_on_a_passed_stream(fp8act):  # noqa: F811
+    """In a capture that the current stream has no part in, outputs and workspace must be brought; then it replays."""
+    args, draft = verify_problem(3, 2, 2000, 7)
+    want = fp8act.verify_drafts(*args, draft_logits=draft)
+    outs = dict(zip(("accepted", "tokens", "accept_prob"), (torch.zeros_like(t) for t in want)))
+    ws = torch.empty(fp8act.verify_drafts_workspace(3, 2), dtype=torch.uint8, device="cuda")
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        with torch.cuda.stream(other):
+            with pytest.raises(ValueError):
+                fp8act.verify_drafts(*args, draft_logits=draft, stream=side)
+            with pytest.raises(ValueError):
+                fp8act.verify_drafts(*args, draft_logits=draft, **outs, stream=side)
+            fp8act.verify_drafts(*args, draft_logits=draft, **outs, workspace=ws, stream=side)
+    for _ in range(2):
+        for t in outs.values():
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs.values(), want))
+
+
+def test_fork_inside_a_capture(fp8act):  # noqa: F811
+    """A stream that joined torch's capture may be passed; the graph owns what the calls make."""
+    args, draft = verify_problem(3, 2, 2000, 8)
+    x, w = randn(5, 640, seed=1), randn(640, seed=2)
+    want = *fp8act.verify_drafts(*args, draft_logits=draft), *fp8act.fp8_rmsnorm_quant(x, w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = *fp8act.verify_drafts(*args, draft_logits=draft, stream=side), *fp8act.fp8_rmsnorm_quant(x, w, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        junk = [torch.full((1 << 12,), 255, dtype=torch.uint8, device="cuda") for _ in range(16)]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(junk) == 16
