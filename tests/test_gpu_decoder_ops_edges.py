@@ -5,7 +5,8 @@ from __future__ import annotations
 
 import pytest
 import torch
-from test_gpu_decoder_ops import check_verify, clean_status, drafts, fp8act, gen, randn  # noqa: F401  (fixtures too)
+from test_gpu_decoder_ops import (check_verify, clean_status, drafts, e4m3, fp8act, gen,  # noqa: F401  (fixtures too)
+                                  randn)
 
 pytestmark = pytest.mark.gpu
 
@@ -243,3 +244,28 @@ def test_fork_inside_a_capture(fp8act):  # noqa: F811
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(junk) == 16
+
+
+# ------------------------------------------------------------------- silu
+def test_silu_of_gates_with_a_large_exponential(fp8act):  # noqa: F811
+    """Down to where exp(-gate) overflows the gate's share is still a normal number, and a large `up` shows it.
+
+    An exponent of up to 128 is rounded by 2^-18 and the constant's error adds 2^-19, times ln 2: a relative error
+    below 2^-17 with the other roundings."""
+    gates = [-88.5, -88.0, -87.5, -87.0, -80.0, -60.0, -20.0]
+    x = torch.empty((len(gates), 256), device="cuda")
+    x[:, :128] = torch.tensor(gates, device="cuda").view(-1, 1)
+    x[:, 128:] = 2e38 * (2 * torch.rand((len(gates), 128), device="cuda", generator=gen(3)) - 1)
+    x[-1, 128:] *= 1e-10
+    x = x.bfloat16()
+    q, sa = fp8act.fp8_silu_mul_quant(x)
+    g, u = x.double().chunk(2, -1)
+    y = g * torch.sigmoid(g) * u
+    want = y.abs().amax(-1, keepdim=True) / 448.0
+    assert (want > 0.02).all() and ((sa.double() - want).abs() <= 2.0 ** -17 * want).all()
+    r, got = y / want, q.view(torch.float8_e4m3fn).double()
+    lo, hi = e4m3(r * (1 - 2.0 ** -16)), e4m3(r * (1 + 2.0 ** -16))
+    assert ((got >= torch.minimum(lo, hi)) & (got <= torch.maximum(lo, hi))).all()
+    x[:, :128] = -89.0  # exp(89) is infinite in fp32
+    q, sa = fp8act.fp8_silu_mul_quant(x)
+    assert (q & 0x7F == 0).all() and (sa == 1).all()
