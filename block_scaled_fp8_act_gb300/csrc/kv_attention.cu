@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
         // Queries: power-of-two scaled f16 in fragment order.
         {
             constexpr int kLanes = kD / 8;
+            static_assert(kLanes <= 32 && kRows % (32 / kLanes) == 0, "whole warps of rows");
             const int c = threadIdx.x % kLanes;
             for (int r = threadIdx.x / kLanes; r < kRows; r += S::kWarps * 32 / kLanes) {
                 uint4 x = make_uint4(0, 0, 0, 0);
@@ -261,9 +262,10 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
                     const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
                     x = ld_dep_v4(a.q + (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD + c * 8);
                 }
+                // (a warp's rows are all below kRows or none is, so that the whole warp is here)
                 uint32_t top = top_bits(x);
 #pragma unroll
-                for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(__activemask(), top, o));
+                for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                 // (a zero row's exponent is as good as any)
                 const uint32_t e = top == 0 ? 127 : min(max(top >> 7, 1u), 253u);
                 const float up = __uint_as_float((254 - e) << 23);  // 2^(127 - e)
