@@ -153,7 +153,9 @@ struct Sequence {
     __device__ __forceinline__ void read_temperature(const VerifyProblem& p, int b) {
         const float temp = ld_dep_f32(p.temperature + b);
         greedy = !(temp > 0.0f);
-        c = greedy ? 1.0f : 1.4426950408889634f / temp;
+        // Kept a positive normal number, so that its products with differences of logits, -inf among them, are none of
+        // them NaN: at an infinite temperature a masked logit stays masked, at a tiny one the largest keeps its 0.
+        c = greedy ? 1.0f : fminf(fmaxf(1.4426950408889634f / temp, 0x1p-126f), 0x1p126f);
     }
     __device__ __forceinline__ Row<kF32> row(int r) const {
         return {r < targets ? target + r * row_bytes : draft + (r - targets) * row_bytes, V};

@@ -269,3 +269,20 @@ def test_silu_of_gates_with_a_large_exponential(fp8act):  # noqa: F811
     x[:, :128] = -89.0  # exp(89) is infinite in fp32
     q, sa = fp8act.fp8_silu_mul_quant(x)
     assert (q & 0x7F == 0).all() and (sa == 1).all()
+
+
+# ---------------------------------------------- verification: temperatures
+@pytest.mark.parametrize("V", [4096, 5001])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_verify_ends_of_the_temperature_range(fp8act, V, dtype):  # noqa: F811
+    """An infinite temperature draws evenly from what is not masked, as a huge one does; a tiny one is nearly greedy."""
+    t, d, x, u, e = drafts(4, 3, V, seed=V, dtype=dtype)
+    t = torch.where(t > 0, t, -torch.inf)
+    d[1] = torch.where(d[1] > 0, d[1], -torch.inf)
+    for extreme, plain in ((torch.inf, 1e30), (3e38, 1e30), (1e-45, 1e-20), (1e-38, 1e-20)):
+        # (at 1e30 every difference of logits is 0 to fp32, at 1e-20 any that is not 0 takes the smaller one's weight)
+        want = check_verify(fp8act, t, d, x, u, e, torch.full((4,), plain, device="cuda"))
+        got = fp8act.verify_drafts(t, x, u, e, torch.full((4,), extreme, device="cuda"), draft_logits=d)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), extreme
+        assert all(v >= 0 and t[b, int(got[0][b]), v] > -torch.inf
+                   for b in range(4) for v in [int(got[1][b, int(got[0][b])])])
