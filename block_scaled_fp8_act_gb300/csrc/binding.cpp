@@ -204,7 +204,7 @@ int64_t heads_of(const at::Tensor& t, int64_t heads, int64_t dim, const char* na
         raise(PyExc_ValueError, std::string(name) + " must be [tokens, heads, " + std::to_string(dim) + "], got " + text(t.sizes()));
     if (t.stride(2) != 1 || (t.stride(1) != dim && t.size(1) > 1))
         raise(PyExc_ValueError, std::string(name) + ": the heads of a token must be contiguous");
-    return t.size(0) > 1 ? t.stride(0) : std::max(t.stride(0), t.size(1) * dim);
+    return t.size(0) > 1 ? t.stride(0) : t.size(1) * dim;  // (the stride of a single token is not used)
 }
 
 // (x, weight, residual, eps, weight_offset, q, sa, residual_out, stream) -> (q, sa[, residual_out])

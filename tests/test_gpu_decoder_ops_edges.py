@@ -286,3 +286,22 @@ def test_verify_ends_of_the_temperature_range(fp8act, V, dtype):  # noqa: F811
         assert all(torch.equal(a, b) for a, b in zip(got, want)), extreme
         assert all(v >= 0 and t[b, int(got[0][b]), v] > -torch.inf
                    for b in range(4) for v in [int(got[1][b, int(got[0][b])])])
+
+
+# ------------------------------------------------------------------ layout
+@pytest.mark.parametrize("T", [0, 1])
+def test_single_token_of_odd_rows(fp8act, T):  # noqa: F811
+    """The distance to a next token that is not there does not matter."""
+    H, D = 2, 128
+    rows = randn(3, (2 + 2 + 4) * D + 3, seed=1)
+    q, k, v = (rows[:, n:m].unflatten(1, (-1, D))[:T] for n, m in ((0, 4 * D), (4 * D, 6 * D), (6 * D, 8 * D)))
+    assert T == 0 or q.stride(0) % 8
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    lens = torch.full((1,), T, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    out = []
+    for a, b, c in ((q, k, v), (q.contiguous(), k.contiguous(), v.contiguous())):
+        cache = fp8act.kv_cache(1, H, 16, D)
+        fp8act.fp8_kv_append(b, c, torch.arange(T, device="cuda"), cache)
+        out.append((fp8act.fp8_kv_attention(a, cache, table, lens, cu), *cache))
+    assert all(torch.equal(a, b) for a, b in zip(*out))
