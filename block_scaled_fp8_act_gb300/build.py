@@ -4,12 +4,14 @@ Each .cu file under csrc/ compiles to an object in parallel, then nvcc links
 the shared library against the shared CUDA runtime (the same libcudart.so.13
 PyTorch loads). csrc/binding.cpp, the Python binding of the operators between
 the linear layers, compiles with the host compiler against PyTorch's headers
-into an extension module beside it, linked to the library. No CMake; a rebuild
-happens only when a source is newer than the libraries.
+into an extension module beside it, linked to the library; without PyTorch only
+the library is built, for callers of the C ABI. No CMake; a rebuild happens only
+when a source is newer than the libraries.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -46,10 +48,15 @@ def _deps() -> list[str]:
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def _has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(EXT_PATH):
+    made = [LIB_PATH, EXT_PATH] if _has_torch() else [LIB_PATH]
+    if not all(os.path.exists(p) for p in made):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(EXT_PATH))
+    t = min(os.path.getmtime(p) for p in made)
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
@@ -71,41 +78,48 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(r.stderr, end="")
         return obj
 
-    import torch
-
-    torch_dir = os.path.dirname(torch.__file__)
-    cuda = os.path.dirname(os.path.dirname(cc))
-    binding_obj = os.path.join(BUILD_DIR, "binding.cpp.o")
-
     def run(cmd: list[str], what: str) -> None:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"{what} failed:\n{r.stderr}")
 
-    def compile_binding() -> None:
-        run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
-             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-             "-I", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"],
-             "-I", os.path.join(cuda, "include"), "-c", BINDING, "-o", binding_obj], f"g++ on {BINDING}")
-
     with ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        binding = ex.submit(compile_binding)
+        binding = ex.submit(_compile_binding, cc, run) if _has_torch() else None
         objs = list(ex.map(compile_one, sources()))
-        binding.result()
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-cudart", "shared", *objs, "-o", tmp,
-           "-Xlinker", "-rpath", "-Xlinker", "/usr/local/cuda/lib64"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc link failed:\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
+        tmp = LIB_PATH + f".tmp{os.getpid()}"
+        run([cc, *ARCH, "-shared", "-cudart", "shared", *objs, "-o", tmp,
+             "-Xlinker", "-rpath", "-Xlinker", "/usr/local/cuda/lib64"], "nvcc link")
+        os.replace(tmp, LIB_PATH)
+        if binding:
+            _link_binding(cc, run, binding.result())
+    return LIB_PATH
+
+
+def _cuda_dir(cc: str) -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(cc)))
+
+
+def _compile_binding(cc: str, run) -> str:
+    import torch
+
+    torch_dir = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD_DIR, "binding.cpp.o")
+    run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         "-I", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"],
+         "-I", os.path.join(_cuda_dir(cc), "include"), "-c", BINDING, "-o", obj], f"g++ on {BINDING}")
+    return obj
+
+
+def _link_binding(cc: str, run, obj: str) -> None:
+    import torch
+
     tmp = EXT_PATH + f".tmp{os.getpid()}"
-    torch_lib, cuda_lib = os.path.join(torch_dir, "lib"), os.path.join(cuda, "lib64")
-    run(["g++", "-shared", binding_obj, "-o", tmp, "-L", BUILD_DIR, "-l:libfp8act.so", "-L", torch_lib, "-ltorch_python",
+    torch_lib, cuda_lib = os.path.join(os.path.dirname(torch.__file__), "lib"), os.path.join(_cuda_dir(cc), "lib64")
+    run(["g++", "-shared", obj, "-o", tmp, "-L", BUILD_DIR, "-l:libfp8act.so", "-L", torch_lib, "-ltorch_python",
          "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", cuda_lib, "-lcudart",
          f"-Wl,-rpath,$ORIGIN,-rpath,{torch_lib},-rpath,{cuda_lib}"], "linking the binding")
     os.replace(tmp, EXT_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":
