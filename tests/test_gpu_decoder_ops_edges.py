@@ -305,3 +305,27 @@ def test_single_token_of_odd_rows(fp8act, T):  # noqa: F811
         fp8act.fp8_kv_append(b, c, torch.arange(T, device="cuda"), cache)
         out.append((fp8act.fp8_kv_attention(a, cache, table, lens, cu), *cache))
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+# --------------------------------------------- verification: distribution
+@pytest.mark.parametrize("temperature", [1.0, 0.6])
+@pytest.mark.parametrize("greedy_draft", [False, True])
+def test_verify_keeps_the_targets_distribution_in_many_draws(fp8act, greedy_draft, temperature):  # noqa: F811
+    """960000 first tokens, chi-square over 6 tokens: below 35.9, which 5 degrees of freedom pass with 1 - 1e-6."""
+    B, V, rounds = 60000, 6, 16
+    t = torch.tensor([0.3, -1.0, 1.1, 0.0, -2.0, 0.6], device="cuda").expand(B, 2, V).contiguous()
+    d = torch.tensor([1.0, 0.5, -0.5, 0.0, 0.2, 0.1], device="cuda").expand(B, 1, V).contiguous()
+    temp = torch.full((B,), temperature, device="cuda")
+    seen = torch.zeros(V, dtype=torch.float64, device="cuda")
+    for i in range(rounds):
+        g = gen(1000 + i)
+        race = torch.empty((B, 1, V), device="cuda").exponential_(generator=g)
+        x = ((d / temperature).softmax(-1) / race).argmax(-1).to(torch.int32)
+        if greedy_draft:
+            x = torch.full_like(x, 2)
+        u = torch.rand((B, 1), device="cuda", generator=g)
+        e = torch.empty((B, V), device="cuda").exponential_(generator=g)
+        _, tokens, _ = fp8act.verify_drafts(t, x, u, e, temp, draft_logits=None if greedy_draft else d)
+        seen += torch.bincount(tokens[:, 0].long(), minlength=V).double()
+    want = (t[0, 0].double() / temperature).softmax(-1) * B * rounds
+    assert float(((seen - want) ** 2 / want).sum()) < 35.9
