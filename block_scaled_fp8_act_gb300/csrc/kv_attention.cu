@@ -17,9 +17,10 @@
 // fits f16 exactly down to 2^-17 of the largest value, and below that to
 // within 2^-25 of it. The weights W = p * s_v are rounded to f16 (11 bits; bf16
 // would give 8) after scaling by 2^6 / R, R the power of two below the largest
-// s_v so far: they keep full precision down to 2^-20 of the largest weight. The
-// running maximum moves only when a score passes it by 8 (in log2), so that
-// the accumulators are seldom rescaled; a weight then stays below 2^15. Maxima, sums, and both accumulations are fp32.
+// s_v so far: p s_v keeps its 11 bits down to 2^-20 R, and below that is within
+// 2^-31 R. The running maximum moves only when a score passes it by 8 (in
+// log2), so that the accumulators are seldom rescaled; a weight then stays
+// below 2^15. Maxima, sums, and both accumulations are fp32.
 //
 // Work split. A row tile is up to 192 rows of (new token, query head of one KV
 // head); a unit is one row tile x 32 cached tokens. The units of all

@@ -356,7 +356,7 @@ def kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, devic
 
 
 def fp8_kv_append(k, v, slots, cache, stream=None) -> None:
-    """Quantise bf16 k, v [T, kv_heads, head_dim] into the cache's slots (int64 [T], negative = skip)."""
+    """Quantise bf16 k, v [T, kv_heads, head_dim] into the cache's slots (int64 [T], distinct; negative = skip)."""
     _native().kv_append(k, v, slots, cache, stream)
 
 
@@ -374,7 +374,7 @@ def fp8_kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len: int | None 
     page_table int32 [B, max_pages], kv_lens int32 [B] (cached tokens, the new ones included),
     cu_q int32 [B + 1] (rows of q per sequence). max_q_len (the most new tokens of a sequence)
     picks the row tile; softmax_scale defaults to head_dim ** -0.5. `lse` (fp32 [tokens, q_heads])
-    is filled if given. `workspace`: a uint8 tensor of kv_attention_workspace() bytes, kept by the
+    is filled if given. Rows that no sequence has (past cu_q[B]) are not written. `workspace`: a uint8 tensor of kv_attention_workspace() bytes, kept by the
     caller per stream; without one the binding keeps its own per device and stream."""
     return _native().kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, out, lse, workspace,
                                   stream)

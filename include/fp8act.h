@@ -279,6 +279,8 @@ FP8ACT_API int fp8_silu_mul_quant(const void* gate_up_bf16, int M, int I, void* 
  *                    token and head; a value is code * scale
  * page_size is 16, 32, 64, 128 or 256, head_dim 64, 128 or 256, all four
  * buffers 16-byte aligned. Slot s is place s % page_size of page s / page_size.
+ * Codes are finite: E4M3's NaN (0x7F, 0xFF) may stand only where no sequence
+ * has a token. A token that is to read back as NaN has a NaN scale.
  */
 typedef struct {
     void* k_e4m3;
@@ -293,8 +295,9 @@ typedef struct {
  * slots[t]; a negative slot (padding) is skipped, and its input is not read.
  * The scale and codes of a head vector follow the activation rule over
  * head_dim values (bit-exact with the IEEE division). A vector with a NaN or
- * an infinity is stored as zero codes with a NaN scale. Two tokens with one
- * slot leave either's values.
+ * an infinity is stored as zero codes with a NaN scale. Slots that are not
+ * negative are distinct: of two tokens with one slot, codes and scales of
+ * either may be left.
  *   k, v   [T, kv_heads, head_dim] bf16, tokens k_stride / v_stride elements
  *          apart (multiples of 8, at least kv_heads * head_dim)
  *   slots  [T] int64
@@ -312,8 +315,16 @@ FP8ACT_API int fp8_kv_append(const void* k_bf16, const void* v_bf16, const int64
  *   out[t, h] = softmax_j(softmax_scale * q[t, h] . k[j]) v[j]     (bf16)
  *   lse[t, h] = log sum_j exp(softmax_scale * q[t, h] . k[j])      (fp32, may be NULL)
  * A row that sees nothing (kv_lens[b] = 0, or fewer cached than new tokens)
- * gets zeros and lse = -infinity. Slots at or past kv_lens[b] are never read.
- * A NaN in a cached token reaches the rows that see it and no other.
+ * gets zeros and lse = -infinity. What slots at or past kv_lens[b] hold is
+ * never used (a copy may take it along). A NaN scale of a cached token, as
+ * fp8_kv_append stores one, reaches the rows that see it and no other (a NaN
+ * code would reach more: see the cache). Rows of out and lse that no sequence
+ * has (past cu_q[batch], or all of them if batch is 0) are left as they are.
+ * Rounding: scores and sums are fp32. Weights (and from 49 rows of a KV head
+ * on values) are f16 on a scale that the sequence's largest value scale so far
+ * sets: beside 2^-8 |out| and 2^-10 sum p |v| an error of up to about 2^-30 of
+ * the largest |v| cached for the KV head is left, whether the row sees that
+ * token or not, so that values below 2^-20 of it lose bits.
  *   q          [tokens, q_heads, head_dim] bf16, tokens q_stride elements apart
  *   cu_q       [batch + 1] int32, cu_q[0] = 0, non-decreasing
  *   kv_lens    [batch] int32, at most max_pages * page_size
