@@ -328,11 +328,10 @@ int fp8_rmsnorm_quant(const void* x_bf16, const void* residual_bf16, const void*
         !aligned(residual_out_bf16, 16) || !aligned(sa, 4))
         return FP8ACT_ERR_ALIGN;
     int st = FP8ACT_OK;
-    const int sms = current_device_sms(&st);
+    current_device_sms(&st);
     if (st) return st;
     return launch_status(fp8act::launch_rmsnorm_quant(x_bf16, residual_bf16, weight_bf16, eps, weight_offset, M, K,
-                                                      q_e4m3, sa, residual_out_bf16, sms,
-                                                      static_cast<cudaStream_t>(stream)));
+                                                      q_e4m3, sa, residual_out_bf16, static_cast<cudaStream_t>(stream)));
 }
 
 int fp8_silu_mul_quant(const void* gate_up_bf16, int M, int I, void* q_e4m3, float* sa, void* stream) {

@@ -103,7 +103,7 @@ cudaError_t launch_stream_read(const void* src, int64_t bytes, unsigned int* sin
 // chunks of at most 4096. residual and residual_out are both null or neither.
 cudaError_t launch_rmsnorm_quant(const void* x, const void* residual, const void* weight, float eps,
                                  float weight_offset, int M, int K, void* q, float* sa, void* residual_out,
-                                 int num_sms, cudaStream_t stream);
+                                 cudaStream_t stream);
 
 // silu(gate) * up of gate_up bf16 [M, 2I] with E4M3 codes and 1x128 scales out.
 cudaError_t launch_silu_mul_quant(const void* gate_up, int M, int I, void* q, float* sa, int num_sms,

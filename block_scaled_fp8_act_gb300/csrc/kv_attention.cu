@@ -56,12 +56,6 @@ constexpr int kLeastUnits = 8;  // least share of a CTA
 constexpr int kItemCost = 20;   // units that an item counts beside its own
 using Work = Units<kTile, kItemCost>;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kN>
 __device__ __forceinline__ void cp_async_wait() {

@@ -39,6 +39,14 @@ struct AttnArgs {
 // CTAs of the main kernel (two per SM at most) that the workspace is made for.
 constexpr int kMaxAttnGrid = 2 * 160;
 
+// Asynchronous copies to shared memory; zeros are written where `in` is false, and nothing is read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+
 // Two E4M3 codes (the low or the high 16 bits of `codes`) to f16x2, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_lo_to_f16x2(uint32_t codes) {
     uint32_t r;

@@ -200,12 +200,6 @@ __device__ __forceinline__ void load_tokens(uint32_t dst, const CUtensorMap* map
         "l"(map), "r"(bar), "r"(0), "r"(line)
         : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Arrive on `bar` (one of its expected arrivals) once this thread's cp.asyncs so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {

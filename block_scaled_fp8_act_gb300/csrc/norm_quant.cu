@@ -158,7 +158,7 @@ cudaError_t launch_norm(const void* x, const void* residual, const void* weight,
 
 cudaError_t launch_rmsnorm_quant(const void* x, const void* residual, const void* weight, float eps,
                                  float weight_offset, int M, int K, void* q, float* sa, void* residual_out,
-                                 int num_sms, cudaStream_t stream) {
+                                 cudaStream_t stream) {
     const int chunks = K / 8;
     // One chunk per thread wherever a CTA holds the row: 4096 x 5120 with residual took 27.4 us so, with 2 or 4 chunks
     // per thread 28.9 or 32.5. (CTAs that stay and request the next row early: 26.7 to 31, then 26.2 with a CTA a row.)
