@@ -5,8 +5,8 @@
 //   silu: y = gate / (1 + exp(-gate)) * up
 // Both read and write each value once, so memory bounds them: 4096 x 5120 with
 // residual moves 147 MB in 26.1 us (5.6 TB/s, 0.83 of a copy's rate), 4096 x
-// 8704 gates 179 MB in 29.3 us (6.1 TB/s, 0.90; with loads that pass L1 by
-// 30.0 us). One row takes 1.8 us, a launch
+// 8704 gates 179 MB in 29.7 us (6.0 TB/s, 0.89; with loads that pass L1 by
+// 0.7 us more). One row takes 1.8 us, a launch
 // with one trip to memory and the row's reductions. The sum of squares is fp32.
 // Arithmetic goes in pairs and the scale and its reciprocal without divisions:
 // at 250 instructions per 8 columns issue slots were 72 % busy (27.4 us).

@@ -19,9 +19,11 @@
 // and 53 us for 34 x 2 drafts.)
 //
 // Measured over 151936 bf16 logits: 27.2 us for 34 sequences of 2 drafts (72 MB read once, 2.7 TB/s; 10.7 us at the
-// rate of a copy) and 11.3 us for one sequence of 7 (0.8). What bounds it: the first kernel, about half of the time, by
-// issue (an exponential, a widening and a maximum per logit: 2.6 of 4 instructions a clock); the second, and a single
+// rate of a copy) and 11.3 us for one sequence of 7 (0.8). What bounds it: in the first kernel, about half of the time,
+// neither issue (an exponential, a widening and a maximum per logit: 2.6 of 4 instructions a clock) nor memory (39 %) is
+// full, but some SMs have 4 CTAs where others have 3; the second, and a single
 // sequence, by the chain of dependent latencies: statistics, acceptance, the row drawn from, the cluster's meeting.
+// (With fp32 logits the second spills 164 bytes a thread at 64 registers, which two CTAs per SM leave.)
 // Widening and adding in pairs (packed maximum, fp32 pairs) took 0.8 us off the first.
 // The second reads nothing before its own wait, which alone makes what earlier kernels wrote visible to it; so that its
 // acceptance is still one trip to memory, the first notes the drafted token's logit in the record of a row's first part.
@@ -483,7 +485,7 @@ size_t verify_drafts_workspace(int B, int k) {
 cudaError_t launch_verify_drafts(const VerifyProblem& p, int num_sms, cudaStream_t stream) {
     const int rows = p.draft ? 2 * p.k + 1 : p.k + 1;
     // Parts of a row: as many as run at once with 4 CTAs of the first kernel per SM, of 2048 logits at least. (Rounded
-    // up, which leaves a second wave, 34 x 2 drafts over 151936 logits take 27.5 us instead of 26.8 and fp32 ones over
+    // up, which leaves a second wave, 34 x 2 drafts over 151936 logits took 27.5 us instead of 26.8 and fp32 ones over
     // 248320 58.4 instead of 51.5; parts for 5 or 6 CTAs per SM are within 3 % either way.)
     int shares = static_cast<int>(4 * static_cast<int64_t>(num_sms) / (static_cast<int64_t>(p.B) * rows));
     if (shares < 1) shares = 1;
