@@ -143,7 +143,7 @@ def test_kept_workspace_is_the_streams_own(fp8act):  # noqa: F811
         fp8act.verify_drafts(*large, draft_logits=dl, **outs[1])
     second = allocated(side.cuda_stream)
     side.synchronize()
-    assert allocated(main) == before
+    assert allocated(main) <= before  # (less if something old is collected meanwhile)
     assert 0 < fp8act.verify_drafts_workspace(1, 1) <= first and fp8act.verify_drafts_workspace(60, 7) <= second
 
 
