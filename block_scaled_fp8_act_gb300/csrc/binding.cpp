@@ -41,7 +41,7 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
 }
 
 constexpr auto kBf16 = at::kBFloat16, kF32 = at::kFloat, kI32 = at::kInt, kI64 = at::kLong, kU8 = at::kByte,
-               kE4m3 = at::kFloat8_e4m3fn;
+               kF64 = at::kDouble, kE4m3 = at::kFloat8_e4m3fn;
 
 // A contiguous CUDA tensor of a known shape and one of two types.
 template <class T>
@@ -259,6 +259,38 @@ PyObject* kv_append(PyObject* const* a) {
     Py_RETURN_NONE;
 }
 
+// (q, k, v, positions, inv_freq, slots, cache, q_weight, k_weight, eps, weight_offset, axes, interleaved, rope_scale,
+//  q_out, stream) -> q_out
+PyObject* rope_append(PyObject* const* a) {
+    const fp8act_kv_cache c = cache_of(a[6]);
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &pos = tensor(a[3], "positions"),
+                     &freq = tensor(a[4], "inv_freq");
+    const int64_t D = c.head_dim, qs = heads_of(q, -1, D, "q"), ks = heads_of(k, c.kv_heads, D, "k"),
+                  vs = heads_of(v, c.kv_heads, D, "v"), T = q.size(0), Hq = q.size(1);
+    if (k.size(0) != T || v.size(0) != T) raise(PyExc_ValueError, "q, k and v have different numbers of tokens");
+    if (pos.dim() != 1 && pos.dim() != 2) raise(PyExc_ValueError, "positions must be [T] or [axes, T]");
+    const int64_t axes = pos.dim() == 2 ? pos.size(0) : 1;
+    const int64_t* pp = pos.dim() == 2 ? data<int64_t>(pos, kI64, {axes, T}, "positions") : data<int64_t>(pos, kI64, {T}, "positions");
+    if (freq.dim() != 1) raise(PyExc_ValueError, "inv_freq must be 1-D");
+    const int64_t half = freq.size(0);
+    const double* fp = data<double>(freq, kF64, {half}, "inv_freq");
+    const int64_t* slots = data<int64_t>(a[5], kI64, {T}, "slots");
+    const void *wq = optional(a[7], kBf16, {D}, "q_weight"), *wk = optional(a[8], kBf16, {D}, "k_weight");
+    const int* ap = optional<int>(a[11], kI32, {half}, "axes");
+    const double eps = PyFloat_AsDouble(a[9]), offset = PyFloat_AsDouble(a[10]), scale = PyFloat_AsDouble(a[13]);
+    if (PyErr_Occurred()) throw Raised{};
+    const int interleaved = PyObject_IsTrue(a[12]);
+    if (interleaved < 0) throw Raised{};
+    cudaStream_t stream = stream_of(a[15]);
+    at::Tensor out = output(a[14], kBf16, {T, Hq, D}, q, stream, "q_out");
+    void* op = data(out, kBf16, {T, Hq, D}, "q_out");
+    check("fp8_rope_append",
+          fp8_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, wq, wk, static_cast<float>(eps),
+                          static_cast<float>(offset), pp, fp, ap, to_int(axes, "axes"), to_int(2 * half, "inv_freq"), interleaved,
+                          static_cast<float>(scale), slots, to_int(T, "T"), to_int(Hq, "q_heads"), &c, op, stream));
+    return THPVariable_Wrap(out);
+}
+
 // (q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, out, lse, workspace, stream) -> out
 PyObject* kv_attention(PyObject* const* a) {
     const fp8act_kv_cache c = cache_of(a[1]);
@@ -339,6 +371,7 @@ PyMethodDef g_methods[] = {
     {"rmsnorm_quant", fast<rmsnorm_quant, 9>(), METH_FASTCALL, nullptr},
     {"silu_mul_quant", fast<silu_mul_quant, 4>(), METH_FASTCALL, nullptr},
     {"kv_append", fast<kv_append, 5>(), METH_FASTCALL, nullptr},
+    {"rope_append", fast<rope_append, 16>(), METH_FASTCALL, nullptr},
     {"kv_attention", fast<kv_attention, 11>(), METH_FASTCALL, nullptr},
     {"verify_drafts", fast<verify_drafts, 12>(), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},

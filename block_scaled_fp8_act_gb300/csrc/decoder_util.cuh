@@ -87,6 +87,35 @@ __device__ __forceinline__ float quant_f32_group_halfwarp(float2 (&f)[4], uint2&
     return s;
 }
 
+// Quantises one head vector, 8 fp32 values a lane: s = amax / 448 (1 for an
+// all-zero vector), f becomes the quotients f / s. `top` is the bit pattern of
+// the largest magnitude, where NaN and infinity order above every finite value;
+// a vector that holds one becomes zeros with a NaN scale. The quotients are
+// formed as in act_group.cuh: for bf16 values those of the IEEE division, for
+// rounded fp32 ones within an ulp of it.
+__device__ __forceinline__ float quant_head(float (&f)[8], uint32_t top) {
+    const float amax = __uint_as_float(top);
+    float s;
+    if (amax >= kFastQuotientMinAmax && amax <= kFastQuotientMaxAmax) {
+        constexpr float kInv448 = 1.0f / kE4M3Max;
+        const float s0 = __fmul_rn(amax, kInv448);
+        s = __fmaf_rn(-__fmaf_rn(kE4M3Max, s0, -amax), kInv448, s0);
+        const float y0 = rcp_approx_ftz(s);
+        const float y = __fmaf_rn(__fmaf_rn(-s, y0, 1.0f), y0, y0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q0 = __fmul_rn(f[i], y);
+            f[i] = __fmaf_rn(-__fmaf_rn(s, q0, -f[i]), y, q0);
+        }
+    } else {
+        const bool finite = top < 0x7F800000u;
+        s = top == 0 ? 1.0f : finite ? __fdiv_rn(amax, kE4M3Max) : __uint_as_float(0x7FFFFFFFu);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = finite ? __fdiv_rn(f[i], s) : 0.0f;
+    }
+    return s;
+}
+
 // Launch with programmatic stream serialization (and a cluster size when it
 // is above 1): the kernel may start before the previous one has finished and
 // waits for it itself.

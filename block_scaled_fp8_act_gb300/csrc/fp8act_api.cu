@@ -201,6 +201,7 @@ int w8a16_common(const void* x, const void* w, const float* sw, int M, int N, in
 constexpr int kNormMaxK = 32768;  // one CTA holds a row: 1024 threads x 4 chunks of 8
 constexpr int kMaxQLen = 1 << 20;
 constexpr int kMaxVerifyB = 65535;
+constexpr int kMaxRopeHeads = 1 << 20, kMaxRopeAxes = 4;
 
 // The cache's own rules; fills the launchers' form of it.
 int check_cache(const fp8act_kv_cache* c, fp8act::KvCache* out) {
@@ -365,6 +366,36 @@ int fp8_kv_append(const void* k_bf16, const void* v_bf16, const int64_t* slots, 
                                                   static_cast<cudaStream_t>(stream)));
 }
 
+int fp8_rope_append(const void* q_bf16, const void* k_bf16, const void* v_bf16, int64_t q_stride, int64_t k_stride,
+                    int64_t v_stride, const void* q_weight_bf16, const void* k_weight_bf16, float eps,
+                    float weight_offset, const int64_t* positions, const double* inv_freq, const int* axis, int n_axes,
+                    int rot_dim, int interleaved, float rope_scale, const int64_t* slots, int T, int q_heads,
+                    const fp8act_kv_cache* cache, void* q_out_bf16, void* stream) {
+    fp8act::KvCache c;
+    if (int st = check_cache(cache, &c)) return st;
+    const int64_t width = static_cast<int64_t>(c.heads) * c.head_dim;
+    if (T < 0 || q_heads <= 0 || q_heads > kMaxRopeHeads || c.heads > kMaxRopeHeads || n_axes < 1 ||
+        n_axes > kMaxRopeAxes || rot_dim < 0 || rot_dim > c.head_dim || rot_dim % 16 || k_stride < width ||
+        v_stride < width || q_stride < static_cast<int64_t>(q_heads) * c.head_dim)
+        return FP8ACT_ERR_SHAPE;
+    if (T == 0) return FP8ACT_OK;
+    if (!q_bf16 || !k_bf16 || !v_bf16 || !positions || !slots || !q_out_bf16 || (rot_dim > 0 && !inv_freq))
+        return FP8ACT_ERR_NULL;
+    if (!aligned(q_bf16, 16) || !aligned(k_bf16, 16) || !aligned(v_bf16, 16) || q_stride % 8 || k_stride % 8 ||
+        v_stride % 8 || !aligned(q_weight_bf16, 16) || !aligned(k_weight_bf16, 16) || !aligned(positions, 8) ||
+        !aligned(inv_freq, 8) || !aligned(axis, 4) || !aligned(slots, 8) || !aligned(q_out_bf16, 16))
+        return FP8ACT_ERR_ALIGN;
+    int st = FP8ACT_OK;
+    current_device_sms(&st);
+    if (st) return st;
+    using bf16 = const uint16_t*;
+    const fp8act::RopeProblem p = {static_cast<bf16>(q_bf16), static_cast<bf16>(k_bf16), static_cast<bf16>(v_bf16),
+                                   q_stride, k_stride, v_stride, static_cast<bf16>(q_weight_bf16),
+                                   static_cast<bf16>(k_weight_bf16), eps, weight_offset, rope_scale, positions,
+                                   inv_freq, axis, slots, T, q_heads, rot_dim, n_axes, interleaved != 0, c, q_out_bf16};
+    return launch_status(fp8act::launch_rope_append(p, static_cast<cudaStream_t>(stream)));
+}
+
 size_t fp8_kv_attention_workspace(int max_q_len, int q_heads, const fp8act_kv_cache* cache) {
     fp8act::KvCache c;
     if (check_cache(cache, &c) || max_q_len < 0 || max_q_len > kMaxQLen || q_heads <= 0 || q_heads % c.heads) return 0;
@@ -454,8 +485,8 @@ int fp8act_check_status(void* stream) {
     const unsigned int tc = fp8act::read_and_clear_tc_error();
     const unsigned int mid = fp8act::read_and_clear_midm_error();
     const unsigned int rd = fp8act::read_and_clear_read_error();
-    const unsigned int index = fp8act::read_and_clear_kv_index_error() | fp8act::read_and_clear_attn_index_error() |
-                               fp8act::read_and_clear_verify_index_error();
+    const unsigned int index = fp8act::read_and_clear_kv_index_error() | fp8act::read_and_clear_rope_index_error() |
+                               fp8act::read_and_clear_attn_index_error() | fp8act::read_and_clear_verify_index_error();
     const unsigned int at = fp8act::read_and_clear_attn_timeout();
     if (tc | mid | rd | at) return FP8ACT_ERR_TIMEOUT;
     return index ? FP8ACT_ERR_INDEX : FP8ACT_OK;

@@ -123,6 +123,29 @@ struct KvCache {
 cudaError_t launch_kv_append(const void* k, const void* v, const int64_t* slots, int T, int64_t k_stride,
                              int64_t v_stride, const KvCache& cache, cudaStream_t stream);
 
+// Head norms, rotary positions and the cache append of `tokens` tokens: q, k, v
+// rows of heads (strides in elements), positions [n_axes, tokens], one
+// frequency per pair of the first `rot` columns, `axis` (or null: the first)
+// its row of positions.
+struct RopeProblem {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t q_stride, k_stride, v_stride;
+    const uint16_t* q_weight;  // [head_dim] or null
+    const uint16_t* k_weight;
+    float eps, weight_offset, rope_scale;
+    const int64_t* positions;
+    const double* inv_freq;
+    const int* axis;
+    const int64_t* slots;
+    int tokens, q_heads, rot, n_axes;
+    bool interleaved;
+    KvCache cache;
+    void* q_out;
+};
+cudaError_t launch_rope_append(const RopeProblem& p, cudaStream_t stream);
+
 // Attention of `tokens` new tokens of `batch` sequences over the cache.
 struct AttentionProblem {
     const void* q;
@@ -163,6 +186,7 @@ cudaError_t launch_verify_drafts(const VerifyProblem& p, int num_sms, cudaStream
 
 // Device-side words set by a page, slot, length or token index out of range.
 unsigned int read_and_clear_kv_index_error();
+unsigned int read_and_clear_rope_index_error();
 unsigned int read_and_clear_attn_index_error();
 unsigned int read_and_clear_attn_timeout();
 unsigned int read_and_clear_verify_index_error();

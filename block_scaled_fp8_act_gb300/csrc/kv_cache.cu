@@ -20,10 +20,8 @@ namespace {
 
 __device__ unsigned int g_kv_index_error;
 
-// kLanes = D / 8 lanes hold one vector, 8 values each. The quotients are
-// formed as in act_group.cuh (short fused multiply-add sequences that give the
-// IEEE division's codes for every bf16 pair in range); the maximum is taken on
-// the bit patterns, where NaN and infinity order above every finite value.
+// kLanes = D / 8 lanes hold one vector, 8 values each; the maximum is taken on
+// the bit patterns.
 template <int kLanes>
 __global__ void __launch_bounds__(256) kv_append_kernel(const uint4* k, const uint4* v, const int64_t* slots,
                                                         int64_t vectors, int heads, int64_t k_stride, int64_t v_stride,
@@ -51,26 +49,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const uint4* k, const ui
     top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
     for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float amax = __uint_as_float(top << 16);
-    float f[8], s;
+    float f[8];
     unpack_bf16x8(x, f);
-    if (amax >= kFastQuotientMinAmax && amax <= kFastQuotientMaxAmax) {
-        constexpr float kInv448 = 1.0f / kE4M3Max;
-        const float s0 = __fmul_rn(amax, kInv448);
-        s = __fmaf_rn(-__fmaf_rn(kE4M3Max, s0, -amax), kInv448, s0);
-        const float y0 = rcp_approx_ftz(s);
-        const float y = __fmaf_rn(__fmaf_rn(-s, y0, 1.0f), y0, y0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q0 = __fmul_rn(f[i], y);
-            f[i] = __fmaf_rn(-__fmaf_rn(s, q0, -f[i]), y, q0);
-        }
-    } else {
-        const bool finite = top < 0x7F80u;
-        s = top == 0 ? 1.0f : finite ? __fdiv_rn(amax, kE4M3Max) : __uint_as_float(0x7FFFFFFFu);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = finite ? __fdiv_rn(f[i], s) : 0.0f;
-    }
+    const float s = quant_head(f, top << 16);
     if (slot < 0) return;
     const int64_t page = slot >> c.page_log2;
     const int64_t at = ((page * heads + h) << c.page_log2) + (slot & ((1 << c.page_log2) - 1));

@@ -85,13 +85,14 @@ def load(build: bool = False) -> ctypes.CDLL:
     L.fp8_rmsnorm_quant.argtypes = [p, p, p, f, f, i, i, p, p, p, p]
     L.fp8_silu_mul_quant.argtypes = [p, i, i, p, p, p]
     L.fp8_kv_append.argtypes = [p, p, p, i, i64, i64, p, p]
+    L.fp8_rope_append.argtypes = [p, p, p, i64, i64, i64, p, p, f, f, p, p, p, i, i, i, f, p, i, i, p, p, p]
     L.fp8_kv_attention.argtypes = [p, i64, p, p, p, i, i, i, i, i, f, p, p, p, p, ctypes.c_size_t, p]
     L.fp8_kv_attention_workspace.argtypes = [i, i, p]
     L.fp8_kv_attention_workspace.restype = ctypes.c_size_t
     L.fp8act_verify_drafts.argtypes = [p, p, i, p, p, p, p, p, i, i, i, p, p, p, p, ctypes.c_size_t, p]
     L.fp8act_verify_drafts_workspace.argtypes = [i, i]
     L.fp8act_verify_drafts_workspace.restype = ctypes.c_size_t
-    for fn in (L.fp8_rmsnorm_quant, L.fp8_silu_mul_quant, L.fp8_kv_append, L.fp8_kv_attention,
+    for fn in (L.fp8_rmsnorm_quant, L.fp8_silu_mul_quant, L.fp8_kv_append, L.fp8_rope_append, L.fp8_kv_attention,
                L.fp8act_verify_drafts, L.fp8_act_quant, L.fp8_weight_quant, L.fp8_block_gemm, L.fp8_block_gemm_f32,
                L.fp8_block_gemm_w8a16, L.fp8_block_gemm_w8a16_f32,
                L.fp8_act_quant_grouped, L.fp8_block_gemm_grouped, L.fp8_block_gemm_grouped_f32,
@@ -358,6 +359,21 @@ def kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, devic
 def fp8_kv_append(k, v, slots, cache, stream=None) -> None:
     """Quantise bf16 k, v [T, kv_heads, head_dim] into the cache's slots (int64 [T], distinct; negative = skip)."""
     _native().kv_append(k, v, slots, cache, stream)
+
+
+def fp8_rope_append(q, k, v, positions, inv_freq, slots, cache, q_weight=None, k_weight=None, eps: float = 1e-6,
+                    weight_offset: float = 0.0, axes=None, interleaved: bool = False, rope_scale: float = 1.0,
+                    q_out=None, stream=None):
+    """Head norms, rotary positions and the cache append of new tokens -> q_out bf16 [T, q_heads, head_dim].
+
+    bf16 q [T, q_heads, head_dim], k, v [T, kv_heads, head_dim] (columns of wider rows may be passed);
+    q_weight, k_weight [head_dim] (None: no norm). positions int64 [T], or [n, T] with `axes` int32
+    [rot / 2] naming the row that turns each pair (None: the first); inv_freq float64 [rot / 2] turns the
+    first rot columns, pairs (i, i + rot / 2) or, interleaved, (2i, 2i + 1), by positions * inv_freq, times
+    rope_scale. The turned keys and the values go to `slots` (int64 [T], distinct; negative = the cache is
+    left alone) of the cache."""
+    return _native().rope_append(q, k, v, positions, inv_freq, slots, cache, q_weight, k_weight, eps, weight_offset, axes,
+                                 interleaved, rope_scale, q_out, stream)
 
 
 def kv_attention_workspace(max_q_len: int, q_heads: int, cache) -> int:

@@ -239,8 +239,8 @@ FP8ACT_API int fp8_block_gemm_grouped_f32(const fp8act_gemm_problem* problems, i
  * Operators between the linear layers
  * -----------------------------------
  * One decode or draft-verify step of a decoder layer runs
- *   fp8_rmsnorm_quant -> fp8_block_gemm (q, k, v) -> fp8_kv_append ->
- *   fp8_kv_attention -> fp8_act_quant -> fp8_block_gemm -> fp8_rmsnorm_quant ->
+ *   fp8_rmsnorm_quant -> fp8_block_gemm (q, k, v) -> fp8_rope_append (or, with
+ *   no positions, fp8_kv_append) -> fp8_kv_attention -> fp8_act_quant -> fp8_block_gemm -> fp8_rmsnorm_quant ->
  *   fp8_block_gemm (gate, up) -> fp8_silu_mul_quant -> fp8_block_gemm,
  * and after the vocabulary head fp8act_verify_drafts. They follow the
  * conventions above (device pointers, no allocation, capturable, launched with
@@ -304,6 +304,39 @@ typedef struct {
  */
 FP8ACT_API int fp8_kv_append(const void* k_bf16, const void* v_bf16, const int64_t* slots, int T, int64_t k_stride,
                              int64_t v_stride, const fp8act_kv_cache* cache, void* stream);
+
+/*
+ * What lies between the q, k, v product and the attention, in one pass: RMS
+ * norm of every query and key head, rotary positions, keys and values into the
+ * cache. Per head vector x of head_dim values, in fp32:
+ *   y = x * rsqrt(mean(x^2) + eps) * (weight + weight_offset)   (with a weight; else y = x)
+ *   (a, b) -> rope_scale * (a cos - b sin, a sin + b cos)  for pair i of the first
+ *   rot_dim columns, angle = positions[axis[i], t] * inv_freq[i]
+ * Pair i is columns (i, i + rot_dim / 2), interleaved != 0: (2i, 2i + 1). Queries
+ * are rounded once to bf16 (q_out); keys are quantised as they are, with no
+ * rounding to bf16 between; values, neither normed nor turned, as by
+ * fp8_kv_append. A key or value vector with a NaN or an infinity is stored as
+ * zero codes with a NaN scale. A negative slot (padding) leaves the cache
+ * alone; the token's query is still written. Slots that are not negative are
+ * distinct.
+ * Several axes are rows of positions (time, height, width): axis[i] says which
+ * one turns pair i, so sections and interleaved axes are both a table.
+ * Angles are reduced in whole numbers (2^64 to a turn), so positions may be any
+ * int64; the frequency's rounding leaves an error of 2^-52 of the angle.
+ *   q [T, q_heads, head_dim], k, v [T, kv_heads, head_dim] bf16, tokens *_stride
+ *     elements apart (multiples of 8, at least the width of their heads)
+ *   q_weight, k_weight [head_dim] bf16, either may be NULL: no norm
+ *   positions [n_axes, T] int64; n_axes 1 .. 4
+ *   inv_freq  [rot_dim / 2] fp64, finite; rot_dim a multiple of 16, 0 .. head_dim
+ *   axis      [rot_dim / 2] int32 below n_axes, or NULL: axis 0
+ *   slots     [T] int64;  q_out [T, q_heads, head_dim] bf16, not q itself
+ */
+FP8ACT_API int fp8_rope_append(const void* q_bf16, const void* k_bf16, const void* v_bf16, int64_t q_stride,
+                               int64_t k_stride, int64_t v_stride, const void* q_weight_bf16,
+                               const void* k_weight_bf16, float eps, float weight_offset, const int64_t* positions,
+                               const double* inv_freq, const int* axis, int n_axes, int rot_dim, int interleaved,
+                               float rope_scale, const int64_t* slots, int T, int q_heads,
+                               const fp8act_kv_cache* cache, void* q_out_bf16, void* stream);
 
 /*
  * Attention of new tokens over the cache, for any number of new tokens per
