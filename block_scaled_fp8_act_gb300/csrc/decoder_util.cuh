@@ -33,11 +33,6 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float (&f)[8]) {
     f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
 }
 
-__device__ __forceinline__ uint2 pack_e4m3x8(const float (&f)[8]) {
-    return make_uint2(cvt_e4m3x2(f[0], f[1]) | (cvt_e4m3x2(f[2], f[3]) << 16),
-                      cvt_e4m3x2(f[4], f[5]) | (cvt_e4m3x2(f[6], f[7]) << 16));
-}
-
 // The same in pairs, for the two-wide fp32 instructions.
 __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float2 (&f)[4]) {
     f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
@@ -48,6 +43,17 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float2 (&f)[4]) {
 __device__ __forceinline__ uint4 pack_bf16x8(const float2 (&f)[4]) {
     return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
                       pack_bf16x2(f[3].x, f[3].y));
+}
+
+__device__ __forceinline__ uint2 pack_e4m3x8(const float2 (&f)[4]) {
+    return make_uint2(cvt_e4m3x2(f[0].x, f[0].y) | (cvt_e4m3x2(f[1].x, f[1].y) << 16),
+                      cvt_e4m3x2(f[2].x, f[2].y) | (cvt_e4m3x2(f[3].x, f[3].y) << 16));
+}
+
+// The largest bit pattern of 8 bf16 magnitudes: NaN and infinity order above every finite value.
+__device__ __forceinline__ uint32_t top_bits(const uint4& x) {
+    const uint32_t t = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+    return max(t & 0xFFFFu, t >> 16);
 }
 
 // Quantises one 128-wide group of fp32 values held by a half-warp (8 per
@@ -82,8 +88,7 @@ __device__ __forceinline__ float quant_f32_group_halfwarp(float2 (&f)[4], uint2&
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = make_float2(__fdiv_rn(f[i].x, s), __fdiv_rn(f[i].y, s));
     }
-    codes = make_uint2(cvt_e4m3x2(f[0].x, f[0].y) | (cvt_e4m3x2(f[1].x, f[1].y) << 16),
-                       cvt_e4m3x2(f[2].x, f[2].y) | (cvt_e4m3x2(f[3].x, f[3].y) << 16));
+    codes = pack_e4m3x8(f);
     return s;
 }
 
@@ -93,7 +98,7 @@ __device__ __forceinline__ float quant_f32_group_halfwarp(float2 (&f)[4], uint2&
 // a vector that holds one becomes zeros with a NaN scale. The quotients are
 // formed as in act_group.cuh: for bf16 values those of the IEEE division, for
 // rounded fp32 ones within an ulp of it.
-__device__ __forceinline__ float quant_head(float (&f)[8], uint32_t top) {
+__device__ __forceinline__ float quant_head(float2 (&f)[4], uint32_t top) {
     const float amax = __uint_as_float(top);
     float s;
     if (amax >= kFastQuotientMinAmax && amax <= kFastQuotientMaxAmax) {
@@ -102,16 +107,18 @@ __device__ __forceinline__ float quant_head(float (&f)[8], uint32_t top) {
         s = __fmaf_rn(-__fmaf_rn(kE4M3Max, s0, -amax), kInv448, s0);
         const float y0 = rcp_approx_ftz(s);
         const float y = __fmaf_rn(__fmaf_rn(-s, y0, 1.0f), y0, y0);
+        const float2 y2 = make_float2(y, y), minus_s = make_float2(-s, -s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q0 = __fmul_rn(f[i], y);
-            f[i] = __fmaf_rn(-__fmaf_rn(s, q0, -f[i]), y, q0);
+        for (int i = 0; i < 4; ++i) {
+            const float2 q0 = __fmul2_rn(f[i], y2);
+            f[i] = __ffma2_rn(__ffma2_rn(minus_s, q0, f[i]), y2, q0);
         }
     } else {
         const bool finite = top < 0x7F800000u;
         s = top == 0 ? 1.0f : finite ? __fdiv_rn(amax, kE4M3Max) : __uint_as_float(0x7FFFFFFFu);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = finite ? __fdiv_rn(f[i], s) : 0.0f;
+        for (int i = 0; i < 4; ++i)
+            f[i] = finite ? make_float2(__fdiv_rn(f[i].x, s), __fdiv_rn(f[i].y, s)) : make_float2(0.0f, 0.0f);
     }
     return s;
 }

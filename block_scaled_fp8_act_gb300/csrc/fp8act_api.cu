@@ -386,14 +386,14 @@ int fp8_rope_append(const void* q_bf16, const void* k_bf16, const void* v_bf16, 
         !aligned(inv_freq, 8) || !aligned(axis, 4) || !aligned(slots, 8) || !aligned(q_out_bf16, 16))
         return FP8ACT_ERR_ALIGN;
     int st = FP8ACT_OK;
-    current_device_sms(&st);
+    const int sms = current_device_sms(&st);
     if (st) return st;
     using bf16 = const uint16_t*;
     const fp8act::RopeProblem p = {static_cast<bf16>(q_bf16), static_cast<bf16>(k_bf16), static_cast<bf16>(v_bf16),
                                    q_stride, k_stride, v_stride, static_cast<bf16>(q_weight_bf16),
                                    static_cast<bf16>(k_weight_bf16), eps, weight_offset, rope_scale, positions,
                                    inv_freq, axis, slots, T, q_heads, rot_dim, n_axes, interleaved != 0, c, q_out_bf16};
-    return launch_status(fp8act::launch_rope_append(p, static_cast<cudaStream_t>(stream)));
+    return launch_status(fp8act::launch_rope_append(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t fp8_kv_attention_workspace(int max_q_len, int q_heads, const fp8act_kv_cache* cache) {

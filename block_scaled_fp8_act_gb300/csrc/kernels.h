@@ -144,7 +144,7 @@ struct RopeProblem {
     KvCache cache;
     void* q_out;
 };
-cudaError_t launch_rope_append(const RopeProblem& p, cudaStream_t stream);
+cudaError_t launch_rope_append(const RopeProblem& p, int num_sms, cudaStream_t stream);
 
 // Attention of `tokens` new tokens of `batch` sequences over the cache.
 struct AttentionProblem {

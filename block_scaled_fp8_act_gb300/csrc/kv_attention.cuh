@@ -65,12 +65,6 @@ __device__ __forceinline__ uint32_t scale_exponent(float s) {
     return e == 0x7F800000u ? 0u : e;
 }
 
-// The largest bit pattern of 8 bf16 magnitudes: NaN and infinity order above every finite value.
-__device__ __forceinline__ uint32_t top_bits(const uint4& x) {
-    const uint32_t t = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
-    return max(t & 0xFFFFu, t >> 16);
-}
-
 // One item and where it lies in the unit list. A unit is kTok cached tokens of
 // a row tile; an item counts kCost units beside its own.
 struct Item {

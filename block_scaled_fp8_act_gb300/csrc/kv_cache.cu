@@ -45,11 +45,10 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const uint4* k, const ui
     }
     uint4 x = make_uint4(0, 0, 0, 0);
     if (slot >= 0) x = ld_dep_stream_v4(is_v ? v + t * v_stride + h * kLanes + hl : k + t * k_stride + h * kLanes + hl);
-    uint32_t top = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
-    top = max(top & 0xFFFFu, top >> 16);
+    uint32_t top = top_bits(x);
 #pragma unroll
     for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float f[8];
+    float2 f[4];
     unpack_bf16x8(x, f);
     const float s = quant_head(f, top << 16);
     if (slot < 0) return;
