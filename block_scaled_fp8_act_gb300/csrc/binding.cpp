@@ -316,6 +316,36 @@ PyObject* kv_attention(PyObject* const* a) {
     return THPVariable_Wrap(out);
 }
 
+int to_count(PyObject* o, const char* name) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Raised{};
+    if (v < INT32_MIN) raise(PyExc_ValueError, std::string(name) + " is too small");
+    return to_int(v, name);
+}
+
+// (cache, mass, page_table, kv_lens, keep, new_table, recent, first, new_lens, kept, stream) -> (new_lens, kept)
+PyObject* kv_evict(PyObject* const* a) {
+    const fp8act_kv_cache c = cache_of(a[0]);
+    const at::Tensor &table = tensor(a[2], "page_table"), &next = tensor(a[5], "new_table");
+    float* mass = data<float>(a[1], kF32, {c.num_pages, c.kv_heads, c.page_size}, "mass");
+    if (table.dim() != 2 || next.dim() != 2) raise(PyExc_ValueError, "page_table and new_table must be 2-D [B, pages]");
+    const int64_t B = table.size(0), pages = table.size(1), fresh_pages = next.size(1);
+    const int* tp = data<int>(table, kI32, {B, pages}, "page_table");
+    const int* np = data<int>(next, kI32, {B, fresh_pages}, "new_table");
+    const int* lens = data<int>(a[3], kI32, {B}, "kv_lens");
+    const int* keep = data<int>(a[4], kI32, {B}, "keep");
+    const int recent = to_count(a[6], "recent"), first = to_count(a[7], "first");
+    cudaStream_t stream = stream_of(a[10]);
+    const int64_t places = fresh_pages * c.page_size;
+    at::Tensor new_lens = output(a[8], kI32, {B}, table, stream, "new_lens"),
+               kept = output(a[9], kI32, {B, c.kv_heads, places}, table, stream, "kept");
+    int* lp = data<int>(new_lens, kI32, {B}, "new_lens");
+    int* kp = data<int>(kept, kI32, {B, c.kv_heads, places}, "kept");
+    check("fp8_kv_evict", fp8_kv_evict(&c, mass, tp, to_int(pages, "max_pages"), lens, keep, np, to_int(fresh_pages, "new_pages"),
+                                       to_int(B, "B"), recent, first, lp, kp, stream));
+    return tuple<2>({new_lens, kept});
+}
+
 // (target_logits, draft_tokens, uniform, noise, temperature, draft_logits, n_draft, accepted, tokens, accept_prob,
 //  workspace, stream) -> (accepted, tokens, accept_prob)
 PyObject* verify_drafts(PyObject* const* a) {
@@ -373,6 +403,7 @@ PyMethodDef g_methods[] = {
     {"kv_append", fast<kv_append, 5>(), METH_FASTCALL, nullptr},
     {"rope_append", fast<rope_append, 16>(), METH_FASTCALL, nullptr},
     {"kv_attention", fast<kv_attention, 11>(), METH_FASTCALL, nullptr},
+    {"kv_evict", fast<kv_evict, 11>(), METH_FASTCALL, nullptr},
     {"verify_drafts", fast<verify_drafts, 12>(), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},

@@ -432,6 +432,35 @@ int fp8_kv_attention(const void* q_bf16, int64_t q_stride, const int* cu_q, cons
     return launch_status(fp8act::launch_kv_attention(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
+int fp8_kv_evict(const fp8act_kv_cache* cache, float* mass, const int* page_table, int max_pages, const int* kv_lens,
+                 const int* keep, const int* new_table, int new_pages, int batch, int recent, int first, int* new_lens,
+                 int* kept, void* stream) {
+    fp8act::KvCache c;
+    if (int st = check_cache(cache, &c)) return st;
+    if (batch < 0 || max_pages < 0 || new_pages < 0 || recent < 0 || first < 0 ||
+        static_cast<int64_t>(max_pages) << c.page_log2 > 0x7FFFFF00 ||
+        static_cast<int64_t>(new_pages) << c.page_log2 > 0x7FFFFF00)
+        return FP8ACT_ERR_SHAPE;
+    // (CTAs of a launch: 8 per sequence and head, or one per 64 places)
+    const int64_t items = static_cast<int64_t>(batch) * c.heads;
+    if (items > 0x7FFFFFFF / 8 || items * ((static_cast<int64_t>(new_pages) << c.page_log2) / 64 + 1) > 0x7FFFFFFF)
+        return FP8ACT_ERR_SHAPE;
+    if (batch == 0) return FP8ACT_OK;
+    if (c.num_pages == 0) return FP8ACT_ERR_SHAPE;
+    if (!mass || !kv_lens || !keep || !new_lens || (max_pages > 0 && !page_table) || (new_pages > 0 && (!new_table || !kept)))
+        return FP8ACT_ERR_NULL;
+    if (new_lens == kv_lens || new_lens == keep) return FP8ACT_ERR_SHAPE;
+    if (!aligned(mass, 16) || !aligned(page_table, 4) || !aligned(kv_lens, 4) || !aligned(keep, 4) ||
+        !aligned(new_table, 4) || !aligned(new_lens, 4) || !aligned(kept, 4))
+        return FP8ACT_ERR_ALIGN;
+    int st = FP8ACT_OK;
+    const int sms = current_device_sms(&st);
+    if (st) return st;
+    const fp8act::EvictProblem p = {c, mass, page_table, kv_lens, keep, new_table, max_pages, new_pages, batch, recent,
+                                    first, new_lens, kept};
+    return launch_status(fp8act::launch_kv_evict(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
 int fp8act_verify_drafts(const void* target, const void* draft, int logits_f32, const int* draft_tokens,
                          const float* uniform, const float* noise, const float* temperature, const int* n_draft, int B,
                          int k, int V, int* accepted, int* tokens, float* accept_prob, void* workspace,
@@ -486,7 +515,8 @@ int fp8act_check_status(void* stream) {
     const unsigned int mid = fp8act::read_and_clear_midm_error();
     const unsigned int rd = fp8act::read_and_clear_read_error();
     const unsigned int index = fp8act::read_and_clear_kv_index_error() | fp8act::read_and_clear_rope_index_error() |
-                               fp8act::read_and_clear_attn_index_error() | fp8act::read_and_clear_verify_index_error();
+                               fp8act::read_and_clear_attn_index_error() | fp8act::read_and_clear_evict_index_error() |
+                               fp8act::read_and_clear_verify_index_error();
     const unsigned int at = fp8act::read_and_clear_attn_timeout();
     if (tc | mid | rd | at) return FP8ACT_ERR_TIMEOUT;
     return index ? FP8ACT_ERR_INDEX : FP8ACT_OK;

@@ -164,6 +164,22 @@ struct AttentionProblem {
 size_t kv_attention_workspace(int max_q_len, int group, int head_dim);
 cudaError_t launch_kv_attention(const AttentionProblem& p, int num_sms, cudaStream_t stream);
 
+// Eviction: per sequence and KV head the keep[b] tokens of the largest weight,
+// in their order, into the pages of new_table.
+struct EvictProblem {
+    KvCache cache;
+    float* mass;  // [num_pages, heads, page]
+    const int* page_table;
+    const int* kv_lens;
+    const int* keep;
+    const int* new_table;
+    int64_t table_stride, new_stride;  // pages of a sequence
+    int batch, recent, first;
+    int* new_lens;
+    int* kept;  // [batch, heads, new_stride * page]
+};
+cudaError_t launch_kv_evict(const EvictProblem& p, int num_sms, cudaStream_t stream);
+
 // Verification of k drafted tokens per sequence.
 struct VerifyProblem {
     const void* target;  // [B, k + 1, V]
@@ -188,6 +204,7 @@ cudaError_t launch_verify_drafts(const VerifyProblem& p, int num_sms, cudaStream
 unsigned int read_and_clear_kv_index_error();
 unsigned int read_and_clear_rope_index_error();
 unsigned int read_and_clear_attn_index_error();
+unsigned int read_and_clear_evict_index_error();
 unsigned int read_and_clear_attn_timeout();
 unsigned int read_and_clear_verify_index_error();
 

@@ -1,0 +1,340 @@
+// Eviction from the paged cache: per sequence and KV head the `keep` tokens of
+// the largest accumulated weight, in their order, copied into other pages.
+//
+// Select. A weight's bits become a whole number of the same order, the kept
+// class above it: the last `recent` and the first `first` tokens are the largest
+// number, NaN counts as -infinity. The keep-th largest number T is found 11, 11
+// and 10 bits at a time from counts in shared memory, then the tokens above T
+// and the first of those equal to it are listed by a running count. A (sequence,
+// head) has a cluster of up to 8 CTAs, each with a run of tokens whose numbers
+// stay in shared memory: the weights are read once. The CTAs add each other's
+// counts through distributed shared memory, so nothing goes through global
+// memory but the list.
+//
+// Copy. A CTA takes 64 places of the list: one thread each looks up where a
+// token is and where it goes, then the codes move 16 bytes a thread, all of a
+// thread's loads before its stores.
+#include <atomic>
+
+#include "decoder_util.cuh"
+#include "kernels.h"
+
+namespace fp8act {
+namespace {
+
+__device__ unsigned int g_evict_index_error;
+
+constexpr int kThreads = 1024;
+constexpr int kBins = 2048;
+constexpr int kMostKeys = 40960;  // that a CTA holds in shared memory; more are read again
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// What a sequence comes to: its cached tokens, how many stay, and how many of those by their place.
+struct Budget {
+    int len, count, recent, first;
+};
+__device__ __forceinline__ Budget budget_of(const EvictProblem& p, int b, bool report) {
+    const int64_t most = p.table_stride << p.cache.page_log2, room = p.new_stride << p.cache.page_log2;
+    const int len = ld_dep_s32(p.kv_lens + b), keep = ld_dep_s32(p.keep + b);
+    if (report && (len < 0 || len > most || keep < 0 || keep > room)) atomicOr(&g_evict_index_error, 1u);
+    Budget g;
+    g.len = len < 0 ? 0 : static_cast<int>(len > most ? most : len);
+    const int k = keep < 0 ? 0 : static_cast<int>(keep > room ? room : keep);
+    g.count = min(g.len, k);
+    g.recent = min(p.recent, g.count);
+    g.first = min(p.first, g.count - g.recent);
+    return g;
+}
+
+// The order of weights as that of whole numbers; NaN as -infinity, -0 as 0.
+__device__ __forceinline__ uint32_t ordered(float w) {
+    uint32_t u = __float_as_uint(w);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) u = 0xFF800000u;
+    if (u == 0x80000000u) u = 0;
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Exclusive sums over the CTA's threads, and the sum of all.
+__device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t (&warps)[33], uint32_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    __syncthreads();  // (the sums of a scan before have been read)
+    if (lane == 31) warps[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        const uint32_t w = warps[lane];
+        uint32_t s = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        warps[lane] = s - w;
+        if (lane == 31) warps[32] = s;
+    }
+    __syncthreads();
+    total = warps[32];
+    return warps[warp] + incl - v;
+}
+
+__global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_constant__ EvictProblem p, int ctas, int held) {
+    extern __shared__ __align__(16) uint32_t keys[];
+    __shared__ uint32_t hist[3][kBins];
+    __shared__ uint32_t warps[33], found[2], mine_above[2];
+    const int item = blockIdx.x / ctas, rank = blockIdx.x - item * ctas;
+    const int b = item / p.cache.heads, h = item - b * p.cache.heads;
+    for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const Budget g = budget_of(p, b, h == 0 && rank == 0 && threadIdx.x == 0);
+    const int64_t room = p.new_stride << p.cache.page_log2;
+    int* const kept = p.kept + item * room;
+    if (h == 0 && rank == 0 && threadIdx.x == 0) p.new_lens[b] = g.count;
+    const int64_t me = static_cast<int64_t>(rank) * kThreads + threadIdx.x, all = static_cast<int64_t>(ctas) * kThreads;
+    for (int64_t i = g.count + me; i < room; i += all) kept[i] = -1;
+    if (g.count == g.len || g.count == 0) {  // (the whole cluster)
+        for (int64_t i = me; i < g.count; i += all) kept[i] = static_cast<int>(i);
+        return;
+    }
+
+    // This CTA's tokens: [begin, end), begin a multiple of 4.
+    const int64_t run = ((static_cast<int64_t>(g.len) + ctas - 1) / ctas + 3) & ~int64_t{3};
+    const int64_t begin64 = rank * run;
+    const int begin = static_cast<int>(begin64 < g.len ? begin64 : g.len);
+    const int n = static_cast<int>(begin64 + run < g.len ? run : g.len - begin);
+    const int* table = p.page_table + static_cast<int64_t>(b) * p.table_stride;
+    auto read = [&](int i) -> uint4 {  // the numbers of tokens begin + i .. + 3
+        const int pos = begin + i, page = ld_dep_s32(table + (pos >> p.cache.page_log2));
+        uint4 w = make_uint4(0x7FFFFFFFu, 0x7FFFFFFFu, 0x7FFFFFFFu, 0x7FFFFFFFu);
+        if (page >= 0 && page < p.cache.num_pages)
+            w = ld_dep_v4(p.mass + ((static_cast<int64_t>(page) * p.cache.heads + h) << p.cache.page_log2) +
+                          (pos & ((1 << p.cache.page_log2) - 1)));
+        else
+            atomicOr(&g_evict_index_error, 1u);
+        uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            u[j] = ordered(__uint_as_float(u[j]));
+            if (pos + j >= g.len - g.recent || pos + j < g.first) u[j] = 0xFFFFFFFFu;
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    };
+    auto again = [&](int i) { return i < held ? *reinterpret_cast<const uint4*>(keys + i) : read(i); };
+    auto each = [&](int i, const uint4& k, auto f) {  // of those there are
+        f(k.x);
+        if (i + 1 < n) f(k.y);
+        if (i + 2 < n) f(k.z);
+        if (i + 3 < n) f(k.w);
+    };
+    __syncthreads();
+
+    uint32_t want = g.count, prefix = 0;  // the want-th largest of those whose upper bits are `prefix`
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, top = pass == 0 ? 32 : pass == 1 ? 21 : 10;
+        const uint32_t mask = pass == 2 ? 1023u : 2047u;
+        uint32_t* const count = hist[pass];
+        if (pass == 0) {
+#pragma unroll 4
+            for (int i = threadIdx.x * 4; i < n; i += kThreads * 4) {
+                const uint4 k = read(i);
+                if (i < held) *reinterpret_cast<uint4*>(keys + i) = k;
+                each(i, k, [&](uint32_t u) { atomicAdd(count + (u >> 21), 1u); });
+            }
+        } else {
+            for (int i = threadIdx.x * 4; i < n; i += kThreads * 4)
+                each(i, again(i), [&](uint32_t u) {
+                    if (u >> top == prefix) atomicAdd(count + (u >> shift & mask), 1u);
+                });
+        }
+        if (ctas > 1)
+            ptx::cluster_sync();
+        else
+            __syncthreads();
+        // Counts from the largest bin down, two a thread.
+        const int bin = kBins - 2 - 2 * static_cast<int>(threadIdx.x);
+        uint32_t lo = 0, hi = 0;
+        if (ctas > 1) {
+            const uint32_t at = ptx::smem_u32(count + bin);
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                if (r < ctas) {
+                    const uint32_t from = ptx::mapa_shared(at, r);
+                    lo += ld_shared_cluster_u32(from);
+                    hi += ld_shared_cluster_u32(from + 4);
+                }
+        } else {
+            lo = count[bin];
+            hi = count[bin + 1];
+        }
+        uint32_t total;
+        const uint32_t above = scan(lo + hi, warps, total);
+        if (above < want && want <= above + lo + hi) {
+            const bool upper = want <= above + hi;
+            found[0] = bin + (upper ? 1 : 0);
+            found[1] = want - above - (upper ? 0 : hi);
+        }
+        __syncthreads();
+        prefix = prefix << (pass == 2 ? 10 : 11) | found[0];
+        want = found[1];
+    }
+    const uint32_t threshold = prefix;  // `want` of those equal to it stay
+
+    // Tokens above the threshold and equal to it in the CTAs before this one.
+    uint32_t base_above = 0, base_equal = 0;
+    if (ctas > 1) {
+        uint32_t above = 0, equal = 0;
+        for (int i = threadIdx.x * 4; i < n; i += kThreads * 4)
+            each(i, again(i), [&](uint32_t u) {
+                above += u > threshold;
+                equal += u == threshold;
+            });
+        uint32_t total_above, total_equal;
+        scan(above, warps, total_above);
+        scan(equal, warps, total_equal);
+        if (threadIdx.x == 0) {
+            mine_above[0] = total_above;
+            mine_above[1] = total_equal;
+        }
+        ptx::cluster_sync();
+        const uint32_t at = ptx::smem_u32(mine_above);
+        for (int r = 0; r < rank; ++r) {
+            const uint32_t from = ptx::mapa_shared(at, r);
+            base_above += ld_shared_cluster_u32(from);
+            base_equal += ld_shared_cluster_u32(from + 4);
+        }
+    }
+    for (int i0 = 0; i0 < n; i0 += kThreads * 4) {
+        const int i = i0 + threadIdx.x * 4;
+        uint32_t here = 0;  // above in the lower half, equal in the upper: at most 4096 of each
+        const uint4 k = i < n ? again(i) : make_uint4(0, 0, 0, 0);
+        if (i < n) each(i, k, [&](uint32_t u) { here += u > threshold ? 1u : u == threshold ? 1u << 16 : 0u; });
+        uint32_t total;
+        const uint32_t before = scan(here, warps, total);
+        uint32_t above = base_above + (before & 0xFFFFu), equal = base_equal + (before >> 16);
+        int pos = begin + i;
+        if (i < n)
+            each(i, k, [&](uint32_t u) {
+                if (u > threshold || (u == threshold && equal < want)) kept[above + min(equal, want)] = pos;
+                above += u > threshold;
+                equal += u == threshold;
+                ++pos;
+            });
+        base_above += total & 0xFFFFu;
+        base_equal += total >> 16;
+    }
+    if (ctas > 1) ptx::cluster_sync();  // no CTA leaves while another reads its counts
+}
+
+constexpr int kCopyTokens = 64, kCopyThreads = 256;
+
+template <int kD>
+__global__ void __launch_bounds__(kCopyThreads) kv_evict_copy_kernel(const __grid_constant__ EvictProblem p, int chunks) {
+    __shared__ int64_t from[kCopyTokens], to[kCopyTokens];
+    const int64_t item = blockIdx.x / static_cast<unsigned>(chunks);
+    const int chunk = blockIdx.x % static_cast<unsigned>(chunks);
+    const int b = static_cast<int>(item / p.cache.heads), h = static_cast<int>(item % p.cache.heads);
+    const KvCache& c = p.cache;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int64_t at = static_cast<int64_t>(chunk) * kCopyTokens;
+    const Budget g = budget_of(p, b, false);
+    if (at >= g.count) return;
+    const int n = static_cast<int>(min(static_cast<int64_t>(kCopyTokens), g.count - at));
+    if (threadIdx.x < kCopyTokens) {
+        int64_t src = -1, dst = -1;
+        if (static_cast<int>(threadIdx.x) < n) {
+            const int in_page = (1 << c.page_log2) - 1, i = static_cast<int>(at) + threadIdx.x;
+            const int pos = ld_dep_s32(p.kept + ((item * p.new_stride) << c.page_log2) + i);
+            const int a = ld_dep_s32(p.page_table + b * p.table_stride + (pos >> c.page_log2));
+            const int z = ld_dep_s32(p.new_table + b * p.new_stride + (i >> c.page_log2));
+            if (a >= 0 && a < c.num_pages && z >= 0 && z < c.num_pages) {
+                src = ((static_cast<int64_t>(a) * c.heads + h) << c.page_log2) + (pos & in_page);
+                dst = ((static_cast<int64_t>(z) * c.heads + h) << c.page_log2) + (i & in_page);
+            } else {
+                atomicOr(&g_evict_index_error, 1u);
+            }
+        }
+        from[threadIdx.x] = src;
+        to[threadIdx.x] = dst;
+    }
+    __syncthreads();
+    constexpr int kC = kD / 16, kSteps = kCopyTokens * kC / kCopyThreads;  // 16-byte chunks of a vector; a thread's
+    const int col = threadIdx.x % kC, row = threadIdx.x / kC;
+    const uint4 *k = reinterpret_cast<const uint4*>(c.k) + col, *v = reinterpret_cast<const uint4*>(c.v) + col;
+    uint4 x[kSteps], y[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int64_t src = from[row + i * (kCopyThreads / kC)];
+        if (src >= 0) {
+            x[i] = ld_dep_stream_v4(k + src * kC);
+            y[i] = ld_dep_stream_v4(v + src * kC);
+        }
+    }
+    float s0 = 0.0f;
+    const int which = threadIdx.x / kCopyTokens;  // key scales, value scales, weights
+    float* const words = which == 0 ? c.k_scale : which == 1 ? c.v_scale : p.mass;
+    const int64_t src = from[threadIdx.x % kCopyTokens], dst = to[threadIdx.x % kCopyTokens];
+    if (which < 3 && src >= 0) s0 = ld_dep_f32(words + src);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int64_t z = to[row + i * (kCopyThreads / kC)];
+        if (z >= 0) {
+            reinterpret_cast<uint4*>(c.k)[z * kC + col] = x[i];
+            reinterpret_cast<uint4*>(c.v)[z * kC + col] = y[i];
+        }
+    }
+    if (which < 3 && dst >= 0) words[dst] = s0;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_evict(const EvictProblem& p, int num_sms, cudaStream_t stream) {
+    const int items = p.batch * p.cache.heads;
+    const int64_t most = p.table_stride << p.cache.page_log2;
+    // A cluster while the SMs are not full and a CTA has work for every thread.
+    int ctas = 1;
+    while (ctas < kMaxCluster && 2 * ctas * static_cast<int64_t>(items) <= num_sms && most > ctas * int64_t{4 * kThreads}) ctas *= 2;
+    const int64_t run = ((most + ctas - 1) / ctas + 3) & ~int64_t{3};
+    const int held = static_cast<int>(run < kMostKeys ? run : kMostKeys);
+    static std::atomic<bool> configured[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!configured[dev & 63].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(kv_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4);
+        if (e != cudaSuccess) return e;
+        configured[dev & 63].store(true, std::memory_order_relaxed);
+    }
+    cudaError_t e = launch_dependent(kv_evict_select_kernel, dim3(items * ctas), kThreads, held * 4, stream, ctas, p, ctas, held);
+    if (e != cudaSuccess) return e;
+    const int64_t chunks = ((p.new_stride << p.cache.page_log2) + kCopyTokens - 1) / kCopyTokens;
+    if (chunks == 0) return cudaSuccess;
+    auto copy = p.cache.head_dim == 64 ? kv_evict_copy_kernel<64> : p.cache.head_dim == 128 ? kv_evict_copy_kernel<128> : kv_evict_copy_kernel<256>;
+    return launch_dependent(copy, dim3(static_cast<unsigned>(items * chunks)), kCopyThreads, 0, stream, 1, p, static_cast<int>(chunks));
+}
+
+unsigned int read_and_clear_evict_index_error() {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_evict_index_error, sizeof(v)) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (v) {
+        const unsigned int zero = 0;
+        cudaMemcpyToSymbol(g_evict_index_error, &zero, sizeof(zero));
+    }
+    return v;
+}
+
+}  // namespace fp8act

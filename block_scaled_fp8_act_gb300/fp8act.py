@@ -89,10 +89,12 @@ def load(build: bool = False) -> ctypes.CDLL:
     L.fp8_kv_attention.argtypes = [p, i64, p, p, p, i, i, i, i, i, f, p, p, p, p, ctypes.c_size_t, p]
     L.fp8_kv_attention_workspace.argtypes = [i, i, p]
     L.fp8_kv_attention_workspace.restype = ctypes.c_size_t
+    L.fp8_kv_evict.argtypes = [p, p, p, i, p, p, p, i, i, i, i, p, p, p]
     L.fp8act_verify_drafts.argtypes = [p, p, i, p, p, p, p, p, i, i, i, p, p, p, p, ctypes.c_size_t, p]
     L.fp8act_verify_drafts_workspace.argtypes = [i, i]
     L.fp8act_verify_drafts_workspace.restype = ctypes.c_size_t
     for fn in (L.fp8_rmsnorm_quant, L.fp8_silu_mul_quant, L.fp8_kv_append, L.fp8_rope_append, L.fp8_kv_attention,
+               L.fp8_kv_evict,
                L.fp8act_verify_drafts, L.fp8_act_quant, L.fp8_weight_quant, L.fp8_block_gemm, L.fp8_block_gemm_f32,
                L.fp8_block_gemm_w8a16, L.fp8_block_gemm_w8a16_f32,
                L.fp8_act_quant_grouped, L.fp8_block_gemm_grouped, L.fp8_block_gemm_grouped_f32,
@@ -394,6 +396,22 @@ def fp8_kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len: int | None 
     caller per stream; without one the binding keeps its own per device and stream."""
     return _native().kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, out, lse, workspace,
                                   stream)
+
+
+def kv_mass(cache) -> torch.Tensor:
+    """Zeroed weights of a cache's tokens, fp32 [pages, kv_heads, page_size]."""
+    return torch.zeros_like(cache[2])
+
+
+def fp8_kv_evict(cache, mass, page_table, kv_lens, keep, new_table, recent: int = 0, first: int = 0, new_lens=None,
+                 kept=None, stream=None):
+    """Copies the tokens that matter most into other pages -> (new_lens int32 [B], kept int32 [B, kv_heads, places]).
+
+    Of each sequence and KV head min(kv_lens, keep) tokens stay (keep int32 [B]): the last `recent`, the first
+    `first`, then those of largest `mass` (fp32 [pages, kv_heads, page_size]; equal ones by position). They go,
+    in their order, with their scales and masses to the pages of new_table (int32 [B, new_pages], none of them in
+    use); `kept` holds the positions they had, -1 from new_lens on. The old pages are not written."""
+    return _native().kv_evict(cache, mass, page_table, kv_lens, keep, new_table, recent, first, new_lens, kept, stream)
 
 
 def verify_drafts_workspace(B: int, k: int) -> int:

@@ -381,6 +381,30 @@ FP8ACT_API int fp8_kv_attention(const void* q_bf16, int64_t q_stride, const int*
 FP8ACT_API size_t fp8_kv_attention_workspace(int max_q_len, int q_heads, const fp8act_kv_cache* cache);
 
 /*
+ * Eviction from the cache: of each sequence and KV head the
+ * n = min(kv_lens[b], keep[b]) tokens that matter most are copied, in their
+ * order, to places 0 .. n - 1 of the sequence's pages in new_table: codes, scales
+ * and weights. What matters: the last `recent` tokens first (at most n), then the
+ * first `first` tokens (at most what is left of n), then the tokens of largest
+ * mass; of equal ones the lower position. A mass of NaN counts as -infinity. KV
+ * heads choose by themselves, so place i of two heads may hold different tokens.
+ * The old pages are left as they are (other sequences may share them) and may be
+ * given back once the call has run; new tokens go on at place n of the new ones.
+ *   mass        [num_pages, kv_heads, page_size] fp32, 16-byte aligned: the weight
+ *               of every cached token, as fp8_kv_attention_mass adds it up
+ *   page_table  [batch, max_pages] int32;  kv_lens [batch] int32
+ *   keep        [batch] int32, 0 .. new_pages * page_size
+ *   new_table   [batch, new_pages] int32, pages that stand once and in no row of
+ *               page_table (a page that does may hold either's tokens after)
+ *   new_lens    [batch] int32 out: n; neither kv_lens nor keep
+ *   kept        [batch, kv_heads, new_pages * page_size] int32 out: the positions
+ *               that the places' tokens had, -1 from n on
+ */
+FP8ACT_API int fp8_kv_evict(const fp8act_kv_cache* cache, float* mass, const int* page_table, int max_pages,
+                            const int* kv_lens, const int* keep, const int* new_table, int new_pages, int batch,
+                            int recent, int first, int* new_lens, int* kept, void* stream);
+
+/*
  * Verification of drafted tokens (speculative sampling) from given random
  * numbers. p_j = softmax(target[b, j] / T), q_j = softmax(draft[b, j] / T)
  * with T = temperature[b]; with draft == NULL the drafts were chosen greedily

@@ -37,3 +37,23 @@ def test_binding_rejects_what_is_not_on_the_gpu(lib):  # noqa: F811
     x, i = torch.zeros((1, 1, 64), dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int64)
     with pytest.raises(TypeError):
         fp8act.fp8_rope_append(x, x, x, i, torch.zeros(32, dtype=torch.float64), i, c)
+
+
+def evict(lib, mass=A16, table=A16, mp=4, lens=A16, keep=A16 + 64, new=A16, np=2, B=1, recent=0, first=0, out=A16 + 128, kept=A16,  # noqa: F811
+          c=None, **kw):
+    return lib.fp8_kv_evict(ctypes.byref(cache(**kw)) if c is None else c, mass, table, mp, lens, keep, new, np, B, recent, first,
+                            out, kept, None)
+
+
+def test_evict_argument_checks(lib):  # noqa: F811
+    for bad in (dict(page=24), dict(dim=96), dict(B=-1), dict(mp=-1), dict(np=-1), dict(recent=-1), dict(first=-1), dict(mp=1 << 26),
+                dict(np=1 << 26), dict(B=1 << 30), dict(np=1 << 20, B=1 << 12), dict(pages=0), dict(out=A16), dict(out=A16 + 64)):
+        assert evict(lib, **bad) == SHAPE, bad
+    assert evict(lib, B=0, mass=None, lens=None) == OK
+    for name in ("mass", "table", "lens", "keep", "new", "out", "kept"):
+        assert evict(lib, **{name: None}) == NULL, name
+    for bad in (dict(mass=A16 + 8), dict(table=A16 + 2), dict(lens=A16 + 1), dict(keep=A16 + 2), dict(new=A16 + 3), dict(out=A16 + 2),
+                dict(kept=A16 + 2)):
+        assert evict(lib, **bad) == ALIGN, bad
+    if not torch.cuda.is_available():
+        assert evict(lib) == DEVICE and evict(lib, np=0, new=None, kept=None) == DEVICE
