@@ -291,11 +291,26 @@ PyObject* rope_append(PyObject* const* a) {
     return THPVariable_Wrap(out);
 }
 
-// (q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, out, lse, workspace, stream) -> out
-PyObject* kv_attention(PyObject* const* a) {
+int to_count(PyObject* o, const char* name) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Raised{};
+    if (v < INT32_MIN) raise(PyExc_ValueError, std::string(name) + " is too small");
+    return to_int(v, name);
+}
+
+// What attention and its weights have in common: (q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale).
+struct Rows {
+    fp8act_kv_cache c;
+    const at::Tensor& q;
+    int64_t q_stride, T, Hq;
+    int pages, B, max_q;
+    const int *table, *lens, *cu;
+    double scale;
+};
+Rows rows_of(PyObject* const* a) {
     const fp8act_kv_cache c = cache_of(a[1]);
     const at::Tensor &q = tensor(a[0], "q"), &table = tensor(a[2], "page_table");
-    const int64_t qs = heads_of(q, -1, c.head_dim, "q"), T = q.size(0), Hq = q.size(1);
+    const int64_t qs = heads_of(q, -1, c.head_dim, "q"), T = q.size(0);
     if (table.dim() != 2) raise(PyExc_ValueError, "page_table must be 2-D [B, max_pages]");
     const int64_t B = table.size(0), pages = table.size(1);
     const int* tp = data<int>(table, kI32, {B, pages}, "page_table");
@@ -304,23 +319,55 @@ PyObject* kv_attention(PyObject* const* a) {
     const int64_t most = given(a[5]) ? PyLong_AsLongLong(a[5]) : T == B ? 1 : T;
     const double scale = given(a[6]) ? PyFloat_AsDouble(a[6]) : 1.0 / std::sqrt(static_cast<double>(c.head_dim));
     if (PyErr_Occurred()) throw Raised{};
+    to_int(T, "tokens");
+    to_int(q.size(1), "q_heads");
+    return {c, q, qs, T, q.size(1), to_int(pages, "max_pages"), to_int(B, "B"), to_int(most, "max_q_len"), tp, lens, cu, scale};
+}
+
+// (soft_cap, window, prefix_lens, first, slopes)
+fp8act_scores scores_of(PyObject* const* a, const Rows& r) {
+    fp8act_scores s = {};
+    s.soft_cap = given(a[0]) ? static_cast<float>(PyFloat_AsDouble(a[0])) : 0.0f;
+    if (PyErr_Occurred()) throw Raised{};
+    s.window = given(a[1]) ? to_count(a[1], "window") : 0;
+    s.prefix_lens = optional<int>(a[2], kI32, {r.B}, "prefix_lens");
+    s.first = optional<int>(a[3], kI32, {r.T}, "first");
+    s.slopes = optional<float>(a[4], kF32, {r.Hq}, "slopes");
+    return s;
+}
+
+// (q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, out, lse, workspace, stream, soft_cap, window,
+//  prefix_lens, first, slopes) -> out
+PyObject* kv_attention(PyObject* const* a) {
+    const Rows r = rows_of(a);
+    const fp8act_scores s = scores_of(a + 11, r);
     cudaStream_t stream = stream_of(a[10]);
-    at::Tensor out = output(a[7], kBf16, {T, Hq, c.head_dim}, q, stream, "out");
-    void* op = data(out, kBf16, {T, Hq, c.head_dim}, "out");
-    float* lse = optional<float>(a[8], kF32, {T, Hq}, "lse");
-    const int max_q = to_int(most, "max_q_len"), hq = to_int(Hq, "q_heads");
-    const Workspace w = workspace(a[9], fp8_kv_attention_workspace(max_q, hq, &c), q, stream);
-    check("fp8_kv_attention", fp8_kv_attention(q.data_ptr(), qs, cu, lens, tp, to_int(pages, "max_pages"), to_int(B, "B"),
-                                               to_int(T, "tokens"), max_q, hq, static_cast<float>(scale), &c, op, lse, w.p,
-                                               w.bytes, stream));
+    const int64_t D = r.c.head_dim;
+    at::Tensor out = output(a[7], kBf16, {r.T, r.Hq, D}, r.q, stream, "out");
+    void* op = data(out, kBf16, {r.T, r.Hq, D}, "out");
+    float* lse = optional<float>(a[8], kF32, {r.T, r.Hq}, "lse");
+    const int hq = static_cast<int>(r.Hq);
+    const Workspace w = workspace(a[9], fp8_kv_attention_workspace(r.max_q, hq, &r.c), r.q, stream);
+    check("fp8_kv_attention",
+          fp8_kv_attention_scored(r.q.data_ptr(), r.q_stride, r.cu, r.lens, r.table, r.pages, r.B, static_cast<int>(r.T), r.max_q,
+                                  hq, static_cast<float>(r.scale), &s, &r.c, op, lse, w.p, w.bytes, stream));
     return THPVariable_Wrap(out);
 }
 
-int to_count(PyObject* o, const char* name) {
-    const long long v = PyLong_AsLongLong(o);
-    if (v == -1 && PyErr_Occurred()) throw Raised{};
-    if (v < INT32_MIN) raise(PyExc_ValueError, std::string(name) + " is too small");
-    return to_int(v, name);
+// (q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, lse, mass, accumulate, stream, soft_cap, window,
+//  prefix_lens, first, slopes)
+PyObject* kv_attention_mass(PyObject* const* a) {
+    const Rows r = rows_of(a);
+    const fp8act_scores s = scores_of(a + 11, r);
+    const float* lse = data<float>(a[7], kF32, {r.T, r.Hq}, "lse");
+    float* mass = data<float>(a[8], kF32, {r.c.num_pages, r.c.kv_heads, r.c.page_size}, "mass");
+    const int accumulate = PyObject_IsTrue(a[9]);
+    if (accumulate < 0) throw Raised{};
+    check("fp8_kv_attention_mass",
+          fp8_kv_attention_mass(r.q.data_ptr(), r.q_stride, r.cu, r.lens, r.table, r.pages, r.B, static_cast<int>(r.T), r.max_q,
+                                static_cast<int>(r.Hq), static_cast<float>(r.scale), &s, &r.c, lse, mass, accumulate,
+                                stream_of(a[10])));
+    Py_RETURN_NONE;
 }
 
 // (cache, mass, page_table, kv_lens, keep, new_table, recent, first, new_lens, kept, stream) -> (new_lens, kept)
@@ -402,7 +449,8 @@ PyMethodDef g_methods[] = {
     {"silu_mul_quant", fast<silu_mul_quant, 4>(), METH_FASTCALL, nullptr},
     {"kv_append", fast<kv_append, 5>(), METH_FASTCALL, nullptr},
     {"rope_append", fast<rope_append, 16>(), METH_FASTCALL, nullptr},
-    {"kv_attention", fast<kv_attention, 11>(), METH_FASTCALL, nullptr},
+    {"kv_attention", fast<kv_attention, 16>(), METH_FASTCALL, nullptr},
+    {"kv_attention_mass", fast<kv_attention_mass, 16>(), METH_FASTCALL, nullptr},
     {"kv_evict", fast<kv_evict, 11>(), METH_FASTCALL, nullptr},
     {"verify_drafts", fast<verify_drafts, 12>(), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},

@@ -222,6 +222,36 @@ int check_cache(const fp8act_kv_cache* c, fp8act::KvCache* out) {
     return FP8ACT_OK;
 }
 
+// What attention over the cache and its weights have in common.
+int check_rows(const fp8act::KvCache& c, int64_t q_stride, int max_pages, int batch, int tokens, int max_q_len, int q_heads,
+               float softmax_scale) {
+    if (batch < 0 || tokens < 0 || max_pages < 0 || max_q_len < 0 || max_q_len > kMaxQLen || q_heads <= 0 ||
+        q_heads % c.heads || q_heads / c.heads > 256 || q_stride < static_cast<int64_t>(q_heads) * c.head_dim ||
+        static_cast<int64_t>(max_pages) << c.page_log2 > 0x7FFFFF00 ||
+        static_cast<int64_t>(tokens) * (q_heads / c.heads) > 0x7FFFFF00)
+        return FP8ACT_ERR_SHAPE;
+    if (!(softmax_scale > 0.0f) || softmax_scale > 3e38f) return FP8ACT_ERR_SHAPE;
+    return FP8ACT_OK;
+}
+
+// The caller's score function as the kernels take it, in units of log2.
+int check_scores(const fp8act_scores* in, fp8act::Scores* out, bool* scored) {
+    *out = {};
+    *scored = false;
+    if (!in) return FP8ACT_OK;
+    if (in->window < 0 || !(in->soft_cap == 0.0f || (in->soft_cap >= 1e-30f && in->soft_cap <= 1e30f)))
+        return FP8ACT_ERR_SHAPE;
+    out->cap = in->soft_cap * 1.4426950408889634f;
+    out->cap_inv = in->soft_cap > 0.0f ? 1.0f / out->cap : 0.0f;
+    out->window = in->window;
+    out->prefix = in->prefix_lens;
+    out->first = in->first;
+    out->slopes = in->slopes;
+    *scored = in->soft_cap > 0.0f || in->window || in->prefix_lens || in->first || in->slopes;
+    return FP8ACT_OK;
+}
+bool aligned_scores(const fp8act::Scores& s) { return aligned(s.prefix, 4) && aligned(s.first, 4) && aligned(s.slopes, 4); }
+
 }  // namespace
 
 namespace fp8act {
@@ -406,20 +436,27 @@ int fp8_kv_attention(const void* q_bf16, int64_t q_stride, const int* cu_q, cons
                      int max_pages, int batch, int tokens, int max_q_len, int q_heads, float softmax_scale,
                      const fp8act_kv_cache* cache, void* out_bf16, float* lse, void* workspace,
                      size_t workspace_bytes, void* stream) {
+    return fp8_kv_attention_scored(q_bf16, q_stride, cu_q, kv_lens, page_table, max_pages, batch, tokens, max_q_len,
+                                   q_heads, softmax_scale, nullptr, cache, out_bf16, lse, workspace, workspace_bytes,
+                                   stream);
+}
+
+int fp8_kv_attention_scored(const void* q_bf16, int64_t q_stride, const int* cu_q, const int* kv_lens,
+                            const int* page_table, int max_pages, int batch, int tokens, int max_q_len, int q_heads,
+                            float softmax_scale, const fp8act_scores* scores, const fp8act_kv_cache* cache,
+                            void* out_bf16, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
     fp8act::KvCache c;
     if (int st = check_cache(cache, &c)) return st;
-    if (batch < 0 || tokens < 0 || max_pages < 0 || max_q_len < 0 || max_q_len > kMaxQLen || q_heads <= 0 ||
-        q_heads % c.heads || q_heads / c.heads > 256 || q_stride < static_cast<int64_t>(q_heads) * c.head_dim ||
-        static_cast<int64_t>(max_pages) << c.page_log2 > 0x7FFFFF00 ||
-        static_cast<int64_t>(tokens) * (q_heads / c.heads) > 0x7FFFFF00)
-        return FP8ACT_ERR_SHAPE;
-    if (!(softmax_scale > 0.0f) || softmax_scale > 3e38f) return FP8ACT_ERR_SHAPE;
+    if (int st = check_rows(c, q_stride, max_pages, batch, tokens, max_q_len, q_heads, softmax_scale)) return st;
+    fp8act::Scores s;
+    bool scored = false;
+    if (int st = check_scores(scores, &s, &scored)) return st;
     if (batch == 0 || tokens == 0) return FP8ACT_OK;
     if (c.num_pages == 0) return FP8ACT_ERR_SHAPE;
     if (!q_bf16 || !cu_q || !kv_lens || !out_bf16 || !workspace || (max_pages > 0 && !page_table))
         return FP8ACT_ERR_NULL;
     if (!aligned(q_bf16, 16) || q_stride % 8 || !aligned(out_bf16, 16) || !aligned(workspace, 16) || !aligned(cu_q, 4) ||
-        !aligned(kv_lens, 4) || !aligned(page_table, 4) || !aligned(lse, 4))
+        !aligned(kv_lens, 4) || !aligned(page_table, 4) || !aligned(lse, 4) || !aligned_scores(s))
         return FP8ACT_ERR_ALIGN;
     if (workspace_bytes < fp8act::kv_attention_workspace(max_q_len, q_heads / c.heads, c.head_dim))
         return FP8ACT_ERR_SHAPE;
@@ -428,8 +465,33 @@ int fp8_kv_attention(const void* q_bf16, int64_t q_stride, const int* cu_q, cons
     if (st) return st;
     const fp8act::AttentionProblem p = {q_bf16,    q_stride,  cu_q,          kv_lens, page_table, max_pages,
                                         batch,     tokens,    max_q_len,     q_heads / c.heads,   softmax_scale,
-                                        c,         out_bf16,  lse,           workspace};
+                                        c,         out_bf16,  lse,           workspace,           scored, s};
     return launch_status(fp8act::launch_kv_attention(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int fp8_kv_attention_mass(const void* q_bf16, int64_t q_stride, const int* cu_q, const int* kv_lens,
+                          const int* page_table, int max_pages, int batch, int tokens, int max_q_len, int q_heads,
+                          float softmax_scale, const fp8act_scores* scores, const fp8act_kv_cache* cache,
+                          const float* lse, float* mass, int accumulate, void* stream) {
+    fp8act::KvCache c;
+    if (int st = check_cache(cache, &c)) return st;
+    if (int st = check_rows(c, q_stride, max_pages, batch, tokens, max_q_len, q_heads, softmax_scale)) return st;
+    fp8act::Scores s;
+    bool scored = false;
+    if (int st = check_scores(scores, &s, &scored)) return st;
+    if (batch == 0) return FP8ACT_OK;
+    if (c.num_pages == 0) return FP8ACT_ERR_SHAPE;
+    if (!cu_q || !kv_lens || !mass || (tokens > 0 && (!q_bf16 || !lse)) || (max_pages > 0 && !page_table))
+        return FP8ACT_ERR_NULL;
+    if (!aligned(q_bf16, 16) || q_stride % 8 || !aligned(cu_q, 4) || !aligned(kv_lens, 4) || !aligned(page_table, 4) ||
+        !aligned(lse, 4) || !aligned(mass, 16) || !aligned_scores(s))
+        return FP8ACT_ERR_ALIGN;
+    int st = FP8ACT_OK;
+    const int sms = current_device_sms(&st);
+    if (st) return st;
+    const fp8act::MassProblem p = {q_bf16, q_stride, cu_q, kv_lens, page_table, max_pages, batch, tokens, max_q_len,
+                                   q_heads / c.heads, softmax_scale, c, lse, mass, accumulate != 0, scored, s};
+    return launch_status(fp8act::launch_kv_mass(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int fp8_kv_evict(const fp8act_kv_cache* cache, float* mass, const int* page_table, int max_pages, const int* kv_lens,
@@ -515,7 +577,8 @@ int fp8act_check_status(void* stream) {
     const unsigned int mid = fp8act::read_and_clear_midm_error();
     const unsigned int rd = fp8act::read_and_clear_read_error();
     const unsigned int index = fp8act::read_and_clear_kv_index_error() | fp8act::read_and_clear_rope_index_error() |
-                               fp8act::read_and_clear_attn_index_error() | fp8act::read_and_clear_evict_index_error() |
+                               fp8act::read_and_clear_attn_index_error() | fp8act::read_and_clear_mass_index_error() |
+                               fp8act::read_and_clear_evict_index_error() |
                                fp8act::read_and_clear_verify_index_error();
     const unsigned int at = fp8act::read_and_clear_attn_timeout();
     if (tc | mid | rd | at) return FP8ACT_ERR_TIMEOUT;

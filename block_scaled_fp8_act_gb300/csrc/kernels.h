@@ -146,6 +146,16 @@ struct RopeProblem {
 };
 cudaError_t launch_rope_append(const RopeProblem& p, int num_sms, cudaStream_t stream);
 
+// What an attention score is beside the scaled product (see scores.cuh); cap
+// in units of log2. All zero: nothing.
+struct Scores {
+    float cap, cap_inv;
+    int window;
+    const int* prefix;    // [batch] or null
+    const int* first;     // [tokens] or null
+    const float* slopes;  // [q_heads] or null
+};
+
 // Attention of `tokens` new tokens of `batch` sequences over the cache.
 struct AttentionProblem {
     const void* q;
@@ -160,9 +170,30 @@ struct AttentionProblem {
     void* out;
     float* lse;
     void* workspace;
+    bool scored;  // whether `scores` says anything
+    Scores scores;
 };
 size_t kv_attention_workspace(int max_q_len, int group, int head_dim);
 cudaError_t launch_kv_attention(const AttentionProblem& p, int num_sms, cudaStream_t stream);
+
+// The attention weight of every cached token, added up over the rows of
+// `tokens` new tokens whose log-sum-exp the attention left.
+struct MassProblem {
+    const void* q;
+    int64_t q_stride;
+    const int* cu_q;
+    const int* kv_lens;
+    const int* page_table;
+    int64_t table_stride;
+    int batch, tokens, max_q_len, group;
+    float softmax_scale;
+    KvCache cache;
+    const float* lse;
+    float* mass;  // [num_pages, heads, page]
+    bool accumulate, scored;
+    Scores scores;
+};
+cudaError_t launch_kv_mass(const MassProblem& p, int num_sms, cudaStream_t stream);
 
 // Eviction: per sequence and KV head the keep[b] tokens of the largest weight,
 // in their order, into the pages of new_table.
@@ -204,6 +235,7 @@ cudaError_t launch_verify_drafts(const VerifyProblem& p, int num_sms, cudaStream
 unsigned int read_and_clear_kv_index_error();
 unsigned int read_and_clear_rope_index_error();
 unsigned int read_and_clear_attn_index_error();
+unsigned int read_and_clear_mass_index_error();
 unsigned int read_and_clear_evict_index_error();
 unsigned int read_and_clear_attn_timeout();
 unsigned int read_and_clear_verify_index_error();

@@ -54,20 +54,9 @@ __device__ unsigned int g_attn_index_error;
 constexpr int kTile = 32;  // cached tokens per unit
 constexpr int kLeastUnits = 8;  // least share of a CTA
 constexpr int kItemCost = 20;   // units that an item counts beside its own
-using Work = Units<kTile, kItemCost>;
+template <bool kScored>
+using WorkOf = Units<kTile, kItemCost, kScored ? List::kScored : List::kPlain>;
 
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kN>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
-}
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // Transpose of an 8 x 8 matrix of 16-bit values held as an MMA fragment.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
     uint32_t r;
@@ -75,33 +64,11 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
     return r;
 }
 
-// A stage holds the cached codes as 128-byte lines, as the cache does (a token
-// is half a line, a line or two); chunk c of a line sits at c ^ (line % 8).
-// Byte offset of 16-byte chunk c of
-// token `row`:
-template <int kD>
-__device__ __forceinline__ uint32_t stage_offset(int row, int c) {
-    const int line = kD == 64 ? row >> 1 : kD == 128 ? row : row * 2 + (c >> 3);
-    const int chunk = kD == 64 ? ((row & 1) << 2) | c : c & 7;
-    return line * 128 + ((chunk ^ (line & 7)) << 4);
-}
-
-// The MMA's rows are the cached tokens of a block of 8 in an order of our own:
-// row i is token order<kD>(i). The 8 lanes of a shared-memory phase read 4
-// chunks of 2 neighbouring rows; the order gives those two tokens swizzles
-// that differ in bit 2, so that they read distinct banks.
-template <int kD>
-__device__ __forceinline__ int order(int i) {
-    if (kD == 64) return i;
-    if (kD == 128) return (i >> 1) | ((i & 1) << 2);
-    return ((i >> 1) & 1) | ((i & 1) << 1) | (i & 4);
-}
-
 // kWR warps of a group split the row tile, kRW groups of 8 rows each; kG groups in a CTA; kCtas CTAs per SM (two
 // where a group is one warp: one streams while the other starts or ends an item, 38 us instead of 46 for 34 ragged
 // sequences x 3 tokens; but one for D = 256, whose stages are twice as large: one token over 32768 with 8 heads on 4
 // 30.2 us instead of 42.2, two tokens of 8 ragged sequences 23.1 instead of 32.8).
-template <int kD, int kWR, int kRW, int kG, int kCtas_>
+template <int kD, int kWR, int kRW, int kG, int kCtas_, bool kScored>
 struct Attn {
     static constexpr int kCtas = kCtas_;
     static constexpr int kWarpRows = kRW * 8;
@@ -112,7 +79,7 @@ struct Attn {
     static constexpr int kQ = 0;
     static constexpr int kML = kQ + kRows * kD * 2;
     static constexpr int kQScale = kML + kG * kRows * 8;
-    static constexpr int kRing = (kQScale + kRows * 4 + 127) / 128 * 128;
+    static constexpr int kRing = (kQScale + kRows * (kScored ? 16 : 4) + 127) / 128 * 128;  // (kScored: RowScores)
     static constexpr int kFit = (226 * 1024 / kCtas - 1024 * (kCtas - 1) - kRing) / kG / kStageBytes;
     static constexpr int kStages = kFit < 8 ? kFit : kFit < 16 && kG > 1 ? 8 : kFit < 16 ? kFit : 16;
     static constexpr int kRingBytes = kStages * kStageBytes;
@@ -133,21 +100,23 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int q0, int h, int 
     if (a.lse && lane == 0) a.lse[at] = sum == 0.0f ? kNegInf : (m + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <int kD, int kWR, int kRW, int kG, int kCtas>
-__global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas)
+template <int kD, int kWR, int kRW, int kG, int kCtas, bool kScored>
+__global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas, kScored>::kThreads, kCtas)
     kv_attention_kernel(const __grid_constant__ AttnArgs a) {
-    using S = Attn<kD, kWR, kRW, kG, kCtas>;
+    using S = Attn<kD, kWR, kRW, kG, kCtas, kScored>;
+    using Work = WorkOf<kScored>;
     constexpr int kRows = S::kRows, kStages = S::kStages;
     constexpr int kKS = kD / 32;  // pairs of k-steps of the score product
     constexpr int kDT = kD / 16;  // 16-row tiles of the transposed output
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Work::Scratch scratch;
+    __shared__ typename Work::Scratch scratch;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
     const int og = order<kD>(g);                  // the token of a block of 8 that is the lane's MMA row
     const int vg = kD == 64 ? g : order<128>(g);  // the chunk of output columns that is the lane's (the same reason)
     const int group = warp / kWR, wr = warp % kWR;
     uint8_t* const ring = smem + S::kRing + group * S::kRingBytes;
     float* qscale = reinterpret_cast<float*>(smem + S::kQScale);
+    RowScore* row_scores = reinterpret_cast<RowScore*>(smem + S::kQScale);  // (in its place with kScored)
     float2* ml = reinterpret_cast<float2*>(smem + S::kML);
     auto group_sync = [&]() {
         if constexpr (kWR == 1)
@@ -173,13 +142,20 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
         const int nrows = rows_total - row0 < kRows ? rows_total - row0 : kRows;
         // This CTA's tiles [f0, f1): units past the item's cost, as far as some row of the tile sees.
         const int seen = max(it.len - it.nq + (row0 + nrows - 1) / a.group + 1, 0);
-        const int f0 = max(t0 - kItemCost, 0), f1 = min((seen + kTile - 1) / kTile, t1 - kItemCost);
+        const int f0 = max(t0 - kItemCost, 0);
+        int f1 = min((seen + kTile - 1) / kTile, t1 - kItemCost);
+        TileReach reach = {};
+        if constexpr (kScored) {
+            reach = tile_reach<kTile>(a, it, row0, nrows);
+            f1 = min(reach.tiles.end, t1 - kItemCost);
+        }
+        auto position = [&](int t) { return (kScored ? reach.tiles.at(t) : t) * kTile; };
 
         // The group's tiles are f0 + group, + kG, ... Pages of its next 16, one per 16 tokens and lane.
         const int* table = a.table + it.b * a.table_stride;
         auto look_up = [&](int t) -> int {
             t += (lane >> 1) * kG;
-            const int pos = t * kTile + (lane & 1) * 16;
+            const int pos = position(t) + (lane & 1) * 16;
             if (t >= f1 || pos >= it.len) return -1;
             const int p = ld_dep_s32(table + (pos >> a.c.page_log2));
             if (p >= 0 && p < a.c.num_pages) return p;
@@ -194,7 +170,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
                 const uint32_t dst = ptx::smem_u32(ring) + stage * S::kStageBytes;
                 constexpr int kC = kD / 16, kStep = 32 / kC;  // chunks per token, tokens per instruction
                 const int c = lane % kC, r0 = lane / kC;
-                const int pos0 = t * kTile, in_page = (1 << a.c.page_log2) - 1;
+                const int pos0 = position(t), in_page = (1 << a.c.page_log2) - 1;
                 const int64_t row_a = ((static_cast<int64_t>(p0) * a.c.heads + it.h) << a.c.page_log2) + (pos0 & in_page);
                 const int64_t row_b =
                     ((static_cast<int64_t>(p1) * a.c.heads + it.h) << a.c.page_log2) + ((pos0 + 16) & in_page) - 16;
@@ -247,38 +223,23 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
         for (int i = 0; i < kStages - 1; ++i) request(f0 + group + i * kG, i);
 
         // Queries: power-of-two scaled f16 in fragment order.
-        {
-            constexpr int kLanes = kD / 8;
-            static_assert(kLanes <= 32 && kRows % (32 / kLanes) == 0, "whole warps of rows");
-            const int c = threadIdx.x % kLanes;
-            for (int r = threadIdx.x / kLanes; r < kRows; r += S::kWarps * 32 / kLanes) {
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (r < nrows) {
-                    const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
-                    x = ld_dep_v4(a.q + (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD + c * 8);
+        stage_queries<kD, S::kThreads>(
+            smem + S::kQ, kRows,
+            [&](int r, int c) {
+                if (r >= nrows) return make_uint4(0, 0, 0, 0);
+                const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
+                return ld_dep_v4(a.q + (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD + c * 8);
+            },
+            [&](int r, float step) {
+                const float qs = fmaxf(step * a.scale_log2, 0x1p-126f);
+                if constexpr (kScored) {
+                    RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, row0 + r, a.index_error);
+                    info.qs = qs;
+                    row_scores[r] = info;
+                } else {
+                    qscale[r] = qs;
                 }
-                // (a warp's rows are all below kRows or none is, so that the whole warp is here)
-                uint32_t top = top_bits(x);
-#pragma unroll
-                for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                // (a zero row's exponent is as good as any)
-                const uint32_t e = top == 0 ? 127 : min(max(top >> 7, 1u), 253u);
-                const float up = __uint_as_float((254 - e) << 23);  // 2^(127 - e)
-                if (c == 0) qscale[r] = fmaxf(__uint_as_float(e << 23) * a.scale_log2, 0x1p-126f);
-                float f[8];
-                unpack_bf16x8(x, f);
-                uint32_t h[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const __half2 v = __floats2half2_rn(f[2 * j] * up, f[2 * j + 1] * up);
-                    h[j] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-                // d = 8c .. 8c + 7: two k-steps of lane (r & 7, (c % 8) / 2)
-                const int ks = (c / 8) * 2 + (c & 1);
-                reinterpret_cast<uint4*>(smem + S::kQ)[((r >> 3) * kKS + ks) * 32 + (r & 7) * 4 + (c % 8) / 2] =
-                    make_uint4(h[0], h[1], h[2], h[3]);
-            }
-        }
+            });
         __syncthreads();
 
         float acc[kDT][kRW][4];
@@ -297,7 +258,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
                 const int r = wr * S::kWarpRows + i * 8 + qd * 2 + e;
                 mq[i][e] = kNegInf;
                 l[i][e] = 0.0f;
-                qs[i][e] = qscale[r];
+                qs[i][e] = kScored ? 1.0f : qscale[r];  // (kScored: scores are whole before the softmax)
                 limit[i][e] = it.len - it.nq + (row0 + r) / a.group + 1;
             }
         }
@@ -368,15 +329,39 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas>::kThreads, kCtas
             }
             // Key scales and mask; exponents relative to the rows' references. A tile that every row sees whole needs
             // no mask.
-            const bool edge = t * kTile + kTile > all_see;
+            const int pos0 = position(t);
+            const bool edge = kScored ? on_edge(pos0, kTile, it.prefix, reach.lo, reach.limit) : pos0 + kTile > all_see;
             bool passed = __uint_as_float(rb) > r_ref;
-            auto masked = [&](int i, int x, int e) { return edge && t * kTile + x * 8 + og >= limit[i][e]; };
+            const RowScore* const info = row_scores + wr * S::kWarpRows + qd * 2;  // of rows i * 8 + e
+            auto masked = [&](int i, int x, int e) {
+                const int pos = pos0 + x * 8 + og;
+                if constexpr (kScored)
+                    return edge && pos >= it.prefix && (pos < info[i * 8 + e].lo || pos >= info[i * 8 + e].limit);
+                else
+                    return edge && pos >= limit[i][e];
+            };
 #pragma unroll
             for (int i = 0; i < kRW; ++i)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) s[x >> 1][i][(x & 1) * 2 + e] *= ks[x];
+            if constexpr (kScored) {
+#pragma unroll
+                for (int i = 0; i < kRW; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const RowScore row = info[i * 8 + e];
+                        const float far = static_cast<float>(row.limit - 1 - pos0 - og);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            float y = s[x >> 1][i][(x & 1) * 2 + e] * row.qs;
+                            if (a.scores.cap > 0.0f) y = capped(y, a.scores.cap, a.scores.cap_inv);
+                            if (a.scores.slopes) y = fmaf(-row.slope, fabsf(far - x * 8), y);
+                            s[x >> 1][i][(x & 1) * 2 + e] = y;
+                        }
+                    }
+            }
             if (edge) {
 #pragma unroll
                 for (int i = 0; i < kRW; ++i)
@@ -672,13 +657,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kWide ? 4 : 1) kv_attention_j
         write_row<kD>(a, static_cast<int>(s0.z), static_cast<int>(s0.w), static_cast<int>(s1.x) + r, lane, mm, sum, o);
 }
 
-template <int kD, int kWR, int kRW, int kG, int kCtas>
+template <int kD, int kWR, int kRW, int kG, int kCtas, bool kScored>
 cudaError_t launch_attention(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream) {
-    using S = Attn<kD, kWR, kRW, kG, kCtas>;
+    using S = Attn<kD, kWR, kRW, kG, kCtas, kScored>;
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
-    auto kernel = kv_attention_kernel<kD, kWR, kRW, kG, kCtas>;
+    auto kernel = kv_attention_kernel<kD, kWR, kRW, kG, kCtas, kScored>;
     if (!configured[dev & 63].load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
         if (e != cudaSuccess) return e;
@@ -709,47 +694,40 @@ int rows_of(int max_q_len, int group, int head_dim) {
 }
 
 // Launches the kernel for the row tile; `grid` is its CTAs.
-template <int kD>
-cudaError_t launch_rows(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream);
-
-template <>
-cudaError_t launch_rows<64>(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream) {
-    switch (a.rows) {
-        case 8: return launch_attention<64, 1, 1, 6, 2>(a, num_sms, grid, stream);
-        case 16: return launch_attention<64, 1, 2, 6, 2>(a, num_sms, grid, stream);
-        case 24: return launch_attention<64, 1, 3, 6, 2>(a, num_sms, grid, stream);
-        case 48: return launch_attention<64, 2, 3, 4, 1>(a, num_sms, grid, stream);
-        case 96: return launch_attention<64, 4, 3, 2, 1>(a, num_sms, grid, stream);
-        default: return launch_attention<64, 8, 3, 1, 1>(a, num_sms, grid, stream);
-    }
-}
-
-template <>
-cudaError_t launch_rows<128>(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream) {
-    switch (a.rows) {
-        case 8: return launch_attention<128, 1, 1, 6, 2>(a, num_sms, grid, stream);
-        case 16: return launch_attention<128, 1, 2, 6, 2>(a, num_sms, grid, stream);
-        case 24: return launch_attention<128, 1, 3, 4, 2>(a, num_sms, grid, stream);
-        case 48: return launch_attention<128, 2, 3, 4, 1>(a, num_sms, grid, stream);
-        default: grid = num_sms; return launch_attention_tc(a, num_sms, stream);
-    }
-}
-
-template <>
-cudaError_t launch_rows<256>(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream) {
-    switch (a.rows) {
-        case 8: return launch_attention<256, 1, 1, 6, 1>(a, num_sms, grid, stream);
-        case 16: return launch_attention<256, 2, 1, 4, 1>(a, num_sms, grid, stream);
-        case 32: return launch_attention<256, 2, 2, 4, 1>(a, num_sms, grid, stream);
-        default: return launch_attention<256, 4, 2, 2, 1>(a, num_sms, grid, stream);
+template <int kD, bool kScored>
+cudaError_t launch_rows(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream) {
+    if constexpr (kD == 64) {
+        switch (a.rows) {
+            case 8: return launch_attention<64, 1, 1, 6, 2, kScored>(a, num_sms, grid, stream);
+            case 16: return launch_attention<64, 1, 2, 6, 2, kScored>(a, num_sms, grid, stream);
+            case 24: return launch_attention<64, 1, 3, 6, 2, kScored>(a, num_sms, grid, stream);
+            case 48: return launch_attention<64, 2, 3, 4, 1, kScored>(a, num_sms, grid, stream);
+            case 96: return launch_attention<64, 4, 3, 2, 1, kScored>(a, num_sms, grid, stream);
+            default: return launch_attention<64, 8, 3, 1, 1, kScored>(a, num_sms, grid, stream);
+        }
+    } else if constexpr (kD == 128) {
+        switch (a.rows) {
+            case 8: return launch_attention<128, 1, 1, 6, 2, kScored>(a, num_sms, grid, stream);
+            case 16: return launch_attention<128, 1, 2, 6, 2, kScored>(a, num_sms, grid, stream);
+            case 24: return launch_attention<128, 1, 3, 4, 2, kScored>(a, num_sms, grid, stream);
+            case 48: return launch_attention<128, 2, 3, 4, 1, kScored>(a, num_sms, grid, stream);
+            default: grid = num_sms; return launch_attention_tc(a, kScored, num_sms, stream);
+        }
+    } else {
+        switch (a.rows) {
+            case 8: return launch_attention<256, 1, 1, 6, 1, kScored>(a, num_sms, grid, stream);
+            case 16: return launch_attention<256, 2, 1, 4, 1, kScored>(a, num_sms, grid, stream);
+            case 32: return launch_attention<256, 2, 2, 4, 1, kScored>(a, num_sms, grid, stream);
+            default: return launch_attention<256, 4, 2, 2, 1, kScored>(a, num_sms, grid, stream);
+        }
     }
 }
 
 template <int kD>
-cudaError_t launch_both(const AttnArgs& a, int max_q_len, int num_sms, cudaStream_t stream) {
+cudaError_t launch_both(const AttnArgs& a, bool scored, int max_q_len, int num_sms, cudaStream_t stream) {
     if (num_sms > kMaxAttnGrid / 2) num_sms = kMaxAttnGrid / 2;
     int grid = 0;
-    const cudaError_t e = launch_rows<kD>(a, num_sms, grid, stream);
+    const cudaError_t e = scored ? launch_rows<kD, true>(a, num_sms, grid, stream) : launch_rows<kD, false>(a, num_sms, grid, stream);
     if (e != cudaSuccess) return e;
     const int64_t items = static_cast<int64_t>(a.batch) * a.c.heads * ((static_cast<int64_t>(max_q_len) * a.group + a.rows - 1) / a.rows);
     // 4 warps a row while the items are few, so that each has many parts: (us, 1 and 4 warps) one token over 4096 10.1 and
@@ -799,10 +777,11 @@ cudaError_t launch_kv_attention(const AttentionProblem& p, int num_sms, cudaStre
     a.split = static_cast<SplitItem*>(p.workspace);
     a.part_ml = reinterpret_cast<float*>(a.split + kMaxAttnGrid);
     a.part_o = a.part_ml + slots * 2;
+    a.scores = p.scores;
     switch (p.cache.head_dim) {
-        case 64: return launch_both<64>(a, p.max_q_len, num_sms, stream);
-        case 128: return launch_both<128>(a, p.max_q_len, num_sms, stream);
-        default: return launch_both<256>(a, p.max_q_len, num_sms, stream);
+        case 64: return launch_both<64>(a, p.scored, p.max_q_len, num_sms, stream);
+        case 128: return launch_both<128>(a, p.scored, p.max_q_len, num_sms, stream);
+        default: return launch_both<256>(a, p.scored, p.max_q_len, num_sms, stream);
     }
 }
 

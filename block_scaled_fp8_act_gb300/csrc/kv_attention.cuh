@@ -6,6 +6,7 @@
 
 #include "decoder_util.cuh"
 #include "kernels.h"
+#include "scores.cuh"
 
 namespace fp8act {
 
@@ -34,6 +35,10 @@ struct AttnArgs {
     float* part_ml;    // [2 * grid][rows][2]
     SplitItem* split;  // [grid]
     unsigned int* index_error;
+    Scores scores;
+    // the accumulated weights alone
+    float* mass;       // [pages, heads, page]
+    bool accumulate;
 };
 
 // CTAs of the main kernel (two per SM at most) that the workspace is made for.
@@ -45,6 +50,19 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool i
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kN>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // Two E4M3 codes (the low or the high 16 bits of `codes`) to f16x2, exactly.
@@ -65,16 +83,76 @@ __device__ __forceinline__ uint32_t scale_exponent(float s) {
     return e == 0x7F800000u ? 0u : e;
 }
 
+// A stage holds the cached codes as 128-byte lines, as the cache does (a token
+// is half a line, a line or two); chunk c of a line sits at c ^ (line % 8).
+// Byte offset of 16-byte chunk c of
+// token `row`:
+template <int kD>
+__device__ __forceinline__ uint32_t stage_offset(int row, int c) {
+    const int line = kD == 64 ? row >> 1 : kD == 128 ? row : row * 2 + (c >> 3);
+    const int chunk = kD == 64 ? ((row & 1) << 2) | c : c & 7;
+    return line * 128 + ((chunk ^ (line & 7)) << 4);
+}
+
+// The MMA's rows are the cached tokens of a block of 8 in an order of our own:
+// row i is token order<kD>(i). The 8 lanes of a shared-memory phase read 4
+// chunks of 2 neighbouring rows; the order gives those two tokens swizzles
+// that differ in bit 2, so that they read distinct banks.
+template <int kD>
+__device__ __forceinline__ int order(int i) {
+    if (kD == 64) return i;
+    if (kD == 128) return (i >> 1) | ((i & 1) << 2);
+    return ((i >> 1) & 1) | ((i & 1) << 1) | (i & 4);
+}
+
+// Rows of queries to shared memory as f16 in the order of the MMA's B fragments, each scaled by a power of two so that its
+// largest value is in [1, 2): bf16 then fits f16 exactly down to 2^-17 of that, and below to within 2^-25 of it. `load`
+// gives 8 values of a row, `scale` takes the row's power of two. Called by the whole CTA; `rows` is a multiple of 8.
+template <int kD, int kThreads, class Load, class Scale>
+__device__ __forceinline__ void stage_queries(uint8_t* q, int rows, Load load, Scale scale) {
+    constexpr int kLanes = kD / 8, kKS = kD / 32;
+    static_assert(kLanes <= 32 && 8 % (32 / kLanes) == 0, "whole warps of rows");
+    const int c = threadIdx.x % kLanes;
+    for (int r = threadIdx.x / kLanes; r < rows; r += kThreads / kLanes) {
+        const uint4 x = load(r, c);
+        // (a warp's rows are all below `rows` or none is, so that the whole warp is here)
+        uint32_t top = top_bits(x);
+#pragma unroll
+        for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // (a zero row's exponent is as good as any)
+        const uint32_t e = top == 0 ? 127 : min(max(top >> 7, 1u), 253u);
+        const float up = __uint_as_float((254 - e) << 23);  // 2^(127 - e)
+        if (c == 0) scale(r, __uint_as_float(e << 23));
+        float f[8];
+        unpack_bf16x8(x, f);
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __half2 v = __floats2half2_rn(f[2 * j] * up, f[2 * j + 1] * up);
+            h[j] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        // d = 8c .. 8c + 7: two k-steps of lane (r & 7, (c % 8) / 2)
+        const int ks = (c / 8) * 2 + (c & 1);
+        reinterpret_cast<uint4*>(q)[((r >> 3) * kKS + ks) * 32 + (r & 7) * 4 + (c % 8) / 2] = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+}
+
 // One item and where it lies in the unit list. A unit is kTok cached tokens of
 // a row tile; an item counts kCost units beside its own.
 struct Item {
     int b, h, rt;      // sequence, KV head, row tile
     int nq, q0, len;   // new tokens, first one's row in q, cached tokens
     int rts, tiles;    // row tiles of this sequence and units of each, kCost included
+    int prefix;        // positions that every row sees (0 in a plain list)
     int64_t first;     // index of the item's first unit
 };
 
-template <int kTok, int kCost>
+// kScored: units are the tiles that the sequence's rows may see. kMass: an item has all the sequence's rows, and a token
+// tile counts as often as they have 64 (at most 16 times).
+enum class List { kPlain, kScored, kMass };
+__device__ __forceinline__ int mass_weight(int rows) { return min(max((rows + 63) / 64, 1), 16); }
+
+template <int kTok, int kCost, List kList>
 struct Units {
     static __device__ __forceinline__ void load_sequence(const AttnArgs& a, int b, Item& it) {
         const int q0 = ld_dep_s32(a.cu_q + b), q1 = ld_dep_s32(a.cu_q + b + 1);
@@ -90,6 +168,16 @@ struct Units {
         it.len = len;
         it.rts = (it.nq * a.group + a.rows - 1) / a.rows;
         it.tiles = (len + kTok - 1) / kTok + kCost;  // (an empty sequence still writes its rows)
+        it.prefix = 0;
+        if constexpr (kList == List::kMass) {
+            it.prefix = prefix_of(a.scores, b, len);
+            it.rts = len > 0 && (it.nq > 0 || !a.accumulate) ? 1 : 0;
+            it.tiles = (len + kTok - 1) / kTok * mass_weight(it.nq * a.group) + kCost;
+        }
+        if constexpr (kList == List::kScored) {
+            it.prefix = prefix_of(a.scores, b, len);
+            if (it.nq > 0) it.tiles = reach_of<kTok>(it.prefix, first_seen(a.scores, q0, len, it.nq, 0), len).end + kCost;
+        }
     }
 
     // Units per CTA: an even share, but not less than is worth a part of an item.
@@ -143,7 +231,7 @@ struct Units {
             }
             if (lane == 0) {
                 sh.total = total;
-                a.split[blockIdx.x].parts = 0;
+                if constexpr (kList != List::kMass) a.split[blockIdx.x].parts = 0;
             }
         }
         __syncthreads();
@@ -185,8 +273,23 @@ __device__ __forceinline__ void write_split(const AttnArgs& a, const Item& it, i
     a.split[blockIdx.x] = sp;
 }
 
+// What the rows of one row tile, row0 .. row0 + nrows - 1 of a sequence, see (kScored).
+struct TileReach {
+    Reach tiles;
+    int lo, limit;  // no row needs a mask in [lo, limit), but for the prefix
+};
+template <int kTok>
+__device__ __forceinline__ TileReach tile_reach(const AttnArgs& a, const Item& it, int row0, int nrows) {
+    const int q_first = row0 / a.group, q_last = (row0 + nrows - 1) / a.group;
+    TileReach r;
+    r.tiles = reach_of<kTok>(it.prefix, first_seen(a.scores, it.q0, it.len, it.nq, q_first), it.len - it.nq + q_last + 1);
+    r.lo = first_seen(a.scores, it.q0, it.len, it.nq, q_last);
+    r.limit = it.len - it.nq + q_first + 1;
+    return r;
+}
+
 // The kernel for wide row tiles of head size 128 (kv_attention_tc.cu); the
 // caller launches the join of the split items after it.
-cudaError_t launch_attention_tc(const AttnArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_attention_tc(const AttnArgs& a, bool scored, int num_sms, cudaStream_t stream);
 
 }  // namespace fp8act

@@ -73,12 +73,12 @@ static_assert(256 * kRegsOther + 256 * kRegsSoftmax <= kThreads * 128, "register
 constexpr int kTileBytes = kTok * kD;
 constexpr int kKSets = 4;  // tiles whose key scales are at hand (the values widened are at most 2 behind)
 
-template <bool kPair>  // two row tiles of 128 on the same tokens
+template <bool kPair, bool kScored>  // kPair: two row tiles of 128 on the same tokens
 struct Tc {
     // Units that an item counts beside its own, for its queries and its result. (Rows up to 128, 16 tokens x 6 heads over
     // 131072: 5 units 63.6 us, 8 62.0; two row tiles, 512 tokens over 16384: 4 units 122.8 us, 6 126.5.)
     static constexpr int kItemCost = kPair ? 4 : 8;
-    using Work = Units<kTok, kItemCost>;
+    using Work = Units<kTok, kItemCost, kScored ? List::kScored : List::kPlain>;
     static constexpr int kQTiles = kPair ? 2 : 1;
     static constexpr int kKStages = kPair ? 3 : 4;
     static constexpr int kVStages = kPair ? 2 : 3;
@@ -91,7 +91,8 @@ struct Tc {
     static constexpr int kR = kScaleK + kKSets * kTok * 4;         // the same ring: R
     static constexpr int kQScale = kR + kKSets * 4;
     static constexpr int kML = kQScale + kQTiles * 128 * 4;        // second result's (maximum, sum, R) per row
-    static constexpr int kBytes = kML + 128 * 16 + 1024;           // (the base is rounded up to 1024)
+    static constexpr int kRowScores = kML + 128 * 16;              // kScored
+    static constexpr int kBytes = kRowScores + (kScored ? kQTiles * 128 * 16 : 0) + 1024;  // (the base is rounded up to 1024)
 };
 
 struct TcExtra {
@@ -223,12 +224,12 @@ __device__ __forceinline__ void swap(T& a, T& b) {
     b = c;
 }
 
-template <bool kPair>
+template <bool kPair, bool kScored>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __grid_constant__ AttnArgs a,
                                                                       const __grid_constant__ CUtensorMap k_map,
                                                                       const __grid_constant__ CUtensorMap v_map,
                                                                       const TcExtra x) {
-    using C = Tc<kPair>;
+    using C = Tc<kPair, kScored>;
     using Work = typename C::Work;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -314,6 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
         int row0, nrows, slots;  // rows of the row tile; row halves in use (kPair) or 2
         int f0, n;               // first token tile and how many
         bool whole;              // no other CTA works on the item
+        TileReach reach;         // kScored: what the rows see
+        __device__ int at(int t) const { return kScored ? reach.tiles.at(t) : t; }  // where token tile t is
     };
     auto span_of = [&]() {
         Span s;
@@ -325,7 +328,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
         s.slots = kPair && s.nrows <= 128 ? 1 : 2;
         const int seen = max(it.len - it.nq + (s.row0 + s.nrows - 1) / a.group + 1, 0);
         s.f0 = max(t0 - C::kItemCost, 0);
-        s.n = max(min((seen + kTok - 1) / kTok, t1 - C::kItemCost) - s.f0, 0);
+        int end = (seen + kTok - 1) / kTok;
+        if constexpr (kScored) {
+            s.reach = tile_reach<kTok>(a, it, s.row0, s.nrows);
+            end = s.reach.tiles.end;
+        }
+        s.n = max(min(end, t1 - C::kItemCost) - s.f0, 0);
         s.whole = t0 == 0 && t1 == it.tiles;
         return s;
     };
@@ -356,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
             const int* table = a.table + it.b * a.table_stride;
             // Pages of 4 tiles at a time, one per 16 tokens and lane, looked up one such span ahead.
             auto look_up = [&](int t) -> int {
-                const int pos = t * kTok + lane * 16;
-                if (t >= s.f0 + s.n || pos >= it.len) return -1;
+                const int pos = s.at(t + (lane >> 3)) * kTok + (lane & 7) * 16;
+                if (t + (lane >> 3) >= s.f0 + s.n || pos >= it.len) return -1;
                 const int p = ld_dep_s32(table + (pos >> a.c.page_log2));
                 if (p >= 0 && p < a.c.num_pages) return p;
                 atomicOr(a.index_error, 1u);
@@ -372,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                 const uint32_t round = values ? n / C::kVStages : n / C::kKStages;  // (constant divisors)
                 const uint32_t stage = n - round * stages, bar = full + 8 * stage;
                 if (round > 0 && !(ok = wait(empty + 8 * stage, (round - 1) & 1))) break;
-                const int pos = (s.f0 + i) * kTok;
+                const int pos = s.at(s.f0 + i) * kTok;
                 // Lane j < 128 / box: copy j of the tile, if it holds a token.
                 const int mine = __shfl_sync(0xffffffffu, now, (i & 3) * 8 + min(lane * box / 16, 7));
                 const bool copy = lane < kTok / box && pos + lane * box < it.len && mine >= 0;
@@ -484,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                 for (int j = 0; j < kTok / 32; ++j) rb = max(rb, scale_exponent(sc[kTok + j * 32 + lane]));
                 rb = __reduce_max_sync(0xffffffffu, rb);
                 r_ref = fmaxf(__uint_as_float(rb), r_ref);
-                const bool in = (s.f0 + i) * kTok + t < it.len;  // else anything may be there
+                const bool in = s.at(s.f0 + i) * kTok + t < it.len;  // else anything may be there
                 const float sv = sc[kTok + t], sk = sc[t];
                 const bool poisoned = !(fabsf(sv) < 3e38f);
                 // The softmax may go ahead with the key scales.
@@ -534,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
         const uint32_t t_s = lane_base + slot * 128, t_o = lane_base + 256 + slot * 128;
         const int row_in = (kPair ? slot * 128 : 0) + quad * 32 + lane;  // this thread's row of the row tile
         float* qscale = reinterpret_cast<float*>(smem + C::kQScale);
+        RowScore* row_scores = reinterpret_cast<RowScore*>(smem + C::kRowScores);
         float4* ml = reinterpret_cast<float4*>(smem + C::kML);
         uint32_t jobs_done = 0, item = 0;
         bool ok = any;
@@ -605,6 +614,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                         *reinterpret_cast<uint4*>(to + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
+                if constexpr (kScored) {
+                    __syncwarp();  // (the rows' scales were written by other lanes)
+                    RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, r, a.index_error);
+                    info.qs = qscale[row_in];
+                    row_scores[row_in] = info;
+                }
                 fence_async_proxy();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(q_full);
@@ -621,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int at = row_in - lane + (lane >> 2) + 8 * i;
-                qs[i] = qscale[at];
+                qs[i] = kScored ? 1.0f : qscale[at];  // (kScored: scores are whole before the softmax)
                 limit[i] = it.len - it.nq + (s.row0 + at) / a.group + 1;
                 m[i] = kNegInf;
                 mq[i] = 0.0f;
@@ -649,8 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                 if (rows_here) {
                     const uint32_t ks = base + C::kScaleK + set * kTok * 4 + (lane & 3) * 16;
                     const float r_new = reinterpret_cast<const float*>(smem + C::kR)[set];
-                    const int pos = (s.f0 + i) * kTok;
-                    const bool edge = pos + kTok > all_see;
+                    const int pos = s.at(s.f0 + i) * kTok;
+                    const bool edge = kScored ? on_edge(pos, kTok, it.prefix, s.reach.lo, s.reach.limit) : pos + kTok > all_see;
                     float alpha[4] = {1.0f, 1.0f, 1.0f, 1.0f};
                     bool rescale = false;
 #pragma unroll 1
@@ -662,7 +677,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                         k4[0] = lds_v4(ks);
                         tc::wait_ld();
                         float top[2] = {kNegInf, kNegInf};
+                        const RowScore* const info = row_scores + row_in - lane + (lane >> 2) + 16 * h;  // of rows 8 x
                         auto scaled = [&](bool masked) {
+                            RowScore row[2];
+                            float far[2];
+                            if constexpr (kScored) {
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    row[x] = info[8 * x];
+                                    far[x] = static_cast<float>(row[x].limit - 1 - pos - 2 * (lane & 3));
+                                }
+                            }
 #pragma unroll
                             for (int j = 0; j < kTok / 16; ++j) {
                                 if (j + 1 < kTok / 16) k4[(j + 1) & 1] = lds_v4(ks + (j + 1) * 64);
@@ -675,7 +700,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                                         uint32_t &v0 = v[4 * n + 2 * x], &v1 = v[4 * n + 2 * x + 1];
                                         float2 y = __fmul2_rn(make_float2(__uint_as_float(v0), __uint_as_float(v1)),
                                                               e ? make_float2(k.z, k.w) : make_float2(k.x, k.y));
-                                        if (masked) {
+                                        if constexpr (kScored) {
+                                            y = __fmul2_rn(y, make_float2(row[x].qs, row[x].qs));
+                                            if (a.scores.cap > 0.0f)
+                                                y = make_float2(capped(y.x, a.scores.cap, a.scores.cap_inv),
+                                                                capped(y.y, a.scores.cap, a.scores.cap_inv));
+                                            if (a.scores.slopes) {
+                                                y.x = fmaf(-row[x].slope, fabsf(far[x] - 8 * n), y.x);
+                                                y.y = fmaf(-row[x].slope, fabsf(far[x] - 8 * n - 1), y.y);
+                                            }
+                                            if (masked) {
+                                                const int at = pos + 2 * (lane & 3) + 8 * n;
+                                                if (at >= it.prefix && (at < row[x].lo || at >= row[x].limit)) y.x = kNegInf;
+                                                if (at + 1 >= it.prefix && (at + 1 < row[x].lo || at + 1 >= row[x].limit)) y.y = kNegInf;
+                                            }
+                                        } else if (masked) {
                                             const int end = limit[x] - pos - 2 * (lane & 3);
                                             if (8 * n >= end) y.x = kNegInf;
                                             if (8 * n + 1 >= end) y.y = kNegInf;
@@ -866,13 +905,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
     }
 }
 
-template <bool kPair>
+template <bool kPair, bool kScored>
 cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
-    using C = Tc<kPair>;
+    using C = Tc<kPair, kScored>;
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
-    auto kernel = kv_attention_tc_kernel<kPair>;
+    auto kernel = kv_attention_tc_kernel<kPair, kScored>;
     if (!configured[dev & 63].load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
         if (e != cudaSuccess) return e;
@@ -891,8 +930,9 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_attention_tc(const AttnArgs& a, int num_sms, cudaStream_t stream) {
-    return a.rows > 128 ? launch<true>(a, num_sms, stream) : launch<false>(a, num_sms, stream);
+cudaError_t launch_attention_tc(const AttnArgs& a, bool scored, int num_sms, cudaStream_t stream) {
+    if (scored) return a.rows > 128 ? launch<true, true>(a, num_sms, stream) : launch<false, true>(a, num_sms, stream);
+    return a.rows > 128 ? launch<true, false>(a, num_sms, stream) : launch<false, false>(a, num_sms, stream);
 }
 
 unsigned int read_and_clear_attn_timeout() {

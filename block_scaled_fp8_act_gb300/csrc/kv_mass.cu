@@ -1,0 +1,345 @@
+// The attention weight that every cached token gets: with the scores x of
+// kv_attention.cu and the log-sum-exp that the attention left of each row,
+//   mass[j] (+)= sum over the rows of a KV head of exp(x[r, j] - lse[r]).
+//
+// The scores are computed again, f16 MMAs of S^T = K Q^T as there, and no
+// maximum is needed: the log-sum-exp bounds every exponent by 0. A row of the
+// accumulator is a cached token, so its sum over the query rows stays in the
+// lane that has it, and a token's codes stay in registers, widened once, while
+// all the rows go by in shared memory.
+//
+// Work split. A unit is 32 cached tokens of a KV head with all the sequence's
+// rows; a warp takes whole units, so that no sum is joined and the order is
+// fixed. The units of all sequences and heads form one list, shared evenly by one
+// CTA per SM, weighted by their rows. A warp has its own ring of key tiles in
+// flight. Rows come 256 at a time (128 for D = 256); with more, a token's sum
+// goes through its place in memory between them.
+#include <atomic>
+
+#include "kv_attention.cuh"
+
+namespace fp8act {
+namespace {
+
+__device__ unsigned int g_mass_index_error;
+
+constexpr int kTile = 32;
+constexpr int kItemCost = 2;  // units that an item counts beside its own, for its queries
+using Work = Units<kTile, kItemCost, List::kMass>;
+
+// kWarps of a CTA go by the registers that a tile's widened codes take (half of kD a thread).
+template <int kD>
+struct Mass {
+    static constexpr int kWarps = kD == 64 ? 16 : kD == 128 ? 12 : 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kRows = kD == 256 ? 128 : 256;
+    static constexpr int kStageBytes = kTile * kD + kTile * 4;  // keys, key scales
+    static constexpr int kRowBytes = kD * 2 + 16 + 8;           // queries, RowScore, (qs, -lse)
+    static constexpr int kRoom = 226 * 1024;
+    static int stages(int rows) {
+        const int fit = (kRoom - rows * kRowBytes) / (kWarps * kStageBytes);
+        return fit < 8 ? fit : 8;
+    }
+};
+
+template <int kD, bool kScored>
+__global__ void __launch_bounds__(Mass<kD>::kThreads, 1) kv_mass_kernel(const __grid_constant__ AttnArgs a, int stages) {
+    using M = Mass<kD>;
+    constexpr int kKS = kD / 32;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Work::Scratch scratch;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
+    const int og = order<kD>(g);  // the token of a block of 8 that is the lane's MMA row
+    uint8_t* const queries = smem;
+    RowScore* const row_scores = reinterpret_cast<RowScore*>(smem + a.rows * kD * 2);
+    float2* const row_mass = reinterpret_cast<float2*>(row_scores + a.rows);  // (qs, -lse) in log2
+    uint8_t* const ring = smem + a.rows * M::kRowBytes + warp * stages * M::kStageBytes;
+
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+
+    Item it;
+    int64_t per, u, u_end;
+    if (!Work::first_item(a, M::kWarps, scratch, it, per, u, u_end)) return;
+    while (true) {
+        const int64_t item_end = it.first + it.tiles;
+        const int rows_total = it.nq * a.group, weight = mass_weight(rows_total);
+        // Tile t of the item is this CTA's if its first unit is.
+        auto tile_of = [&](int64_t unit) {
+            return static_cast<int>((max(unit - it.first - kItemCost, int64_t{0}) + weight - 1) / weight);
+        };
+        const int t0 = tile_of(u), t1 = tile_of(item_end < u_end ? item_end : u_end);
+        const int* table = a.table + it.b * a.table_stride;
+        const int in_page = (1 << a.c.page_log2) - 1;
+        const int old_end = it.len - it.nq;  // positions before it keep their weight if accumulating
+
+        int row0 = 0;
+        do {
+            const int nrows = min(rows_total - row0, a.rows), blocks = (nrows + 7) / 8;
+            int lo_first = 0, lo_last = 0, limit_first = 0, limit_last = 0;
+            if (nrows > 0) {
+                const int q_first = row0 / a.group, q_last = (row0 + nrows - 1) / a.group;
+                limit_first = it.len - it.nq + q_first + 1;
+                limit_last = it.len - it.nq + q_last + 1;
+                if constexpr (kScored) {
+                    lo_first = first_seen(a.scores, it.q0, it.len, it.nq, q_first);
+                    lo_last = first_seen(a.scores, it.q0, it.len, it.nq, q_last);
+                }
+            }
+            // Whether some row may see a token of tile t.
+            auto seen = [&](int t) {
+                const int pos = t * kTile;
+                return pos < it.prefix || (pos < limit_last && pos + kTile > lo_first);
+            };
+            // The warp's tiles are t0 + warp, + kWarps, ... Pages of its next 16, one per 16 tokens and lane.
+            auto look_up = [&](int t) -> int {
+                t += (lane >> 1) * M::kWarps;
+                const int pos = t * kTile + (lane & 1) * 16;
+                if (t >= t1 || pos >= it.len) return -1;
+                const int p = ld_dep_s32(table + (pos >> a.c.page_log2));
+                if (p >= 0 && p < a.c.num_pages) return p;
+                atomicOr(a.index_error, 1u);
+                return -1;
+            };
+            // Where token `lane` of the tile is, or -1 (the page in `pages` is asked + 2 i's).
+            int pages = look_up(t0 + warp), asked = 0;
+            auto place_of = [&](int t, int page) -> int64_t {
+                const int pos = t * kTile + lane;
+                return page >= 0 && pos < it.len
+                           ? ((static_cast<int64_t>(page) * a.c.heads + it.h) << a.c.page_log2) + (pos & in_page)
+                           : -1;
+            };
+            auto request = [&](int t, int stage) {
+                if (t < t1) {
+                    const int page = __shfl_sync(0xffffffffu, pages, 2 * asked + (lane >> 4));
+                    if (seen(t)) {
+                        const int64_t place = place_of(t, page);
+                        const uint32_t dst = ptx::smem_u32(ring) + stage * M::kStageBytes;
+                        constexpr int kC = kD / 16, kStep = 32 / kC;  // chunks per token, tokens per instruction
+                        const int c = lane % kC, r0 = lane / kC;
+#pragma unroll
+                        for (int j = 0; j < kTile / kStep; ++j) {
+                            const int64_t at = __shfl_sync(0xffffffffu, place, j * kStep + r0);
+                            cp_async16(dst + stage_offset<kD>(j * kStep + r0, c), a.c.k + (at >= 0 ? at : 0) * kD + c * 16, at >= 0);
+                        }
+                        cp_async4(dst + kTile * kD + lane * 4, a.c.k_scale + (place >= 0 ? place : 0), place >= 0);
+                    }
+                    if (++asked == 16) {
+                        asked = 0;
+                        pages = look_up(t + M::kWarps);
+                    }
+                }
+                cp_async_commit();
+            };
+            // (the number of stages is not known to the compiler, the number of groups in flight has to be)
+            auto wait_for_tile = [&]() {
+                switch (stages) {
+                    case 2: cp_async_wait<0>(); break;
+                    case 3: cp_async_wait<1>(); break;
+                    case 4: cp_async_wait<2>(); break;
+                    case 5: cp_async_wait<3>(); break;
+                    case 6: cp_async_wait<4>(); break;
+                    case 7: cp_async_wait<5>(); break;
+                    default: cp_async_wait<6>(); break;
+                }
+                __syncwarp();
+            };
+#pragma unroll 1
+            for (int i = 0; i < stages - 1; ++i) request(t0 + warp + i * M::kWarps, i);
+
+            stage_queries<kD, M::kThreads>(
+                queries, blocks * 8,
+                [&](int r, int c) {
+                    if (r >= nrows) return make_uint4(0, 0, 0, 0);
+                    const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
+                    return ld_dep_v4(a.q + (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD + c * 8);
+                },
+                [&](int r, float step) {
+                    RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, row0 + r, a.index_error);
+                    info.qs = fmaxf(step * a.scale_log2, 0x1p-126f);
+                    float less = kNegInf;  // a row that is not one, or sees nothing, adds nothing
+                    if (r < nrows) {
+                        const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
+                        const float lse = ld_dep_f32(a.lse + static_cast<int64_t>(it.q0 + qi) * (a.c.heads * a.group) + it.h * a.group + hg);
+                        if (lse != kNegInf) less = lse * -1.4426950408889634f;
+                    } else {
+                        info.lo = info.limit = 0;
+                    }
+                    row_scores[r] = info;
+                    row_mass[r] = make_float2(info.qs, less);
+                });
+            __syncthreads();
+
+            int stage = 0, used = 0, held = look_up(t0 + warp);  // pages of the tiles being worked on
+#pragma unroll 1
+            for (int t = t0 + warp; t < t1; t += M::kWarps) {
+                const int64_t place = place_of(t, __shfl_sync(0xffffffffu, held, 2 * used + (lane >> 4)));
+                if (++used == 16) {
+                    used = 0;
+                    held = look_up(t + M::kWarps);
+                }
+                // What the token (lane & 3) * 8 + og, this lane's in the end, has so far.
+                const int my_token = qd * 8 + og;
+                const int64_t mine = __shfl_sync(0xffffffffu, place, my_token);
+                const bool adds = row0 > 0 || (a.accumulate && t * kTile + my_token < old_end);
+                float have = adds && mine >= 0 ? ld_dep_f32(a.mass + mine) : 0.0f;
+                wait_for_tile();
+                const uint8_t* kt = ring + stage * M::kStageBytes;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (seen(t)) {
+                    // The tile's codes as A fragments: af[k-step][16 tokens][4].
+                    uint32_t af[kD / 16][2][4];
+                    float ks[4];
+                    const float* sk = reinterpret_cast<const float*>(kt + kTile * kD);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) ks[x] = sk[x * 8 + og];
+#pragma unroll
+                    for (int w = 0; w < kD / 64; ++w)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint4 v = *reinterpret_cast<const uint4*>(kt + stage_offset<kD>(x * 16 + y * 8 + og, w * 4 + qd));
+                                const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) {
+                                    af[w * 4 + z][x][y] = e4m3x2_lo_to_f16x2(words[z]);
+                                    af[w * 4 + z][x][y + 2] = e4m3x2_hi_to_f16x2(words[z]);
+                                }
+                            }
+                    __syncwarp();  // the stage is read
+                    request(t + (stages - 1) * M::kWarps, stage == 0 ? stages - 1 : stage - 1);
+                    const int pos0 = t * kTile;
+                    const bool edge = on_edge(pos0, kTile, it.prefix, lo_last, limit_first);
+                    const uint4* qf = reinterpret_cast<const uint4*>(queries) + lane;
+                    auto rows_of = [&](auto masks, int i) {
+                        float s[2][4] = {};
+#pragma unroll
+                        for (int k = 0; k < kKS; ++k) {
+                            const uint4 b = qf[(i * kKS + k) * 32];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) mma_f16(s[x], af[2 * k][x], b.x, b.y);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) mma_f16(s[x], af[2 * k + 1][x], b.z, b.w);
+                        }
+                        const float4 row = *reinterpret_cast<const float4*>(row_mass + i * 8 + qd * 2);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float qs = e ? row.z : row.x, less = e ? row.w : row.y;
+                            RowScore info = {};
+                            if (kScored || decltype(masks)::value) info = row_scores[i * 8 + qd * 2 + e];
+                            const float far = static_cast<float>(info.limit - 1 - pos0 - og);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                float y = s[x >> 1][(x & 1) * 2 + e] * ks[x];
+                                if constexpr (kScored) {
+                                    y *= qs;
+                                    if (a.scores.cap > 0.0f) y = capped(y, a.scores.cap, a.scores.cap_inv);
+                                    if (a.scores.slopes) y = fmaf(-info.slope, fabsf(far - x * 8), y);
+                                    y += less;
+                                } else {
+                                    y = fmaf(y, qs, less);
+                                }
+                                float p = ex2(y);
+                                if constexpr (decltype(masks)::value) {
+                                    const int pos = pos0 + x * 8 + og;
+                                    if (pos >= it.prefix && (pos < info.lo || pos >= info.limit)) p = 0.0f;
+                                }
+                                sum[x] += p;
+                            }
+                        }
+                    };
+                    if (edge) {
+#pragma unroll 1
+                        for (int i = 0; i < blocks; ++i) rows_of(std::true_type{}, i);
+                    } else {
+#pragma unroll 2
+                        for (int i = 0; i < blocks; ++i) rows_of(std::false_type{}, i);
+                    }
+                } else {
+                    __syncwarp();
+                    request(t + (stages - 1) * M::kWarps, stage == 0 ? stages - 1 : stage - 1);
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
+                    sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
+                }
+                const float total = qd == 0 ? sum[0] : qd == 1 ? sum[1] : qd == 2 ? sum[2] : sum[3];
+                if (mine >= 0) a.mass[mine] = have + total;
+                stage = stage + 1 == stages ? 0 : stage + 1;
+            }
+            cp_async_wait<0>();
+            row0 += a.rows;
+            __syncthreads();  // the queries and the rings are free
+        } while (row0 < rows_total);
+        if (item_end >= u_end) break;
+        u = item_end;
+        Work::next_item(a, it);
+    }
+}
+
+template <int kD, bool kScored>
+cudaError_t launch(AttnArgs& a, int max_q_len, int num_sms, cudaStream_t stream) {
+    using M = Mass<kD>;
+    const int64_t rows = static_cast<int64_t>(max_q_len) * a.group;
+    a.rows = rows >= M::kRows ? M::kRows : rows < 8 ? 8 : static_cast<int>((rows + 7) / 8 * 8);
+    const int stages = M::stages(a.rows);
+    static std::atomic<bool> configured[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    auto kernel = kv_mass_kernel<kD, kScored>;
+    if (!configured[dev & 63].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kRoom);
+        if (e != cudaSuccess) return e;
+        configured[dev & 63].store(true, std::memory_order_relaxed);
+    }
+    const size_t bytes = a.rows * M::kRowBytes + static_cast<size_t>(M::kWarps) * stages * M::kStageBytes;
+    return launch_dependent(kernel, dim3(num_sms), M::kThreads, bytes, stream, 1, a, stages);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_mass(const MassProblem& p, int num_sms, cudaStream_t stream) {
+    AttnArgs a = {};
+    a.q = static_cast<const uint16_t*>(p.q);
+    a.q_stride = p.q_stride;
+    a.cu_q = p.cu_q;
+    a.kv_lens = p.kv_lens;
+    a.table = p.page_table;
+    a.table_stride = p.table_stride;
+    a.batch = p.batch;
+    a.tokens = p.tokens;
+    a.group = p.group;
+    a.rows = 1;
+    void* error = nullptr;
+    const cudaError_t found = cudaGetSymbolAddress(&error, g_mass_index_error);
+    if (found != cudaSuccess) return found;
+    a.index_error = static_cast<unsigned int*>(error);
+    a.scale_log2 = p.softmax_scale * 1.4426950408889634f;
+    a.c = p.cache;
+    a.lse = const_cast<float*>(p.lse);
+    a.scores = p.scores;
+    a.mass = p.mass;
+    a.accumulate = p.accumulate;
+    switch (p.cache.head_dim) {
+        case 64: return p.scored ? launch<64, true>(a, p.max_q_len, num_sms, stream) : launch<64, false>(a, p.max_q_len, num_sms, stream);
+        case 128: return p.scored ? launch<128, true>(a, p.max_q_len, num_sms, stream) : launch<128, false>(a, p.max_q_len, num_sms, stream);
+        default: return p.scored ? launch<256, true>(a, p.max_q_len, num_sms, stream) : launch<256, false>(a, p.max_q_len, num_sms, stream);
+    }
+}
+
+unsigned int read_and_clear_mass_index_error() {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_mass_index_error, sizeof(v)) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (v) {
+        const unsigned int zero = 0;
+        cudaMemcpyToSymbol(g_mass_index_error, &zero, sizeof(zero));
+    }
+    return v;
+}
+
+}  // namespace fp8act

@@ -1,0 +1,84 @@
+// Scores that are more than a scaled product, for the attention kernels and the
+// accumulated weights: a cap, a bias by distance, and which positions a row sees.
+// Everything is in units of log2, as the exponentials want it.
+#pragma once
+
+#include "decoder_util.cuh"
+#include "kernels.h"
+
+namespace fp8act {
+
+// cap * tanh(y / cap), to within 2^-22 of itself up to |y| = 0.625 cap and 2^-21 cap beyond. Near zero, where most scores
+// are, tanh(z) / z is a polynomial in z^2 (interpolated at the Chebyshev points of [0, 0.625^2], 1.0e-7 off in fp32): eight
+// instructions at the multipliers' rate, where 1 - 2 / (1 + e^2z) takes two of the special functions', an eighth of it,
+// and loses the small values' bits in the difference. Which one an element takes goes by its own value.
+__device__ __forceinline__ float capped(float y, float cap, float cap_inv) {
+    const float z = y * cap_inv, u = z * z;
+    float p = fmaf(-0.005657135f, u, 0.020588191f);
+    p = fmaf(p, u, -0.05372011f);
+    p = fmaf(p, u, 0.13331114f);
+    p = fmaf(p, u, -0.3333326f);
+    p = fmaf(p, u, 1.0f);
+    y *= p;
+    if (fabsf(z) > 0.625f) {
+        const float e = ex2(fabsf(z) * 2.8853900817779268f);  // 2 / ln 2
+        y = copysignf(fmaf(-2.0f * cap, rcp_approx_ftz(1.0f + e), cap), z);
+    }
+    return y;
+}
+
+// How a row (new token, query head) scores and what it sees: positions below the sequence's prefix, and [lo, limit).
+struct __align__(16) RowScore {
+    float qs;  // of the query's scaling, with the softmax's scale
+    int lo, limit;
+    float slope;
+};
+
+// The first position that new token qi of a sequence with `len` cached tokens, `nq` of them new, sees behind the prefix.
+__device__ __forceinline__ int first_seen(const Scores& s, int q0, int len, int nq, int qi) {
+    int64_t lo = 0;
+    if (s.window > 0) lo = static_cast<int64_t>(len) - nq + qi - s.window + 1;
+    if (s.first) lo = max(lo, static_cast<int64_t>(ld_dep_s32(s.first + q0 + qi)));
+    return static_cast<int>(max(lo, int64_t{0}));
+}
+
+// Row `row` of a sequence's (rows past its last are as that one), of KV head h.
+__device__ __forceinline__ RowScore row_score(const Scores& s, int q0, int len, int nq, int group, int h, int row, unsigned int* error) {
+    const int qi = min(row / group, nq - 1);
+    RowScore r;
+    r.qs = 0.0f;
+    r.lo = first_seen(s, q0, len, nq, qi);
+    r.limit = len - nq + qi + 1;
+    r.slope = s.slopes ? ld_dep_f32(s.slopes + h * group + row % group) * 1.4426950408889634f : 0.0f;
+    if (s.first && qi > 0 && ld_dep_s32(s.first + q0 + qi) < ld_dep_s32(s.first + q0 + qi - 1)) atomicOr(error, 1u);
+    return r;
+}
+
+__device__ __forceinline__ int prefix_of(const Scores& s, int b, int len) {
+    return s.prefix ? min(max(ld_dep_s32(s.prefix + b), 0), len) : 0;
+}
+
+// Tiles of kTok positions that a sequence's or a row tile's rows may see: [0, prefix) and then from `skip` further on.
+// Tile v of them is at position at(v) * kTok.
+struct Reach {
+    int prefix_tiles, skip, end;
+    __device__ __forceinline__ int at(int v) const { return v < prefix_tiles ? v : v + skip; }
+};
+template <int kTok>
+__device__ __forceinline__ Reach reach_of(int prefix, int lo, int limit) {
+    Reach r;
+    r.prefix_tiles = (prefix + kTok - 1) / kTok;
+    const int start = max(lo / kTok, r.prefix_tiles);
+    r.skip = start - r.prefix_tiles;
+    r.end = r.prefix_tiles + max((max(limit, 0) + kTok - 1) / kTok - start, 0);
+    return r;
+}
+
+// Whether positions [pos, pos + n) hold one that some row of a row tile does not see; `lo` is its last row's, `limit` its
+// first one's.
+__device__ __forceinline__ bool on_edge(int pos, int n, int prefix, int lo, int limit) {
+    if (lo <= prefix) return pos + n > max(limit, prefix);
+    return pos + n > prefix && (pos < lo || pos + n > limit);
+}
+
+}  // namespace fp8act

@@ -87,6 +87,8 @@ def load(build: bool = False) -> ctypes.CDLL:
     L.fp8_kv_append.argtypes = [p, p, p, i, i64, i64, p, p]
     L.fp8_rope_append.argtypes = [p, p, p, i64, i64, i64, p, p, f, f, p, p, p, i, i, i, f, p, i, i, p, p, p]
     L.fp8_kv_attention.argtypes = [p, i64, p, p, p, i, i, i, i, i, f, p, p, p, p, ctypes.c_size_t, p]
+    L.fp8_kv_attention_scored.argtypes = [p, i64, p, p, p, i, i, i, i, i, f, p, p, p, p, p, ctypes.c_size_t, p]
+    L.fp8_kv_attention_mass.argtypes = [p, i64, p, p, p, i, i, i, i, i, f, p, p, p, p, i, p]
     L.fp8_kv_attention_workspace.argtypes = [i, i, p]
     L.fp8_kv_attention_workspace.restype = ctypes.c_size_t
     L.fp8_kv_evict.argtypes = [p, p, p, i, p, p, p, i, i, i, i, p, p, p]
@@ -94,7 +96,7 @@ def load(build: bool = False) -> ctypes.CDLL:
     L.fp8act_verify_drafts_workspace.argtypes = [i, i]
     L.fp8act_verify_drafts_workspace.restype = ctypes.c_size_t
     for fn in (L.fp8_rmsnorm_quant, L.fp8_silu_mul_quant, L.fp8_kv_append, L.fp8_rope_append, L.fp8_kv_attention,
-               L.fp8_kv_evict,
+               L.fp8_kv_attention_scored, L.fp8_kv_attention_mass, L.fp8_kv_evict,
                L.fp8act_verify_drafts, L.fp8_act_quant, L.fp8_weight_quant, L.fp8_block_gemm, L.fp8_block_gemm_f32,
                L.fp8_block_gemm_w8a16, L.fp8_block_gemm_w8a16_f32,
                L.fp8_act_quant_grouped, L.fp8_block_gemm_grouped, L.fp8_block_gemm_grouped_f32,
@@ -350,6 +352,12 @@ class KvCacheStruct(ctypes.Structure):
                 ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
 
 
+class ScoresStruct(ctypes.Structure):
+    """fp8act_scores of include/fp8act.h."""
+    _fields_ = [("soft_cap", ctypes.c_float), ("window", ctypes.c_int), ("prefix_lens", ctypes.c_void_p),
+                ("first", ctypes.c_void_p), ("slopes", ctypes.c_void_p)]
+
+
 def kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> KvCache:
     """A cache of zeroed pages."""
     shape = (num_pages, kv_heads, page_size)
@@ -386,16 +394,34 @@ def kv_attention_workspace(max_q_len: int, q_heads: int, cache) -> int:
 
 
 def fp8_kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len: int | None = None,
-                     softmax_scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
+                     softmax_scale: float | None = None, out=None, lse=None, workspace=None, stream=None,
+                     soft_cap: float = 0.0, window: int = 0, prefix_lens=None, first=None, slopes=None):
     """bf16 [tokens, q_heads, head_dim] = causal attention of the new tokens q over the cache.
 
     page_table int32 [B, max_pages], kv_lens int32 [B] (cached tokens, the new ones included),
     cu_q int32 [B + 1] (rows of q per sequence). max_q_len (the most new tokens of a sequence)
     picks the row tile; softmax_scale defaults to head_dim ** -0.5. `lse` (fp32 [tokens, q_heads])
     is filled if given. Rows that no sequence has (past cu_q[B]) are not written. `workspace`: a uint8 tensor of kv_attention_workspace() bytes, kept by the
-    caller per stream; without one the binding keeps its own per device and stream."""
+    caller per stream; without one the binding keeps its own per device and stream.
+
+    Scores: soft_cap > 0 caps them, soft_cap * tanh(x / soft_cap); slopes (fp32 [q_heads]) take
+    slopes * distance off. A new token at position i sees position j if j < prefix_lens (int32 [B]), or if
+    first <= j <= i (int32 [tokens], not falling over a sequence's) and, with a window, j > i - window."""
     return _native().kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, out, lse, workspace,
-                                  stream)
+                                  stream, soft_cap, window, prefix_lens, first, slopes)
+
+
+def fp8_kv_attention_mass(q, cache, page_table, kv_lens, cu_q, lse, mass, max_q_len: int | None = None,
+                          softmax_scale: float | None = None, accumulate: bool = True, stream=None,
+                          soft_cap: float = 0.0, window: int = 0, prefix_lens=None, first=None, slopes=None) -> None:
+    """Adds to mass (fp32 [pages, kv_heads, page_size]) the attention weight that every cached token gets.
+
+    The weights exp(score - lse) of the new tokens q, summed over them and over the query heads of a KV head;
+    lse (fp32 [tokens, q_heads]) is what fp8_kv_attention left with the same arguments. The new tokens' own
+    places start from zero, all of a sequence's places if not `accumulate`. A page that gets weight belongs
+    to one sequence of the call."""
+    _native().kv_attention_mass(q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, lse, mass, accumulate, stream,
+                                soft_cap, window, prefix_lens, first, slopes)
 
 
 def kv_mass(cache) -> torch.Tensor:

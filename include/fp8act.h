@@ -377,6 +377,66 @@ FP8ACT_API int fp8_kv_attention(const void* q_bf16, int64_t q_stride, const int*
                                 int q_heads, float softmax_scale, const fp8act_kv_cache* cache, void* out_bf16,
                                 float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Scores that are more than a scaled product. With x = softmax_scale * q . k and
+ * i the new token's position, kv_lens[b] - n + (its number):
+ *   x = soft_cap * tanh(x / soft_cap)              if soft_cap > 0
+ *   x = x - slopes[head] * |i - j|                 if slopes
+ * and position j is seen if j < prefix_lens[b], by every new token (also past its
+ * own place: a prefix whose tokens see each other), or if
+ *   first[token] <= j <= i  and, with window > 0,  j > i - window.
+ * That is a sliding window, with `prefix_lens` one that keeps its first tokens; the
+ * document that a token is in, if `first` is where that starts; a prefix mask.
+ * Positions that no row sees are not read.
+ *   soft_cap     0 (none) or 1e-30 .. 1e30
+ *   window       0 (none) or the positions that a token sees, its own included
+ *   prefix_lens  [batch] int32 or NULL; cut to 0 .. kv_lens[b]
+ *   first        [tokens] int32 or NULL, not falling over a sequence's new tokens
+ *                (else FP8ACT_ERR_INDEX, and what those tokens get is unspecified)
+ *   slopes       [q_heads] fp32, finite, or NULL
+ */
+typedef struct {
+    float soft_cap;
+    int window;
+    const int* prefix_lens;
+    const int* first;
+    const float* slopes;
+} fp8act_scores;
+
+/*
+ * fp8_kv_attention with such scores (lse is theirs too). `scores` lives in host
+ * memory and is read during the call; NULL or all zero is fp8_kv_attention.
+ * Workspace and errors as there. A capped score is off by at most 2^-21 of its
+ * size or 2^-21 soft_cap.
+ */
+FP8ACT_API int fp8_kv_attention_scored(const void* q_bf16, int64_t q_stride, const int* cu_q, const int* kv_lens,
+                                       const int* page_table, int max_pages, int batch, int tokens, int max_q_len,
+                                       int q_heads, float softmax_scale, const fp8act_scores* scores,
+                                       const fp8act_kv_cache* cache, void* out_bf16, float* lse, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
+ * The attention weight that every cached token gets, summed over the new tokens
+ * and the query heads of its KV head, for fp8_kv_evict:
+ *   mass[j, kv head] (+)= sum over rows (token, head) that see j of exp(x - lse[row])
+ * with the scores x of the attention call that left `lse`, and q, scores and
+ * tables as there. All new tokens of a sequence or its last ones may be passed (a
+ * prompt's last 32, say: cu_q counts those that are; they are the last of the
+ * sequence's kv_lens[b]).
+ *   mass        [num_pages, kv_heads, page_size] fp32
+ *   accumulate  0: the weights of positions 0 .. kv_lens[b] - 1 are replaced;
+ *               else they are added to, but that those of the new tokens' own
+ *               positions start from zero (a place may hold a former token's)
+ * Sums are fp32 in a fixed order. A row whose lse is -infinity adds nothing; a NaN
+ * scale of a cached token makes that token's weight NaN. Places past kv_lens[b] are
+ * left as they are. A page that gets weight belongs to one sequence of the call.
+ */
+FP8ACT_API int fp8_kv_attention_mass(const void* q_bf16, int64_t q_stride, const int* cu_q, const int* kv_lens,
+                                     const int* page_table, int max_pages, int batch, int tokens, int max_q_len,
+                                     int q_heads, float softmax_scale, const fp8act_scores* scores,
+                                     const fp8act_kv_cache* cache, const float* lse, float* mass, int accumulate,
+                                     void* stream);
+
 /* Bytes of workspace for fp8_kv_attention; 0 for arguments it would refuse. */
 FP8ACT_API size_t fp8_kv_attention_workspace(int max_q_len, int q_heads, const fp8act_kv_cache* cache);
 

@@ -2,11 +2,14 @@
 from __future__ import annotations
 
 import ctypes
+import os
+import re
 
 import pytest
 import torch
 from test_decoder_ops_abi import A16, ALIGN, DEVICE, NULL, OK, SHAPE, cache, lib  # noqa: F401
 
+from block_scaled_fp8_act_gb300 import build as fp8build
 from block_scaled_fp8_act_gb300 import fp8act
 
 
@@ -57,3 +60,37 @@ def test_evict_argument_checks(lib):  # noqa: F811
         assert evict(lib, **bad) == ALIGN, bad
     if not torch.cuda.is_available():
         assert evict(lib) == DEVICE and evict(lib, np=0, new=None, kept=None) == DEVICE
+
+
+def test_structs_match_the_header():
+    text = open(os.path.join(fp8build.INCLUDE, "fp8act.h"), encoding="utf-8").read()
+    body = re.search(r"typedef struct \{([^{}]*)\}\s*fp8act_scores;", text).group(1)
+    assert re.findall(r"(\w+)(?:,|;)", body) == [f[0] for f in fp8act.ScoresStruct._fields_]
+    assert ctypes.sizeof(fp8act.ScoresStruct) == 32
+
+
+def scored(lib, mass, q=A16, qs=1024, cu=A16, lens=A16, table=A16, mp=4, B=1, T=1, mq=1, hq=8, scale=0.1, out=A16, lse=A16, ws=A16,  # noqa: F811
+           cap=0.0, window=0, prefix=None, first=None, slopes=None, scores=True, **kw):
+    s = ctypes.byref(fp8act.ScoresStruct(cap, window, prefix, first, slopes)) if scores else None
+    c = ctypes.byref(cache(**kw))
+    if mass:
+        return lib.fp8_kv_attention_mass(q, qs, cu, lens, table, mp, B, T, mq, hq, scale, s, c, lse, out, 1, None)
+    return lib.fp8_kv_attention_scored(q, qs, cu, lens, table, mp, B, T, mq, hq, scale, s, c, out, lse, ws, 1 << 40, None)
+
+
+@pytest.mark.parametrize("mass", [False, True])
+def test_score_argument_checks(lib, mass):  # noqa: F811
+    inf, nan = float("inf"), float("nan")
+    for bad in (dict(cap=-1.0), dict(cap=nan), dict(cap=inf), dict(cap=1e-32), dict(cap=1e31), dict(window=-1), dict(hq=7), dict(hq=0),
+                dict(qs=1000), dict(B=-1), dict(T=-1), dict(mq=-1), dict(mp=-1), dict(mp=1 << 26), dict(hq=514, qs=1 << 20),
+                dict(scale=0.0), dict(scale=nan), dict(pages=0), dict(page=48)):
+        assert scored(lib, mass, **bad) == SHAPE, bad
+    assert scored(lib, mass, B=0, q=None) == OK
+    for name in ("q", "cu", "lens", "table", "out") + (("lse",) if mass else ("ws",)):
+        assert scored(lib, mass, **{name: None}) == NULL, name
+    for bad in (dict(prefix=A16 + 2), dict(first=A16 + 1), dict(slopes=A16 + 2), dict(q=A16 + 8), dict(qs=1028), dict(lse=A16 + 2),
+                dict(out=A16 + 4), dict(lens=A16 + 2)):
+        assert scored(lib, mass, **bad) == ALIGN, bad
+    if not torch.cuda.is_available():
+        for ok in (dict(), dict(cap=30.0, window=5, prefix=A16, first=A16, slopes=A16), dict(scores=False)):
+            assert scored(lib, mass, **ok) == DEVICE
