@@ -351,16 +351,32 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas, kScored>::kThrea
                 for (int i = 0; i < kRW; ++i)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const RowScore row = info[i * 8 + e];
-                        const float far = static_cast<float>(row.limit - 1 - pos0 - og);
+                        const float row_qs = info[i * 8 + e].qs;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            float y = s[x >> 1][i][(x & 1) * 2 + e] * row.qs;
-                            if (a.scores.cap > 0.0f) y = capped(y, a.scores.cap, a.scores.cap_inv);
-                            if (a.scores.slopes) y = fmaf(-row.slope, fabsf(far - x * 8), y);
-                            s[x >> 1][i][(x & 1) * 2 + e] = y;
-                        }
+                        for (int x = 0; x < 4; ++x) s[x >> 1][i][(x & 1) * 2 + e] *= row_qs;
                     }
+                if (a.scores.cap > 0.0f)
+                    cap_scores<kRW * 4>(
+                        a.scores.cap, a.scores.cap_inv,
+                        [&](int j) { return make_float2(s[j & 1][j >> 2][j & 2], s[j & 1][j >> 2][(j & 2) + 1]); },
+                        [&](int j, const float2& y) {
+                            s[j & 1][j >> 2][j & 2] = y.x;
+                            s[j & 1][j >> 2][(j & 2) + 1] = y.y;
+                        });
+                if (a.scores.slopes) {
+#pragma unroll
+                    for (int i = 0; i < kRW; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const RowScore row = info[i * 8 + e];
+                            const float far = static_cast<float>(row.limit - 1 - pos0 - og);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                float& y = s[x >> 1][i][(x & 1) * 2 + e];
+                                y = fmaf(-row.slope, fabsf(far - x * 8), y);
+                            }
+                        }
+                }
             }
             if (edge) {
 #pragma unroll

@@ -679,15 +679,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                         float top[2] = {kNegInf, kNegInf};
                         const RowScore* const info = row_scores + row_in - lane + (lane >> 2) + 16 * h;  // of rows 8 x
                         auto scaled = [&](bool masked) {
-                            RowScore row[2];
-                            float far[2];
-                            if constexpr (kScored) {
-#pragma unroll
-                                for (int x = 0; x < 2; ++x) {
-                                    row[x] = info[8 * x];
-                                    far[x] = static_cast<float>(row[x].limit - 1 - pos - 2 * (lane & 3));
-                                }
-                            }
 #pragma unroll
                             for (int j = 0; j < kTok / 16; ++j) {
                                 if (j + 1 < kTok / 16) k4[(j + 1) & 1] = lds_v4(ks + (j + 1) * 64);
@@ -700,36 +691,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                                         uint32_t &v0 = v[4 * n + 2 * x], &v1 = v[4 * n + 2 * x + 1];
                                         float2 y = __fmul2_rn(make_float2(__uint_as_float(v0), __uint_as_float(v1)),
                                                               e ? make_float2(k.z, k.w) : make_float2(k.x, k.y));
-                                        if constexpr (kScored) {
-                                            y = __fmul2_rn(y, make_float2(row[x].qs, row[x].qs));
-                                            if (a.scores.cap > 0.0f)
-                                                y = make_float2(capped(y.x, a.scores.cap, a.scores.cap_inv),
-                                                                capped(y.y, a.scores.cap, a.scores.cap_inv));
-                                            if (a.scores.slopes) {
-                                                y.x = fmaf(-row[x].slope, fabsf(far[x] - 8 * n), y.x);
-                                                y.y = fmaf(-row[x].slope, fabsf(far[x] - 8 * n - 1), y.y);
-                                            }
-                                            if (masked) {
-                                                const int at = pos + 2 * (lane & 3) + 8 * n;
-                                                if (at >= it.prefix && (at < row[x].lo || at >= row[x].limit)) y.x = kNegInf;
-                                                if (at + 1 >= it.prefix && (at + 1 < row[x].lo || at + 1 >= row[x].limit)) y.y = kNegInf;
-                                            }
-                                        } else if (masked) {
+                                        if (!kScored && masked) {
                                             const int end = limit[x] - pos - 2 * (lane & 3);
                                             if (8 * n >= end) y.x = kNegInf;
                                             if (8 * n + 1 >= end) y.y = kNegInf;
                                         }
-                                        top[x] = fmaxf(top[x], fmaxf(y.x, y.y));
+                                        if (!kScored) top[x] = fmaxf(top[x], fmaxf(y.x, y.y));
                                         v0 = __float_as_uint(y.x);
                                         v1 = __float_as_uint(y.y);
                                     }
                                 }
                             }
                         };
-                        if (edge)
+                        if (!kScored && edge)
                             scaled(true);
                         else
                             scaled(false);
+                        if constexpr (kScored) {
+                            auto get = [&](int i) { return make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])); };
+                            auto set = [&](int i, const float2& y) {
+                                v[2 * i] = __float_as_uint(y.x);
+                                v[2 * i + 1] = __float_as_uint(y.y);
+                            };
+                            // (pair i is row i & 1, columns 8 (i / 2) + 2 (lane % 4) and the next)
+                            const float row_qs[2] = {info[0].qs, info[8].qs};
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) set(i, __fmul2_rn(get(i), make_float2(row_qs[i & 1], row_qs[i & 1])));
+                            if (a.scores.cap > 0.0f) cap_scores<32>(a.scores.cap, a.scores.cap_inv, get, set);
+                            const int first = pos + 2 * (lane & 3);
+                            if (a.scores.slopes) {
+                                const float2 down[2] = {make_float2(-info[0].slope, -info[0].slope), make_float2(-info[8].slope, -info[8].slope)};
+                                const float far[2] = {static_cast<float>(info[0].limit - 1 - first), static_cast<float>(info[8].limit - 1 - first)};
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    const float d = far[i & 1] - 8 * (i >> 1);
+                                    set(i, __ffma2_rn(down[i & 1], make_float2(fabsf(d), fabsf(d - 1.0f)), get(i)));
+                                }
+                            }
+                            if (edge) {
+                                const int lo[2] = {info[0].lo, info[8].lo}, end[2] = {info[0].limit, info[8].limit};
+#pragma unroll
+                                for (int i = 0; i < 64; ++i) {
+                                    const int at = first + 8 * (i >> 2) + (i & 1), x = i >> 1 & 1;
+                                    if (at >= it.prefix && (at < lo[x] || at >= end[x])) v[i] = __float_as_uint(kNegInf);
+                                }
+                            }
+                            top[0] = top[1] = kNegInf;
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) top[i >> 1 & 1] = fmaxf(top[i >> 1 & 1], __uint_as_float(v[i]));
+                        }
                         // A reference moves only when the row's maximum passes it by 2^8.
                         bool moves = false;
 #pragma unroll

@@ -24,27 +24,31 @@ namespace {
 __device__ unsigned int g_mass_index_error;
 
 constexpr int kTile = 32;
-constexpr int kItemCost = 2;  // units that an item counts beside its own, for its queries
+constexpr int kItemCost = 4;  // units that an item counts beside its own, for its start
 using Work = Units<kTile, kItemCost, List::kMass>;
 
-// kWarps of a CTA go by the registers that a tile's widened codes take (half of kD a thread).
-template <int kD>
+// Many rows: one CTA per SM whose warps share the rows in shared memory, as many as the registers allow that a tile's
+// widened codes take (half of kD a thread). Few rows (kFew): CTAs of one warp, several per SM, so that a short sequence
+// costs one warp its start and not a CTA; 34 sequences of one token to 16384: 51.0 us with whole CTAs.
+template <int kD, bool kFew>
 struct Mass {
-    static constexpr int kWarps = kD == 64 ? 16 : kD == 128 ? 12 : 8;
+    static constexpr int kWarps = kFew ? 1 : kD == 64 ? 16 : kD == 128 ? 12 : 8;
+    static constexpr int kCtas = !kFew ? 1 : kD == 256 ? 6 : 8;
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kRows = kD == 256 ? 128 : 256;
+    static constexpr int kRows = kFew ? 16 : kD == 256 ? 128 : 256;
     static constexpr int kStageBytes = kTile * kD + kTile * 4;  // keys, key scales
     static constexpr int kRowBytes = kD * 2 + 16 + 8;           // queries, RowScore, (qs, -lse)
-    static constexpr int kRoom = 226 * 1024;
+    static constexpr int kRoom = 226 * 1024 / kCtas - 1024 * (kCtas > 1 ? 1 : 0);
     static int stages(int rows) {
         const int fit = (kRoom - rows * kRowBytes) / (kWarps * kStageBytes);
         return fit < 8 ? fit : 8;
     }
 };
 
-template <int kD, bool kScored>
-__global__ void __launch_bounds__(Mass<kD>::kThreads, 1) kv_mass_kernel(const __grid_constant__ AttnArgs a, int stages) {
-    using M = Mass<kD>;
+template <int kD, bool kFew, bool kScored>
+__global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCtas)
+    kv_mass_kernel(const __grid_constant__ AttnArgs a, int stages) {
+    using M = Mass<kD, kFew>;
     constexpr int kKS = kD / 32;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Work::Scratch scratch;
@@ -60,7 +64,7 @@ __global__ void __launch_bounds__(Mass<kD>::kThreads, 1) kv_mass_kernel(const __
 
     Item it;
     int64_t per, u, u_end;
-    if (!Work::first_item(a, M::kWarps, scratch, it, per, u, u_end)) return;
+    if (!Work::first_item(a, kFew ? 4 : M::kWarps, scratch, it, per, u, u_end)) return;
     while (true) {
         const int64_t item_end = it.first + it.tiles;
         const int rows_total = it.nq * a.group, weight = mass_weight(rows_total);
@@ -102,7 +106,8 @@ __global__ void __launch_bounds__(Mass<kD>::kThreads, 1) kv_mass_kernel(const __
                 return -1;
             };
             // Where token `lane` of the tile is, or -1 (the page in `pages` is asked + 2 i's).
-            int pages = look_up(t0 + warp), asked = 0;
+            const int first_pages = look_up(t0 + warp);
+            int pages = first_pages, asked = 0;
             auto place_of = [&](int t, int page) -> int64_t {
                 const int pos = t * kTile + lane;
                 return page >= 0 && pos < it.len
@@ -170,19 +175,29 @@ __global__ void __launch_bounds__(Mass<kD>::kThreads, 1) kv_mass_kernel(const __
                 });
             __syncthreads();
 
-            int stage = 0, used = 0, held = look_up(t0 + warp);  // pages of the tiles being worked on
-#pragma unroll 1
-            for (int t = t0 + warp; t < t1; t += M::kWarps) {
+            // Where the weight of the token is that is this lane's in the end, and what it has so far: a tile ahead.
+            int used = 0, held = first_pages;
+            const int my_token = qd * 8 + og;
+            int64_t mine = -1;
+            float have = 0.0f;
+            auto look_ahead = [&](int t) {
+                if (t >= t1) return;
                 const int64_t place = place_of(t, __shfl_sync(0xffffffffu, held, 2 * used + (lane >> 4)));
                 if (++used == 16) {
                     used = 0;
                     held = look_up(t + M::kWarps);
                 }
-                // What the token (lane & 3) * 8 + og, this lane's in the end, has so far.
-                const int my_token = qd * 8 + og;
-                const int64_t mine = __shfl_sync(0xffffffffu, place, my_token);
+                mine = __shfl_sync(0xffffffffu, place, my_token);
                 const bool adds = row0 > 0 || (a.accumulate && t * kTile + my_token < old_end);
-                float have = adds && mine >= 0 ? ld_dep_f32(a.mass + mine) : 0.0f;
+                have = adds && mine >= 0 ? ld_dep_f32(a.mass + mine) : 0.0f;
+            };
+            look_ahead(t0 + warp);
+            int stage = 0;
+#pragma unroll 1
+            for (int t = t0 + warp; t < t1; t += M::kWarps) {
+                const int64_t to = mine;
+                const float old = have;
+                look_ahead(t + M::kWarps);
                 wait_for_tile();
                 const uint8_t* kt = ring + stage * M::kStageBytes;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -223,30 +238,40 @@ __global__ void __launch_bounds__(Mass<kD>::kThreads, 1) kv_mass_kernel(const __
                             for (int x = 0; x < 2; ++x) mma_f16(s[x], af[2 * k + 1][x], b.z, b.w);
                         }
                         const float4 row = *reinterpret_cast<const float4*>(row_mass + i * 8 + qd * 2);
+                        const RowScore* const info = row_scores + i * 8 + qd * 2;
+                        // y[2 j + e]: token j * 8 + og, row 2 qd + e
+                        float y[8];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float qs = e ? row.z : row.x, less = e ? row.w : row.y;
-                            RowScore info = {};
-                            if (kScored || decltype(masks)::value) info = row_scores[i * 8 + qd * 2 + e];
-                            const float far = static_cast<float>(info.limit - 1 - pos0 - og);
+                        for (int j = 0; j < 8; ++j) {
+                            y[j] = s[j >> 2][j & 3] * ks[j >> 1];
+                            const float qs = j & 1 ? row.z : row.x, less = j & 1 ? row.w : row.y;
+                            y[j] = kScored ? y[j] * qs : fmaf(y[j], qs, less);
+                        }
+                        if constexpr (kScored) {
+                            if (a.scores.cap > 0.0f)
+                                cap_scores<4>(
+                                    a.scores.cap, a.scores.cap_inv, [&](int j) { return make_float2(y[2 * j], y[2 * j + 1]); },
+                                    [&](int j, const float2& z) {
+                                        y[2 * j] = z.x;
+                                        y[2 * j + 1] = z.y;
+                                    });
+                            if (a.scores.slopes) {
+                                const float slope[2] = {info[0].slope, info[1].slope};
+                                const float far[2] = {static_cast<float>(info[0].limit - 1 - pos0 - og), static_cast<float>(info[1].limit - 1 - pos0 - og)};
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                float y = s[x >> 1][(x & 1) * 2 + e] * ks[x];
-                                if constexpr (kScored) {
-                                    y *= qs;
-                                    if (a.scores.cap > 0.0f) y = capped(y, a.scores.cap, a.scores.cap_inv);
-                                    if (a.scores.slopes) y = fmaf(-info.slope, fabsf(far - x * 8), y);
-                                    y += less;
-                                } else {
-                                    y = fmaf(y, qs, less);
-                                }
-                                float p = ex2(y);
-                                if constexpr (decltype(masks)::value) {
-                                    const int pos = pos0 + x * 8 + og;
-                                    if (pos >= it.prefix && (pos < info.lo || pos >= info.limit)) p = 0.0f;
-                                }
-                                sum[x] += p;
+                                for (int j = 0; j < 8; ++j) y[j] = fmaf(-slope[j & 1], fabsf(far[j & 1] - (j >> 1) * 8), y[j]);
                             }
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) y[j] += j & 1 ? row.w : row.y;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float p = ex2(y[j]);
+                            if constexpr (decltype(masks)::value) {
+                                const int pos = pos0 + (j >> 1) * 8 + og;
+                                if (pos >= it.prefix && (pos < info[j & 1].lo || pos >= info[j & 1].limit)) p = 0.0f;
+                            }
+                            sum[j >> 1] += p;
                         }
                     };
                     if (edge) {
@@ -266,7 +291,7 @@ __global__ void __launch_bounds__(Mass<kD>::kThreads, 1) kv_mass_kernel(const __
                     sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
                 }
                 const float total = qd == 0 ? sum[0] : qd == 1 ? sum[1] : qd == 2 ? sum[2] : sum[3];
-                if (mine >= 0) a.mass[mine] = have + total;
+                if (to >= 0) a.mass[to] = old + total;
                 stage = stage + 1 == stages ? 0 : stage + 1;
             }
             cp_async_wait<0>();
@@ -279,23 +304,30 @@ __global__ void __launch_bounds__(Mass<kD>::kThreads, 1) kv_mass_kernel(const __
     }
 }
 
-template <int kD, bool kScored>
-cudaError_t launch(AttnArgs& a, int max_q_len, int num_sms, cudaStream_t stream) {
-    using M = Mass<kD>;
-    const int64_t rows = static_cast<int64_t>(max_q_len) * a.group;
+template <int kD, bool kFew, bool kScored>
+cudaError_t launch(AttnArgs& a, int64_t rows, int num_sms, cudaStream_t stream) {
+    using M = Mass<kD, kFew>;
     a.rows = rows >= M::kRows ? M::kRows : rows < 8 ? 8 : static_cast<int>((rows + 7) / 8 * 8);
     const int stages = M::stages(a.rows);
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
-    auto kernel = kv_mass_kernel<kD, kScored>;
+    auto kernel = kv_mass_kernel<kD, kFew, kScored>;
     if (!configured[dev & 63].load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kRoom);
         if (e != cudaSuccess) return e;
         configured[dev & 63].store(true, std::memory_order_relaxed);
     }
     const size_t bytes = a.rows * M::kRowBytes + static_cast<size_t>(M::kWarps) * stages * M::kStageBytes;
-    return launch_dependent(kernel, dim3(num_sms), M::kThreads, bytes, stream, 1, a, stages);
+    return launch_dependent(kernel, dim3(num_sms * M::kCtas), M::kThreads, bytes, stream, 1, a, stages);
+}
+
+template <int kD>
+cudaError_t launch_rows(AttnArgs& a, bool scored, int max_q_len, int num_sms, cudaStream_t stream) {
+    const int64_t rows = static_cast<int64_t>(max_q_len) * a.group;
+    if (rows <= Mass<kD, true>::kRows)
+        return scored ? launch<kD, true, true>(a, rows, num_sms, stream) : launch<kD, true, false>(a, rows, num_sms, stream);
+    return scored ? launch<kD, false, true>(a, rows, num_sms, stream) : launch<kD, false, false>(a, rows, num_sms, stream);
 }
 
 }  // namespace
@@ -323,9 +355,9 @@ cudaError_t launch_kv_mass(const MassProblem& p, int num_sms, cudaStream_t strea
     a.mass = p.mass;
     a.accumulate = p.accumulate;
     switch (p.cache.head_dim) {
-        case 64: return p.scored ? launch<64, true>(a, p.max_q_len, num_sms, stream) : launch<64, false>(a, p.max_q_len, num_sms, stream);
-        case 128: return p.scored ? launch<128, true>(a, p.max_q_len, num_sms, stream) : launch<128, false>(a, p.max_q_len, num_sms, stream);
-        default: return p.scored ? launch<256, true>(a, p.max_q_len, num_sms, stream) : launch<256, false>(a, p.max_q_len, num_sms, stream);
+        case 64: return launch_rows<64>(a, p.scored, p.max_q_len, num_sms, stream);
+        case 128: return launch_rows<128>(a, p.scored, p.max_q_len, num_sms, stream);
+        default: return launch_rows<256>(a, p.scored, p.max_q_len, num_sms, stream);
     }
 }
 

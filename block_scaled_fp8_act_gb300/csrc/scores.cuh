@@ -8,23 +8,50 @@
 
 namespace fp8act {
 
-// cap * tanh(y / cap), to within 2^-22 of itself up to |y| = 0.625 cap and 2^-21 cap beyond. Near zero, where most scores
-// are, tanh(z) / z is a polynomial in z^2 (interpolated at the Chebyshev points of [0, 0.625^2], 1.0e-7 off in fp32): eight
-// instructions at the multipliers' rate, where 1 - 2 / (1 + e^2z) takes two of the special functions', an eighth of it,
-// and loses the small values' bits in the difference. Which one an element takes goes by its own value.
-__device__ __forceinline__ float capped(float y, float cap, float cap_inv) {
-    const float z = y * cap_inv, u = z * z;
-    float p = fmaf(-0.005657135f, u, 0.020588191f);
-    p = fmaf(p, u, -0.05372011f);
-    p = fmaf(p, u, 0.13331114f);
-    p = fmaf(p, u, -0.3333326f);
-    p = fmaf(p, u, 1.0f);
-    y *= p;
-    if (fabsf(z) > 0.625f) {
-        const float e = ex2(fabsf(z) * 2.8853900817779268f);  // 2 / ln 2
-        y = copysignf(fmaf(-2.0f * cap, rcp_approx_ftz(1.0f + e), cap), z);
+// cap * tanh(y / cap) of a thread's scores, kPairs pairs that `get` gives and `set` takes; the whole warp calls it. To within
+// 2^-22 of a score up to |y| = 0.625 cap and 2^-21 cap beyond. Near zero, where most scores are, tanh(z) / z is a polynomial
+// in z^2 (interpolated at the Chebyshev points of [0, 0.625^2], 1.0e-7 off in fp32), four two-wide instructions a score;
+// 1 - 2 / (1 + e^2z) takes two of the special functions', at an eighth of the rate, and loses a small score's bits in the
+// difference, so it is for warps that hold a larger one. Which form a score gets goes by its own value alone.
+template <int kPairs, class Get, class Set>
+__device__ __forceinline__ void cap_scores(float cap, float cap_inv, Get get, Set set) {
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        const float2 y = get(i);
+        most = fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y)));
     }
-    return y;
+    const bool far = __any_sync(0xffffffffu, most * cap_inv > 0.625f);
+    auto near = [&](const float2& y, const float2& z) {
+        const float2 u = __fmul2_rn(z, z);
+        auto both = [](float x) { return make_float2(x, x); };
+        float2 p = __ffma2_rn(both(-0.005657135f), u, both(0.020588191f));
+        p = __ffma2_rn(p, u, both(-0.05372011f));
+        p = __ffma2_rn(p, u, both(0.13331114f));
+        p = __ffma2_rn(p, u, both(-0.3333326f));
+        return __fmul2_rn(y, __ffma2_rn(p, u, both(1.0f)));
+    };
+    const float2 inv = make_float2(cap_inv, cap_inv);
+    if (!far) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const float2 y = get(i);
+            set(i, near(y, __fmul2_rn(y, inv)));
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        const float2 y = get(i), z = __fmul2_rn(y, inv);
+        float2 w = near(y, z);
+        auto flat = [&](float x) {
+            const float e = ex2(fabsf(x) * 2.8853900817779268f);  // 2 / ln 2
+            return copysignf(fmaf(-2.0f * cap, rcp_approx_ftz(1.0f + e), cap), x);
+        };
+        if (fabsf(z.x) > 0.625f) w.x = flat(z.x);
+        if (fabsf(z.y) > 0.625f) w.y = flat(z.y);
+        set(i, w);
+    }
 }
 
 // How a row (new token, query head) scores and what it sees: positions below the sequence's prefix, and [lo, limit).
