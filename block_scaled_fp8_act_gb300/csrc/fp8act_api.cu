@@ -580,7 +580,7 @@ int fp8act_check_status(void* stream) {
                                fp8act::read_and_clear_attn_index_error() | fp8act::read_and_clear_mass_index_error() |
                                fp8act::read_and_clear_evict_index_error() |
                                fp8act::read_and_clear_verify_index_error();
-    const unsigned int at = fp8act::read_and_clear_attn_timeout();
+    const unsigned int at = fp8act::read_and_clear_attn_timeout() | fp8act::read_and_clear_mass_timeout();
     if (tc | mid | rd | at) return FP8ACT_ERR_TIMEOUT;
     return index ? FP8ACT_ERR_INDEX : FP8ACT_OK;
 }

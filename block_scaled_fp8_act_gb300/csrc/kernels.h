@@ -238,6 +238,7 @@ unsigned int read_and_clear_attn_index_error();
 unsigned int read_and_clear_mass_index_error();
 unsigned int read_and_clear_evict_index_error();
 unsigned int read_and_clear_attn_timeout();
+unsigned int read_and_clear_mass_timeout();
 unsigned int read_and_clear_verify_index_error();
 
 // Device-side error words of the tcgen05 kernels (non-zero after a bounded

@@ -2,6 +2,7 @@
 // the record of items that cross CTAs.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "decoder_util.cuh"
@@ -134,6 +135,83 @@ __device__ __forceinline__ void stage_queries(uint8_t* q, int rows, Load load, S
         // d = 8c .. 8c + 7: two k-steps of lane (r & 7, (c % 8) / 2)
         const int ks = (c / 8) * 2 + (c & 1);
         reinterpret_cast<uint4*>(q)[((r >> 3) * kKS + ks) * 32 + (r & 7) * 4 + (c % 8) / 2] = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+}
+
+// One token's codes and its neighbours' from the cache's tensor map to shared memory.
+__device__ __forceinline__ void load_tokens(uint32_t dst, const CUtensorMap* map, uint32_t bar, int line) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(0), "r"(line)
+        : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 32 rows of queries of head size 128 as the two E4M3 parts of a tcgen05 operand (128-byte rows, swizzled), the low one
+// `apart` bytes behind the high one: a row, scaled by a power of two so that its largest value is in [128, 256), is
+// E4M3(q) + E4M3(q - E4M3(q)), exact down to 2^-9 of its largest value and within 2^-17 of that below. `at` is the
+// element of the lane's row, rows from `valid` on are zero; `scale` takes a row and its power of two. By a whole warp; the
+// caller fences the asynchronous proxy.
+template <class Scale>
+__device__ __forceinline__ void stage_query_parts(uint8_t* q, int apart, const uint16_t* src, int64_t at, int valid, Scale scale) {
+    const int lane = threadIdx.x & 31;
+    // The rows' bf16 values land where the two parts of the row will be (256 bytes either way), all requested together.
+    {
+        const int c = lane & 15;
+#pragma unroll 4
+        for (int j = 0; j < 32; j += 2) {
+            const int row = j + (lane >> 4);
+            const int64_t from = __shfl_sync(0xffffffffu, at, row) + c * 8;
+            const bool in = row < valid;
+            cp_async16(ptx::smem_u32(q) + (c >> 3) * apart + row * 128 + (((c & 7) ^ (row & 7)) << 4), src + (in ? from : 0), in);
+        }
+        cp_async_wait_all();
+        __syncwarp();
+    }
+    // 4 lanes a row, 32 columns each.
+    const int quarter = lane & 3;
+#pragma unroll 1
+    for (int row = lane >> 2; row < 32; row += 8) {
+        uint8_t* const to_row = q + row * 128;
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = *reinterpret_cast<const uint4*>(to_row + (quarter >> 1) * apart + ((((quarter & 1) * 4 + i) ^ (row & 7)) << 4));
+        __syncwarp();  // before the row's other lanes write over them
+        uint32_t top = max(max(top_bits(v[0]), top_bits(v[1])), max(top_bits(v[2]), top_bits(v[3])));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // (a zero row's exponent is as good as any)
+        const uint32_t e = top == 0 ? 127 : min(max(top >> 7, 8u), 253u);
+        const float up = __uint_as_float((261 - e) << 23);  // 2^(134 - e)
+        if (quarter == 0) scale(row, __uint_as_float((e - 7) << 23));
+        const bool bad = top >= 0x7F80u;  // NaN or infinite: the whole row is NaN
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                float f[8];
+                unpack_bf16x8(v[2 * i + (w >> 1)], f);
+                float d[4];
+                hi[w] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                    const float x0 = f[(w & 1) * 4 + j] * up, x1 = f[(w & 1) * 4 + j + 1] * up;
+                    const uint32_t pair = cvt_e4m3x2(x0, x1), back = e4m3x2_lo_to_f16x2(pair);
+                    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
+                    d[j] = x0 - b.x;
+                    d[j + 1] = x1 - b.y;
+                    hi[w] |= pair << (8 * j);
+                }
+                lo[w] = cvt_e4m3x2(d[0], d[1]) | (cvt_e4m3x2(d[2], d[3]) << 16);
+                if (bad) hi[w] = 0x7F7F7F7Fu;
+            }
+            uint8_t* const to = to_row + (((quarter * 2 + i) ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(to + apart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
     }
 }
 
@@ -291,5 +369,8 @@ __device__ __forceinline__ TileReach tile_reach(const AttnArgs& a, const Item& i
 // The kernel for wide row tiles of head size 128 (kv_attention_tc.cu); the
 // caller launches the join of the split items after it.
 cudaError_t launch_attention_tc(const AttnArgs& a, bool scored, int num_sms, cudaStream_t stream);
+
+// The weights of cached tokens from many rows of head size 128 (kv_mass_tc.cu).
+cudaError_t launch_mass_tc(const AttnArgs& a, bool scored, int num_sms, cudaStream_t stream);
 
 }  // namespace fp8act

@@ -156,29 +156,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// D[tmem] (+)= A[smem desc] x B[smem desc], E4M3 with fp32 accumulation.
-__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n"
-        ".reg .pred p, e;\n"
-        "elect.sync _|e, 0xffffffff;\n"
-        "setp.ne.b32 p, %4, 0;\n"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-        "}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void commit_elected(uint32_t mbar) {
-    asm volatile(
-        "{\n"
-        ".reg .pred e;\n"
-        "elect.sync _|e, 0xffffffff;\n"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
-        "}\n" ::"r"(mbar)
-        : "memory");
-}
-
 // Descriptor of the widened values as the N x K operand with N contiguous
 // (128-byte swizzle): blocks of 64 columns x 8 tokens, column blocks 16 KB
 // apart (leading byte offset), token blocks 1 KB apart (stride byte offset).
@@ -196,13 +173,6 @@ constexpr uint32_t kIdescValues = (1u << 4)                                   //
                                   | (1u << 16)                                // B with N contiguous
                                   | (static_cast<uint32_t>(kD >> 3) << 17) | (128u >> 4 << 24);
 
-__device__ __forceinline__ void load_tokens(uint32_t dst, const CUtensorMap* map, uint32_t bar, int line) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(map), "r"(bar), "r"(0), "r"(line)
-        : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Arrive on `bar` (one of its expected arrivals) once this thread's cp.asyncs so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -212,7 +182,6 @@ __device__ __forceinline__ float4 lds_v4(uint32_t addr) {
     asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Where the key scale of a tile's token lies, so that a lane reads those of its columns 4 at a time.
 __device__ __forceinline__ int scale_at(int t) { return (t & ~15) | ((t >> 1 & 3) << 2) | ((t >> 3 & 1) << 1) | (t & 1); }
@@ -442,10 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int i = 0; i < kD / 32; ++i)  // (a descriptor counts 16 bytes)
-                        mma_e4m3_ss(tmem + slot * 128, q_desc + (part * kTileBytes + 32 * i) / 16, k_desc + 2 * i, kIdescScores,
+                        tc::mma_e4m3_ss(tmem + slot * 128, q_desc + (part * kTileBytes + 32 * i) / 16, k_desc + 2 * i, kIdescScores,
                                     part + i > 0 ? 1u : 0u);
-                commit_elected(s_full + 8 * slot);
-                if (last_use(j)) commit_elected(k_empty + 8 * stage);
+                tc::commit_elected(s_full + 8 * slot);
+                if (last_use(j)) tc::commit_elected(k_empty + 8 * stage);
             };
             if (!(ok = wait(q_full, item & 1))) break;
             tc::fence_after_sync();
@@ -462,17 +431,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                 for (int i = 0; i < kTok / 16; ++i)
                     mma_f16_ts(tmem + 256 + slot * 128, tmem + slot * 128 + 8 * i, v_desc + 2048 * i / 16, kIdescValues,
                                fresh && i == 0 ? 0u : 1u);
-                commit_elected(pv_done + 8 * slot);
-                if (last_use(j)) commit_elected(v16_empty + 8 * buf);
+                tc::commit_elected(pv_done + 8 * slot);
+                if (last_use(j)) tc::commit_elected(v16_empty + 8 * buf);
                 if (j + depth < jobs) scores(j + depth);
             }
             if (!ok) break;
-            commit_elected(item_done);
+            tc::commit_elected(item_done);
             ++item;
             if (!next(s)) break;
         }
         // No MMA may still run when tensor memory is freed or the CTA leaves.
-        commit_elected(drain);
+        tc::commit_elected(drain);
         if (!ptx::mbar_wait(drain, 0)) atomicOr(&g_attn_timeout, 4u);
         __syncwarp();
     } else if (warp >= 4) {
@@ -551,69 +520,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
             // Queries. The MMAs of the item before have read theirs (item_done was waited for).
             const int r = s.row0 + row_in;
             if (kPair || slot == 0) {
-                // A warp's rows are those that its threads own. Their bf16 values land where the two parts of the row will be
-                // (256 bytes either way), all requested together.
+                // A warp's rows are those that its threads own.
                 uint8_t* const q = smem + C::kQ + slot * 2 * kTileBytes + quad * 32 * 128;
-                {
-                    const int qi = r / a.group, hg = r - qi * a.group;
-                    const int64_t at = (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD;
-                    const int c = lane & 15;
-#pragma unroll 4
-                    for (int j = 0; j < 32; j += 2) {
-                        const int row = j + (lane >> 4);
-                        const int64_t from = __shfl_sync(0xffffffffu, at, row) + c * 8;
-                        const bool in = row_in - lane + row < s.nrows;
-                        cp_async16(ptx::smem_u32(q) + (c >> 3) * kTileBytes + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                                   a.q + (in ? from : 0), in);
-                    }
-                    cp_async_wait_all();
-                    __syncwarp();
-                }
-                // 4 lanes a row, 32 columns each.
-                const int quarter = lane & 3;
-#pragma unroll 1
-                for (int row = lane >> 2; row < 32; row += 8) {
-                    uint8_t* const at = q + row * 128;
-                    uint4 v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = *reinterpret_cast<const uint4*>(at + (quarter >> 1) * kTileBytes +
-                                                               ((((quarter & 1) * 4 + i) ^ (row & 7)) << 4));
-                    __syncwarp();  // before the row's other lanes write over them
-                    uint32_t top = max(max(top_bits(v[0]), top_bits(v[1])), max(top_bits(v[2]), top_bits(v[3])));
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    // (a zero row's exponent is as good as any)
-                    const uint32_t e = top == 0 ? 127 : min(max(top >> 7, 8u), 253u);
-                    const float up = __uint_as_float((261 - e) << 23);  // 2^(134 - e)
-                    if (quarter == 0) qscale[row_in - lane + row] = fmaxf(__uint_as_float((e - 7) << 23) * a.scale_log2, 0x1p-126f);
-                    const bool bad = top >= 0x7F80u;  // NaN or infinite: the whole row is NaN
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            float f[8];
-                            unpack_bf16x8(v[2 * i + (w >> 1)], f);
-                            float d[4];
-                            hi[w] = 0;
-#pragma unroll
-                            for (int j = 0; j < 4; j += 2) {
-                                const float x0 = f[(w & 1) * 4 + j] * up, x1 = f[(w & 1) * 4 + j + 1] * up;
-                                const uint32_t pair = cvt_e4m3x2(x0, x1), back = e4m3x2_lo_to_f16x2(pair);
-                                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
-                                d[j] = x0 - b.x;
-                                d[j + 1] = x1 - b.y;
-                                hi[w] |= pair << (8 * j);
-                            }
-                            lo[w] = cvt_e4m3x2(d[0], d[1]) | (cvt_e4m3x2(d[2], d[3]) << 16);
-                            if (bad) hi[w] = 0x7F7F7F7Fu;
-                        }
-                        uint8_t* const to = at + (((quarter * 2 + i) ^ (row & 7)) << 4);
-                        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(to + kTileBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
-                }
+                const int qi = r / a.group, hg = r - qi * a.group;
+                const int64_t at = (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD;
+                stage_query_parts(q, kTileBytes, a.q, at, s.nrows - (row_in - lane), [&](int row, float step) {
+                    qscale[row_in - lane + row] = fmaxf(step * a.scale_log2, 0x1p-126f);
+                });
                 if constexpr (kScored) {
                     __syncwarp();  // (the rows' scales were written by other lanes)
                     RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, r, a.index_error);

@@ -29,9 +29,9 @@ constexpr int kBins = 2048;
 constexpr int kMostKeys = 40960;  // that a CTA holds in shared memory; more are read again
 constexpr int kMaxCluster = 8;
 
-__device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ uint2 ld_shared_cluster_v2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
 }
 
@@ -90,11 +90,13 @@ __device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t (&warps)[33], uint
 
 __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_constant__ EvictProblem p, int ctas, int held) {
     extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ uint32_t hist[3][kBins];
-    __shared__ uint32_t warps[33], found[2], mine_above[2];
+    __shared__ __align__(8) uint32_t hist[3][kBins];
+    __shared__ uint32_t warps[33], found[2];
+    __shared__ __align__(8) uint2 mine;  // tokens above the threshold and equal to it
     const int item = blockIdx.x / ctas, rank = blockIdx.x - item * ctas;
     const int b = item / p.cache.heads, h = item - b * p.cache.heads;
     for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
+    if (threadIdx.x == 0) mine = make_uint2(0, 0);
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const Budget g = budget_of(p, b, h == 0 && rank == 0 && threadIdx.x == 0);
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
     const int begin = static_cast<int>(begin64 < g.len ? begin64 : g.len);
     const int n = static_cast<int>(begin64 + run < g.len ? run : g.len - begin);
     const int* table = p.page_table + static_cast<int64_t>(b) * p.table_stride;
-    auto read = [&](int i) -> uint4 {  // the numbers of tokens begin + i .. + 3
+    auto read = [&](int i) -> uint4 {  // the numbers of tokens begin + i .. + 3; 0, below every weight's, past the last
         const int pos = begin + i, page = ld_dep_s32(table + (pos >> p.cache.page_log2));
         uint4 w = make_uint4(0x7FFFFFFFu, 0x7FFFFFFFu, 0x7FFFFFFFu, 0x7FFFFFFFu);
         if (page >= 0 && page < p.cache.num_pages)
@@ -124,18 +126,25 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
             atomicOr(&g_evict_index_error, 1u);
         uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            u[j] = ordered(__uint_as_float(u[j]));
-            if (pos + j >= g.len - g.recent || pos + j < g.first) u[j] = 0xFFFFFFFFu;
+        for (int j = 0; j < 4; ++j) u[j] = ordered(__uint_as_float(u[j]));
+        if (pos + 4 > g.len - g.recent || pos < g.first) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (pos + j >= g.len - g.recent || pos + j < g.first) u[j] = pos + j < g.len ? 0xFFFFFFFFu : 0;
+        }
+        if (i + 4 > n) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + j >= n) u[j] = 0;
         }
         return make_uint4(u[0], u[1], u[2], u[3]);
     };
     auto again = [&](int i) { return i < held ? *reinterpret_cast<const uint4*>(keys + i) : read(i); };
-    auto each = [&](int i, const uint4& k, auto f) {  // of those there are
+    auto each = [&](const uint4& k, auto f) {
         f(k.x);
-        if (i + 1 < n) f(k.y);
-        if (i + 2 < n) f(k.z);
-        if (i + 3 < n) f(k.w);
+        f(k.y);
+        f(k.z);
+        f(k.w);
     };
     __syncthreads();
 
@@ -150,11 +159,11 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
             for (int i = threadIdx.x * 4; i < n; i += kThreads * 4) {
                 const uint4 k = read(i);
                 if (i < held) *reinterpret_cast<uint4*>(keys + i) = k;
-                each(i, k, [&](uint32_t u) { atomicAdd(count + (u >> 21), 1u); });
+                each(k, [&](uint32_t u) { atomicAdd(count + (u >> 21), 1u); });
             }
         } else {
             for (int i = threadIdx.x * 4; i < n; i += kThreads * 4)
-                each(i, again(i), [&](uint32_t u) {
+                each(again(i), [&](uint32_t u) {
                     if (u >> top == prefix) atomicAdd(count + (u >> shift & mask), 1u);
                 });
         }
@@ -167,13 +176,14 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
         uint32_t lo = 0, hi = 0;
         if (ctas > 1) {
             const uint32_t at = ptx::smem_u32(count + bin);
+            uint2 v[kMaxCluster];
 #pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r)
-                if (r < ctas) {
-                    const uint32_t from = ptx::mapa_shared(at, r);
-                    lo += ld_shared_cluster_u32(from);
-                    hi += ld_shared_cluster_u32(from + 4);
-                }
+            for (int r = 0; r < kMaxCluster; ++r) v[r] = r < ctas ? ld_shared_cluster_v2(ptx::mapa_shared(at, r)) : make_uint2(0, 0);
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                lo += v[r].x;
+                hi += v[r].y;
+            }
         } else {
             lo = count[bin];
             hi = count[bin + 1];
@@ -196,36 +206,35 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
     if (ctas > 1) {
         uint32_t above = 0, equal = 0;
         for (int i = threadIdx.x * 4; i < n; i += kThreads * 4)
-            each(i, again(i), [&](uint32_t u) {
+            each(again(i), [&](uint32_t u) {
                 above += u > threshold;
                 equal += u == threshold;
             });
-        uint32_t total_above, total_equal;
-        scan(above, warps, total_above);
-        scan(equal, warps, total_equal);
-        if (threadIdx.x == 0) {
-            mine_above[0] = total_above;
-            mine_above[1] = total_equal;
+        above = __reduce_add_sync(0xffffffffu, above);
+        equal = __reduce_add_sync(0xffffffffu, equal);
+        if ((threadIdx.x & 31) == 0) {
+            atomicAdd(&mine.x, above);
+            atomicAdd(&mine.y, equal);
         }
         ptx::cluster_sync();
-        const uint32_t at = ptx::smem_u32(mine_above);
+        const uint32_t at = ptx::smem_u32(&mine);
         for (int r = 0; r < rank; ++r) {
-            const uint32_t from = ptx::mapa_shared(at, r);
-            base_above += ld_shared_cluster_u32(from);
-            base_equal += ld_shared_cluster_u32(from + 4);
+            const uint2 v = ld_shared_cluster_v2(ptx::mapa_shared(at, r));
+            base_above += v.x;
+            base_equal += v.y;
         }
     }
     for (int i0 = 0; i0 < n; i0 += kThreads * 4) {
         const int i = i0 + threadIdx.x * 4;
         uint32_t here = 0;  // above in the lower half, equal in the upper: at most 4096 of each
         const uint4 k = i < n ? again(i) : make_uint4(0, 0, 0, 0);
-        if (i < n) each(i, k, [&](uint32_t u) { here += u > threshold ? 1u : u == threshold ? 1u << 16 : 0u; });
+        each(k, [&](uint32_t u) { here += u > threshold ? 1u : u == threshold ? 1u << 16 : 0u; });
         uint32_t total;
         const uint32_t before = scan(here, warps, total);
         uint32_t above = base_above + (before & 0xFFFFu), equal = base_equal + (before >> 16);
         int pos = begin + i;
-        if (i < n)
-            each(i, k, [&](uint32_t u) {
+        if (here)
+            each(k, [&](uint32_t u) {
                 if (u > threshold || (u == threshold && equal < want)) kept[above + min(equal, want)] = pos;
                 above += u > threshold;
                 equal += u == threshold;

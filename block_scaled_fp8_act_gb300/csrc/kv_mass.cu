@@ -24,7 +24,8 @@ namespace {
 __device__ unsigned int g_mass_index_error;
 
 constexpr int kTile = 32;
-constexpr int kItemCost = 4;  // units that an item counts beside its own, for its start
+constexpr int kWideRows = 33;  // rows from which on head size 128 takes the tcgen05 kernel
+constexpr int kItemCost = 8;  // units that an item counts beside its own, for its start
 using Work = Units<kTile, kItemCost, List::kMass>;
 
 // Many rows: one CTA per SM whose warps share the rows in shared memory, as many as the registers allow that a tile's
@@ -33,7 +34,7 @@ using Work = Units<kTile, kItemCost, List::kMass>;
 template <int kD, bool kFew>
 struct Mass {
     static constexpr int kWarps = kFew ? 1 : kD == 64 ? 16 : kD == 128 ? 12 : 8;
-    static constexpr int kCtas = !kFew ? 1 : kD == 256 ? 6 : 8;
+    static constexpr int kCtas = !kFew ? 1 : kD == 256 ? 8 : 16;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRows = kFew ? 16 : kD == 256 ? 128 : 256;
     static constexpr int kStageBytes = kTile * kD + kTile * 4;  // keys, key scales
@@ -43,6 +44,7 @@ struct Mass {
         const int fit = (kRoom - rows * kRowBytes) / (kWarps * kStageBytes);
         return fit < 8 ? fit : 8;
     }
+    static_assert((kRoom - kRows * kRowBytes) / (kWarps * kStageBytes) >= 2, "a tile in flight beside the one being read");
 };
 
 template <int kD, bool kFew, bool kScored>
@@ -105,29 +107,41 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
                 atomicOr(a.index_error, 1u);
                 return -1;
             };
-            // Where token `lane` of the tile is, or -1 (the page in `pages` is asked + 2 i's).
             const int first_pages = look_up(t0 + warp);
             int pages = first_pages, asked = 0;
-            auto place_of = [&](int t, int page) -> int64_t {
-                const int pos = t * kTile + lane;
+            auto place_of = [&](int pos, int page) -> int64_t {
                 return page >= 0 && pos < it.len
                            ? ((static_cast<int64_t>(page) * a.c.heads + it.h) << a.c.page_log2) + (pos & in_page)
                            : -1;
             };
             auto request = [&](int t, int stage) {
                 if (t < t1) {
-                    const int page = __shfl_sync(0xffffffffu, pages, 2 * asked + (lane >> 4));
+                    const int p0 = __shfl_sync(0xffffffffu, pages, 2 * asked), p1 = __shfl_sync(0xffffffffu, pages, 2 * asked + 1);
                     if (seen(t)) {
-                        const int64_t place = place_of(t, page);
                         const uint32_t dst = ptx::smem_u32(ring) + stage * M::kStageBytes;
-                        constexpr int kC = kD / 16, kStep = 32 / kC;  // chunks per token, tokens per instruction
-                        const int c = lane % kC, r0 = lane / kC;
+                        constexpr int kC = kD / 16, kStep = 32 / kC, kSteps = 32 / kStep;  // chunks per token, tokens per instruction
+                        const int c = lane % kC, r0 = lane / kC, pos0 = t * kTile;
+                        const int64_t row_a = ((static_cast<int64_t>(p0) * a.c.heads + it.h) << a.c.page_log2) + (pos0 & in_page);
+                        const int64_t row_b =
+                            ((static_cast<int64_t>(p1) * a.c.heads + it.h) << a.c.page_log2) + ((pos0 + 16) & in_page) - 16;
+                        const int end_a = p0 >= 0 ? it.len - pos0 : 0, end_b = p1 >= 0 ? it.len - pos0 : 0;  // tokens there are
+                        const uint32_t scales = dst + kTile * kD + lane * 4;
+                        if (min(end_a, end_b) >= kTile) {
+                            const uint8_t *ka = a.c.k + (row_a + r0) * kD + c * 16, *kb = a.c.k + (row_b + r0) * kD + c * 16;
 #pragma unroll
-                        for (int j = 0; j < kTile / kStep; ++j) {
-                            const int64_t at = __shfl_sync(0xffffffffu, place, j * kStep + r0);
-                            cp_async16(dst + stage_offset<kD>(j * kStep + r0, c), a.c.k + (at >= 0 ? at : 0) * kD + c * 16, at >= 0);
+                            for (int j = 0; j < kSteps; ++j)
+                                cp_async16(dst + stage_offset<kD>(j * kStep + r0, c), (j * kStep < 16 ? ka : kb) + j * kStep * kD, true);
+                            cp_async4(scales, a.c.k_scale + (lane < 16 ? row_a : row_b) + lane, true);
+                        } else {
+#pragma unroll 1
+                            for (int j = 0; j < kSteps; ++j) {
+                                const int row = j * kStep + r0;
+                                const bool first = j * kStep < 16, in = row < (first ? end_a : end_b);
+                                cp_async16(dst + stage_offset<kD>(row, c), a.c.k + (in ? ((first ? row_a : row_b) + row) * kD + c * 16 : 0), in);
+                            }
+                            const bool in = lane < (lane < 16 ? end_a : end_b);
+                            cp_async4(scales, a.c.k_scale + (in ? (lane < 16 ? row_a : row_b) + lane : 0), in);
                         }
-                        cp_async4(dst + kTile * kD + lane * 4, a.c.k_scale + (place >= 0 ? place : 0), place >= 0);
                     }
                     if (++asked == 16) {
                         asked = 0;
@@ -182,12 +196,11 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
             float have = 0.0f;
             auto look_ahead = [&](int t) {
                 if (t >= t1) return;
-                const int64_t place = place_of(t, __shfl_sync(0xffffffffu, held, 2 * used + (lane >> 4)));
+                mine = place_of(t * kTile + my_token, __shfl_sync(0xffffffffu, held, 2 * used + (my_token >> 4)));
                 if (++used == 16) {
                     used = 0;
                     held = look_up(t + M::kWarps);
                 }
-                mine = __shfl_sync(0xffffffffu, place, my_token);
                 const bool adds = row0 > 0 || (a.accumulate && t * kTile + my_token < old_end);
                 have = adds && mine >= 0 ? ld_dep_f32(a.mass + mine) : 0.0f;
             };
@@ -325,6 +338,10 @@ cudaError_t launch(AttnArgs& a, int64_t rows, int num_sms, cudaStream_t stream) 
 template <int kD>
 cudaError_t launch_rows(AttnArgs& a, bool scored, int max_q_len, int num_sms, cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(max_q_len) * a.group;
+    if (kD == 128 && rows >= kWideRows) {
+        a.rows = kWideRows;  // (any: an item has all rows)
+        return launch_mass_tc(a, scored, num_sms, stream);
+    }
     if (rows <= Mass<kD, true>::kRows)
         return scored ? launch<kD, true, true>(a, rows, num_sms, stream) : launch<kD, true, false>(a, rows, num_sms, stream);
     return scored ? launch<kD, false, true>(a, rows, num_sms, stream) : launch<kD, false, false>(a, rows, num_sms, stream);

@@ -518,7 +518,7 @@ FP8ACT_API int fp8act_check_status(void* stream);
 
 /*
  * Test hook for the failure path of the tcgen05 kernels (the GEMMs above M =
- * 16, attention with wide row tiles). Every wait
+ * 16, attention with wide row tiles, the weights of many rows). Every wait
  * of those kernels on a barrier that another role completes is bounded by
  * wall time (2 s by default); on expiry the CTA stops issuing work, waits for
  * the copies and MMAs it has already issued, frees its tensor memory, leaves,

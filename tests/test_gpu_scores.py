@@ -338,3 +338,42 @@ def test_score_refusals(fp8act):  # noqa: F811
         a.update(bad)
         with pytest.raises((TypeError, ValueError)):
             fp8act.fp8_kv_attention_mass(q, cache, table, kv, cu, **a)
+
+
+@pytest.mark.parametrize("n,group", [(6, 6), (9, 6), (16, 6), (32, 6), (43, 6), (64, 4), (100, 7)])
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_masses_of_many_rows(fp8act, n, group, page):  # noqa: F811
+    """The tcgen05 kernel of head size 128: one to three times its rows, ragged tiles of 128 tokens, pages of every size."""
+    lens = [n, 127, 128, 129, 1, 700, 0, 2500]
+    ns = [min(n, L) if b % 2 == 0 else n for b, L in enumerate(lens)]
+    cache, table = make_cache(fp8act, lens, 2, 128, page, seed=n + page)
+    q = randn(sum(ns), 2 * group, 128, seed=3)
+    check(fp8act, q, cache, table, lens, ns)
+    check(fp8act, q, cache, table, lens, ns, **options(lens, ns, 2 * group, n)["sinks"])
+
+
+def test_masses_of_many_rows_over_long_contexts(fp8act):  # noqa: F811
+    rng = np.random.default_rng(4)
+    lens = [int(x) for x in rng.integers(1, 3000, 30)] + [40000]
+    ns = [min(int(x), L) for x, L in zip(rng.integers(0, 40, 31), lens)]
+    cache, table = make_cache(fp8act, lens, 2, 128, 16, seed=63)
+    q = randn(sum(ns), 8, 128, seed=64)
+    for hint in (20, 100):
+        check(fp8act, q, cache, table, lens, ns, max_q_len=hint)
+
+
+def test_mass_wait_that_runs_out(fp8act):  # noqa: F811
+    """The tcgen05 kernel leaves cleanly when a copy never comes, and the next call is right."""
+    lens, ns = [3000, 100], [16, 16]
+    cache, table = make_cache(fp8act, lens, 2, 128, 64, seed=71)
+    q = randn(32, 12, 128, seed=72)
+    _, lse = check(fp8act, q, cache, table, lens, ns)
+    args = (q, cache, table, i32(lens), i32([0, 16, 32]), lse)
+    mass = torch.zeros(cache.k_scale.shape, device="cuda")
+    try:
+        fp8act.set_wait_limit(1_000_000, True)
+        fp8act.fp8_kv_attention_mass(*args, mass, max_q_len=16)
+        assert fp8act.check_status() == 5  # FP8ACT_ERR_TIMEOUT
+    finally:
+        fp8act.set_wait_limit(-1, False)
+    check(fp8act, q, cache, table, lens, ns)
