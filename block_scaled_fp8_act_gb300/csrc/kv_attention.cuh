@@ -148,6 +148,12 @@ __device__ __forceinline__ void load_tokens(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+__device__ __forceinline__ float4 lds_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 // 32 rows of queries of head size 128 as the two E4M3 parts of a tcgen05 operand (128-byte rows, swizzled), the low one
 // `apart` bytes behind the high one: a row, scaled by a power of two so that its largest value is in [128, 256), is
 // E4M3(q) + E4M3(q - E4M3(q)), exact down to 2^-9 of its largest value and within 2^-17 of that below. `at` is the

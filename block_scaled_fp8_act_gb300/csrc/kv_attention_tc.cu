@@ -177,11 +177,6 @@ constexpr uint32_t kIdescValues = (1u << 4)                                   //
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ float4 lds_v4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
-}
 
 // Where the key scale of a tile's token lies, so that a lane reads those of its columns 4 at a time.
 __device__ __forceinline__ int scale_at(int t) { return (t & ~15) | ((t >> 1 & 3) << 2) | ((t >> 3 & 1) << 1) | (t & 1); }

@@ -161,12 +161,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
         return true;
     };
     const int* table = nullptr;
-    auto page_of = [&](int pos) -> int {  // of a position of the item, -1 if there is none
-        if (pos >= it.len) return -1;
-        const int p = ld_dep_s32(table + (pos >> a.c.page_log2));
-        if (p >= 0 && p < a.c.num_pages) return p;
-        atomicOr(a.index_error, 1u);
-        return -1;
+    // The page of a position of the item as the table has it (0 past its end), and whether there is one. Apart, so that a
+    // page is not waited for where it is asked for.
+    auto page_of = [&](int pos) { return pos < it.len ? ld_dep_s32(table + (pos >> a.c.page_log2)) : 0; };
+    auto is_page = [&](int pos, int page) {
+        if (pos >= it.len) return false;
+        const bool ok = page >= 0 && page < a.c.num_pages;
+        if (!ok) atomicOr(a.index_error, 1u);
+        return ok;
     };
     auto place_of = [&](int page, int pos) {
         return ((static_cast<int64_t>(page) * a.c.heads + it.h) << a.c.page_log2) + (pos & ((1 << a.c.page_log2) - 1));
@@ -183,20 +185,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
             const Job j = job_of();
             table = a.table + it.b * a.table_stride;
             // Lane i < 128 / box: copy i of the tile, if it holds a token; its page is looked up a tile ahead.
-            auto look_up = [&](int i) { return i < j.n && lane < kTok / box ? page_of(j.tile(i) * kTok + lane * box) : -1; };
+            auto look_up = [&](int i) { return i < j.n && lane < kTok / box ? page_of(j.tile(i) * kTok + lane * box) : 0; };
             int ahead = look_up(0);
             for (int i = 0; i < j.n; ++i, ++n) {
                 const int page = ahead;
                 ahead = look_up(i + 1);
                 const uint32_t round = n / kStages, stage = n - round * kStages, bar = k_full + 8 * stage;
                 if (round > 0 && !(ok = wait(k_empty + 8 * stage, (round - 1) & 1))) break;
-                const uint32_t copies = __ballot_sync(0xffffffffu, page >= 0);
+                const int pos = j.tile(i) * kTok + lane * box;
+                const bool copy = lane < kTok / box && is_page(pos, page);
+                const uint32_t copies = __ballot_sync(0xffffffffu, copy);
                 const bool withheld = x.withhold && n == 0;
                 if (lane == 0 && !withheld) ptx::mbar_arrive_expect_tx(bar, __popc(copies) * box * kD);
                 __syncwarp();
-                if (page >= 0 && !withheld)
-                    load_tokens(base + kK + stage * kTileBytes + lane * box * kD, &k_map, bar,
-                                static_cast<int>(place_of(page, j.tile(i) * kTok + lane * box)));
+                if (copy && !withheld)
+                    load_tokens(base + kK + stage * kTileBytes + lane * box * kD, &k_map, bar, static_cast<int>(place_of(page, pos)));
             }
             if (!ok || !next(j)) break;
         }
@@ -251,29 +254,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
             const Job j = job_of();
             table = a.table + it.b * a.table_stride;
             const int old_end = it.len - it.nq;  // positions before it keep their weight if accumulating
-            // What token `pos` has so far; its place.
-            auto fetch = [&](int t, int64_t& place, float& have, float& ks) {
-                const int pos = t * kTok + mine, page = page_of(pos);
-                place = page >= 0 ? place_of(page, pos) : -1;
+            // The place of this thread's token of tile t, what it has so far and its key scale.
+            auto fetch = [&](int t, int page, int64_t& place, float& have, float& ks) {
+                const int pos = t * kTok + mine;
+                place = is_page(pos, page) ? place_of(page, pos) : -1;
                 const bool adds = j.row0 > 0 || (a.accumulate && pos < old_end);
                 have = adds && place >= 0 ? ld_dep_f32(a.mass + place) : 0.0f;
                 ks = place >= 0 ? ld_dep_f32(a.c.k_scale + place) : 0.0f;
             };
-            // The accumulator's tiles are every other one; the first one's values, on their way while the queries are staged
-            // (unless another warpgroup may still write them, for the rows before).
+            auto look_up = [&](int i) { return i < j.n ? page_of(j.tile(i) * kTok + mine) : 0; };
+            // The accumulator's tiles are every other one; the first one's values are on their way while the queries are staged,
+            // once the rows before are done with theirs.
             const int first = (static_cast<uint32_t>(acc) - seq) & 1;
             int64_t place = -1;
             float have = 0.0f, ks = 0.0f;
-            if (first < j.n && j.row0 == 0) fetch(j.tile(first), place, have, ks);
+            const int page = look_up(first);
+            int page_ahead = look_up(first + 2);
+            const int r0 = (warp - 4) * 32;
+            const int r = j.row0 + r0 + lane;  // this lane's row of the sequence's
+            const int qi = r / a.group, hg = r - qi * a.group;
+            float lse = kNegInf;
+            if (r0 + lane < j.nrows)
+                lse = ld_dep_f32(a.lse + static_cast<int64_t>(it.q0 + qi) * (a.c.heads * a.group) + it.h * a.group + hg);
 
             // Queries: rows 32 (warp - 4) .. + 31 of the job, once the job before is done with its own.
             if (jobs > 0 && !(ok = wait(rows_done, (jobs - 1) & 1))) break;
             if (jobs > 0 && !(ok = wait(mma_done, (jobs - 1) & 1))) break;
-            if (first < j.n && j.row0 > 0) fetch(j.tile(first), place, have, ks);
-            const int r0 = (warp - 4) * 32;
+            if (first < j.n) fetch(j.tile(first), page, place, have, ks);
             if (r0 < j.columns) {
-                const int r = j.row0 + r0 + lane;  // this lane's row of the sequence's
-                const int qi = r / a.group, hg = r - qi * a.group;
                 stage_query_parts(smem + kQ + r0 * kD, kRows * kD, a.q,
                                   (it.q0 + qi) * a.q_stride + static_cast<int64_t>(it.h * a.group + hg) * kD, j.nrows - r0,
                                   [&](int row, float step) { row_scores[r0 + row].qs = fmaxf(step * a.scale_log2, 0x1p-126f); });
@@ -282,12 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
                 RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, r, a.index_error);
                 info.qs = qs;
                 float less = kNegInf;  // a row that is not one, or sees nothing, adds nothing
-                if (r0 + lane < j.nrows) {
-                    const float lse = ld_dep_f32(a.lse + static_cast<int64_t>(it.q0 + qi) * (a.c.heads * a.group) + it.h * a.group + hg);
-                    if (lse != kNegInf) less = lse * -1.4426950408889634f;
-                } else {
-                    info.lo = info.limit = 0;
-                }
+                if (lse != kNegInf) less = lse * -1.4426950408889634f;
+                if (r0 + lane >= j.nrows) info.lo = info.limit = 0;
                 row_scores[r0 + lane] = info;
                 float* const pair = pairs + (r0 + lane) / 2 * 4 + (lane & 1);
                 pair[0] = qs;
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
                     if (j.seen(t) || (a.accumulate && (t + 1) * kTok <= old_end)) continue;
                     int64_t at;
                     float old, unused;
-                    fetch(t, at, old, unused);
+                    fetch(t, page_of(t * kTok + mine), at, old, unused);
                     if (at >= 0) a.mass[at] = old;
                 }
 
@@ -314,22 +318,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
                 const int64_t to = place;
                 const float old = have, k = ks;
                 const int pos0 = j.tile(i) * kTok, pos = pos0 + mine;
-                if (i + 2 < j.n) fetch(j.tile(i + 2), place, have, ks);
+                if (i + 2 < j.n) fetch(j.tile(i + 2), page_ahead, place, have, ks);
+                page_ahead = look_up(i + 4);
                 if (!(ok = wait(s_full + 8 * acc, n >> 1 & 1))) break;
                 tc::fence_after_sync();
                 const bool edge = on_edge(pos0, kTok, it.prefix, j.lo, j.limit);
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 const float2 k2 = make_float2(k, k);
-                auto add = [&](const uint32_t (&s)[32], int c) {  // columns c .. c + 31
+                auto add = [&](const uint32_t (&s)[32], const float4 (&row)[16], int c) {  // columns c .. c + 31
                     float2 y[16];
 #pragma unroll
                     for (int w = 0; w < 16; ++w) {
-                        const float4 row = *reinterpret_cast<const float4*>(pairs + (c + 2 * w) * 2);
                         y[w] = __fmul2_rn(make_float2(__uint_as_float(s[2 * w]), __uint_as_float(s[2 * w + 1])), k2);
-                        if constexpr (kScored)
-                            y[w] = __fmul2_rn(y[w], make_float2(row.x, row.y));
-                        else
-                            y[w] = __ffma2_rn(y[w], make_float2(row.x, row.y), make_float2(row.z, row.w));
+                        y[w] = kScored ? __fmul2_rn(y[w], make_float2(row[w].x, row[w].y))
+                                       : __ffma2_rn(y[w], make_float2(row[w].x, row[w].y), make_float2(row[w].z, row[w].w));
                     }
                     if constexpr (kScored) {
                         if (a.scores.cap > 0.0f)
@@ -346,10 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
                             }
                         }
 #pragma unroll
-                        for (int w = 0; w < 16; ++w) {
-                            const float2 less = *reinterpret_cast<const float2*>(pairs + (c + 2 * w) * 2 + 2);
-                            y[w] = __fadd2_rn(y[w], less);
-                        }
+                        for (int w = 0; w < 16; ++w) y[w] = __fadd2_rn(y[w], make_float2(row[w].z, row[w].w));
                     }
                     if (edge) {
 #pragma unroll
@@ -362,18 +361,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
 #pragma unroll
                     for (int w = 0; w < 16; ++w) sum[w & 1] = __fadd2_rn(sum[w & 1], make_float2(ex2(y[w].x), ex2(y[w].y)));
                 };
+                // The rows' values of 32 columns are asked for together, and the scores of the next 32.
+                float4 row[16];
+                auto rows_from = [&](int c) {
+#pragma unroll
+                    for (int w = 0; w < 16; ++w) row[w] = lds_v4(ptx::smem_u32(pairs) + (c + 2 * w) * 8);
+                };
                 uint32_t s0[32], s1[32];
                 tc::ld_32x32b_x32(t_s, s0);
-                tc::wait_ld(s0);
 #pragma unroll 1
-                for (int c = 0; c < j.columns; c += 64) {  // the next columns on their way
+                for (int c = 0; c < j.columns; c += 64) {
+                    rows_from(c);
+                    tc::wait_ld(s0);
                     if (c + 32 < j.columns) tc::ld_32x32b_x32(t_s + c + 32, s1);
-                    add(s0, c);
+                    add(s0, row, c);
                     if (c + 32 >= j.columns) break;
+                    rows_from(c + 32);
                     tc::wait_ld(s1);
                     if (c + 64 < j.columns) tc::ld_32x32b_x32(t_s + c + 64, s0);
-                    add(s1, c + 32);
-                    if (c + 64 < j.columns) tc::wait_ld(s0);
+                    add(s1, row, c + 32);
                 }
                 tc::fence_before_sync();
                 __syncwarp();
