@@ -92,13 +92,14 @@ __device__ __forceinline__ float quant_f32_group_halfwarp(float2 (&f)[4], uint2&
     return s;
 }
 
-// Quantises one head vector, 8 fp32 values a lane: s = amax / 448 (1 for an
-// all-zero vector), f becomes the quotients f / s. `top` is the bit pattern of
+// Quantises one head vector, 8 or 16 fp32 values a lane: s = amax / 448 (1 for
+// an all-zero vector), which become the quotients by s. `top` is the bit pattern of
 // the largest magnitude, where NaN and infinity order above every finite value;
 // a vector that holds one becomes zeros with a NaN scale. The quotients are
 // formed as in act_group.cuh: for bf16 values those of the IEEE division, for
 // rounded fp32 ones within an ulp of it.
-__device__ __forceinline__ float quant_head(float2 (&f)[4], uint32_t top) {
+template <class... Chunk>
+__device__ __forceinline__ float quant_head_chunks(uint32_t top, Chunk&... chunks) {
     const float amax = __uint_as_float(top);
     float s;
     if (amax >= kFastQuotientMinAmax && amax <= kFastQuotientMaxAmax) {
@@ -108,20 +109,28 @@ __device__ __forceinline__ float quant_head(float2 (&f)[4], uint32_t top) {
         const float y0 = rcp_approx_ftz(s);
         const float y = __fmaf_rn(__fmaf_rn(-s, y0, 1.0f), y0, y0);
         const float2 y2 = make_float2(y, y), minus_s = make_float2(-s, -s);
+        auto quotients = [&](float2 (&f)[4]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 q0 = __fmul2_rn(f[i], y2);
-            f[i] = __ffma2_rn(__ffma2_rn(minus_s, q0, f[i]), y2, q0);
-        }
+            for (int i = 0; i < 4; ++i) {
+                const float2 q0 = __fmul2_rn(f[i], y2);
+                f[i] = __ffma2_rn(__ffma2_rn(minus_s, q0, f[i]), y2, q0);
+            }
+        };
+        (quotients(chunks), ...);
     } else {
         const bool finite = top < 0x7F800000u;
         s = top == 0 ? 1.0f : finite ? __fdiv_rn(amax, kE4M3Max) : __uint_as_float(0x7FFFFFFFu);
+        auto quotients = [&](float2 (&f)[4]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f[i] = finite ? make_float2(__fdiv_rn(f[i].x, s), __fdiv_rn(f[i].y, s)) : make_float2(0.0f, 0.0f);
+            for (int i = 0; i < 4; ++i)
+                f[i] = finite ? make_float2(__fdiv_rn(f[i].x, s), __fdiv_rn(f[i].y, s)) : make_float2(0.0f, 0.0f);
+        };
+        (quotients(chunks), ...);
     }
     return s;
 }
+__device__ __forceinline__ float quant_head(float2 (&f)[4], uint32_t top) { return quant_head_chunks(top, f); }
+__device__ __forceinline__ float quant_head(float2 (&f)[4], float2 (&g)[4], uint32_t top) { return quant_head_chunks(top, f, g); }
 
 // Launch with programmatic stream serialization (and a cluster size when it
 // is above 1): the kernel may start before the previous one has finished and

@@ -15,11 +15,15 @@
 // remainder, in [-1/2, 1/2) of a turn, is cut to 32 bits and rounded to fp32:
 // 2^-25 of itself and 2^-32 of a turn.
 //
-// Work split. A CTA is one warp: it takes some rounds of a token's heads, a
-// round up to kAhead steps of 32 / (D / 8) vectors of one kind, the next
-// round's loads in flight. It finds the token's sines and cosines itself, a few
-// per lane, and no warp waits for another. A token is cut into as many pieces
-// as fill the SMs (its sines are cheap beside a second wait for memory).
+// Work split. A lane holds two chunks of 8 columns of a vector, those whose
+// columns turn together, so that a turn needs no other lane; D / 16 lanes hold
+// the vector, and a warp has 512 / D heads of one kind. It keeps them: a CTA's
+// warps go through tokens, each with its heads, their weights in registers and the
+// loads of the next two tokens in flight, and the CTA finds the next tokens' sines
+// and cosines, a pair a thread, while it works on the present ones. More heads
+// than a CTA's warps hold are other CTAs'. (4096 tokens x 32 heads of 128: a warp
+// per token, which finds its own sines, 17.9 us, with one chunk a lane and a
+// vector's halves exchanged 21.0.)
 #include "decoder_util.cuh"
 #include "kernels.h"
 
@@ -29,7 +33,8 @@ namespace {
 __device__ unsigned int g_rope_index_error;
 
 constexpr int kMaxHalf = 128;  // pairs of a head
-constexpr int kCtas = 20;      // warps per SM
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kCtas = 2;       // per SM
 
 enum Kind { kQuery, kKey, kValue };
 
@@ -45,203 +50,242 @@ __device__ __forceinline__ uint64_t units_of(uint64_t bits) {
     return bits >> 63 ? 0 - u : u;
 }
 
-// Lane l of a vector's kLanes holds columns 8l .. 8l + 7.
-template <int kLanes, bool kInterleaved, int kAhead>
-__global__ void __launch_bounds__(32, kCtas) rope_append_kernel(const __grid_constant__ RopeProblem p, int pieces, int rounds) {
-    __shared__ float2 turns[kMaxHalf];  // (cos, sin) * rope_scale
-    constexpr int kPer = 32 / kLanes;   // vectors of a step
-    const int lane = threadIdx.x, hl = lane % kLanes, mine = lane / kLanes;
-    const int64_t t = blockIdx.x / static_cast<unsigned>(pieces);
-    const int piece = blockIdx.x % static_cast<unsigned>(pieces);
+// Sixteen columns of a vector: two chunks of 8.
+struct Half {
+    float2 a[4], b[4];
+};
+__device__ __forceinline__ void unpack(const uint4 (&x)[2], Half& f) {
+    unpack_bf16x8(x[0], f.a);
+    unpack_bf16x8(x[1], f.b);
+}
+
+// The largest magnitude of `most` and the two of `f`; NaN if one is.
+__device__ __forceinline__ float largest(float most, const float2& f) {
+    asm("{\n.reg .f32 a, b;\nabs.f32 a, %1;\nabs.f32 b, %2;\nmax.NaN.f32 %0, %0, a;\nmax.NaN.f32 %0, %0, b;\n}" : "+f"(most) : "f"(f.x), "f"(f.y));
+    return most;
+}
+
+// kLanes = D / 16 lanes hold a vector.
+template <int kLanes, bool kInterleaved, int kTok>
+__global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __grid_constant__ RopeProblem p) {
+    constexpr int kPer = 32 / kLanes;  // vectors of a step
+    constexpr int kD = 16 * kLanes;
+    constexpr int kPairs = (kD / 2 * kTok + 95) / 96;  // pairs of a thread, at most (a CTA has at least 3 warps)
+    __shared__ __align__(16) float2 turns[2][kTok][kMaxHalf];  // (cos, sin) * rope_scale
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hl = lane % kLanes;
     const KvCache& c = p.cache;
-    const int half = p.rot / 2;
-    // Rounds of queries, then of keys, then of values.
-    const int rounds_q = (p.q_heads + kAhead * kPer - 1) / (kAhead * kPer), rounds_k = (c.heads + kAhead * kPer - 1) / (kAhead * kPer);
-    const int begin = piece * rounds, end = min(begin + rounds, rounds_q + 2 * rounds_k);
+    const int half = p.rot / 2, tiles = (p.tokens + kTok - 1) / kTok;
+    // This warp's heads: steps of queries, then of keys, then of values.
+    const int steps_q = (p.q_heads + kPer - 1) / kPer, steps_k = (c.heads + kPer - 1) / kPer;
+    const int s = blockIdx.y * (blockDim.x >> 5) + warp;
+    const Kind kind = s < steps_q ? kQuery : s < steps_q + steps_k ? kKey : kValue;
+    const int heads = kind == kQuery ? p.q_heads : c.heads;
+    const int h = (s - (kind == kQuery ? 0 : kind == kKey ? steps_q : steps_q + steps_k)) * kPer + lane / kLanes;
+    const bool mine = h < heads;  // (past the values' heads: an idle warp)
+    const bool normed = kind == kQuery ? p.q_weight != nullptr : kind == kKey && p.k_weight != nullptr;
+    // The lane's chunks: columns i and i + R / 2 turn together (or, interleaved, neighbours); what does not turn is shared
+    // out after that.
+    const int reach = p.rot / 16;  // chunks of half the rotated columns
+    const bool rotated = hl < reach;
+    const int chunk_a = kInterleaved || !rotated ? 2 * hl : hl, chunk_b = kInterleaved || !rotated ? 2 * hl + 1 : hl + reach;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
 
-    auto kind_of = [&](int r) { return r < rounds_q ? kQuery : r < rounds_q + rounds_k ? kKey : kValue; };
-    auto first_of = [&](int r) {  // the round's first vector among those of its kind
-        return (r < rounds_q ? r : r < rounds_q + rounds_k ? r - rounds_q : r - rounds_q - rounds_k) * kAhead * kPer;
+    const int64_t stride = kind == kQuery ? p.q_stride : kind == kKey ? p.k_stride : p.v_stride;
+    const uint16_t* row = (kind == kQuery ? p.q : kind == kKey ? p.k : p.v) + (mine ? h : 0) * kD + chunk_a * 8;
+    const int apart = (chunk_b - chunk_a) * 8;
+    // Token i of this CTA's, kTok of every gridDim.x tiles.
+    auto token_at = [&](int i) { return (static_cast<int64_t>(i / kTok) * gridDim.x + blockIdx.x) * kTok + i % kTok; };
+    auto load = [&](int i, uint4 (&x)[2]) {
+        const int64_t t = token_at(i);
+        x[0] = x[1] = make_uint4(0, 0, 0, 0);
+        if (mine && t < p.tokens) {
+            x[0] = ld_dep_stream_v4(row + t * stride);
+            x[1] = ld_dep_stream_v4(row + t * stride + apart);
+        }
     };
-    // A round's vectors: this lane's part of the first, 512 bytes apart, and how many of them are the lane's.
-    auto row_of = [&](int r) {
-        const Kind kind = kind_of(r);
-        const uint16_t* row = kind == kQuery ? p.q + t * p.q_stride : kind == kKey ? p.k + t * p.k_stride : p.v + t * p.v_stride;
-        return row + static_cast<int64_t>(first_of(r)) * (8 * kLanes) + lane * 8;
-    };
-    auto left_of = [&](int r) { return r < end ? (kind_of(r) == kQuery ? p.q_heads : c.heads) - first_of(r) - mine : 0; };
-    auto load = [&](const uint16_t* row, int left, int i) {
-        return i * kPer < left ? ld_dep_stream_v4(row + i * 256) : make_uint4(0, 0, 0, 0);
-    };
-    uint4 x[kAhead];
+    uint4 x[kTok][2];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) x[i] = load(row_of(begin), left_of(begin), i);
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    const uint4 wq = p.q_weight ? ld_dep_v4(p.q_weight + hl * 8) : none, wk = p.k_weight ? ld_dep_v4(p.k_weight + hl * 8) : none;
-    int64_t slot = *const_cast<const volatile int64_t*>(p.slots + t);
-    if (kind_of(begin) != kValue) {
-        for (int i = lane; i < half; i += 32) {
-            const uint64_t freq = *const_cast<const volatile uint64_t*>(reinterpret_cast<const uint64_t*>(p.inv_freq) + i);
-            int axis = p.axis ? ld_dep_s32(p.axis + i) : 0;
+    for (int i = 0; i < kTok; ++i) load(i, x[i]);
+    Half w;
+    {
+        const uint16_t* from = kind == kQuery ? p.q_weight : p.k_weight;
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        const uint4 packed[2] = {normed ? ld_dep_v4(from + chunk_a * 8) : none, normed ? ld_dep_v4(from + chunk_b * 8) : none};
+        unpack(packed, w);
+        const float2 offset = make_float2(p.weight_offset, p.weight_offset);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w.a[j] = __fadd2_rn(w.a[j], offset);
+            w.b[j] = __fadd2_rn(w.b[j], offset);
+        }
+    }
+
+    // This thread's pairs of a tile: their units a position, and where their positions are.
+    uint64_t units[kPairs];
+    const int64_t* position[kPairs];
+    int pair[kPairs], token[kPairs];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+        const int at = threadIdx.x + j * blockDim.x;
+        token[j] = half > 0 ? min(at / half, kTok) : kTok;
+        pair[j] = at - token[j] * half;
+        units[j] = 0;
+        position[j] = p.positions;
+        if (token[j] < kTok) {
+            units[j] = units_of(*const_cast<const volatile uint64_t*>(reinterpret_cast<const uint64_t*>(p.inv_freq) + pair[j]));
+            int axis = p.axis ? ld_dep_s32(p.axis + pair[j]) : 0;
             if (axis < 0 || axis >= p.n_axes) {
                 atomicOr(&g_rope_index_error, 1u);
                 axis = 0;
             }
-            const int64_t pos = *const_cast<const volatile int64_t*>(p.positions + static_cast<int64_t>(axis) * p.tokens + t);
-            const uint32_t units = static_cast<uint32_t>(static_cast<uint64_t>(pos) * units_of(freq) >> 32);
-            const float at = __int2float_rn(static_cast<int>(units)) * 0x1p-31f;  // half turns
+            position[j] += static_cast<int64_t>(axis) * p.tokens;
+        }
+    }
+    auto position_of = [&](int tile, int j) -> int64_t {
+        const int64_t t = static_cast<int64_t>(tile) * kTok + token[j];
+        return token[j] < kTok && tile < tiles && t < p.tokens ? *const_cast<const volatile int64_t*>(position[j] + t) : 0;
+    };
+    auto turn_by = [&](const int64_t (&pos)[kPairs], int buffer) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            if (token[j] >= kTok) continue;
+            const uint32_t u = static_cast<uint32_t>(static_cast<uint64_t>(pos[j]) * units[j] >> 32);
+            const float at = __int2float_rn(static_cast<int>(u)) * 0x1p-31f;  // half turns
             float sn, cs;
             sincospif(at, &sn, &cs);
-            turns[i] = make_float2(cs * p.rope_scale, sn * p.rope_scale);
+            turns[buffer][token[j]][pair[j]] = make_float2(cs * p.rope_scale, sn * p.rope_scale);
         }
-    }
-    if (slot >= static_cast<int64_t>(c.num_pages) << c.page_log2) {
-        if (lane == 0) atomicOr(&g_rope_index_error, 1u);
-        slot = -1;
-    }
-    const int64_t place = slot < 0 ? 0 : ((slot >> c.page_log2) * c.heads << c.page_log2) + (slot & ((1 << c.page_log2) - 1));
-    __syncwarp();
-
-    // The lane's cosines and sines, two columns each: of its 8 columns' pairs, the first half's sines negative, or of its
-    // 4 pairs, the first column's.
-    const int reach = p.rot / 16;  // lanes of half the rotated columns
-    const bool rotated = hl < 2 * reach, second = hl >= reach, all_rotated = p.rot == 8 * kLanes;
-    float2 cs[4], sn[4];
+    };
+    int64_t pos[kPairs];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        cs[i] = sn[i] = make_float2(0.0f, 0.0f);
-        if (rotated) {
-            if constexpr (kInterleaved) {
-                const float2 u = turns[hl * 4 + i];
-                cs[i] = make_float2(u.x, u.x);
-                sn[i] = make_float2(-u.y, u.y);
-            } else {
-                const float4 u = *reinterpret_cast<const float4*>(turns + (second ? hl - reach : hl) * 8 + 2 * i);
-                cs[i] = make_float2(u.x, u.z);
-                sn[i] = second ? make_float2(u.y, u.w) : make_float2(-u.y, -u.w);
-            }
-        }
-    }
-    const int partner = rotated ? (second ? lane - reach : lane + reach) : lane;
+    for (int j = 0; j < kPairs; ++j) pos[j] = position_of(blockIdx.x, j);
+    turn_by(pos, 0);
+    __syncthreads();
 
     // Norm and turn of a vector (a turn is linear, so that the reciprocal root comes last and its sum is not waited for).
-    auto turned = [&](float2 (&f)[4], const float2 (&w)[4], bool normed) {
+    auto turned = [&](Half& f, const float2* turn) {
         float r = 1.0f;
         if (normed) {
-            float2 sum = __fmul2_rn(f[0], f[0]);
+            float2 sum = __fmul2_rn(f.a[0], f.a[0]);
 #pragma unroll
-            for (int j = 1; j < 4; ++j) sum = __ffma2_rn(f[j], f[j], sum);
+            for (int j = 1; j < 4; ++j) sum = __ffma2_rn(f.a[j], f.a[j], sum);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum = __ffma2_rn(f.b[j], f.b[j], sum);
             float all = sum.x + sum.y;
 #pragma unroll
             for (int o = kLanes / 2; o >= 1; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-            asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(fmaf(all, 1.0f / (8 * kLanes), p.eps)));
+            asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(fmaf(all, 1.0f / kD, p.eps)));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = __fmul2_rn(f[j], w[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float2 other = make_float2(f[j].y, f[j].x);
-            if constexpr (!kInterleaved) {
-                other.x = __shfl_sync(0xffffffffu, f[j].x, partner);
-                other.y = __shfl_sync(0xffffffffu, f[j].y, partner);
+            for (int j = 0; j < 4; ++j) {
+                f.a[j] = __fmul2_rn(f.a[j], w.a[j]);
+                f.b[j] = __fmul2_rn(f.b[j], w.b[j]);
             }
-            const float2 z = __ffma2_rn(other, sn[j], __fmul2_rn(f[j], cs[j]));
-            if (all_rotated || rotated) f[j] = z;
         }
-        if (normed) {
+        if (rotated) {
+            // The lane's 8 pairs: the two chunks' columns of one number, or, interleaved, 4 in each chunk.
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = __fmul2_rn(f[j], make_float2(r, r));
-        }
-    };
-    auto weight = [&](const uint4& packed, float2 (&w)[4]) {
-        unpack_bf16x8(packed, w);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = __fadd2_rn(w[j], make_float2(p.weight_offset, p.weight_offset));
-    };
-    auto store = [&](float2 (&f)[4], uint32_t top, int h, uint8_t* codes, float* scales) {
-#pragma unroll
-        for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float s = quant_head(f, top);
-        if (slot < 0 || h >= c.heads) return;
-        const int64_t at = place + (static_cast<int64_t>(h) << c.page_log2);
-        reinterpret_cast<uint2*>(codes)[at * kLanes + hl] = pack_e4m3x8(f);
-        if (hl == 0) scales[at] = s;
-    };
-
-    for (int r = begin; r < end; ++r) {
-        const int first = first_of(r), left = left_of(r), left_next = left_of(r + 1);
-        const uint16_t* const row_next = row_of(r + 1);
-        const Kind kind = kind_of(r);
-        // Each step's registers are asked for again as soon as they are read.
-        if (kind == kQuery) {
-            float2 w[4];
-            weight(wq, w);
-            uint4* const out = reinterpret_cast<uint4*>(p.q_out) + (t * p.q_heads + first) * kLanes + lane;
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                float2 f[4];
-                unpack_bf16x8(x[i], f);
-                x[i] = load(row_next, left_next, i);
-                if (first + i * kPer >= p.q_heads) continue;
-                turned(f, w, p.q_weight != nullptr);
-                if (i * kPer < left) out[i * 32] = pack_bf16x8(f);
-            }
-        } else {
-            float2 w[4];
-            weight(wk, w);
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                float2 f[4];
-                unpack_bf16x8(x[i], f);
-                uint32_t top = top_bits(x[i]) << 16;
-                x[i] = load(row_next, left_next, i);
-                if (first + i * kPer >= c.heads) continue;
-                if (kind == kKey) {
-                    turned(f, w, p.k_weight != nullptr);
-                    top = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        top = max(top, max(__float_as_uint(f[j].x) & 0x7FFFFFFFu, __float_as_uint(f[j].y) & 0x7FFFFFFFu));
-                    store(f, top, first + i * kPer + mine, c.k, c.k_scale);
+            for (int j = 0; j < 4; ++j) {
+                const float2 a = f.a[j], b = f.b[j];
+                const float4 u = *reinterpret_cast<const float4*>(turn + hl * 8 + 2 * j);
+                if constexpr (kInterleaved) {
+                    // (pairs 2j, 2j + 1 of the lane's 8 are chunk a's columns 4j .. for j < 2, then chunk b's)
+                    float2& y0 = j < 2 ? f.a[2 * j] : f.b[2 * j - 4];
+                    float2& y1 = j < 2 ? f.a[2 * j + 1] : f.b[2 * j - 3];
+                    y0 = make_float2(fmaf(-u.y, y0.y, u.x * y0.x), fmaf(u.y, y0.x, u.x * y0.y));
+                    y1 = make_float2(fmaf(-u.w, y1.y, u.z * y1.x), fmaf(u.w, y1.x, u.z * y1.y));
                 } else {
-                    store(f, top, first + i * kPer + mine, c.v, c.v_scale);
+                    f.a[j] = make_float2(fmaf(-u.y, b.x, u.x * a.x), fmaf(-u.w, b.y, u.z * a.y));
+                    f.b[j] = make_float2(fmaf(u.y, a.x, u.x * b.x), fmaf(u.w, a.y, u.z * b.y));
                 }
             }
         }
+        if (normed) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f.a[j] = __fmul2_rn(f.a[j], make_float2(r, r));
+                f.b[j] = __fmul2_rn(f.b[j], make_float2(r, r));
+            }
+        }
+    };
+    uint16_t* const out = reinterpret_cast<uint16_t*>(p.q_out) + h * kD + chunk_a * 8;
+    const int64_t out_stride = static_cast<int64_t>(p.q_heads) * kD;
+    uint8_t* const codes = kind == kKey ? c.k : c.v;
+    float* const scales = kind == kKey ? c.k_scale : c.v_scale;
+    int buffer = 0;
+    for (int tile = blockIdx.x, i0 = 0; tile < tiles; tile += gridDim.x, i0 += kTok) {
+        int64_t pos_next[kPairs];
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) pos_next[j] = position_of(tile + gridDim.x, j);
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+            const int64_t t = static_cast<int64_t>(tile) * kTok + i;
+            int64_t slot = -1;
+            if (kind != kQuery && t < p.tokens) slot = *const_cast<const volatile int64_t*>(p.slots + t);
+            Half f;
+            unpack(x[i], f);
+            uint32_t top = max(top_bits(x[i][0]), top_bits(x[i][1])) << 16;
+            load(i0 + kTok + i, x[i]);
+            if (kind != kValue) turned(f, turns[buffer][i]);
+            if (kind == kQuery) {
+                if (mine && t < p.tokens) {
+                    *reinterpret_cast<uint4*>(out + t * out_stride) = pack_bf16x8(f.a);
+                    *reinterpret_cast<uint4*>(out + t * out_stride + apart) = pack_bf16x8(f.b);
+                }
+                continue;
+            }
+            if (slot >= static_cast<int64_t>(c.num_pages) << c.page_log2) {
+                atomicOr(&g_rope_index_error, 1u);
+                slot = -1;
+            }
+            if (kind == kKey) {
+                float most = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    most = largest(most, f.a[j]);
+                    most = largest(most, f.b[j]);
+                }
+                top = __float_as_uint(most) & 0x7FFFFFFFu;
+            }
+#pragma unroll
+            for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float scale = quant_head(f.a, f.b, top);
+            if (!mine || slot < 0) continue;
+            const int64_t at = (((slot >> c.page_log2) * c.heads + h) << c.page_log2) + (slot & ((1 << c.page_log2) - 1));
+            uint2* const to = reinterpret_cast<uint2*>(codes + at * kD);
+            to[chunk_a] = pack_e4m3x8(f.a);
+            to[chunk_b] = pack_e4m3x8(f.b);
+            if (hl == 0) scales[at] = scale;
+        }
+        if (tile + static_cast<int>(gridDim.x) >= tiles) break;
+        buffer ^= 1;
+        turn_by(pos_next, buffer);
+        __syncthreads();  // the next turns are there, and the warps have read the ones before the present
     }
 }
 
-template <int kLanes, int kAhead>
-cudaError_t launch(const RopeProblem& p, int num_sms, cudaStream_t stream) {
-    constexpr int kRound = kAhead * 32 / kLanes;
-    const int64_t whole = (static_cast<int64_t>(p.q_heads) + kRound - 1) / kRound + 2 * ((static_cast<int64_t>(p.cache.heads) + kRound - 1) / kRound);
-    // Pieces of a token: enough for every warp that fits the SMs at once.
-    const int64_t room = (static_cast<int64_t>(num_sms) * kCtas + p.tokens - 1) / p.tokens;
-    const int64_t rounds = (whole + room - 1) / room;
-    const int64_t pieces = (whole + rounds - 1) / rounds;
-    if (p.tokens * pieces > INT32_MAX) return cudaErrorInvalidConfiguration;
-    auto kernel = p.interleaved ? rope_append_kernel<kLanes, true, kAhead> : rope_append_kernel<kLanes, false, kAhead>;
-    return launch_dependent(kernel, dim3(static_cast<unsigned>(p.tokens * pieces)), 32, 0, stream, 1, p, static_cast<int>(pieces),
-                            static_cast<int>(rounds));
-}
-
-// A step at a time while that gives no more warps than fit: a token's heads are then all on their way at once.
 template <int kLanes>
-cudaError_t launch_ahead(const RopeProblem& p, int num_sms, cudaStream_t stream) {
-    const int64_t vectors = (p.q_heads + 2 * static_cast<int64_t>(p.cache.heads)) * p.tokens;
-    return vectors * kLanes / 32 <= static_cast<int64_t>(num_sms) * kCtas ? launch<kLanes, 1>(p, num_sms, stream)
-                                                                          : launch<kLanes, 4>(p, num_sms, stream);
+cudaError_t launch(const RopeProblem& p, int num_sms, cudaStream_t stream) {
+    constexpr int kPer = 32 / kLanes;
+    const int steps = (p.q_heads + kPer - 1) / kPer + 2 * ((p.cache.heads + kPer - 1) / kPer);
+    const int groups = (steps + kWarps - 1) / kWarps, warps = (steps + groups - 1) / groups;
+    if (groups > 65535) return cudaErrorInvalidConfiguration;
+    // Two tokens at a time once there are enough to keep every CTA busy with more than one such pair.
+    const int resident = (num_sms * kCtas + groups - 1) / groups;
+    const bool many = p.tokens > 2 * resident;
+    const int tiles = many ? (p.tokens + 1) / 2 : p.tokens;
+    auto kernel = many ? (p.interleaved ? rope_append_kernel<kLanes, true, 2> : rope_append_kernel<kLanes, false, 2>)
+                       : (p.interleaved ? rope_append_kernel<kLanes, true, 1> : rope_append_kernel<kLanes, false, 1>);
+    return launch_dependent(kernel, dim3(tiles < resident ? tiles : resident, groups), warps * 32, 0, stream, 1, p);
 }
 
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeProblem& p, int num_sms, cudaStream_t stream) {
     switch (p.cache.head_dim) {
-        case 64: return launch_ahead<8>(p, num_sms, stream);
-        case 128: return launch_ahead<16>(p, num_sms, stream);
-        default: return launch_ahead<32>(p, num_sms, stream);
+        case 64: return launch<4>(p, num_sms, stream);
+        case 128: return launch<8>(p, num_sms, stream);
+        default: return launch<16>(p, num_sms, stream);
     }
 }
 
