@@ -234,15 +234,16 @@ int check_rows(const fp8act::KvCache& c, int64_t q_stride, int max_pages, int ba
     return FP8ACT_OK;
 }
 
-// The caller's score function as the kernels take it, in units of log2.
+// The caller's score function as the kernels take it.
 int check_scores(const fp8act_scores* in, fp8act::Scores* out, bool* scored) {
     *out = {};
+    out->unit = 1.0f;
     *scored = false;
     if (!in) return FP8ACT_OK;
     if (in->window < 0 || !(in->soft_cap == 0.0f || (in->soft_cap >= 1e-30f && in->soft_cap <= 1e30f)))
         return FP8ACT_ERR_SHAPE;
-    out->cap = in->soft_cap * 1.4426950408889634f;
-    out->cap_inv = in->soft_cap > 0.0f ? 1.0f / out->cap : 0.0f;
+    out->capped = in->soft_cap > 0.0f;
+    if (out->capped) out->unit = in->soft_cap * 1.4426950408889634f;
     out->window = in->window;
     out->prefix = in->prefix_lens;
     out->first = in->first;

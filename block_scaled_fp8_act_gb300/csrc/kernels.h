@@ -146,10 +146,11 @@ struct RopeProblem {
 };
 cudaError_t launch_rope_append(const RopeProblem& p, int num_sms, cudaStream_t stream);
 
-// What an attention score is beside the scaled product (see scores.cuh); cap
-// in units of log2. All zero: nothing.
+// What an attention score is beside the scaled product (see scores.cuh); the
+// unit is the cap in units of log2, or 1, and goes into the softmax's scale.
 struct Scores {
-    float cap, cap_inv;
+    bool capped;
+    float unit;
     int window;
     const int* prefix;    // [batch] or null
     const int* first;     // [tokens] or null

@@ -233,9 +233,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas, kScored>::kThrea
             [&](int r, float step) {
                 const float qs = fmaxf(step * a.scale_log2, 0x1p-126f);
                 if constexpr (kScored) {
-                    RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, row0 + r, a.index_error);
-                    info.qs = qs;
-                    row_scores[r] = info;
+                    row_scores[r] = row_score(a.scores, qs, it.q0, it.len, it.nq, a.group, it.h, row0 + r, a.index_error);
                 } else {
                     qscale[r] = qs;
                 }
@@ -258,7 +256,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas, kScored>::kThrea
                 const int r = wr * S::kWarpRows + i * 8 + qd * 2 + e;
                 mq[i][e] = kNegInf;
                 l[i][e] = 0.0f;
-                qs[i][e] = kScored ? 1.0f : qscale[r];  // (kScored: scores are whole before the softmax)
+                qs[i][e] = kScored ? a.scores.unit : qscale[r];  // (kScored: the rows' own are in their scores)
                 limit[i][e] = it.len - it.nq + (row0 + r) / a.group + 1;
             }
         }
@@ -355,9 +353,8 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas, kScored>::kThrea
 #pragma unroll
                         for (int x = 0; x < 4; ++x) s[x >> 1][i][(x & 1) * 2 + e] *= row_qs;
                     }
-                if (a.scores.cap > 0.0f)
+                if (a.scores.capped)
                     cap_scores<kRW * 4>(
-                        a.scores.cap, a.scores.cap_inv,
                         [&](int j) { return make_float2(s[j & 1][j >> 2][j & 2], s[j & 1][j >> 2][(j & 2) + 1]); },
                         [&](int j, const float2& y) {
                             s[j & 1][j >> 2][j & 2] = y.x;
@@ -786,7 +783,7 @@ cudaError_t launch_kv_attention(const AttentionProblem& p, int num_sms, cudaStre
     const cudaError_t found = cudaGetSymbolAddress(&error, g_attn_index_error);
     if (found != cudaSuccess) return found;
     a.index_error = static_cast<unsigned int*>(error);
-    a.scale_log2 = p.softmax_scale * 1.4426950408889634f;
+    a.scale_log2 = p.softmax_scale * 1.4426950408889634f / p.scores.unit;
     a.c = p.cache;
     a.out = static_cast<uint32_t*>(p.out);
     a.lse = p.lse;

@@ -524,9 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                 });
                 if constexpr (kScored) {
                     __syncwarp();  // (the rows' scales were written by other lanes)
-                    RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, r, a.index_error);
-                    info.qs = qscale[row_in];
-                    row_scores[row_in] = info;
+                    row_scores[row_in] = row_score(a.scores, qscale[row_in], it.q0, it.len, it.nq, a.group, it.h, r, a.index_error);
                 }
                 fence_async_proxy();
                 __syncwarp();
@@ -544,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int at = row_in - lane + (lane >> 2) + 8 * i;
-                qs[i] = kScored ? 1.0f : qscale[at];  // (kScored: scores are whole before the softmax)
+                qs[i] = kScored ? a.scores.unit : qscale[at];  // (kScored: the rows' own are in their scores)
                 limit[i] = it.len - it.nq + (s.row0 + at) / a.group + 1;
                 m[i] = kNegInf;
                 mq[i] = 0.0f;
@@ -625,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                             const float row_qs[2] = {info[0].qs, info[8].qs};
 #pragma unroll
                             for (int i = 0; i < 32; ++i) set(i, __fmul2_rn(get(i), make_float2(row_qs[i & 1], row_qs[i & 1])));
-                            if (a.scores.cap > 0.0f) cap_scores<32>(a.scores.cap, a.scores.cap_inv, get, set);
+                            if (a.scores.capped) cap_scores<32>(get, set);
                             const int first = pos + 2 * (lane & 3);
                             if (a.scores.slopes) {
                                 const float2 down[2] = {make_float2(-info[0].slope, -info[0].slope), make_float2(-info[8].slope, -info[8].slope)};

@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
                     return ld_dep_v4(a.q + (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD + c * 8);
                 },
                 [&](int r, float step) {
-                    RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, row0 + r, a.index_error);
-                    info.qs = fmaxf(step * a.scale_log2, 0x1p-126f);
+                    RowScore info = row_score(a.scores, fmaxf(step * a.scale_log2, 0x1p-126f), it.q0, it.len, it.nq, a.group, it.h,
+                                              row0 + r, a.index_error);
                     float less = kNegInf;  // a row that is not one, or sees nothing, adds nothing
                     if (r < nrows) {
                         const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
@@ -261,9 +261,9 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
                             y[j] = kScored ? y[j] * qs : fmaf(y[j], qs, less);
                         }
                         if constexpr (kScored) {
-                            if (a.scores.cap > 0.0f)
+                            if (a.scores.capped)
                                 cap_scores<4>(
-                                    a.scores.cap, a.scores.cap_inv, [&](int j) { return make_float2(y[2 * j], y[2 * j + 1]); },
+                                    [&](int j) { return make_float2(y[2 * j], y[2 * j + 1]); },
                                     [&](int j, const float2& z) {
                                         y[2 * j] = z.x;
                                         y[2 * j + 1] = z.y;
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
                                 for (int j = 0; j < 8; ++j) y[j] = fmaf(-slope[j & 1], fabsf(far[j & 1] - (j >> 1) * 8), y[j]);
                             }
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) y[j] += j & 1 ? row.w : row.y;
+                            for (int j = 0; j < 8; ++j) y[j] = fmaf(y[j], a.scores.unit, j & 1 ? row.w : row.y);
                         }
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
@@ -365,7 +365,7 @@ cudaError_t launch_kv_mass(const MassProblem& p, int num_sms, cudaStream_t strea
     const cudaError_t found = cudaGetSymbolAddress(&error, g_mass_index_error);
     if (found != cudaSuccess) return found;
     a.index_error = static_cast<unsigned int*>(error);
-    a.scale_log2 = p.softmax_scale * 1.4426950408889634f;
+    a.scale_log2 = p.softmax_scale * 1.4426950408889634f / p.scores.unit;
     a.c = p.cache;
     a.lse = const_cast<float*>(p.lse);
     a.scores = p.scores;

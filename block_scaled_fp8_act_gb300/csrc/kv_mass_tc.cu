@@ -287,14 +287,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
                                   [&](int row, float step) { row_scores[r0 + row].qs = fmaxf(step * a.scale_log2, 0x1p-126f); });
                 __syncwarp();  // (the rows' scales were written by other lanes)
                 const float qs = row_scores[r0 + lane].qs;
-                RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, r, a.index_error);
-                info.qs = qs;
+                RowScore info = row_score(a.scores, qs, it.q0, it.len, it.nq, a.group, it.h, r, a.index_error);
                 float less = kNegInf;  // a row that is not one, or sees nothing, adds nothing
                 if (lse != kNegInf) less = lse * -1.4426950408889634f;
                 if (r0 + lane >= j.nrows) info.lo = info.limit = 0;
                 row_scores[r0 + lane] = info;
                 float* const pair = pairs + (r0 + lane) / 2 * 4 + (lane & 1);
-                pair[0] = qs;
+                pair[0] = info.qs;
                 pair[2] = less;
                 fence_async_proxy();
             }
@@ -334,9 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
                                        : __ffma2_rn(y[w], make_float2(row[w].x, row[w].y), make_float2(row[w].z, row[w].w));
                     }
                     if constexpr (kScored) {
-                        if (a.scores.cap > 0.0f)
-                            cap_scores<16>(
-                                a.scores.cap, a.scores.cap_inv, [&](int w) { return y[w]; }, [&](int w, const float2& z) { y[w] = z; });
+                        if (a.scores.capped)
+                            cap_scores<16>([&](int w) { return y[w]; }, [&](int w, const float2& z) { y[w] = z; });
                         if (a.scores.slopes) {
                             // (distances from the sequence's end, which are small whole numbers where they matter)
                             const float from = static_cast<float>(pos - it.len);
@@ -348,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
                             }
                         }
 #pragma unroll
-                        for (int w = 0; w < 16; ++w) y[w] = __fadd2_rn(y[w], make_float2(row[w].z, row[w].w));
+                        for (int w = 0; w < 16; ++w) y[w] = __ffma2_rn(y[w], make_float2(a.scores.unit, a.scores.unit), make_float2(row[w].z, row[w].w));
                     }
                     if (edge) {
 #pragma unroll

@@ -1,6 +1,6 @@
 // Scores that are more than a scaled product, for the attention kernels and the
 // accumulated weights: a cap, a bias by distance, and which positions a row sees.
-// Everything is in units of log2, as the exponentials want it.
+// A score times Scores::unit is an exponent of 2: the unit is the cap, or 1.
 #pragma once
 
 #include "decoder_util.cuh"
@@ -8,55 +8,55 @@
 
 namespace fp8act {
 
-// cap * tanh(y / cap) of a thread's scores, kPairs pairs that `get` gives and `set` takes; the whole warp calls it. To within
-// 2^-22 of a score up to |y| = 0.625 cap and 2^-21 cap beyond. Near zero, where most scores are, tanh(z) / z is a polynomial
-// in z^2 (interpolated at the Chebyshev points of [0, 0.625^2], 1.0e-7 off in fp32), four two-wide instructions a score;
-// 1 - 2 / (1 + e^2z) takes two of the special functions', at an eighth of the rate, and loses a small score's bits in the
-// difference, so it is for warps that hold a larger one. Which form a score gets goes by its own value alone.
+// Scores are carried in units of the cap while there is one, so that its division is the queries' scale's and its product
+// the exponent's: tanh(z) of a thread's scores, kPairs pairs that `get` gives and `set` takes; the whole warp calls it. To
+// within 2^-22 of a score up to |z| = 0.625 and 2^-21 beyond. Near zero, where most scores are, tanh(z) / z is a polynomial
+// in z^2 (interpolated at the Chebyshev points of [0, 0.625^2], 1.0e-7 off in fp32), 3.5 two-wide instructions a score;
+// 1 - 2 / (1 + e^2z) takes two of the special functions' and loses a small score's bits in the difference, so it is for
+// warps that hold a larger one. Which form a score gets goes by its own value alone.
 template <int kPairs, class Get, class Set>
-__device__ __forceinline__ void cap_scores(float cap, float cap_inv, Get get, Set set) {
+__device__ __forceinline__ void cap_scores(Get get, Set set) {
     float most = 0.0f;
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-        const float2 y = get(i);
-        most = fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y)));
+        const float2 z = get(i);
+        most = fmaxf(most, fmaxf(fabsf(z.x), fabsf(z.y)));
     }
-    const bool far = __any_sync(0xffffffffu, most * cap_inv > 0.625f);
-    auto near = [&](const float2& y, const float2& z) {
+    const bool far = __any_sync(0xffffffffu, most > 0.625f);
+    auto near = [&](const float2& z) {
         const float2 u = __fmul2_rn(z, z);
         auto both = [](float x) { return make_float2(x, x); };
         float2 p = __ffma2_rn(both(-0.005657135f), u, both(0.020588191f));
         p = __ffma2_rn(p, u, both(-0.05372011f));
         p = __ffma2_rn(p, u, both(0.13331114f));
         p = __ffma2_rn(p, u, both(-0.3333326f));
-        return __fmul2_rn(y, __ffma2_rn(p, u, both(1.0f)));
+        return __fmul2_rn(z, __ffma2_rn(p, u, both(1.0f)));
     };
-    const float2 inv = make_float2(cap_inv, cap_inv);
     if (!far) {
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-            const float2 y = get(i);
-            set(i, near(y, __fmul2_rn(y, inv)));
-        }
+        for (int i = 0; i < kPairs; ++i) set(i, near(get(i)));
         return;
     }
+    auto any = [](float z) {  // (one at a time: in pairs the tcgen05 kernel spilled half as much again)
+        const float u = z * z;
+        float p = fmaf(-0.005657135f, u, 0.020588191f);
+        p = fmaf(p, u, -0.05372011f);
+        p = fmaf(p, u, 0.13331114f);
+        p = fmaf(p, u, -0.3333326f);
+        p = z * fmaf(p, u, 1.0f);
+        const float e = ex2(fabsf(z) * 2.8853900817779268f);  // 2 / ln 2
+        return fabsf(z) > 0.625f ? copysignf(fmaf(-2.0f, rcp_approx_ftz(1.0f + e), 1.0f), z) : p;
+    };
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-        const float2 y = get(i), z = __fmul2_rn(y, inv);
-        float2 w = near(y, z);
-        auto flat = [&](float x) {
-            const float e = ex2(fabsf(x) * 2.8853900817779268f);  // 2 / ln 2
-            return copysignf(fmaf(-2.0f * cap, rcp_approx_ftz(1.0f + e), cap), x);
-        };
-        if (fabsf(z.x) > 0.625f) w.x = flat(z.x);
-        if (fabsf(z.y) > 0.625f) w.y = flat(z.y);
-        set(i, w);
+        const float2 z = get(i);
+        set(i, make_float2(any(z.x), any(z.y)));
     }
 }
 
 // How a row (new token, query head) scores and what it sees: positions below the sequence's prefix, and [lo, limit).
 struct __align__(16) RowScore {
-    float qs;  // of the query's scaling, with the softmax's scale
+    float qs;  // of the query's scaling, with the softmax's scale, over the unit
     int lo, limit;
     float slope;
 };
@@ -70,13 +70,14 @@ __device__ __forceinline__ int first_seen(const Scores& s, int q0, int len, int 
 }
 
 // Row `row` of a sequence's (rows past its last are as that one), of KV head h.
-__device__ __forceinline__ RowScore row_score(const Scores& s, int q0, int len, int nq, int group, int h, int row, unsigned int* error) {
+__device__ __forceinline__ RowScore row_score(const Scores& s, float qs, int q0, int len, int nq, int group, int h, int row,
+                                              unsigned int* error) {
     const int qi = min(row / group, nq - 1);
     RowScore r;
-    r.qs = 0.0f;
+    r.qs = fminf(qs, 3e38f);  // (a tiny cap of huge queries: still 0 times a product of 0)
     r.lo = first_seen(s, q0, len, nq, qi);
     r.limit = len - nq + qi + 1;
-    r.slope = s.slopes ? ld_dep_f32(s.slopes + h * group + row % group) * 1.4426950408889634f : 0.0f;
+    r.slope = s.slopes ? ld_dep_f32(s.slopes + h * group + row % group) * (1.4426950408889634f / s.unit) : 0.0f;
     if (s.first && qi > 0 && ld_dep_s32(s.first + q0 + qi) < ld_dep_s32(s.first + q0 + qi - 1)) atomicOr(error, 1u);
     return r;
 }
