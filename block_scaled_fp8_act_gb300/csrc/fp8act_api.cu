@@ -235,10 +235,9 @@ int check_rows(const fp8act::KvCache& c, int64_t q_stride, int max_pages, int ba
 }
 
 // The caller's score function as the kernels take it.
-int check_scores(const fp8act_scores* in, fp8act::Scores* out, bool* scored) {
+int check_scores(const fp8act_scores* in, fp8act::Scores* out) {
     *out = {};
     out->unit = 1.0f;
-    *scored = false;
     if (!in) return FP8ACT_OK;
     if (in->window < 0 || !(in->soft_cap == 0.0f || (in->soft_cap >= 1e-30f && in->soft_cap <= 1e30f)))
         return FP8ACT_ERR_SHAPE;
@@ -248,7 +247,9 @@ int check_scores(const fp8act_scores* in, fp8act::Scores* out, bool* scored) {
     out->prefix = in->prefix_lens;
     out->first = in->first;
     out->slopes = in->slopes;
-    *scored = in->soft_cap > 0.0f || in->window || in->prefix_lens || in->first || in->slopes;
+    out->kind = out->capped || in->slopes                             ? fp8act::ScoreKind::kChanged
+                : in->window || in->prefix_lens || in->first ? fp8act::ScoreKind::kMasked
+                                                              : fp8act::ScoreKind::kPlain;
     return FP8ACT_OK;
 }
 bool aligned_scores(const fp8act::Scores& s) { return aligned(s.prefix, 4) && aligned(s.first, 4) && aligned(s.slopes, 4); }
@@ -450,8 +451,7 @@ int fp8_kv_attention_scored(const void* q_bf16, int64_t q_stride, const int* cu_
     if (int st = check_cache(cache, &c)) return st;
     if (int st = check_rows(c, q_stride, max_pages, batch, tokens, max_q_len, q_heads, softmax_scale)) return st;
     fp8act::Scores s;
-    bool scored = false;
-    if (int st = check_scores(scores, &s, &scored)) return st;
+    if (int st = check_scores(scores, &s)) return st;
     if (batch == 0 || tokens == 0) return FP8ACT_OK;
     if (c.num_pages == 0) return FP8ACT_ERR_SHAPE;
     if (!q_bf16 || !cu_q || !kv_lens || !out_bf16 || !workspace || (max_pages > 0 && !page_table))
@@ -466,7 +466,7 @@ int fp8_kv_attention_scored(const void* q_bf16, int64_t q_stride, const int* cu_
     if (st) return st;
     const fp8act::AttentionProblem p = {q_bf16,    q_stride,  cu_q,          kv_lens, page_table, max_pages,
                                         batch,     tokens,    max_q_len,     q_heads / c.heads,   softmax_scale,
-                                        c,         out_bf16,  lse,           workspace,           scored, s};
+                                        c,         out_bf16,  lse,           workspace,           s};
     return launch_status(fp8act::launch_kv_attention(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -478,8 +478,7 @@ int fp8_kv_attention_mass(const void* q_bf16, int64_t q_stride, const int* cu_q,
     if (int st = check_cache(cache, &c)) return st;
     if (int st = check_rows(c, q_stride, max_pages, batch, tokens, max_q_len, q_heads, softmax_scale)) return st;
     fp8act::Scores s;
-    bool scored = false;
-    if (int st = check_scores(scores, &s, &scored)) return st;
+    if (int st = check_scores(scores, &s)) return st;
     if (batch == 0) return FP8ACT_OK;
     if (c.num_pages == 0) return FP8ACT_ERR_SHAPE;
     if (!cu_q || !kv_lens || !mass || (tokens > 0 && (!q_bf16 || !lse)) || (max_pages > 0 && !page_table))
@@ -491,7 +490,7 @@ int fp8_kv_attention_mass(const void* q_bf16, int64_t q_stride, const int* cu_q,
     const int sms = current_device_sms(&st);
     if (st) return st;
     const fp8act::MassProblem p = {q_bf16, q_stride, cu_q, kv_lens, page_table, max_pages, batch, tokens, max_q_len,
-                                   q_heads / c.heads, softmax_scale, c, lse, mass, accumulate != 0, scored, s};
+                                   q_heads / c.heads, softmax_scale, c, lse, mass, accumulate != 0, s};
     return launch_status(fp8act::launch_kv_mass(p, sms, static_cast<cudaStream_t>(stream)));
 }
 

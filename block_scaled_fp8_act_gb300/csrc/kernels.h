@@ -148,7 +148,9 @@ cudaError_t launch_rope_append(const RopeProblem& p, int num_sms, cudaStream_t s
 
 // What an attention score is beside the scaled product (see scores.cuh); the
 // unit is the cap in units of log2, or 1, and goes into the softmax's scale.
+enum class ScoreKind { kPlain, kMasked, kChanged };
 struct Scores {
+    ScoreKind kind;  // whether there are masks alone, or a cap or a bias too
     bool capped;
     float unit;
     int window;
@@ -171,7 +173,6 @@ struct AttentionProblem {
     void* out;
     float* lse;
     void* workspace;
-    bool scored;  // whether `scores` says anything
     Scores scores;
 };
 size_t kv_attention_workspace(int max_q_len, int group, int head_dim);
@@ -191,7 +192,7 @@ struct MassProblem {
     KvCache cache;
     const float* lse;
     float* mass;  // [num_pages, heads, page]
-    bool accumulate, scored;
+    bool accumulate;
     Scores scores;
 };
 cudaError_t launch_kv_mass(const MassProblem& p, int num_sms, cudaStream_t stream);

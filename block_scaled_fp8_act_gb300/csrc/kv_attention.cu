@@ -54,8 +54,8 @@ __device__ unsigned int g_attn_index_error;
 constexpr int kTile = 32;  // cached tokens per unit
 constexpr int kLeastUnits = 8;  // least share of a CTA
 constexpr int kItemCost = 20;   // units that an item counts beside its own
-template <bool kScored>
-using WorkOf = Units<kTile, kItemCost, kScored ? List::kScored : List::kPlain>;
+template <ScoreKind kKind>
+using WorkOf = Units<kTile, kItemCost, kKind == ScoreKind::kPlain ? List::kPlain : List::kScored>;
 
 // Transpose of an 8 x 8 matrix of 16-bit values held as an MMA fragment.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
@@ -68,8 +68,9 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
 // where a group is one warp: one streams while the other starts or ends an item, 38 us instead of 46 for 34 ragged
 // sequences x 3 tokens; but one for D = 256, whose stages are twice as large: one token over 32768 with 8 heads on 4
 // 30.2 us instead of 42.2, two tokens of 8 ragged sequences 23.1 instead of 32.8).
-template <int kD, int kWR, int kRW, int kG, int kCtas_, bool kScored>
+template <int kD, int kWR, int kRW, int kG, int kCtas_, ScoreKind kKind>
 struct Attn {
+    static constexpr bool kScored = kKind != ScoreKind::kPlain;
     static constexpr int kCtas = kCtas_;
     static constexpr int kWarpRows = kRW * 8;
     static constexpr int kRows = kWR * kWarpRows;
@@ -100,11 +101,12 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int q0, int h, int 
     if (a.lse && lane == 0) a.lse[at] = sum == 0.0f ? kNegInf : (m + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <int kD, int kWR, int kRW, int kG, int kCtas, bool kScored>
-__global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas, kScored>::kThreads, kCtas)
+template <int kD, int kWR, int kRW, int kG, int kCtas, ScoreKind kKind>
+__global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas, kKind>::kThreads, kCtas)
     kv_attention_kernel(const __grid_constant__ AttnArgs a) {
-    using S = Attn<kD, kWR, kRW, kG, kCtas, kScored>;
-    using Work = WorkOf<kScored>;
+    using S = Attn<kD, kWR, kRW, kG, kCtas, kKind>;
+    using Work = WorkOf<kKind>;
+    constexpr bool kScored = S::kScored, kChanged = kKind == ScoreKind::kChanged;
     constexpr int kRows = S::kRows, kStages = S::kStages;
     constexpr int kKS = kD / 32;  // pairs of k-steps of the score product
     constexpr int kDT = kD / 16;  // 16-row tiles of the transposed output
@@ -231,13 +233,19 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas, kScored>::kThrea
                 return ld_dep_v4(a.q + (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD + c * 8);
             },
             [&](int r, float step) {
-                const float qs = fmaxf(step * a.scale_log2, 0x1p-126f);
-                if constexpr (kScored) {
-                    row_scores[r] = row_score(a.scores, qs, it.q0, it.len, it.nq, a.group, it.h, row0 + r, a.index_error);
-                } else {
-                    qscale[r] = qs;
-                }
+                if constexpr (kScored)
+                    row_scores[r].qs = row_scale(step, a.scale_log2);
+                else
+                    qscale[r] = fmaxf(step * a.scale_log2, 0x1p-126f);
             });
+        if constexpr (kScored) {  // (a thread per row, not one after the other beside its queries)
+            for (int r = threadIdx.x; r < kRows; r += S::kThreads) {
+                const RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, row0 + r, a.index_error);
+                row_scores[r].lo = info.lo;
+                row_scores[r].limit = info.limit;
+                row_scores[r].slope = info.slope;
+            }
+        }
         __syncthreads();
 
         float acc[kDT][kRW][4];
@@ -256,7 +264,8 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas, kScored>::kThrea
                 const int r = wr * S::kWarpRows + i * 8 + qd * 2 + e;
                 mq[i][e] = kNegInf;
                 l[i][e] = 0.0f;
-                qs[i][e] = kScored ? a.scores.unit : qscale[r];  // (kScored: the rows' own are in their scores)
+                // (changed scores have the rows' own scales in them)
+                qs[i][e] = kChanged ? a.scores.unit : kScored ? row_scores[r].qs : qscale[r];
                 limit[i][e] = it.len - it.nq + (row0 + r) / a.group + 1;
             }
         }
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas, kScored>::kThrea
                 for (int x = 0; x < 4; ++x)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) s[x >> 1][i][(x & 1) * 2 + e] *= ks[x];
-            if constexpr (kScored) {
+            if constexpr (kChanged) {
 #pragma unroll
                 for (int i = 0; i < kRW; ++i)
 #pragma unroll
@@ -670,13 +679,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kWide ? 4 : 1) kv_attention_j
         write_row<kD>(a, static_cast<int>(s0.z), static_cast<int>(s0.w), static_cast<int>(s1.x) + r, lane, mm, sum, o);
 }
 
-template <int kD, int kWR, int kRW, int kG, int kCtas, bool kScored>
+template <int kD, int kWR, int kRW, int kG, int kCtas, ScoreKind kKind>
 cudaError_t launch_attention(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream) {
-    using S = Attn<kD, kWR, kRW, kG, kCtas, kScored>;
+    using S = Attn<kD, kWR, kRW, kG, kCtas, kKind>;
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
-    auto kernel = kv_attention_kernel<kD, kWR, kRW, kG, kCtas, kScored>;
+    auto kernel = kv_attention_kernel<kD, kWR, kRW, kG, kCtas, kKind>;
     if (!configured[dev & 63].load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
         if (e != cudaSuccess) return e;
@@ -707,40 +716,42 @@ int rows_of(int max_q_len, int group, int head_dim) {
 }
 
 // Launches the kernel for the row tile; `grid` is its CTAs.
-template <int kD, bool kScored>
+template <int kD, ScoreKind kKind>
 cudaError_t launch_rows(const AttnArgs& a, int num_sms, int& grid, cudaStream_t stream) {
     if constexpr (kD == 64) {
         switch (a.rows) {
-            case 8: return launch_attention<64, 1, 1, 6, 2, kScored>(a, num_sms, grid, stream);
-            case 16: return launch_attention<64, 1, 2, 6, 2, kScored>(a, num_sms, grid, stream);
-            case 24: return launch_attention<64, 1, 3, 6, 2, kScored>(a, num_sms, grid, stream);
-            case 48: return launch_attention<64, 2, 3, 4, 1, kScored>(a, num_sms, grid, stream);
-            case 96: return launch_attention<64, 4, 3, 2, 1, kScored>(a, num_sms, grid, stream);
-            default: return launch_attention<64, 8, 3, 1, 1, kScored>(a, num_sms, grid, stream);
+            case 8: return launch_attention<64, 1, 1, 6, 2, kKind>(a, num_sms, grid, stream);
+            case 16: return launch_attention<64, 1, 2, 6, 2, kKind>(a, num_sms, grid, stream);
+            case 24: return launch_attention<64, 1, 3, 6, 2, kKind>(a, num_sms, grid, stream);
+            case 48: return launch_attention<64, 2, 3, 4, 1, kKind>(a, num_sms, grid, stream);
+            case 96: return launch_attention<64, 4, 3, 2, 1, kKind>(a, num_sms, grid, stream);
+            default: return launch_attention<64, 8, 3, 1, 1, kKind>(a, num_sms, grid, stream);
         }
     } else if constexpr (kD == 128) {
         switch (a.rows) {
-            case 8: return launch_attention<128, 1, 1, 6, 2, kScored>(a, num_sms, grid, stream);
-            case 16: return launch_attention<128, 1, 2, 6, 2, kScored>(a, num_sms, grid, stream);
-            case 24: return launch_attention<128, 1, 3, 4, 2, kScored>(a, num_sms, grid, stream);
-            case 48: return launch_attention<128, 2, 3, 4, 1, kScored>(a, num_sms, grid, stream);
-            default: grid = num_sms; return launch_attention_tc(a, kScored, num_sms, stream);
+            case 8: return launch_attention<128, 1, 1, 6, 2, kKind>(a, num_sms, grid, stream);
+            case 16: return launch_attention<128, 1, 2, 6, 2, kKind>(a, num_sms, grid, stream);
+            case 24: return launch_attention<128, 1, 3, 4, 2, kKind>(a, num_sms, grid, stream);
+            case 48: return launch_attention<128, 2, 3, 4, 1, kKind>(a, num_sms, grid, stream);
+            default: grid = num_sms; return launch_attention_tc(a, num_sms, stream);
         }
     } else {
         switch (a.rows) {
-            case 8: return launch_attention<256, 1, 1, 6, 1, kScored>(a, num_sms, grid, stream);
-            case 16: return launch_attention<256, 2, 1, 4, 1, kScored>(a, num_sms, grid, stream);
-            case 32: return launch_attention<256, 2, 2, 4, 1, kScored>(a, num_sms, grid, stream);
-            default: return launch_attention<256, 4, 2, 2, 1, kScored>(a, num_sms, grid, stream);
+            case 8: return launch_attention<256, 1, 1, 6, 1, kKind>(a, num_sms, grid, stream);
+            case 16: return launch_attention<256, 2, 1, 4, 1, kKind>(a, num_sms, grid, stream);
+            case 32: return launch_attention<256, 2, 2, 4, 1, kKind>(a, num_sms, grid, stream);
+            default: return launch_attention<256, 4, 2, 2, 1, kKind>(a, num_sms, grid, stream);
         }
     }
 }
 
 template <int kD>
-cudaError_t launch_both(const AttnArgs& a, bool scored, int max_q_len, int num_sms, cudaStream_t stream) {
+cudaError_t launch_both(const AttnArgs& a, int max_q_len, int num_sms, cudaStream_t stream) {
     if (num_sms > kMaxAttnGrid / 2) num_sms = kMaxAttnGrid / 2;
     int grid = 0;
-    const cudaError_t e = scored ? launch_rows<kD, true>(a, num_sms, grid, stream) : launch_rows<kD, false>(a, num_sms, grid, stream);
+    const cudaError_t e = a.scores.kind == ScoreKind::kPlain    ? launch_rows<kD, ScoreKind::kPlain>(a, num_sms, grid, stream)
+                          : a.scores.kind == ScoreKind::kMasked ? launch_rows<kD, ScoreKind::kMasked>(a, num_sms, grid, stream)
+                                                                : launch_rows<kD, ScoreKind::kChanged>(a, num_sms, grid, stream);
     if (e != cudaSuccess) return e;
     const int64_t items = static_cast<int64_t>(a.batch) * a.c.heads * ((static_cast<int64_t>(max_q_len) * a.group + a.rows - 1) / a.rows);
     // 4 warps a row while the items are few, so that each has many parts: (us, 1 and 4 warps) one token over 4096 10.1 and
@@ -792,9 +803,9 @@ cudaError_t launch_kv_attention(const AttentionProblem& p, int num_sms, cudaStre
     a.part_o = a.part_ml + slots * 2;
     a.scores = p.scores;
     switch (p.cache.head_dim) {
-        case 64: return launch_both<64>(a, p.scored, p.max_q_len, num_sms, stream);
-        case 128: return launch_both<128>(a, p.scored, p.max_q_len, num_sms, stream);
-        default: return launch_both<256>(a, p.scored, p.max_q_len, num_sms, stream);
+        case 64: return launch_both<64>(a, p.max_q_len, num_sms, stream);
+        case 128: return launch_both<128>(a, p.max_q_len, num_sms, stream);
+        default: return launch_both<256>(a, p.max_q_len, num_sms, stream);
     }
 }
 

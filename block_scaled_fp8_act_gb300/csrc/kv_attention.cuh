@@ -374,9 +374,9 @@ __device__ __forceinline__ TileReach tile_reach(const AttnArgs& a, const Item& i
 
 // The kernel for wide row tiles of head size 128 (kv_attention_tc.cu); the
 // caller launches the join of the split items after it.
-cudaError_t launch_attention_tc(const AttnArgs& a, bool scored, int num_sms, cudaStream_t stream);
+cudaError_t launch_attention_tc(const AttnArgs& a, int num_sms, cudaStream_t stream);
 
 // The weights of cached tokens from many rows of head size 128 (kv_mass_tc.cu).
-cudaError_t launch_mass_tc(const AttnArgs& a, bool scored, int num_sms, cudaStream_t stream);
+cudaError_t launch_mass_tc(const AttnArgs& a, int num_sms, cudaStream_t stream);
 
 }  // namespace fp8act

@@ -50,6 +50,7 @@
 // word and the CTA's abort flag; every role then leaves its loop, copies and
 // MMAs in flight are waited for, tensor memory is freed.
 #include <atomic>
+#include <type_traits>
 
 #include "host_util.h"
 #include "kv_attention.cuh"
@@ -73,8 +74,9 @@ static_assert(256 * kRegsOther + 256 * kRegsSoftmax <= kThreads * 128, "register
 constexpr int kTileBytes = kTok * kD;
 constexpr int kKSets = 4;  // tiles whose key scales are at hand (the values widened are at most 2 behind)
 
-template <bool kPair, bool kScored>  // kPair: two row tiles of 128 on the same tokens
+template <bool kPair, ScoreKind kKind>  // kPair: two row tiles of 128 on the same tokens
 struct Tc {
+    static constexpr bool kScored = kKind != ScoreKind::kPlain;
     // Units that an item counts beside its own, for its queries and its result. (Rows up to 128, 16 tokens x 6 heads over
     // 131072: 5 units 63.6 us, 8 62.0; two row tiles, 512 tokens over 16384: 4 units 122.8 us, 6 126.5.)
     static constexpr int kItemCost = kPair ? 4 : 8;
@@ -188,13 +190,14 @@ __device__ __forceinline__ void swap(T& a, T& b) {
     b = c;
 }
 
-template <bool kPair, bool kScored>
+template <bool kPair, ScoreKind kKind>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __grid_constant__ AttnArgs a,
                                                                       const __grid_constant__ CUtensorMap k_map,
                                                                       const __grid_constant__ CUtensorMap v_map,
                                                                       const TcExtra x) {
-    using C = Tc<kPair, kScored>;
+    using C = Tc<kPair, kKind>;
     using Work = typename C::Work;
+    constexpr bool kScored = C::kScored, kChanged = kKind == ScoreKind::kChanged;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* const smem = smem_raw + (base - ptx::smem_u32(smem_raw));
@@ -520,11 +523,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                 const int qi = r / a.group, hg = r - qi * a.group;
                 const int64_t at = (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD;
                 stage_query_parts(q, kTileBytes, a.q, at, s.nrows - (row_in - lane), [&](int row, float step) {
-                    qscale[row_in - lane + row] = fmaxf(step * a.scale_log2, 0x1p-126f);
+                    qscale[row_in - lane + row] = kScored ? row_scale(step, a.scale_log2) : fmaxf(step * a.scale_log2, 0x1p-126f);
                 });
                 if constexpr (kScored) {
                     __syncwarp();  // (the rows' scales were written by other lanes)
-                    row_scores[row_in] = row_score(a.scores, qscale[row_in], it.q0, it.len, it.nq, a.group, it.h, r, a.index_error);
+                    RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, r, a.index_error);
+                    info.qs = qscale[row_in];
+                    row_scores[row_in] = info;
                 }
                 fence_async_proxy();
                 __syncwarp();
@@ -542,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int at = row_in - lane + (lane >> 2) + 8 * i;
-                qs[i] = kScored ? a.scores.unit : qscale[at];  // (kScored: the rows' own are in their scores)
+                qs[i] = kChanged ? a.scores.unit : qscale[at];  // (changed scores have the rows' own in them)
                 limit[i] = it.len - it.nq + (s.row0 + at) / a.group + 1;
                 m[i] = kNegInf;
                 mq[i] = 0.0f;
@@ -584,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                         tc::wait_ld();
                         float top[2] = {kNegInf, kNegInf};
                         const RowScore* const info = row_scores + row_in - lane + (lane >> 2) + 16 * h;  // of rows 8 x
-                        auto scaled = [&](bool masked) {
+                        auto scaled = [&](bool masked, bool last) {  // `last`: nothing more comes to the scores
 #pragma unroll
                             for (int j = 0; j < kTok / 16; ++j) {
                                 if (j + 1 < kTok / 16) k4[(j + 1) & 1] = lds_v4(ks + (j + 1) * 64);
@@ -602,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                                             if (8 * n >= end) y.x = kNegInf;
                                             if (8 * n + 1 >= end) y.y = kNegInf;
                                         }
-                                        if (!kScored) top[x] = fmaxf(top[x], fmaxf(y.x, y.y));
+                                        if (last) top[x] = fmaxf(top[x], fmaxf(y.x, y.y));
                                         v0 = __float_as_uint(y.x);
                                         v1 = __float_as_uint(y.y);
                                     }
@@ -610,22 +615,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                             }
                         };
                         if (!kScored && edge)
-                            scaled(true);
+                            scaled(true, true);
+                        else if (kChanged || (kScored && edge))
+                            scaled(false, false);
                         else
-                            scaled(false);
-                        if constexpr (kScored) {
+                            scaled(false, true);
+                        if (kChanged || (kScored && edge)) {
                             auto get = [&](int i) { return make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])); };
                             auto set = [&](int i, const float2& y) {
                                 v[2 * i] = __float_as_uint(y.x);
                                 v[2 * i + 1] = __float_as_uint(y.y);
                             };
                             // (pair i is row i & 1, columns 8 (i / 2) + 2 (lane % 4) and the next)
-                            const float row_qs[2] = {info[0].qs, info[8].qs};
+                            if constexpr (kChanged) {
+                                const float row_qs[2] = {info[0].qs, info[8].qs};
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) set(i, __fmul2_rn(get(i), make_float2(row_qs[i & 1], row_qs[i & 1])));
-                            if (a.scores.capped) cap_scores<32>(get, set);
+                                for (int i = 0; i < 32; ++i) set(i, __fmul2_rn(get(i), make_float2(row_qs[i & 1], row_qs[i & 1])));
+                                if (a.scores.capped) cap_scores<32>(get, set);
+                            }
                             const int first = pos + 2 * (lane & 3);
-                            if (a.scores.slopes) {
+                            if (kChanged && a.scores.slopes) {
                                 const float2 down[2] = {make_float2(-info[0].slope, -info[0].slope), make_float2(-info[8].slope, -info[8].slope)};
                                 const float far[2] = {static_cast<float>(info[0].limit - 1 - first), static_cast<float>(info[8].limit - 1 - first)};
 #pragma unroll
@@ -642,7 +651,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
                                     if (at >= it.prefix && (at < lo[x] || at >= end[x])) v[i] = __float_as_uint(kNegInf);
                                 }
                             }
-                            top[0] = top[1] = kNegInf;
 #pragma unroll
                             for (int i = 0; i < 64; ++i) top[i >> 1 & 1] = fmaxf(top[i >> 1 & 1], __uint_as_float(v[i]));
                         }
@@ -821,13 +829,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const __gr
     }
 }
 
-template <bool kPair, bool kScored>
+template <bool kPair, ScoreKind kKind>
 cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
-    using C = Tc<kPair, kScored>;
+    using C = Tc<kPair, kKind>;
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
-    auto kernel = kv_attention_tc_kernel<kPair, kScored>;
+    auto kernel = kv_attention_tc_kernel<kPair, kKind>;
     if (!configured[dev & 63].load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
         if (e != cudaSuccess) return e;
@@ -846,9 +854,16 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_attention_tc(const AttnArgs& a, bool scored, int num_sms, cudaStream_t stream) {
-    if (scored) return a.rows > 128 ? launch<true, true>(a, num_sms, stream) : launch<false, true>(a, num_sms, stream);
-    return a.rows > 128 ? launch<true, false>(a, num_sms, stream) : launch<false, false>(a, num_sms, stream);
+cudaError_t launch_attention_tc(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+    auto of_kind = [&](auto pair) {
+        constexpr bool kPair = decltype(pair)::value;
+        switch (a.scores.kind) {
+            case ScoreKind::kPlain: return launch<kPair, ScoreKind::kPlain>(a, num_sms, stream);
+            case ScoreKind::kMasked: return launch<kPair, ScoreKind::kMasked>(a, num_sms, stream);
+            default: return launch<kPair, ScoreKind::kChanged>(a, num_sms, stream);
+        }
+    };
+    return a.rows > 128 ? of_kind(std::true_type{}) : of_kind(std::false_type{});
 }
 
 unsigned int read_and_clear_attn_timeout() {

@@ -47,7 +47,7 @@ struct Mass {
     static_assert((kRoom - kRows * kRowBytes) / (kWarps * kStageBytes) >= 2, "a tile in flight beside the one being read");
 };
 
-template <int kD, bool kFew, bool kScored>
+template <int kD, bool kFew, bool kChanged>
 __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCtas)
     kv_mass_kernel(const __grid_constant__ AttnArgs a, int stages) {
     using M = Mass<kD, kFew>;
@@ -87,10 +87,8 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
                 const int q_first = row0 / a.group, q_last = (row0 + nrows - 1) / a.group;
                 limit_first = it.len - it.nq + q_first + 1;
                 limit_last = it.len - it.nq + q_last + 1;
-                if constexpr (kScored) {
-                    lo_first = first_seen(a.scores, it.q0, it.len, it.nq, q_first);
-                    lo_last = first_seen(a.scores, it.q0, it.len, it.nq, q_last);
-                }
+                lo_first = first_seen(a.scores, it.q0, it.len, it.nq, q_first);
+                lo_last = first_seen(a.scores, it.q0, it.len, it.nq, q_last);
             }
             // Whether some row may see a token of tile t.
             auto seen = [&](int t) {
@@ -173,20 +171,22 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
                     const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
                     return ld_dep_v4(a.q + (it.q0 + qi) * a.q_stride + (it.h * a.group + hg) * kD + c * 8);
                 },
-                [&](int r, float step) {
-                    RowScore info = row_score(a.scores, fmaxf(step * a.scale_log2, 0x1p-126f), it.q0, it.len, it.nq, a.group, it.h,
-                                              row0 + r, a.index_error);
-                    float less = kNegInf;  // a row that is not one, or sees nothing, adds nothing
-                    if (r < nrows) {
-                        const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
-                        const float lse = ld_dep_f32(a.lse + static_cast<int64_t>(it.q0 + qi) * (a.c.heads * a.group) + it.h * a.group + hg);
-                        if (lse != kNegInf) less = lse * -1.4426950408889634f;
-                    } else {
-                        info.lo = info.limit = 0;
-                    }
-                    row_scores[r] = info;
-                    row_mass[r] = make_float2(info.qs, less);
-                });
+                [&](int r, float step) { row_scores[r].qs = row_mass[r].x = row_scale(step, a.scale_log2); });
+            for (int r = threadIdx.x; r < blocks * 8; r += M::kThreads) {  // (a thread per row)
+                RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, row0 + r, a.index_error);
+                float less = kNegInf;  // a row that is not one, or sees nothing, adds nothing
+                if (r < nrows) {
+                    const int qi = (row0 + r) / a.group, hg = (row0 + r) - qi * a.group;
+                    const float lse = ld_dep_f32(a.lse + static_cast<int64_t>(it.q0 + qi) * (a.c.heads * a.group) + it.h * a.group + hg);
+                    if (lse != kNegInf) less = lse * -1.4426950408889634f;
+                } else {
+                    info.lo = info.limit = 0;
+                }
+                row_scores[r].lo = info.lo;
+                row_scores[r].limit = info.limit;
+                row_scores[r].slope = info.slope;
+                row_mass[r].y = less;
+            }
             __syncthreads();
 
             // Where the weight of the token is that is this lane's in the end, and what it has so far: a tile ahead.
@@ -258,9 +258,9 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
                         for (int j = 0; j < 8; ++j) {
                             y[j] = s[j >> 2][j & 3] * ks[j >> 1];
                             const float qs = j & 1 ? row.z : row.x, less = j & 1 ? row.w : row.y;
-                            y[j] = kScored ? y[j] * qs : fmaf(y[j], qs, less);
+                            y[j] = kChanged ? y[j] * qs : fmaf(y[j], qs, less);
                         }
-                        if constexpr (kScored) {
+                        if constexpr (kChanged) {
                             if (a.scores.capped)
                                 cap_scores<4>(
                                     [&](int j) { return make_float2(y[2 * j], y[2 * j + 1]); },
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
     }
 }
 
-template <int kD, bool kFew, bool kScored>
+template <int kD, bool kFew, bool kChanged>
 cudaError_t launch(AttnArgs& a, int64_t rows, int num_sms, cudaStream_t stream) {
     using M = Mass<kD, kFew>;
     a.rows = rows >= M::kRows ? M::kRows : rows < 8 ? 8 : static_cast<int>((rows + 7) / 8 * 8);
@@ -325,7 +325,7 @@ cudaError_t launch(AttnArgs& a, int64_t rows, int num_sms, cudaStream_t stream) 
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
-    auto kernel = kv_mass_kernel<kD, kFew, kScored>;
+    auto kernel = kv_mass_kernel<kD, kFew, kChanged>;
     if (!configured[dev & 63].load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kRoom);
         if (e != cudaSuccess) return e;
@@ -336,15 +336,16 @@ cudaError_t launch(AttnArgs& a, int64_t rows, int num_sms, cudaStream_t stream) 
 }
 
 template <int kD>
-cudaError_t launch_rows(AttnArgs& a, bool scored, int max_q_len, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rows(AttnArgs& a, int max_q_len, int num_sms, cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(max_q_len) * a.group;
+    const bool changed = a.scores.kind == ScoreKind::kChanged;
     if (kD == 128 && rows >= kWideRows) {
         a.rows = kWideRows;  // (any: an item has all rows)
-        return launch_mass_tc(a, scored, num_sms, stream);
+        return launch_mass_tc(a, num_sms, stream);
     }
     if (rows <= Mass<kD, true>::kRows)
-        return scored ? launch<kD, true, true>(a, rows, num_sms, stream) : launch<kD, true, false>(a, rows, num_sms, stream);
-    return scored ? launch<kD, false, true>(a, rows, num_sms, stream) : launch<kD, false, false>(a, rows, num_sms, stream);
+        return changed ? launch<kD, true, true>(a, rows, num_sms, stream) : launch<kD, true, false>(a, rows, num_sms, stream);
+    return changed ? launch<kD, false, true>(a, rows, num_sms, stream) : launch<kD, false, false>(a, rows, num_sms, stream);
 }
 
 }  // namespace
@@ -372,9 +373,9 @@ cudaError_t launch_kv_mass(const MassProblem& p, int num_sms, cudaStream_t strea
     a.mass = p.mass;
     a.accumulate = p.accumulate;
     switch (p.cache.head_dim) {
-        case 64: return launch_rows<64>(a, p.scored, p.max_q_len, num_sms, stream);
-        case 128: return launch_rows<128>(a, p.scored, p.max_q_len, num_sms, stream);
-        default: return launch_rows<256>(a, p.scored, p.max_q_len, num_sms, stream);
+        case 64: return launch_rows<64>(a, p.max_q_len, num_sms, stream);
+        case 128: return launch_rows<128>(a, p.max_q_len, num_sms, stream);
+        default: return launch_rows<256>(a, p.max_q_len, num_sms, stream);
     }
 }
 

@@ -47,7 +47,7 @@ struct Extra {
     int withhold;                // test hook: the CTA's first key tile is never requested
 };
 
-template <bool kScored>
+template <bool kChanged>
 __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_constant__ AttnArgs a,
                                                                  const __grid_constant__ CUtensorMap k_map, const Extra x) {
     extern __shared__ uint8_t smem_raw[];
@@ -284,16 +284,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
             if (r0 < j.columns) {
                 stage_query_parts(smem + kQ + r0 * kD, kRows * kD, a.q,
                                   (it.q0 + qi) * a.q_stride + static_cast<int64_t>(it.h * a.group + hg) * kD, j.nrows - r0,
-                                  [&](int row, float step) { row_scores[r0 + row].qs = fmaxf(step * a.scale_log2, 0x1p-126f); });
+                                  [&](int row, float step) { row_scores[r0 + row].qs = row_scale(step, a.scale_log2); });
                 __syncwarp();  // (the rows' scales were written by other lanes)
                 const float qs = row_scores[r0 + lane].qs;
-                RowScore info = row_score(a.scores, qs, it.q0, it.len, it.nq, a.group, it.h, r, a.index_error);
+                RowScore info = row_score(a.scores, it.q0, it.len, it.nq, a.group, it.h, r, a.index_error);
+                info.qs = qs;
                 float less = kNegInf;  // a row that is not one, or sees nothing, adds nothing
                 if (lse != kNegInf) less = lse * -1.4426950408889634f;
                 if (r0 + lane >= j.nrows) info.lo = info.limit = 0;
                 row_scores[r0 + lane] = info;
                 float* const pair = pairs + (r0 + lane) / 2 * 4 + (lane & 1);
-                pair[0] = info.qs;
+                pair[0] = qs;
                 pair[2] = less;
                 fence_async_proxy();
             }
@@ -329,10 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
 #pragma unroll
                     for (int w = 0; w < 16; ++w) {
                         y[w] = __fmul2_rn(make_float2(__uint_as_float(s[2 * w]), __uint_as_float(s[2 * w + 1])), k2);
-                        y[w] = kScored ? __fmul2_rn(y[w], make_float2(row[w].x, row[w].y))
+                        y[w] = kChanged ? __fmul2_rn(y[w], make_float2(row[w].x, row[w].y))
                                        : __ffma2_rn(y[w], make_float2(row[w].x, row[w].y), make_float2(row[w].z, row[w].w));
                     }
-                    if constexpr (kScored) {
+                    if constexpr (kChanged) {
                         if (a.scores.capped)
                             cap_scores<16>([&](int w) { return y[w]; }, [&](int w, const float2& z) { y[w] = z; });
                         if (a.scores.slopes) {
@@ -401,12 +402,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
     }
 }
 
-template <bool kScored>
+template <bool kChanged>
 cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
-    auto kernel = kv_mass_tc_kernel<kScored>;
+    auto kernel = kv_mass_tc_kernel<kChanged>;
     if (!configured[dev & 63].load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
         if (e != cudaSuccess) return e;
@@ -423,8 +424,8 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_mass_tc(const AttnArgs& a, bool scored, int num_sms, cudaStream_t stream) {
-    return scored ? launch<true>(a, num_sms, stream) : launch<false>(a, num_sms, stream);
+cudaError_t launch_mass_tc(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+    return a.scores.kind == ScoreKind::kChanged ? launch<true>(a, num_sms, stream) : launch<false>(a, num_sms, stream);
 }
 
 unsigned int read_and_clear_mass_timeout() {

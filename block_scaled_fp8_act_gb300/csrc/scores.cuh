@@ -1,6 +1,7 @@
 // Scores that are more than a scaled product, for the attention kernels and the
 // accumulated weights: a cap, a bias by distance, and which positions a row sees.
-// A score times Scores::unit is an exponent of 2: the unit is the cap, or 1.
+// A changed score times Scores::unit is an exponent of 2: the unit is the cap, or
+// 1. With masks alone (kMasked) the rows' scales stay factors of the exponent.
 #pragma once
 
 #include "decoder_util.cuh"
@@ -70,17 +71,20 @@ __device__ __forceinline__ int first_seen(const Scores& s, int q0, int len, int 
 }
 
 // Row `row` of a sequence's (rows past its last are as that one), of KV head h.
-__device__ __forceinline__ RowScore row_score(const Scores& s, float qs, int q0, int len, int nq, int group, int h, int row,
-                                              unsigned int* error) {
+// Its qs comes from the staging of the queries.
+__device__ __forceinline__ RowScore row_score(const Scores& s, int q0, int len, int nq, int group, int h, int row, unsigned int* error) {
     const int qi = min(row / group, nq - 1);
     RowScore r;
-    r.qs = fminf(qs, 3e38f);  // (a tiny cap of huge queries: still 0 times a product of 0)
+    r.qs = 0.0f;
     r.lo = first_seen(s, q0, len, nq, qi);
     r.limit = len - nq + qi + 1;
     r.slope = s.slopes ? ld_dep_f32(s.slopes + h * group + row % group) * (1.4426950408889634f / s.unit) : 0.0f;
     if (s.first && qi > 0 && ld_dep_s32(s.first + q0 + qi) < ld_dep_s32(s.first + q0 + qi - 1)) atomicOr(error, 1u);
     return r;
 }
+
+// A row's qs from its power of two; bounded, so that a tiny cap of huge queries is still 0 times a product of 0.
+__device__ __forceinline__ float row_scale(float step, float scale) { return fminf(fmaxf(step * scale, 0x1p-126f), 3e38f); }
 
 __device__ __forceinline__ int prefix_of(const Scores& s, int b, int len) {
     return s.prefix ? min(max(ld_dep_s32(s.prefix + b), 0), len) : 0;
