@@ -355,17 +355,18 @@ PyObject* kv_attention(PyObject* const* a) {
 }
 
 // (q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, lse, mass, accumulate, stream, soft_cap, window,
-//  prefix_lens, first, slopes)
+//  prefix_lens, first, slopes, old_lens)
 PyObject* kv_attention_mass(PyObject* const* a) {
     const Rows r = rows_of(a);
     const fp8act_scores s = scores_of(a + 11, r);
     const float* lse = data<float>(a[7], kF32, {r.T, r.Hq}, "lse");
     float* mass = data<float>(a[8], kF32, {r.c.num_pages, r.c.kv_heads, r.c.page_size}, "mass");
+    const int* old = optional<int>(a[16], kI32, {r.B}, "old_lens");
     const int accumulate = PyObject_IsTrue(a[9]);
     if (accumulate < 0) throw Raised{};
     check("fp8_kv_attention_mass",
           fp8_kv_attention_mass(r.q.data_ptr(), r.q_stride, r.cu, r.lens, r.table, r.pages, r.B, static_cast<int>(r.T), r.max_q,
-                                static_cast<int>(r.Hq), static_cast<float>(r.scale), &s, &r.c, lse, mass, accumulate,
+                                static_cast<int>(r.Hq), static_cast<float>(r.scale), &s, &r.c, lse, mass, accumulate, old,
                                 stream_of(a[10])));
     Py_RETURN_NONE;
 }
@@ -450,7 +451,7 @@ PyMethodDef g_methods[] = {
     {"kv_append", fast<kv_append, 5>(), METH_FASTCALL, nullptr},
     {"rope_append", fast<rope_append, 16>(), METH_FASTCALL, nullptr},
     {"kv_attention", fast<kv_attention, 16>(), METH_FASTCALL, nullptr},
-    {"kv_attention_mass", fast<kv_attention_mass, 16>(), METH_FASTCALL, nullptr},
+    {"kv_attention_mass", fast<kv_attention_mass, 17>(), METH_FASTCALL, nullptr},
     {"kv_evict", fast<kv_evict, 11>(), METH_FASTCALL, nullptr},
     {"verify_drafts", fast<verify_drafts, 12>(), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},

@@ -473,7 +473,7 @@ int fp8_kv_attention_scored(const void* q_bf16, int64_t q_stride, const int* cu_
 int fp8_kv_attention_mass(const void* q_bf16, int64_t q_stride, const int* cu_q, const int* kv_lens,
                           const int* page_table, int max_pages, int batch, int tokens, int max_q_len, int q_heads,
                           float softmax_scale, const fp8act_scores* scores, const fp8act_kv_cache* cache,
-                          const float* lse, float* mass, int accumulate, void* stream) {
+                          const float* lse, float* mass, int accumulate, const int* old_lens, void* stream) {
     fp8act::KvCache c;
     if (int st = check_cache(cache, &c)) return st;
     if (int st = check_rows(c, q_stride, max_pages, batch, tokens, max_q_len, q_heads, softmax_scale)) return st;
@@ -484,13 +484,13 @@ int fp8_kv_attention_mass(const void* q_bf16, int64_t q_stride, const int* cu_q,
     if (!cu_q || !kv_lens || !mass || (tokens > 0 && (!q_bf16 || !lse)) || (max_pages > 0 && !page_table))
         return FP8ACT_ERR_NULL;
     if (!aligned(q_bf16, 16) || q_stride % 8 || !aligned(cu_q, 4) || !aligned(kv_lens, 4) || !aligned(page_table, 4) ||
-        !aligned(lse, 4) || !aligned(mass, 16) || !aligned_scores(s))
+        !aligned(lse, 4) || !aligned(mass, 16) || !aligned(old_lens, 4) || !aligned_scores(s))
         return FP8ACT_ERR_ALIGN;
     int st = FP8ACT_OK;
     const int sms = current_device_sms(&st);
     if (st) return st;
     const fp8act::MassProblem p = {q_bf16, q_stride, cu_q, kv_lens, page_table, max_pages, batch, tokens, max_q_len,
-                                   q_heads / c.heads, softmax_scale, c, lse, mass, accumulate != 0, s};
+                                   q_heads / c.heads, softmax_scale, c, lse, mass, accumulate != 0, old_lens, s};
     return launch_status(fp8act::launch_kv_mass(p, sms, static_cast<cudaStream_t>(stream)));
 }
 

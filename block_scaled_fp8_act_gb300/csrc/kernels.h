@@ -193,6 +193,7 @@ struct MassProblem {
     const float* lse;
     float* mass;  // [num_pages, heads, page]
     bool accumulate;
+    const int* old_lens;  // [batch] or null
     Scores scores;
 };
 cudaError_t launch_kv_mass(const MassProblem& p, int num_sms, cudaStream_t stream);

@@ -40,6 +40,7 @@ struct AttnArgs {
     // the accumulated weights alone
     float* mass;       // [pages, heads, page]
     bool accumulate;
+    const int* old_lens;  // [batch] or null: all but the new tokens
 };
 
 // CTAs of the main kernel (two per SM at most) that the workspace is made for.
@@ -234,6 +235,9 @@ struct Item {
 // kScored: units are the tiles that the sequence's rows may see. kMass: an item has all the sequence's rows, and a token
 // tile counts as often as they have 64 (at most 16 times).
 enum class List { kPlain, kScored, kMass };
+__device__ __forceinline__ int old_end(const AttnArgs& a, int b, int len, int nq) {  // positions before it keep their weight
+    return !a.accumulate ? 0 : a.old_lens ? ld_dep_s32(a.old_lens + b) : len - nq;
+}
 __device__ __forceinline__ int mass_weight(int rows) { return min(max((rows + 63) / 64, 1), 16); }
 
 template <int kTok, int kCost, List kList>
@@ -255,7 +259,7 @@ struct Units {
         it.prefix = 0;
         if constexpr (kList == List::kMass) {
             it.prefix = prefix_of(a.scores, b, len);
-            it.rts = len > 0 && (it.nq > 0 || !a.accumulate) ? 1 : 0;
+            it.rts = len > 0 && (it.nq > 0 || !a.accumulate || a.old_lens) ? 1 : 0;
             it.tiles = (len + kTok - 1) / kTok * mass_weight(it.nq * a.group) + kCost;
         }
         if constexpr (kList == List::kScored) {

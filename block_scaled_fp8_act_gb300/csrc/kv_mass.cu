@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
         const int t0 = tile_of(u), t1 = tile_of(item_end < u_end ? item_end : u_end);
         const int* table = a.table + it.b * a.table_stride;
         const int in_page = (1 << a.c.page_log2) - 1;
-        const int old_end = it.len - it.nq;  // positions before it keep their weight if accumulating
+        const int kept_end = old_end(a, it.b, it.len, it.nq);
 
         int row0 = 0;
         do {
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
                     used = 0;
                     held = look_up(t + M::kWarps);
                 }
-                const bool adds = row0 > 0 || (a.accumulate && t * kTile + my_token < old_end);
+                const bool adds = row0 > 0 || t * kTile + my_token < kept_end;
                 have = adds && mine >= 0 ? ld_dep_f32(a.mass + mine) : 0.0f;
             };
             look_ahead(t0 + warp);
@@ -372,6 +372,7 @@ cudaError_t launch_kv_mass(const MassProblem& p, int num_sms, cudaStream_t strea
     a.scores = p.scores;
     a.mass = p.mass;
     a.accumulate = p.accumulate;
+    a.old_lens = p.old_lens;
     switch (p.cache.head_dim) {
         case 64: return launch_rows<64>(a, p.max_q_len, num_sms, stream);
         case 128: return launch_rows<128>(a, p.max_q_len, num_sms, stream);

@@ -253,12 +253,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
         while (ok) {
             const Job j = job_of();
             table = a.table + it.b * a.table_stride;
-            const int old_end = it.len - it.nq;  // positions before it keep their weight if accumulating
+            const int kept_end = old_end(a, it.b, it.len, it.nq);
             // The place of this thread's token of tile t, what it has so far and its key scale.
             auto fetch = [&](int t, int page, int64_t& place, float& have, float& ks) {
                 const int pos = t * kTok + mine;
                 place = is_page(pos, page) ? place_of(page, pos) : -1;
-                const bool adds = j.row0 > 0 || (a.accumulate && pos < old_end);
+                const bool adds = j.row0 > 0 || pos < kept_end;
                 have = adds && place >= 0 ? ld_dep_f32(a.mass + place) : 0.0f;
                 ks = place >= 0 ? ld_dep_f32(a.c.k_scale + place) : 0.0f;
             };
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
             // Tiles that no row sees get nothing.
             if (j.row0 == 0 && j.n < j.t1 - j.t0)
                 for (int t = j.t0 + acc; t < j.t1; t += 2) {
-                    if (j.seen(t) || (a.accumulate && (t + 1) * kTok <= old_end)) continue;
+                    if (j.seen(t) || (t + 1) * kTok <= kept_end) continue;
                     int64_t at;
                     float old, unused;
                     fetch(t, page_of(t * kTok + mine), at, old, unused);

@@ -88,7 +88,7 @@ def load(build: bool = False) -> ctypes.CDLL:
     L.fp8_rope_append.argtypes = [p, p, p, i64, i64, i64, p, p, f, f, p, p, p, i, i, i, f, p, i, i, p, p, p]
     L.fp8_kv_attention.argtypes = [p, i64, p, p, p, i, i, i, i, i, f, p, p, p, p, ctypes.c_size_t, p]
     L.fp8_kv_attention_scored.argtypes = [p, i64, p, p, p, i, i, i, i, i, f, p, p, p, p, p, ctypes.c_size_t, p]
-    L.fp8_kv_attention_mass.argtypes = [p, i64, p, p, p, i, i, i, i, i, f, p, p, p, p, i, p]
+    L.fp8_kv_attention_mass.argtypes = [p, i64, p, p, p, i, i, i, i, i, f, p, p, p, p, i, p, p]
     L.fp8_kv_attention_workspace.argtypes = [i, i, p]
     L.fp8_kv_attention_workspace.restype = ctypes.c_size_t
     L.fp8_kv_evict.argtypes = [p, p, p, i, p, p, p, i, i, i, i, p, p, p]
@@ -413,15 +413,16 @@ def fp8_kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len: int | None 
 
 def fp8_kv_attention_mass(q, cache, page_table, kv_lens, cu_q, lse, mass, max_q_len: int | None = None,
                           softmax_scale: float | None = None, accumulate: bool = True, stream=None,
-                          soft_cap: float = 0.0, window: int = 0, prefix_lens=None, first=None, slopes=None) -> None:
+                          soft_cap: float = 0.0, window: int = 0, prefix_lens=None, first=None, slopes=None,
+                          old_lens=None) -> None:
     """Adds to mass (fp32 [pages, kv_heads, page_size]) the attention weight that every cached token gets.
 
     The weights exp(score - lse) of the new tokens q, summed over them and over the query heads of a KV head;
-    lse (fp32 [tokens, q_heads]) is what fp8_kv_attention left with the same arguments. The new tokens' own
-    places start from zero, all of a sequence's places if not `accumulate`. A page that gets weight belongs
-    to one sequence of the call."""
+    lse (fp32 [tokens, q_heads]) is what fp8_kv_attention left with the same arguments. The places from
+    old_lens (int32 [B]; None: all but the new tokens) on start from zero, all of a sequence's if not
+    `accumulate`. A page that gets weight belongs to one sequence of the call."""
     _native().kv_attention_mass(q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, lse, mass, accumulate, stream,
-                                soft_cap, window, prefix_lens, first, slopes)
+                                soft_cap, window, prefix_lens, first, slopes, old_lens)
 
 
 def kv_mass(cache) -> torch.Tensor:

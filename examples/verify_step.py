@@ -10,12 +10,14 @@ and verifies the drafts:
     fp8_silu_mul_quant -> fp8_block_gemm (down)            per layer, then
     fp8_rmsnorm_quant -> fp8_block_gemm (vocabulary) -> verify_drafts
 
-Weights are random and there is no positional encoding: the example shows the
-calls, their buffers and a CUDA graph around them.
+Weights are random: the example shows the calls, their buffers and a CUDA graph
+around them. There is no positional encoding unless --rope-theta is given, which
+has fp8_rope_append (head norms, rotary positions, append) take the place of
+fp8_kv_append; --window and --soft-cap are the attention's.
 
     python examples/verify_step.py                      # small, on cuda:0
     python examples/verify_step.py --hidden 5120 --mlp 8704 --heads 24 --kv-heads 4 \
-        --layers 4 --vocab 151936 --batch 34 --drafts 2 --context 4096
+        --layers 4 --vocab 151936 --batch 34 --drafts 2 --context 4096 --rope-theta 1e6
 """
 from __future__ import annotations
 
@@ -44,6 +46,9 @@ class Config:
     context: int = 100
     page: int = 16
     seed: int = 0
+    rope_theta: float = 0.0
+    window: int = 0
+    soft_cap: float = 0.0
 
 
 class Decoder:
@@ -81,6 +86,13 @@ class Decoder:
         for cache in self.caches:  # what earlier steps cached
             kv = torch.randn((2, c.batch * c.context, c.kv_heads, c.head_dim), device="cuda", generator=g).bfloat16()
             fp8act.fp8_kv_append(kv[0], kv[1], slots[:, :c.context].reshape(-1).contiguous(), cache)
+        if c.rope_theta:
+            i = torch.arange(c.head_dim // 2, device="cuda", dtype=torch.float64)
+            self.inv_freq = c.rope_theta ** (-2.0 * i / c.head_dim)
+            self.positions = (c.context + torch.arange(n, device="cuda")).repeat(c.batch)
+            for w in self.layers:
+                w["q_norm"], w["k_norm"] = ((1.0 + 0.1 * torch.randn(c.head_dim, device="cuda", generator=g)).bfloat16()
+                                            for _ in range(2))
         self.workspace = torch.empty(fp8act.kv_attention_workspace(n, c.heads, self.caches[0]), dtype=torch.uint8,
                                      device="cuda")
 
@@ -97,9 +109,13 @@ class Decoder:
             qkv = fp8act.fp8_block_gemm(q, sa, *w["qkv"])
             heads = qkv[:, :width].unflatten(1, (c.heads, c.head_dim))
             k, v = (t.unflatten(1, (c.kv_heads, c.head_dim)) for t in qkv[:, width:].split(self.kv_width, 1))
-            fp8act.fp8_kv_append(k, v, self.slots, cache)
+            if c.rope_theta:
+                heads = fp8act.fp8_rope_append(heads, k, v, self.positions, self.inv_freq, self.slots, cache,
+                                               q_weight=w["q_norm"], k_weight=w["k_norm"])
+            else:
+                fp8act.fp8_kv_append(k, v, self.slots, cache)
             o = fp8act.fp8_kv_attention(heads, cache, self.table, self.kv_lens, self.cu_q, max_q_len=n,
-                                        workspace=self.workspace)
+                                        workspace=self.workspace, window=c.window, soft_cap=c.soft_cap)
             x = fp8act.fp8_block_gemm(*fp8act.fp8_act_quant(o.view(-1, width)), *w["out"])
             q, sa, residual = fp8act.fp8_rmsnorm_quant(x, w["norm2"], residual=residual)
             q, sa = fp8act.fp8_silu_mul_quant(fp8act.fp8_block_gemm(q, sa, *w["gate_up"]))
@@ -128,7 +144,7 @@ def inputs(c: Config, seed: int):
 def main() -> None:
     p = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     for f in Config.__dataclass_fields__.values():
-        p.add_argument("--" + f.name.replace("_", "-"), type=int, default=f.default)
+        p.add_argument("--" + f.name.replace("_", "-"), type=type(f.default), default=f.default)
     p.add_argument("--steps", type=int, default=20)
     a = vars(p.parse_args())
     steps = a.pop("steps")

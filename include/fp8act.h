@@ -425,8 +425,10 @@ FP8ACT_API int fp8_kv_attention_scored(const void* q_bf16, int64_t q_stride, con
  * sequence's kv_lens[b]).
  *   mass        [num_pages, kv_heads, page_size] fp32
  *   accumulate  0: the weights of positions 0 .. kv_lens[b] - 1 are replaced;
- *               else they are added to, but that those of the new tokens' own
- *               positions start from zero (a place may hold a former token's)
+ *               else they are added to, but that those from old_lens[b] on start
+ *               from zero (a place may hold a former token's weight)
+ *   old_lens    [batch] int32, the tokens that have weights; NULL: all but the new
+ *               ones. Needed where only the last of a chunk's tokens are passed
  * Sums are fp32 in a fixed order. A row whose lse is -infinity adds nothing; a NaN
  * scale of a cached token makes that token's weight NaN. Places past kv_lens[b] are
  * left as they are. A page that gets weight belongs to one sequence of the call.
@@ -435,7 +437,7 @@ FP8ACT_API int fp8_kv_attention_mass(const void* q_bf16, int64_t q_stride, const
                                      const int* page_table, int max_pages, int batch, int tokens, int max_q_len,
                                      int q_heads, float softmax_scale, const fp8act_scores* scores,
                                      const fp8act_kv_cache* cache, const float* lse, float* mass, int accumulate,
-                                     void* stream);
+                                     const int* old_lens, void* stream);
 
 /* Bytes of workspace for fp8_kv_attention; 0 for arguments it would refuse. */
 FP8ACT_API size_t fp8_kv_attention_workspace(int max_q_len, int q_heads, const fp8act_kv_cache* cache);

@@ -70,11 +70,11 @@ def test_structs_match_the_header():
 
 
 def scored(lib, mass, q=A16, qs=1024, cu=A16, lens=A16, table=A16, mp=4, B=1, T=1, mq=1, hq=8, scale=0.1, out=A16, lse=A16, ws=A16,  # noqa: F811
-           cap=0.0, window=0, prefix=None, first=None, slopes=None, scores=True, **kw):
+           old=None, cap=0.0, window=0, prefix=None, first=None, slopes=None, scores=True, **kw):
     s = ctypes.byref(fp8act.ScoresStruct(cap, window, prefix, first, slopes)) if scores else None
     c = ctypes.byref(cache(**kw))
     if mass:
-        return lib.fp8_kv_attention_mass(q, qs, cu, lens, table, mp, B, T, mq, hq, scale, s, c, lse, out, 1, None)
+        return lib.fp8_kv_attention_mass(q, qs, cu, lens, table, mp, B, T, mq, hq, scale, s, c, lse, out, 1, old, None)
     return lib.fp8_kv_attention_scored(q, qs, cu, lens, table, mp, B, T, mq, hq, scale, s, c, out, lse, ws, 1 << 40, None)
 
 
@@ -89,7 +89,7 @@ def test_score_argument_checks(lib, mass):  # noqa: F811
     for name in ("q", "cu", "lens", "table", "out") + (("lse",) if mass else ("ws",)):
         assert scored(lib, mass, **{name: None}) == NULL, name
     for bad in (dict(prefix=A16 + 2), dict(first=A16 + 1), dict(slopes=A16 + 2), dict(q=A16 + 8), dict(qs=1028), dict(lse=A16 + 2),
-                dict(out=A16 + 4), dict(lens=A16 + 2)):
+                dict(out=A16 + 4), dict(lens=A16 + 2)) + ((dict(old=A16 + 2),) if mass else ()):
         assert scored(lib, mass, **bad) == ALIGN, bad
     if not torch.cuda.is_available():
         for ok in (dict(), dict(cap=30.0, window=5, prefix=A16, first=A16, slopes=A16), dict(scores=False)):

@@ -377,3 +377,27 @@ def test_mass_wait_that_runs_out(fp8act):  # noqa: F811
     finally:
         fp8act.set_wait_limit(-1, False)
     check(fp8act, q, cache, table, lens, ns)
+
+
+@pytest.mark.parametrize("n", [2, 30])
+def test_mass_of_the_last_tokens_of_a_chunk(fp8act, n):  # noqa: F811
+    """With old_lens, places that hold a token's first weight start from zero whether the token is passed or not."""
+    lens, ns, old = [700, 300, 40, 90], [n, n, 0, n], [600, 0, 25, 200]
+    cache, table = make_cache(fp8act, lens, 2, 128, 16, seed=81)
+    q = randn(sum(ns), 12, 128, seed=82)
+    lse = torch.empty(q.shape[:2], device="cuda")
+    attend(fp8act, q, cache, table, lens, ns, lse=lse)
+    args = (q, cache, table, i32(lens), i32(np.concatenate([[0], np.cumsum(ns)])), lse)
+    before = torch.rand(cache.k_scale.shape, device="cuda", generator=gen(3))
+    alone = torch.zeros_like(before)
+    fp8act.fp8_kv_attention_mass(*args, alone, max_q_len=n, accumulate=False)
+    mass = before.clone()
+    for b, (L, o) in enumerate(zip(lens, old)):
+        at = torch.arange(min(o, L), L, device="cuda")
+        mass[table[b, at // 16].long(), :, at % 16] = math.nan
+    fp8act.fp8_kv_attention_mass(*args, mass, max_q_len=n, old_lens=i32(old))
+    for b, (L, o) in enumerate(zip(lens, old)):
+        at = torch.arange(L, device="cuda")
+        p, s = table[b, at // 16].long(), at % 16
+        want = torch.where((at < o).unsqueeze(1), before[p, :, s], 0.0) + alone[p, :, s]
+        assert torch.equal(mass[p, :, s], want)
