@@ -400,4 +400,6 @@ def test_mass_of_the_last_tokens_of_a_chunk(fp8act, n):  # noqa: F811
         at = torch.arange(L, device="cuda")
         p, s = table[b, at // 16].long(), at % 16
         want = torch.where((at < o).unsqueeze(1), before[p, :, s], 0.0) + alone[p, :, s]
-        assert torch.equal(mass[p, :, s], want)
+        # (with more rows than one pass takes the old weight is added to the first pass's sum and the second's to that: each of
+        # the two sides rounds at most twice, 2^-24 of a sum that only grows)
+        assert ((mass[p, :, s].double() - want.double()).abs() <= 2.0 ** -22 * want).all()
