@@ -53,9 +53,11 @@ __device__ unsigned int g_attn_index_error;
 
 constexpr int kTile = 32;  // cached tokens per unit
 constexpr int kLeastUnits = 8;  // least share of a CTA
-constexpr int kItemCost = 20;   // units that an item counts beside its own
+// Units that an item counts beside its own. Masks make an item's start longer (34 ragged sequences x 3 tokens in a window
+// that holds them: 20 units 45.0 us, 26 40.9, 32 40.2; in one of 512 tokens 23.1, 24.1, 26.7).
+constexpr int item_cost(ScoreKind kind) { return kind == ScoreKind::kPlain ? 20 : 28; }
 template <ScoreKind kKind>
-using WorkOf = Units<kTile, kItemCost, kKind == ScoreKind::kPlain ? List::kPlain : List::kScored>;
+using WorkOf = Units<kTile, item_cost(kKind), kKind == ScoreKind::kPlain ? List::kPlain : List::kScored>;
 
 // Transpose of an 8 x 8 matrix of 16-bit values held as an MMA fragment.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
@@ -106,6 +108,7 @@ __global__ void __launch_bounds__(Attn<kD, kWR, kRW, kG, kCtas, kKind>::kThreads
     kv_attention_kernel(const __grid_constant__ AttnArgs a) {
     using S = Attn<kD, kWR, kRW, kG, kCtas, kKind>;
     using Work = WorkOf<kKind>;
+    constexpr int kItemCost = item_cost(kKind);
     constexpr bool kScored = S::kScored, kChanged = kKind == ScoreKind::kChanged;
     constexpr int kRows = S::kRows, kStages = S::kStages;
     constexpr int kKS = kD / 32;  // pairs of k-steps of the score product
