@@ -11,9 +11,8 @@
 // Angles. A turn is 2^64 units: inv_freq / 2 pi becomes a whole number of
 // units, and its product with the position wraps to the angle's remainder
 // exactly, with no table and no bound on the position. What is lost is the
-// frequency's rounding to a unit, or 2^-62 of itself where that is more. The
-// remainder, in [-1/2, 1/2) of a turn, is cut to 32 bits and rounded to fp32:
-// 2^-25 of itself and 2^-32 of a turn.
+// frequency's rounding to a unit, or 2^-62 of itself where that is more, and what
+// is cut off the remainder, in [-1/2, 1/2) of a turn, behind 32 bits.
 //
 // Work split. A lane holds two chunks of 8 columns of a vector, those whose
 // columns turn together, so that a turn needs no other lane; D / 16 lanes hold
@@ -151,10 +150,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
         for (int j = 0; j < kPairs; ++j) {
             if (token[j] >= kTok) continue;
             const uint32_t u = static_cast<uint32_t>(static_cast<uint64_t>(pos[j]) * units[j] >> 32);
-            const float at = __int2float_rn(static_cast<int>(u)) * 0x1p-31f;  // half turns
+            // The upper 24 bits, in half turns, are an fp32 number; the lower 8 turn a little further.
+            const float at = __int2float_rn(static_cast<int>(u & ~0xFFu)) * 0x1p-31f;
+            const float more = __uint2float_rn(u & 0xFFu) * 1.4629180792671596e-9f;  // pi 2^-31
             float sn, cs;
             sincospif(at, &sn, &cs);
-            turns[buffer][token[j]][pair[j]] = make_float2(cs * p.rope_scale, sn * p.rope_scale);
+            turns[buffer][token[j]][pair[j]] = make_float2(fmaf(-more, sn, cs) * p.rope_scale, fmaf(more, cs, sn) * p.rope_scale);
         }
     };
     int64_t pos[kPairs];
@@ -249,8 +250,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
             }
 #pragma unroll
             for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float scale = quant_head(f.a, f.b, top);
-            if (!mine || slot < 0) continue;
+            const bool there = mine && slot >= 0;
+            // (a lane with nothing to store must not take its warp through the divisions that all-zero vectors get)
+            const float scale = quant_head(f.a, f.b, there ? top : __float_as_uint(1.0f));
+            if (!there) continue;
             const int64_t at = (((slot >> c.page_log2) * c.heads + h) << c.page_log2) + (slot & ((1 << c.page_log2) - 1));
             uint2* const to = reinterpret_cast<uint2*>(codes + at * kD);
             to[chunk_a] = pack_e4m3x8(f.a);
@@ -271,7 +274,7 @@ cudaError_t launch(const RopeProblem& p, int num_sms, cudaStream_t stream) {
     const int groups = (steps + kWarps - 1) / kWarps, warps = (steps + groups - 1) / groups;
     if (groups > 65535) return cudaErrorInvalidConfiguration;
     // Two tokens at a time once there are enough to keep every CTA busy with more than one such pair.
-    const int resident = (num_sms * kCtas + groups - 1) / groups;
+    const int resident = (num_sms * (kCtas * kWarps / warps) + groups - 1) / groups;
     const bool many = p.tokens > 2 * resident;
     const int tiles = many ? (p.tokens + 1) / 2 : p.tokens;
     auto kernel = many ? (p.interleaved ? rope_append_kernel<kLanes, true, 2> : rope_append_kernel<kLanes, false, 2>)
