@@ -16,7 +16,8 @@
 //
 // Work split. A lane holds two chunks of 8 columns of a vector, those whose
 // columns turn together, so that a turn needs no other lane; D / 16 lanes hold
-// the vector, and a warp has 512 / D heads of one kind. It keeps them: a CTA's
+// the vector, and a warp has 512 / D heads of one kind (with fewer heads than that
+// in all, those of several tokens). It keeps them: a CTA's
 // warps go through tokens, each with its heads, their weights in registers and the
 // loads of the next two tokens in flight, and the CTA finds the next tokens' sines
 // and cosines, a pair a thread, while it works on the present ones. More heads
@@ -31,7 +32,6 @@ namespace {
 
 __device__ unsigned int g_rope_index_error;
 
-constexpr int kMaxHalf = 128;  // pairs of a head
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCtas = 2;       // per SM
 
@@ -65,21 +65,22 @@ __device__ __forceinline__ float largest(float most, const float2& f) {
 }
 
 // kLanes = D / 16 lanes hold a vector.
-template <int kLanes, bool kInterleaved, int kTok>
+template <int kLanes, bool kInterleaved, int kIt, int kTps>
 __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __grid_constant__ RopeProblem p) {
-    constexpr int kPer = 32 / kLanes;  // vectors of a step
     constexpr int kD = 16 * kLanes;
-    constexpr int kPairs = (kD / 2 * kTok + 95) / 96;  // pairs of a thread, at most (a CTA has at least 3 warps)
-    __shared__ __align__(16) float2 turns[2][kTok][kMaxHalf];  // (cos, sin) * rope_scale
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hl = lane % kLanes;
+    constexpr int kHps = 32 / kLanes / kTps;                // heads of a step, of each of kTps tokens
+    constexpr int kTile = kIt * kTps;                       // tokens of a tile
+    constexpr int kPairs = (kD / 2 * kTile + 95) / 96;      // pairs of a thread, at most (a CTA has at least 3 warps)
+    __shared__ __align__(16) float2 turns[2][kTile][kD / 2];  // (cos, sin) * rope_scale
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hl = lane % kLanes, sub = lane / kLanes / kHps;
     const KvCache& c = p.cache;
-    const int half = p.rot / 2, tiles = (p.tokens + kTok - 1) / kTok;
+    const int half = p.rot / 2, tiles = (p.tokens + kTile - 1) / kTile;
     // This warp's heads: steps of queries, then of keys, then of values.
-    const int steps_q = (p.q_heads + kPer - 1) / kPer, steps_k = (c.heads + kPer - 1) / kPer;
+    const int steps_q = (p.q_heads + kHps - 1) / kHps, steps_k = (c.heads + kHps - 1) / kHps;
     const int s = blockIdx.y * (blockDim.x >> 5) + warp;
     const Kind kind = s < steps_q ? kQuery : s < steps_q + steps_k ? kKey : kValue;
     const int heads = kind == kQuery ? p.q_heads : c.heads;
-    const int h = (s - (kind == kQuery ? 0 : kind == kKey ? steps_q : steps_q + steps_k)) * kPer + lane / kLanes;
+    const int h = (s - (kind == kQuery ? 0 : kind == kKey ? steps_q : steps_q + steps_k)) * kHps + lane / kLanes % kHps;
     const bool mine = h < heads;  // (past the values' heads: an idle warp)
     const bool normed = kind == kQuery ? p.q_weight != nullptr : kind == kKey && p.k_weight != nullptr;
     // The lane's chunks: columns i and i + R / 2 turn together (or, interleaved, neighbours); what does not turn is shared
@@ -93,8 +94,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
     const int64_t stride = kind == kQuery ? p.q_stride : kind == kKey ? p.k_stride : p.v_stride;
     const uint16_t* row = (kind == kQuery ? p.q : kind == kKey ? p.k : p.v) + (mine ? h : 0) * kD + chunk_a * 8;
     const int apart = (chunk_b - chunk_a) * 8;
-    // Token i of this CTA's, kTok of every gridDim.x tiles.
-    auto token_at = [&](int i) { return (static_cast<int64_t>(i / kTok) * gridDim.x + blockIdx.x) * kTok + i % kTok; };
+    // This lane's token of the CTA's i-th round, kIt rounds of every gridDim.x tiles.
+    auto token_at = [&](int i) { return (static_cast<int64_t>(i / kIt) * gridDim.x + blockIdx.x) * kTile + i % kIt * kTps + sub; };
     auto load = [&](int i, uint4 (&x)[2]) {
         const int64_t t = token_at(i);
         x[0] = x[1] = make_uint4(0, 0, 0, 0);
@@ -103,9 +104,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
             x[1] = ld_dep_stream_v4(row + t * stride + apart);
         }
     };
-    uint4 x[kTok][2];
+    uint4 x[kIt][2];
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) load(i, x[i]);
+    for (int i = 0; i < kIt; ++i) load(i, x[i]);
     Half w;
     {
         const uint16_t* from = kind == kQuery ? p.q_weight : p.k_weight;
@@ -127,11 +128,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) {
         const int at = threadIdx.x + j * blockDim.x;
-        token[j] = half > 0 ? min(at / half, kTok) : kTok;
+        token[j] = half > 0 ? min(at / half, kTile) : kTile;
         pair[j] = at - token[j] * half;
         units[j] = 0;
         position[j] = p.positions;
-        if (token[j] < kTok) {
+        if (token[j] < kTile) {
             units[j] = units_of(*const_cast<const volatile uint64_t*>(reinterpret_cast<const uint64_t*>(p.inv_freq) + pair[j]));
             int axis = p.axis ? ld_dep_s32(p.axis + pair[j]) : 0;
             if (axis < 0 || axis >= p.n_axes) {
@@ -142,13 +143,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
         }
     }
     auto position_of = [&](int tile, int j) -> int64_t {
-        const int64_t t = static_cast<int64_t>(tile) * kTok + token[j];
-        return token[j] < kTok && tile < tiles && t < p.tokens ? *const_cast<const volatile int64_t*>(position[j] + t) : 0;
+        const int64_t t = static_cast<int64_t>(tile) * kTile + token[j];
+        return token[j] < kTile && tile < tiles && t < p.tokens ? *const_cast<const volatile int64_t*>(position[j] + t) : 0;
     };
     auto turn_by = [&](const int64_t (&pos)[kPairs], int buffer) {
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-            if (token[j] >= kTok) continue;
+            if (token[j] >= kTile) continue;
             const uint32_t u = static_cast<uint32_t>(static_cast<uint64_t>(pos[j]) * units[j] >> 32);
             // The upper 24 bits, in half turns, are an fp32 number; the lower 8 turn a little further.
             const float at = __int2float_rn(static_cast<int>(u & ~0xFFu)) * 0x1p-31f;
@@ -214,20 +215,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
     uint8_t* const codes = kind == kKey ? c.k : c.v;
     float* const scales = kind == kKey ? c.k_scale : c.v_scale;
     int buffer = 0;
-    for (int tile = blockIdx.x, i0 = 0; tile < tiles; tile += gridDim.x, i0 += kTok) {
+    for (int tile = blockIdx.x, i0 = 0; tile < tiles; tile += gridDim.x, i0 += kIt) {
         int64_t pos_next[kPairs];
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) pos_next[j] = position_of(tile + gridDim.x, j);
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            const int64_t t = static_cast<int64_t>(tile) * kTok + i;
+        for (int i = 0; i < kIt; ++i) {
+            const int64_t t = static_cast<int64_t>(tile) * kTile + i * kTps + sub;
             int64_t slot = -1;
             if (kind != kQuery && t < p.tokens) slot = *const_cast<const volatile int64_t*>(p.slots + t);
             Half f;
             unpack(x[i], f);
             uint32_t top = max(top_bits(x[i][0]), top_bits(x[i][1])) << 16;
-            load(i0 + kTok + i, x[i]);
-            if (kind != kValue) turned(f, turns[buffer][i]);
+            load(i0 + kIt + i, x[i]);
+            if (kind != kValue) turned(f, turns[buffer][i * kTps + sub]);
             if (kind == kQuery) {
                 if (mine && t < p.tokens) {
                     *reinterpret_cast<uint4*>(out + t * out_stride) = pack_bf16x8(f.a);
@@ -267,28 +268,42 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
     }
 }
 
-template <int kLanes>
+template <int kLanes, int kIt, int kTps>
 cudaError_t launch(const RopeProblem& p, int num_sms, cudaStream_t stream) {
-    constexpr int kPer = 32 / kLanes;
-    const int steps = (p.q_heads + kPer - 1) / kPer + 2 * ((p.cache.heads + kPer - 1) / kPer);
-    const int groups = (steps + kWarps - 1) / kWarps, warps = (steps + groups - 1) / groups;
+    constexpr int kHps = 32 / kLanes / kTps, kTile = kIt * kTps;
+    const int64_t steps = (static_cast<int64_t>(p.q_heads) + kHps - 1) / kHps + 2 * ((static_cast<int64_t>(p.cache.heads) + kHps - 1) / kHps);
+    const int64_t groups = (steps + kWarps - 1) / kWarps, warps = (steps + groups - 1) / groups;
     if (groups > 65535) return cudaErrorInvalidConfiguration;
-    // Two tokens at a time once there are enough to keep every CTA busy with more than one such pair.
-    const int resident = (num_sms * (kCtas * kWarps / warps) + groups - 1) / groups;
-    const bool many = p.tokens > 2 * resident;
-    const int tiles = many ? (p.tokens + 1) / 2 : p.tokens;
-    auto kernel = many ? (p.interleaved ? rope_append_kernel<kLanes, true, 2> : rope_append_kernel<kLanes, false, 2>)
-                       : (p.interleaved ? rope_append_kernel<kLanes, true, 1> : rope_append_kernel<kLanes, false, 1>);
-    return launch_dependent(kernel, dim3(tiles < resident ? tiles : resident, groups), warps * 32, 0, stream, 1, p);
+    const int64_t tiles = (static_cast<int64_t>(p.tokens) + kTile - 1) / kTile;
+    const int64_t resident = (num_sms * (kCtas * kWarps / warps) + groups - 1) / groups;
+    auto kernel = p.interleaved ? rope_append_kernel<kLanes, true, kIt, kTps> : rope_append_kernel<kLanes, false, kIt, kTps>;
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(tiles < resident ? tiles : resident), static_cast<unsigned>(groups)),
+                            static_cast<int>(warps) * 32, 0, stream, 1, p);
+}
+
+// Many tokens: two at a time, or, where a warp has room for more heads than there are, that many. (3 heads on 1 of 128,
+// 20000 tokens: 29.2 us with one token a round.) With no more than a few for every CTA, one.
+template <int kLanes>
+cudaError_t launch_tokens(const RopeProblem& p, int num_sms, cudaStream_t stream) {
+    constexpr int kPer = 32 / kLanes;
+    const int heads = p.q_heads > p.cache.heads ? p.q_heads : p.cache.heads;
+    const int64_t steps = (static_cast<int64_t>(p.q_heads) + kPer - 1) / kPer + 2 * ((static_cast<int64_t>(p.cache.heads) + kPer - 1) / kPer);
+    if (p.tokens * steps <= 2 * static_cast<int64_t>(num_sms) * kCtas * kWarps) return launch<kLanes, 1, 1>(p, num_sms, stream);
+    if constexpr (kPer >= 8)
+        if (heads <= kPer / 8) return launch<kLanes, 1, 8>(p, num_sms, stream);
+    if constexpr (kPer >= 4)
+        if (heads <= kPer / 4) return launch<kLanes, 1, 4>(p, num_sms, stream);
+    if (heads <= kPer / 2) return launch<kLanes, 1, 2>(p, num_sms, stream);
+    return launch<kLanes, 2, 1>(p, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeProblem& p, int num_sms, cudaStream_t stream) {
     switch (p.cache.head_dim) {
-        case 64: return launch<4>(p, num_sms, stream);
-        case 128: return launch<8>(p, num_sms, stream);
-        default: return launch<16>(p, num_sms, stream);
+        case 64: return launch_tokens<4>(p, num_sms, stream);
+        case 128: return launch_tokens<8>(p, num_sms, stream);
+        default: return launch_tokens<16>(p, num_sms, stream);
     }
 }
 

@@ -74,7 +74,11 @@ def filled(fp8act, pages, H, page, D):  # noqa: F811
     (1, 24, 4, 128, 128, 1, True, False, 64), (1, 1, 1, 64, 64, 1, True, False, 16), (3, 5, 1, 256, 256, 2, True, True, 32),
     (37, 6, 3, 64, 48, 3, False, False, 16), (37, 6, 3, 64, 16, 1, True, True, 128), (102, 24, 4, 128, 64, 3, True, False, 16),
     (9, 7, 7, 256, 240, 4, False, False, 256), (5, 40, 8, 128, 112, 2, True, True, 64), (700, 12, 2, 128, 128, 3, True, False, 64),
-    (650, 3, 1, 64, 64, 1, True, True, 32), (4, 130, 2, 256, 32, 1, True, False, 16), (2, 3, 2, 128, 0, 1, True, False, 16)])
+    (650, 3, 1, 64, 64, 1, True, True, 32), (4, 130, 2, 256, 32, 1, True, False, 16), (2, 3, 2, 128, 0, 1, True, False, 16),
+    # many tokens: two a round, or as many as a warp has room for
+    (4097, 24, 4, 128, 128, 3, True, False, 64), (6001, 1, 1, 64, 64, 1, True, False, 16), (6003, 2, 1, 64, 32, 2, True, True, 32),
+    (5001, 3, 1, 64, 48, 1, False, False, 16), (4003, 1, 1, 128, 128, 2, True, True, 64), (4999, 2, 2, 128, 64, 1, True, False, 16),
+    (3001, 1, 1, 256, 256, 3, True, False, 16), (2999, 2, 2, 256, 128, 1, True, True, 256), (1501, 40, 8, 64, 64, 4, True, False, 16)])
 def test_rope_append(fp8act, T, Hq, H, D, rot, axes, norm, interleaved, page):  # noqa: F811
     q, k, v, qw, kw, inv, pos, axis = problem(T, Hq, H, D, rot, axes, norm, seed=T + D)
     pages = T // page + 2
