@@ -79,6 +79,12 @@ int to_int(int64_t v, const char* name) {
     return static_cast<int>(v);
 }
 
+// The library launches on the current device.
+void on_current_device(const at::Tensor& t, const char* name) {
+    if (t.is_cuda() && t.get_device() != c10::cuda::current_device())
+        raise(PyExc_ValueError, std::string(name) + " is not on the current CUDA device");
+}
+
 cudaStream_t stream_of(PyObject* o) {
     if (!given(o)) return c10::cuda::getCurrentCUDAStream().stream();
     PyObject* id = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
@@ -267,6 +273,7 @@ PyObject* rope_append(PyObject* const* a) {
                      &freq = tensor(a[4], "inv_freq");
     const int64_t D = c.head_dim, qs = heads_of(q, -1, D, "q"), ks = heads_of(k, c.kv_heads, D, "k"),
                   vs = heads_of(v, c.kv_heads, D, "v"), T = q.size(0), Hq = q.size(1);
+    on_current_device(q, "q");
     if (k.size(0) != T || v.size(0) != T) raise(PyExc_ValueError, "q, k and v have different numbers of tokens");
     if (pos.dim() != 1 && pos.dim() != 2) raise(PyExc_ValueError, "positions must be [T] or [axes, T]");
     const int64_t axes = pos.dim() == 2 ? pos.size(0) : 1;
@@ -311,6 +318,7 @@ Rows rows_of(PyObject* const* a) {
     const fp8act_kv_cache c = cache_of(a[1]);
     const at::Tensor &q = tensor(a[0], "q"), &table = tensor(a[2], "page_table");
     const int64_t qs = heads_of(q, -1, c.head_dim, "q"), T = q.size(0);
+    on_current_device(q, "q");
     if (table.dim() != 2) raise(PyExc_ValueError, "page_table must be 2-D [B, max_pages]");
     const int64_t B = table.size(0), pages = table.size(1);
     const int* tp = data<int>(table, kI32, {B, pages}, "page_table");
@@ -376,6 +384,7 @@ PyObject* kv_evict(PyObject* const* a) {
     const fp8act_kv_cache c = cache_of(a[0]);
     const at::Tensor &table = tensor(a[2], "page_table"), &next = tensor(a[5], "new_table");
     float* mass = data<float>(a[1], kF32, {c.num_pages, c.kv_heads, c.page_size}, "mass");
+    on_current_device(table, "page_table");
     if (table.dim() != 2 || next.dim() != 2) raise(PyExc_ValueError, "page_table and new_table must be 2-D [B, pages]");
     const int64_t B = table.size(0), pages = table.size(1), fresh_pages = next.size(1);
     const int* tp = data<int>(table, kI32, {B, pages}, "page_table");

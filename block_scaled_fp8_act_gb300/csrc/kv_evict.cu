@@ -95,7 +95,7 @@ __device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t (&warps)[33], uint
     return warps[warp] + incl - v;
 }
 
-__global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_constant__ EvictProblem p, int ctas, int held) {
+__global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_constant__ EvictProblem p, int ctas, uint32_t held) {
     extern __shared__ __align__(16) uint32_t keys[];
     __shared__ __align__(8) uint32_t hist[3][kBins];  // this CTA's counts of a round
     __shared__ __align__(8) uint32_t all[3][kBins];   // the cluster's (only there with more CTAs than one)
@@ -124,10 +124,11 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
     const int64_t run = ((static_cast<int64_t>(g.len) + ctas - 1) / ctas + 3) & ~int64_t{3};
     const int64_t begin64 = rank * run;
     const int begin = static_cast<int>(begin64 < g.len ? begin64 : g.len);
-    const int n = static_cast<int>(begin64 + run < g.len ? run : g.len - begin);
+    // (unsigned, so that a step past the longest run does not wrap)
+    const uint32_t n = static_cast<uint32_t>(begin64 + run < g.len ? run : g.len - begin);
     const int* table = p.page_table + static_cast<int64_t>(b) * p.table_stride;
-    auto read = [&](int i) -> uint4 {  // the numbers of tokens begin + i .. + 3; 0, below every weight's, past the last
-        const int pos = begin + i, page = ld_dep_s32(table + (pos >> p.cache.page_log2));
+    auto read = [&](uint32_t i) -> uint4 {  // the numbers of tokens begin + i .. + 3; 0, below every weight's, past the last
+        const int pos = begin + static_cast<int>(i), page = ld_dep_s32(table + (pos >> p.cache.page_log2));
         uint4 w = make_uint4(0x7FFFFFFFu, 0x7FFFFFFFu, 0x7FFFFFFFu, 0x7FFFFFFFu);
         if (page >= 0 && page < p.cache.num_pages)
             w = ld_dep_v4(p.mass + ((static_cast<int64_t>(page) * p.cache.heads + h) << p.cache.page_log2) +
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
         }
         return make_uint4(u[0], u[1], u[2], u[3]);
     };
-    auto again = [&](int i) { return i < held ? *reinterpret_cast<const uint4*>(keys + i) : read(i); };
+    auto again = [&](uint32_t i) { return i < held ? *reinterpret_cast<const uint4*>(keys + i) : read(i); };
     auto each = [&](const uint4& k, auto f) {
         f(k.x);
         f(k.y);
@@ -166,13 +167,13 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
         uint32_t* const count = hist[pass];
         if (pass == 0) {
 #pragma unroll 4
-            for (int i = threadIdx.x * 4; i < n; i += kThreads * 4) {
+            for (uint32_t i = threadIdx.x * 4; i < n; i += kThreads * 4) {
                 const uint4 k = read(i);
                 if (i < held) *reinterpret_cast<uint4*>(keys + i) = k;
                 each(k, [&](uint32_t u) { atomicAdd(count + (u >> 21), 1u); });
             }
         } else {
-            for (int i = threadIdx.x * 4; i < n; i += kThreads * 4)
+            for (uint32_t i = threadIdx.x * 4; i < n; i += kThreads * 4)
                 each(again(i), [&](uint32_t u) {
                     if (u >> top == prefix) atomicAdd(count + (u >> shift & mask), 1u);
                 });
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
     uint32_t base_above = 0, base_equal = 0;
     if (ctas > 1) {
         uint32_t above = 0, equal = 0;
-        for (int i = threadIdx.x * 4; i < n; i += kThreads * 4)
+        for (uint32_t i = threadIdx.x * 4; i < n; i += kThreads * 4)
             each(again(i), [&](uint32_t u) {
                 above += u > threshold;
                 equal += u == threshold;
@@ -247,8 +248,8 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
     // Every thread lists kRun tokens in a row at a time (counts of a round fit 16 bits), 4 where that is enough.
     auto list = [&](auto run) {
         constexpr int kRun = decltype(run)::value;
-        for (int i0 = 0; i0 < n; i0 += kThreads * kRun) {
-            const int i = i0 + threadIdx.x * kRun;
+        for (uint32_t i0 = 0; i0 < n; i0 += kThreads * kRun) {
+            const uint32_t i = i0 + threadIdx.x * kRun;
             uint4 k[kRun / 4];
             uint32_t here = 0;  // above in the lower half, equal in the upper
 #pragma unroll
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
             uint32_t total;
             const uint32_t before = scan(here, warps, total);
             uint32_t above = base_above + (before & 0xFFFFu), equal = base_equal + (before >> 16);
-            int pos = begin + i;
+            int pos = begin + static_cast<int>(i);
             if (here)
 #pragma unroll
                 for (int j = 0; j < kRun / 4; ++j)
@@ -350,7 +351,7 @@ cudaError_t launch_kv_evict(const EvictProblem& p, int num_sms, cudaStream_t str
     int ctas = 1;
     while (ctas < kMaxCluster && 2 * ctas * static_cast<int64_t>(items) <= num_sms && most > ctas * int64_t{4 * kThreads}) ctas *= 2;
     const int64_t run = ((most + ctas - 1) / ctas + 3) & ~int64_t{3};
-    const int held = static_cast<int>(run < kMostKeys ? run : kMostKeys);
+    const uint32_t held = static_cast<uint32_t>(run < kMostKeys ? run : kMostKeys);
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);

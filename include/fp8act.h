@@ -387,7 +387,7 @@ FP8ACT_API int fp8_kv_attention(const void* q_bf16, int64_t q_stride, const int*
  *   first[token] <= j <= i  and, with window > 0,  j > i - window.
  * That is a sliding window, with `prefix_lens` one that keeps its first tokens; the
  * document that a token is in, if `first` is where that starts; a prefix mask.
- * Positions that no row sees are not read.
+ * Tiles of up to 128 positions that no row of a sequence sees are not read.
  *   soft_cap     0 (none) or 1e-30 .. 1e30
  *   window       0 (none) or the positions that a token sees, its own included
  *   prefix_lens  [batch] int32 or NULL; cut to 0 .. kv_lens[b]

@@ -119,3 +119,33 @@ def test_verify_step_with_positions(kw):
     d.positions += 1000  # the new tokens move away from the cached ones
     assert not torch.equal(d.step(*state)[3], want[3])
     assert f.check_status() == 0
+
+
+def test_past_four_gigabytes(fp8act):  # noqa: F811
+    """Codes beyond 2^32 bytes: turned keys go there, are attended to, weighed and moved from one end to the other."""
+    H, page, D = 8, 256, 256
+    pages = (1 << 32) // (H * page * D) + 3
+    cache = fp8act.kv_cache(pages, H, page, D)
+    assert cache.k.numel() > 1 << 32
+    mass = fp8act.kv_mass(cache)
+    q, k, v = randn(5, 2 * H, D, seed=1), randn(5, H, D, seed=2), randn(5, H, D, seed=3)
+    inv = 1e4 ** (-2.0 * torch.arange(D // 2, device="cuda", dtype=torch.float64) / D)
+    pos = torch.arange(5, device="cuda")
+    at = (pages - 1) * page + pos
+    turned = fp8act.fp8_rope_append(q, k, v, pos, inv, at, cache)
+    want, tol = rope_ref(k, None, pos, inv, None, False)
+    check_cached(cache.k[pages - 1, :, :5].transpose(0, 1), cache.k_scale[pages - 1, :, :5].T, want, tol)
+    table, cu = i32([[pages - 1]]), i32([0, 5])
+    lse = torch.empty((5, 2 * H), device="cuda")
+    out = fp8act.fp8_kv_attention(turned, cache, table, i32([5]), cu, max_q_len=5, lse=lse, window=3, soft_cap=10.0)
+    fp8act.fp8_kv_attention_mass(turned, cache, table, i32([5]), cu, lse, mass, max_q_len=5, accumulate=False, window=3, soft_cap=10.0)
+    for rows, x, values in scores_ref(turned, cache, table, [5], [5], D ** -0.5, window=3, soft_cap=10.0):
+        p = torch.softmax(x, -1)
+        check_attention(out[rows], *(torch.einsum("nhl,lhd->nhd", p, t) for t in (values, values.abs())))
+        got = mass[pages - 1, :, :5].T.double()
+        w = p.unflatten(1, (H, 2)).sum((0, 2)).T
+        assert ((got - w).abs() <= 2.0 ** -11 * w + 1e-20).all()
+    new_lens, kept = fp8act.fp8_kv_evict(cache, mass, table, i32([5]), i32([4]), i32([[pages - 2]]), recent=2)
+    for h in range(H):
+        assert torch.equal(cache.k[pages - 2, h, :4], cache.k[pages - 1, h, kept[0, h, :4].long()])
+    assert new_lens.tolist() == [4] and (kept[0, :, 2:4].cpu() == torch.tensor([3, 4])).all()
