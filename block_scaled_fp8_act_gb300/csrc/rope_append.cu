@@ -19,11 +19,20 @@
 // the vector, and a warp has 512 / D heads of one kind (with fewer heads than that
 // in all, those of several tokens). It keeps them: a CTA's
 // warps go through tokens, each with its heads, their weights in registers and the
-// loads of the next two tokens in flight, and the CTA finds the next tokens' sines
-// and cosines, a pair a thread, while it works on the present ones. More heads
-// than a CTA's warps hold are other CTAs'. (4096 tokens x 32 heads of 128: a warp
-// per token, which finds its own sines, 17.9 us, with one chunk a lane and a
-// vector's halves exchanged 21.0.)
+// loads of the next two vectors and their slot in flight, and the CTA finds the
+// next tokens' sines and cosines, a pair a thread, while it works on the present
+// ones. Two vectors a lane go through each step together: a query's of two tokens,
+// or a key and a value of one, since a warp with two keys kept the others waiting.
+// More heads than a CTA's warps hold are other CTAs'.
+//
+// What bounds it (4096 tokens x 32 heads of 128: 15.2 us, 4.1 TB/s of the least
+// traffic): the chains of a round of two tokens, 3200 clocks with 4 warps a
+// scheduler to hide them (norm and turn 950, a key and a value to codes 1250,
+// unpacking and the next loads 500). One vector after the other, the slot read
+// when it is needed and the keys in warps of their own took 19.6 us, a warp per
+// token that finds its own sines 17.9, with one chunk a lane and a vector's halves
+// exchanged 21.0; the next rows brought to L2 ahead change nothing. One token
+// takes 2.5 us, a trip to memory and one to the slots.
 #include "decoder_util.cuh"
 #include "kernels.h"
 
@@ -75,14 +84,21 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hl = lane % kLanes, sub = lane / kLanes / kHps;
     const KvCache& c = p.cache;
     const int half = p.rot / 2, tiles = (p.tokens + kTile - 1) / kTile;
-    // This warp's heads: steps of queries, then of keys, then of values.
+    // Steps of queries, then those of keys and of values.
     const int steps_q = (p.q_heads + kHps - 1) / kHps, steps_k = (c.heads + kHps - 1) / kHps;
     const int s = blockIdx.y * (blockDim.x >> 5) + warp;
-    const Kind kind = s < steps_q ? kQuery : s < steps_q + steps_k ? kKey : kValue;
-    const int heads = kind == kQuery ? p.q_heads : c.heads;
-    const int h = (s - (kind == kQuery ? 0 : kind == kKey ? steps_q : steps_q + steps_k)) * kHps + lane / kLanes % kHps;
-    const bool mine = h < heads;  // (past the values' heads: an idle warp)
-    const bool normed = kind == kQuery ? p.q_weight != nullptr : kind == kKey && p.k_weight != nullptr;
+    // This warp's vectors of a tile: the same heads of its kIt tokens, or, so that no warp has keys alone, which take
+    // longest, the keys and the values of one of its two.
+    constexpr bool kBoth = kIt == 2;
+    const bool query = s < steps_q;
+    const int kv_step = s - steps_q, of = kBoth ? kv_step % 2 : kv_step / steps_k;  // the token; keys, values (or neither)
+    auto kind_of = [&](int i) { return query ? kQuery : (kBoth ? i : of) == 0 ? kKey : kValue; };
+    auto offset_of = [&](int i) { return kBoth && !query ? of : i * kTps + sub; };  // of the token in the tile
+    const int heads = query ? p.q_heads : c.heads;
+    const int h = (query ? s : kBoth ? kv_step / 2 : kv_step - of * steps_k) * kHps + lane / kLanes % kHps;
+    const bool mine = h < heads && (kBoth || of < 2);  // (past the values' heads: an idle warp)
+    const uint16_t* const weight = query ? p.q_weight : kind_of(0) == kKey ? p.k_weight : nullptr;
+    const bool normed = weight != nullptr;
     // The lane's chunks: columns i and i + R / 2 turn together (or, interleaved, neighbours); what does not turn is shared
     // out after that.
     const int reach = p.rot / 16;  // chunks of half the rotated columns
@@ -91,27 +107,32 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
 
-    const int64_t stride = kind == kQuery ? p.q_stride : kind == kKey ? p.k_stride : p.v_stride;
-    const uint16_t* row = (kind == kQuery ? p.q : kind == kKey ? p.k : p.v) + (mine ? h : 0) * kD + chunk_a * 8;
+    const uint16_t* row[kIt];
+#pragma unroll
+    for (int i = 0; i < kIt; ++i)
+        row[i] = (kind_of(i) == kQuery ? p.q : kind_of(i) == kKey ? p.k : p.v) + (mine ? h : 0) * kD + chunk_a * 8;
     const int apart = (chunk_b - chunk_a) * 8;
-    // This lane's token of the CTA's i-th round, kIt rounds of every gridDim.x tiles.
-    auto token_at = [&](int i) { return (static_cast<int64_t>(i / kIt) * gridDim.x + blockIdx.x) * kTile + i % kIt * kTps + sub; };
-    auto load = [&](int i, uint4 (&x)[2]) {
-        const int64_t t = token_at(i);
-        x[0] = x[1] = make_uint4(0, 0, 0, 0);
+    // A tile's vectors and, for what goes to the cache, its slots.
+    constexpr int kSlots = kBoth ? 1 : kIt;
+    uint4 x[kIt][2];
+    int64_t next_slots[kSlots];
+    auto load = [&](int tile, int i) {
+        const int64_t t = static_cast<int64_t>(tile) * kTile + offset_of(i);
+        const int64_t stride = kind_of(i) == kQuery ? p.q_stride : kind_of(i) == kKey ? p.k_stride : p.v_stride;
+        x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+        if (i < kSlots) next_slots[i] = -1;
         if (mine && t < p.tokens) {
-            x[0] = ld_dep_stream_v4(row + t * stride);
-            x[1] = ld_dep_stream_v4(row + t * stride + apart);
+            x[i][0] = ld_dep_stream_v4(row[i] + t * stride);
+            x[i][1] = ld_dep_stream_v4(row[i] + t * stride + apart);
+            if (i < kSlots && !query) next_slots[i] = *const_cast<const volatile int64_t*>(p.slots + t);
         }
     };
-    uint4 x[kIt][2];
 #pragma unroll
-    for (int i = 0; i < kIt; ++i) load(i, x[i]);
+    for (int i = 0; i < kIt; ++i) load(blockIdx.x, i);
     Half w;
     {
-        const uint16_t* from = kind == kQuery ? p.q_weight : p.k_weight;
         const uint4 none = make_uint4(0, 0, 0, 0);
-        const uint4 packed[2] = {normed ? ld_dep_v4(from + chunk_a * 8) : none, normed ? ld_dep_v4(from + chunk_b * 8) : none};
+        const uint4 packed[2] = {normed ? ld_dep_v4(weight + chunk_a * 8) : none, normed ? ld_dep_v4(weight + chunk_b * 8) : none};
         unpack(packed, w);
         const float2 offset = make_float2(p.weight_offset, p.weight_offset);
 #pragma unroll
@@ -142,6 +163,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
             position[j] += static_cast<int64_t>(axis) * p.tokens;
         }
     }
+    // A lane's pairs 2j and 2j + 1 of its 8 lie together, beside the other lanes'.
+    auto place_of = [](int pair) { return ((pair / 2 % 4) * kLanes + pair / 8) * 2 + pair % 2; };
     auto position_of = [&](int tile, int j) -> int64_t {
         const int64_t t = static_cast<int64_t>(tile) * kTile + token[j];
         return token[j] < kTile && tile < tiles && t < p.tokens ? *const_cast<const volatile int64_t*>(position[j] + t) : 0;
@@ -156,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
             const float more = __uint2float_rn(u & 0xFFu) * 1.4629180792671596e-9f;  // pi 2^-31
             float sn, cs;
             sincospif(at, &sn, &cs);
-            turns[buffer][token[j]][pair[j]] = make_float2(fmaf(-more, sn, cs) * p.rope_scale, fmaf(more, cs, sn) * p.rope_scale);
+            turns[buffer][token[j]][place_of(pair[j])] = make_float2(fmaf(-more, sn, cs) * p.rope_scale, fmaf(more, cs, sn) * p.rope_scale);
         }
     };
     int64_t pos[kPairs];
@@ -165,101 +188,123 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
     turn_by(pos, 0);
     __syncthreads();
 
-    // Norm and turn of a vector (a turn is linear, so that the reciprocal root comes last and its sum is not waited for).
-    auto turned = [&](Half& f, const float2* turn) {
-        float r = 1.0f;
+    // Norm and turn of a tile's first n vectors (a turn is linear, so that the reciprocal root comes last and its sum is not waited for).
+    auto turned = [&](const int n, Half (&f)[kIt], const float2 (&turn)[kTile][kD / 2]) {
+        float r[kIt];
         if (normed) {
-            float2 sum = __fmul2_rn(f.a[0], f.a[0]);
 #pragma unroll
-            for (int j = 1; j < 4; ++j) sum = __ffma2_rn(f.a[j], f.a[j], sum);
+            for (int i = 0; i < n; ++i) {
+                float2 sum = __fmul2_rn(f[i].a[0], f[i].a[0]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum = __ffma2_rn(f.b[j], f.b[j], sum);
-            float all = sum.x + sum.y;
+                for (int j = 1; j < 4; ++j) sum = __ffma2_rn(f[i].a[j], f[i].a[j], sum);
 #pragma unroll
-            for (int o = kLanes / 2; o >= 1; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-            asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(fmaf(all, 1.0f / kD, p.eps)));
+                for (int j = 0; j < 4; ++j) sum = __ffma2_rn(f[i].b[j], f[i].b[j], sum);
+                r[i] = sum.x + sum.y;
+            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f.a[j] = __fmul2_rn(f.a[j], w.a[j]);
-                f.b[j] = __fmul2_rn(f.b[j], w.b[j]);
+            for (int o = kLanes / 2; o >= 1; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < n; ++i) r[i] += __shfl_xor_sync(0xffffffffu, r[i], o);
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                asm("rsqrt.approx.f32 %0, %1;" : "=f"(r[i]) : "f"(fmaf(r[i], 1.0f / kD, p.eps)));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[i].a[j] = __fmul2_rn(f[i].a[j], w.a[j]);
+                    f[i].b[j] = __fmul2_rn(f[i].b[j], w.b[j]);
+                }
             }
         }
         if (rotated) {
             // The lane's 8 pairs: the two chunks' columns of one number, or, interleaved, 4 in each chunk.
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 a = f.a[j], b = f.b[j];
-                const float4 u = *reinterpret_cast<const float4*>(turn + hl * 8 + 2 * j);
-                if constexpr (kInterleaved) {
-                    // (pairs 2j, 2j + 1 of the lane's 8 are chunk a's columns 4j .. for j < 2, then chunk b's)
-                    float2& y0 = j < 2 ? f.a[2 * j] : f.b[2 * j - 4];
-                    float2& y1 = j < 2 ? f.a[2 * j + 1] : f.b[2 * j - 3];
-                    y0 = make_float2(fmaf(-u.y, y0.y, u.x * y0.x), fmaf(u.y, y0.x, u.x * y0.y));
-                    y1 = make_float2(fmaf(-u.w, y1.y, u.z * y1.x), fmaf(u.w, y1.x, u.z * y1.y));
-                } else {
-                    f.a[j] = make_float2(fmaf(-u.y, b.x, u.x * a.x), fmaf(-u.w, b.y, u.z * a.y));
-                    f.b[j] = make_float2(fmaf(u.y, a.x, u.x * b.x), fmaf(u.w, a.y, u.z * b.y));
+            for (int i = 0; i < n; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 a = f[i].a[j], b = f[i].b[j];
+                    const float4 u = *reinterpret_cast<const float4*>(turn[offset_of(i)] + (j * kLanes + hl) * 2);
+                    if constexpr (kInterleaved) {
+                        // (pairs 2j, 2j + 1 of the lane's 8 are chunk a's columns 4j .. for j < 2, then chunk b's)
+                        float2& y0 = j < 2 ? f[i].a[2 * j] : f[i].b[2 * j - 4];
+                        float2& y1 = j < 2 ? f[i].a[2 * j + 1] : f[i].b[2 * j - 3];
+                        y0 = make_float2(fmaf(-u.y, y0.y, u.x * y0.x), fmaf(u.y, y0.x, u.x * y0.y));
+                        y1 = make_float2(fmaf(-u.w, y1.y, u.z * y1.x), fmaf(u.w, y1.x, u.z * y1.y));
+                    } else {
+                        f[i].a[j] = make_float2(fmaf(-u.y, b.x, u.x * a.x), fmaf(-u.w, b.y, u.z * a.y));
+                        f[i].b[j] = make_float2(fmaf(u.y, a.x, u.x * b.x), fmaf(u.w, a.y, u.z * b.y));
+                    }
                 }
-            }
         }
         if (normed) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f.a[j] = __fmul2_rn(f.a[j], make_float2(r, r));
-                f.b[j] = __fmul2_rn(f.b[j], make_float2(r, r));
-            }
+            for (int i = 0; i < n; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[i].a[j] = __fmul2_rn(f[i].a[j], make_float2(r[i], r[i]));
+                    f[i].b[j] = __fmul2_rn(f[i].b[j], make_float2(r[i], r[i]));
+                }
         }
     };
     uint16_t* const out = reinterpret_cast<uint16_t*>(p.q_out) + h * kD + chunk_a * 8;
     const int64_t out_stride = static_cast<int64_t>(p.q_heads) * kD;
-    uint8_t* const codes = kind == kKey ? c.k : c.v;
-    float* const scales = kind == kKey ? c.k_scale : c.v_scale;
     int buffer = 0;
-    for (int tile = blockIdx.x, i0 = 0; tile < tiles; tile += gridDim.x, i0 += kIt) {
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         int64_t pos_next[kPairs];
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) pos_next[j] = position_of(tile + gridDim.x, j);
+        Half f[kIt];
+        int64_t slots[kSlots];
 #pragma unroll
         for (int i = 0; i < kIt; ++i) {
-            const int64_t t = static_cast<int64_t>(tile) * kTile + i * kTps + sub;
-            int64_t slot = -1;
-            if (kind != kQuery && t < p.tokens) slot = *const_cast<const volatile int64_t*>(p.slots + t);
-            Half f;
-            unpack(x[i], f);
-            uint32_t top = max(top_bits(x[i][0]), top_bits(x[i][1])) << 16;
-            load(i0 + kIt + i, x[i]);
-            if (kind != kValue) turned(f, turns[buffer][i * kTps + sub]);
-            if (kind == kQuery) {
+            unpack(x[i], f[i]);
+            if (i < kSlots) slots[i] = next_slots[i];
+            load(tile + gridDim.x, i);
+        }
+        if (query) {
+            turned(kIt, f, turns[buffer]);
+#pragma unroll
+            for (int i = 0; i < kIt; ++i) {
+                const int64_t t = static_cast<int64_t>(tile) * kTile + offset_of(i);
                 if (mine && t < p.tokens) {
-                    *reinterpret_cast<uint4*>(out + t * out_stride) = pack_bf16x8(f.a);
-                    *reinterpret_cast<uint4*>(out + t * out_stride + apart) = pack_bf16x8(f.b);
+                    *reinterpret_cast<uint4*>(out + t * out_stride) = pack_bf16x8(f[i].a);
+                    *reinterpret_cast<uint4*>(out + t * out_stride + apart) = pack_bf16x8(f[i].b);
                 }
-                continue;
             }
-            if (slot >= static_cast<int64_t>(c.num_pages) << c.page_log2) {
-                atomicOr(&g_rope_index_error, 1u);
-                slot = -1;
-            }
-            if (kind == kKey) {
+        } else {
+            if (kind_of(0) == kKey) turned(kSlots, f, turns[buffer]);
+            uint32_t top[kIt];
+#pragma unroll
+            for (int i = 0; i < kIt; ++i) {
                 float most = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    most = largest(most, f.a[j]);
-                    most = largest(most, f.b[j]);
+                    most = largest(most, f[i].a[j]);
+                    most = largest(most, f[i].b[j]);
                 }
-                top = __float_as_uint(most) & 0x7FFFFFFFu;
+                top[i] = __float_as_uint(most) & 0x7FFFFFFFu;
             }
 #pragma unroll
-            for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const bool there = mine && slot >= 0;
-            // (a lane with nothing to store must not take its warp through the divisions that all-zero vectors get)
-            const float scale = quant_head(f.a, f.b, there ? top : __float_as_uint(1.0f));
-            if (!there) continue;
-            const int64_t at = (((slot >> c.page_log2) * c.heads + h) << c.page_log2) + (slot & ((1 << c.page_log2) - 1));
-            uint2* const to = reinterpret_cast<uint2*>(codes + at * kD);
-            to[chunk_a] = pack_e4m3x8(f.a);
-            to[chunk_b] = pack_e4m3x8(f.b);
-            if (hl == 0) scales[at] = scale;
+            for (int o = kLanes / 2; o >= 1; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < kIt; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+#pragma unroll
+            for (int i = 0; i < kIt; ++i) {
+                int64_t& slot = slots[kBoth ? 0 : i];
+                if (slot >= static_cast<int64_t>(c.num_pages) << c.page_log2) {
+                    atomicOr(&g_rope_index_error, 1u);
+                    slot = -1;
+                }
+                const bool there = mine && slot >= 0;
+                // (a lane with nothing to store must not take its warp through the divisions that all-zero vectors get)
+                const float scale = quant_head(f[i].a, f[i].b, there ? top[i] : __float_as_uint(1.0f));
+                if (!there) continue;
+                const bool key = kind_of(i) == kKey;
+                const int64_t at = (((slot >> c.page_log2) * c.heads + h) << c.page_log2) + (slot & ((1 << c.page_log2) - 1));
+                uint2* const to = reinterpret_cast<uint2*>((key ? c.k : c.v) + at * kD);
+                to[chunk_a] = pack_e4m3x8(f[i].a);
+                to[chunk_b] = pack_e4m3x8(f[i].b);
+                if (hl == 0) (key ? c.k_scale : c.v_scale)[at] = scale;
+            }
         }
         if (tile + static_cast<int>(gridDim.x) >= tiles) break;
         buffer ^= 1;
