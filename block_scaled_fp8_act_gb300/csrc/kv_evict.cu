@@ -5,17 +5,25 @@
 // class above it: the last `recent` and the first `first` tokens are the largest
 // number, NaN counts as -infinity. The keep-th largest number T is found 11, 10
 // and 11 bits at a time from counts in shared memory, then the tokens above T
-// and the first of those equal to it are listed by a running count. A (sequence,
+// and the first of those equal to it are listed by a running count; a thread has
+// 16 in a row as bits of a word and goes through those that stay. A (sequence,
 // head) has a cluster of up to 8 CTAs, each with a run of tokens whose numbers
 // stay in shared memory: the weights are read once. The CTAs join their counts
 // through distributed shared memory, so nothing goes through global memory but
 // the list: in the first and the last round, where few bins hold something, each
 // adds its own to every other's (0.8 us; reading all bins of all CTAs 2.4), in the
-// second, where most of them do, they read each other's.
+// second, where most of them do, they read each other's. How many tokens of a CTA
+// lie above T and at it is known from its own counts.
+//
+// What bounds it: the trips of a selection. 131072 tokens x 4 heads to 8192, 19.9
+// us with a copy of 4: start 2.5, weights and first counts 3, the three exchanges
+// 2, 2.2 and 1.4, sums of the bins 1.6, the other rounds' counts 2.1, the list 1.7
+// (3.4 with a test and a store for each token). Clusters of 16 CTAs took 2 us more.
 //
 // Copy. A CTA takes 64 places of the list: one thread each looks up where a
 // token is and where it goes, then the codes move 16 bytes a thread, all of a
-// thread's loads before its stores.
+// thread's loads before its stores. 34 sequences up to 16384 -> 4096: 34.9 us with
+// the selection, 5.1 TB/s.
 #include <atomic>
 #include <type_traits>
 
@@ -150,7 +158,10 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
         }
         return make_uint4(u[0], u[1], u[2], u[3]);
     };
-    auto again = [&](uint32_t i) { return i < held ? *reinterpret_cast<const uint4*>(keys + i) : read(i); };
+    // Where four tokens' numbers are held: in an order in which both those of neighbouring threads and every fourth of them
+    // (a thread's of 16 in a row) lie in different banks.
+    auto at_keys = [&](uint32_t i) { return reinterpret_cast<uint4*>(keys) + (i >> 2 ^ (i >> 4 & 7)); };
+    auto again = [&](uint32_t i) { return i < held ? *at_keys(i) : read(i); };
     auto each = [&](const uint4& k, auto f) {
         f(k.x);
         f(k.y);
@@ -160,6 +171,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
     __syncthreads();
 
     uint32_t want = g.count, prefix = 0;  // the want-th largest of those whose upper bits are `prefix`
+    uint32_t above_here = 0, equal_here = 0;  // this CTA's tokens above those and among them, in this thread's bins
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 11 : 0, top = pass == 0 ? 32 : pass == 1 ? 21 : 11;
@@ -169,19 +181,25 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
 #pragma unroll 4
             for (uint32_t i = threadIdx.x * 4; i < n; i += kThreads * 4) {
                 const uint4 k = read(i);
-                if (i < held) *reinterpret_cast<uint4*>(keys + i) = k;
+                if (i < held) *at_keys(i) = k;
                 each(k, [&](uint32_t u) { atomicAdd(count + (u >> 21), 1u); });
             }
         } else {
-            for (uint32_t i = threadIdx.x * 4; i < n; i += kThreads * 4)
-                each(again(i), [&](uint32_t u) {
-                    if (u >> top == prefix) atomicAdd(count + (u >> shift & mask), 1u);
-                });
+            const uint32_t least = prefix << top, span = 1u << top;
+            for (uint32_t i = threadIdx.x * 4; i < n; i += kThreads * 4) {
+                const uint4 k = again(i);
+                // (in the last round most warps have none)
+                if (min(min(k.x - least, k.y - least), min(k.z - least, k.w - least)) < span)
+                    each(k, [&](uint32_t u) {
+                        if (u - least < span) atomicAdd(count + (u >> shift & mask), 1u);
+                    });
+            }
         }
         __syncthreads();
         // Counts from the largest bin down, two a thread.
         const int bin = kBins - 2 - 2 * static_cast<int>(threadIdx.x);
-        uint32_t lo = count[bin], hi = count[bin + 1];
+        const uint32_t own_lo = count[bin], own_hi = count[bin + 1];
+        uint32_t lo = own_lo, hi = own_hi;
         if (ctas > 1) {
             if (pass == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
             if (pass != 1) {
@@ -217,6 +235,9 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
             found[1] = want - above - (upper ? 0 : hi);
         }
         __syncthreads();
+        const int at = static_cast<int>(found[0]);
+        above_here += (bin > at ? own_lo : 0) + (bin + 1 > at ? own_hi : 0);
+        equal_here = bin == at ? own_lo : bin + 1 == at ? own_hi : 0;
         prefix = prefix << (pass == 1 ? 10 : 11) | found[0];
         want = found[1];
     }
@@ -225,14 +246,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
     // Tokens above the threshold and equal to it in the CTAs before this one.
     uint32_t base_above = 0, base_equal = 0;
     if (ctas > 1) {
-        uint32_t above = 0, equal = 0;
-        for (uint32_t i = threadIdx.x * 4; i < n; i += kThreads * 4)
-            each(again(i), [&](uint32_t u) {
-                above += u > threshold;
-                equal += u == threshold;
-            });
-        above = __reduce_add_sync(0xffffffffu, above);
-        equal = __reduce_add_sync(0xffffffffu, equal);
+        const uint32_t above = __reduce_add_sync(0xffffffffu, above_here), equal = __reduce_add_sync(0xffffffffu, equal_here);
         if ((threadIdx.x & 31) == 0) {
             atomicAdd(&mine.x, above);
             atomicAdd(&mine.y, equal);
@@ -250,26 +264,24 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const __grid_
         constexpr int kRun = decltype(run)::value;
         for (uint32_t i0 = 0; i0 < n; i0 += kThreads * kRun) {
             const uint32_t i = i0 + threadIdx.x * kRun;
-            uint4 k[kRun / 4];
-            uint32_t here = 0;  // above in the lower half, equal in the upper
+            uint32_t above = 0, equal = 0;  // a bit a token
 #pragma unroll
             for (int j = 0; j < kRun / 4; ++j) {
-                k[j] = i + 4 * j < n ? again(i + 4 * j) : make_uint4(0, 0, 0, 0);
-                each(k[j], [&](uint32_t u) { here += u > threshold ? 1u : u == threshold ? 1u << 16 : 0u; });
+                const uint4 k = i + 4 * j < n ? again(i + 4 * j) : make_uint4(0, 0, 0, 0);
+                uint32_t bit = 1u << 4 * j;
+                each(k, [&](uint32_t u) {
+                    above |= u > threshold ? bit : 0;
+                    equal |= u == threshold ? bit : 0;
+                    bit <<= 1;
+                });
             }
             uint32_t total;
-            const uint32_t before = scan(here, warps, total);
-            uint32_t above = base_above + (before & 0xFFFFu), equal = base_equal + (before >> 16);
-            int pos = begin + static_cast<int>(i);
-            if (here)
-#pragma unroll
-                for (int j = 0; j < kRun / 4; ++j)
-                    each(k[j], [&](uint32_t u) {
-                        if (u > threshold || (u == threshold && equal < want)) kept[above + min(equal, want)] = pos;
-                        above += u > threshold;
-                        equal += u == threshold;
-                        ++pos;
-                    });
+            const uint32_t before = scan(__popc(above) | __popc(equal) << 16, warps, total);
+            const uint32_t equals = base_equal + (before >> 16);  // in front of this thread's
+            uint32_t stay = above;
+            for (uint32_t left = equals < want ? want - equals : 0; equal && left; --left, equal &= equal - 1) stay |= equal & -equal;
+            int* to = kept + base_above + (before & 0xFFFFu) + min(equals, want);
+            for (; stay; stay &= stay - 1) *to++ = begin + static_cast<int>(i) + __ffs(stay) - 1;
             base_above += total & 0xFFFFu;
             base_equal += total >> 16;
         }
@@ -351,7 +363,7 @@ cudaError_t launch_kv_evict(const EvictProblem& p, int num_sms, cudaStream_t str
     int ctas = 1;
     while (ctas < kMaxCluster && 2 * ctas * static_cast<int64_t>(items) <= num_sms && most > ctas * int64_t{4 * kThreads}) ctas *= 2;
     const int64_t run = ((most + ctas - 1) / ctas + 3) & ~int64_t{3};
-    const uint32_t held = static_cast<uint32_t>(run < kMostKeys ? run : kMostKeys);
+    const uint32_t held = static_cast<uint32_t>(run < kMostKeys ? (run + 31) / 32 * 32 : kMostKeys);  // (whole sets of banks)
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
