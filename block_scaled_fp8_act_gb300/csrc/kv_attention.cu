@@ -41,6 +41,13 @@
 // to scores to weights to output, with 8 and 12 warps an SM to hide it: their
 // accumulators fill the registers. A single token over 4096 tokens takes 9.0
 // us, the chain of the two kernels.
+//
+// Masks, and a cap or a bias with them, are kinds of their own (ScoreKind), so
+// that plain scores keep their registers; tiles that no row of a sequence sees are
+// not in the list. Capped, a token in a window of 1024 takes 9.6 us, the two
+// kernels' chain again, and 34 x 3 tokens in one of 4096 of up to 16384 32.7, the
+// starts of 136 items and then latency as above (34.5 without the cap). A bias by
+// distance adds to the chain of a unit: 8 tokens over 131072 69.1 us.
 #include <atomic>
 #include <type_traits>
 

@@ -43,7 +43,8 @@
 // tiles of 64 tokens do not help, since an MMA 64 columns wide takes longer than
 // one of 128 (104 clocks against 64). Measured and slower: the softmax on 16
 // warps with 96 registers, the weights taken first and the maximum checked after,
-// a third widened buffer. The kernel spills (364 bytes of stores and 468 of loads
+// a third widened buffer. A cap makes the softmax's chain half as long again (512
+// over 16384: 121 us with masks alone, 176 capped). The kernel spills (364 bytes of stores and 468 of loads
 // a thread with one row tile, 280 and 328 with two); of which role is not known.
 //
 // Every wait is bounded by wall time. The first that gives up sets the error

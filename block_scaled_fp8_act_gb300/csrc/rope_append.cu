@@ -327,7 +327,7 @@ cudaError_t launch(const RopeProblem& p, int num_sms, cudaStream_t stream) {
 }
 
 // Many tokens: two at a time, or, where a warp has room for more heads than there are, that many. (3 heads on 1 of 128,
-// 20000 tokens: 29.2 us with one token a round.) With no more than a few for every CTA, one.
+// 20000 tokens: 23.6 us, and 27.5 where one token a warp and round took 29.2.) With no more than a few for every CTA, one.
 template <int kLanes>
 cudaError_t launch_tokens(const RopeProblem& p, int num_sms, cudaStream_t stream) {
     constexpr int kPer = 32 / kLanes;
