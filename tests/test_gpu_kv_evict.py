@@ -106,6 +106,15 @@ def test_evict_ties_and_odd_weights(fp8act):  # noqa: F811
     evict_and_check(fp8act, cache, mass, table, lens, keep, new_table)  # neighbours in the last bit
 
 
+@pytest.mark.parametrize("values", [1, 2, 5])
+@pytest.mark.parametrize("L,keep", [(131071, 50001), (70000, 69999), (20011, 3)])
+def test_evict_ties_in_long_contexts(fp8act, L, keep, values):  # noqa: F811
+    """Of equal tokens the first stay, wherever among a sequence's CTAs and threads the last of them falls."""
+    cache, mass, table, lens, keep, new_table = problem(fp8act, [L], [keep], 2, 64, 64, seed=values)
+    mass.copy_(torch.randint(0, values, mass.shape, device="cuda", generator=gen(L)).float())
+    evict_and_check(fp8act, cache, mass, table, lens, keep, new_table, recent=9, first=5)
+
+
 def test_evict_leaves_the_old_pages(fp8act):  # noqa: F811
     """Two sequences that share a prefix are cut from the same old pages; again gives the same."""
     cache, mass, table, lens, keep, new_table = problem(fp8act, [200, 170], [64, 90], 2, 128, 16, seed=12)

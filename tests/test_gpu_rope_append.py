@@ -218,3 +218,25 @@ def test_rope_binding_refusals(fp8act):  # noqa: F811
                 dict(positions=pos.repeat(3, 1)), dict(positions=pos[:0].contiguous())):
         with pytest.raises(fp8act.Fp8ActError):
             call(**bad)
+
+
+@pytest.mark.parametrize("T,Hq,H,D,interleaved", [(1301, 24, 4, 128, False), (2999, 5, 3, 64, True), (3000, 1, 1, 64, False), (1500, 3, 3, 256, True)])
+def test_rope_many_tokens_are_as_few(fp8act, T, Hq, H, D, interleaved):  # noqa: F811
+    """However the tokens are shared out, their bits are those of calls with a few: among slots left out and heads of zeros,
+    infinities and NaN."""
+    q, k, v, qw, kw, inv, pos, axis = problem(T, Hq, H, D, D, 2, True, seed=T)
+    g = gen(T)
+    for x in (q, k, v):
+        for odd in (0.0, math.inf, math.nan, 1e-40, 3e38):
+            x[torch.randint(0, T, (20,), device="cuda", generator=g), torch.randint(0, x.shape[1], (20,), device="cuda", generator=g)] = odd
+    pages = T // 16 + 2
+    slots = torch.randperm(pages * 16, device="cuda", generator=g)[:T]
+    slots[torch.randint(0, T, (T // 10,), device="cuda", generator=g)] = -1
+    got, few = filled(fp8act, pages, H, 16, D), filled(fp8act, pages, H, 16, D)
+    how = dict(axes=axis, q_weight=qw, k_weight=kw, interleaved=interleaved)
+    out = fp8act.fp8_rope_append(q, k, v, pos, inv, slots, got, **how)
+    for i in range(0, T, 97):
+        at = slice(i, i + 97)
+        part = fp8act.fp8_rope_append(q[at], k[at], v[at], pos[:, at].contiguous(), inv, slots[at], few, **how)
+        assert torch.equal(out[at].view(torch.int16), part.view(torch.int16))
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, few))
