@@ -229,11 +229,12 @@ struct Item {
     int nq, q0, len;   // new tokens, first one's row in q, cached tokens
     int rts, tiles;    // row tiles of this sequence and units of each, kCost included
     int prefix;        // positions that every row sees (0 in a plain list)
+    int skip;          // kMass: tiles left out behind the prefix's
     int64_t first;     // index of the item's first unit
 };
 
-// kScored: units are the tiles that the sequence's rows may see. kMass: an item has all the sequence's rows, and a token
-// tile counts as often as they have 64 (at most 16 times).
+// kScored: units are the tiles that the sequence's rows may see. kMass: those and the ones whose weights start from zero;
+// an item has all the sequence's rows, and a token tile counts as often as they have 64 (at most 16 times).
 enum class List { kPlain, kScored, kMass };
 __device__ __forceinline__ int old_end(const AttnArgs& a, int b, int len, int nq) {  // positions before it keep their weight
     return !a.accumulate ? 0 : a.old_lens ? ld_dep_s32(a.old_lens + b) : len - nq;
@@ -258,9 +259,13 @@ struct Units {
         it.tiles = (len + kTok - 1) / kTok + kCost;  // (an empty sequence still writes its rows)
         it.prefix = 0;
         if constexpr (kList == List::kMass) {
-            it.prefix = prefix_of(a.scores, b, len);
-            it.rts = len > 0 && (it.nq > 0 || !a.accumulate || a.old_lens) ? 1 : 0;
-            it.tiles = (len + kTok - 1) / kTok * mass_weight(it.nq * a.group) + kCost;
+            const int kept = old_end(a, b, len, it.nq);
+            it.prefix = it.nq > 0 ? prefix_of(a.scores, b, len) : 0;
+            const int lo = min(it.nq > 0 ? min(first_seen(a.scores, q0, len, it.nq, 0), kept) : kept, len);
+            const Reach r = reach_of<kTok>(it.prefix, lo, len);
+            it.skip = r.skip;
+            it.rts = len > 0 && (it.nq > 0 || kept < len) ? 1 : 0;
+            it.tiles = r.end * mass_weight(it.nq * a.group) + kCost;
         }
         if constexpr (kList == List::kScored) {
             it.prefix = prefix_of(a.scores, b, len);

@@ -11,7 +11,8 @@
 // Work split. A unit is 32 cached tokens of a KV head with all the sequence's
 // rows; a warp takes whole units, so that no sum is joined and the order is
 // fixed. The units of all sequences and heads form one list, shared evenly by the
-// CTAs, weighted by their rows. A warp has its own ring of key tiles in
+// CTAs, weighted by their rows; tiles that no row sees and whose tokens keep their
+// weights are not in it. A warp has its own ring of key tiles in
 // flight. Rows come 256 at a time (128 for D = 256); with more, a token's sum
 // goes through its place in memory between them.
 //
@@ -52,11 +53,14 @@ struct Mass {
     static_assert((kRoom - kRows * kRowBytes) / (kWarps * kStageBytes) >= 2, "a tile in flight beside the one being read");
 };
 
-template <int kD, bool kFew, bool kChanged>
+// (Plain scores have an instance of their own, without the masks' tests of what a row sees: 34 single tokens over 16384
+// 56.8 us, and 60.2 with them.)
+template <int kD, bool kFew, ScoreKind kKind>
 __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCtas)
     kv_mass_kernel(const __grid_constant__ AttnArgs a, int stages) {
     using M = Mass<kD, kFew>;
     constexpr int kKS = kD / 32;
+    constexpr bool kScored = kKind != ScoreKind::kPlain, kChanged = kKind == ScoreKind::kChanged;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Work::Scratch scratch;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, qd = lane & 3;
@@ -83,6 +87,8 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
         const int* table = a.table + it.b * a.table_stride;
         const int in_page = (1 << a.c.page_log2) - 1;
         const int kept_end = old_end(a, it.b, it.len, it.nq);
+        const int prefix = kScored ? it.prefix : 0;
+        auto position = [&](int t) { return t * kTile + (t * kTile < prefix ? 0 : it.skip * kTile); };
 
         int row0 = 0;
         do {
@@ -92,19 +98,22 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
                 const int q_first = row0 / a.group, q_last = (row0 + nrows - 1) / a.group;
                 limit_first = it.len - it.nq + q_first + 1;
                 limit_last = it.len - it.nq + q_last + 1;
-                lo_first = first_seen(a.scores, it.q0, it.len, it.nq, q_first);
-                lo_last = first_seen(a.scores, it.q0, it.len, it.nq, q_last);
+                if constexpr (kScored) {
+                    lo_first = first_seen(a.scores, it.q0, it.len, it.nq, q_first);
+                    lo_last = first_seen(a.scores, it.q0, it.len, it.nq, q_last);
+                }
             }
-            // Whether some row may see a token of tile t.
-            auto seen = [&](int t) {
-                const int pos = t * kTile;
-                return pos < it.prefix || (pos < limit_last && pos + kTile > lo_first);
-            };
+            // Whether some row may see a token of the tile at pos.
+            auto seen = [&](int pos) { return pos < prefix || (pos < limit_last && pos + kTile > lo_first); };
+            // Whether one of n tokens from pos on may be touched: not those that no row sees and that keep their weight, whose
+            // pages may be another sequence's by now.
+            const int touched_from = row0 > 0 ? lo_first : nrows > 0 ? min(lo_first, kept_end) : kept_end;
+            auto touched = [&](int pos, int n) { return pos < prefix || pos + n > touched_from; };
             // The warp's tiles are t0 + warp, + kWarps, ... Pages of its next 16, one per 16 tokens and lane.
             auto look_up = [&](int t) -> int {
                 t += (lane >> 1) * M::kWarps;
-                const int pos = t * kTile + (lane & 1) * 16;
-                if (t >= t1 || pos >= it.len) return -1;
+                const int pos = position(t) + (lane & 1) * 16;
+                if (t >= t1 || pos >= it.len || !touched(pos, 16)) return -1;
                 const int p = ld_dep_s32(table + (pos >> a.c.page_log2));
                 if (p >= 0 && p < a.c.num_pages) return p;
                 atomicOr(a.index_error, 1u);
@@ -113,17 +122,18 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
             const int first_pages = look_up(t0 + warp);
             int pages = first_pages, asked = 0;
             auto place_of = [&](int pos, int page) -> int64_t {
-                return page >= 0 && pos < it.len
+                return page >= 0 && pos < it.len && touched(pos, 1)
                            ? ((static_cast<int64_t>(page) * a.c.heads + it.h) << a.c.page_log2) + (pos & in_page)
                            : -1;
             };
             auto request = [&](int t, int stage) {
                 if (t < t1) {
                     const int p0 = __shfl_sync(0xffffffffu, pages, 2 * asked), p1 = __shfl_sync(0xffffffffu, pages, 2 * asked + 1);
-                    if (seen(t)) {
+                    const int pos0 = position(t);
+                    if (seen(pos0)) {
                         const uint32_t dst = ptx::smem_u32(ring) + stage * M::kStageBytes;
                         constexpr int kC = kD / 16, kStep = 32 / kC, kSteps = 32 / kStep;  // chunks per token, tokens per instruction
-                        const int c = lane % kC, r0 = lane / kC, pos0 = t * kTile;
+                        const int c = lane % kC, r0 = lane / kC;
                         const int64_t row_a = ((static_cast<int64_t>(p0) * a.c.heads + it.h) << a.c.page_log2) + (pos0 & in_page);
                         const int64_t row_b =
                             ((static_cast<int64_t>(p1) * a.c.heads + it.h) << a.c.page_log2) + ((pos0 + 16) & in_page) - 16;
@@ -201,12 +211,13 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
             float have = 0.0f;
             auto look_ahead = [&](int t) {
                 if (t >= t1) return;
-                mine = place_of(t * kTile + my_token, __shfl_sync(0xffffffffu, held, 2 * used + (my_token >> 4)));
+                const int pos = position(t) + my_token;
+                mine = place_of(pos, __shfl_sync(0xffffffffu, held, 2 * used + (my_token >> 4)));
                 if (++used == 16) {
                     used = 0;
                     held = look_up(t + M::kWarps);
                 }
-                const bool adds = row0 > 0 || t * kTile + my_token < kept_end;
+                const bool adds = row0 > 0 || pos < kept_end;
                 have = adds && mine >= 0 ? ld_dep_f32(a.mass + mine) : 0.0f;
             };
             look_ahead(t0 + warp);
@@ -219,7 +230,8 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
                 wait_for_tile();
                 const uint8_t* kt = ring + stage * M::kStageBytes;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (seen(t)) {
+                const int pos0 = position(t);
+                if (seen(pos0)) {
                     // The tile's codes as A fragments: af[k-step][16 tokens][4].
                     uint32_t af[kD / 16][2][4];
                     float ks[4];
@@ -242,8 +254,7 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
                             }
                     __syncwarp();  // the stage is read
                     request(t + (stages - 1) * M::kWarps, stage == 0 ? stages - 1 : stage - 1);
-                    const int pos0 = t * kTile;
-                    const bool edge = on_edge(pos0, kTile, it.prefix, lo_last, limit_first);
+                    const bool edge = on_edge(pos0, kTile, prefix, lo_last, limit_first);
                     const uint4* qf = reinterpret_cast<const uint4*>(queries) + lane;
                     auto rows_of = [&](auto masks, int i) {
                         float s[2][4] = {};
@@ -287,7 +298,7 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
                             float p = ex2(y[j]);
                             if constexpr (decltype(masks)::value) {
                                 const int pos = pos0 + (j >> 1) * 8 + og;
-                                if (pos >= it.prefix && (pos < info[j & 1].lo || pos >= info[j & 1].limit)) p = 0.0f;
+                                if (pos >= prefix && (pos < info[j & 1].lo || pos >= info[j & 1].limit)) p = 0.0f;
                             }
                             sum[j >> 1] += p;
                         }
@@ -322,7 +333,7 @@ __global__ void __launch_bounds__(Mass<kD, kFew>::kThreads, Mass<kD, kFew>::kCta
     }
 }
 
-template <int kD, bool kFew, bool kChanged>
+template <int kD, bool kFew, ScoreKind kKind>
 cudaError_t launch(AttnArgs& a, int64_t rows, int num_sms, cudaStream_t stream) {
     using M = Mass<kD, kFew>;
     a.rows = rows >= M::kRows ? M::kRows : rows < 8 ? 8 : static_cast<int>((rows + 7) / 8 * 8);
@@ -330,7 +341,7 @@ cudaError_t launch(AttnArgs& a, int64_t rows, int num_sms, cudaStream_t stream) 
     static std::atomic<bool> configured[64];
     int dev = 0;
     cudaGetDevice(&dev);
-    auto kernel = kv_mass_kernel<kD, kFew, kChanged>;
+    auto kernel = kv_mass_kernel<kD, kFew, kKind>;
     if (!configured[dev & 63].load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kRoom);
         if (e != cudaSuccess) return e;
@@ -340,17 +351,24 @@ cudaError_t launch(AttnArgs& a, int64_t rows, int num_sms, cudaStream_t stream) 
     return launch_dependent(kernel, dim3(num_sms * M::kCtas), M::kThreads, bytes, stream, 1, a, stages);
 }
 
-template <int kD>
+template <int kD, ScoreKind kKind>
 cudaError_t launch_rows(AttnArgs& a, int max_q_len, int num_sms, cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(max_q_len) * a.group;
-    const bool changed = a.scores.kind == ScoreKind::kChanged;
     if (kD == 128 && rows >= kWideRows) {
         a.rows = kWideRows;  // (any: an item has all rows)
         return launch_mass_tc(a, num_sms, stream);
     }
-    if (rows <= Mass<kD, true>::kRows)
-        return changed ? launch<kD, true, true>(a, rows, num_sms, stream) : launch<kD, true, false>(a, rows, num_sms, stream);
-    return changed ? launch<kD, false, true>(a, rows, num_sms, stream) : launch<kD, false, false>(a, rows, num_sms, stream);
+    return rows <= Mass<kD, true>::kRows ? launch<kD, true, kKind>(a, rows, num_sms, stream)
+                                         : launch<kD, false, kKind>(a, rows, num_sms, stream);
+}
+
+template <int kD>
+cudaError_t launch_kind(AttnArgs& a, int max_q_len, int num_sms, cudaStream_t stream) {
+    switch (a.scores.kind) {
+        case ScoreKind::kPlain: return launch_rows<kD, ScoreKind::kPlain>(a, max_q_len, num_sms, stream);
+        case ScoreKind::kMasked: return launch_rows<kD, ScoreKind::kMasked>(a, max_q_len, num_sms, stream);
+        default: return launch_rows<kD, ScoreKind::kChanged>(a, max_q_len, num_sms, stream);
+    }
 }
 
 }  // namespace
@@ -379,9 +397,9 @@ cudaError_t launch_kv_mass(const MassProblem& p, int num_sms, cudaStream_t strea
     a.accumulate = p.accumulate;
     a.old_lens = p.old_lens;
     switch (p.cache.head_dim) {
-        case 64: return launch_rows<64>(a, p.max_q_len, num_sms, stream);
-        case 128: return launch_rows<128>(a, p.max_q_len, num_sms, stream);
-        default: return launch_rows<256>(a, p.max_q_len, num_sms, stream);
+        case 64: return launch_kind<64>(a, p.max_q_len, num_sms, stream);
+        case 128: return launch_kind<128>(a, p.max_q_len, num_sms, stream);
+        default: return launch_kind<256>(a, p.max_q_len, num_sms, stream);
     }
 }
 

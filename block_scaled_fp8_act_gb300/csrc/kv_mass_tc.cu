@@ -123,14 +123,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
         return ok;
     };
 
-    // What every role knows of a job: some rows of an item and this CTA's tiles. Tiles [t0, t1) are seen where they are among
-    // a0 .. a0 + a_n - 1 (the prefix's) or b0 .. b0 + b_n - 1.
+    // What every role knows of a job: some rows of an item and this CTA's tiles, [t0, t1) of the item's list. The rows see
+    // the a_n ones from t0 on (the prefix's, where the list leaves out none) and the n - a_n ones from b0 on, which is
+    // counted in the sequence.
     struct Job {
         int row0, nrows, columns;
         int t0, t1, a_n, b0, n;
-        int lo, limit;  // no row needs a mask in [lo, limit), but for the prefix
+        int lo, limit;   // no row needs a mask in [lo, limit), but for the prefix
+        int from;        // no row sees anything before it, but for the prefix
         __device__ int tile(int i) const { return i < a_n ? t0 + i : b0 + i - a_n; }
-        __device__ bool seen(int t) const { return t < t0 + a_n || (t >= b0 && t < b0 + n - a_n); }
     };
     int row0 = 0;
     auto job_of = [&]() {
@@ -145,15 +146,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
         j.row0 = row0;
         j.nrows = min(rows_total - row0, kRows);
         j.columns = (j.nrows + 31) / 32 * 32;
-        j.a_n = j.n = j.b0 = j.lo = j.limit = 0;
+        j.a_n = j.n = j.b0 = j.lo = j.limit = j.from = 0;
         if (j.nrows > 0) {
             const TileReach r = tile_reach<kTok>(a, it, row0, j.nrows);
             j.lo = r.lo;
             j.limit = r.limit;
-            const int prefix = r.tiles.prefix_tiles, start = prefix + r.tiles.skip;
+            j.from = first_seen(a.scores, it.q0, it.len, it.nq, row0 / a.group);
+            const int prefix = r.tiles.prefix_tiles;
             j.a_n = max(min(j.t1, prefix) - j.t0, 0);
-            j.b0 = max(j.t0, start);
-            j.n = j.a_n + max(min(j.t1, start + r.tiles.end - prefix) - j.b0, 0);
+            j.b0 = max(max(j.t0, prefix) + it.skip, prefix + r.tiles.skip);
+            j.n = j.a_n + max(min(j.t1 + it.skip, r.tiles.end + r.tiles.skip) - j.b0, 0);
         }
         return j;
     };
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
                 const uint32_t round = n / kStages, stage = n - round * kStages, bar = k_full + 8 * stage;
                 if (round > 0 && !(ok = wait(k_empty + 8 * stage, (round - 1) & 1))) break;
                 const int pos = j.tile(i) * kTok + lane * box;
-                const bool copy = lane < kTok / box && is_page(pos, page);
+                const bool copy = lane < kTok / box && (pos < it.prefix || pos + box > j.from) && is_page(pos, page);
                 const uint32_t copies = __ballot_sync(0xffffffffu, copy);
                 const bool withheld = x.withhold && n == 0;
                 if (lane == 0 && !withheld) ptx::mbar_arrive_expect_tx(bar, __popc(copies) * box * kD);
@@ -262,10 +264,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
             const Job j = job_of();
             table = a.table + it.b * a.table_stride;
             const int kept_end = old_end(a, it.b, it.len, it.nq);
-            // The place of this thread's token of tile t, what it has so far and its key scale.
+            // The place of this thread's token of tile t, what it has so far and its key scale. There is none for a token that no
+            // row sees and that keeps its weight, whose page may be another sequence's by now.
+            const int touched_from = j.row0 > 0 ? j.from : j.nrows > 0 ? min(j.from, kept_end) : kept_end;
             auto fetch = [&](int t, int page, int64_t& place, float& have, float& ks) {
                 const int pos = t * kTok + mine;
-                place = is_page(pos, page) ? place_of(page, pos) : -1;
+                place = (pos < it.prefix || pos >= touched_from) && is_page(pos, page) ? place_of(page, pos) : -1;
                 const bool adds = j.row0 > 0 || pos < kept_end;
                 have = adds && place >= 0 ? ld_dep_f32(a.mass + place) : 0.0f;
                 ks = place >= 0 ? ld_dep_f32(a.c.k_scale + place) : 0.0f;
@@ -311,10 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_mass_tc_kernel(const __grid_co
             if (lane == 0) ptx::mbar_arrive(q_full);
             if (!(ok = wait(q_full, jobs & 1))) break;
 
-            // Tiles that no row sees get nothing.
+            // Tiles that no row sees get nothing; those that start from zero are zero.
             if (j.row0 == 0 && j.n < j.t1 - j.t0)
-                for (int t = j.t0 + acc; t < j.t1; t += 2) {
-                    if (j.seen(t) || (t + 1) * kTok <= kept_end) continue;
+                for (int v = j.t0 + acc; v < j.t1; v += 2) {
+                    const int t = v * kTok < it.prefix ? v : v + it.skip;
+                    if (v < j.t0 + j.a_n || (t >= j.b0 && t < j.b0 + j.n - j.a_n) || (t + 1) * kTok <= kept_end) continue;
                     int64_t at;
                     float old, unused;
                     fetch(t, page_of(t * kTok + mine), at, old, unused);

@@ -420,7 +420,8 @@ def fp8_kv_attention_mass(q, cache, page_table, kv_lens, cu_q, lse, mass, max_q_
     The weights exp(score - lse) of the new tokens q, summed over them and over the query heads of a KV head;
     lse (fp32 [tokens, q_heads]) is what fp8_kv_attention left with the same arguments. The places from
     old_lens (int32 [B]; None: all but the new tokens) on start from zero, all of a sequence's if not
-    `accumulate`. A page that gets weight belongs to one sequence of the call."""
+    `accumulate`; pages that no token of q sees and whose weights stay are left alone, whatever the table has
+    there. A page that gets weight belongs to one sequence of the call."""
     _native().kv_attention_mass(q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, lse, mass, accumulate, stream,
                                 soft_cap, window, prefix_lens, first, slopes, old_lens)
 

@@ -431,7 +431,10 @@ FP8ACT_API int fp8_kv_attention_scored(const void* q_bf16, int64_t q_stride, con
  *               ones. Needed where only the last of a chunk's tokens are passed
  * Sums are fp32 in a fixed order. A row whose lse is -infinity adds nothing; a NaN
  * scale of a cached token makes that token's weight NaN. Places past kv_lens[b] are
- * left as they are. A page that gets weight belongs to one sequence of the call.
+ * left as they are, and so are those that no passed token sees and that keep their
+ * weight: they are not read, and a page of the table that holds nothing else may be
+ * any (one that a window has left behind, say). A page that gets weight belongs to
+ * one sequence of the call.
  */
 FP8ACT_API int fp8_kv_attention_mass(const void* q_bf16, int64_t q_stride, const int* cu_q, const int* kv_lens,
                                      const int* page_table, int max_pages, int batch, int tokens, int max_q_len,
