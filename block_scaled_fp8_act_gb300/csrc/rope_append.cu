@@ -188,10 +188,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
     turn_by(pos, 0);
     __syncthreads();
 
-    // Norm and turn of a tile's first n vectors (a turn is linear, so that the reciprocal root comes last and its sum is not waited for).
+    // Norm and turn of a tile's first n vectors. (The reciprocal root comes first, as in the formula: a finite vector whose sum
+    // of squares passes fp32's range is then zeros, and not infinity times zero.)
     auto turned = [&](const int n, Half (&f)[kIt], const float2 (&turn)[kTile][kD / 2]) {
-        float r[kIt];
         if (normed) {
+            float r[kIt];
 #pragma unroll
             for (int i = 0; i < n; ++i) {
                 float2 sum = __fmul2_rn(f[i].a[0], f[i].a[0]);
@@ -210,8 +211,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
                 asm("rsqrt.approx.f32 %0, %1;" : "=f"(r[i]) : "f"(fmaf(r[i], 1.0f / kD, p.eps)));
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    f[i].a[j] = __fmul2_rn(f[i].a[j], w.a[j]);
-                    f[i].b[j] = __fmul2_rn(f[i].b[j], w.b[j]);
+                    f[i].a[j] = __fmul2_rn(__fmul2_rn(f[i].a[j], make_float2(r[i], r[i])), w.a[j]);
+                    f[i].b[j] = __fmul2_rn(__fmul2_rn(f[i].b[j], make_float2(r[i], r[i])), w.b[j]);
                 }
             }
         }
@@ -233,15 +234,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) rope_append_kernel(const __gr
                         f[i].a[j] = make_float2(fmaf(-u.y, b.x, u.x * a.x), fmaf(-u.w, b.y, u.z * a.y));
                         f[i].b[j] = make_float2(fmaf(u.y, a.x, u.x * b.x), fmaf(u.w, a.y, u.z * b.y));
                     }
-                }
-        }
-        if (normed) {
-#pragma unroll
-            for (int i = 0; i < n; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f[i].a[j] = __fmul2_rn(f[i].a[j], make_float2(r[i], r[i]));
-                    f[i].b[j] = __fmul2_rn(f[i].b[j], make_float2(r[i], r[i]));
                 }
         }
     };

@@ -308,7 +308,8 @@ FP8ACT_API int fp8_kv_append(const void* k_bf16, const void* v_bf16, const int64
 /*
  * What lies between the q, k, v product and the attention, in one pass: RMS
  * norm of every query and key head, rotary positions, keys and values into the
- * cache. Per head vector x of head_dim values, in fp32:
+ * cache. Per head vector x of head_dim values, in fp32 and in this order (a normed
+ * head whose squares sum past fp32's range becomes zeros):
  *   y = x * rsqrt(mean(x^2) + eps) * (weight + weight_offset)   (with a weight; else y = x)
  *   (a, b) -> rope_scale * (a cos - b sin, a sin + b cos)  for pair i of the first
  *   rot_dim columns, angle = positions[axis[i], t] * inv_freq[i]
