@@ -323,7 +323,8 @@ FP8ACT_API int fp8_kv_append(const void* k_bf16, const void* v_bf16, const int64
  * Several axes are rows of positions (time, height, width): axis[i] says which
  * one turns pair i, so sections and interleaved axes are both a table.
  * Angles are reduced in whole numbers (2^64 to a turn), so positions may be any
- * int64; the frequency's rounding leaves an error of 2^-52 of the angle.
+ * int64: an angle is off by at most |position| * 2^-64 turns, since a frequency is a
+ * whole number of those, and 2^-62 of itself, beside the fp32 arithmetic's 2^-24.
  *   q [T, q_heads, head_dim], k, v [T, kv_heads, head_dim] bf16, tokens *_stride
  *     elements apart (multiples of 8, at least the width of their heads)
  *   q_weight, k_weight [head_dim] bf16, either may be NULL: no norm
