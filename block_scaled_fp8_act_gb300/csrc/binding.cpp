@@ -43,12 +43,21 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
 constexpr auto kBf16 = at::kBFloat16, kF32 = at::kFloat, kI32 = at::kInt, kI64 = at::kLong, kU8 = at::kByte,
                kF64 = at::kDouble, kE4m3 = at::kFloat8_e4m3fn;
 
+// The library launches on the current device, which cannot read another one's memory in general: every tensor of a call
+// is there. (Asked for once a call.)
+thread_local int g_device = -1;
+void on_current_device(const at::Tensor& t, const char* name) {
+    if (g_device < 0) g_device = c10::cuda::current_device();
+    if (t.get_device() != g_device) raise(PyExc_ValueError, std::string(name) + " is not on the current CUDA device");
+}
+
 // A contiguous CUDA tensor of a known shape and one of two types.
 template <class T>
 T* data(const at::Tensor& t, at::ScalarType a, at::ScalarType b, at::IntArrayRef shape, const char* name) {
     if (!t.is_cuda() || (t.scalar_type() != a && t.scalar_type() != b))
         raise(PyExc_TypeError, std::string(name) + " must be a CUDA tensor of type " + c10::toString(a) +
                                    (a == b ? "" : std::string(" or ") + c10::toString(b)));
+    on_current_device(t, name);
     if (t.sizes() != shape || !t.is_contiguous())
         raise(PyExc_ValueError, std::string(name) + " must be contiguous with shape " + text(shape) + ", got " + text(t.sizes()));
     return static_cast<T*>(t.data_ptr());
@@ -70,6 +79,7 @@ T* optional(PyObject* o, at::ScalarType a, at::IntArrayRef shape, const char* na
 const at::Tensor& matrix(PyObject* o, const char* name) {
     const at::Tensor& t = tensor(o, name);
     if (!t.is_cuda() || t.scalar_type() != kBf16) raise(PyExc_TypeError, std::string(name) + " must be a bf16 CUDA tensor");
+    on_current_device(t, name);
     if (t.dim() != 2 || !t.is_contiguous()) raise(PyExc_ValueError, std::string(name) + " must be a contiguous 2-D tensor");
     return t;
 }
@@ -77,12 +87,6 @@ const at::Tensor& matrix(PyObject* o, const char* name) {
 int to_int(int64_t v, const char* name) {
     if (v > INT32_MAX) raise(PyExc_ValueError, std::string(name) + " is too large");
     return static_cast<int>(v);
-}
-
-// The library launches on the current device.
-void on_current_device(const at::Tensor& t, const char* name) {
-    if (t.is_cuda() && t.get_device() != c10::cuda::current_device())
-        raise(PyExc_ValueError, std::string(name) + " is not on the current CUDA device");
 }
 
 cudaStream_t stream_of(PyObject* o) {
@@ -159,6 +163,7 @@ Workspace workspace(PyObject* o, size_t need, const at::Tensor& like, cudaStream
     if (given(o)) {
         const at::Tensor& t = tensor(o, "workspace");
         if (!t.is_cuda() || !t.is_contiguous()) raise(PyExc_TypeError, "workspace must be a contiguous CUDA tensor");
+        on_current_device(t, "workspace");
         return {t, t.data_ptr(), static_cast<size_t>(t.nbytes())};
     }
     if (need < 16) need = 16;
@@ -206,6 +211,7 @@ fp8act_kv_cache cache_of(PyObject* o) {
 // A bf16 [tokens, heads, dim] tensor whose tokens may be apart (columns of wider rows); its token stride.
 int64_t heads_of(const at::Tensor& t, int64_t heads, int64_t dim, const char* name) {
     if (!t.is_cuda() || t.scalar_type() != kBf16) raise(PyExc_TypeError, std::string(name) + " must be a bf16 CUDA tensor");
+    on_current_device(t, name);
     if (t.dim() != 3 || t.size(2) != dim || (heads >= 0 && t.size(1) != heads))
         raise(PyExc_ValueError, std::string(name) + " must be [tokens, heads, " + std::to_string(dim) + "], got " + text(t.sizes()));
     if (t.stride(2) != 1 || (t.stride(1) != dim && t.size(1) > 1))
@@ -273,7 +279,6 @@ PyObject* rope_append(PyObject* const* a) {
                      &freq = tensor(a[4], "inv_freq");
     const int64_t D = c.head_dim, qs = heads_of(q, -1, D, "q"), ks = heads_of(k, c.kv_heads, D, "k"),
                   vs = heads_of(v, c.kv_heads, D, "v"), T = q.size(0), Hq = q.size(1);
-    on_current_device(q, "q");
     if (k.size(0) != T || v.size(0) != T) raise(PyExc_ValueError, "q, k and v have different numbers of tokens");
     if (pos.dim() != 1 && pos.dim() != 2) raise(PyExc_ValueError, "positions must be [T] or [axes, T]");
     const int64_t axes = pos.dim() == 2 ? pos.size(0) : 1;
@@ -318,7 +323,6 @@ Rows rows_of(PyObject* const* a) {
     const fp8act_kv_cache c = cache_of(a[1]);
     const at::Tensor &q = tensor(a[0], "q"), &table = tensor(a[2], "page_table");
     const int64_t qs = heads_of(q, -1, c.head_dim, "q"), T = q.size(0);
-    on_current_device(q, "q");
     if (table.dim() != 2) raise(PyExc_ValueError, "page_table must be 2-D [B, max_pages]");
     const int64_t B = table.size(0), pages = table.size(1);
     const int* tp = data<int>(table, kI32, {B, pages}, "page_table");
@@ -384,7 +388,6 @@ PyObject* kv_evict(PyObject* const* a) {
     const fp8act_kv_cache c = cache_of(a[0]);
     const at::Tensor &table = tensor(a[2], "page_table"), &next = tensor(a[5], "new_table");
     float* mass = data<float>(a[1], kF32, {c.num_pages, c.kv_heads, c.page_size}, "mass");
-    on_current_device(table, "page_table");
     if (table.dim() != 2 || next.dim() != 2) raise(PyExc_ValueError, "page_table and new_table must be 2-D [B, pages]");
     const int64_t B = table.size(0), pages = table.size(1), fresh_pages = next.size(1);
     const int* tp = data<int>(table, kI32, {B, pages}, "page_table");
@@ -434,6 +437,7 @@ PyObject* verify_drafts(PyObject* const* a) {
 template <PyObject* (*kFunction)(PyObject* const*), Py_ssize_t kArgs>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (n != kArgs) return PyErr_Format(PyExc_TypeError, "%zd arguments expected, got %zd", kArgs, n);
+    g_device = -1;
     try {
         return kFunction(args);
     } catch (const Raised&) {

@@ -11,6 +11,9 @@ point of the same name (include/fp8act.h) and raises Fp8ActError on a
 non-zero status. All arithmetic runs in the library's CUDA kernels; there is
 no fallback: if the library is not built, loading it raises.
 
+The library launches on the current device. The operators between the layers
+refuse a tensor of another one (ValueError), whichever argument it is.
+
 With a `stream` that is not torch's current one, what an operator between the
 layers makes itself (outputs, a workspace) comes from that stream's memory
 pool; the outputs may be read and dropped on the current stream once it has
