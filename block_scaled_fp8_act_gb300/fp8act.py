@@ -409,7 +409,8 @@ def fp8_kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len: int | None 
 
     Scores: soft_cap > 0 caps them, soft_cap * tanh(x / soft_cap); slopes (fp32 [q_heads]) take
     slopes * distance off. A new token at position i sees position j if j < prefix_lens (int32 [B]), or if
-    first <= j <= i (int32 [tokens], not falling over a sequence's) and, with a window, j > i - window."""
+    first <= j <= i (int32 [tokens], not falling over a sequence's) and, with a window, j > i - window. Positions
+    are places of the cache: after fp8_kv_evict they are not those that the tokens had."""
     return _native().kv_attention(q, cache, page_table, kv_lens, cu_q, max_q_len, softmax_scale, out, lse, workspace,
                                   stream, soft_cap, window, prefix_lens, first, slopes)
 
@@ -441,7 +442,8 @@ def fp8_kv_evict(cache, mass, page_table, kv_lens, keep, new_table, recent: int 
     Of each sequence and KV head min(kv_lens, keep) tokens stay (keep int32 [B]): the last `recent`, the first
     `first`, then those of largest `mass` (fp32 [pages, kv_heads, page_size]; equal ones by position). They go,
     in their order, with their scales and masses to the pages of new_table (int32 [B, new_pages], none of them in
-    use); `kept` holds the positions they had, -1 from new_lens on. The old pages are not written."""
+    use); `kept` holds the positions they had, -1 from new_lens on. The old pages are not written. Windows, documents
+    and biases over the new pages count places there, not those positions."""
     return _native().kv_evict(cache, mass, page_table, kv_lens, keep, new_table, recent, first, new_lens, kept, stream)
 
 

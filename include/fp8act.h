@@ -389,6 +389,9 @@ FP8ACT_API int fp8_kv_attention(const void* q_bf16, int64_t q_stride, const int*
  *   first[token] <= j <= i  and, with window > 0,  j > i - window.
  * That is a sliding window, with `prefix_lens` one that keeps its first tokens; the
  * document that a token is in, if `first` is where that starts; a prefix mask.
+ * i and j are places of the cache. Where tokens have left it (fp8_kv_evict) those are
+ * no longer the positions that its tokens had: windows, documents and biases then
+ * count the tokens that stayed, which differ from KV head to KV head.
  * Tiles of up to 128 positions that no row of a sequence sees are not read.
  *   soft_cap     0 (none) or 1e-30 .. 1e30
  *   window       0 (none) or the positions that a token sees, its own included
@@ -454,7 +457,9 @@ FP8ACT_API size_t fp8_kv_attention_workspace(int max_q_len, int q_heads, const f
  * and weights. What matters: the last `recent` tokens first (at most n), then the
  * first `first` tokens (at most what is left of n), then the tokens of largest
  * mass; of equal ones the lower position. A mass of NaN counts as -infinity. KV
- * heads choose by themselves, so place i of two heads may hold different tokens.
+ * heads choose by themselves, so place i of two heads may hold different tokens, and
+ * what counts places afterwards (fp8act_scores: window, first, slopes) no longer
+ * counts positions; `kept` has those. Rotary positions are in the keys and stay.
  * The old pages are left as they are (other sequences may share them) and may be
  * given back once the call has run; new tokens go on at place n of the new ones.
  *   mass        [num_pages, kv_heads, page_size] fp32, 16-byte aligned: the weight
