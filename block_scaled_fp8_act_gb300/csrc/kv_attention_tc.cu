@@ -44,8 +44,9 @@
 // one of 128 (104 clocks against 64). Measured and slower: the softmax on 16
 // warps with 96 registers, the weights taken first and the maximum checked after,
 // a third widened buffer. A cap makes the softmax's chain half as long again (512
-// over 16384: 121 us with masks alone, 176 capped). The kernel spills (364 bytes of stores and 468 of loads
-// a thread with one row tile, 280 and 328 with two); of which role is not known.
+// over 16384: 121 us with masks alone, 176 capped). The kernel spills; of which role is not known. Bytes of stores and
+// loads a thread, one row tile and two: 364 and 468, 280 and 328 for plain scores, 412 and 524, 392 and 488 with masks,
+// 516 and 732, 392 and 488 with a cap or a bias.
 //
 // Every wait is bounded by wall time. The first that gives up sets the error
 // word and the CTA's abort flag; every role then leaves its loop, copies and

@@ -17,8 +17,9 @@
 // goes through its place in memory between them.
 //
 // What bounds it with few rows: the trips at a warp's start, lengths to page
-// table to keys. 34 sequences of one token to 16384, 6 heads on each of 4: 18.0
-// us on the device, 2.3 TB/s (6.0 us at a copy's rate).
+// table to keys. 34 sequences of one token to 16384, 6 heads on each of 4: 17.4
+// us on the device, 2.3 TB/s (6.0 us at a copy's rate); all of 16384 56.8, 5.5 TB/s.
+// In a window a sequence's other tokens cost nothing: of 4096 20.4 us.
 #include <atomic>
 
 #include "kv_attention.cuh"
@@ -29,7 +30,10 @@ namespace {
 __device__ unsigned int g_mass_index_error;
 
 constexpr int kTile = 32;
-constexpr int kWideRows = 33;  // rows from which on head size 128 takes the tcgen05 kernel
+// Rows from which on head size 128 takes the tcgen05 kernel, which is then faster throughout (us, here and there: 36 rows of
+// one sequence of 131072 26.5 and 25.0, of one of 4096 11.1 and 9.0, of 34 ragged ones to 16384 70.1 and 54.1). With fewer it
+// goes by the lengths: 24 rows 21.3 and 22.1, 9.5 and 8.4, 55.9 and 48.5, of 8 sequences of 2048 9.9 and 10.3.
+constexpr int kWideRows = 33;
 constexpr int kItemCost = 8;  // units that an item counts beside its own, for its start
 using Work = Units<kTile, kItemCost, List::kMass>;
 
@@ -358,6 +362,8 @@ cudaError_t launch_rows(AttnArgs& a, int max_q_len, int num_sms, cudaStream_t st
         a.rows = kWideRows;  // (any: an item has all rows)
         return launch_mass_tc(a, num_sms, stream);
     }
+    // CTAs of one warp for as many rows as one pass of them takes (us, with them and with whole CTAs, D = 128: 12 rows of 34
+    // ragged sequences to 16384 40.8 and 50.0, of one of 131072 21.4 and 18.6; 18 rows, two passes, 69.2 and 56.2, 33.7 and 21.5).
     return rows <= Mass<kD, true>::kRows ? launch<kD, true, kKind>(a, rows, num_sms, stream)
                                          : launch<kD, false, kKind>(a, rows, num_sms, stream);
 }

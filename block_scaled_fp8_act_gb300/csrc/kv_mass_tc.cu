@@ -21,6 +21,11 @@
 // accumulator 49.7, four accumulators of 128 rows 51.6, the rows' values in three
 // quarters of the bytes (a power of two as bf16 beside the log-sum-exp) 51.8 for
 // the instructions that widen them, 8 columns at a time with 16 in flight 55.2.
+// A cap takes it to 87.2 us, a bias by distance to 119: with either the kernel
+// spills, 628 bytes of stores and 732 of loads a thread at 168 registers (56 and 40
+// without), since 32 scores, the next 32 and the rows' values are live across the
+// cap, and a bias reads a row's slope and place for every score beside them. In a
+// window of 4096 of the 131072: 12.1 us, capped 14.1.
 //
 // Every wait is bounded as in kv_attention_tc.cu.
 #include <atomic>

@@ -25,7 +25,7 @@
 // or a key and a value of one, since a warp with two keys kept the others waiting.
 // More heads than a CTA's warps hold are other CTAs'.
 //
-// What bounds it (4096 tokens x 32 heads of 128: 15.2 us, 4.1 TB/s of the least
+// What bounds it (4096 tokens x 32 heads of 128: 15.1 us, 4.2 TB/s of the least
 // traffic): the chains of a round of two tokens, 3200 clocks with 4 warps a
 // scheduler to hide them (norm and turn 950, a key and a value to codes 1250,
 // unpacking and the next loads 500). One vector after the other, the slot read
@@ -319,7 +319,9 @@ cudaError_t launch(const RopeProblem& p, int num_sms, cudaStream_t stream) {
 }
 
 // Many tokens: two at a time, or, where a warp has room for more heads than there are, that many. (3 heads on 1 of 128,
-// 20000 tokens: 23.6 us, and 27.5 where one token a warp and round took 29.2.) With no more than a few for every CTA, one.
+// 20000 tokens: 23.0 us, and 27.5 where one token a warp and round took 29.2.) With no more than a few for every CTA, one (us,
+// one and two at a time: 24 heads on 4 of 128, 256 tokens 2.9 and 3.7, 512 3.75 and 3.9, 2500 9.7 and 9.2; 64 on 8, 64 tokens
+// 2.9 and 3.2, 384 6.7 and 5.8; in between either may be ahead, 1000 tokens of 24 on 4 5.2 and 5.4).
 template <int kLanes>
 cudaError_t launch_tokens(const RopeProblem& p, int num_sms, cudaStream_t stream) {
     constexpr int kPer = 32 / kLanes;

@@ -429,7 +429,8 @@ FP8ACT_API int fp8_kv_attention_scored(const void* q_bf16, int64_t q_stride, con
  * prompt's last 32, say: cu_q counts those that are; they are the last of the
  * sequence's kv_lens[b]).
  *   mass        [num_pages, kv_heads, page_size] fp32
- *   accumulate  0: the weights of positions 0 .. kv_lens[b] - 1 are replaced;
+ *   accumulate  0: the weights of positions 0 .. kv_lens[b] - 1 are replaced (so
+ *               that all the pages of a sequence have to be its own);
  *               else they are added to, but that those from old_lens[b] on start
  *               from zero (a place may hold a former token's weight)
  *   old_lens    [batch] int32, the tokens that have weights; NULL: all but the new
