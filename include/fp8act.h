@@ -412,7 +412,8 @@ typedef struct {
  * fp8_kv_attention with such scores (lse is theirs too). `scores` lives in host
  * memory and is read during the call; NULL or all zero is fp8_kv_attention.
  * Workspace and errors as there. A capped score is off by at most 2^-21 of its
- * size or 2^-21 soft_cap.
+ * size or 2^-21 soft_cap, a biased one by 2^-21 of its bias (scores are fp32: where
+ * a row sees nothing but tokens with biases of 4000 their weights are within 2^-8).
  */
 FP8ACT_API int fp8_kv_attention_scored(const void* q_bf16, int64_t q_stride, const int* cu_q, const int* kv_lens,
                                        const int* page_table, int max_pages, int batch, int tokens, int max_q_len,
